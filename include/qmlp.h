@@ -63,7 +63,7 @@ typedef enum {
 } qmlp_status;
 
 typedef enum { QMLP_FMT_NVFP4 = 1, QMLP_FMT_FP8_PC = 2 } qmlp_format;
-typedef enum { QMLP_DT_BF16 = 1, QMLP_DT_FP16 = 2 } qmlp_dtype;
+typedef enum { QMLP_DT_BF16 = 1, QMLP_DT_FP16 = 2, QMLP_DT_FP32 = 3 } qmlp_dtype;
 typedef enum { QMLP_META_3B = 3, QMLP_META_4B = 4 } qmlp_meta;
 /* Kernel family used by a forward call: AUTO picks the decode (GEMV) family
  * for small token counts and the tensor-core GEMM above. GEMM_PAIR is the
@@ -400,6 +400,62 @@ qmlp_status qmlp_moe_check(qmlp_moe_t* h, qmlp_stream_t stream);
 qmlp_status qmlp_moe_m1_forward_noalloc(const qmlp_moe_desc* banks, const void* x, qmlp_dtype xdt,
                                         const int32_t* expert_ids, const float* router_w, int topk,
                                         void* out, qmlp_stream_t stream);
+
+/*
+ * AdamW over many tensors at once (one launch a step), for the adapters and
+ * other small tensors trained beside the frozen weights. For every element,
+ * in fp32, with step number t:
+ *   g = grad_scale * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * 8-bit states: each 256 consecutive elements of a tensor have one fp32 scale
+ * (the last block may be short): m = e4m3fn(code) * scale, and sqrt(v) =
+ * e4m3fn(code) * scale, where the scale is the block's largest magnitude / 448
+ * and a root above zero keeps at least the smallest code. A new state is
+ * zeros (codes and scales). A gradient that is not finite makes its element's
+ * states NaN (and, where it is infinite, its block's), as in any AdamW: check
+ * for it before the step.
+ */
+typedef enum { QMLP_STATE_FP32 = 1, QMLP_STATE_8BIT = 2 } qmlp_state;
+
+typedef struct {
+    int64_t n;        /* elements, >= 1                                            */
+    void* param;      /* device [n], fp32 or bf16                                  */
+    float* master;    /* device fp32 [n] beside a bf16 param, or NULL: the step is
+                         taken on it and param = bf16(master) is written           */
+    const void* grad; /* device [n], fp32 or bf16                                  */
+    void* m;          /* device [n]: fp32, or e4m3fn codes                         */
+    void* v;          /* device [n]: fp32, or the e4m3fn codes of its square root  */
+    float* m_scale;   /* 8-bit states: device fp32 [ceil(n / 256)]; else NULL      */
+    float* v_scale;
+} qmlp_adamw_tensor;
+
+typedef struct {
+    double lr, beta1, beta2, eps, weight_decay;
+    double grad_scale; /* multiplies every gradient (1: none)  */
+    int64_t step;      /* t, from 1                            */
+} qmlp_adamw_hyper;
+
+typedef struct qmlp_adamw_s qmlp_adamw_t;
+
+/* Make a handle over `count` tensors (host array, copied; the tensors stay the
+ * caller's and must live as long as the handle). All parameters have one type
+ * (pdt: FP32 or BF16), all gradients one (gdt: FP32 or BF16), all states one
+ * (state); with a master, every tensor has one. Any alignment of the elements'
+ * own size is served; tensors whose pointers are 16-byte aligned (8 for
+ * codes) are read and written 8 elements at a time. Synchronizes `stream`.
+ * Errors: INVALID_ARG (null, bad enum, mixed masters, a master beside fp32,
+ * missing scales), SHAPE (count < 1, n < 1, over 2^31 chunks of 2048),
+ * ALIGNMENT, ALIAS (a written buffer overlaps another one), UNSUPPORTED_ARCH,
+ * OOM, CUDA. */
+qmlp_status qmlp_adamw_create(qmlp_adamw_t** out, const qmlp_adamw_tensor* tensors, int count, qmlp_dtype pdt,
+                              qmlp_dtype gdt, qmlp_state state, qmlp_stream_t stream);
+void qmlp_adamw_destroy(qmlp_adamw_t* h);
+
+/* One step on every tensor. Allocates nothing; can be captured in a CUDA graph
+ * (the hyperparameters are then the captured ones).
+ * Errors: INVALID_ARG (null; step < 1; beta outside [0, 1); a value that is
+ * not finite), CUDA. */
+qmlp_status qmlp_adamw_step(qmlp_adamw_t* h, const qmlp_adamw_hyper* hyper, qmlp_stream_t stream);
 
 /* Human-readable name of a status ("QMLP_OK", ...). Never NULL. */
 const char* qmlp_status_str(qmlp_status s);

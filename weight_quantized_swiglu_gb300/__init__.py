@@ -28,7 +28,8 @@ STATUS = {0: "QMLP_OK", 1: "QMLP_ERR_INVALID_ARG", 2: "QMLP_ERR_ALIGNMENT", 3: "
           4: "QMLP_ERR_SHAPE", 5: "QMLP_ERR_UNSUPPORTED_ARCH", 6: "QMLP_ERR_OOM", 7: "QMLP_ERR_CUDA",
           8: "QMLP_ERR_DEVICE_TIMEOUT", 9: "QMLP_ERR_DEVICE_BOUNDS"}
 FMT_NVFP4, FMT_FP8_PC = 1, 2
-DT_BF16, DT_FP16 = 1, 2
+DT_BF16, DT_FP16, DT_FP32 = 1, 2, 3
+STATE_FP32, STATE_8BIT = 1, 2
 META_3B, META_4B = 3, 4
 PATH_AUTO, PATH_GEMV, PATH_GEMM, PATH_GEMM_PAIR, PATH_GEMM_DQ = 0, 1, 2, 3, 4
 
@@ -52,6 +53,18 @@ class qmlp_moe_desc(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int), ("K", ctypes.c_int), ("I", ctypes.c_int), ("meta", ctypes.c_int),
                 ("w13", ctypes.c_void_p), ("w13_meta", ctypes.c_void_p), ("w2", ctypes.c_void_p),
                 ("w2_meta", ctypes.c_void_p)]
+
+
+class qmlp_adamw_tensor(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("param", ctypes.c_void_p), ("master", ctypes.c_void_p),
+                ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class qmlp_adamw_hyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
+                ("step", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -87,6 +100,9 @@ _SIGS = {
     "qmlp_moe_reserve": ([_VP, _I, _VP], _I),
     "qmlp_moe_forward": ([_VP, _VP, _I, _VP, _VP, _I, _I, _VP, _VP], _I),
     "qmlp_moe_m1_forward_noalloc": ([ctypes.POINTER(qmlp_moe_desc), _VP, _I, _VP, _VP, _I, _VP, _VP], _I),
+    "qmlp_adamw_create": ([ctypes.POINTER(_VP), ctypes.POINTER(qmlp_adamw_tensor), _I, _I, _I, _I, _VP], _I),
+    "qmlp_adamw_destroy": ([_VP], None),
+    "qmlp_adamw_step": ([_VP, ctypes.POINTER(qmlp_adamw_hyper), _VP], _I),
     "qmlp_status_str": ([_I], ctypes.c_char_p),
     "qmlp_abi_version": ([], _I),
 }
@@ -272,6 +288,23 @@ def qmlp_moe_m1_forward_noalloc(banks: qmlp_moe_desc, x, xdt, ids, rw, topk, out
                                              _ptr(out), _stream(stream))
 
 
+def qmlp_adamw_create(tensors, pdt, gdt, state, stream=None) -> int:
+    """tensors: a sequence of qmlp_adamw_tensor."""
+    h = ctypes.c_void_p()
+    arr = (qmlp_adamw_tensor * len(tensors))(*tensors)
+    st = lib().qmlp_adamw_create(ctypes.byref(h), arr, len(tensors), pdt, gdt, state, _stream(stream))
+    _chk(st, "qmlp_adamw_create")
+    return h.value
+
+
+def qmlp_adamw_destroy(h: int):
+    lib().qmlp_adamw_destroy(h)
+
+
+def qmlp_adamw_step(h, hyper: qmlp_adamw_hyper, stream=None) -> int:
+    return lib().qmlp_adamw_step(h, ctypes.byref(hyper), _stream(stream))
+
+
 # ---- convenience handles ------------------------------------------------------
 def _host_or_dev(a):
     """Keep numpy arrays (host) alive and return (address, owner)."""
@@ -415,6 +448,65 @@ class MoeAWQ:
     def close(self):
         if getattr(self, "h", None):
             qmlp_moe_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class AdamW:
+    """AdamW over many CUDA tensors, one launch a step (qmlp_adamw_*).
+
+    params: fp32 or bf16; grads: fp32 or bf16; m, v: fp32, or float8_e4m3fn
+    (or uint8) codes with m_scale / v_scale, fp32 [ceil(n / 256)] a tensor
+    (v's codes are those of its square root). master: fp32 copies of bf16
+    parameters, which the step is then taken on. The lists go tensor by
+    tensor; the tensors are contiguous, are kept alive by this object, and
+    are updated in place."""
+
+    def __init__(self, params, grads, m, v, m_scale=None, v_scale=None, master=None, stream=None):
+        import torch
+        count = len(params)
+        lists = {"params": params, "grads": grads, "m": m, "v": v, "m_scale": m_scale, "v_scale": v_scale,
+                 "master": master}
+        for name, ts in lists.items():
+            if ts is None:
+                continue
+            if len(ts) != count:
+                raise ValueError(f"AdamW: {len(ts)} tensors in {name}, {count} in params")
+            for i, t in enumerate(ts):
+                n = params[i].numel()
+                want = -(-n // 256) if name.endswith("scale") else n
+                if not t.is_cuda or not t.is_contiguous() or t.numel() != want or t.dtype != ts[0].dtype:
+                    raise ValueError(f"AdamW: {name}[{i}] has to be a contiguous CUDA tensor of {want} elements, "
+                                     f"all of one type")
+        if not count:
+            raise ValueError("AdamW: no tensors")
+        kinds = {torch.float32: DT_FP32, torch.bfloat16: DT_BF16}
+        eight = m[0].dtype in (torch.uint8, torch.float8_e4m3fn)
+        if (params[0].dtype not in kinds or grads[0].dtype not in kinds or m[0].dtype != v[0].dtype or
+                not (eight or m[0].dtype == torch.float32) or eight != (m_scale is not None) or
+                eight != (v_scale is not None) or
+                any(ts is not None and ts[0].dtype != torch.float32 for ts in (m_scale, v_scale, master))):
+            raise ValueError("AdamW: params and grads are fp32 or bf16, states fp32 or 8-bit codes with fp32 scales, "
+                             "a master fp32")
+        at = lambda ts, i: None if ts is None else ts[i].data_ptr()  # noqa: E731
+        ts = [qmlp_adamw_tensor(params[i].numel(), at(params, i), at(master, i), at(grads, i), at(m, i), at(v, i),
+                                at(m_scale, i), at(v_scale, i)) for i in range(count)]
+        self.h = qmlp_adamw_create(ts, kinds[params[0].dtype], kinds[grads[0].dtype],
+                                   STATE_8BIT if eight else STATE_FP32, stream)
+        self._keep = lists
+
+    def step(self, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=1, grad_scale=1.0, stream=None):
+        hyper = qmlp_adamw_hyper(lr, beta1, beta2, eps, weight_decay, grad_scale, step)
+        _chk(qmlp_adamw_step(self.h, hyper, stream), "qmlp_adamw_step")
+
+    def close(self):
+        if getattr(self, "h", None):
+            qmlp_adamw_destroy(self.h)
             self.h = None
 
     def __del__(self):

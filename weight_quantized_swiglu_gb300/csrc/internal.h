@@ -263,6 +263,28 @@ cudaError_t repack_moe_w13_blocks(const uint8_t* w, const uint8_t* meta, int met
 cudaError_t repack_moe(const uint8_t* w, const uint8_t* meta, int meta_bytes, int E, int N,
                        int Kr, uint8_t* w_out, uint8_t* meta_out, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// AdamW over many tensors (adamw.cu)
+// ---------------------------------------------------------------------------
+constexpr int kAdamWBlock = 256;   // elements that share a scale in an 8-bit state
+constexpr int kAdamWChunk = 2048;  // elements a CTA takes: 8 blocks of one tensor
+struct alignas(16) AdamWChunk {    // one CTA's part of a tensor; pointers at its first element
+    void* param;
+    float* master;   // fp32 master of a bf16 parameter, or null
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;  // 8-bit states: the scale of the chunk's first block
+    float* v_scale;
+    int n;           // elements, 1 .. kAdamWChunk
+    int vec;         // every pointer is aligned for 8 elements at a time
+};
+struct AdamWStep {  // the constants of a step, fp32 of fp64 values
+    float gscale, b1, omb1, b2, omb2, rbc2, eps, decay, step;
+};
+cudaError_t launch_adamw(const AdamWChunk* chunks, long count, bool param_bf16, bool master, bool grad_bf16, bool s8,
+                         const AdamWStep& k, cudaStream_t s);
+
 // Index checks of a QMLP_DEBUG_BOUNDS build (common.cuh): each translation
 // unit's first failed check, (site << 48) | index, or 0; reading clears it.
 // The default build returns 0.
