@@ -402,6 +402,55 @@ qmlp_status qmlp_moe_m1_forward_noalloc(const qmlp_moe_desc* banks, const void* 
                                         void* out, qmlp_stream_t stream);
 
 /*
+ * Low-rank adapters (LoRA) of many requests at once beside the dense MLP. An
+ * adapter of a projection W [N, D] is A [r, D], B [N, r] and a factor c; the
+ * projection of z becomes  W z + c B (A z). Every token names the slot of its
+ * adapter, so requests with different adapters share one call and one read of
+ * the quantized weights:
+ *   g = sigma_g x Wg^T + c B_g A_g x   (u alike),  act = bf16(SiLU(g) u)
+ *   out = bf16( sigma_d act Wd^T + c B_d A_d act )
+ * with each token's own A, B and c. Sums are fp32, and c A z is held as fp32.
+ */
+/* One adapter: bf16 device arrays, any alignment of 2 bytes, any rank from 1.
+ * A projection that is not adapted has both its pointers NULL. */
+typedef struct {
+    int rank;
+    float scale; /* c: alpha / r */
+    const void* gate_a; /* [r, K] */
+    const void* gate_b; /* [I, r] */
+    const void* up_a;   /* [r, K] */
+    const void* up_b;   /* [I, r] */
+    const void* down_a; /* [r, I] */
+    const void* down_b; /* [K, r] */
+} qmlp_adapter;
+
+typedef struct qmlp_lora_s qmlp_lora_t;
+
+/* Make `slots` empty adapter slots of ranks up to max_rank for the handle h,
+ * which must outlive them. Holds slots * 3 (K + I) * R bf16 values, R = 16, 32
+ * or 64 (max_rank rounded up), and a workspace for h's max_M tokens. The slots
+ * share h's workspace: calls on them and on h go on one stream at a time.
+ * Limits: 1 <= slots <= 1024, 1 <= max_rank <= 64. Synchronizes `stream`.
+ * Errors: INVALID_ARG, SHAPE, OOM, CUDA. */
+qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_rank, qmlp_stream_t stream);
+void qmlp_lora_destroy(qmlp_lora_t* l);
+
+/* Copy an adapter into a slot (in stream order: its arrays may be changed by
+ * later work on `stream`). NULL empties the slot.
+ * Errors: INVALID_ARG (null handle, slot out of range, one of A and B NULL),
+ * SHAPE (rank < 1 or over max_rank), ALIGNMENT (2 bytes), CUDA. */
+qmlp_status qmlp_lora_set(qmlp_lora_t* l, int slot, const qmlp_adapter* adapter, qmlp_stream_t stream);
+
+/* The MLP block with each token's adapter.
+ *  x   = device bf16 [M, K];  out = device bf16 [M, K]
+ *  ids = device int32 [M]: the token's slot; a value outside [0, slots) or an
+ *        empty slot: the block without an adapter (read on the device)
+ * Allocates nothing; can be captured in a CUDA graph. 1 <= M <= h's max_M.
+ * Errors: as qmlp_forward (ALIGNMENT: ids 4 bytes; ALIAS: out overlaps ids). */
+qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids, int M, void* out,
+                              qmlp_stream_t stream);
+
+/*
  * AdamW over many tensors at once (one launch a step), for the adapters and
  * other small tensors trained beside the frozen weights. For every element,
  * in fp32, with step number t:

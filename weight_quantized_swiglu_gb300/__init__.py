@@ -55,6 +55,13 @@ class qmlp_moe_desc(ctypes.Structure):
                 ("w2_meta", ctypes.c_void_p)]
 
 
+ADAPTER_PARTS = ("gate_a", "gate_b", "up_a", "up_b", "down_a", "down_b")
+
+
+class qmlp_adapter(ctypes.Structure):
+    _fields_ = [("rank", ctypes.c_int), ("scale", ctypes.c_float)] + [(n, ctypes.c_void_p) for n in ADAPTER_PARTS]
+
+
 class qmlp_adamw_tensor(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int64), ("param", ctypes.c_void_p), ("master", ctypes.c_void_p),
                 ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
@@ -100,6 +107,10 @@ _SIGS = {
     "qmlp_moe_reserve": ([_VP, _I, _VP], _I),
     "qmlp_moe_forward": ([_VP, _VP, _I, _VP, _VP, _I, _I, _VP, _VP], _I),
     "qmlp_moe_m1_forward_noalloc": ([ctypes.POINTER(qmlp_moe_desc), _VP, _I, _VP, _VP, _I, _VP, _VP], _I),
+    "qmlp_lora_create": ([ctypes.POINTER(_VP), _VP, _I, _I, _VP], _I),
+    "qmlp_lora_destroy": ([_VP], None),
+    "qmlp_lora_set": ([_VP, _I, ctypes.POINTER(qmlp_adapter), _VP], _I),
+    "qmlp_lora_forward": ([_VP, _VP, _VP, _I, _VP, _VP], _I),
     "qmlp_adamw_create": ([ctypes.POINTER(_VP), ctypes.POINTER(qmlp_adamw_tensor), _I, _I, _I, _I, _VP], _I),
     "qmlp_adamw_destroy": ([_VP], None),
     "qmlp_adamw_step": ([_VP, ctypes.POINTER(qmlp_adamw_hyper), _VP], _I),
@@ -288,6 +299,25 @@ def qmlp_moe_m1_forward_noalloc(banks: qmlp_moe_desc, x, xdt, ids, rw, topk, out
                                              _ptr(out), _stream(stream))
 
 
+def qmlp_lora_create(h, slots, max_rank, stream=None) -> int:
+    p = ctypes.c_void_p()
+    st = lib().qmlp_lora_create(ctypes.byref(p), h, slots, max_rank, _stream(stream))
+    _chk(st, "qmlp_lora_create")
+    return p.value
+
+
+def qmlp_lora_destroy(p: int):
+    lib().qmlp_lora_destroy(p)
+
+
+def qmlp_lora_set(p, slot, adapter: qmlp_adapter | None, stream=None) -> int:
+    return lib().qmlp_lora_set(p, slot, None if adapter is None else ctypes.byref(adapter), _stream(stream))
+
+
+def qmlp_lora_forward(p, x, ids, M, out, stream=None) -> int:
+    return lib().qmlp_lora_forward(p, _ptr(x), _ptr(ids), M, _ptr(out), _stream(stream))
+
+
 def qmlp_adamw_create(tensors, pdt, gdt, state, stream=None) -> int:
     """tensors: a sequence of qmlp_adamw_tensor."""
     h = ctypes.c_void_p()
@@ -448,6 +478,71 @@ class MoeAWQ:
     def close(self):
         if getattr(self, "h", None):
             qmlp_moe_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class Adapter:
+    """A low-rank adapter of the block: scale (alpha / r) and, for each adapted
+    projection, A [r, in] and B [out, r], contiguous bf16 CUDA tensors of one
+    rank. A projection that is not adapted has neither."""
+
+    def __init__(self, scale, gate_a=None, gate_b=None, up_a=None, up_b=None, down_a=None, down_b=None):
+        import torch
+        self.parts = dict(zip(ADAPTER_PARTS, (gate_a, gate_b, up_a, up_b, down_a, down_b)))
+        self.scale, self.rank = float(scale), 0
+        for n, t in self.parts.items():
+            if t is None:
+                continue
+            if not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 2 or not t.is_contiguous():
+                raise ValueError(f"Adapter: {n} has to be a contiguous bf16 CUDA matrix")
+            r = t.shape[0] if n.endswith("_a") else t.shape[1]
+            if self.rank not in (0, r):
+                raise ValueError(f"Adapter: {n} has rank {r}, another part {self.rank}")
+            self.rank = r
+        for p in ("gate", "up", "down"):
+            if (self.parts[p + "_a"] is None) != (self.parts[p + "_b"] is None):
+                raise ValueError(f"Adapter: {p} needs both A and B")
+        self.c = qmlp_adapter(self.rank, self.scale, *[_ptr(t) for t in self.parts.values()])
+
+    def check(self, K, I):
+        want = {"gate": (I, K), "up": (I, K), "down": (K, I)}
+        for n, t in self.parts.items():
+            if t is not None:
+                out, inp = want[n[:-2]]
+                shape = (self.rank, inp) if n.endswith("_a") else (out, self.rank)
+                if tuple(t.shape) != shape:
+                    raise ValueError(f"Adapter: {n} is {tuple(t.shape)}, {shape} is wanted")
+
+
+class LoraMLP:
+    """A QuantMLP with `slots` low-rank adapters, one a token (qmlp_lora_*).
+    The QuantMLP has to stay open while this object is."""
+
+    def __init__(self, mlp: QuantMLP, slots: int, max_rank: int, stream=None):
+        self.mlp, self.slots = mlp, slots
+        self.h = qmlp_lora_create(mlp.h, slots, max_rank, stream)
+
+    def set(self, slot, adapter: Adapter | None, stream=None):
+        """Copy an adapter into a slot (None: empty it), in stream order."""
+        if adapter is not None:
+            adapter.check(self.mlp.K, self.mlp.I)
+        _chk(qmlp_lora_set(self.h, slot, None if adapter is None else adapter.c, stream), "qmlp_lora_set")
+
+    def forward(self, x, ids, out, M=None, stream=None):
+        """x [M, K] bf16, ids [M] int32 (the token's slot; none: -1), out [M, K] bf16."""
+        M = x.shape[0] if M is None else M
+        _chk(qmlp_lora_forward(self.h, x, ids, M, out, stream), "qmlp_lora_forward")
+        return out
+
+    def close(self):
+        if getattr(self, "h", None):
+            qmlp_lora_destroy(self.h)
             self.h = None
 
     def __del__(self):

@@ -10,8 +10,6 @@ using namespace qmlp;
 
 namespace {
 
-constexpr int kMaxGemvM = 16;
-
 // x of a host-buffer call, from pinned host memory (over the CPU-GPU link)
 // into device memory, once: the decode kernel's CTAs would otherwise each read
 // all of it over the link. The decode kernel, launched next with programmatic
@@ -32,41 +30,6 @@ static void release_handle(qmlp_s* h) {
     h->mem.release();
     delete h;
 }
-
-// Largest token block one launch of the I-partitioned decode kernel takes: 16
-// for FP8 (two 8-token column tiles, x staged in two halves) where the
-// partition allows it, else 8. Measured on the 27B-class shape at 16 tokens:
-// FP8 85 us against 96 us on the split-K GEMM; NVFP4 144 us against 87 us
-// (its group scales cost two fp32 FMAs per accumulator element, and every CTA
-// writes and the reduce kernel reads a [16, K] fp32 partial: 2 x 44.6 MB).
-static int split_max_m(const qmlp_s* h) {
-    if (!h->sp.G) return 0;
-    return h->fmt == kFP8 && split_fits(h->fmt, kMaxGemvM, h->K, h->sp) ? kMaxGemvM : 8;
-}
-
-// Fewest tokens the automatic path sends to the tensor-core GEMM: past what
-// one launch of the I-partitioned decode kernel takes (a second launch, which
-// streams the weights again, loses to the split-K GEMM: measured on the
-// 27B-class shape, 106-142 us for 9..16 tokens as two 8-token launches
-// against 87-117 us). Shapes without the I partition decode 16 tokens per
-// stream-K pass.
-static int gemm_min_m(const qmlp_s* h) { return h->sp.G ? split_max_m(h) + 1 : kMaxGemvM + 1; }
-
-// Fewest tokens the automatic path sends to the dequantise-once GEMM (each
-// projection decoded once per call into fp16 stage images, then a GEMM
-// without decoder warps), and the handle's max_M from which it holds the
-// decode buffer (4 I K bytes: the larger projection). Measured on the
-// 27B-class shape (NVFP4 / FP8, ms, decoder warps against decoded once):
-// M = 512 0.322 / 0.345 against 0.357 / 0.386; M = 1024 0.607 / 0.644
-// against 0.552 / 0.578; M = 8192 3.49 / 3.70 against 2.79 / 2.80. With the
-// CTA-pair form: M = 640 0.360 / 0.386 against 0.378 / 0.409, M = 768
-// 0.402 / 0.428 against 0.383 / 0.414 (below, the down projection's few
-// 256-token tiles leave most pairs idle).
-constexpr int kDqMinM = 768;
-// The dequantise-once GEMM runs on CTA pairs from kPairMinM tokens (measured
-// at M = 8192, NVFP4 / FP8: 2.67 / 2.72 ms against 2.79 / 2.81 on single
-// CTAs; at M = 1024 0.520 / 0.550 against 0.553 / 0.578).
-constexpr bool kDqPair = true;
 
 struct qmlp_moe_s {
     int E = 0, K = 0, I = 0, meta = 0, device = 0, num_sms = 0;
@@ -417,6 +380,67 @@ static uint8_t* dq_buffer(const qmlp_t* h, qmlp_path path, int M) {
     return path == QMLP_PATH_AUTO && M >= kDqMinM ? h->wdec : nullptr;
 }
 
+extern "C++" {
+// The stages on the tensor-core GEMMs (see run_stages); `ex`: the low-rank
+// adapters' terms beside them.
+qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M, void* out, cudaStream_t s,
+                     float* out_f32, const GemmTerms* ex) {
+    GemmLaunch g;
+    g.wdec = dq_buffer(h, path, M);
+    g.wdec_bytes = h->wdec_bytes;
+    g.pair = path == QMLP_PATH_GEMM_PAIR || (g.wdec && kDqPair && M >= kPairMinM);
+    g.M = M;
+    g.err = h->err;
+    g.a16 = h->a16;
+    g.sig = h->sig;
+    g.ws = h->gemm_ws;
+    g.wait_ns = h->wait_ns;
+    g.withhold = h->withhold;
+    // dequantise-once, whole block: the gate/up images here, then the
+    // down images on the side stream while the gate/up GEMM runs (the
+    // fork follows everything already on s, so the previous call's down
+    // GEMM has finished reading wdec2)
+    const bool fork = g.wdec && stages == 3 && h->wdec2 && h->side;
+    if (fork && (launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s) != cudaSuccess ||
+                 cudaEventRecord(h->ev_fork, s) != cudaSuccess ||
+                 cudaStreamWaitEvent(h->side, h->ev_fork, 0) != cudaSuccess ||
+                 launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, h->side) != cudaSuccess ||
+                 cudaEventRecord(h->ev_join, h->side) != cudaSuccess))
+        return QMLP_ERR_CUDA;
+    g.images_ready = fork;
+    if (stages & 1) {
+        g.epi = kEpiSwiGLU;
+        if (ex) {
+            g.add = ex->add;
+            g.ldadd = (size_t)2 * h->I;
+        }
+        g.w = h->gm_gu;
+        g.a = x;
+        g.out = h->act;
+        if (launch_gemm(g, h->num_sms, s) != cudaSuccess) return QMLP_ERR_CUDA;
+    }
+    if (stages & 2) {
+        if (fork) {
+            if (cudaStreamWaitEvent(s, h->ev_join, 0) != cudaSuccess) return QMLP_ERR_CUDA;
+            g.wdec = h->wdec2;
+            g.wdec_bytes = h->wdec2_bytes;
+        }
+        if (ex) {
+            if (ex->between(s) != cudaSuccess) return QMLP_ERR_CUDA;
+            g.add = ex->add_down;
+            g.ldadd = (size_t)h->K;
+        }
+        g.epi = out_f32 ? kEpiRaw : kEpiPlain;
+        g.raw_sel = 0;
+        g.w = h->gm_d;
+        g.a = h->act;
+        g.out = out_f32 ? static_cast<void*>(out_f32) : out;
+        if (launch_gemm(g, h->num_sms, s) != cudaSuccess) return QMLP_ERR_CUDA;
+    }
+    return QMLP_OK;
+}
+}  // extern "C++"
+
 // stage bit 0: gate/up + SwiGLU (x -> workspace act); bit 1: down (act ->
 // out). With out_f32 the down stage writes its fp32 sums without the down
 // factor there (a tensor-parallel shard's partial) instead of bf16 to out.
@@ -427,52 +451,7 @@ static qmlp_status run_stages(qmlp_t* h, qmlp_path path, int stages, const void*
     if (gemm && !h->has_gemm) return QMLP_ERR_SHAPE;
     if (path == QMLP_PATH_GEMM_PAIR && M < kPairMinM) return QMLP_ERR_SHAPE;
     if (path == QMLP_PATH_GEMM_DQ && !h->wdec) return QMLP_ERR_SHAPE;
-    if (gemm) {
-        GemmLaunch g;
-        g.wdec = dq_buffer(h, path, M);
-        g.wdec_bytes = h->wdec_bytes;
-        g.pair = path == QMLP_PATH_GEMM_PAIR || (g.wdec && kDqPair && M >= kPairMinM);
-        g.M = M;
-        g.err = h->err;
-        g.a16 = h->a16;
-        g.sig = h->sig;
-        g.ws = h->gemm_ws;
-        g.wait_ns = h->wait_ns;
-        g.withhold = h->withhold;
-        // dequantise-once, whole block: the gate/up images here, then the
-        // down images on the side stream while the gate/up GEMM runs (the
-        // fork follows everything already on s, so the previous call's down
-        // GEMM has finished reading wdec2)
-        const bool fork = g.wdec && stages == 3 && h->wdec2 && h->side;
-        if (fork && (launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s) != cudaSuccess ||
-                     cudaEventRecord(h->ev_fork, s) != cudaSuccess ||
-                     cudaStreamWaitEvent(h->side, h->ev_fork, 0) != cudaSuccess ||
-                     launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, h->side) != cudaSuccess ||
-                     cudaEventRecord(h->ev_join, h->side) != cudaSuccess))
-            return QMLP_ERR_CUDA;
-        g.images_ready = fork;
-        if (stages & 1) {
-            g.epi = kEpiSwiGLU;
-            g.w = h->gm_gu;
-            g.a = x;
-            g.out = h->act;
-            if (launch_gemm(g, h->num_sms, s) != cudaSuccess) return QMLP_ERR_CUDA;
-        }
-        if (stages & 2) {
-            if (fork) {
-                if (cudaStreamWaitEvent(s, h->ev_join, 0) != cudaSuccess) return QMLP_ERR_CUDA;
-                g.wdec = h->wdec2;
-                g.wdec_bytes = h->wdec2_bytes;
-            }
-            g.epi = out_f32 ? kEpiRaw : kEpiPlain;
-            g.raw_sel = 0;
-            g.w = h->gm_d;
-            g.a = h->act;
-            g.out = out_f32 ? static_cast<void*>(out_f32) : out;
-            if (launch_gemm(g, h->num_sms, s) != cudaSuccess) return QMLP_ERR_CUDA;
-        }
-        return QMLP_OK;
-    }
+    if (gemm) return run_gemm(h, path, stages, x, M, out, s, out_f32, nullptr);
     const size_t Ntg = (size_t)(h->I / kTileRows);
     // the whole MLP in token blocks: up to 8 tokens per launch of the
     // I-partitioned kernel when the shape has a partition (its shared-memory
@@ -502,27 +481,11 @@ static qmlp_status run_stages(qmlp_t* h, qmlp_path path, int stages, const void*
         const bool fitAB = gemv_stream_fits(h->fmt, mb, std::max(h->K, h->I), 2, h->gv[0].Rr) &&
                            gemv_stream_fits(h->fmt, mb, std::max(h->K, h->I), 1, h->gv[2].Rr);
         if (split && split_fits(h->fmt, mb, h->K, h->sp)) {
-            SplitLaunch S;
-            S.fmt = h->fmt;
-            S.M = mb;
-            S.K = h->K;
-            S.I = h->I;
-            S.gate = h->gv[0];
-            S.up = h->gv[1];
-            S.wdown = h->wsplit;
-            S.chsd = h->gv[2].chs;
-            S.invd = h->gv[2].inv_g;
-            S.x = xb;
+            SplitLaunch S = split_launch(h, xb, mb);
             S.x_in_host = host_io;
             S.act_out = ab;  // the workspace act (qmlp_forward_debug returns it)
             S.out = out_f32 ? nullptr : ob;
             S.out_f32 = out_f32 ? static_cast<float*>(ob) : nullptr;
-            S.part = h->spart;
-            S.ticket = h->ticket;
-            S.err = h->err;
-            S.wait_ns = h->wait_ns;
-            S.withhold = h->withhold;
-            S.lim_a = h->lim_a;
             if (launch_split(S, h->sp, s) != cudaSuccess) return QMLP_ERR_CUDA;
             continue;
         }
@@ -802,28 +765,11 @@ qmlp_status qmlp_debug_split(qmlp_t* h, const void* x, const void* act_in, int M
             if (overlaps(outs[i], osz[i], outs[j], osz[j])) return QMLP_ERR_ALIAS;
     }
     if (fault("launch")) return QMLP_ERR_CUDA;
-    SplitLaunch S;
-    S.fmt = h->fmt;
-    S.M = M;
-    S.K = h->K;
-    S.I = h->I;
-    S.gate = h->gv[0];
-    S.up = h->gv[1];
-    S.wdown = h->wsplit;
-    S.chsd = h->gv[2].chs;
-    S.invd = h->gv[2].inv_g;
-    S.x = x;
-    S.act_out = h->act;
+    SplitLaunch S = split_launch(h, x, M);
     S.out_f32 = out_f32;
     S.act_in = act_in;
     S.dbg_g = g;
     S.dbg_u = u;
-    S.part = h->spart;
-    S.ticket = h->ticket;
-    S.err = h->err;
-    S.wait_ns = h->wait_ns;
-    S.withhold = h->withhold;
-    S.lim_a = h->lim_a;
     return launch_split(S, h->sp, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QMLP_OK
                                                                                           : QMLP_ERR_CUDA;
 }

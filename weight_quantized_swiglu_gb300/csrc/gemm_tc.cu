@@ -138,6 +138,8 @@ struct Args {
     size_t ws_elems;       // index checks: floats of the split-K partial buffer
     const uint8_t* wdec;   // PRE: decoded stage images [Nt][KS][32 KB]
     size_t wdec_bytes;     // PRE: bytes of wdec (index checks)
+    const float* add;      // EXT: fp32 [M][ldadd] added after the factor (gate then up columns, or the output's)
+    size_t ldadd;
 };
 
 // Instruction descriptor, kind::f16: fp32 accumulator, fp16 A and B, both
@@ -208,7 +210,8 @@ QMLP_DEV uint32_t pack_bf16x2(float lo, float hi) {
 
 // The tile epilogue (no split): accumulator columns of TMEM base `tbase`
 // (this thread's lane = token row m) -> SwiGLU act, plain output or raw fp32.
-template <int FMT>
+// EXT: the instances of low-rank adapters, which add their fp32 terms.
+template <int FMT, bool EXT>
 QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg, int nt) {
     if (a.epi == kEpiSwiGLU) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
@@ -223,11 +226,21 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                 for (int j = 0; j < 32; j += 4) {
                     const float4 fg = factor4<FMT>(a.cs0, a.inv0, nt * (BN / 2) + c0 + j);
                     const float4 fu = factor4<FMT>(a.cs1, a.inv1, nt * (BN / 2) + c0 + j);
+                    float4 dg, du;
+                    if (EXT) {
+                        const float* ad = a.add + (size_t)m * a.ldadd + nt * (BN / 2) + c0 + j;
+                        dg = *reinterpret_cast<const float4*>(ad);
+                        du = *reinterpret_cast<const float4*>(ad + a.ldo);
+                    }
                     float r4[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float gv = scalbnf(g[j + e], -sg) * f4_at(fg, e);
-                        const float uv = scalbnf(u[j + e], -sg) * f4_at(fu, e);
+                        float gv = scalbnf(g[j + e], -sg) * f4_at(fg, e);
+                        float uv = scalbnf(u[j + e], -sg) * f4_at(fu, e);
+                        if (EXT) {
+                            gv += f4_at(dg, e);
+                            uv += f4_at(du, e);
+                        }
                         r4[e] = silu_f32(gv) * uv;
                     }
                     pk[j / 2] = pack_bf16x2(r4[0], r4[1]);
@@ -251,6 +264,13 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 f = factor4<FMT>(a.cs0, a.inv0, nt * BN + c0 + j);
+                    if (EXT) {
+                        const float4 d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + nt * BN + c0 + j);
+                        pk[j / 2] = pack_bf16x2(scalbnf(y[j], -sg) * f.x + d.x, scalbnf(y[j + 1], -sg) * f.y + d.y);
+                        pk[j / 2 + 1] =
+                            pack_bf16x2(scalbnf(y[j + 2], -sg) * f.z + d.z, scalbnf(y[j + 3], -sg) * f.w + d.w);
+                        continue;
+                    }
                     pk[j / 2] = pack_bf16x2(scalbnf(y[j], -sg) * f.x, scalbnf(y[j + 1], -sg) * f.y);
                     pk[j / 2 + 1] = pack_bf16x2(scalbnf(y[j + 2], -sg) * f.z, scalbnf(y[j + 3], -sg) * f.w);
                 }
@@ -282,7 +302,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
     }
 }
 
-template <int FMT, bool SPLIT, bool PRE>
+template <int FMT, bool SPLIT, bool PRE, bool EXT = false>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ CUtensorMap amap, const Args a) {
     using S = Smem<FMT, PRE>;
     constexpr int kLStages = S::L;
@@ -457,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     }
                 }
             } else {
-                store_tile<FMT>(a, tbase, m, live, sg, nt);
+                store_tile<FMT, EXT>(a, tbase, m, live, sg, nt);
             }
             tc_fence_before();
             mbar_arrive(acc_empty(buf));
@@ -643,7 +663,7 @@ QMLP_DEV void umma_commit_pair(uint32_t bar) {
         : "memory");
 }
 
-template <int FMT, bool PRE>
+template <int FMT, bool PRE, bool EXT = false>
 __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_constant__ CUtensorMap amap,
                                                                 const __grid_constant__ CUtensorMap bmap, const Args a) {
     using S = SmemP<FMT, PRE>;
@@ -829,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
             const bool live = m < a.M;
             const int sg = live && a.sig ? a.sig[m] : 0;  // no prescale (null sig): bf16 operands
             const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
-            store_tile<FMT>(a, tbase, m, live, sg, nt);
+            store_tile<FMT, EXT>(a, tbase, m, live, sg, nt);
             tc_fence_before();
             mbar_arrive(acc_empty(buf));
         }
@@ -910,14 +930,20 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const Args a) {
             u += ws[sp * plane + col + BN / 2];
         }
         const float fg = FMT == kNVFP4 ? a.inv0 : a.cs0[n], fu = FMT == kNVFP4 ? a.inv1 : a.cs1[n];
-        const float gv = scalbnf(g, -sg) * fg, uv = scalbnf(u, -sg) * fu;
+        float gv = scalbnf(g, -sg) * fg, uv = scalbnf(u, -sg) * fu;
+        if (a.add) {
+            gv += a.add[(size_t)m * a.ldadd + n];
+            uv += a.add[(size_t)m * a.ldadd + nout + n];
+        }
         *out = __float2bfloat16_rn(silu_f32(gv) * uv);
     } else {
         float y = 0.0f;
         for (int sp = 0; sp < a.splits; ++sp)
             if (QMLP_INB((size_t)m * a.N + sp * plane + n, a.ws_elems, 14)) y += ws[sp * plane + n];
         const float f = FMT == kNVFP4 ? a.inv0 : a.cs0[n];
-        *out = __float2bfloat16_rn(scalbnf(y, -sg) * f);
+        y = scalbnf(y, -sg) * f;
+        if (a.add) y += a.add[(size_t)m * a.ldadd + n];
+        *out = __float2bfloat16_rn(y);
     }
 }
 
@@ -1090,7 +1116,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // The CTA-pair GEMM over `pairs_wanted` clusters of two (fewer if fewer fit at
 // once: the pairs loop over the tiles).
-template <int FMT, bool PRE>
+template <int FMT, bool PRE, bool EXT = false>
 cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const Args& a, int pairs_wanted,
                         cudaStream_t s) {
     static int max_pairs = -1;
@@ -1106,34 +1132,34 @@ cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const A
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (max_pairs < 0) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<FMT, PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<FMT, PRE, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              SmemP<FMT, PRE>::Bytes);
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2);
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<FMT, PRE>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<FMT, PRE, EXT>, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         max_pairs = n;
     }
     cfg.gridDim = dim3((unsigned)(2 * std::min(pairs_wanted, max_pairs)));
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<FMT, PRE>, map, bmap, a);
+    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<FMT, PRE, EXT>, map, bmap, a);
 }
 
-template <int FMT, bool PRE>
+template <int FMT, bool PRE, bool EXT = false>
 cudaError_t launch_inst(const CUtensorMap& map, const Args& a, int grid, cudaStream_t s) {
     static bool attr = false;
     constexpr int bytes = Smem<FMT, PRE>::Bytes;
     if (!attr) {
         cudaError_t e =
-            cudaFuncSetAttribute(gemm_kernel<FMT, false, PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+            cudaFuncSetAttribute(gemm_kernel<FMT, false, PRE, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(gemm_kernel<FMT, true, PRE>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         attr = true;
     }
     if (a.splits > 1) gemm_kernel<FMT, true, PRE><<<grid, kThreads, bytes, s>>>(map, a);
-    else gemm_kernel<FMT, false, PRE><<<grid, kThreads, bytes, s>>>(map, a);
+    else gemm_kernel<FMT, false, PRE, EXT><<<grid, kThreads, bytes, s>>>(map, a);
     return cudaPeekAtLastError();
 }
 
@@ -1150,7 +1176,10 @@ cudaError_t launch_predecode(const Args& a, uint8_t* wdec, int num_sms, cudaStre
 
 template <int FMT>
 cudaError_t launch_fmt(const CUtensorMap& map, const Args& a, int grid, cudaStream_t s) {
-    cudaError_t e = a.wdec ? launch_inst<FMT, true>(map, a, grid, s) : launch_inst<FMT, false>(map, a, grid, s);
+    cudaError_t e = a.add ? (a.wdec ? launch_inst<FMT, true, true>(map, a, grid, s)
+                                    : launch_inst<FMT, false, true>(map, a, grid, s))
+                    : a.wdec ? launch_inst<FMT, true>(map, a, grid, s)
+                             : launch_inst<FMT, false>(map, a, grid, s);
     if (e != cudaSuccess || a.splits == 1) return e;
     const long n = (long)a.M * (a.epi == kEpiSwiGLU ? a.N / 2 : a.N);
     splitk_reduce_kernel<FMT><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
@@ -1249,6 +1278,9 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.sig = dq ? nullptr : L.sig;
     a.out = L.out;
     a.ldo = L.epi == kEpiSwiGLU ? P.N / 2 : (L.epi == kEpiRaw && P.interleaved ? P.N / 2 : P.N);
+    a.add = L.add;
+    a.ldadd = L.ldadd;
+    if (L.add && (L.epi == kEpiRaw || (L.pair && !dq) || L.ldadd % 4)) return cudaErrorInvalidValue;
     a.err = L.err;
     a.limit = L.wait_ns ? L.wait_ns : kGemmWaitNs;
     a.withhold = L.withhold ? 1 : 0;
@@ -1289,6 +1321,9 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
+        if (a.add)
+            return P.fmt == kFP8 ? launch_pair<kFP8, true, true>(map, bmap, a, pairs, s)
+                                 : launch_pair<kNVFP4, true, true>(map, bmap, a, pairs, s);
         return P.fmt == kFP8 ? launch_pair<kFP8, true>(map, bmap, a, pairs, s)
                              : launch_pair<kNVFP4, true>(map, bmap, a, pairs, s);
     }

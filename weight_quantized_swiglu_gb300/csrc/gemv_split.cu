@@ -78,6 +78,7 @@ struct Args {
     const __nv_bfloat16* act_in;  // optional [M, I]: phase B consumes these act values (debug)
     float* dbg_g;              // optional [M, I]: gate dot products, fp32, no factor (debug)
     float* dbg_u;              // optional [M, I]: up dot products, likewise
+    const float* add;          // optional [M, 2I]: added to gate (first I) and up after the factor
     float* part;               // [G][M][K]
     unsigned long long* ticket;
     int* err;
@@ -241,8 +242,12 @@ QMLP_DEV void epilogue_a(const Args& a, int M, int lt, const float (&v)[2][NT][4
             const float s1 = FMT == kNVFP4 ? a.inv1 : a.chs1[i];
             const float pw = pow2_neg(s_sig[m]);
             const float graw = v[0][n][e] * pw, uraw = v[1][n][e] * pw;
-            const float gv = graw * s0;
-            const float uv = uraw * s1;
+            float gv = graw * s0;
+            float uv = uraw * s1;
+            if (a.add) {  // the low-rank adapters' terms
+                gv += a.add[(size_t)m * 2 * a.I + i];
+                uv += a.add[(size_t)m * 2 * a.I + a.I + i];
+            }
             __nv_bfloat16 act = __float2bfloat16_rn(silu_f32(gv) * uv);
             if (a.dbg_g) {
                 a.dbg_g[(size_t)m * a.I + i] = graw;
@@ -1110,6 +1115,7 @@ cudaError_t launch_split(const SplitLaunch& L, const SplitPlan& P, cudaStream_t 
     a.act_in = static_cast<const __nv_bfloat16*>(L.act_in);
     a.dbg_g = L.dbg_g;
     a.dbg_u = L.dbg_u;
+    a.add = L.add;
     a.part = L.part;
     a.ticket = L.ticket;
     a.err = L.err;

@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <functional>
 #include <vector>
 
 #include "internal.h"
@@ -106,3 +107,74 @@ struct qmlp_s {
     bool withhold = false;     // error-path tests: the kernels' producers skip their last step
     qmlp::Owner mem;
 };
+
+constexpr int kMaxGemvM = 16;
+
+// Largest token block one launch of the I-partitioned decode kernel takes: 16
+// for FP8 (two 8-token column tiles, x staged in two halves) where the
+// partition allows it, else 8. Measured on the 27B-class shape at 16 tokens:
+// FP8 85 us against 96 us on the split-K GEMM; NVFP4 144 us against 87 us
+// (its group scales cost two fp32 FMAs per accumulator element, and every CTA
+// writes and the reduce kernel reads a [16, K] fp32 partial: 2 x 44.6 MB).
+inline int split_max_m(const qmlp_s* h) {
+    if (!h->sp.G) return 0;
+    return h->fmt == qmlp::kFP8 && qmlp::split_fits(h->fmt, kMaxGemvM, h->K, h->sp) ? kMaxGemvM : 8;
+}
+
+// Fewest tokens the automatic path sends to the tensor-core GEMM: past what
+// one launch of the I-partitioned decode kernel takes (a second launch, which
+// streams the weights again, loses to the split-K GEMM: measured on the
+// 27B-class shape, 106-142 us for 9..16 tokens as two 8-token launches
+// against 87-117 us). Shapes without the I partition decode 16 tokens per
+// stream-K pass.
+inline int gemm_min_m(const qmlp_s* h) { return h->sp.G ? split_max_m(h) + 1 : kMaxGemvM + 1; }
+
+// Fewest tokens the automatic path sends to the dequantise-once GEMM (each
+// projection decoded once per call into fp16 stage images, then a GEMM
+// without decoder warps), and the handle's max_M from which it holds the
+// decode buffer (4 I K bytes: the larger projection). Measured on the
+// 27B-class shape (NVFP4 / FP8, ms, decoder warps against decoded once):
+// M = 512 0.322 / 0.345 against 0.357 / 0.386; M = 1024 0.607 / 0.644
+// against 0.552 / 0.578; M = 8192 3.49 / 3.70 against 2.79 / 2.80. With the
+// CTA-pair form: M = 640 0.360 / 0.386 against 0.378 / 0.409, M = 768
+// 0.402 / 0.428 against 0.383 / 0.414 (below, the down projection's few
+// 256-token tiles leave most pairs idle).
+constexpr int kDqMinM = 768;
+// The dequantise-once GEMM runs on CTA pairs from kPairMinM tokens (measured
+// at M = 8192, NVFP4 / FP8: 2.67 / 2.72 ms against 2.79 / 2.81 on single
+// CTAs; at M = 1024 0.520 / 0.550 against 0.553 / 0.578).
+constexpr bool kDqPair = true;
+
+// The I-partitioned decode kernel on M tokens, without its output: act goes to
+// the workspace.
+inline qmlp::SplitLaunch split_launch(const qmlp_s* h, const void* x, int M) {
+    qmlp::SplitLaunch S;
+    S.fmt = h->fmt;
+    S.M = M;
+    S.K = h->K;
+    S.I = h->I;
+    S.gate = h->gv[0];
+    S.up = h->gv[1];
+    S.wdown = h->wsplit;
+    S.chsd = h->gv[2].chs;
+    S.invd = h->gv[2].inv_g;
+    S.x = x;
+    S.act_out = h->act;
+    S.part = h->spart;
+    S.ticket = h->ticket;
+    S.err = h->err;
+    S.wait_ns = h->wait_ns;
+    S.withhold = h->withhold;
+    S.lim_a = h->lim_a;
+    return S;
+}
+
+// Terms of low-rank adapters that the GEMMs add: gate and up [M][2I], then,
+// once `between` has run on the workspace act, down's [M][K].
+struct GemmTerms {
+    const float* add = nullptr;
+    const float* add_down = nullptr;
+    std::function<cudaError_t(cudaStream_t)> between;
+};
+qmlp_status run_gemm(qmlp_s* h, qmlp_path path, int stages, const void* x, int M, void* out, cudaStream_t s,
+                     float* out_f32, const GemmTerms* ex);

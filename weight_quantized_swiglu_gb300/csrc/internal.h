@@ -129,6 +129,7 @@ struct SplitLaunch {
     const void* act_in = nullptr;    // optional bf16 [M, I]: the down projection consumes these (debug)
     float* dbg_g = nullptr;          // optional fp32 [M, I]: raw gate dot products (debug; with dbg_u)
     float* dbg_u = nullptr;          // optional fp32 [M, I]: raw up dot products (debug)
+    const float* add = nullptr;      // optional fp32 [M, 2I]: added to gate and up after the factor
     float* part = nullptr;           // >= split_part_elems
     unsigned long long* ticket = nullptr;  // grid-barrier ticket counter (zeroed at create)
     int* err = nullptr;
@@ -178,6 +179,8 @@ struct GemmLaunch {
     bool pair = false;        // the CTA-pair kernel (M >= kPairMinM; never split-K)
     uint8_t* wdec = nullptr;  // dequantise-once: decoded stage images of w (null: the decoder warps decode)
     size_t wdec_bytes = 0;    // bytes of wdec, >= gemm_decoded_bytes(w.N, w.K)
+    const float* add = nullptr;  // fp32 [M][ldadd], added after the factor: gate's I columns then up's
+    size_t ldadd = 0;            // (SwiGLU), or the output's columns (plain); low-rank adapters
     bool images_ready = false;  // dequantise-once: wdec already holds w's images (no predecode launch)
 };
 constexpr int kPairMinM = 256;  // one 256-token tile of a CTA pair

@@ -1,0 +1,662 @@
+// lowrank.cu -- the products of low-rank adapters: z A^T (wide in, r out),
+// v B^T (r in, wide out) and z^T v (over the tokens), r <= 64.
+//
+// Notation: an adapter of a projection W [N, D] is A [r, D], B [N, r] and a
+// factor c; it adds c B (A z) to W z. All inputs are bf16 and every sum is
+// fp32. v = c A z is kept in three bf16 words, each the rounding of what the
+// ones before it leave, so that the second product sees v as fp32 holds it, at
+// the price of two more MMAs of a product that is bound by memory. (With two
+// words, 2^-17 of v: the block's output differed from the 64-bit one, both in
+// bf16, by 5e-4 where the adapters' terms are as large as the block's; 2e-4
+// with three, as without adapters.)
+//
+// Ranks are padded to Rp = 16, 32 or 64 with zeros (the packed copies of a
+// handle), tokens are taken in tiles of 64 of one adapter: for calls of many
+// requests a plan kernel groups the tokens by adapter (perm, tiles); with one
+// adapter a tile is 64 consecutive tokens. Every row of a tile is summed on
+// its own and in an order that depends on the sizes alone, so a token's result
+// does not depend on the tokens beside it.
+//
+// Bound by memory: z (or the wide output) passes once; the MMAs (mma.sync
+// m16n8k16) are far below the tensor cores' rate at these ranks.
+#include "lowrank.cuh"
+
+namespace qmlp {
+namespace {
+
+constexpr int kT = kLrTile;    // tokens of a tile
+constexpr int kThr = 128;      // 4 warps, 16 tokens each
+constexpr int kStep = 64;      // contraction length of a step
+
+QMLP_DEV void cp16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+QMLP_DEV void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+QMLP_DEV void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+QMLP_DEV void ldsm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+QMLP_DEV void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a)
+                 : "memory");
+}
+QMLP_DEV void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk c of row `row` in a tile of rows of CPR chunks
+// (CPR 2, 4, 8 or 16), swizzled so that eight rows at one c, or eight chunks
+// of a row, fall into different banks.
+template <int CPR>
+QMLP_DEV uint32_t sw(int row, int c) {
+    const int x = CPR >= 8 ? row & 7 : CPR == 4 ? (row >> 1) & 3 : (row >> 2) & 1;
+    return (uint32_t)((row * CPR + (c ^ x)) * 16);
+}
+
+// The B fragments (two n8 tiles, one k16) of columns n0..n0+15, contraction
+// k0..k0+15 of a tile in shared memory: rows of k (TRANS: [k][n]) or of n.
+template <bool TRANS, int CPR>
+QMLP_DEV void load_b(uint32_t base, int n0, int k0, int lane, uint32_t (&b)[4]) {
+    const int q = lane >> 3, r = lane & 7;
+    if (TRANS) ldsm4t(b, base + sw<CPR>(k0 + (q & 1) * 8 + r, (n0 >> 3) + (q >> 1)));
+    else ldsm4(b, base + sw<CPR>(n0 + (q >> 1) * 8 + r, (k0 >> 3) + (q & 1)));
+}
+
+// v as NW bf16 words, the largest first.
+template <int NW>
+QMLP_DEV void split_bf16(float v, __nv_bfloat16 (&w)[NW]) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        w[i] = __float2bfloat16_rn(v);
+        v -= __bfloat162float(w[i]);
+    }
+}
+
+// The tile of this CTA: slot, first position, tokens. False: no such tile.
+QMLP_DEV bool tile_of(const LrTokens& t, int i, int& slot, int& pos0, int& n) {
+    if (!t.tiles) {
+        slot = 0;
+        pos0 = i * kT;
+        n = min(kT, t.M - pos0);
+        return n > 0;
+    }
+    if (i >= *t.n_tiles) return false;
+    const int4 e = t.tiles[i];
+    slot = e.x;
+    pos0 = e.y;
+    n = e.z;
+    return true;
+}
+
+// True in every thread of the last of `n` CTAs that call it for one counter
+// (whose writes all of them then see); the counter is left at zero.
+QMLP_DEV bool last_arrival(int* cnt, int n) {
+    __shared__ int last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        last = atomicAdd(cnt, 1) == n - 1;
+        if (last) *cnt = 0;
+    }
+    __syncthreads();
+    if (last) __threadfence();
+    return last != 0;
+}
+
+// ---------------------------------------------------------------------------
+// v = c z W^T of a tile, NC columns. W: [NC][D], or with TRANS [D][NC]. The
+// contraction is split over gridDim.y CTAs; the last one adds the splits'
+// partials in order.
+// ---------------------------------------------------------------------------
+template <int NC, bool TRANS, bool TWO>
+struct ShrinkSmem {
+    static constexpr int X = kT * kStep * 2, W = NC * kStep * 2;
+    static constexpr int Stage = X + W * (TWO ? 2 : 1);
+    static constexpr int Stages = 4;
+    static constexpr int Bytes = Stage * Stages;
+};
+
+template <int NC, bool TRANS, bool TWO>
+__global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
+    using S = ShrinkSmem<NC, TRANS, TWO>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    int slot, pos0, n;
+    if (!tile_of(a.tok, blockIdx.x, slot, pos0, n) || slot < 0) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int z = blockIdx.z;
+    const __nv_bfloat16* x = a.x + (size_t)z * a.x_z;
+    const __nv_bfloat16* w = a.w + (size_t)slot * a.w_slot + (size_t)z * a.w_z;
+    const __nv_bfloat16* w2 = TWO ? a.w_lo + (size_t)z * a.w_z : nullptr;
+    const int steps = (a.D + kStep - 1) / kStep;
+    const int s0 = (int)((long)steps * blockIdx.y / gridDim.y), s1 = (int)((long)steps * (blockIdx.y + 1) / gridDim.y);
+    const uint32_t base = smem_u32(smem);
+
+    // this thread's chunks of a step: x rows (tid >> 3) + 16 i, chunk tid & 7
+    const __nv_bfloat16* xr[4];
+    bool xl[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = (tid >> 3) + 16 * i;
+        xl[i] = r < n;
+        const int tok = xl[i] ? (a.tok.perm ? a.tok.perm[pos0 + r] : pos0 + r) : 0;
+        xr[i] = x + (size_t)tok * a.ldx;
+    }
+    auto load = [&](int step, int stage) {
+        const uint32_t sx = base + stage * S::Stage, swt = sx + S::X;
+        const int d0 = step * kStep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = (tid >> 3) + 16 * i, c = tid & 7, d = d0 + c * 8;
+            const bool live = xl[i] && d < a.D;
+            cp16(sx + sw<8>(r, c), live ? xr[i] + d : x, live);
+        }
+        constexpr int kW = NC * kStep / 8;  // chunks of the W tile
+#pragma unroll
+        for (int i = 0; i < kW / kThr; ++i) {
+            const int k = tid + i * kThr;
+            if (TRANS) {
+                const int r = k / (NC / 8), c = k % (NC / 8);
+                const bool live = d0 + r < a.D;
+                const size_t off = live ? (size_t)(d0 + r) * NC + c * 8 : 0;
+                cp16(swt + sw<NC / 8>(r, c), w + off, live);
+                if (TWO) cp16(swt + S::W + sw<NC / 8>(r, c), w2 + off, live);
+            } else {
+                const int r = k >> 3, c = k & 7, d = d0 + c * 8;
+                const bool live = d < a.D;
+                cp16(swt + sw<8>(r, c), w + (live ? (size_t)r * a.D + d : 0), live);
+            }
+        }
+        cp_commit();
+    };
+
+    float acc[NC / 8][4];
+#pragma unroll
+    for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+#pragma unroll
+    for (int p = 0; p < S::Stages - 1; ++p) {
+        if (s0 + p < s1) load(s0 + p, p);
+        else cp_commit();
+    }
+    const int q = lane >> 3, r8 = lane & 7;
+    for (int st = s0; st < s1; ++st) {
+        cp_wait<S::Stages - 2>();
+        __syncthreads();
+        const int nx = st + S::Stages - 1;
+        if (nx < s1) load(nx, (nx - s0) % S::Stages);
+        else cp_commit();
+        const uint32_t sx = base + ((st - s0) % S::Stages) * S::Stage, swt = sx + S::X;
+        if (warp * 16 < n) {
+#pragma unroll
+            for (int k = 0; k < kStep; k += 16) {
+                uint32_t af[4];
+                ldsm4(af, sx + sw<8>(warp * 16 + (q & 1) * 8 + r8, (k >> 3) + (q >> 1)));
+#pragma unroll
+                for (int j = 0; j < NC / 16; ++j) {
+                    uint32_t b[4];
+                    load_b<TRANS, TRANS ? NC / 8 : 8>(swt, j * 16, k, lane, b);
+                    mma_bf16(acc[2 * j], af, b[0], b[1]);
+                    mma_bf16(acc[2 * j + 1], af, b[2], b[3]);
+                    if (TWO) {
+                        load_b<TRANS, TRANS ? NC / 8 : 8>(swt + S::W, j * 16, k, lane, b);
+                        mma_bf16(acc[2 * j], af, b[0], b[1]);
+                        mma_bf16(acc[2 * j + 1], af, b[2], b[3]);
+                    }
+                }
+            }
+        }
+    }
+
+    // fragment (j, e): row 16 warp + g + 8 (e >> 1), column 8 j + 2 t + (e & 1)
+    const int g = lane >> 2, t = lane & 3;
+    const float c = a.scale ? a.scale[slot] : 1.0f;
+    auto emit = [&](int row, int col, float v0, float v1) {
+        __nv_bfloat16 w0[kLrWords], w1[kLrWords];
+        split_bf16(v0 * c, w0);
+        split_bf16(v1 * c, w1);
+        __nv_bfloat16* o = a.v + (size_t)(pos0 + row) * a.ldv + z * NC + col;
+#pragma unroll
+        for (int i = 0; i < kLrWords; ++i)
+            *reinterpret_cast<__nv_bfloat162*>(o + i * a.v_word) = __halves2bfloat162(w0[i], w1[i]);
+    };
+    if (gridDim.y == 1) {
+#pragma unroll
+        for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = warp * 16 + g + 8 * h;
+                if (row < n) emit(row, j * 8 + 2 * t, acc[j][2 * h], acc[j][2 * h + 1]);
+            }
+        return;
+    }
+    const size_t tile = (size_t)blockIdx.x + (size_t)gridDim.x * z;
+    float* part = a.part + (tile * gridDim.y + blockIdx.y) * (kT * NC);
+#pragma unroll
+    for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = warp * 16 + g + 8 * h;
+            if (row < n)
+                *reinterpret_cast<float2*>(part + row * NC + j * 8 + 2 * t) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+        }
+    if (!last_arrival(a.cnt + tile, gridDim.y)) return;
+    const float* all = a.part + tile * gridDim.y * (kT * NC);
+    for (int i = tid; i < n * (NC / 2); i += kThr) {
+        const int row = i / (NC / 2), col = (i % (NC / 2)) * 2;
+        float v0 = 0.0f, v1 = 0.0f;
+        for (unsigned s = 0; s < gridDim.y; ++s) {
+            const float2 p = __ldcg(reinterpret_cast<const float2*>(all + s * (kT * NC) + row * NC + col));
+            v0 += p.x;
+            v1 += p.y;
+        }
+        emit(row, col, v0, v1);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// y = v W^T of a tile (RC columns of v): W [N][RC], or with TRANS [RC][N].
+// A CTA takes kNB columns of y in pieces of 64; the fragments of v stay in
+// registers. Epilogue: fp32 y, or bf16(factor[n] raw + y).
+// ---------------------------------------------------------------------------
+constexpr int kNB = 256;
+template <int RC>
+constexpr int expand_smem() { return 3 * 64 * RC * 2; }
+
+template <int RC, bool TRANS, int NW>
+__global__ void __launch_bounds__(kThr) expand_kernel(const LrExpand a) {
+    constexpr int kPiece = 64 * RC * 2;
+    extern __shared__ __align__(128) uint8_t smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    int slot, pos0, n;
+    if (!tile_of(a.tok, blockIdx.x, slot, pos0, n)) return;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int z = blockIdx.z;
+    const int n0 = blockIdx.y * kNB, n1 = min(a.N, n0 + kNB);
+    const int pieces = (n1 - n0 + 63) / 64;
+    const __nv_bfloat16* w = a.w + (size_t)max(slot, 0) * a.w_slot + (size_t)z * a.w_z;
+    const uint32_t base = smem_u32(smem);
+    const int row0 = warp * 16 + g;
+    int tok[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int r = row0 + 8 * h;
+        tok[h] = r < n ? (a.tok.perm ? a.tok.perm[pos0 + r] : pos0 + r) : -1;
+    }
+    auto load = [&](int p, int stage) {
+        constexpr int kC = 64 * RC / 8;
+        const int nb = n0 + p * 64;
+#pragma unroll
+        for (int i = 0; i < kC / kThr; ++i) {
+            const int k = tid + i * kThr;
+            if (TRANS) {
+                const int r = k >> 3, c = k & 7;
+                const bool live = nb + c * 8 < a.N;
+                cp16(base + stage * kPiece + sw<8>(r, c), w + (live ? (size_t)r * a.N + nb + c * 8 : 0), live);
+            } else {
+                const int r = k / (RC / 8), c = k % (RC / 8);
+                const bool live = nb + r < a.N;
+                cp16(base + stage * kPiece + sw<RC / 8>(r, c), w + (live ? (size_t)(nb + r) * RC + c * 8 : 0), live);
+            }
+        }
+        cp_commit();
+    };
+    uint32_t af[RC / 16][NW][4];
+    if (slot >= 0) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            if (p < pieces) load(p, p);
+            else cp_commit();
+        }
+#pragma unroll
+        for (int k = 0; k < RC / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = row0 + 8 * (e & 1);
+                const __nv_bfloat16* o = a.v + (size_t)(pos0 + r) * a.ldv + z * RC + k * 16 + 2 * t + 8 * (e >> 1);
+#pragma unroll
+                for (int i = 0; i < NW; ++i)
+                    af[k][i][e] = r < n ? *reinterpret_cast<const uint32_t*>(o + i * a.v_word) : 0u;
+            }
+    }
+    for (int p = 0; p < pieces; ++p) {
+        float acc[8][4];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.0f;
+        if (slot >= 0) {
+            cp_wait<1>();
+            __syncthreads();
+            if (p + 2 < pieces) load(p + 2, (p + 2) % 3);
+            else cp_commit();
+            if (warp * 16 < n) {
+                const uint32_t sb = base + (p % 3) * kPiece;
+#pragma unroll
+                for (int k = 0; k < RC / 16; ++k)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t b[4];
+                        load_b<TRANS, TRANS ? 8 : RC / 8>(sb, j * 16, k * 16, lane, b);
+#pragma unroll
+                        for (int i = 0; i < NW; ++i) {
+                            mma_bf16(acc[2 * j], af[k][i], b[0], b[1]);
+                            mma_bf16(acc[2 * j + 1], af[k][i], b[2], b[3]);
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int col = n0 + p * 64 + j * 8 + 2 * t;
+            if (col >= a.N) continue;  // N is even
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (tok[h] < 0) continue;
+                const float v0 = acc[j][2 * h], v1 = acc[j][2 * h + 1];
+                if (a.out) {
+                    const float2 r = *reinterpret_cast<const float2*>(a.raw + (size_t)tok[h] * a.N + col);
+                    const float f0 = a.factor ? a.factor[col] : a.factor_all, f1 = a.factor ? a.factor[col + 1] : a.factor_all;
+                    *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)tok[h] * a.N + col) =
+                        __floats2bfloat162_rn(r.x * f0 + v0, r.y * f1 + v1);
+                } else {
+                    *reinterpret_cast<float2*>(a.y + (size_t)tok[h] * a.ldy + (size_t)z * a.N + col) = make_float2(v0, v1);
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens (M <= kLrFew): each names its slot itself; no plan.
+// ---------------------------------------------------------------------------
+QMLP_DEV float dot8(const uint4& a, const uint4& b, float s) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), s);
+        s = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), s);
+    }
+    return s;
+}
+
+// v[m, j] = c A[slot(m)][j] . x[m]: a CTA a (row j, token m).
+__global__ void __launch_bounds__(kThr) shrink_few_kernel(const LrFew a) {
+    pdl_launch_dependents();
+    const int j = blockIdx.x, m = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    const int slot = a.ids[m];
+    const bool has = slot >= 0 && slot < a.slots && a.rank[slot] > j % a.Rp;
+    float s = 0.0f;
+    if (has) {
+        const uint4* x = reinterpret_cast<const uint4*>(a.x + (size_t)m * a.D);
+        const uint4* w = reinterpret_cast<const uint4*>(a.w + (size_t)slot * a.w_slot + (size_t)j * a.D);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < a.D / 8; i += kThr) s = dot8(__ldg(x + i), __ldg(w + i), s);
+    }
+    __shared__ float red[kThr / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane == 0) red[warp] = s;
+    __syncthreads();
+    if (threadIdx.x == 0)
+        a.v[(size_t)m * a.ncol + j] = has ? (red[0] + red[1] + red[2] + red[3]) * a.scale[slot] : 0.0f;
+}
+
+// y[m, n] = sum_j v[m, j] B[slot(m)][n][j]: a thread an n, the tokens in turn.
+__global__ void __launch_bounds__(kThr) expand_few_kernel(const LrFew a) {
+    pdl_launch_dependents();
+    const int n = blockIdx.x * kThr + threadIdx.x, z = blockIdx.z, m = blockIdx.y;
+    pdl_wait();
+    if (n >= a.D) return;
+    const int slot = a.ids[m];
+    float s = 0.0f;
+    if (slot >= 0 && slot < a.slots && a.rank[slot] > 0) {
+        const uint4* b = reinterpret_cast<const uint4*>(a.w + (size_t)slot * a.w_slot + ((size_t)z * a.D + n) * a.Rp);
+        const float* v = a.v + (size_t)m * a.ncol + z * a.Rp;
+        const int nr = (a.rank[slot] + 7) / 8;
+        for (int i = 0; i < nr; ++i) {
+            const uint4 q = __ldg(b + i);
+            const uint32_t y[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s = fmaf(v[i * 8 + 2 * e], __uint_as_float(y[e] << 16), s);
+                s = fmaf(v[i * 8 + 2 * e + 1], __uint_as_float(y[e] & 0xFFFF0000u), s);
+            }
+        }
+    }
+    if (a.out) {
+        const float f = a.factor ? a.factor[n] : a.factor_all;
+        a.out[(size_t)m * a.D + n] = __float2bfloat16_rn(a.raw[(size_t)m * a.D + n] * f + s);
+    } else {
+        a.y[(size_t)m * a.ldy + (size_t)z * a.D + n] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// act = bf16(SiLU(fg raw_g + y_g) * (fu raw_u + y_u)), y = [M][2I] the adapters'
+// terms: shapes whose gate/up kernels cannot add them themselves.
+__global__ void __launch_bounds__(256) swiglu_raw_kernel(const LrSwiGLU a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long i = (long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (long)a.M * a.I) return;
+    const int m = (int)(i / a.I), n = (int)(i % a.I);
+    const float g = a.raw_g[i] * (a.fg ? a.fg[n] : a.fg_all) + a.y[(size_t)m * 2 * a.I + n];
+    const float u = a.raw_u[i] * (a.fu ? a.fu[n] : a.fu_all) + a.y[(size_t)m * 2 * a.I + a.I + n];
+    a.act[i] = __float2bfloat16_rn(silu_f32(g) * u);
+}
+
+// Tokens grouped by slot: perm holds the tokens slot by slot (those without an
+// adapter last), tiles the {slot or -1, first position, tokens} of at most 64.
+// One CTA; the order of a slot's tokens is left to the atomics (no result
+// depends on it).
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids, int M, int slots,
+                                                    const int* __restrict__ rank, int* perm, int4* tiles,
+                                                    int* n_tiles) {
+    __shared__ int cnt[kLrMaxSlots + 1], pos[kLrMaxSlots + 1];
+    __shared__ int wsum[2][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i <= slots; i += 1024) cnt[i] = 0;
+    __syncthreads();
+    auto group = [&](int m) {
+        const int s = ids[m];
+        return s >= 0 && s < slots && rank[s] > 0 ? s : slots;
+    };
+    // one atomic a warp and group: the lanes of a group find each other first
+    auto claim = [&](int* at, int gr) {
+        const unsigned mask = __match_any_sync(0xffffffffu, gr);
+        const int lead = __ffs(mask) - 1;
+        int b = 0;
+        if (lane == lead && gr >= 0) b = atomicAdd(&at[gr], __popc(mask));
+        return __shfl_sync(0xffffffffu, b, lead) + __popc(mask & ((1u << lane) - 1u));
+    };
+    for (int m = tid; m < (M + 31) / 32 * 32; m += 1024) claim(cnt, m < M ? group(m) : -1);
+    __syncthreads();
+    // exclusive sums over the groups of tokens and of tiles, 1024 groups a round
+    int tok0 = 0, til0 = 0;
+    for (int b = 0; b <= slots; b += 1024) {
+        const int i = b + tid;
+        const int c = i <= slots ? cnt[i] : 0, tl = (c + kT - 1) / kT;
+        int sc = c, st = tl;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, sc, o), v = __shfl_up_sync(0xffffffffu, st, o);
+            if (lane >= o) sc += u, st += v;
+        }
+        if (lane == 31) wsum[0][warp] = sc, wsum[1][warp] = st;
+        __syncthreads();
+        int bc = tok0, bt = til0, ac = 0, at = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) bc += wsum[0][w], bt += wsum[1][w];
+            ac += wsum[0][w], at += wsum[1][w];
+        }
+        if (i <= slots) {
+            const int p0 = bc + sc - c;
+            pos[i] = p0;
+            for (int k = 0; k < tl; ++k)
+                tiles[bt + st - tl + k] = make_int4(i < slots ? i : -1, p0 + k * kT, min(kT, c - k * kT), 0);
+        }
+        tok0 += ac;
+        til0 += at;
+        __syncthreads();
+    }
+    for (int m = tid; m < (M + 31) / 32 * 32; m += 1024) {
+        const int at = claim(pos, m < M ? group(m) : -1);
+        if (m < M) perm[at] = m;
+    }
+    if (tid == 0) *n_tiles = til0;
+}
+
+// One adapter into a slot's padded rows: A [r, D] -> [Rp][D], B [N, r] ->
+// [N][Rp] (B / div[n] where div is given, in two bf16 words), zero past r or
+// where the projection is not adapted.
+__global__ void __launch_bounds__(256) pack_kernel(const LrPack a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int p = blockIdx.y;  // 0..2: A of gate, up, down; 3..5: B
+    const LrPackPart& q = a.part[p];
+    const long total = (long)q.rows * q.cols;
+    for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long)gridDim.x * blockDim.x) {
+        const int row = (int)(i / q.cols), col = (int)(i % q.cols);
+        // A: rows are the rank; B: columns are
+        const bool in = q.src && (p < 3 ? row : col) < a.r;
+        __nv_bfloat16 v = __float2bfloat16_rn(0.0f);
+        if (in) v = q.src[p < 3 ? (size_t)row * q.cols + col : (size_t)row * a.r + col];
+        q.dst[i] = v;
+        if (q.dst_h) {
+            __nv_bfloat16 d[2];
+            split_bf16(__bfloat162float(v) / (q.div ? q.div[row] : q.div_all), d);
+            q.dst_h[i] = d[0];
+            q.dst_l[i] = d[1];
+        }
+    }
+    if (p == 0 && blockIdx.x == 0 && threadIdx.x == 0) {
+        *a.rank_out = a.r;
+        *a.scale_out = a.scale;
+    }
+}
+
+template <typename K, typename A>
+cudaError_t launch_pdl(K kern, dim3 grid, int threads, int smem, const A& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <int NC, bool TRANS, bool TWO>
+cudaError_t shrink_t(const LrShrink& a, int tiles, int splits, int zs, cudaStream_t s) {
+    static bool attr = false;
+    using S = ShrinkSmem<NC, TRANS, TWO>;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(shrink_kernel<NC, TRANS, TWO>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, S::Bytes);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    return launch_pdl(shrink_kernel<NC, TRANS, TWO>, dim3(tiles, splits, zs), kThr, S::Bytes, a, s);
+}
+template <bool TRANS, bool TWO>
+cudaError_t shrink_n(const LrShrink& a, int nc, int tiles, int splits, int zs, cudaStream_t s) {
+    switch (nc) {
+        case 16: return shrink_t<16, TRANS, TWO>(a, tiles, splits, zs, s);
+        case 32: return shrink_t<32, TRANS, TWO>(a, tiles, splits, zs, s);
+        case 64: return shrink_t<64, TRANS, TWO>(a, tiles, splits, zs, s);
+        case 128:
+            if constexpr (!TRANS) return shrink_t<128, false, false>(a, tiles, splits, zs, s);
+    }
+    return cudaErrorInvalidValue;
+}
+template <int RC, bool TRANS, int NW>
+cudaError_t expand_t(const LrExpand& a, int tiles, int zs, cudaStream_t s) {
+    static bool attr = false;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(expand_kernel<RC, TRANS, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   expand_smem<RC>());
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    return launch_pdl(expand_kernel<RC, TRANS, NW>, dim3(tiles, (a.N + kNB - 1) / kNB, zs), kThr, expand_smem<RC>(), a, s);
+}
+
+}  // namespace
+
+int lr_max_tiles(int M, int slots) { return M / kT + std::min(slots + 1, M) + 1; }
+
+// Splits of the contraction: enough CTAs for three on an SM, steps left for
+// the pipeline to run, and no more partials than the buffer holds.
+int lr_shrink_splits(int tiles, int zs, int D, int num_sms) {
+    const int steps = (D + kStep - 1) / kStep;
+    return std::max(1, std::min({3 * num_sms / std::max(1, tiles * zs), steps / 4, kLrMaxSplits}));
+}
+// Floats of the partials: where the contraction is split at all, tiles * splits
+// * zs <= 3 num_sms, of 64 x 128 floats at most.
+size_t lr_part_elems(int num_sms) { return (size_t)3 * num_sms * kT * 128; }
+
+cudaError_t launch_lr_shrink(const LrShrink& a, int nc, bool trans, int tiles, int zs, int num_sms, cudaStream_t s) {
+    const int splits = lr_shrink_splits(tiles, zs, a.D, num_sms);
+    if (!trans) return shrink_n<false, false>(a, nc, tiles, splits, zs, s);
+    return a.w_lo ? shrink_n<true, true>(a, nc, tiles, splits, zs, s) : shrink_n<true, false>(a, nc, tiles, splits, zs, s);
+}
+
+cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, int zs, cudaStream_t s) {
+    switch (rc) {
+        case 16: return trans ? expand_t<16, true, 2>(a, tiles, zs, s) : expand_t<16, false, 3>(a, tiles, zs, s);
+        case 32: return trans ? expand_t<32, true, 2>(a, tiles, zs, s) : expand_t<32, false, 3>(a, tiles, zs, s);
+        case 64: return trans ? expand_t<64, true, 2>(a, tiles, zs, s) : expand_t<64, false, 3>(a, tiles, zs, s);
+        case 128:
+            if (trans) return expand_t<128, true, 2>(a, tiles, zs, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_lr_shrink_few(const LrFew& a, int M, cudaStream_t s) {
+    return launch_pdl(shrink_few_kernel, dim3(a.ncol, M), kThr, 0, a, s);
+}
+cudaError_t launch_lr_expand_few(const LrFew& a, int M, int zs, cudaStream_t s) {
+    return launch_pdl(expand_few_kernel, dim3((a.D + kThr - 1) / kThr, M, zs), kThr, 0, a, s);
+}
+
+cudaError_t launch_lr_swiglu_raw(const LrSwiGLU& a, cudaStream_t s) {
+    const long n = (long)a.M * a.I;
+    return launch_pdl(swiglu_raw_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, a, s);
+}
+
+cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, int* perm, int4* tiles, int* n_tiles,
+                           cudaStream_t s) {
+    if (slots < 1 || slots > kLrMaxSlots) return cudaErrorInvalidValue;
+    plan_kernel<<<1, 1024, 0, s>>>(ids, M, slots, rank, perm, tiles, n_tiles);
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_lr_pack(const LrPack& a, cudaStream_t s) {
+    pack_kernel<<<dim3(256, 6), 256, 0, s>>>(a);
+    return cudaPeekAtLastError();
+}
+
+}  // namespace qmlp

@@ -1,0 +1,117 @@
+// lowrank.cuh -- launch arguments of the low-rank products (lowrank.cu).
+#pragma once
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace qmlp {
+
+constexpr int kLrTile = 64;       // tokens of a tile
+constexpr int kLrMaxRank = 64;
+constexpr int kLrWords = 3;       // bf16 words of a value of v
+constexpr int kLrMaxSlots = 1024;
+constexpr int kLrMaxSplits = 32;
+constexpr int kLrFew = 16;        // tokens the kernels without a plan take
+
+// Which tokens a tile holds: tiles null: one adapter, 64 consecutive tokens.
+struct LrTokens {
+    const int4* tiles = nullptr;  // {slot or -1, first position, tokens}
+    const int* n_tiles = nullptr;
+    const int* perm = nullptr;    // position -> token
+    int M = 0;
+};
+
+struct LrShrink {
+    LrTokens tok;
+    const __nv_bfloat16* x = nullptr;  // [M][ldx], D columns from z * x_z on
+    size_t ldx = 0, x_z = 0;
+    int D = 0;
+    const __nv_bfloat16* w = nullptr;     // slot and part strides in elements
+    const __nv_bfloat16* w_lo = nullptr;  // second word of w, or null
+    size_t w_slot = 0, w_z = 0;
+    const float* scale = nullptr;  // per slot
+    __nv_bfloat16* v = nullptr;    // kLrWords planes of [position][ldv], columns z * NC on
+    size_t v_word = 0;             // elements of a plane
+    int ldv = 0;
+    float* part = nullptr;
+    int* cnt = nullptr;            // a zeroed counter a tile and part
+};
+
+struct LrExpand {
+    LrTokens tok;
+    const __nv_bfloat16* v = nullptr;
+    size_t v_word = 0;
+    int ldv = 0;
+    const __nv_bfloat16* w = nullptr;
+    size_t w_slot = 0, w_z = 0;
+    int N = 0;
+    float* y = nullptr;  // fp32 [M][ldy], columns z * N on
+    size_t ldy = 0;
+    // or out = bf16(factor raw + y)
+    __nv_bfloat16* out = nullptr;
+    const float* raw = nullptr;     // fp32 [M][N]
+    const float* factor = nullptr;  // per column, or factor_all
+    float factor_all = 1.0f;
+};
+
+struct LrFew {
+    const int* ids = nullptr;  // [M]
+    const int* rank = nullptr;
+    const float* scale = nullptr;
+    int slots = 0, Rp = 0;
+    const __nv_bfloat16* x = nullptr;  // shrink: [M][D]
+    const __nv_bfloat16* w = nullptr;
+    size_t w_slot = 0;
+    int D = 0;           // shrink: contraction; expand: columns of a part
+    int ncol = 0;        // columns of v
+    float* v = nullptr;  // [M][ncol]
+    float* y = nullptr;  // expand: as LrExpand
+    size_t ldy = 0;
+    __nv_bfloat16* out = nullptr;
+    const float* raw = nullptr;
+    const float* factor = nullptr;
+    float factor_all = 1.0f;
+};
+
+struct LrSwiGLU {
+    const float* raw_g = nullptr;  // [M][I]
+    const float* raw_u = nullptr;
+    const float* y = nullptr;      // [M][2I]
+    const float* fg = nullptr;     // factors per column, or fg_all / fu_all
+    const float* fu = nullptr;
+    float fg_all = 1.0f, fu_all = 1.0f;
+    __nv_bfloat16* act = nullptr;
+    int M = 0, I = 0;
+};
+
+struct LrPackPart {
+    const __nv_bfloat16* src = nullptr;
+    __nv_bfloat16* dst = nullptr;
+    int rows = 0, cols = 0;  // of dst
+    __nv_bfloat16* dst_h = nullptr;  // B / div in two words, or null
+    __nv_bfloat16* dst_l = nullptr;
+    const float* div = nullptr;
+    float div_all = 1.0f;
+};
+struct LrPack {
+    LrPackPart part[6];
+    int r = 0;
+    float scale = 0.0f;
+    int* rank_out = nullptr;
+    float* scale_out = nullptr;
+};
+
+int lr_max_tiles(int M, int slots);
+int lr_shrink_splits(int tiles, int zs, int D, int num_sms);
+size_t lr_part_elems(int num_sms);
+cudaError_t launch_lr_shrink(const LrShrink& a, int nc, bool trans, int tiles, int zs, int num_sms, cudaStream_t s);
+cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, int zs, cudaStream_t s);
+cudaError_t launch_lr_shrink_few(const LrFew& a, int M, cudaStream_t s);
+cudaError_t launch_lr_expand_few(const LrFew& a, int M, int zs, cudaStream_t s);
+cudaError_t launch_lr_swiglu_raw(const LrSwiGLU& a, cudaStream_t s);
+cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, int* perm, int4* tiles, int* n_tiles,
+                           cudaStream_t s);
+cudaError_t launch_lr_pack(const LrPack& a, cudaStream_t s);
+
+}  // namespace qmlp
