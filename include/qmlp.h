@@ -451,6 +451,54 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
                               qmlp_stream_t stream);
 
 /*
+ * Training through the dense MLP: its forward, keeping what the backward pass
+ * needs, and the backward pass through the frozen quantized weights, with one
+ * low-rank adapter or none. With d = the gradient of a loss by ...:
+ *   dact = (dout sigma_d) Wd + c (dout B_d) A_d
+ *   dg = dact u SiLU'(g),  du = dact SiLU(g)
+ *   dx = (dg sigma_g) Wg + (du sigma_u) Wu + c (dg B_g) A_g + c (du B_u) A_u
+ *   dB_p = c dy^T (z A_p^T),  dA_p = c (dy B_p)^T z    (z the projection's input, dy its output's gradient)
+ * Sums are fp32; g and u are kept in fp32, act in bf16; dg sigma_g and du
+ * sigma_u are rounded once to bf16 between the two products. dx and the
+ * adapter's gradients are bf16. The sums' order depends on the sizes alone:
+ * the same call gives the same bytes.
+ */
+typedef struct qmlp_train_s qmlp_train_t;
+
+/* Make the training workspace of h (made with max_M >= 768, K % 256 == 0 and
+ * I % 128 == 0: the dequantise-once GEMM), which must outlive it, for adapters
+ * of ranks up to max_rank (1..64). It shares h's workspace: calls on it and on
+ * h go on one stream at a time. Synchronizes `stream`.
+ * Errors: INVALID_ARG (null; an NVFP4 factor 1/global under 2^-60), SHAPE,
+ * OOM, CUDA. */
+qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_stream_t stream);
+void qmlp_train_destroy(qmlp_train_t* t);
+
+/* Bytes of the buffer that a forward of M tokens fills for its backward pass
+ * (about 10 M I); 0 where M is out of range. */
+size_t qmlp_train_saved_bytes(qmlp_train_t* t, int M);
+
+/* The block as qmlp_lora_forward with one adapter for every token (NULL:
+ * none), for any 1 <= M <= max_M.
+ *  x = device bf16 [M, K];  out = device bf16 [M, K]
+ *  saved = device, qmlp_train_saved_bytes(t, M) bytes, 16-byte aligned
+ * Allocates nothing; can be captured in a CUDA graph.
+ * Errors: as qmlp_forward and qmlp_lora_set. */
+qmlp_status qmlp_train_forward(qmlp_train_t* t, const qmlp_adapter* adapter, const void* x, int M, void* out,
+                               void* saved, qmlp_stream_t stream);
+
+/* The backward pass of the forward that filled `saved` with the same x, M and
+ * adapter (only read).
+ *  dout = device bf16 [M, K];  dx = device bf16 [M, K]
+ *  grads = where the gradients of the adapter's parts go: bf16, shaped and
+ *          packed as the parts; a NULL part (or grads NULL) is not wanted.
+ *          rank and scale are not read. Without an adapter: NULL.
+ * Errors: as qmlp_train_forward (INVALID_ARG: gradients without an adapter or
+ * of a part that it lacks). */
+qmlp_status qmlp_train_backward(qmlp_train_t* t, const qmlp_adapter* adapter, const void* x, int M, const void* saved,
+                                const void* dout, void* dx, const qmlp_adapter* grads, qmlp_stream_t stream);
+
+/*
  * AdamW over many tensors at once (one launch a step), for the adapters and
  * other small tensors trained beside the frozen weights. For every element,
  * in fp32, with step number t:

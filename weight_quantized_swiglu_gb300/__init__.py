@@ -111,6 +111,12 @@ _SIGS = {
     "qmlp_lora_destroy": ([_VP], None),
     "qmlp_lora_set": ([_VP, _I, ctypes.POINTER(qmlp_adapter), _VP], _I),
     "qmlp_lora_forward": ([_VP, _VP, _VP, _I, _VP, _VP], _I),
+    "qmlp_train_create": ([ctypes.POINTER(_VP), _VP, _I, _VP], _I),
+    "qmlp_train_destroy": ([_VP], None),
+    "qmlp_train_saved_bytes": ([_VP, _I], ctypes.c_size_t),
+    "qmlp_train_forward": ([_VP, ctypes.POINTER(qmlp_adapter), _VP, _I, _VP, _VP, _VP], _I),
+    "qmlp_train_backward": ([_VP, ctypes.POINTER(qmlp_adapter), _VP, _I, _VP, _VP, _VP,
+                             ctypes.POINTER(qmlp_adapter), _VP], _I),
     "qmlp_adamw_create": ([ctypes.POINTER(_VP), ctypes.POINTER(qmlp_adamw_tensor), _I, _I, _I, _I, _VP], _I),
     "qmlp_adamw_destroy": ([_VP], None),
     "qmlp_adamw_step": ([_VP, ctypes.POINTER(qmlp_adamw_hyper), _VP], _I),
@@ -316,6 +322,34 @@ def qmlp_lora_set(p, slot, adapter: qmlp_adapter | None, stream=None) -> int:
 
 def qmlp_lora_forward(p, x, ids, M, out, stream=None) -> int:
     return lib().qmlp_lora_forward(p, _ptr(x), _ptr(ids), M, _ptr(out), _stream(stream))
+
+
+def qmlp_train_create(h, max_rank, stream=None) -> int:
+    p = ctypes.c_void_p()
+    st = lib().qmlp_train_create(ctypes.byref(p), h, max_rank, _stream(stream))
+    _chk(st, "qmlp_train_create")
+    return p.value
+
+
+def qmlp_train_destroy(p: int):
+    lib().qmlp_train_destroy(p)
+
+
+def qmlp_train_saved_bytes(p, M) -> int:
+    return lib().qmlp_train_saved_bytes(p, M)
+
+
+def _ref(c):
+    return None if c is None else ctypes.byref(c)
+
+
+def qmlp_train_forward(p, adapter, x, M, out, saved, stream=None) -> int:
+    return lib().qmlp_train_forward(p, _ref(adapter), _ptr(x), M, _ptr(out), _ptr(saved), _stream(stream))
+
+
+def qmlp_train_backward(p, adapter, x, M, saved, dout, dx, grads, stream=None) -> int:
+    return lib().qmlp_train_backward(p, _ref(adapter), _ptr(x), M, _ptr(saved), _ptr(dout), _ptr(dx), _ref(grads),
+                                     _stream(stream))
 
 
 def qmlp_adamw_create(tensors, pdt, gdt, state, stream=None) -> int:
@@ -543,6 +577,52 @@ class LoraMLP:
     def close(self):
         if getattr(self, "h", None):
             qmlp_lora_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class TrainMLP:
+    """Forward and backward of a QuantMLP with frozen weights and one low-rank
+    adapter or none (qmlp_train_*). The QuantMLP has to stay open while this
+    object is."""
+
+    def __init__(self, mlp: QuantMLP, max_rank: int, stream=None):
+        self.mlp = mlp
+        self.h = qmlp_train_create(mlp.h, max_rank, stream)
+
+    def saved_bytes(self, M):
+        """Bytes of the buffer that forward fills for backward."""
+        return qmlp_train_saved_bytes(self.h, M)
+
+    def _adapter(self, a):
+        if a is None:
+            return None
+        a.check(self.mlp.K, self.mlp.I)
+        return a.c
+
+    def forward(self, x, out, saved, adapter: Adapter | None = None, M=None, stream=None):
+        """x, out [M, K] bf16; saved: saved_bytes(M) bytes on the device."""
+        M = x.shape[0] if M is None else M
+        _chk(qmlp_train_forward(self.h, self._adapter(adapter), x, M, out, saved, stream), "qmlp_train_forward")
+        return out
+
+    def backward(self, x, saved, dout, dx, adapter: Adapter | None = None, grads: Adapter | None = None, M=None,
+                 stream=None):
+        """dout, dx [M, K] bf16; grads: the tensors that take the gradients of
+        the adapter's parts (its scale is not used)."""
+        M = x.shape[0] if M is None else M
+        _chk(qmlp_train_backward(self.h, self._adapter(adapter), x, M, saved, dout, dx, self._adapter(grads), stream),
+             "qmlp_train_backward")
+        return dx
+
+    def close(self):
+        if getattr(self, "h", None):
+            qmlp_train_destroy(self.h)
             self.h = None
 
     def __del__(self):

@@ -30,6 +30,32 @@ struct qmlp_lora_s {
     Owner mem;
 };
 
+// The workspace of forward and backward with frozen weights.
+struct qmlp_train_s {
+    qmlp_t* h = nullptr;
+    qmlp_lora_t* l = nullptr;        // one slot: the call's adapter
+    uint8_t* img_t = nullptr;        // images of the transposed down projection
+    size_t img_t_bytes = 0;
+    __nv_bfloat16* bq = nullptr;     // two words of [2][I][Rp]: B of gate and up over the factors
+    __nv_bfloat16* dgu = nullptr;    // [max_M][2I]: d gate, d up times their factors
+    __nv_bfloat16* dgu_lo = nullptr; // [kTwoWordM][2I]: what their rounding leaves
+    __nv_bfloat16* dv = nullptr;     // kLrWords planes of [max_M][2 Rp]
+    __nv_bfloat16* dvd = nullptr;    // likewise [max_M][Rp]
+    float* part = nullptr;
+    int* cnt = nullptr;
+    // FP8: the factors that d gate and d up carry (1 where a channel's is too
+    // small to divide by: it is then in the weights' image, `row`)
+    float* eff = nullptr;            // [2][I]
+    float* row = nullptr;            // [2][I]
+    Owner mem;
+};
+
+// Fewer tokens than this: act, d gate and d up are kept in two bf16 words for
+// the products with the adapter, whose r sums a token are few enough for a
+// rounding of their terms to show in a gradient; over more tokens it averages
+// out. (One token, rank 4: the gradient of A 5.4e-3 off with one word.)
+constexpr int kTwoWordM = 256;
+
 struct qmlp_adamw_s {
     AdamWChunk* chunks = nullptr;
     long count = 0;
@@ -38,6 +64,17 @@ struct qmlp_adamw_s {
 };
 
 namespace {
+
+constexpr float kLeastFactor = 8.673617e-19f;  // 2^-60
+
+__global__ void __launch_bounds__(256) factors_kernel(const float* g, const float* u, int I, float* eff, float* row) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= 2 * I) return;
+    const float f = i < I ? g[i] : u[i - I];
+    const bool big = !(fabsf(f) < kLeastFactor);
+    eff[i] = big ? f : 1.0f;
+    row[i] = big ? 1.0f : f;
+}
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
@@ -311,6 +348,429 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
     t.add_down = l->y;
     t.between = [&](cudaStream_t st) { return terms(true, h->act, st); };
     return run_gemm(h, QMLP_PATH_AUTO, 3, x, M, out, s, nullptr, &t);
+}
+
+// ---------------------------------------------------------------------------
+// training
+// ---------------------------------------------------------------------------
+extern "C++" {
+namespace {
+
+// What a forward keeps (see qmlp_train_saved_bytes).
+struct Saved {
+    uint8_t *g, *u;          // fp32 gate and up, in quads of 32 rows
+    __nv_bfloat16* act;      // [M][I]
+    __nv_bfloat16* act_lo;   // likewise, its second word (M < kTwoWordM), or null
+    __nv_bfloat16 *vgu, *vd; // words of [M][2 Rp] and [M][Rp]
+    size_t bytes;
+};
+Saved saved_of(const qmlp_train_s* t, int M, const void* base) {
+    const size_t I = t->h->I, R = t->l->Rp, m = M;
+    Saved v;
+    size_t at = reinterpret_cast<size_t>(base);
+    auto take = [&](size_t bytes) {
+        const size_t p = at;
+        at += (bytes + 255) / 256 * 256;
+        return reinterpret_cast<uint8_t*>(p);
+    };
+    v.g = take(gemm_gu_bytes(M, (int)I));
+    v.u = take(gemm_gu_bytes(M, (int)I));
+    v.act = reinterpret_cast<__nv_bfloat16*>(take(m * I * 2));
+    v.act_lo = M < kTwoWordM ? reinterpret_cast<__nv_bfloat16*>(take(m * I * 2)) : nullptr;
+    v.vgu = reinterpret_cast<__nv_bfloat16*>(take(kLrWords * m * 2 * R * 2));
+    v.vd = reinterpret_cast<__nv_bfloat16*>(take(kLrWords * m * R * 2));
+    v.bytes = at - reinterpret_cast<size_t>(base);
+    return v;
+}
+
+int tiles_for(int M) { return (M + kLrTile - 1) / kLrTile; }
+
+// v = c z W^T for every token (one adapter), W [nc][D] or, trans, [D][nc].
+LrShrink shrink_all(const qmlp_train_s* t, const void* z, int M, int D, __nv_bfloat16* v, int ldv) {
+    LrShrink a;
+    a.tok.M = M;
+    a.x = static_cast<const __nv_bfloat16*>(z);
+    a.ldx = D;
+    a.D = D;
+    a.scale = t->l->scale;
+    a.v = v;
+    a.v_word = (size_t)M * ldv;
+    a.ldv = ldv;
+    a.part = t->l->part;
+    a.cnt = t->l->cnt;
+    return a;
+}
+// The adapter's terms into l->y: v W^T, W [N][rc] or, trans, [rc][N].
+cudaError_t expand_all(const qmlp_train_s* t, const __nv_bfloat16* v, int M, int rc, int zs, const __nv_bfloat16* w,
+                       size_t w_z, int N, bool trans, cudaStream_t s) {
+    LrExpand a;
+    a.tok.M = M;
+    a.v = v;
+    a.ldv = rc * zs;
+    a.v_word = (size_t)M * a.ldv;
+    a.w = w;
+    a.w_z = w_z;
+    a.N = N;
+    a.y = t->l->y;
+    a.ldy = (size_t)N * zs;
+    return launch_lr_expand(a, rc, trans, tiles_for(M), zs, s);
+}
+
+GemmLaunch dq_gemm(const qmlp_train_s* t, int M) {
+    qmlp_t* h = t->h;
+    GemmLaunch g;
+    g.M = M;
+    g.pair = kDqPair && M >= kPairMinM;
+    g.err = h->err;
+    g.a16 = h->a16;
+    g.sig = h->sig;
+    g.ws = h->gemm_ws;
+    g.wait_ns = h->wait_ns;
+    g.withhold = h->withhold;
+    g.images_ready = true;
+    return g;
+}
+
+// Work on the handle's side stream between the events: `fork` follows all that
+// is on s, and the caller waits for ev_join.
+template <typename F>
+cudaError_t beside(qmlp_t* h, cudaStream_t s, F&& f) {
+    cudaError_t e = cudaEventRecord(h->ev_fork, s);
+    if (e == cudaSuccess) e = cudaStreamWaitEvent(h->side, h->ev_fork, 0);
+    if (e == cudaSuccess) e = f(h->side);
+    if (e == cudaSuccess) e = cudaEventRecord(h->ev_join, h->side);
+    return e;
+}
+
+#define TRY(call)                                          \
+    do {                                                   \
+        const cudaError_t try_e = (call);                  \
+        if (try_e != cudaSuccess) return try_e;            \
+    } while (0)
+
+LrPack pack_train(const qmlp_train_s* t, const qmlp_adapter* a, bool back) {
+    const qmlp_lora_t* l = t->l;
+    LrPack p = pack_of(l, 0, a);
+    if (!back) return p;
+    const size_t n = (size_t)t->h->I * l->Rp;
+    for (int i = 0; i < 2; ++i) {  // gate, up: over the factor that their gradients carry
+        LrPackPart& q = p.part[3 + i];
+        q.dst_h = t->bq + i * n;
+        q.dst_l = t->bq + (2 + i) * n;
+        q.div = t->eff ? t->eff + (size_t)i * t->h->I : nullptr;
+        q.div_all = t->h->gv[i].inv_g;
+    }
+    return p;
+}
+
+cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x, int M, void* out, const Saved& v,
+                          cudaStream_t s) {
+    qmlp_t* h = t->h;
+    const qmlp_lora_t* l = t->l;
+    const int K = h->K, I = h->I, R = l->Rp;
+    TRY(launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s));
+    TRY(beside(h, s, [&](cudaStream_t b) {
+        return launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, b);
+    }));
+    if (ad) {
+        TRY(launch_lr_pack(pack_train(t, ad, false), s));
+        LrShrink a = shrink_all(t, x, M, K, v.vgu, 2 * R);
+        a.w = l->a_gu;
+        TRY(launch_lr_shrink(a, 2 * R, false, tiles_for(M), 1, h->num_sms, s));
+        TRY(expand_all(t, v.vgu, M, R, 2, l->b_gu, (size_t)I * R, I, false, s));
+    }
+    GemmLaunch g = dq_gemm(t, M);
+    g.epi = kEpiSwiGLU;
+    g.w = h->gm_gu;
+    g.wdec = h->wdec;
+    g.wdec_bytes = h->wdec_bytes;
+    g.a = x;
+    g.out = v.act;
+    g.gu_g = v.g;
+    g.gu_u = v.u;
+    if (ad) {
+        g.out_lo = v.act_lo;
+        g.add = l->y;
+        g.ldadd = (size_t)2 * I;
+    }
+    TRY(launch_gemm(g, h->num_sms, s));
+    if (ad) {
+        LrShrink a = shrink_all(t, v.act, M, I, v.vd, R);
+        a.x_lo = v.act_lo;
+        a.w = l->a_d;
+        TRY(launch_lr_shrink(a, R, false, tiles_for(M), 1, h->num_sms, s));
+        TRY(expand_all(t, v.vd, M, R, 1, l->b_d, 0, K, false, s));
+    }
+    TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
+    g = dq_gemm(t, M);
+    g.epi = kEpiPlain;
+    g.w = h->gm_d;
+    g.wdec = h->wdec2;
+    g.wdec_bytes = h->wdec2_bytes;
+    g.a = v.act;
+    g.out = out;
+    if (ad) {
+        g.add = l->y;
+        g.ldadd = K;
+    }
+    return launch_gemm(g, h->num_sms, s);
+}
+
+cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x, int M, const Saved& v,
+                           const void* dout, void* dx, const qmlp_adapter* gr, cudaStream_t s) {
+    qmlp_t* h = t->h;
+    const qmlp_lora_t* l = t->l;
+    const int K = h->K, I = h->I, R = l->Rp;
+    const bool fp8 = h->fmt == kFP8;
+    const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(dout);
+    // the transposed images: down's (FP8: with its per-channel factors, which
+    // lie along the contraction here), then gate's and up's beside the first GEMM
+    TRY(launch_gemm_predecode_t(h->gm_d, fp8 ? h->gv[2].chs : nullptr, nullptr, t->img_t, t->img_t_bytes, s));
+    TRY(beside(h, s, [&](cudaStream_t b) {
+        return launch_gemm_predecode_t(h->gm_gu, t->row, t->row ? t->row + I : nullptr, h->wdec, h->wdec_bytes, b);
+    }));
+    if (ad) {
+        TRY(launch_lr_pack(pack_train(t, ad, true), s));
+        LrShrink a = shrink_all(t, dy, M, K, t->dvd, R);
+        a.w = l->b_d;
+        TRY(launch_lr_shrink(a, R, true, tiles_for(M), 1, h->num_sms, s));
+        TRY(expand_all(t, t->dvd, M, R, 1, l->a_d, 0, I, true, s));
+    }
+    // d act, and through the activation d gate and d up
+    GemmLaunch g = dq_gemm(t, M);
+    g.epi = kEpiSwiGLUGrad;
+    g.w.fmt = kNVFP4;  // one factor for all columns
+    g.w.inv_g0 = fp8 ? 1.0f : h->gv[2].inv_g;
+    g.w.N = (I + 255) / 256 * 256;
+    g.w.K = K;
+    g.wdec = t->img_t;
+    g.wdec_bytes = t->img_t_bytes;
+    g.a = dy;
+    g.out = t->dgu;
+    g.gu_g = v.g;
+    g.gu_u = v.u;
+    g.ncols = I;
+    g.gf0 = h->gv[0].inv_g;
+    g.gf1 = h->gv[1].inv_g;
+    g.gc0 = t->eff;
+    g.gc1 = t->eff ? t->eff + I : nullptr;
+    __nv_bfloat16* lo = ad && M < kTwoWordM ? t->dgu_lo : nullptr;
+    if (ad) {
+        g.out_lo = lo;
+        g.add = l->y;
+        g.ldadd = I;
+    }
+    TRY(launch_gemm(g, h->num_sms, s));
+    if (ad) {
+        LrShrink a = shrink_all(t, t->dgu, M, I, t->dv, 2 * R);
+        a.x_lo = lo;
+        a.ldx = (size_t)2 * I;
+        a.x_z = I;
+        a.w = t->bq;
+        a.w_lo = t->bq + (size_t)2 * I * R;
+        a.w_z = (size_t)I * R;
+        TRY(launch_lr_shrink(a, R, true, tiles_for(M), 2, h->num_sms, s));
+        TRY(expand_all(t, t->dv, M, 2 * R, 1, l->a_gu, 0, K, true, s));
+    }
+    TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
+    g = dq_gemm(t, M);
+    g.epi = kEpiPlain;
+    g.w.fmt = kNVFP4;
+    g.w.N = K;
+    g.w.K = 2 * I;
+    g.wdec = h->wdec;
+    g.wdec_bytes = h->wdec_bytes;
+    g.a = t->dgu;
+    g.out = dx;
+    if (ad) {
+        g.add = l->y;
+        g.ldadd = K;
+    }
+    TRY(launch_gemm(g, h->num_sms, s));
+    if (!gr) return cudaSuccess;
+    auto bf = [](const void* p) { return static_cast<__nv_bfloat16*>(const_cast<void*>(p)); };
+    LrTokGrad q;
+    q.M = M;
+    q.r = ad->rank;
+    q.Rp = R;
+    q.part = t->part;
+    q.cnt = t->cnt;
+    auto v_of = [&](LrTokGrad& c, const __nv_bfloat16* p, int ld) {
+        c.v = p;
+        c.ldv = ld;
+        c.v_word = (size_t)M * ld;
+    };
+    if (gr->down_b) {
+        LrTokGrad c = q;
+        c.x = dy;
+        c.ldx = c.D = K;
+        v_of(c, v.vd, R);
+        c.rows_d = true;
+        c.out[0] = bf(gr->down_b);
+        TRY(launch_lr_tokgrad(c, R, 1, h->num_sms, s));
+    }
+    if (gr->down_a) {
+        LrTokGrad c = q;
+        c.x = v.act;
+        c.x_lo = v.act_lo;
+        c.ldx = c.D = I;
+        v_of(c, t->dvd, R);
+        c.out[0] = bf(gr->down_a);
+        TRY(launch_lr_tokgrad(c, R, 1, h->num_sms, s));
+    }
+    if (gr->gate_b || gr->up_b) {
+        LrTokGrad c = q;
+        c.x = t->dgu;
+        c.x_lo = lo;
+        c.ldx = (size_t)2 * I;
+        c.x_z = I;
+        c.D = I;
+        v_of(c, v.vgu, 2 * R);
+        c.rows_d = true;
+        c.out[0] = bf(gr->gate_b);
+        c.out[1] = bf(gr->up_b);
+        for (int i = 0; i < 2; ++i) {
+            c.div[i] = t->eff ? t->eff + (size_t)i * I : nullptr;
+            c.div_all[i] = h->gv[i].inv_g;
+        }
+        TRY(launch_lr_tokgrad(c, R, 2, h->num_sms, s));
+    }
+    if (gr->gate_a || gr->up_a) {
+        LrTokGrad c = q;
+        c.x = static_cast<const __nv_bfloat16*>(x);
+        c.ldx = c.D = K;
+        v_of(c, t->dv, 2 * R);
+        c.out[0] = bf(gr->gate_a);
+        c.out[1] = bf(gr->up_a);
+        TRY(launch_lr_tokgrad(c, 2 * R, 1, h->num_sms, s));
+    }
+    return cudaSuccess;
+}
+#undef TRY
+
+}  // namespace
+}  // extern "C++"
+
+qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_stream_t stream) {
+    if (!out) return QMLP_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!h) return QMLP_ERR_INVALID_ARG;
+    if (!h->has_gemm || !h->wdec || !h->side || max_rank < 1 || max_rank > kLrMaxRank) return QMLP_ERR_SHAPE;
+    if (h->fmt == kNVFP4 && (!(fabsf(h->gv[0].inv_g) >= kLeastFactor) || !(fabsf(h->gv[1].inv_g) >= kLeastFactor)))
+        return QMLP_ERR_INVALID_ARG;
+    qmlp_train_t* t = new qmlp_train_t();
+    t->h = h;
+    qmlp_status st = qmlp_lora_create(&t->l, h, 1, max_rank, stream);
+    if (st != QMLP_OK) {
+        delete t;
+        return st;
+    }
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const size_t I = h->I, K = h->K, M = h->max_M, R = t->l->Rp;
+    t->img_t_bytes = gemm_decoded_t_bytes((int)K, (int)I);
+    cudaError_t e = cudaSuccess;
+    auto get = [&](auto** p, size_t count) {
+        if (e == cudaSuccess) e = t->mem.alloc(reinterpret_cast<void**>(p), count * sizeof(**p));
+    };
+    get(&t->img_t, t->img_t_bytes);
+    get(&t->bq, 4 * I * R);
+    get(&t->dgu, M * 2 * I);
+    get(&t->dgu_lo, std::min<size_t>(M, kTwoWordM) * 2 * I);
+    get(&t->dv, kLrWords * M * 2 * R);
+    get(&t->dvd, kLrWords * M * R);
+    get(&t->part, lr_grad_part_elems(h->num_sms));
+    const size_t cnt = 2 * (size_t)lr_grad_tiles((int)std::max(I, K));
+    get(&t->cnt, cnt);
+    if (e == cudaSuccess) e = cudaMemsetAsync(t->cnt, 0, cnt * sizeof(int), s);
+    if (h->fmt == kFP8) {
+        get(&t->eff, 2 * I);
+        get(&t->row, 2 * I);
+        if (e == cudaSuccess) {
+            factors_kernel<<<(unsigned)((2 * I + 255) / 256), 256, 0, s>>>(h->gv[0].chs, h->gv[1].chs, (int)I, t->eff,
+                                                                          t->row);
+            e = cudaPeekAtLastError();
+        }
+    }
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e != cudaSuccess) {
+        cudaStreamSynchronize(s);
+        qmlp_lora_destroy(t->l);
+        t->mem.release();
+        delete t;
+        return from_cuda(e);
+    }
+    *out = t;
+    return QMLP_OK;
+}
+
+void qmlp_train_destroy(qmlp_train_t* t) {
+    if (!t) return;
+    cudaDeviceSynchronize();
+    qmlp_lora_destroy(t->l);
+    t->mem.release();
+    delete t;
+}
+
+size_t qmlp_train_saved_bytes(qmlp_train_t* t, int M) {
+    return !t || M < 1 || M > t->h->max_M ? 0 : saved_of(t, M, nullptr).bytes;
+}
+
+// The checks that forward and backward share.
+static qmlp_status check_train(const qmlp_train_t* t, const qmlp_adapter* a, int M) {
+    if (M < 1 || M > t->h->max_M) return QMLP_ERR_SHAPE;
+    return a ? check_adapter(a, t->l->max_rank) : QMLP_OK;
+}
+
+qmlp_status qmlp_train_forward(qmlp_train_t* t, const qmlp_adapter* adapter, const void* x, int M, void* out,
+                               void* saved, qmlp_stream_t stream) {
+    if (!t || !x || !out || !saved) return QMLP_ERR_INVALID_ARG;
+    const qmlp_status st = check_train(t, adapter, M);
+    if (st != QMLP_OK) return st;
+    if (!aligned16(x) || !aligned16(out) || !aligned16(saved)) return QMLP_ERR_ALIGNMENT;
+    const size_t xb = (size_t)M * t->h->K * 2, sb = saved_of(t, M, nullptr).bytes;
+    if (overlaps(out, xb, x, xb) || overlaps(saved, sb, x, xb) || overlaps(saved, sb, out, xb)) return QMLP_ERR_ALIAS;
+    if (fault("launch")) return QMLP_ERR_CUDA;
+    return train_forward(t, adapter, x, M, out, saved_of(t, M, saved), reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? QMLP_OK
+               : QMLP_ERR_CUDA;
+}
+
+qmlp_status qmlp_train_backward(qmlp_train_t* t, const qmlp_adapter* adapter, const void* x, int M, const void* saved,
+                                const void* dout, void* dx, const qmlp_adapter* grads, qmlp_stream_t stream) {
+    if (!t || !x || !saved || !dout || !dx || (grads && !adapter)) return QMLP_ERR_INVALID_ARG;
+    const qmlp_status st = check_train(t, adapter, M);
+    if (st != QMLP_OK) return st;
+    if (!aligned16(x) || !aligned16(saved) || !aligned16(dout) || !aligned16(dx)) return QMLP_ERR_ALIGNMENT;
+    const size_t K = t->h->K, I = t->h->I, xb = (size_t)M * K * 2;
+    std::vector<Range> r;
+    auto add = [&](const void* p, size_t bytes, bool w) {
+        if (p) r.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, w});
+    };
+    add(x, xb, false);
+    add(dout, xb, false);
+    add(saved, saved_of(t, M, nullptr).bytes, false);
+    add(dx, xb, true);
+    if (adapter) {
+        const size_t rk = (size_t)adapter->rank * 2;
+        const size_t bytes[6] = {rk * K, rk * I, rk * K, rk * I, rk * I, rk * K};
+        const void* p[6] = {adapter->gate_a, adapter->gate_b, adapter->up_a, adapter->up_b, adapter->down_a, adapter->down_b};
+        for (int i = 0; i < 6; ++i) add(p[i], bytes[i], false);
+        if (grads) {
+            const void* g[6] = {grads->gate_a, grads->gate_b, grads->up_a, grads->up_b, grads->down_a, grads->down_b};
+            for (int i = 0; i < 6; ++i) {
+                if (g[i] && !p[i]) return QMLP_ERR_INVALID_ARG;
+                if (!aligned(g[i], 2)) return QMLP_ERR_ALIGNMENT;
+                add(g[i], bytes[i], true);
+            }
+        }
+    }
+    if (any_alias(r)) return QMLP_ERR_ALIAS;
+    if (fault("launch")) return QMLP_ERR_CUDA;
+    return train_backward(t, adapter, x, M, saved_of(t, M, saved), dout, dx, grads,
+                          reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? QMLP_OK
+               : QMLP_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------

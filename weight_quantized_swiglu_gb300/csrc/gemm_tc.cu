@@ -138,9 +138,22 @@ struct Args {
     size_t ws_elems;       // index checks: floats of the split-K partial buffer
     const uint8_t* wdec;   // PRE: decoded stage images [Nt][KS][32 KB]
     size_t wdec_bytes;     // PRE: bytes of wdec (index checks)
-    const float* add;      // EXT: fp32 [M][ldadd] added after the factor (gate then up columns, or the output's)
+    // EXT instances (low-rank adapters and training)
+    const float* add;      // optional fp32 [M][ldadd] added after the factor (gate then up columns, or the output's)
     size_t ldadd;
+    float4* gu_g;          // SwiGLU: optional, the gate and up values that act is made of, kept for the backward
+    float4* gu_u;          //   pass; SwiGLUGrad: the values kept. [ceil(M / 32)][ldo / 4][32] quads (see gu_at)
+    int ncols;             // SwiGLUGrad: I, the columns of each half of out (the last tile may reach past it)
+    float gf0, gf1;        // SwiGLUGrad: factors of d gate and d up, or per column:
+    const float* gc0;
+    const float* gc1;
+    void* out_lo;          // SwiGLU, SwiGLUGrad: optional, bf16 of what out's rounding leaves
 };
+
+// Quad (columns col..col+3) of row m in the gate / up values kept for the
+// backward pass: 32 rows' quads lie together, so that a warp, whose lanes are
+// 32 rows of the accumulator, writes and reads 512 contiguous bytes.
+QMLP_DEV size_t gu_at(int m, int col, int I) { return ((size_t)(m >> 5) * (I >> 2) + (col >> 2)) * 32 + (m & 31); }
 
 // Instruction descriptor, kind::f16: fp32 accumulator, fp16 A and B, both
 // K-major, N = BN, M = BM.
@@ -197,12 +210,17 @@ QMLP_DEV void decode_item_fp8(const uint8_t* raw, uint8_t* bt, int n, int h) {
 // per-channel scales (FP8; the same four for every thread, a broadcast
 // load) or the global factor (NVFP4). col is a multiple of 4.
 template <int FMT>
-QMLP_DEV float4 factor4(const float* cs, float inv, int col) {
-    if (FMT == kNVFP4) return make_float4(inv, inv, inv, inv);
+QMLP_DEV float4 factor4(const float* cs, float inv, int col, bool one = false) {
+    if (FMT == kNVFP4 || one) return make_float4(inv, inv, inv, inv);
     return __ldg(reinterpret_cast<const float4*>(cs + col));
 }
 QMLP_DEV float f4_at(const float4& f, int e) { return e == 0 ? f.x : e == 1 ? f.y : e == 2 ? f.z : f.w; }
 
+QMLP_DEV uint32_t pack_bf16x2(float lo, float hi);
+// What the rounding of lo and hi to the packed `p` leaves, packed.
+QMLP_DEV uint32_t rest_bf16x2(float lo, float hi, uint32_t p) {
+    return pack_bf16x2(lo - __uint_as_float(p << 16), hi - __uint_as_float(p & 0xFFFF0000u));
+}
 QMLP_DEV uint32_t pack_bf16x2(float lo, float hi) {
     const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&p);
@@ -226,13 +244,13 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                 for (int j = 0; j < 32; j += 4) {
                     const float4 fg = factor4<FMT>(a.cs0, a.inv0, nt * (BN / 2) + c0 + j);
                     const float4 fu = factor4<FMT>(a.cs1, a.inv1, nt * (BN / 2) + c0 + j);
-                    float4 dg, du;
-                    if (EXT) {
+                    float4 dg = make_float4(0, 0, 0, 0), du = dg;
+                    if (EXT && a.add) {
                         const float* ad = a.add + (size_t)m * a.ldadd + nt * (BN / 2) + c0 + j;
                         dg = *reinterpret_cast<const float4*>(ad);
                         du = *reinterpret_cast<const float4*>(ad + a.ldo);
                     }
-                    float r4[4];
+                    float r4[4], g4[4], u4[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float gv = scalbnf(g[j + e], -sg) * f4_at(fg, e);
@@ -242,15 +260,76 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                             uv += f4_at(du, e);
                         }
                         r4[e] = silu_f32(gv) * uv;
+                        g4[e] = gv;
+                        u4[e] = uv;
+                    }
+                    if (EXT && a.gu_g) {
+                        const size_t at = gu_at(m, nt * (BN / 2) + c0 + j, a.ldo);
+                        a.gu_g[at] = make_float4(g4[0], g4[1], g4[2], g4[3]);
+                        a.gu_u[at] = make_float4(u4[0], u4[1], u4[2], u4[3]);
                     }
                     pk[j / 2] = pack_bf16x2(r4[0], r4[1]);
                     pk[j / 2 + 1] = pack_bf16x2(r4[2], r4[3]);
+                    if (EXT && a.out_lo)
+                        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out_lo) + (size_t)m * a.ldo +
+                                                  nt * (BN / 2) + c0 + j) =
+                            make_uint2(rest_bf16x2(r4[0], r4[1], pk[j / 2]), rest_bf16x2(r4[2], r4[3], pk[j / 2 + 1]));
                 }
                 uint4* dst = reinterpret_cast<uint4*>(out + (size_t)m * a.ldo + nt * (BN / 2) + c0);
                 if (QMLP_INB(nt * (BN / 2) + c0 + 31, a.ldo, 12) && QMLP_INB(m, a.M, 12))
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
+            }
+        }
+    } else if (EXT && a.epi == kEpiSwiGLUGrad) {
+        // d act -> d gate and d up through act = SiLU(g) u, each times the
+        // factor of its projection, which the product with the weights (held
+        // without factors) then lacks: out = [M][d gate | d up], bf16 -- the
+        // one rounding between the two products of the backward pass
+        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
+#pragma unroll 1
+        for (int c0 = 0; c0 < BN; c0 += 32) {
+            float y[32];
+            tmem_ld32(tbase + c0, y);
+            const int col = nt * BN + c0;
+            if (live && col < a.ncols) {
+                uint32_t pg[16], pu[16];
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const size_t at = gu_at(m, col + j, a.ncols);
+                    const float4 g = __ldcs(a.gu_g + at), u = __ldcs(a.gu_u + at);
+                    float4 ad = make_float4(0, 0, 0, 0);
+                    if (a.add) ad = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + col + j);
+                    const float4 fg = factor4<kFP8>(a.gc0, a.gf0, col + j, a.gc0 == nullptr),
+                                 fu = factor4<kFP8>(a.gc1, a.gf1, col + j, a.gc1 == nullptr);
+                    float dg[4], du[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float d = y[j + e] * a.inv0 + f4_at(ad, e), gv = f4_at(g, e);
+                        const float sg1 = 1.0f / (1.0f + expf(-gv));
+                        du[e] = d * (gv * sg1) * f4_at(fu, e);
+                        dg[e] = d * f4_at(u, e) * (sg1 * (1.0f + gv * (1.0f - sg1))) * f4_at(fg, e);
+                    }
+                    pg[j / 2] = pack_bf16x2(dg[0], dg[1]);
+                    pg[j / 2 + 1] = pack_bf16x2(dg[2], dg[3]);
+                    pu[j / 2] = pack_bf16x2(du[0], du[1]);
+                    pu[j / 2 + 1] = pack_bf16x2(du[2], du[3]);
+                    if (a.out_lo) {
+                        __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(a.out_lo) + (size_t)m * 2 * a.ncols + col + j;
+                        *reinterpret_cast<uint2*>(lo) =
+                            make_uint2(rest_bf16x2(dg[0], dg[1], pg[j / 2]), rest_bf16x2(dg[2], dg[3], pg[j / 2 + 1]));
+                        *reinterpret_cast<uint2*>(lo + a.ncols) =
+                            make_uint2(rest_bf16x2(du[0], du[1], pu[j / 2]), rest_bf16x2(du[2], du[3], pu[j / 2 + 1]));
+                    }
+                }
+                uint4* dst = reinterpret_cast<uint4*>(out + (size_t)m * 2 * a.ncols + col);
+                uint4* dsu = reinterpret_cast<uint4*>(out + (size_t)m * 2 * a.ncols + a.ncols + col);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    dst[v] = make_uint4(pg[4 * v], pg[4 * v + 1], pg[4 * v + 2], pg[4 * v + 3]);
+                    dsu[v] = make_uint4(pu[4 * v], pu[4 * v + 1], pu[4 * v + 2], pu[4 * v + 3]);
+                }
             }
         }
     } else if (a.epi == kEpiPlain) {
@@ -264,7 +343,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 f = factor4<FMT>(a.cs0, a.inv0, nt * BN + c0 + j);
-                    if (EXT) {
+                    if (EXT && a.add) {
                         const float4 d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + nt * BN + c0 + j);
                         pk[j / 2] = pack_bf16x2(scalbnf(y[j], -sg) * f.x + d.x, scalbnf(y[j + 1], -sg) * f.y + d.y);
                         pk[j / 2 + 1] =
@@ -994,6 +1073,103 @@ __global__ void __launch_bounds__(256) predecode_kernel(const uint8_t* __restric
     }
 }
 
+// The same images of the transposed projection, for products that contract
+// over the weight rows (d x = d y W): image (rt, cs) holds source columns 256
+// rt.. +255 as its rows and source rows 64 cs.. +63 as its contraction, read
+// from 64 rows of four weight blocks. One CTA an image: decode into shared
+// memory [64 source rows][256 columns], pack eight source rows of a column
+// into a 16-byte chunk of the swizzled image, copy the image out with one bulk
+// copy. Interleaved sources (gate and up halves) are taken gate rows first,
+// then up rows. mul0 / mul1: optional factors of the source rows (gate or the
+// projection's, and up's), rounded into the bf16 image; without them the
+// decoded values are exact, as above. Columns past the source's are zero.
+struct PreT {
+    const uint8_t* tiles;
+    uint8_t* img;
+    int KSs;        // 64-column blocks of a source row tile
+    int cols;       // source columns
+    int steps;      // contraction steps of an image row (source rows / 64)
+    int half;       // interleaved: contraction steps of the gate half, else 0
+    const float* mul0;
+    const float* mul1;
+    size_t tiles_bytes;
+};
+constexpr int kPitchT = 256 + 2;  // bf16 of a decoded source row in shared memory
+constexpr int kSmemT = kBBytes + 64 * kPitchT * 2 + 128;
+
+template <int FMT>
+__global__ void __launch_bounds__(256) predecode_t_kernel(const PreT a) {
+    extern __shared__ __align__(128) uint8_t pre_smem[];
+    const uint32_t base_s = (smem_u32(pre_smem) + 127u) & ~127u;
+    uint8_t* img = pre_smem + (base_s - smem_u32(pre_smem));
+    __nv_bfloat16* dec = reinterpret_cast<__nv_bfloat16*>(img + kBBytes);
+    const int cs = blockIdx.x, rt = blockIdx.y;
+    const bool up = a.half && cs >= a.half;
+    const int n0 = (up ? cs - a.half : cs) * 64;  // first source row of its projection
+    const int j = a.half ? n0 / (BN / 2) : n0 / BN;
+    const int r0 = a.half ? n0 % (BN / 2) + (up ? BN / 2 : 0) : n0 % BN;
+    const float* mul = up ? a.mul1 : a.mul0;
+    // 16-byte pieces of decoded values: (row, 8 columns), 32 pieces a row
+    for (int i = threadIdx.x; i < 64 * 32; i += 256) {
+        const int r = i >> 5, c8 = i & 31, q = c8 >> 3, l = c8 & 7;
+        const size_t blk = (size_t)j * a.KSs + rt * 4 + q;
+        float f[8];
+        if (rt * 4 + q < a.KSs && QMLP_INB((blk + 1) * raw_bytes<FMT>() - 1, a.tiles_bytes, 18)) {
+            const uint8_t* raw = a.tiles + blk * raw_bytes<FMT>();
+            const int n = r0 + r;
+            uint32_t h[4];
+            if (FMT == kNVFP4) {
+                const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(raw + n * 32 + l * 4));
+                const uint32_t sc = dup_lo16(e4m3x2_to_f16x2(__ldg(raw + kRawCodes + n * 4 + (l >> 1))));
+                e2m1x4_to_f16x2x4(w, h[0], h[1], h[2], h[3]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = hmul2_u32(h[e], sc);
+            } else {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(raw + n * 64 + l * 8));
+                e4m3x4_to_f16x2x2(w.x, h[0], h[1]);
+                e4m3x4_to_f16x2x2(w.y, h[2], h[3]);
+            }
+            const float m = mul ? __ldg(mul + n0 + r) : 1.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+                f[2 * e] = v.x * m;
+                f[2 * e + 1] = v.y * m;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+        }
+        uint32_t* d = reinterpret_cast<uint32_t*>(dec + r * kPitchT + c8 * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+    }
+    __syncthreads();
+    // a thread a pair of columns and a chunk of eight source rows
+    for (int i = threadIdx.x; i < 128 * 8; i += 256) {
+        const int k = (i & 127) * 2, l = i >> 7;
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint32_t*>(dec + (l * 8 + e) * kPitchT + k);
+        uint4 lo, hi;
+        lo = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410),
+                        __byte_perm(w[4], w[5], 0x5410), __byte_perm(w[6], w[7], 0x5410));
+        hi = make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632),
+                        __byte_perm(w[4], w[5], 0x7632), __byte_perm(w[6], w[7], 0x7632));
+        *reinterpret_cast<uint4*>(img + k * 128 + ((l ^ (k & 7)) * 16)) = lo;
+        *reinterpret_cast<uint4*>(img + (k + 1) * 128 + ((l ^ ((k + 1) & 7)) * 16)) = hi;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        uint8_t* dst = a.img + ((size_t)rt * a.steps + cs) * kBBytes;
+        asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(base_s),
+                     "r"(kBBytes)
+                     : "memory");
+        asm volatile("cp.async.bulk.commit_group;\n\tcp.async.bulk.wait_group 0;" ::: "memory");
+    }
+}
+
 // a (bf16 [M, C]) -> a16 (fp16 [M, C]) * 2^sig[m], sig[m] = the exponent
 // that brings max|a[m, :]| into [2^14, 2^15). One CTA per row.
 __global__ void __launch_bounds__(256) prescale_rows_kernel(const __nv_bfloat16* __restrict__ a, __half* a16,
@@ -1175,8 +1351,8 @@ cudaError_t launch_predecode(const Args& a, uint8_t* wdec, int num_sms, cudaStre
 }
 
 template <int FMT>
-cudaError_t launch_fmt(const CUtensorMap& map, const Args& a, int grid, cudaStream_t s) {
-    cudaError_t e = a.add ? (a.wdec ? launch_inst<FMT, true, true>(map, a, grid, s)
+cudaError_t launch_fmt(const CUtensorMap& map, const Args& a, bool ext, int grid, cudaStream_t s) {
+    cudaError_t e = ext ? (a.wdec ? launch_inst<FMT, true, true>(map, a, grid, s)
                                     : launch_inst<FMT, false, true>(map, a, grid, s))
                     : a.wdec ? launch_inst<FMT, true>(map, a, grid, s)
                              : launch_inst<FMT, false>(map, a, grid, s);
@@ -1203,6 +1379,36 @@ cudaError_t launch_gemm_predecode(const GemmProj& P, uint8_t* wdec, size_t wdec_
     a.wdec = wdec;
     a.wdec_bytes = gemm_decoded_bytes(P.N, P.K);
     return P.fmt == kFP8 ? launch_predecode<kFP8>(a, wdec, num_sms, s) : launch_predecode<kNVFP4>(a, wdec, num_sms, s);
+}
+
+size_t gemm_decoded_t_bytes(int N, int K) { return (size_t)((K + BN - 1) / BN) * (N / BK) * kBBytes; }
+
+cudaError_t launch_gemm_predecode_t(const GemmProj& P, const float* mul0, const float* mul1, uint8_t* img,
+                                    size_t img_bytes, cudaStream_t s) {
+    if (!gemm_supported(P.K, P.N) || !P.tiles || !img || img_bytes < gemm_decoded_t_bytes(P.N, P.K))
+        return cudaErrorInvalidValue;
+    PreT a;
+    a.tiles = P.tiles;
+    a.img = img;
+    a.KSs = P.K / BK;
+    a.cols = P.K;
+    a.steps = P.N / BK;
+    a.half = P.interleaved ? P.N / 2 / BK : 0;
+    a.mul0 = mul0;
+    a.mul1 = mul1;
+    a.tiles_bytes = gemm_tiles_bytes(P.fmt, P.N, P.K);
+    static bool attr = false;
+    if (!attr) {
+        cudaError_t e = cudaFuncSetAttribute(predecode_t_kernel<kNVFP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemT);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(predecode_t_kernel<kFP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemT);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    const dim3 grid((unsigned)a.steps, (unsigned)((P.K + BN - 1) / BN));
+    if (P.fmt == kFP8) predecode_t_kernel<kFP8><<<grid, 256, kSmemT, s>>>(a);
+    else predecode_t_kernel<kNVFP4><<<grid, 256, kSmemT, s>>>(a);
+    return cudaPeekAtLastError();
 }
 
 size_t gemm_tiles_bytes(int fmt, int N, int K) {
@@ -1280,7 +1486,17 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.ldo = L.epi == kEpiSwiGLU ? P.N / 2 : (L.epi == kEpiRaw && P.interleaved ? P.N / 2 : P.N);
     a.add = L.add;
     a.ldadd = L.ldadd;
-    if (L.add && (L.epi == kEpiRaw || (L.pair && !dq) || L.ldadd % 4)) return cudaErrorInvalidValue;
+    a.gu_g = static_cast<float4*>(L.gu_g);
+    a.gu_u = static_cast<float4*>(L.gu_u);
+    a.ncols = L.ncols;
+    a.gf0 = L.gf0;
+    a.gf1 = L.gf1;
+    a.gc0 = L.gc0;
+    a.gc1 = L.gc1;
+    a.out_lo = L.out_lo;
+    const bool grad = L.epi == kEpiSwiGLUGrad, ext = L.add || L.gu_g || grad;
+    if (ext && (L.epi == kEpiRaw || (L.pair && !dq) || L.ldadd % 4 || (grad && (!L.gu_g || L.ncols > P.N))))
+        return cudaErrorInvalidValue;
     a.err = L.err;
     a.limit = L.wait_ns ? L.wait_ns : kGemmWaitNs;
     a.withhold = L.withhold ? 1 : 0;
@@ -1301,7 +1517,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     const int KS = P.K / BK;
     a.splits = 1;
     a.ws = L.ws;
-    if (L.ws && L.epi != kEpiRaw && !L.pair && 2 * tiles0 <= num_sms)
+    if (L.ws && L.epi != kEpiRaw && !L.gu_g && !L.pair && 2 * tiles0 <= num_sms)
         a.splits = std::max(1, std::min(std::min(num_sms / tiles0, KS / 8), kMaxSplits));
     // 256-token tiles on CTA pairs (every weight row decoded once per 256
     // tokens), when asked for
@@ -1321,14 +1537,14 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
-        if (a.add)
+        if (ext)
             return P.fmt == kFP8 ? launch_pair<kFP8, true, true>(map, bmap, a, pairs, s)
                                  : launch_pair<kNVFP4, true, true>(map, bmap, a, pairs, s);
         return P.fmt == kFP8 ? launch_pair<kFP8, true>(map, bmap, a, pairs, s)
                              : launch_pair<kNVFP4, true>(map, bmap, a, pairs, s);
     }
     const int grid = std::min(tiles0 * a.splits, std::max(num_sms, 1));
-    return P.fmt == kFP8 ? launch_fmt<kFP8>(map, a, grid, s) : launch_fmt<kNVFP4>(map, a, grid, s);
+    return P.fmt == kFP8 ? launch_fmt<kFP8>(map, a, ext, grid, s) : launch_fmt<kNVFP4>(map, a, ext, grid, s);
 }
 
 QMLP_BOUNDS_UNIT(gemm_tc)

@@ -19,7 +19,8 @@ constexpr int kChunkK = 64;
 enum GemvEpi {
     kEpiSwiGLU = 0,  // two projections (gate, up) -> act = bf16(SiLU(g)*u)
     kEpiPlain = 1,   // one projection -> bf16(sigma * acc)
-    kEpiRaw = 2      // one projection -> fp32 acc (no scale), debug
+    kEpiRaw = 2,     // one projection -> fp32 acc (no scale), debug
+    kEpiSwiGLUGrad = 3  // d act -> [d gate | d up] (GEMM, training)
 };
 
 // One projection [N, K] in the GEMV ("fragment-native") layout: one record
@@ -180,7 +181,14 @@ struct GemmLaunch {
     uint8_t* wdec = nullptr;  // dequantise-once: decoded stage images of w (null: the decoder warps decode)
     size_t wdec_bytes = 0;    // bytes of wdec, >= gemm_decoded_bytes(w.N, w.K)
     const float* add = nullptr;  // fp32 [M][ldadd], added after the factor: gate's I columns then up's
-    size_t ldadd = 0;            // (SwiGLU), or the output's columns (plain); low-rank adapters
+    size_t ldadd = 0;            // (SwiGLU), or the output's columns (plain, grad); low-rank adapters
+    void* gu_g = nullptr;        // training: fp32 gate and up values, kept by SwiGLU and read by SwiGLUGrad,
+    void* gu_u = nullptr;        // gemm_gu_bytes(M, I) each
+    int ncols = 0;               // SwiGLUGrad: I; out = [M][2I]
+    float gf0 = 1.0f, gf1 = 1.0f;  // SwiGLUGrad: factors of d gate, d up, or per column:
+    const float* gc0 = nullptr;
+    const float* gc1 = nullptr;
+    void* out_lo = nullptr;      // with gu_g: optional, bf16 of what the rounding of out leaves
     bool images_ready = false;  // dequantise-once: wdec already holds w's images (no predecode launch)
 };
 constexpr int kPairMinM = 256;  // one 256-token tile of a CTA pair
@@ -189,6 +197,12 @@ size_t gemm_splitk_ws_elems(int num_sms);
 size_t gemm_decoded_bytes(int N, int K);  // bf16 stage images of an [N, K] projection (2 N K bytes)
 // The dequantise-once predecode of projection P into wdec, on its own.
 cudaError_t launch_gemm_predecode(const GemmProj& P, uint8_t* wdec, size_t wdec_bytes, int num_sms, cudaStream_t s);
+// Images of the transposed projection (contraction over its N rows, its K
+// columns as output rows, padded to 256).
+size_t gemm_decoded_t_bytes(int N, int K);
+cudaError_t launch_gemm_predecode_t(const GemmProj& P, const float* mul0, const float* mul1, uint8_t* img,
+                                    size_t img_bytes, cudaStream_t s);
+inline size_t gemm_gu_bytes(int M, int I) { return (size_t)((M + 31) / 32) * 32 * I * 4; }
 bool gemm_supported(int K, int N);
 
 // ---------------------------------------------------------------------------

@@ -137,9 +137,11 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int z = blockIdx.z;
     const __nv_bfloat16* x = a.x + (size_t)z * a.x_z;
+    const ptrdiff_t lo = a.x_lo ? a.x_lo - a.x : 0;
     const __nv_bfloat16* w = a.w + (size_t)slot * a.w_slot + (size_t)z * a.w_z;
     const __nv_bfloat16* w2 = TWO ? a.w_lo + (size_t)z * a.w_z : nullptr;
-    const int steps = (a.D + kStep - 1) / kStep;
+    // a second word of x is the same contraction once more
+    const int one = (a.D + kStep - 1) / kStep, steps = a.x_lo ? 2 * one : one;
     const int s0 = (int)((long)steps * blockIdx.y / gridDim.y), s1 = (int)((long)steps * (blockIdx.y + 1) / gridDim.y);
     const uint32_t base = smem_u32(smem);
 
@@ -155,12 +157,13 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
     }
     auto load = [&](int step, int stage) {
         const uint32_t sx = base + stage * S::Stage, swt = sx + S::X;
-        const int d0 = step * kStep;
+        const int d0 = (step < one ? step : step - one) * kStep;
+        const ptrdiff_t word = step < one ? 0 : lo;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = (tid >> 3) + 16 * i, c = tid & 7, d = d0 + c * 8;
             const bool live = xl[i] && d < a.D;
-            cp16(sx + sw<8>(r, c), live ? xr[i] + d : x, live);
+            cp16(sx + sw<8>(r, c), live ? xr[i] + word + d : x, live);
         }
         constexpr int kW = NC * kStep / 8;  // chunks of the W tile
 #pragma unroll
@@ -377,6 +380,135 @@ __global__ void __launch_bounds__(kThr) expand_kernel(const LrExpand a) {
                 }
             }
         }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// z^T v over the tokens (the words of z in turn): a CTA takes 128 columns of z (32 a warp) and NC of v;
+// the tokens are split over gridDim.y CTAs, whose partials the last one adds in
+// order. v in two words (2^-17): the gradients are bf16.
+// ---------------------------------------------------------------------------
+constexpr int kGD = 128;
+template <int NC>
+struct GradSmem {
+    static constexpr int X = 64 * kGD * 2, V = 64 * NC * 2;
+    static constexpr int Stage = X + 2 * V;
+    static constexpr int Stages = 3;
+    static constexpr int Bytes = Stage * Stages;
+};
+
+template <int NC>
+__global__ void __launch_bounds__(kThr) tokgrad_kernel(const LrTokGrad a) {
+    using S = GradSmem<NC>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, z = blockIdx.z;
+    const int d0 = blockIdx.x * kGD;
+    const int one = (a.M + 63) / 64, steps = a.x_lo ? 2 * one : one;
+    const int s0 = (int)((long)steps * blockIdx.y / gridDim.y), s1 = (int)((long)steps * (blockIdx.y + 1) / gridDim.y);
+    const __nv_bfloat16* x = a.x + (size_t)z * a.x_z + d0;
+    const ptrdiff_t lo = a.x_lo ? a.x_lo - a.x : 0;
+    const __nv_bfloat16* v = a.v + z * NC;
+    const uint32_t base = smem_u32(smem);
+    auto load = [&](int step, int stage) {
+        const uint32_t sx = base + stage * S::Stage, sv = sx + S::X;
+        const int m0 = (step < one ? step : step - one) * 64;
+        const ptrdiff_t word = step < one ? 0 : lo;
+#pragma unroll
+        for (int i = 0; i < 64 * (kGD / 8) / kThr; ++i) {
+            const int k = tid + i * kThr, r = k >> 4, c = k & 15;
+            const bool live = m0 + r < a.M && d0 + c * 8 < a.D;
+            cp16(sx + sw<16>(r, c), live ? x + word + (size_t)(m0 + r) * a.ldx + c * 8 : a.x, live);
+        }
+#pragma unroll
+        for (int i = 0; i < 64 * (NC / 8) / kThr; ++i) {
+            const int k = tid + i * kThr, r = k / (NC / 8), c = k % (NC / 8);
+            const bool live = m0 + r < a.M;
+            const __nv_bfloat16* p = live ? v + (size_t)(m0 + r) * a.ldv + c * 8 : a.v;
+            cp16(sv + sw<NC / 8>(r, c), p, live);
+            cp16(sv + S::V + sw<NC / 8>(r, c), p + (live ? a.v_word : 0), live);
+        }
+        cp_commit();
+    };
+    float acc[2][NC / 8][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[h][j][e] = 0.0f;
+#pragma unroll
+    for (int p = 0; p < S::Stages - 1; ++p) {
+        if (s0 + p < s1) load(s0 + p, p);
+        else cp_commit();
+    }
+    const int q = lane >> 3, r8 = lane & 7;
+    for (int st = s0; st < s1; ++st) {
+        cp_wait<S::Stages - 2>();
+        __syncthreads();
+        const int nx = st + S::Stages - 1;
+        if (nx < s1) load(nx, (nx - s0) % S::Stages);
+        else cp_commit();
+        const uint32_t sx = base + ((st - s0) % S::Stages) * S::Stage, sv = sx + S::X;
+#pragma unroll
+        for (int k = 0; k < 64; k += 16) {
+            uint32_t af[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)  // the transposed tile: rows are columns of z, the contraction tokens
+                ldsm4t(af[h], sx + sw<16>(k + (q >> 1) * 8 + r8, (warp * 32 + h * 16) / 8 + (q & 1)));
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int j = 0; j < NC / 16; ++j) {
+                    uint32_t b[4];
+                    load_b<true, NC / 8>(sv + w * S::V, j * 16, k, lane, b);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mma_bf16(acc[h][2 * j], af[h], b[0], b[1]);
+                        mma_bf16(acc[h][2 * j + 1], af[h], b[2], b[3]);
+                    }
+                }
+        }
+    }
+    auto emit = [&](int row, int col, float val) {  // row: column of z in the tile
+        const int d = d0 + row;
+        if (d >= a.D) return;
+        if (a.rows_d) {
+            if (col >= a.r || !a.out[z]) return;
+            a.out[z][(size_t)d * a.r + col] = __float2bfloat16_rn(val / (a.div[z] ? a.div[z][d] : a.div_all[z]));
+        } else {
+            const int part = col / a.Rp, j = col % a.Rp;
+            if (j < a.r && a.out[part]) a.out[part][(size_t)j * a.D + d] = __float2bfloat16_rn(val);
+        }
+    };
+    const int g = lane >> 2, t = lane & 3;
+    if (gridDim.y == 1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    emit(warp * 32 + h * 16 + g + 8 * (e >> 1), j * 8 + 2 * t + (e & 1), acc[h][j][e]);
+        return;
+    }
+    // partials as [column of v][column of z]: the last CTA reads along z
+    const size_t tile = (size_t)blockIdx.x + (size_t)gridDim.x * z;
+    float* part = a.part + (tile * gridDim.y + blockIdx.y) * (kGD * NC);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < NC / 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                part[(j * 8 + 2 * t + (e & 1)) * kGD + warp * 32 + h * 16 + g + 8 * (e >> 1)] = acc[h][j][e];
+    if (!last_arrival(a.cnt + tile, gridDim.y)) return;
+    const float* all = a.part + tile * gridDim.y * (kGD * NC);
+    for (int i = tid; i < kGD * NC; i += kThr) {
+        float val = 0.0f;
+        for (unsigned s = 0; s < gridDim.y; ++s) val += __ldcg(all + (size_t)s * (kGD * NC) + i);
+        emit(i % kGD, i / kGD, val);
     }
 }
 
@@ -631,6 +763,34 @@ cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, i
         case 64: return trans ? expand_t<64, true, 2>(a, tiles, zs, s) : expand_t<64, false, 3>(a, tiles, zs, s);
         case 128:
             if (trans) return expand_t<128, true, 2>(a, tiles, zs, s);
+    }
+    return cudaErrorInvalidValue;
+}
+
+int lr_grad_tiles(int D) { return (D + kGD - 1) / kGD; }
+size_t lr_grad_part_elems(int num_sms) { return (size_t)2 * num_sms * kGD * 128; }
+
+template <int NC>
+static cudaError_t tokgrad_t(const LrTokGrad& a, dim3 grid, cudaStream_t s) {
+    static bool attr = false;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(tokgrad_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   GradSmem<NC>::Bytes);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    return launch_pdl(tokgrad_kernel<NC>, grid, kThr, GradSmem<NC>::Bytes, a, s);
+}
+cudaError_t launch_lr_tokgrad(const LrTokGrad& a, int nc, int zs, int num_sms, cudaStream_t s) {
+    const int tiles = lr_grad_tiles(a.D), steps = (a.M + 63) / 64;
+    // two CTAs an SM, four steps a CTA at least; tiles * zs * splits <= 2 num_sms where there are splits
+    const int splits = std::max(1, std::min(2 * num_sms / (tiles * zs), steps / 4));
+    const dim3 grid(tiles, splits, zs);
+    switch (nc) {
+        case 16: return tokgrad_t<16>(a, grid, s);
+        case 32: return tokgrad_t<32>(a, grid, s);
+        case 64: return tokgrad_t<64>(a, grid, s);
+        case 128: return tokgrad_t<128>(a, grid, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -25,6 +25,7 @@ struct LrTokens {
 struct LrShrink {
     LrTokens tok;
     const __nv_bfloat16* x = nullptr;  // [M][ldx], D columns from z * x_z on
+    const __nv_bfloat16* x_lo = nullptr;  // optional second word of x
     size_t ldx = 0, x_z = 0;
     int D = 0;
     const __nv_bfloat16* w = nullptr;     // slot and part strides in elements
@@ -74,6 +75,25 @@ struct LrFew {
     float factor_all = 1.0f;
 };
 
+// out = z^T v over the tokens of one adapter, in bf16: with rows_d, out[z][d][r]
+// = B's gradient (part z of x and v); else out[j / Rp][j % Rp][d] = A's.
+struct LrTokGrad {
+    const __nv_bfloat16* x = nullptr;  // [M][ldx], D columns from z * x_z on
+    const __nv_bfloat16* x_lo = nullptr;  // optional second word of x
+    size_t ldx = 0, x_z = 0;
+    int D = 0, M = 0;
+    const __nv_bfloat16* v = nullptr;  // words of [M][ldv], columns z * NC on
+    size_t v_word = 0;
+    int ldv = 0;
+    bool rows_d = false;
+    int r = 0, Rp = 0;
+    __nv_bfloat16* out[2] = {nullptr, nullptr};
+    const float* div[2] = {nullptr, nullptr};  // rows_d: the row's divisor, or div_all
+    float div_all[2] = {1.0f, 1.0f};
+    float* part = nullptr;
+    int* cnt = nullptr;
+};
+
 struct LrSwiGLU {
     const float* raw_g = nullptr;  // [M][I]
     const float* raw_u = nullptr;
@@ -105,6 +125,9 @@ struct LrPack {
 int lr_max_tiles(int M, int slots);
 int lr_shrink_splits(int tiles, int zs, int D, int num_sms);
 size_t lr_part_elems(int num_sms);
+size_t lr_grad_part_elems(int num_sms);
+int lr_grad_tiles(int D);
+cudaError_t launch_lr_tokgrad(const LrTokGrad& a, int nc, int zs, int num_sms, cudaStream_t s);
 cudaError_t launch_lr_shrink(const LrShrink& a, int nc, bool trans, int tiles, int zs, int num_sms, cudaStream_t s);
 cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, int zs, cudaStream_t s);
 cudaError_t launch_lr_shrink_few(const LrFew& a, int M, cudaStream_t s);
