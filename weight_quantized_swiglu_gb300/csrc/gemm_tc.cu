@@ -88,6 +88,12 @@ constexpr int bstages() { return FMT == kNVFP4 ? 3 : 2; }
 constexpr int kEpiWarps = 4;
 constexpr int kMaxSplits = 16;          // split-K ways at most (a split keeps >= 8 k-steps)
 constexpr int kDecWarps = 8;
+// The EXT instances without decoders give those warps to the epilogue: its
+// three groups of four warps take every third 32 columns. (d act with the
+// derivative of SwiGLU, M = 8192: 1814 us with four warps, which then take
+// longer over a tile than the MMAs do.)
+template <bool PRE, bool EXT>
+constexpr int epi_groups() { return PRE && EXT ? (kEpiWarps + kDecWarps) / 4 : 1; }
 constexpr int kDecThreads = kDecWarps * 32;
 constexpr int kThreads = (2 + kEpiWarps + kDecWarps) * 32;  // 448
 constexpr int kTmemCols = 2 * BN;                           // two accumulators
@@ -147,6 +153,10 @@ struct Args {
     float gf0, gf1;        // SwiGLUGrad: factors of d gate and d up, or per column:
     const float* gc0;
     const float* gc1;
+    int f16;               // the images and activations are fp16 (activations prescaled, see sig)
+    // further contraction steps of low-rank adapters (CTA pairs): activations
+    // [M][64 ext] and images [Nt][ext], through tensor maps of their own
+    int ext;
     void* out_lo;          // SwiGLU, SwiGLUGrad: optional, bf16 of what out's rounding leaves
 };
 
@@ -230,11 +240,12 @@ QMLP_DEV uint32_t pack_bf16x2(float lo, float hi) {
 // (this thread's lane = token row m) -> SwiGLU act, plain output or raw fp32.
 // EXT: the instances of low-rank adapters, which add their fp32 terms.
 template <int FMT, bool EXT>
-QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg, int nt) {
+QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg, int nt, int first, int step) {
+    // this warp's columns: 32 from each of first, first + step, ...
     if (a.epi == kEpiSwiGLU) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 #pragma unroll 1
-        for (int c0 = 0; c0 < BN / 2; c0 += 32) {
+        for (int c0 = first; c0 < BN / 2; c0 += step) {
             float g[32], u[32];
             tmem_ld32(tbase + c0, g);
             tmem_ld32(tbase + BN / 2 + c0, u);
@@ -289,7 +300,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
         // one rounding between the two products of the backward pass
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 #pragma unroll 1
-        for (int c0 = 0; c0 < BN; c0 += 32) {
+        for (int c0 = first; c0 < BN; c0 += step) {
             float y[32];
             tmem_ld32(tbase + c0, y);
             const int col = nt * BN + c0;
@@ -306,7 +317,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                     float dg[4], du[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float d = y[j + e] * a.inv0 + f4_at(ad, e), gv = f4_at(g, e);
+                        const float d = scalbnf(y[j + e], -sg) * a.inv0 + f4_at(ad, e), gv = f4_at(g, e);
                         const float sg1 = 1.0f / (1.0f + expf(-gv));
                         du[e] = d * (gv * sg1) * f4_at(fu, e);
                         dg[e] = d * f4_at(u, e) * (sg1 * (1.0f + gv * (1.0f - sg1))) * f4_at(fg, e);
@@ -335,7 +346,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
     } else if (a.epi == kEpiPlain) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 #pragma unroll 1
-        for (int c0 = 0; c0 < BN; c0 += 32) {
+        for (int c0 = first; c0 < BN; c0 += step) {
             float y[32];
             tmem_ld32(tbase + c0, y);
             if (live) {
@@ -366,7 +377,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
         const int cend = a.interleaved ? cbeg + BN / 2 : BN;
         const int ocol = a.interleaved ? nt * (BN / 2) : nt * BN;
 #pragma unroll 1
-        for (int c0 = cbeg; c0 < cend; c0 += 32) {
+        for (int c0 = cbeg + first; c0 < cend; c0 += step) {
             float y[32];
             tmem_ld32(tbase + c0, y);
             if (live) {
@@ -384,6 +395,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
 template <int FMT, bool SPLIT, bool PRE, bool EXT = false>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ CUtensorMap amap, const Args a) {
     using S = Smem<FMT, PRE>;
+    constexpr int kGroups = epi_groups<PRE, EXT>();
     constexpr int kLStages = S::L;
     constexpr int kBStages = S::BS;
     constexpr int kBDiv = kBStages > 0 ? kBStages : 1;  // ring arithmetic (unused by PRE)
@@ -425,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), kEpiWarps * 32);
+            mbar_init(acc_empty(b), kGroups * kEpiWarps * 32);
         }
         mbar_init(done_bar, 1);
         *abort_flag = 0;
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k) {
                         umma_f16(d_tmem, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32),
-                                 PRE ? kIdescBF16 : kIdesc,
+                                 PRE && !(EXT && a.f16) ? kIdescBF16 : kIdesc,
                                  (ks != kb || k != 0) ? 1u : 0u);
                     }
                     issued = true;
@@ -523,9 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 mbar_wait_bounded(done_bar, 0, kGemmWaitNs);
             }
         }
-    } else if (warp < 2 + kEpiWarps) {
+    } else if (warp < 2 + kGroups * kEpiWarps) {
         // ---------------- epilogue ----------------
         const int q = warp & 3;  // TMEM lane quarter of this warp
+        const int grp = (warp - 2) / kEpiWarps;
         const int row_in_tile = q * 32 + lane;
         int tc = 0;
         for (int u = blockIdx.x; u < units; u += gridDim.x, ++tc) {
@@ -556,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     }
                 }
             } else {
-                store_tile<FMT, EXT>(a, tbase, m, live, sg, nt);
+                store_tile<FMT, EXT>(a, tbase, m, live, sg, nt, grp * 32, kGroups * 32);
             }
             tc_fence_before();
             mbar_arrive(acc_empty(buf));
@@ -744,8 +757,11 @@ QMLP_DEV void umma_commit_pair(uint32_t bar) {
 
 template <int FMT, bool PRE, bool EXT = false>
 __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_constant__ CUtensorMap amap,
-                                                                const __grid_constant__ CUtensorMap bmap, const Args a) {
+                                                                const __grid_constant__ CUtensorMap bmap,
+                                                                const __grid_constant__ CUtensorMap amap2,
+                                                                const __grid_constant__ CUtensorMap bmap2, const Args a) {
     using S = SmemP<FMT, PRE>;
+    constexpr int kGroups = epi_groups<PRE, EXT>();
     constexpr int kL = S::L, kBS = S::BS, kR = S::R;
     constexpr int kBSd = kBS > 0 ? kBS : 1;  // ring arithmetic (unused by PRE)
     extern __shared__ uint8_t dyn_smem_raw[];
@@ -772,6 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
     const int Mt2 = (a.M + 2 * BM - 1) / (2 * BM);  // 256-token tiles
     const int Nt = a.N / BN;
     const int KS = a.Kd / BK;
+    const int KT = EXT ? KS + a.ext : KS;  // with the adapters' steps
     const int units = Mt2 * Nt;  // n-tile-major, as the single-CTA kernel
 
     if (threadIdx.x == 0) {
@@ -786,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(acc_full(b), 1);
-            mbar_init(acc_empty(b), kEpiWarps * 32);
+            mbar_init(acc_empty(b), kGroups * kEpiWarps * 32);
             mbar_init(pacc(b), 1);
         }
         mbar_init(done_bar, 1);
@@ -811,7 +828,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
                 const int nt = u / Mt2, mt2 = u % Mt2;
                 const uint8_t* blk = a.tiles + (size_t)nt * KS * raw_bytes<FMT>();
                 // error-path tests: the pair's very last k-step is never loaded
-                const int ks_stop = (a.withhold && u + npairs >= units) ? KS - 1 : KS;
+                const int ks_stop = (a.withhold && u + npairs >= units) ? KT - 1 : KT;
                 for (int ks = 0; ks < ks_stop; ++ks, ++it) {
                     const int s = it % kL;
                     if (it >= kL &&
@@ -825,6 +842,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
                         // image (image rows, 128 B each, are the tensor map's
                         // rows; the row swizzle has period 8) into CTA r
                         mbar_arrive_expect_tx(full(s), 2 * (kABytes + kR));
+                        if (EXT && ks >= KS) {
+                            const int e = ks - KS, row = (nt * a.ext + e) * BN;
+#pragma unroll
+                            for (uint32_t r = 0; r < 2; ++r) {
+                                tma_load_2d_pair(base_s + S::A + s * kABytes, r, &amap2, e * BK,
+                                                 mt2 * 2 * BM + (int)r * BM, full(s));
+                                tma_load_2d_pair(base_s + S::Raw + s * kR, r, &bmap2, 0, row + (int)r * (BN / 2),
+                                                 full(s));
+                            }
+                            continue;
+                        }
                         const int row = (nt * KS + ks) * BN;
                         const bool in = QMLP_INB(((size_t)row + BN) * 128 - 1, a.wdec_bytes, 16);
 #pragma unroll
@@ -872,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
                     }
                     tc_fence_after();
                     const uint32_t d_tmem = tmem + (uint32_t)(buf * BN);
-                    for (int ks = 0; ks < KS; ++ks, ++it) {
+                    for (int ks = 0; ks < KT; ++ks, ++it) {
                         const int s = it % kL, b = it % kBSd;
                         const bool ready =
                             wait_or_abort(full(s), (uint32_t)((it / kL) & 1), abort_flag, a.err, 44, a.limit) &&
@@ -890,7 +918,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
 #pragma unroll
                         for (int k = 0; k < BK / 16; ++k)
                             umma_f16_pair(d_tmem, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32),
-                                          PRE ? kIdescPairBF16 : kIdescPair, (ks != 0 || k != 0) ? 1u : 0u);
+                                          PRE && !(EXT && a.f16) ? kIdescPairBF16 : kIdescPair,
+                                          (ks != 0 || k != 0) ? 1u : 0u);
                         issued = true;
                         umma_commit_pair(empty(s));
                         if (!PRE) umma_commit_pair(bempty(b));
@@ -913,9 +942,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
             if (rank == 0 && issued) umma_commit_pair(done_bar);
             if (rank != 0 || issued) mbar_wait_bounded(done_bar, 0, kGemmWaitNs);
         }
-    } else if (warp < 2 + kEpiWarps) {
+    } else if (warp < 2 + kGroups * kEpiWarps) {
         // ---------------- epilogue: this CTA's 128 tokens ----------------
         const int q = warp & 3;
+        const int grp = (warp - 2) / kEpiWarps;
         const int row_in_tile = q * 32 + lane;
         int tc = 0;
         for (int u = pair; u < units; u += npairs, ++tc) {
@@ -928,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
             const bool live = m < a.M;
             const int sg = live && a.sig ? a.sig[m] : 0;  // no prescale (null sig): bf16 operands
             const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
-            store_tile<FMT, EXT>(a, tbase, m, live, sg, nt);
+            store_tile<FMT, EXT>(a, tbase, m, live, sg, nt, grp * 32, kGroups * 32);
             tc_fence_before();
             mbar_arrive(acc_empty(buf));
         }
@@ -1081,83 +1111,104 @@ __global__ void __launch_bounds__(256) predecode_kernel(const uint8_t* __restric
 // into a 16-byte chunk of the swizzled image, copy the image out with one bulk
 // copy. Interleaved sources (gate and up halves) are taken gate rows first,
 // then up rows. mul0 / mul1: optional factors of the source rows (gate or the
-// projection's, and up's), rounded into the bf16 image; without them the
-// decoded values are exact, as above. Columns past the source's are zero.
+// projection's, and up's), rounded into the image, which is bf16 or, F16, fp16;
+// without them the decoded values are exact, as above. Columns past the source's are zero.
 struct PreT {
     const uint8_t* tiles;
     uint8_t* img;
     int KSs;        // 64-column blocks of a source row tile
-    int cols;       // source columns
     int steps;      // contraction steps of an image row (source rows / 64)
     int half;       // interleaved: contraction steps of the gate half, else 0
     const float* mul0;
     const float* mul1;
     size_t tiles_bytes;
 };
-constexpr int kPitchT = 256 + 2;  // bf16 of a decoded source row in shared memory
-constexpr int kSmemT = kBBytes + 64 * kPitchT * 2 + 128;
+constexpr int kPitchT = 256 + 8;  // 16-bit values of a decoded source row in shared memory
+constexpr int kSmemT = 64 * kPitchT * 2 + 128;
+static_assert(64 * kPitchT * 2 >= kBBytes, "the image takes the decoded rows' place");
 
-template <int FMT>
+template <int FMT, bool F16>
 __global__ void __launch_bounds__(256) predecode_t_kernel(const PreT a) {
     extern __shared__ __align__(128) uint8_t pre_smem[];
     const uint32_t base_s = (smem_u32(pre_smem) + 127u) & ~127u;
     uint8_t* img = pre_smem + (base_s - smem_u32(pre_smem));
-    __nv_bfloat16* dec = reinterpret_cast<__nv_bfloat16*>(img + kBBytes);
+    uint16_t* dec = reinterpret_cast<uint16_t*>(img);
     const int cs = blockIdx.x, rt = blockIdx.y;
     const bool up = a.half && cs >= a.half;
     const int n0 = (up ? cs - a.half : cs) * 64;  // first source row of its projection
     const int j = a.half ? n0 / (BN / 2) : n0 / BN;
     const int r0 = a.half ? n0 % (BN / 2) + (up ? BN / 2 : 0) : n0 % BN;
     const float* mul = up ? a.mul1 : a.mul0;
-    // 16-byte pieces of decoded values: (row, 8 columns), 32 pieces a row
-    for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-        const int r = i >> 5, c8 = i & 31, q = c8 >> 3, l = c8 & 7;
-        const size_t blk = (size_t)j * a.KSs + rt * 4 + q;
-        float f[8];
-        if (rt * 4 + q < a.KSs && QMLP_INB((blk + 1) * raw_bytes<FMT>() - 1, a.tiles_bytes, 18)) {
-            const uint8_t* raw = a.tiles + blk * raw_bytes<FMT>();
-            const int n = r0 + r;
-            uint32_t h[4];
-            if (FMT == kNVFP4) {
-                const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(raw + n * 32 + l * 4));
-                const uint32_t sc = dup_lo16(e4m3x2_to_f16x2(__ldg(raw + kRawCodes + n * 4 + (l >> 1))));
-                e2m1x4_to_f16x2x4(w, h[0], h[1], h[2], h[3]);
+    // 16-byte pieces of decoded values: (row, 8 columns), 32 pieces a row; all
+    // of a thread's loads go out before the first is used
+    constexpr int kItems = 64 * 32 / 256;
+    uint2 w[kItems];
+    uint32_t sc[kItems];
+    float mu[kItems];
+    const int c8 = threadIdx.x & 31, q = c8 >> 3, l = c8 & 7;
+    const size_t blk = (size_t)j * a.KSs + rt * 4 + q;
+    const bool in = rt * 4 + q < a.KSs && QMLP_INB((blk + 1) * raw_bytes<FMT>() - 1, a.tiles_bytes, 18);
+    const uint8_t* raw = a.tiles + (in ? blk : 0) * raw_bytes<FMT>();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = hmul2_u32(h[e], sc);
-            } else {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(raw + n * 64 + l * 8));
-                e4m3x4_to_f16x2x2(w.x, h[0], h[1]);
-                e4m3x4_to_f16x2x2(w.y, h[2], h[3]);
-            }
-            const float m = mul ? __ldg(mul + n0 + r) : 1.0f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
-                f[2 * e] = v.x * m;
-                f[2 * e + 1] = v.y * m;
-            }
+    for (int i = 0; i < kItems; ++i) {
+        const int r = (threadIdx.x >> 5) + 8 * i, n = r0 + r;
+        w[i] = make_uint2(0, 0);
+        sc[i] = 0;
+        mu[i] = 1.0f;
+        if (!in) continue;
+        if (FMT == kNVFP4) {
+            w[i].x = __ldg(reinterpret_cast<const uint32_t*>(raw + n * 32 + l * 4));
+            sc[i] = __ldg(raw + kRawCodes + n * 4 + (l >> 1));
         } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = 0.0f;
+            w[i] = __ldg(reinterpret_cast<const uint2*>(raw + n * 64 + l * 8));
         }
-        uint32_t* d = reinterpret_cast<uint32_t*>(dec + r * kPitchT + c8 * 8);
+        if (mul) mu[i] = __ldg(mul + n0 + r);
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+    for (int i = 0; i < kItems; ++i) {
+        const int r = (threadIdx.x >> 5) + 8 * i;
+        uint32_t h[4], o[4];
+        if (FMT == kNVFP4) {
+            const uint32_t s2 = dup_lo16(e4m3x2_to_f16x2(sc[i]));
+            e2m1x4_to_f16x2x4(w[i].x, h[0], h[1], h[2], h[3]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = hmul2_u32(h[e], s2);
+        } else {
+            e4m3x4_to_f16x2x2(w[i].x, h[0], h[1]);
+            e4m3x4_to_f16x2x2(w[i].y, h[2], h[3]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+            if (F16) {
+                const __half2 p = __floats2half2_rn(v.x * mu[i], v.y * mu[i]);
+                o[e] = *reinterpret_cast<const uint32_t*>(&p);
+            } else {
+                o[e] = pack_bf16x2(v.x * mu[i], v.y * mu[i]);
+            }
+        }
+        *reinterpret_cast<uint4*>(dec + r * kPitchT + c8 * 8) = make_uint4(o[0], o[1], o[2], o[3]);
     }
     __syncthreads();
-    // a thread a pair of columns and a chunk of eight source rows
-    for (int i = threadIdx.x; i < 128 * 8; i += 256) {
-        const int k = (i & 127) * 2, l = i >> 7;
-        uint32_t w[8];
+    // a thread a pair of columns and four chunks of eight source rows, taken
+    // into registers before the image overwrites them
+    const int k = (threadIdx.x & 127) * 2, l0 = threadIdx.x >> 7;
+    uint32_t v[4][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const uint32_t*>(dec + (l * 8 + e) * kPitchT + k);
-        uint4 lo, hi;
-        lo = make_uint4(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410),
-                        __byte_perm(w[4], w[5], 0x5410), __byte_perm(w[6], w[7], 0x5410));
-        hi = make_uint4(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632),
-                        __byte_perm(w[4], w[5], 0x7632), __byte_perm(w[6], w[7], 0x7632));
-        *reinterpret_cast<uint4*>(img + k * 128 + ((l ^ (k & 7)) * 16)) = lo;
-        *reinterpret_cast<uint4*>(img + (k + 1) * 128 + ((l ^ ((k + 1) & 7)) * 16)) = hi;
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[i][e] = *reinterpret_cast<const uint32_t*>(dec + ((l0 + 2 * i) * 8 + e) * kPitchT + k);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int l = l0 + 2 * i;
+        *reinterpret_cast<uint4*>(img + k * 128 + ((l ^ (k & 7)) * 16)) =
+            make_uint4(__byte_perm(v[i][0], v[i][1], 0x5410), __byte_perm(v[i][2], v[i][3], 0x5410),
+                       __byte_perm(v[i][4], v[i][5], 0x5410), __byte_perm(v[i][6], v[i][7], 0x5410));
+        *reinterpret_cast<uint4*>(img + (k + 1) * 128 + ((l ^ ((k + 1) & 7)) * 16)) =
+            make_uint4(__byte_perm(v[i][0], v[i][1], 0x7632), __byte_perm(v[i][2], v[i][3], 0x7632),
+                       __byte_perm(v[i][4], v[i][5], 0x7632), __byte_perm(v[i][6], v[i][7], 0x7632));
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
@@ -1293,8 +1344,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // The CTA-pair GEMM over `pairs_wanted` clusters of two (fewer if fewer fit at
 // once: the pairs loop over the tiles).
 template <int FMT, bool PRE, bool EXT = false>
-cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const Args& a, int pairs_wanted,
-                        cudaStream_t s) {
+cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const CUtensorMap& map2,
+                        const CUtensorMap& bmap2, const Args& a, int pairs_wanted, cudaStream_t s) {
     static int max_pairs = -1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -1319,7 +1370,7 @@ cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const A
         max_pairs = n;
     }
     cfg.gridDim = dim3((unsigned)(2 * std::min(pairs_wanted, max_pairs)));
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<FMT, PRE, EXT>, map, bmap, a);
+    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<FMT, PRE, EXT>, map, bmap, map2, bmap2, a);
 }
 
 template <int FMT, bool PRE, bool EXT = false>
@@ -1383,31 +1434,25 @@ cudaError_t launch_gemm_predecode(const GemmProj& P, uint8_t* wdec, size_t wdec_
 
 size_t gemm_decoded_t_bytes(int N, int K) { return (size_t)((K + BN - 1) / BN) * (N / BK) * kBBytes; }
 
-cudaError_t launch_gemm_predecode_t(const GemmProj& P, const float* mul0, const float* mul1, uint8_t* img,
-                                    size_t img_bytes, cudaStream_t s) {
+cudaError_t launch_gemm_predecode_t(const GemmProj& P, const float* mul0, const float* mul1, bool f16,
+                                    uint8_t* img, size_t img_bytes, cudaStream_t s) {
     if (!gemm_supported(P.K, P.N) || !P.tiles || !img || img_bytes < gemm_decoded_t_bytes(P.N, P.K))
         return cudaErrorInvalidValue;
     PreT a;
     a.tiles = P.tiles;
     a.img = img;
     a.KSs = P.K / BK;
-    a.cols = P.K;
     a.steps = P.N / BK;
     a.half = P.interleaved ? P.N / 2 / BK : 0;
     a.mul0 = mul0;
     a.mul1 = mul1;
     a.tiles_bytes = gemm_tiles_bytes(P.fmt, P.N, P.K);
-    static bool attr = false;
-    if (!attr) {
-        cudaError_t e = cudaFuncSetAttribute(predecode_t_kernel<kNVFP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemT);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(predecode_t_kernel<kFP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemT);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
     const dim3 grid((unsigned)a.steps, (unsigned)((P.K + BN - 1) / BN));
-    if (P.fmt == kFP8) predecode_t_kernel<kFP8><<<grid, 256, kSmemT, s>>>(a);
-    else predecode_t_kernel<kNVFP4><<<grid, 256, kSmemT, s>>>(a);
+    static_assert(kSmemT <= 48 * 1024, "no attribute needed");
+    if (P.fmt == kFP8 && f16) predecode_t_kernel<kFP8, true><<<grid, 256, kSmemT, s>>>(a);
+    else if (P.fmt == kFP8) predecode_t_kernel<kFP8, false><<<grid, 256, kSmemT, s>>>(a);
+    else if (f16) return cudaErrorInvalidValue;
+    else predecode_t_kernel<kNVFP4, false><<<grid, 256, kSmemT, s>>>(a);
     return cudaPeekAtLastError();
 }
 
@@ -1446,7 +1491,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
 
     // 1. per-token fp16 prescale of the activations (decoder-warp GEMMs,
     //    whose decoders write fp16 weights)
-    if (!dq) {
+    if (!dq || L.f16) {
         const int pgrid = std::min(L.M, 8 * std::max(num_sms, 1));
         prescale_rows_kernel<<<pgrid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(L.a),
                                                     static_cast<__half*>(L.a16), L.sig, L.M, P.K);
@@ -1461,8 +1506,9 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     const cuuint64_t strides[1] = {(cuuint64_t)P.K * 2};
     const cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)BM};
     const cuuint32_t estr[2] = {1, 1};
-    if (enc(&map, dq ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
-            dq ? const_cast<void*>(L.a) : L.a16, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const bool bf = dq && !L.f16;
+    if (enc(&map, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
+            bf ? const_cast<void*>(L.a) : L.a16, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
@@ -1481,7 +1527,9 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.cs0 = P.cs0;
     a.cs1 = P.cs1;
     if (P.fmt == kFP8 && (!P.cs0 || (P.interleaved && !P.cs1))) return cudaErrorInvalidValue;
-    a.sig = dq ? nullptr : L.sig;
+    a.sig = bf ? nullptr : L.sig;
+    a.f16 = L.f16 ? 1 : 0;
+    a.ext = L.ext;
     a.out = L.out;
     a.ldo = L.epi == kEpiSwiGLU ? P.N / 2 : (L.epi == kEpiRaw && P.interleaved ? P.N / 2 : P.N);
     a.add = L.add;
@@ -1494,7 +1542,8 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.gc0 = L.gc0;
     a.gc1 = L.gc1;
     a.out_lo = L.out_lo;
-    const bool grad = L.epi == kEpiSwiGLUGrad, ext = L.add || L.gu_g || grad;
+    const bool grad = L.epi == kEpiSwiGLUGrad, ext = L.add || L.gu_g || grad || L.ext || (dq && L.f16);
+    if (L.ext && (!L.pair || !dq || L.f16 || !L.ext_a || !L.ext_b)) return cudaErrorInvalidValue;
     if (ext && (L.epi == kEpiRaw || (L.pair && !dq) || L.ldadd % 4 || (grad && (!L.gu_g || L.ncols > P.N))))
         return cudaErrorInvalidValue;
     a.err = L.err;
@@ -1525,8 +1574,8 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
         if (L.M < kPairMinM) return cudaErrorInvalidValue;
         const int pairs = std::min(((L.M + 2 * BM - 1) / (2 * BM)) * (P.N / BN), std::max(num_sms, 2) / 2);
         if (!dq)
-            return P.fmt == kFP8 ? launch_pair<kFP8, false>(map, map, a, pairs, s)
-                                 : launch_pair<kNVFP4, false>(map, map, a, pairs, s);
+            return P.fmt == kFP8 ? launch_pair<kFP8, false>(map, map, map, map, a, pairs, s)
+                                 : launch_pair<kNVFP4, false>(map, map, map, map, a, pairs, s);
         // the decoded images as rows of 128 bytes, 128-row boxes (a CTA's
         // half of a k-step's image), no swizzle (the images carry it)
         CUtensorMap bmap;
@@ -1537,11 +1586,24 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
-        if (ext)
-            return P.fmt == kFP8 ? launch_pair<kFP8, true, true>(map, bmap, a, pairs, s)
-                                 : launch_pair<kNVFP4, true, true>(map, bmap, a, pairs, s);
-        return P.fmt == kFP8 ? launch_pair<kFP8, true>(map, bmap, a, pairs, s)
-                             : launch_pair<kNVFP4, true>(map, bmap, a, pairs, s);
+        if (!ext)
+            return P.fmt == kFP8 ? launch_pair<kFP8, true>(map, bmap, map, bmap, a, pairs, s)
+                                 : launch_pair<kNVFP4, true>(map, bmap, map, bmap, a, pairs, s);
+        CUtensorMap map2 = map, bmap2 = bmap;
+        if (a.ext) {  // the adapters' steps: the same boxes over their own arrays
+            const cuuint64_t edims[2] = {(cuuint64_t)a.ext * BK, (cuuint64_t)L.M};
+            const cuuint64_t estrides[1] = {(cuuint64_t)a.ext * BK * 2};
+            const cuuint64_t ebdims[2] = {128, (cuuint64_t)(P.N / BN) * a.ext * BN};
+            if (enc(&map2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(L.ext_a), edims, estrides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||
+                enc(&bmap2, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(L.ext_b), ebdims, bstrides, bbox, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+                return cudaErrorInvalidValue;
+        }
+        return P.fmt == kFP8 ? launch_pair<kFP8, true, true>(map, bmap, map2, bmap2, a, pairs, s)
+                             : launch_pair<kNVFP4, true, true>(map, bmap, map2, bmap2, a, pairs, s);
     }
     const int grid = std::min(tiles0 * a.splits, std::max(num_sms, 1));
     return P.fmt == kFP8 ? launch_fmt<kFP8>(map, a, ext, grid, s) : launch_fmt<kNVFP4>(map, a, ext, grid, s);

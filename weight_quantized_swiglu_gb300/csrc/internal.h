@@ -188,6 +188,10 @@ struct GemmLaunch {
     float gf0 = 1.0f, gf1 = 1.0f;  // SwiGLUGrad: factors of d gate, d up, or per column:
     const float* gc0 = nullptr;
     const float* gc1 = nullptr;
+    bool f16 = false;            // dequantise-once: images in fp16, activations prescaled to fp16 (into a16)
+    int ext = 0;                 // CTA pairs: further contraction steps of 64, bf16: activations [M][64 ext]
+    const void* ext_a = nullptr; // and stage images [N / 256][ext] (low-rank adapters)
+    const void* ext_b = nullptr;
     void* out_lo = nullptr;      // with gu_g: optional, bf16 of what the rounding of out leaves
     bool images_ready = false;  // dequantise-once: wdec already holds w's images (no predecode launch)
 };
@@ -200,7 +204,7 @@ cudaError_t launch_gemm_predecode(const GemmProj& P, uint8_t* wdec, size_t wdec_
 // Images of the transposed projection (contraction over its N rows, its K
 // columns as output rows, padded to 256).
 size_t gemm_decoded_t_bytes(int N, int K);
-cudaError_t launch_gemm_predecode_t(const GemmProj& P, const float* mul0, const float* mul1, uint8_t* img,
+cudaError_t launch_gemm_predecode_t(const GemmProj& P, const float* mul0, const float* mul1, bool f16, uint8_t* img,
                                     size_t img_bytes, cudaStream_t s);
 inline size_t gemm_gu_bytes(int M, int I) { return (size_t)((M + 31) / 32) * 32 * I * 4; }
 bool gemm_supported(int K, int N);
