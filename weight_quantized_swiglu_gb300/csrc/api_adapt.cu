@@ -43,6 +43,14 @@ struct qmlp_train_s {
     __nv_bfloat16* dvd = nullptr;    // likewise [max_M][Rp]
     float* part = nullptr;
     int* cnt = nullptr;
+    // From kPairMinM tokens on the adapter's terms are further contraction
+    // steps of the GEMMs: T words of v beside T of the adapter (see LrImage).
+    // NVFP4's one factor a projection goes into v (T = 2); FP8's per-channel
+    // ones into the adapter's images (T = 3), if all can be divided by.
+    bool steps = true;
+    int T = 2;
+    uint8_t* img_gu = nullptr;       // images of B gate/up, B down; of A down, A gate/up
+    uint8_t* img_d = nullptr;
     // FP8: the factors that d gate and d up carry (1 where a channel's is too
     // small to divide by: it is then in the weights' image, `row`)
     float* eff = nullptr;            // [2][I]
@@ -358,12 +366,35 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
 extern "C++" {
 namespace {
 
+// Where a call keeps c z A^T (or c dy B) of every token: bf16 words side by
+// side in rows of ld, nc columns a word. As further steps of a GEMM: T words
+// (the third again the first) and zeros up to a multiple of 64, with the parts'
+// factors divided out; else kLrWords words for the expand kernel.
+struct Words {
+    __nv_bfloat16* p = nullptr;
+    int nc = 0, ld = 0;
+    bool ext = false;
+    int T = 0;
+    int steps() const { return ld / 64; }
+};
+int word_ld(int nc, int T) { return (nc * T + 63) / 64 * 64; }
+Words words_of(__nv_bfloat16* p, int nc, bool ext, int T) {
+    Words w;
+    w.p = p;
+    w.nc = nc;
+    w.ext = ext;
+    w.T = ext ? T : kLrWords;
+    w.ld = ext ? word_ld(nc, T) : nc * kLrWords;
+    return w;
+}
+size_t words_room(size_t M, int nc) { return M * std::max(word_ld(nc, 3), nc * kLrWords); }
+
 // What a forward keeps (see qmlp_train_saved_bytes).
 struct Saved {
     uint8_t *g, *u;          // fp32 gate and up, in quads of 32 rows
     __nv_bfloat16* act;      // [M][I]
     __nv_bfloat16* act_lo;   // likewise, its second word (M < kTwoWordM), or null
-    __nv_bfloat16 *vgu, *vd; // words of [M][2 Rp] and [M][Rp]
+    Words vgu, vd;           // c A z of gate and up, of down
     size_t bytes;
 };
 Saved saved_of(const qmlp_train_s* t, int M, const void* base) {
@@ -379,8 +410,9 @@ Saved saved_of(const qmlp_train_s* t, int M, const void* base) {
     v.u = take(gemm_gu_bytes(M, (int)I));
     v.act = reinterpret_cast<__nv_bfloat16*>(take(m * I * 2));
     v.act_lo = M < kTwoWordM ? reinterpret_cast<__nv_bfloat16*>(take(m * I * 2)) : nullptr;
-    v.vgu = reinterpret_cast<__nv_bfloat16*>(take(kLrWords * m * 2 * R * 2));
-    v.vd = reinterpret_cast<__nv_bfloat16*>(take(kLrWords * m * R * 2));
+    const bool ext = t->steps && M >= kPairMinM;
+    v.vgu = words_of(reinterpret_cast<__nv_bfloat16*>(take(words_room(m, 2 * (int)R) * 2)), 2 * (int)R, ext, t->T);
+    v.vd = words_of(reinterpret_cast<__nv_bfloat16*>(take(words_room(m, (int)R) * 2)), (int)R, ext, t->T);
     v.bytes = at - reinterpret_cast<size_t>(base);
     return v;
 }
@@ -388,28 +420,31 @@ Saved saved_of(const qmlp_train_s* t, int M, const void* base) {
 int tiles_for(int M) { return (M + kLrTile - 1) / kLrTile; }
 
 // v = c z W^T for every token (one adapter), W [nc][D] or, trans, [D][nc].
-LrShrink shrink_all(const qmlp_train_s* t, const void* z, int M, int D, __nv_bfloat16* v, int ldv) {
+LrShrink shrink_all(const qmlp_train_s* t, const void* z, int M, int D, const Words& w) {
     LrShrink a;
     a.tok.M = M;
     a.x = static_cast<const __nv_bfloat16*>(z);
     a.ldx = D;
     a.D = D;
     a.scale = t->l->scale;
-    a.v = v;
-    a.v_word = (size_t)M * ldv;
-    a.ldv = ldv;
+    a.v = w.p;
+    a.v_word = w.nc;
+    a.ldv = w.ld;
+    a.words = w.T;
+    a.again = w.ext && w.T == 3;
+    a.pad = w.ld - w.nc * w.T;
     a.part = t->l->part;
     a.cnt = t->l->cnt;
     return a;
 }
 // The adapter's terms into l->y: v W^T, W [N][rc] or, trans, [rc][N].
-cudaError_t expand_all(const qmlp_train_s* t, const __nv_bfloat16* v, int M, int rc, int zs, const __nv_bfloat16* w,
+cudaError_t expand_all(const qmlp_train_s* t, const Words& v, int M, int rc, int zs, const __nv_bfloat16* w,
                        size_t w_z, int N, bool trans, cudaStream_t s) {
     LrExpand a;
     a.tok.M = M;
-    a.v = v;
-    a.ldv = rc * zs;
-    a.v_word = (size_t)M * a.ldv;
+    a.v = v.p;
+    a.ldv = v.ld;
+    a.v_word = v.nc;
     a.w = w;
     a.w_z = w_z;
     a.N = N;
@@ -433,6 +468,17 @@ GemmLaunch dq_gemm(const qmlp_train_s* t, int M) {
     return g;
 }
 
+// The adapter's terms of a GEMM: further steps, or added by its epilogue.
+void extend(GemmLaunch& g, const Words& w, const uint8_t* img) {
+    g.ext = w.steps();
+    g.ext_a = w.p;
+    g.ext_b = img;
+}
+void add_terms(GemmLaunch& g, const float* y, size_t ld) {
+    g.add = y;
+    g.ldadd = ld;
+}
+
 // Work on the handle's side stream between the events: `fork` follows all that
 // is on s, and the caller waits for ev_join.
 template <typename F>
@@ -450,12 +496,17 @@ cudaError_t beside(qmlp_t* h, cudaStream_t s, F&& f) {
         if (try_e != cudaSuccess) return try_e;            \
     } while (0)
 
-LrPack pack_train(const qmlp_train_s* t, const qmlp_adapter* a, bool back) {
+// What the low-rank kernels read of the adapter, padded: the A parts for the
+// forward, the B parts (gate's and up's over the factor that their gradients
+// carry) for the backward pass; both where expand_all adds the other side.
+LrPack pack_train(const qmlp_train_s* t, const qmlp_adapter* a, bool back, bool both) {
     const qmlp_lora_t* l = t->l;
     LrPack p = pack_of(l, 0, a);
+    p.first = back && !both ? 3 : 0;
+    p.count = both ? 6 : 3;
     if (!back) return p;
     const size_t n = (size_t)t->h->I * l->Rp;
-    for (int i = 0; i < 2; ++i) {  // gate, up: over the factor that their gradients carry
+    for (int i = 0; i < 2; ++i) {
         LrPackPart& q = p.part[3 + i];
         q.dst_h = t->bq + i * n;
         q.dst_l = t->bq + (2 + i) * n;
@@ -465,21 +516,62 @@ LrPack pack_train(const qmlp_train_s* t, const qmlp_adapter* a, bool back) {
     return p;
 }
 
+const __nv_bfloat16* bf(const void* p) { return static_cast<const __nv_bfloat16*>(p); }
+
+// The images of `rows` rows (interleaved: of each part) for words w.
+LrImage image_of(const qmlp_train_s* t, const qmlp_adapter* a, const Words& w, int rows, bool interleaved, int parts,
+                 uint8_t* img) {
+    LrImage g;
+    g.r = a->rank;
+    g.R = t->l->Rp;
+    g.parts = parts;
+    g.T = w.T;
+    g.N = rows;
+    g.interleaved = interleaved;
+    g.tiles = interleaved ? rows / 128 : (rows + 255) / 256;
+    g.ext = w.steps();
+    g.img = img;
+    return g;
+}
+
 cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x, int M, void* out, const Saved& v,
                           cudaStream_t s) {
     qmlp_t* h = t->h;
     const qmlp_lora_t* l = t->l;
     const int K = h->K, I = h->I, R = l->Rp;
+    const bool ext = v.vgu.ext, fp8 = h->fmt == kFP8;
     TRY(launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s));
     TRY(beside(h, s, [&](cudaStream_t b) {
         return launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, b);
     }));
     if (ad) {
-        TRY(launch_lr_pack(pack_train(t, ad, false), s));
-        LrShrink a = shrink_all(t, x, M, K, v.vgu, 2 * R);
+        TRY(launch_lr_pack(pack_train(t, ad, false, !ext), s));
+        LrShrink a = shrink_all(t, x, M, K, v.vgu);
         a.w = l->a_gu;
+        if (ext && !fp8) {
+            a.mul0 = 1.0f / h->gv[0].inv_g;
+            a.mul1 = 1.0f / h->gv[1].inv_g;
+            a.half = R;
+        }
         TRY(launch_lr_shrink(a, 2 * R, false, tiles_for(M), 1, h->num_sms, s));
-        TRY(expand_all(t, v.vgu, M, R, 2, l->b_gu, (size_t)I * R, I, false, s));
+        if (ext) {
+            LrImage m = image_of(t, ad, v.vgu, I, true, 2, t->img_gu);
+            m.src[0] = bf(ad->gate_b);
+            m.src[1] = bf(ad->up_b);
+            m.sn = ad->rank;
+            m.sj = 1;
+            m.div[0] = t->eff;
+            m.div[1] = t->eff + I;
+            TRY(launch_lr_image(m, h->num_sms, s));
+            m = image_of(t, ad, v.vd, K, false, 1, t->img_d);
+            m.src[0] = bf(ad->down_b);
+            m.sn = ad->rank;
+            m.sj = 1;
+            m.div[0] = h->gv[2].chs;
+            TRY(launch_lr_image(m, h->num_sms, s));
+        } else {
+            TRY(expand_all(t, v.vgu, M, R, 2, l->b_gu, (size_t)I * R, I, false, s));
+        }
     }
     GemmLaunch g = dq_gemm(t, M);
     g.epi = kEpiSwiGLU;
@@ -492,16 +584,17 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     g.gu_u = v.u;
     if (ad) {
         g.out_lo = v.act_lo;
-        g.add = l->y;
-        g.ldadd = (size_t)2 * I;
+        if (ext) extend(g, v.vgu, t->img_gu);
+        else add_terms(g, l->y, (size_t)2 * I);
     }
     TRY(launch_gemm(g, h->num_sms, s));
     if (ad) {
-        LrShrink a = shrink_all(t, v.act, M, I, v.vd, R);
+        LrShrink a = shrink_all(t, v.act, M, I, v.vd);
         a.x_lo = v.act_lo;
         a.w = l->a_d;
+        if (ext && !fp8) a.mul0 = 1.0f / h->gv[2].inv_g;
         TRY(launch_lr_shrink(a, R, false, tiles_for(M), 1, h->num_sms, s));
-        TRY(expand_all(t, v.vd, M, R, 1, l->b_d, 0, K, false, s));
+        if (!ext) TRY(expand_all(t, v.vd, M, R, 1, l->b_d, 0, K, false, s));
     }
     TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
     g = dq_gemm(t, M);
@@ -511,10 +604,8 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     g.wdec_bytes = h->wdec2_bytes;
     g.a = v.act;
     g.out = out;
-    if (ad) {
-        g.add = l->y;
-        g.ldadd = K;
-    }
+    if (ad && ext) extend(g, v.vd, t->img_d);
+    else if (ad) add_terms(g, l->y, K);
     return launch_gemm(g, h->num_sms, s);
 }
 
@@ -524,6 +615,9 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     const qmlp_lora_t* l = t->l;
     const int K = h->K, I = h->I, R = l->Rp;
     const bool fp8 = h->fmt == kFP8;
+    // d act's GEMM of FP8 has fp16 operands: its adapter terms are added
+    const bool ext = v.vgu.ext, ext_d = ext && !fp8;
+    const Words wd = words_of(t->dvd, R, ext_d, 2), wv = words_of(t->dv, 2 * R, ext, 2);
     const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(dout);
     // the transposed images: down's (FP8: in fp16 with its per-channel factors,
     // which lie along the contraction here; dout is then prescaled to fp16, so
@@ -534,11 +628,28 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
         return launch_gemm_predecode_t(h->gm_gu, t->row, t->row ? t->row + I : nullptr, false, h->wdec, h->wdec_bytes, b);
     }));
     if (ad) {
-        TRY(launch_lr_pack(pack_train(t, ad, true), s));
-        LrShrink a = shrink_all(t, dy, M, K, t->dvd, R);
+        TRY(launch_lr_pack(pack_train(t, ad, true, !ext_d || !ext), s));
+        LrShrink a = shrink_all(t, dy, M, K, wd);
         a.w = l->b_d;
+        if (ext_d) a.mul0 = 1.0f / h->gv[2].inv_g;
         TRY(launch_lr_shrink(a, R, true, tiles_for(M), 1, h->num_sms, s));
-        TRY(expand_all(t, t->dvd, M, R, 1, l->a_d, 0, I, true, s));
+        if (ext_d) {
+            LrImage m = image_of(t, ad, wd, I, false, 1, t->img_d);
+            m.src[0] = bf(ad->down_a);
+            m.sn = 1;
+            m.sj = I;
+            TRY(launch_lr_image(m, h->num_sms, s));
+        } else {
+            TRY(expand_all(t, wd, M, R, 1, l->a_d, 0, I, true, s));
+        }
+        if (ext) {
+            LrImage m = image_of(t, ad, wv, K, false, 2, t->img_gu);
+            m.src[0] = bf(ad->gate_a);
+            m.src[1] = bf(ad->up_a);
+            m.sn = 1;
+            m.sj = K;
+            TRY(launch_lr_image(m, h->num_sms, s));
+        }
     }
     // d act, and through the activation d gate and d up
     GemmLaunch g = dq_gemm(t, M);
@@ -562,12 +673,12 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     __nv_bfloat16* lo = ad && M < kTwoWordM ? t->dgu_lo : nullptr;
     if (ad) {
         g.out_lo = lo;
-        g.add = l->y;
-        g.ldadd = I;
+        if (ext_d) extend(g, wd, t->img_d);
+        else add_terms(g, l->y, I);
     }
     TRY(launch_gemm(g, h->num_sms, s));
     if (ad) {
-        LrShrink a = shrink_all(t, t->dgu, M, I, t->dv, 2 * R);
+        LrShrink a = shrink_all(t, t->dgu, M, I, wv);
         a.x_lo = lo;
         a.ldx = (size_t)2 * I;
         a.x_z = I;
@@ -575,7 +686,7 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
         a.w_lo = t->bq + (size_t)2 * I * R;
         a.w_z = (size_t)I * R;
         TRY(launch_lr_shrink(a, R, true, tiles_for(M), 2, h->num_sms, s));
-        TRY(expand_all(t, t->dv, M, 2 * R, 1, l->a_gu, 0, K, true, s));
+        if (!ext) TRY(expand_all(t, wv, M, 2 * R, 1, l->a_gu, 0, K, true, s));
     }
     TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
     g = dq_gemm(t, M);
@@ -587,31 +698,32 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     g.wdec_bytes = h->wdec_bytes;
     g.a = t->dgu;
     g.out = dx;
-    if (ad) {
-        g.add = l->y;
-        g.ldadd = K;
-    }
+    if (ad && ext) extend(g, wv, t->img_gu);
+    else if (ad) add_terms(g, l->y, K);
     TRY(launch_gemm(g, h->num_sms, s));
     if (!gr) return cudaSuccess;
-    auto bf = [](const void* p) { return static_cast<__nv_bfloat16*>(const_cast<void*>(p)); };
+    auto to = [](const void* p) { return static_cast<__nv_bfloat16*>(const_cast<void*>(p)); };
     LrTokGrad q;
     q.M = M;
     q.r = ad->rank;
     q.Rp = R;
     q.part = t->part;
     q.cnt = t->cnt;
-    auto v_of = [&](LrTokGrad& c, const __nv_bfloat16* p, int ld) {
-        c.v = p;
-        c.ldv = ld;
-        c.v_word = (size_t)M * ld;
+    auto v_of = [&](LrTokGrad& c, const Words& w) {
+        c.v = w.p;
+        c.ldv = w.ld;
+        c.v_word = w.nc;
     };
+    // NVFP4's factors that v lacks as a GEMM's operand
+    const bool lack = ext && !fp8;
     if (gr->down_b) {
         LrTokGrad c = q;
         c.x = dy;
         c.ldx = c.D = K;
-        v_of(c, v.vd, R);
+        v_of(c, v.vd);
+        if (lack) c.mul[0] = h->gv[2].inv_g;
         c.rows_d = true;
-        c.out[0] = bf(gr->down_b);
+        c.out[0] = to(gr->down_b);
         TRY(launch_lr_tokgrad(c, R, 1, h->num_sms, s));
     }
     if (gr->down_a) {
@@ -619,8 +731,9 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
         c.x = v.act;
         c.x_lo = v.act_lo;
         c.ldx = c.D = I;
-        v_of(c, t->dvd, R);
-        c.out[0] = bf(gr->down_a);
+        v_of(c, wd);
+        if (ext_d) c.mul[0] = h->gv[2].inv_g;
+        c.out[0] = to(gr->down_a);
         TRY(launch_lr_tokgrad(c, R, 1, h->num_sms, s));
     }
     if (gr->gate_b || gr->up_b) {
@@ -630,13 +743,14 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
         c.ldx = (size_t)2 * I;
         c.x_z = I;
         c.D = I;
-        v_of(c, v.vgu, 2 * R);
+        v_of(c, v.vgu);
         c.rows_d = true;
-        c.out[0] = bf(gr->gate_b);
-        c.out[1] = bf(gr->up_b);
+        c.out[0] = to(gr->gate_b);
+        c.out[1] = to(gr->up_b);
         for (int i = 0; i < 2; ++i) {
+            // d gate carries the factor, and v lacks it where it is NVFP4's operand
             c.div[i] = t->eff ? t->eff + (size_t)i * I : nullptr;
-            c.div_all[i] = h->gv[i].inv_g;
+            c.mul[i] = lack ? 1.0f : 1.0f / h->gv[i].inv_g;
         }
         TRY(launch_lr_tokgrad(c, R, 2, h->num_sms, s));
     }
@@ -644,9 +758,9 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
         LrTokGrad c = q;
         c.x = static_cast<const __nv_bfloat16*>(x);
         c.ldx = c.D = K;
-        v_of(c, t->dv, 2 * R);
-        c.out[0] = bf(gr->gate_a);
-        c.out[1] = bf(gr->up_a);
+        v_of(c, wv);
+        c.out[0] = to(gr->gate_a);
+        c.out[1] = to(gr->up_a);
         TRY(launch_lr_tokgrad(c, 2 * R, 1, h->num_sms, s));
     }
     return cudaSuccess;
@@ -661,8 +775,8 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
     *out = nullptr;
     if (!h) return QMLP_ERR_INVALID_ARG;
     if (!h->has_gemm || !h->wdec || !h->side || max_rank < 1 || max_rank > kLrMaxRank) return QMLP_ERR_SHAPE;
-    if (h->fmt == kNVFP4 && (!(fabsf(h->gv[0].inv_g) >= kLeastFactor) || !(fabsf(h->gv[1].inv_g) >= kLeastFactor)))
-        return QMLP_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)
+        if (h->fmt == kNVFP4 && !(fabsf(h->gv[i].inv_g) >= kLeastFactor)) return QMLP_ERR_INVALID_ARG;
     qmlp_train_t* t = new qmlp_train_t();
     t->h = h;
     qmlp_status st = qmlp_lora_create(&t->l, h, 1, max_rank, stream);
@@ -681,8 +795,13 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
     get(&t->bq, 4 * I * R);
     get(&t->dgu, M * 2 * I);
     get(&t->dgu_lo, std::min<size_t>(M, kTwoWordM) * 2 * I);
-    get(&t->dv, kLrWords * M * 2 * R);
-    get(&t->dvd, kLrWords * M * R);
+    get(&t->dv, words_room(M, 2 * (int)R));
+    get(&t->dvd, words_room(M, (int)R));
+    t->T = h->fmt == kFP8 ? 3 : 2;
+    // gate/up: I / 128 tiles, or K / 256 of the transposed; down: K / 256 or I / 256
+    const size_t tg = std::max(I / 128, K / 256), td = std::max(K / 256, (I + 255) / 256);
+    get(&t->img_gu, tg * (size_t)(word_ld(2 * (int)R, 3) / 64) * 32768);
+    get(&t->img_d, td * (size_t)(word_ld((int)R, 3) / 64) * 32768);
     get(&t->part, lr_grad_part_elems(h->num_sms));
     const size_t cnt = 2 * (size_t)lr_grad_tiles((int)std::max(I, K));
     get(&t->cnt, cnt);
@@ -698,9 +817,13 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
     }
     if (e == cudaSuccess && h->fmt == kFP8) {
         // e4m3 (at most 448) times a factor under fac_d, times 2^6: under 2^15
-        std::vector<float> f(K);
-        e = cudaMemcpyAsync(f.data(), h->gv[2].chs, K * sizeof(float), cudaMemcpyDeviceToHost, s);
+        std::vector<float> f(K), fg(2 * I);
+        e = cudaMemcpyAsync(fg.data(), h->gv[0].chs, I * sizeof(float), cudaMemcpyDeviceToHost, s);
+        if (e == cudaSuccess) e = cudaMemcpyAsync(fg.data() + I, h->gv[1].chs, I * sizeof(float), cudaMemcpyDeviceToHost, s);
+        if (e == cudaSuccess) e = cudaMemcpyAsync(f.data(), h->gv[2].chs, K * sizeof(float), cudaMemcpyDeviceToHost, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        for (float v : fg) t->steps = t->steps && fabsf(v) >= kLeastFactor;
+        for (float v : f) t->steps = t->steps && fabsf(v) >= kLeastFactor;
         float top = 0.0f;
         for (float v : f)
             if (isfinite(v)) top = std::max(top, fabsf(v));

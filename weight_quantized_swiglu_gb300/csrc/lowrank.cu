@@ -228,12 +228,18 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
     const float c = a.scale ? a.scale[slot] : 1.0f;
     auto emit = [&](int row, int col, float v0, float v1) {
         __nv_bfloat16 w0[kLrWords], w1[kLrWords];
-        split_bf16(v0 * c, w0);
-        split_bf16(v1 * c, w1);
+        const float f = c * (z * NC + col < a.half ? a.mul0 : a.mul1);
+        split_bf16(v0 * f, w0);
+        split_bf16(v1 * f, w1);
+        if (a.again) w0[2] = w0[0], w1[2] = w1[0];
         __nv_bfloat16* o = a.v + (size_t)(pos0 + row) * a.ldv + z * NC + col;
 #pragma unroll
         for (int i = 0; i < kLrWords; ++i)
-            *reinterpret_cast<__nv_bfloat162*>(o + i * a.v_word) = __halves2bfloat162(w0[i], w1[i]);
+            if (i < a.words)
+                *reinterpret_cast<__nv_bfloat162*>(o + i * a.v_word) = __halves2bfloat162(w0[i], w1[i]);
+        // the columns past the words of a row that a GEMM reads whole
+        for (int p = col + z * NC; p < a.pad; p += NC * gridDim.z)
+            *reinterpret_cast<uint32_t*>(a.v + (size_t)(pos0 + row) * a.ldv + a.ldv - a.pad + p) = 0u;
     };
     if (gridDim.y == 1) {
 #pragma unroll
@@ -256,16 +262,29 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
                 *reinterpret_cast<float2*>(part + row * NC + j * 8 + 2 * t) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
         }
     if (!last_arrival(a.cnt + tile, gridDim.y)) return;
-    const float* all = a.part + tile * gridDim.y * (kT * NC);
-    for (int i = tid; i < n * (NC / 2); i += kThr) {
-        const int row = i / (NC / 2), col = (i % (NC / 2)) * 2;
-        float v0 = 0.0f, v1 = 0.0f;
-        for (unsigned s = 0; s < gridDim.y; ++s) {
-            const float2 p = __ldcg(reinterpret_cast<const float2*>(all + s * (kT * NC) + row * NC + col));
-            v0 += p.x;
-            v1 += p.y;
+    // every thread a few quads, the loads of a split in flight together (rows
+    // past n hold what an earlier launch left; they are not emitted)
+    const float4* all = reinterpret_cast<const float4*>(a.part + tile * gridDim.y * (kT * NC));
+    constexpr int kQ = kT * NC / 4, kPer = kQ / kThr;
+    float4 sum[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum[i] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+    for (unsigned s = 0; s < gridDim.y; ++s)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const float4 p = __ldcg(all + (size_t)s * kQ + tid + i * kThr);
+            sum[i].x += p.x;
+            sum[i].y += p.y;
+            sum[i].z += p.z;
+            sum[i].w += p.w;
         }
-        emit(row, col, v0, v1);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int at = (tid + i * kThr) * 4, row = at / NC, col = at % NC;
+        if (row >= n) continue;
+        emit(row, col, sum[i].x, sum[i].y);
+        emit(row, col + 2, sum[i].z, sum[i].w);
     }
 }
 
@@ -476,10 +495,10 @@ __global__ void __launch_bounds__(kThr) tokgrad_kernel(const LrTokGrad a) {
         if (d >= a.D) return;
         if (a.rows_d) {
             if (col >= a.r || !a.out[z]) return;
-            a.out[z][(size_t)d * a.r + col] = __float2bfloat16_rn(val / (a.div[z] ? a.div[z][d] : a.div_all[z]));
+            a.out[z][(size_t)d * a.r + col] = __float2bfloat16_rn(a.div[z] ? val / a.div[z][d] : val * a.mul[z]);
         } else {
             const int part = col / a.Rp, j = col % a.Rp;
-            if (j < a.r && a.out[part]) a.out[part][(size_t)j * a.D + d] = __float2bfloat16_rn(val);
+            if (j < a.r && a.out[part]) a.out[part][(size_t)j * a.D + d] = __float2bfloat16_rn(val * a.mul[part]);
         }
     };
     const int g = lane >> 2, t = lane & 3;
@@ -504,11 +523,34 @@ __global__ void __launch_bounds__(kThr) tokgrad_kernel(const LrTokGrad a) {
             for (int e = 0; e < 4; ++e)
                 part[(j * 8 + 2 * t + (e & 1)) * kGD + warp * 32 + h * 16 + g + 8 * (e >> 1)] = acc[h][j][e];
     if (!last_arrival(a.cnt + tile, gridDim.y)) return;
-    const float* all = a.part + tile * gridDim.y * (kGD * NC);
-    for (int i = tid; i < kGD * NC; i += kThr) {
-        float val = 0.0f;
-        for (unsigned s = 0; s < gridDim.y; ++s) val += __ldcg(all + (size_t)s * (kGD * NC) + i);
-        emit(i % kGD, i / kGD, val);
+    const float4* all = reinterpret_cast<const float4*>(a.part + tile * gridDim.y * (kGD * NC));
+    constexpr int kQ = kGD * NC / 4, kPer = 8;  // quads of a thread and round
+#pragma unroll 1
+    for (int b = 0; b < kQ; b += kPer * kThr) {
+        float4 sum[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum[i] = make_float4(0, 0, 0, 0);
+#pragma unroll 2
+        for (unsigned s = 0; s < gridDim.y; ++s)
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int at = b + tid + i * kThr;
+                if (kQ % (kPer * kThr) && at >= kQ) continue;
+                const float4 p = __ldcg(all + (size_t)s * kQ + at);
+                sum[i].x += p.x;
+                sum[i].y += p.y;
+                sum[i].z += p.z;
+                sum[i].w += p.w;
+            }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int at = (b + tid + i * kThr) * 4, row = at % kGD, col = at / kGD;
+            if (col >= NC) continue;
+            emit(row, col, sum[i].x);
+            emit(row + 1, col, sum[i].y);
+            emit(row + 2, col, sum[i].z);
+            emit(row + 3, col, sum[i].w);
+        }
     }
 }
 
@@ -663,7 +705,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids,
 __global__ void __launch_bounds__(256) pack_kernel(const LrPack a) {
     pdl_launch_dependents();
     pdl_wait();
-    const int p = blockIdx.y;  // 0..2: A of gate, up, down; 3..5: B
+    const int p = a.first + blockIdx.y;  // 0..2: A of gate, up, down; 3..5: B
     const LrPackPart& q = a.part[p];
     const long total = (long)q.rows * q.cols;
     for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long)gridDim.x * blockDim.x) {
@@ -680,9 +722,42 @@ __global__ void __launch_bounds__(256) pack_kernel(const LrPack a) {
             q.dst_l[i] = d[1];
         }
     }
-    if (p == 0 && blockIdx.x == 0 && threadIdx.x == 0) {
+    if (blockIdx.y == 0 && blockIdx.x == 0 && threadIdx.x == 0) {
         *a.rank_out = a.r;
         *a.scale_out = a.scale;
+    }
+}
+
+// Stage images of an adapter's side of a GEMM's further steps: 256 rows of 64
+// columns each, 128-byte swizzled (16-byte chunk l of row n at l ^ (n & 7)). A
+// column is (word, part, j): with T = 2 words (the activations' v = h + l) both
+// hold the value; with T = 3 the value over the row's factor does not fit one
+// bf16 word: h and l times its first word, h times its second.
+__global__ void __launch_bounds__(256) image_kernel(const LrImage a) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long total = (long)a.tiles * a.ext * 2048;
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
+        const int p = (int)(i & 7), row = (int)(i >> 3) & 255, e = (int)((i >> 11) % a.ext), nt = (int)((i >> 11) / a.ext);
+        const int l = p ^ (row & 7);
+        const int side = a.interleaved ? row >> 7 : 0;
+        const int n = a.interleaved ? nt * 128 + (row & 127) : nt * 256 + row;
+        __align__(16) __nv_bfloat16 o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int c = e * 64 + l * 8 + k;
+            const int w = c / (a.parts * a.R), part = (c / a.R) % a.parts, j = c % a.R;
+            float v = 0.0f;
+            if (w < a.T && j < a.r && n < a.N && a.src[part] && (!a.interleaved || part == side)) {
+                v = __bfloat162float(a.src[part][(size_t)n * a.sn + (size_t)j * a.sj]);
+                if (a.T == 3) {
+                    v /= a.div[part][n];
+                    if (w == 2) v -= __bfloat162float(__float2bfloat16_rn(v));
+                }
+            }
+            o[k] = __float2bfloat16_rn(v);
+        }
+        *reinterpret_cast<uint4*>(a.img + i * 16) = *reinterpret_cast<const uint4*>(o);
     }
 }
 
@@ -814,8 +889,13 @@ cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, in
     return cudaPeekAtLastError();
 }
 
+cudaError_t launch_lr_image(const LrImage& a, int num_sms, cudaStream_t s) {
+    const long n = (long)a.tiles * a.ext * 2048;
+    return launch_pdl(image_kernel, dim3((unsigned)std::min<long>((n + 255) / 256, 8L * num_sms)), 256, 0, a, s);
+}
+
 cudaError_t launch_lr_pack(const LrPack& a, cudaStream_t s) {
-    pack_kernel<<<dim3(256, 6), 256, 0, s>>>(a);
+    pack_kernel<<<dim3(256, a.count), 256, 0, s>>>(a);
     return cudaPeekAtLastError();
 }
 

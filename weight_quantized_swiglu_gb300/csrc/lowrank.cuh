@@ -32,9 +32,14 @@ struct LrShrink {
     const __nv_bfloat16* w_lo = nullptr;  // second word of w, or null
     size_t w_slot = 0, w_z = 0;
     const float* scale = nullptr;  // per slot
-    __nv_bfloat16* v = nullptr;    // kLrWords planes of [position][ldv], columns z * NC on
-    size_t v_word = 0;             // elements of a plane
+    __nv_bfloat16* v = nullptr;    // [position][ldv], columns z * NC on, word i at i * v_word elements
+    size_t v_word = 0;
     int ldv = 0;
+    int words = kLrWords;
+    bool again = false;            // the third word is the first once more
+    int pad = 0;                   // columns at a row's end to fill with zeros
+    float mul0 = 1.0f, mul1 = 1.0f;  // factors of the columns before and from `half` on
+    int half = 1 << 30;
     float* part = nullptr;
     int* cnt = nullptr;            // a zeroed counter a tile and part
 };
@@ -88,8 +93,8 @@ struct LrTokGrad {
     bool rows_d = false;
     int r = 0, Rp = 0;
     __nv_bfloat16* out[2] = {nullptr, nullptr};
-    const float* div[2] = {nullptr, nullptr};  // rows_d: the row's divisor, or div_all
-    float div_all[2] = {1.0f, 1.0f};
+    const float* div[2] = {nullptr, nullptr};  // rows_d: the row's divisor; else mul
+    float mul[2] = {1.0f, 1.0f};
     float* part = nullptr;
     int* cnt = nullptr;
 };
@@ -116,11 +121,24 @@ struct LrPackPart {
 };
 struct LrPack {
     LrPackPart part[6];
+    int first = 0, count = 6;  // the parts to pack
     int r = 0;
     float scale = 0.0f;
     int* rank_out = nullptr;
     float* scale_out = nullptr;
 };
+
+struct LrImage {
+    const __nv_bfloat16* src[2] = {nullptr, nullptr};  // value of row n, column j: src[part][n sn + j sj]
+    size_t sn = 0, sj = 0;
+    int r = 0, R = 0, parts = 1, T = 2;
+    const float* div[2] = {nullptr, nullptr};  // T = 3: the rows' factors
+    int N = 0;            // rows of a part
+    int interleaved = 0;  // tiles of 128 rows of part 0 and the same of part 1, each with its own columns
+    int tiles = 0, ext = 0;
+    uint8_t* img = nullptr;
+};
+cudaError_t launch_lr_image(const LrImage& a, int num_sms, cudaStream_t s);
 
 int lr_max_tiles(int M, int slots);
 int lr_shrink_splits(int tiles, int zs, int D, int num_sms);
