@@ -25,8 +25,6 @@ struct qmlp_lora_s {
     int* perm = nullptr;
     int4* tiles = nullptr;
     int* n_tiles = nullptr;
-    float* part = nullptr;
-    int* cnt = nullptr;
     Owner mem;
 };
 
@@ -41,8 +39,6 @@ struct qmlp_train_s {
     __nv_bfloat16* dgu_lo = nullptr; // [kTwoWordM][2I]: what their rounding leaves
     __nv_bfloat16* dv = nullptr;     // kLrWords planes of [max_M][2 Rp]
     __nv_bfloat16* dvd = nullptr;    // likewise [max_M][Rp]
-    float* part = nullptr;
-    int* cnt = nullptr;
     // From kPairMinM tokens on the adapter's terms are further contraction
     // steps of the GEMMs: T words of v beside T of the adapter (see LrImage).
     // NVFP4's one factor a projection goes into v (T = 2); FP8's per-channel
@@ -160,8 +156,6 @@ cudaError_t lora_shrink(const qmlp_lora_s* l, bool down, const void* z, int M, c
     a.v = l->vw;
     a.v_word = (size_t)l->h->max_M * 2 * l->Rp;
     a.ldv = (down ? 1 : 2) * l->Rp;
-    a.part = l->part;
-    a.cnt = l->cnt;
     return launch_lr_shrink(a, a.ldv, false, lr_max_tiles(M, l->slots), 1, l->h->num_sms, s);
 }
 cudaError_t lora_expand(const qmlp_lora_s* l, bool down, int M, cudaStream_t s) {
@@ -292,8 +286,6 @@ qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_ra
     get(&l->perm, M, false);
     get(&l->tiles, tiles, false);
     get(&l->n_tiles, 1, true);
-    get(&l->part, lr_part_elems(h->num_sms), false);
-    get(&l->cnt, tiles * 2, true);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) {
         cudaStreamSynchronize(s);
@@ -433,8 +425,6 @@ LrShrink shrink_all(const qmlp_train_s* t, const void* z, int M, int D, const Wo
     a.words = w.T;
     a.again = w.ext && w.T == 3;
     a.pad = w.ld - w.nc * w.T;
-    a.part = t->l->part;
-    a.cnt = t->l->cnt;
     return a;
 }
 // The adapter's terms into l->y: v W^T, W [N][rc] or, trans, [rc][N].
@@ -707,8 +697,6 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     q.M = M;
     q.r = ad->rank;
     q.Rp = R;
-    q.part = t->part;
-    q.cnt = t->cnt;
     auto v_of = [&](LrTokGrad& c, const Words& w) {
         c.v = w.p;
         c.ldv = w.ld;
@@ -802,10 +790,6 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
     const size_t tg = std::max(I / 128, K / 256), td = std::max(K / 256, (I + 255) / 256);
     get(&t->img_gu, tg * (size_t)(word_ld(2 * (int)R, 3) / 64) * 32768);
     get(&t->img_d, td * (size_t)(word_ld((int)R, 3) / 64) * 32768);
-    get(&t->part, lr_grad_part_elems(h->num_sms));
-    const size_t cnt = 2 * (size_t)lr_grad_tiles((int)std::max(I, K));
-    get(&t->cnt, cnt);
-    if (e == cudaSuccess) e = cudaMemsetAsync(t->cnt, 0, cnt * sizeof(int), s);
     if (h->fmt == kFP8) {
         get(&t->eff, 2 * I);
         get(&t->row, 2 * I);

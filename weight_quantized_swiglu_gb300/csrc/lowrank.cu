@@ -98,25 +98,33 @@ QMLP_DEV bool tile_of(const LrTokens& t, int i, int& slot, int& pos0, int& n) {
     return true;
 }
 
-// True in every thread of the last of `n` CTAs that call it for one counter
-// (whose writes all of them then see); the counter is left at zero.
-QMLP_DEV bool last_arrival(int* cnt, int n) {
-    __shared__ int last;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        last = atomicAdd(cnt, 1) == n - 1;
-        if (last) *cnt = 0;
+// The CTAs of a cluster (along y) hold partial sums of one tile in their shared
+// memory; each adds a share of it over all of them, in rank order.
+QMLP_DEV void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+QMLP_DEV float4 sum_cluster(uint32_t addr, int n) {
+    float4 s = make_float4(0, 0, 0, 0);
+    for (int r = 0; r < n; ++r) {
+        uint32_t ra;
+        float4 v;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(r));
+        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(ra)
+                     : "memory");
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
     }
-    __syncthreads();
-    if (last) __threadfence();
-    return last != 0;
+    return s;
 }
 
 // ---------------------------------------------------------------------------
 // v = c z W^T of a tile, NC columns. W: [NC][D], or with TRANS [D][NC]. The
-// contraction is split over gridDim.y CTAs; the last one adds the splits'
-// partials in order.
+// contraction is split over the CTAs of a cluster (gridDim.y), which add their
+// partials through distributed shared memory.
 // ---------------------------------------------------------------------------
 template <int NC, bool TRANS, bool TWO>
 struct ShrinkSmem {
@@ -224,68 +232,47 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
     }
 
     // fragment (j, e): row 16 warp + g + 8 (e >> 1), column 8 j + 2 t + (e & 1)
-    const int g = lane >> 2, t = lane & 3;
-    const float c = a.scale ? a.scale[slot] : 1.0f;
-    auto emit = [&](int row, int col, float v0, float v1) {
-        __nv_bfloat16 w0[kLrWords], w1[kLrWords];
-        const float f = c * (z * NC + col < a.half ? a.mul0 : a.mul1);
-        split_bf16(v0 * f, w0);
-        split_bf16(v1 * f, w1);
-        if (a.again) w0[2] = w0[0], w1[2] = w1[0];
-        __nv_bfloat16* o = a.v + (size_t)(pos0 + row) * a.ldv + z * NC + col;
-#pragma unroll
-        for (int i = 0; i < kLrWords; ++i)
-            if (i < a.words)
-                *reinterpret_cast<__nv_bfloat162*>(o + i * a.v_word) = __halves2bfloat162(w0[i], w1[i]);
-        // the columns past the words of a row that a GEMM reads whole
-        for (int p = col + z * NC; p < a.pad; p += NC * gridDim.z)
-            *reinterpret_cast<uint32_t*>(a.v + (size_t)(pos0 + row) * a.ldv + a.ldv - a.pad + p) = 0u;
-    };
-    if (gridDim.y == 1) {
-#pragma unroll
-        for (int j = 0; j < NC / 8; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = warp * 16 + g + 8 * h;
-                if (row < n) emit(row, j * 8 + 2 * t, acc[j][2 * h], acc[j][2 * h + 1]);
-            }
-        return;
-    }
-    const size_t tile = (size_t)blockIdx.x + (size_t)gridDim.x * z;
-    float* part = a.part + (tile * gridDim.y + blockIdx.y) * (kT * NC);
+    const int g = lane >> 2, t = lane & 3, ns = gridDim.y;
+    constexpr int kPitch = NC + 4;  // floats of a row of the partial tile
+    static_assert(kT * kPitch * 4 <= S::Bytes, "the tile takes the stages' place");
+    __syncthreads();
+    float* tile = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int j = 0; j < NC / 8; ++j)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = warp * 16 + g + 8 * h;
-            if (row < n)
-                *reinterpret_cast<float2*>(part + row * NC + j * 8 + 2 * t) = make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2*>(tile + (warp * 16 + g + 8 * h) * kPitch + j * 8 + 2 * t) =
+                make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
+    if (ns > 1) cluster_sync();
+    else __syncthreads();
+    const float c = a.scale ? a.scale[slot] : 1.0f;
+    // this CTA's share of the rows, four columns a thread and round
+    const int rows = kT / ns, r0 = blockIdx.y * rows;
+    for (int i = tid; i < rows * (NC / 4); i += kThr) {
+        const int row = r0 + i / (NC / 4), col = (i % (NC / 4)) * 4;
+        if (row >= n) break;
+        const uint32_t at = base + (row * kPitch + col) * 4;
+        const float4 s = ns > 1 ? sum_cluster(at, ns) : *reinterpret_cast<const float4*>(tile + row * kPitch + col);
+        const float f = c * (z * NC + col < a.half ? a.mul0 : a.mul1);
+        const float val[4] = {s.x * f, s.y * f, s.z * f, s.w * f};
+        __nv_bfloat16 w[4][kLrWords];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            split_bf16(val[e], w[e]);
+            if (a.again) w[e][2] = w[e][0];
         }
-    if (!last_arrival(a.cnt + tile, gridDim.y)) return;
-    // every thread a few quads, the loads of a split in flight together (rows
-    // past n hold what an earlier launch left; they are not emitted)
-    const float4* all = reinterpret_cast<const float4*>(a.part + tile * gridDim.y * (kT * NC));
-    constexpr int kQ = kT * NC / 4, kPer = kQ / kThr;
-    float4 sum[kPer];
+        __nv_bfloat16* o = a.v + (size_t)(pos0 + row) * a.ldv + z * NC + col;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum[i] = make_float4(0, 0, 0, 0);
-#pragma unroll 2
-    for (unsigned s = 0; s < gridDim.y; ++s)
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const float4 p = __ldcg(all + (size_t)s * kQ + tid + i * kThr);
-            sum[i].x += p.x;
-            sum[i].y += p.y;
-            sum[i].z += p.z;
-            sum[i].w += p.w;
-        }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int at = (tid + i * kThr) * 4, row = at / NC, col = at % NC;
-        if (row >= n) continue;
-        emit(row, col, sum[i].x, sum[i].y);
-        emit(row, col + 2, sum[i].z, sum[i].w);
+        for (int k = 0; k < kLrWords; ++k)
+            if (k < a.words) {
+                const __nv_bfloat162 p[2] = {__halves2bfloat162(w[0][k], w[1][k]), __halves2bfloat162(w[2][k], w[3][k])};
+                *reinterpret_cast<uint2*>(o + k * a.v_word) = *reinterpret_cast<const uint2*>(p);
+            }
+        // the columns past the words of a row that a GEMM reads whole
+        for (int p = col + z * NC; p < a.pad; p += NC * gridDim.z)
+            *reinterpret_cast<uint2*>(a.v + (size_t)(pos0 + row) * a.ldv + a.ldv - a.pad + p) = make_uint2(0, 0);
     }
+    if (ns > 1) cluster_sync();  // no CTA leaves while another reads its tile
 }
 
 // ---------------------------------------------------------------------------
@@ -403,9 +390,8 @@ __global__ void __launch_bounds__(kThr) expand_kernel(const LrExpand a) {
 }
 
 // ---------------------------------------------------------------------------
-// z^T v over the tokens (the words of z in turn): a CTA takes 128 columns of z (32 a warp) and NC of v;
-// the tokens are split over gridDim.y CTAs, whose partials the last one adds in
-// order. v in two words (2^-17): the gradients are bf16.
+// z^T v over the tokens (the words of z in turn): a CTA takes 128 columns of z
+// (32 a warp) and NC of v; the tokens are split over the CTAs of a cluster. v in two words (2^-17): the gradients are bf16.
 // ---------------------------------------------------------------------------
 constexpr int kGD = 128;
 template <int NC>
@@ -490,68 +476,47 @@ __global__ void __launch_bounds__(kThr) tokgrad_kernel(const LrTokGrad a) {
                 }
         }
     }
-    auto emit = [&](int row, int col, float val) {  // row: column of z in the tile
-        const int d = d0 + row;
-        if (d >= a.D) return;
-        if (a.rows_d) {
-            if (col >= a.r || !a.out[z]) return;
-            a.out[z][(size_t)d * a.r + col] = __float2bfloat16_rn(a.div[z] ? val / a.div[z][d] : val * a.mul[z]);
-        } else {
-            const int part = col / a.Rp, j = col % a.Rp;
-            if (j < a.r && a.out[part]) a.out[part][(size_t)j * a.D + d] = __float2bfloat16_rn(val * a.mul[part]);
-        }
-    };
-    const int g = lane >> 2, t = lane & 3;
-    if (gridDim.y == 1) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < NC / 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    emit(warp * 32 + h * 16 + g + 8 * (e >> 1), j * 8 + 2 * t + (e & 1), acc[h][j][e]);
-        return;
-    }
-    // partials as [column of v][column of z]: the last CTA reads along z
-    const size_t tile = (size_t)blockIdx.x + (size_t)gridDim.x * z;
-    float* part = a.part + (tile * gridDim.y + blockIdx.y) * (kGD * NC);
+    const int g = lane >> 2, t = lane & 3, ns = gridDim.y;
+    constexpr int kPitch = NC + 4;
+    static_assert(kGD * kPitch * 4 <= S::Bytes, "the tile takes the stages' place");
+    __syncthreads();
+    float* tile = reinterpret_cast<float*>(smem);  // [column of z][column of v]
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < NC / 8; ++j)
 #pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float2*>(tile + (warp * 32 + h * 16 + g + 8 * e) * kPitch + j * 8 + 2 * t) =
+                    make_float2(acc[h][j][2 * e], acc[h][j][2 * e + 1]);
+    if (ns > 1) cluster_sync();
+    else __syncthreads();
+    const int rows = kGD / ns, r0 = blockIdx.y * rows;
+    for (int i = tid; i < rows * (NC / 4); i += kThr) {
+        // B's gradient lies along v's columns, A's along z's
+        const int row = r0 + (a.rows_d ? i / (NC / 4) : i % rows);
+        const int col = (a.rows_d ? i % (NC / 4) : i / rows) * 4;
+        const int d = d0 + row;
+        if (d >= a.D) continue;
+        const uint32_t at = base + (row * kPitch + col) * 4;
+        const float4 s4 = ns > 1 ? sum_cluster(at, ns) : *reinterpret_cast<const float4*>(tile + row * kPitch + col);
+        const float s[4] = {s4.x, s4.y, s4.z, s4.w};
+        if (a.rows_d) {
+            if (!a.out[z]) continue;
+            const float f = a.div[z] ? a.div[z][d] : 1.0f;
+#pragma unroll
             for (int e = 0; e < 4; ++e)
-                part[(j * 8 + 2 * t + (e & 1)) * kGD + warp * 32 + h * 16 + g + 8 * (e >> 1)] = acc[h][j][e];
-    if (!last_arrival(a.cnt + tile, gridDim.y)) return;
-    const float4* all = reinterpret_cast<const float4*>(a.part + tile * gridDim.y * (kGD * NC));
-    constexpr int kQ = kGD * NC / 4, kPer = 8;  // quads of a thread and round
-#pragma unroll 1
-    for (int b = 0; b < kQ; b += kPer * kThr) {
-        float4 sum[kPer];
+                if (col + e < a.r)
+                    a.out[z][(size_t)d * a.r + col + e] = __float2bfloat16_rn(a.div[z] ? s[e] / f : s[e] * a.mul[z]);
+        } else {
+            const int part = col / a.Rp, j = col % a.Rp;
+            if (!a.out[part]) continue;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) sum[i] = make_float4(0, 0, 0, 0);
-#pragma unroll 2
-        for (unsigned s = 0; s < gridDim.y; ++s)
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int at = b + tid + i * kThr;
-                if (kQ % (kPer * kThr) && at >= kQ) continue;
-                const float4 p = __ldcg(all + (size_t)s * kQ + at);
-                sum[i].x += p.x;
-                sum[i].y += p.y;
-                sum[i].z += p.z;
-                sum[i].w += p.w;
-            }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int at = (b + tid + i * kThr) * 4, row = at % kGD, col = at / kGD;
-            if (col >= NC) continue;
-            emit(row, col, sum[i].x);
-            emit(row + 1, col, sum[i].y);
-            emit(row + 2, col, sum[i].z);
-            emit(row + 3, col, sum[i].w);
+            for (int e = 0; e < 4; ++e)
+                if (j + e < a.r) a.out[part][(size_t)(j + e) * a.D + d] = __float2bfloat16_rn(s[e] * a.mul[part]);
         }
     }
+    if (ns > 1) cluster_sync();
 }
 
 // ---------------------------------------------------------------------------
@@ -761,18 +726,23 @@ __global__ void __launch_bounds__(256) image_kernel(const LrImage a) {
     }
 }
 
+// cluster: CTAs of a cluster along y.
 template <typename K, typename A>
-cudaError_t launch_pdl(K kern, dim3 grid, int threads, int smem, const A& a, cudaStream_t s) {
+cudaError_t launch_pdl(K kern, dim3 grid, int threads, int smem, const A& a, cudaStream_t s, int cluster = 1) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = 1;
+    at[1].val.clusterDim.y = (unsigned)cluster;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
@@ -786,7 +756,7 @@ cudaError_t shrink_t(const LrShrink& a, int tiles, int splits, int zs, cudaStrea
         if (e != cudaSuccess) return e;
         attr = true;
     }
-    return launch_pdl(shrink_kernel<NC, TRANS, TWO>, dim3(tiles, splits, zs), kThr, S::Bytes, a, s);
+    return launch_pdl(shrink_kernel<NC, TRANS, TWO>, dim3(tiles, splits, zs), kThr, S::Bytes, a, s, splits);
 }
 template <bool TRANS, bool TWO>
 cudaError_t shrink_n(const LrShrink& a, int nc, int tiles, int splits, int zs, cudaStream_t s) {
@@ -815,18 +785,16 @@ cudaError_t expand_t(const LrExpand& a, int tiles, int zs, cudaStream_t s) {
 
 int lr_max_tiles(int M, int slots) { return M / kT + std::min(slots + 1, M) + 1; }
 
-// Splits of the contraction: enough CTAs for three on an SM, steps left for
-// the pipeline to run, and no more partials than the buffer holds.
-int lr_shrink_splits(int tiles, int zs, int D, int num_sms) {
-    const int steps = (D + kStep - 1) / kStep;
-    return std::max(1, std::min({3 * num_sms / std::max(1, tiles * zs), steps / 4, kLrMaxSplits}));
+// CTAs of a cluster that share a contraction of `steps`: a power of two up to
+// 8, while the grid stays under three CTAs an SM and each has two steps.
+static int lr_splits(int tiles, int steps, int num_sms) {
+    int n = 1;
+    while (n < 8 && 2 * n * tiles <= 3 * num_sms && steps >= 4 * n) n *= 2;
+    return n;
 }
-// Floats of the partials: where the contraction is split at all, tiles * splits
-// * zs <= 3 num_sms, of 64 x 128 floats at most.
-size_t lr_part_elems(int num_sms) { return (size_t)3 * num_sms * kT * 128; }
 
 cudaError_t launch_lr_shrink(const LrShrink& a, int nc, bool trans, int tiles, int zs, int num_sms, cudaStream_t s) {
-    const int splits = lr_shrink_splits(tiles, zs, a.D, num_sms);
+    const int splits = lr_splits(tiles * zs, (a.D + kStep - 1) / kStep, num_sms);
     if (!trans) return shrink_n<false, false>(a, nc, tiles, splits, zs, s);
     return a.w_lo ? shrink_n<true, true>(a, nc, tiles, splits, zs, s) : shrink_n<true, false>(a, nc, tiles, splits, zs, s);
 }
@@ -842,9 +810,6 @@ cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, i
     return cudaErrorInvalidValue;
 }
 
-int lr_grad_tiles(int D) { return (D + kGD - 1) / kGD; }
-size_t lr_grad_part_elems(int num_sms) { return (size_t)2 * num_sms * kGD * 128; }
-
 template <int NC>
 static cudaError_t tokgrad_t(const LrTokGrad& a, dim3 grid, cudaStream_t s) {
     static bool attr = false;
@@ -854,12 +819,10 @@ static cudaError_t tokgrad_t(const LrTokGrad& a, dim3 grid, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         attr = true;
     }
-    return launch_pdl(tokgrad_kernel<NC>, grid, kThr, GradSmem<NC>::Bytes, a, s);
+    return launch_pdl(tokgrad_kernel<NC>, grid, kThr, GradSmem<NC>::Bytes, a, s, (int)grid.y);
 }
 cudaError_t launch_lr_tokgrad(const LrTokGrad& a, int nc, int zs, int num_sms, cudaStream_t s) {
-    const int tiles = lr_grad_tiles(a.D), steps = (a.M + 63) / 64;
-    // two CTAs an SM, four steps a CTA at least; tiles * zs * splits <= 2 num_sms where there are splits
-    const int splits = std::max(1, std::min(2 * num_sms / (tiles * zs), steps / 4));
+    const int tiles = (a.D + kGD - 1) / kGD, splits = lr_splits(tiles * zs, (a.M + 63) / 64, num_sms);
     const dim3 grid(tiles, splits, zs);
     switch (nc) {
         case 16: return tokgrad_t<16>(a, grid, s);

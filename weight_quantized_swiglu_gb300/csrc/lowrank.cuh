@@ -11,7 +11,6 @@ constexpr int kLrTile = 64;       // tokens of a tile
 constexpr int kLrMaxRank = 64;
 constexpr int kLrWords = 3;       // bf16 words of a value of v
 constexpr int kLrMaxSlots = 1024;
-constexpr int kLrMaxSplits = 32;
 constexpr int kLrFew = 16;        // tokens the kernels without a plan take
 
 // Which tokens a tile holds: tiles null: one adapter, 64 consecutive tokens.
@@ -40,8 +39,6 @@ struct LrShrink {
     int pad = 0;                   // columns at a row's end to fill with zeros
     float mul0 = 1.0f, mul1 = 1.0f;  // factors of the columns before and from `half` on
     int half = 1 << 30;
-    float* part = nullptr;
-    int* cnt = nullptr;            // a zeroed counter a tile and part
 };
 
 struct LrExpand {
@@ -95,8 +92,6 @@ struct LrTokGrad {
     __nv_bfloat16* out[2] = {nullptr, nullptr};
     const float* div[2] = {nullptr, nullptr};  // rows_d: the row's divisor; else mul
     float mul[2] = {1.0f, 1.0f};
-    float* part = nullptr;
-    int* cnt = nullptr;
 };
 
 struct LrSwiGLU {
@@ -141,10 +136,6 @@ struct LrImage {
 cudaError_t launch_lr_image(const LrImage& a, int num_sms, cudaStream_t s);
 
 int lr_max_tiles(int M, int slots);
-int lr_shrink_splits(int tiles, int zs, int D, int num_sms);
-size_t lr_part_elems(int num_sms);
-size_t lr_grad_part_elems(int num_sms);
-int lr_grad_tiles(int D);
 cudaError_t launch_lr_tokgrad(const LrTokGrad& a, int nc, int zs, int num_sms, cudaStream_t s);
 cudaError_t launch_lr_shrink(const LrShrink& a, int nc, bool trans, int tiles, int zs, int num_sms, cudaStream_t s);
 cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, int zs, cudaStream_t s);
