@@ -21,7 +21,8 @@ struct qmlp_lora_s {
     float* v = nullptr;             // few tokens: [kLrFew][2 Rp]
     __nv_bfloat16* vw = nullptr;    // [kLrWords][max_M][2 Rp], by position
     float* y = nullptr;             // [max_M][max(2I, K)]: the adapters' terms
-    float* raw = nullptr;           // [kLrFew][2I + K]: projections without their factors
+    float* raw = nullptr;           // [kMaxGemvM][2I + K]: projections without their factors
+    float* vd = nullptr;            // [G][kMaxGemvM][Rp]: the decode CTAs' shares of A_d act
     int* perm = nullptr;
     int4* tiles = nullptr;
     int* n_tiles = nullptr;
@@ -183,8 +184,10 @@ LrFew few_of(const qmlp_lora_s* l, bool down, const int32_t* ids) {
     a.v = l->v;
     return a;
 }
-cudaError_t lora_shrink_few(const qmlp_lora_s* l, bool down, const void* z, const int32_t* ids, int M, cudaStream_t s) {
+cudaError_t lora_shrink_few(const qmlp_lora_s* l, bool down, const void* z, const int32_t* ids, int M, cudaStream_t s,
+                            bool late = false) {
     LrFew a = few_of(l, down, ids);
+    a.late = late;
     a.x = static_cast<const __nv_bfloat16*>(z);
     a.D = down ? l->h->I : l->h->K;
     a.w = down ? l->a_d : l->a_gu;
@@ -207,22 +210,33 @@ cudaError_t lora_expand_few(const qmlp_lora_s* l, bool down, const int32_t* ids,
     return launch_lr_expand_few(a, M, down ? 1 : 2, s);
 }
 
-// One block of at most kLrFew tokens on the GEMV kernels.
+// One block of at most kMaxGemvM tokens on the GEMV kernels.
 qmlp_status lora_block(qmlp_lora_s* l, const void* x, const int32_t* ids, int M, void* out, cudaStream_t s) {
     qmlp_t* h = l->h;
-    if (lora_shrink_few(l, false, x, ids, M, s) != cudaSuccess ||
-        lora_expand_few(l, false, ids, M, nullptr, nullptr, s) != cudaSuccess)
+    const bool split = h->sp.G && M <= split_max_m(h) && split_lora_fits(h->fmt, M, h->K, l->Rp, h->sp);
+    if (lora_shrink_few(l, false, x, ids, M, s, split && split_in_kernel(h->fmt, M)) != cudaSuccess)
         return QMLP_ERR_CUDA;
-    float* raw_d = l->raw;
-    if (h->sp.G && M <= split_max_m(h) && split_fits(h->fmt, M, h->K, h->sp)) {
+    if (split) {
         SplitLaunch S = split_launch(h, x, M);
-        S.add = l->y;
-        S.out_f32 = raw_d;
-        if (launch_split(S, h->sp, s) != cudaSuccess) return QMLP_ERR_CUDA;
-    } else {
+        S.out = out;
+        S.lora.ids = ids;
+        S.lora.rank = l->rank;
+        S.lora.scale = l->scale;
+        S.lora.slots = l->slots;
+        S.lora.Rp = l->Rp;
+        S.lora.v = l->v;
+        S.lora.b_gu = l->b_gu;
+        S.lora.a_d = l->a_d;
+        S.lora.b_d = l->b_d;
+        S.lora.vd = l->vd;
+        return launch_split(S, h->sp, s) == cudaSuccess ? QMLP_OK : QMLP_ERR_CUDA;
+    }
+    if (lora_expand_few(l, false, ids, M, nullptr, nullptr, s) != cudaSuccess) return QMLP_ERR_CUDA;
+    float* raw_d = l->raw;
+    {
         // the two projections on their own, then the activation
-        float* rg = l->raw + (size_t)kLrFew * h->K;
-        float* ru = rg + (size_t)kLrFew * h->I;
+        float* rg = l->raw + (size_t)kMaxGemvM * h->K;
+        float* ru = rg + (size_t)kMaxGemvM * h->I;
         qmlp_status st = qmlp_debug_project(h, 0, QMLP_PATH_GEMV, x, M, rg, s);
         if (st == QMLP_OK) st = qmlp_debug_project(h, 1, QMLP_PATH_GEMV, x, M, ru, s);
         if (st != QMLP_OK) return st;
@@ -282,7 +296,8 @@ qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_ra
     get(&l->v, (size_t)kLrFew * 2 * R, false);
     get(&l->vw, kLrWords * M * 2 * R, false);
     get(&l->y, M * std::max(2 * I, K), false);
-    get(&l->raw, (size_t)kLrFew * (2 * I + K), false);
+    get(&l->raw, (size_t)kMaxGemvM * (2 * I + K), false);
+    get(&l->vd, (size_t)std::max(1, h->sp.G) * kMaxGemvM * R, false);
     get(&l->perm, M, false);
     get(&l->tiles, tiles, false);
     get(&l->n_tiles, 1, true);
@@ -326,7 +341,7 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
     if (fault("launch")) return QMLP_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (!(h->has_gemm && M >= gemm_min_m(h))) {
-        const int block = h->sp.G ? split_max_m(h) : kLrFew;
+        const int block = h->sp.G ? split_max_m(h) : kMaxGemvM;
         for (int m0 = 0; m0 < M; m0 += block) {
             const qmlp_status st =
                 lora_block(l, static_cast<const uint8_t*>(x) + (size_t)m0 * h->K * 2, ids + m0, std::min(block, M - m0),

@@ -238,6 +238,12 @@ QMLP_DEV uint32_t pack_bf16x2(float lo, float hi) {
 
 // The tile epilogue (no split): accumulator columns of TMEM base `tbase`
 // (this thread's lane = token row m) -> SwiGLU act, plain output or raw fp32.
+// 16 packed bf16 values, 16-byte aligned.
+QMLP_DEV void store16(__nv_bfloat16* dst, const uint32_t (&v)[8]) {
+    reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
 // EXT: the instances of low-rank adapters, which add their fp32 terms.
 template <int FMT, bool EXT>
 QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg, int nt, int first, int step) {
@@ -249,42 +255,63 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
             float g[32], u[32];
             tmem_ld32(tbase + c0, g);
             tmem_ld32(tbase + BN / 2 + c0, u);
-            if (live) {
+            if (EXT && live) {
+                // 16 columns at a time, their loads before anything is stored
+                const int col = nt * (BN / 2) + c0;
+#pragma unroll
+                for (int h = 0; h < 32; h += 16) {
+                    float4 dg[4], du[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        dg[j] = du[j] = make_float4(0, 0, 0, 0);
+                        if (a.add) {
+                            const float* ad = a.add + (size_t)m * a.ldadd + col + h + 4 * j;
+                            dg[j] = *reinterpret_cast<const float4*>(ad);
+                            du[j] = *reinterpret_cast<const float4*>(ad + a.ldo);
+                        }
+                    }
+                    uint32_t pk[8], lo[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 fg = factor4<FMT>(a.cs0, a.inv0, col + h + 4 * j);
+                        const float4 fu = factor4<FMT>(a.cs1, a.inv1, col + h + 4 * j);
+                        float r4[4], g4[4], u4[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            g4[e] = scalbnf(g[h + 4 * j + e], -sg) * f4_at(fg, e) + f4_at(dg[j], e);
+                            u4[e] = scalbnf(u[h + 4 * j + e], -sg) * f4_at(fu, e) + f4_at(du[j], e);
+                            r4[e] = silu_f32(g4[e]) * u4[e];
+                        }
+                        if (a.gu_g) {
+                            const size_t at = gu_at(m, col + h + 4 * j, a.ldo);
+                            a.gu_g[at] = make_float4(g4[0], g4[1], g4[2], g4[3]);
+                            a.gu_u[at] = make_float4(u4[0], u4[1], u4[2], u4[3]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            pk[2 * j + e] = pack_bf16x2(r4[2 * e], r4[2 * e + 1]);
+                            lo[2 * j + e] = rest_bf16x2(r4[2 * e], r4[2 * e + 1], pk[2 * j + e]);
+                        }
+                    }
+                    const size_t at = (size_t)m * a.ldo + col + h;
+                    store16(out + at, pk);
+                    if (a.out_lo) store16(reinterpret_cast<__nv_bfloat16*>(a.out_lo) + at, lo);
+                }
+            } else if (live) {
                 uint32_t pk[16];
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 fg = factor4<FMT>(a.cs0, a.inv0, nt * (BN / 2) + c0 + j);
                     const float4 fu = factor4<FMT>(a.cs1, a.inv1, nt * (BN / 2) + c0 + j);
-                    float4 dg = make_float4(0, 0, 0, 0), du = dg;
-                    if (EXT && a.add) {
-                        const float* ad = a.add + (size_t)m * a.ldadd + nt * (BN / 2) + c0 + j;
-                        dg = *reinterpret_cast<const float4*>(ad);
-                        du = *reinterpret_cast<const float4*>(ad + a.ldo);
-                    }
-                    float r4[4], g4[4], u4[4];
+                    float r4[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float gv = scalbnf(g[j + e], -sg) * f4_at(fg, e);
-                        float uv = scalbnf(u[j + e], -sg) * f4_at(fu, e);
-                        if (EXT) {
-                            gv += f4_at(dg, e);
-                            uv += f4_at(du, e);
-                        }
+                        const float gv = scalbnf(g[j + e], -sg) * f4_at(fg, e);
+                        const float uv = scalbnf(u[j + e], -sg) * f4_at(fu, e);
                         r4[e] = silu_f32(gv) * uv;
-                        g4[e] = gv;
-                        u4[e] = uv;
-                    }
-                    if (EXT && a.gu_g) {
-                        const size_t at = gu_at(m, nt * (BN / 2) + c0 + j, a.ldo);
-                        a.gu_g[at] = make_float4(g4[0], g4[1], g4[2], g4[3]);
-                        a.gu_u[at] = make_float4(u4[0], u4[1], u4[2], u4[3]);
                     }
                     pk[j / 2] = pack_bf16x2(r4[0], r4[1]);
                     pk[j / 2 + 1] = pack_bf16x2(r4[2], r4[3]);
-                    if (EXT && a.out_lo)
-                        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out_lo) + (size_t)m * a.ldo +
-                                                  nt * (BN / 2) + c0 + j) =
-                            make_uint2(rest_bf16x2(r4[0], r4[1], pk[j / 2]), rest_bf16x2(r4[2], r4[3], pk[j / 2 + 1]));
                 }
                 uint4* dst = reinterpret_cast<uint4*>(out + (size_t)m * a.ldo + nt * (BN / 2) + c0);
                 if (QMLP_INB(nt * (BN / 2) + c0 + 31, a.ldo, 12) && QMLP_INB(m, a.M, 12))
@@ -305,41 +332,49 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
             tmem_ld32(tbase + c0, y);
             const int col = nt * BN + c0;
             if (live && col < a.ncols) {
-                uint32_t pg[16], pu[16];
+                // 16 columns at a time, their loads before anything is stored
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const size_t at = gu_at(m, col + j, a.ncols);
-                    const float4 g = __ldcs(a.gu_g + at), u = __ldcs(a.gu_u + at);
-                    float4 ad = make_float4(0, 0, 0, 0);
-                    if (a.add) ad = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + col + j);
-                    const float4 fg = factor4<kFP8>(a.gc0, a.gf0, col + j, a.gc0 == nullptr),
-                                 fu = factor4<kFP8>(a.gc1, a.gf1, col + j, a.gc1 == nullptr);
-                    float dg[4], du[4];
+                for (int h = 0; h < 32; h += 16) {
+                    float4 g4[4], u4[4], ad[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float d = scalbnf(y[j + e], -sg) * a.inv0 + f4_at(ad, e), gv = f4_at(g, e);
-                        const float sg1 = 1.0f / (1.0f + expf(-gv));
-                        du[e] = d * (gv * sg1) * f4_at(fu, e);
-                        dg[e] = d * f4_at(u, e) * (sg1 * (1.0f + gv * (1.0f - sg1))) * f4_at(fg, e);
+                    for (int j = 0; j < 4; ++j) {
+                        const size_t at = gu_at(m, col + h + 4 * j, a.ncols);
+                        g4[j] = __ldcs(a.gu_g + at);
+                        u4[j] = __ldcs(a.gu_u + at);
+                        ad[j] = a.add ? *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + col + h + 4 * j)
+                                      : make_float4(0, 0, 0, 0);
                     }
-                    pg[j / 2] = pack_bf16x2(dg[0], dg[1]);
-                    pg[j / 2 + 1] = pack_bf16x2(dg[2], dg[3]);
-                    pu[j / 2] = pack_bf16x2(du[0], du[1]);
-                    pu[j / 2 + 1] = pack_bf16x2(du[2], du[3]);
+                    uint32_t pg[8], pu[8], lg[8], lu[8];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int c = col + h + 4 * j;
+                        const float4 fg = factor4<kFP8>(a.gc0, a.gf0, c, a.gc0 == nullptr),
+                                     fu = factor4<kFP8>(a.gc1, a.gf1, c, a.gc1 == nullptr);
+                        float dg[4], du[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float d = scalbnf(y[h + 4 * j + e], -sg) * a.inv0 + f4_at(ad[j], e),
+                                        gv = f4_at(g4[j], e);
+                            const float sg1 = 1.0f / (1.0f + expf(-gv));
+                            du[e] = d * (gv * sg1) * f4_at(fu, e);
+                            dg[e] = d * f4_at(u4[j], e) * (sg1 * (1.0f + gv * (1.0f - sg1))) * f4_at(fg, e);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            pg[2 * j + e] = pack_bf16x2(dg[2 * e], dg[2 * e + 1]);
+                            pu[2 * j + e] = pack_bf16x2(du[2 * e], du[2 * e + 1]);
+                            lg[2 * j + e] = rest_bf16x2(dg[2 * e], dg[2 * e + 1], pg[2 * j + e]);
+                            lu[2 * j + e] = rest_bf16x2(du[2 * e], du[2 * e + 1], pu[2 * j + e]);
+                        }
+                    }
+                    const size_t at = (size_t)m * 2 * a.ncols + col + h;
+                    store16(out + at, pg);
+                    store16(out + at + a.ncols, pu);
                     if (a.out_lo) {
-                        __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(a.out_lo) + (size_t)m * 2 * a.ncols + col + j;
-                        *reinterpret_cast<uint2*>(lo) =
-                            make_uint2(rest_bf16x2(dg[0], dg[1], pg[j / 2]), rest_bf16x2(dg[2], dg[3], pg[j / 2 + 1]));
-                        *reinterpret_cast<uint2*>(lo + a.ncols) =
-                            make_uint2(rest_bf16x2(du[0], du[1], pu[j / 2]), rest_bf16x2(du[2], du[3], pu[j / 2 + 1]));
+                        __nv_bfloat16* lo = reinterpret_cast<__nv_bfloat16*>(a.out_lo) + at;
+                        store16(lo, lg);
+                        store16(lo + a.ncols, lu);
                     }
-                }
-                uint4* dst = reinterpret_cast<uint4*>(out + (size_t)m * 2 * a.ncols + col);
-                uint4* dsu = reinterpret_cast<uint4*>(out + (size_t)m * 2 * a.ncols + a.ncols + col);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    dst[v] = make_uint4(pg[4 * v], pg[4 * v + 1], pg[4 * v + 2], pg[4 * v + 3]);
-                    dsu[v] = make_uint4(pu[4 * v], pu[4 * v + 1], pu[4 * v + 2], pu[4 * v + 3]);
                 }
             }
         }

@@ -37,6 +37,20 @@
 // without a pause (the down weights do not depend on act), one bulk-async
 // copy per projection and step into a shared-memory ring, as in
 // gemv_stream.cu. No float atomics: every sum has a fixed order.
+// LR instances: low-rank adapters, a slot a token. A small launch before this
+// one writes v = c A x of gate and up. With schedule (b) this kernel starts
+// beside it, fills its ring and waits for it as for any kernel; with schedule
+// (a), whose ring a whole call empties without a pause, it starts only once
+// everything before that launch has completed and then runs beside it, with
+// nothing but the adapters' part waiting for v (one NVFP4 token 37.6 us, 41.9
+// with the other order; eight FP8 tokens 79.7 us, 84.7 with this one). Three
+// more warps do the adapters' part while the weights stream:
+// they put B v of the CTA's rows into shared memory (the gate/up epilogue adds
+// it), and, once the act slice is complete, write the CTA's share of A_d act,
+// [Rp] a token; the reduction over the partials adds those shares (in order)
+// and B_d times their sum. (On the consumer warps, whose epilogues then wait
+// for the adapters' rows one after the other: one NVFP4 token 44 us, eight FP8
+// tokens 112 us, against 31 and 67 without adapters.)
 // Every wait is bounded (globaltimer); on expiry the CTA records the error,
 // still arrives at the grid barrier exactly once, waits for its own copies
 // in flight and leaves.
@@ -50,6 +64,8 @@ namespace {
 constexpr int kW = 16;                // consumer warps
 constexpr int kCT = kW * 32;          // consumer threads
 constexpr int kThr = kCT + 32;        // + one producer warp
+constexpr int kLT = 96;               // LR: + three adapter warps (20 in all: five a scheduler keep 96 registers)
+constexpr int thr(bool lr) { return kThr + (lr ? kLT : 0); }
 constexpr int kDepthMax = 16;
 constexpr int kBudget = 220 * 1024;
 constexpr int kBars = 2 * kDepthMax * 8 + 16;  // full, empty, x
@@ -78,7 +94,8 @@ struct Args {
     const __nv_bfloat16* act_in;  // optional [M, I]: phase B consumes these act values (debug)
     float* dbg_g;              // optional [M, I]: gate dot products, fp32, no factor (debug)
     float* dbg_u;              // optional [M, I]: up dot products, likewise
-    const float* add;          // optional [M, 2I]: added to gate (first I) and up after the factor
+    SplitLora lr;              // LR instances
+    int lr_off;                // LR: shared memory of v and B v
     float* part;               // [G][M][K]
     unsigned long long* ticket;
     int* err;
@@ -222,11 +239,183 @@ QMLP_DEV bool combine_smem(float* slots, int slot_floats, int slot, int nc, int*
     return true;
 }
 
+// Token m's slot and its rank in eights; 0: no adapter.
+QMLP_DEV int lr_slot(const SplitLora& lr, int m, int& slot) {
+    slot = __ldg(lr.ids + m);
+    if (slot < 0 || slot >= lr.slots) return 0;
+    return (__ldg(lr.rank + slot) + 7) / 8;
+}
+
+// s + the eight products of bf16 values q and v.
+QMLP_DEV float lr_fma8(const uint4& q, const float* v, float s) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        s = fmaf(__uint_as_float(w[e] << 16), v[2 * e], s);
+        s = fmaf(__uint_as_float(w[e] & 0xFFFF0000u), v[2 * e + 1], s);
+    }
+    return s;
+}
+
+// The adapter warps (tid 0 .. kLT - 1). s_v [M][2 Rp] floats, then 2 M ints,
+// and s_d [M][2][tslice] floats; bars: s_d written, act slice written, the share of A_d act written.
+QMLP_DEV void lr_warps(const SplitLora& lr, int M, int I, int tslice, int tid, float* s_v, float* s_d,
+                       const float* s_act, uint32_t bar0, uint64_t limit, int* err) {
+    const int R = lr.Rp, lane = tid & 31, i0 = blockIdx.x * tslice;
+    // every token's slot and rank once, and A_d's rows on the way to L2
+    int* s_n8 = reinterpret_cast<int*>(s_v + M * 2 * R);
+    int* s_slot = s_n8 + M;
+    if (tid < M) s_n8[tid] = lr_slot(lr, tid, s_slot[tid]);
+    named_bar_sync(2, kLT);
+    for (int p = tid; p < M * R; p += kLT) {
+        const int m = p / R, j = p - m * R;
+        if (j >= 8 * s_n8[m]) continue;
+        const char* a0 = reinterpret_cast<const char*>(lr.a_d + ((size_t)s_slot[m] * R + j) * I + i0);
+        for (int o = 0; o < 2 * tslice; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(a0 + o));
+    }
+    pdl_wait();  // v is written
+    for (int i = tid; i < M * 2 * R; i += kLT) s_v[i] = __ldcg(lr.v + i);
+    named_bar_sync(2, kLT);
+    // B v: an item a (token, gate or up, row)
+    const int items = M * 2 * tslice;
+    constexpr int kU = 8;  // items whose rows are in flight together
+    for (int b = tid; b < items; b += kU * kLT) {
+        float s[kU];
+        const uint4* row[kU];
+        int n8[kU], vo[kU], most = 0;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int i = b + u * kLT;
+            s[u] = 0.0f;
+            n8[u] = 0;
+            row[u] = nullptr;
+            vo[u] = 0;
+            if (i < items) {
+                const int mp = i / tslice, r = i - mp * tslice;
+                n8[u] = s_n8[mp >> 1];
+                row[u] = reinterpret_cast<const uint4*>(
+                    lr.b_gu + (((size_t)(n8[u] ? s_slot[mp >> 1] : 0) * 2 + (mp & 1)) * I + i0 + r) * R);
+                vo[u] = mp * R;
+            }
+            most = max(most, n8[u]);
+        }
+        for (int e = 0; e < most; e += 2) {
+            uint4 q[kU][2];
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    q[u][k] = e + k < n8[u] ? __ldg(row[u] + e + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    if (e + k < n8[u]) s[u] = lr_fma8(q[u][k], s_v + vo[u] + 8 * (e + k), s[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            if (b + u * kLT < items) s_d[b + u * kLT] = s[u];
+    }
+    mbar_arrive(bar0);
+    // the share of A_d act: a warp eight (token, rank) pairs of one token at a time
+    if (!mbar_wait_bounded(bar0 + 8, 0, limit)) {
+        if (lane == 0) atomicExch(err, 26);
+        mbar_arrive(bar0 + 16);
+        return;
+    }
+    for (int p = (tid >> 5) * 8; p < M * R; p += 8 * (kLT / 32)) {
+        const int m = p / R, j = p - m * R;
+        if (j >= 8 * s_n8[m]) continue;  // never read
+        const int slot = s_slot[m];
+        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        const __nv_bfloat16* a0 = lr.a_d + ((size_t)slot * R + j) * I + i0;
+#pragma unroll 2
+        for (int k = lane; k < tslice / 2; k += 32) {
+            const float2 x = *reinterpret_cast<const float2*>(s_act + m * tslice + 2 * k);
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = __ldg(reinterpret_cast<const uint32_t*>(a0 + (size_t)e * I) + k);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                s[e] = fmaf(__uint_as_float(w[e] << 16), x.x, s[e]);
+                s[e] = fmaf(__uint_as_float(w[e] & 0xFFFF0000u), x.y, s[e]);
+            }
+        }
+        // eight sums over the warp: halve the values a lane keeps in each of
+        // three rounds, then two plain rounds; lane 4 e .. 4 e + 3 hold value e
+#pragma unroll
+        for (int r = 0; r < 3; ++r) {
+            const int o = 16 >> r, half = 4 >> r;
+            const bool up = lane & o;
+#pragma unroll
+            for (int e = 0; e < half; ++e) {
+                const float send = up ? s[e] : s[e + half], keep = up ? s[e + half] : s[e];
+                s[e] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+        }
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+        if ((lane & 3) == 0) lr.vd[((size_t)blockIdx.x * M + m) * R + j + (lane >> 2)] = s[0];
+    }
+    mbar_arrive(bar0 + 16);
+}
+// c A_d act of token m into s_vd[Rp] by `nthr` threads (a multiple of Rp, at
+// most 512; tmp holds as many floats): each adds every (nthr / Rp)-th CTA's
+// share, then the first Rp threads add those sums; the caller's barrier `sync`
+// stands between and after.
+template <typename Sync>
+QMLP_DEV void lr_down_sum(const SplitLora& lr, int G, int M, int m, int tid, int nthr, float* tmp, float* s_vd,
+                          const Sync& sync) {
+    int slot;
+    const int n8 = lr_slot(lr, m, slot);
+    const int j = tid % lr.Rp, b0 = tid / lr.Rp, nb = nthr / lr.Rp;
+    float s = 0.0f;
+    if (j < 8 * n8) {
+        const float* p = lr.vd + (size_t)m * lr.Rp + j;
+#pragma unroll 9
+        for (int b = b0; b < G; b += nb) s += __ldcg(p + (size_t)b * M * lr.Rp);
+    }
+    tmp[tid] = s;
+    sync();
+    if (tid < lr.Rp) {
+        float t = 0.0f;
+        for (int b = 0; b < nb; ++b) t += tmp[b * lr.Rp + tid];
+        s_vd[tid] = n8 ? t * __ldg(lr.scale + slot) : 0.0f;
+    }
+    sync();
+}
+// B_d[n] . s_vd
+QMLP_DEV float lr_down_dot(const SplitLora& lr, int K, int m, int n, const float* s_vd) {
+    int slot;
+    const int n8 = lr_slot(lr, m, slot);
+    float s = 0.0f;
+    const uint4* b = reinterpret_cast<const uint4*>(lr.b_d + ((size_t)(n8 ? slot : 0) * K + n) * lr.Rp);
+#pragma unroll 2
+    for (int i = 0; i < n8; ++i) s = lr_fma8(__ldg(b + i), s_vd + 8 * i, s);
+    return s;
+}
+// Its row on the way to L2.
+QMLP_DEV void lr_down_prefetch(const SplitLora& lr, int K, int m, int n) {
+    int slot;
+    if (n < K && lr_slot(lr, m, slot))
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(lr.b_d + ((size_t)slot * K + n) * lr.Rp));
+}
+
+// What the gate/up epilogue needs of the adapters: B v in shared memory, and
+// the barrier that says so. Nothing in the instances without them.
+template <bool LR>
+struct LrEpi {};
+template <>
+struct LrEpi<true> {
+    const float* d;
+    uint32_t bar;
+};
+
 // Phase-A epilogue of local tile lt: act = bf16(SiLU(g)*u) into the CTA's
 // act slice (and optionally the global act).
-template <int FMT, int NT>
+template <int FMT, int NT, bool LR>
 QMLP_DEV void epilogue_a(const Args& a, int M, int lt, const float (&v)[2][NT][4], const int* s_sig,
-                         float* s_act, int* s_actmax) {
+                         float* s_act, int* s_actmax, const LrEpi<LR>& lre) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int tslice = a.T * 16;
 #pragma unroll
@@ -244,9 +433,9 @@ QMLP_DEV void epilogue_a(const Args& a, int M, int lt, const float (&v)[2][NT][4
             const float graw = v[0][n][e] * pw, uraw = v[1][n][e] * pw;
             float gv = graw * s0;
             float uv = uraw * s1;
-            if (a.add) {  // the low-rank adapters' terms
-                gv += a.add[(size_t)m * 2 * a.I + i];
-                uv += a.add[(size_t)m * 2 * a.I + a.I + i];
+            if constexpr (LR) {
+                gv += lre.d[m * 2 * tslice + r];
+                uv += lre.d[(m * 2 + 1) * tslice + r];
             }
             __nv_bfloat16 act = __float2bfloat16_rn(silu_f32(gv) * uv);
             if (a.dbg_g) {
@@ -271,18 +460,21 @@ template <int NT>
 struct AccA {
     float v[2][NT][4];
 };
-template <int FMT, int NT>
+template <int FMT, int NT, bool LR>
 __device__ __noinline__ void finish_tile_a(const Args& a, int M, int lt, bool whole, int warp, AccA<NT> acc,
                                            float* s_pa, int pa_floats, int* s_cnta, const int* s_sig, float* s_act,
-                                           int* s_actmax) {
+                                           int* s_actmax, LrEpi<LR> lre) {
+    // B v is there (a wait that runs out is reported, and the terms are not added right)
+    if constexpr (LR)
+        if (!mbar_wait_bounded(lre.bar, 0, a.limit) && (threadIdx.x & 31) == 0) atomicExch(a.err, 27);
     if (whole) {
-        epilogue_a<FMT, NT>(a, M, lt, acc.v, s_sig, s_act, s_actmax);
+        epilogue_a<FMT, NT, LR>(a, M, lt, acc.v, s_sig, s_act, s_actmax, lre);
         return;
     }
     const int w0 = (lt * a.KcA) / a.LA, w1 = ((lt + 1) * a.KcA - 1) / a.LA;
     if (combine_smem<NT, 2>(s_pa + (size_t)lt * a.SA * pa_floats, pa_floats, warp - w0, w1 - w0 + 1, &s_cnta[lt], M,
                             acc.v))
-        epilogue_a<FMT, NT>(a, M, lt, acc.v, s_sig, s_act, s_actmax);
+        epilogue_a<FMT, NT, LR>(a, M, lt, acc.v, s_sig, s_act, s_actmax, lre);
 }
 
 // Phase-B result of down row tile rt over this CTA's slice -> global partial.
@@ -499,9 +691,10 @@ QMLP_DEV unsigned long long ld_acquire_u64(const unsigned long long* p) {
 // MC: the token count when the instance fixes it (1, 2, 4, 8), else 0 (the
 // count is a.M). A fixed count folds the token loops and the x-fragment
 // addressing of the streaming loop (measured at 4 tokens: 45.6 -> 43.7 us).
-template <int FMT, int NT, int MC, bool SEP>
-__global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_constant__ Args a) {
+template <int FMT, int NT, int MC, bool SEP, bool LR>
+__global__ void __launch_bounds__(thr(LR), 1) gemv_split_kernel(const __grid_constant__ Args a) {
     constexpr bool M1 = MC == 1;
+    constexpr bool kLate = LR && !SEP;  // only the adapter warps wait for the launch before
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_maxbits[16];
     __shared__ int s_sig[16];
@@ -513,6 +706,10 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
     __shared__ float s_wmax[kW];
     __shared__ int s_fail;
     __shared__ int s_pass;
+    __shared__ __align__(8) uint64_t s_lrbar[LR ? 3 : 1];
+    const uint32_t lr_bar = smem_u32(s_lrbar);
+    LrEpi<LR> lre;
+    if constexpr (LR) lre = {reinterpret_cast<const float*>(smem + a.lr_off), lr_bar};
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int M = MC ? MC : a.M;
     Ring r;
@@ -532,6 +729,11 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
             mbar_init(r.empty0 + 8u * i, kW);
         }
         mbar_init(r.xbar, 1);
+        if (LR) {
+            mbar_init(lr_bar, kLT);
+            mbar_init(lr_bar + 8, 1);
+            mbar_init(lr_bar + 16, kLT);
+        }
         fence_mbar_init();
         s_fail = 0;
     }
@@ -569,7 +771,7 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
             // gains 0.1-0.5 us; two or more delay the x copy behind them.)
             const int pre = min(min(SEP ? kPreStepsSep : kPreStepsBarrier, a.depth), st.steps);
             produce<FMT>(st, r, a.err, 0, pre);
-            pdl_wait();
+            if (!kLate) pdl_wait();
             if (a.xraw_bytes) {
                 if (QMLP_INB(a.xraw_bytes - 1, (size_t)a.M * a.K * 2, 3)) {
                     mbar_arrive_expect_tx(r.xbar, a.xraw_bytes);
@@ -589,6 +791,13 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
         return;
     }
 
+    if (LR && warp > kW) {
+        float* s_d = reinterpret_cast<float*>(smem + a.lr_off);
+        lr_warps(a.lr, M, a.I, a.T * 16, threadIdx.x - kThr, s_d + M * 2 * a.T * 16, s_d,
+                 reinterpret_cast<const float*>(smem + a.act_off), lr_bar, a.limit, a.err);
+        return;
+    }
+
     constexpr int rec = rec_bytes<FMT>();
     uint4* xs = reinterpret_cast<uint4*>(smem);
     float* s_pa = reinterpret_cast<float*>(smem + a.pa_off);
@@ -598,8 +807,9 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
     bool ok = true;
 
     // x, act, the partials and the output belong to the previous kernel until
-    // it has completed
-    pdl_wait();
+    // it has completed (kLate: that one touches none of them, and let this one
+    // start only once all before it had completed)
+    if (!kLate) pdl_wait();
 
     // ---------------- phase A: gate/up over this CTA's tiles ----------------
     if (NT == 2) {
@@ -681,8 +891,8 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
                         pend_lt = lt;
                         pend_whole = cs == 0 && c == a.KcA;
                     } else {
-                        finish_tile_a<FMT, NT>(a, M, lt, cs == 0 && c == a.KcA, warp, av, s_pa, pa_floats, s_cnta,
-                                               s_sig, s_act, s_actmax);
+                        finish_tile_a<FMT, NT, LR>(a, M, lt, cs == 0 && c == a.KcA, warp, av, s_pa, pa_floats, s_cnta,
+                                               s_sig, s_act, s_actmax, lre);
                     }
                     zero_acc<NT, 2>(acc);
                     ++lt;
@@ -700,8 +910,8 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
         if (NT == 2) {
             named_bar_sync(1, kCT);  // x is no longer read: its region takes the combine slots
             if (pend_lt >= 0)
-                finish_tile_a<FMT, NT>(a, M, pend_lt, pend_whole != 0, warp, pend, s_pa, pa_floats, s_cnta, s_sig,
-                                       s_act, s_actmax);
+                finish_tile_a<FMT, NT, LR>(a, M, pend_lt, pend_whole != 0, warp, pend, s_pa, pa_floats, s_cnta, s_sig,
+                                       s_act, s_actmax, lre);
         }
         q = stepsA;
     }
@@ -710,6 +920,10 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
 
     // ---------------- restage act (prescaled fp16 fragments) ----------------
     const int tslice = a.T * 16;
+    if (LR && threadIdx.x == 0) mbar_arrive(lr_bar + 8);  // (s_act keeps the slice from here on)
+    if (LR && !SEP)
+        for (int u = blockIdx.x + warp * gridDim.x; u < (a.K + 31) / 32; u += kW * gridDim.x)
+            lr_down_prefetch(a.lr, a.K, 0, u * 32 + lane);
     if (s_fail == 0) {
         // the slice maxima were kept by the epilogues: the items (8 act
         // values each) convert straight away; one barrier
@@ -799,6 +1013,8 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
     // the CTA barrier that precedes the reads of the other CTAs' partials.
     named_bar_sync(1, kCT);
     if (threadIdx.x == 0) {
+        // the CTA's share of A_d act belongs to what the arrival releases
+        if (LR && !mbar_wait_bounded(lr_bar + 16, 0, a.limit)) atomicExch(a.err, 28);
         unsigned long long tk;
         asm volatile("atom.add.release.gpu.global.u64 %0, [%1], 1;" : "=l"(tk) : "l"(a.ticket) : "memory");
         const unsigned long long target = (tk / (unsigned long long)a.G + 1ull) * (unsigned long long)a.G;
@@ -865,7 +1081,12 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
             ++nu;
         }
     }
-    named_bar_sync(1, kCT);
+    // LR (one token): the sum of the CTAs' shares of A_d act, behind the scratch
+    float* s_vd = red + (size_t)nu * kW * 32;
+    if (LR)
+        lr_down_sum(a.lr, a.G, M, 0, threadIdx.x, kCT, s_vd + 64, s_vd, [] { named_bar_sync(1, kCT); });
+    else
+        named_bar_sync(1, kCT);
     for (int i = warp; i < nu; i += kW) {
         const int u = blockIdx.x + i * gridDim.x;
         const int m = u / units_n, n = (u % units_n) * 32 + lane;
@@ -877,7 +1098,9 @@ __global__ void __launch_bounds__(kThr, 1) gemv_split_kernel(const __grid_consta
                 a.out_f32[(size_t)m * a.K + n] = tot;
             } else {
                 const float sd = FMT == kNVFP4 ? a.invd : a.chsd[n];
-                a.out[(size_t)m * a.K + n] = __float2bfloat16_rn(tot * sd);
+                float o = tot * sd;
+                if (LR) o += lr_down_dot(a.lr, a.K, m, n, s_vd);
+                a.out[(size_t)m * a.K + n] = __float2bfloat16_rn(o);
             }
         }
     }
@@ -905,6 +1128,7 @@ struct RArgs {
     __nv_bfloat16* out; // [M, K]
     float* out_f32;     // optional [M, K]: fp32 sums without the factor, instead of out
     int G, M, K;
+    SplitLora lr;
 };
 
 template <int FMT>
@@ -948,9 +1172,77 @@ __global__ void __launch_bounds__(kRedThr, kRedMinBlocks) gemv_split_reduce_kern
     }
 }
 
-template <int FMT, int NT, int MC, bool SEP>
+// The same sums (in the same order) with adapters: a CTA a token and 64
+// columns, the column's eight sums over four groups of threads, beside them the
+// token's sum of the CTAs' shares of A_d act, whose products with B_d's row the
+// groups share too. All loads of a thread are in flight together, the row's
+// before the wait.
+template <int FMT>
+__global__ void __launch_bounds__(kRedThr) gemv_split_reduce_lr_kernel(const __grid_constant__ RArgs a) {
+    __shared__ float red[kRedWarps][64], low[4][64], s_tmp[kRedThr], s_vd[64];
+    pdl_launch_dependents();
+    const int per_m = (a.K + 63) / 64;
+    const int m = blockIdx.x / per_m, col = threadIdx.x & 63, grp = threadIdx.x >> 6;
+    const int n = (blockIdx.x % per_m) * 64 + col, R = a.lr.Rp, q4 = R / 4;
+    int slot;
+    const int n8 = lr_slot(a.lr, m, slot);
+    // this group's quarter of the row: R / 4 = 4, 8 or 16 values
+    uint2 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = make_uint2(0, 0);
+        if (n8 && n < a.K && 4 * i < q4)
+            w[i] = __ldg(reinterpret_cast<const uint2*>(a.lr.b_d + ((size_t)slot * a.K + n) * R + grp * q4) + i);
+    }
+    pdl_wait();
+    const size_t bstride = (size_t)a.M * a.K;
+    const float* src = a.part + (size_t)m * a.K + n;
+    float s0 = 0.0f, s1 = 0.0f;
+    {
+        float v0[kRedPer], v1[kRedPer];
+#pragma unroll
+        for (int i = 0; i < kRedPer; ++i) {
+            const int b = 2 * grp + i * kRedWarps;
+            v0[i] = (n < a.K && b < a.G && QMLP_INB((size_t)m * a.K + n + (size_t)b * bstride, a.part_elems, 7))
+                        ? __ldcg(src + (size_t)b * bstride)
+                        : 0.0f;
+            v1[i] = (n < a.K && b + 1 < a.G && QMLP_INB((size_t)m * a.K + n + (size_t)(b + 1) * bstride, a.part_elems, 7))
+                        ? __ldcg(src + (size_t)(b + 1) * bstride)
+                        : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < kRedPer; ++i) {
+            s0 += v0[i];
+            s1 += v1[i];
+        }
+    }
+    red[2 * grp][col] = s0;
+    red[2 * grp + 1][col] = s1;
+    lr_down_sum(a.lr, a.G, a.M, m, threadIdx.x, kRedThr, s_tmp, s_vd, [] { __syncthreads(); });
+    float d = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (4 * i < q4) {
+            const float* v = s_vd + grp * q4 + 4 * i;
+            d = fmaf(__uint_as_float(w[i].x << 16), v[0], d);
+            d = fmaf(__uint_as_float(w[i].x & 0xFFFF0000u), v[1], d);
+            d = fmaf(__uint_as_float(w[i].y << 16), v[2], d);
+            d = fmaf(__uint_as_float(w[i].y & 0xFFFF0000u), v[3], d);
+        }
+    low[grp][col] = d;
+    __syncthreads();
+    if (grp || n >= a.K || !QMLP_INB((size_t)m * a.K + n, (size_t)a.M * a.K, 7)) return;
+    float tot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRedWarps; ++i) tot += red[i][col];
+    const float sd = FMT == kNVFP4 ? a.invd : a.chsd[n];
+    a.out[(size_t)m * a.K + n] =
+        __float2bfloat16_rn(tot * sd + (low[0][col] + low[1][col] + low[2][col] + low[3][col]));
+}
+
+template <int FMT, int NT, int MC, bool SEP, bool LR>
 cudaError_t launch_t(const Args& a, size_t smem, cudaStream_t s) {
-    auto kern = gemv_split_kernel<FMT, NT, MC, SEP>;
+    auto kern = gemv_split_kernel<FMT, NT, MC, SEP, LR>;
     static bool attr = false;
     if (!attr) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kBudget);
@@ -959,7 +1251,7 @@ cudaError_t launch_t(const Args& a, size_t smem, cudaStream_t s) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.G);
-    cfg.blockDim = dim3(kThr);
+    cfg.blockDim = dim3(thr(LR));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     // Programmatic dependent launch instead of a cooperative one: a CTA can
@@ -977,20 +1269,29 @@ cudaError_t launch_t(const Args& a, size_t smem, cudaStream_t s) {
 // Schedule (b) with one 8-token column tile: instances with the token count
 // fixed for 2, 4 and 8 tokens (and 1 for FP8; NVFP4 at one token takes
 // schedule (a)), the general one otherwise.
-template <int FMT>
+template <int FMT, bool LR>
 cudaError_t launch_one_tile(const Args& a, size_t smem, int M, cudaStream_t s) {
     if constexpr (FMT == kFP8)
-        if (M == 1) return launch_t<FMT, 1, 1, true>(a, smem, s);
+        if (M == 1) return launch_t<FMT, 1, 1, true, LR>(a, smem, s);
     switch (M) {
-        case 2: return launch_t<FMT, 1, 2, true>(a, smem, s);
-        case 4: return launch_t<FMT, 1, 4, true>(a, smem, s);
-        case 8: return launch_t<FMT, 1, 8, true>(a, smem, s);
-        default: return launch_t<FMT, 1, 0, true>(a, smem, s);
+        case 2: return launch_t<FMT, 1, 2, true, LR>(a, smem, s);
+        case 4: return launch_t<FMT, 1, 4, true, LR>(a, smem, s);
+        case 8: return launch_t<FMT, 1, 8, true, LR>(a, smem, s);
+        default: return launch_t<FMT, 1, 0, true, LR>(a, smem, s);
     }
+}
+template <int FMT, bool LR>
+cudaError_t launch_m(const Args& a, size_t smem, int M, cudaStream_t s) {
+    // M <= 8 (split_fits): one 8-token MMA tile. Schedule (a) for NVFP4 at
+    // one token, (b) otherwise (see the top of the file).
+    if constexpr (FMT == kNVFP4)
+        if (M == 1) return launch_t<kNVFP4, 1, 1, false, LR>(a, smem, s);
+    // 9..16 tokens: two 8-token column tiles, x staged in halves
+    return M > 8 ? launch_t<FMT, 2, 0, true, LR>(a, smem, s) : launch_one_tile<FMT, LR>(a, smem, M, s);
 }
 
 struct Layout {
-    int xs, pa, act, pb, xraw, xraw_bytes, ring, slot, depth, sa;
+    int xs, pa, act, pb, xraw, xraw_bytes, lr, ring, slot, depth, sa;
     size_t total;
 };
 
@@ -1004,7 +1305,8 @@ bool halves_ok(int fmt, int K, const SplitPlan& P) {
     return P.G && K % kChunkK == 0 && kca % 4 == 0 && P.LA * 2 == kca && (P.LA / gemv_recs_pair(fmt)) % 2 == 0;
 }
 
-Layout layout_for(int fmt, int M, int K, const SplitPlan& P) {
+// lora_r: padded rank of the adapters (LR instances), else 0
+Layout layout_for(int fmt, int M, int K, const SplitPlan& P, int lora_r = 0) {
     Layout L;
     const int kca = (K + kChunkK - 1) / kChunkK;
     const int rec = fmt == kNVFP4 ? kRecNVFP4 : kRecFP8;
@@ -1028,7 +1330,8 @@ Layout layout_for(int fmt, int M, int K, const SplitPlan& P) {
     const bool fixed_b = (P.Cb == 1 || P.Cb == 2 || P.Cb == 4) && rb % P.Cb == 0;
     L.xraw = L.pb + (fixed_b ? 0 : al((size_t)kW * 2 * M * 16 * 4));
     L.xraw_bytes = (size_t)M * K * 2 <= (size_t)kXRawMax ? M * K * 2 : 0;
-    L.ring = L.xraw + al((size_t)L.xraw_bytes);
+    L.lr = L.xraw + al((size_t)L.xraw_bytes);
+    L.ring = L.lr + (lora_r ? al((size_t)M * 2 * (P.T * 16 + lora_r + 1) * 4) : 0);
     L.slot = std::max(2 * kW * gemv_recs_pair(fmt) * rec, kW * rb * rec);
     const long avail = (long)kBudget - L.ring - kBars - 1024;
     L.depth = avail > 0 ? (int)std::min<long>(kDepthMax, avail / L.slot) : 0;
@@ -1085,6 +1388,16 @@ bool split_fits(int fmt, int M, int K, const SplitPlan& P) {
     return L.depth >= 2 && per_cta * kW * 32 * 4 <= (size_t)L.depth * L.slot;
 }
 
+// The same with adapters: the in-kernel reduction also keeps the sum of the
+// CTAs' shares and its threads' parts in the ring.
+bool split_lora_fits(int fmt, int M, int K, int lora_r, const SplitPlan& P) {
+    if (!split_fits(fmt, M, K, P)) return false;
+    const Layout L = layout_for(fmt, M, K, P, lora_r);
+    if (L.depth < 2) return false;
+    const size_t per_cta = ((size_t)M * ((K + 31) / 32) + P.G - 1) / P.G;
+    return (per_cta * kW * 32 + 64 + kCT) * 4 <= (size_t)L.depth * L.slot;
+}
+
 size_t split_part_elems(int K, const SplitPlan& P) { return (size_t)P.G * 16 * K; }
 
 size_t split_codes_bytes(int fmt, const SplitPlan& P) {
@@ -1096,7 +1409,7 @@ cudaError_t launch_split(const SplitLaunch& L, const SplitPlan& P, cudaStream_t 
     if (L.gate.TWr != P.G * kW || L.gate.Lr != P.LA || L.gate.Rr != P.RA || L.up.TWr != P.G * kW ||
         P.RA != gemv_recs_pair(L.fmt) || P.RB != gemv_recs_single(L.fmt))
         return cudaErrorInvalidValue;
-    const Layout lay = layout_for(L.fmt, L.M, L.K, P);
+    const Layout lay = layout_for(L.fmt, L.M, L.K, P, L.lora.ids ? L.lora.Rp : 0);
     if (P.T > 64) return cudaErrorInvalidValue;
     Args a;
     a.wa0 = L.gate.wc;
@@ -1115,7 +1428,8 @@ cudaError_t launch_split(const SplitLaunch& L, const SplitPlan& P, cudaStream_t 
     a.act_in = static_cast<const __nv_bfloat16*>(L.act_in);
     a.dbg_g = L.dbg_g;
     a.dbg_u = L.dbg_u;
-    a.add = L.add;
+    a.lr = L.lora;
+    a.lr_off = lay.lr;
     a.part = L.part;
     a.ticket = L.ticket;
     a.err = L.err;
@@ -1146,15 +1460,14 @@ cudaError_t launch_split(const SplitLaunch& L, const SplitPlan& P, cudaStream_t 
     a.part_elems = split_part_elems(L.K, P);
     // the bulk copy of x needs device memory; host-resident x is staged by loads
     a.xraw_bytes = L.x_in_host ? 0 : lay.xraw_bytes;
-    // M <= 8 (split_fits): one 8-token MMA tile. Schedule (a) for NVFP4 at
-    // one token, (b) otherwise (see the top of the file).
-    if (L.fmt == kNVFP4 && L.M == 1) return launch_t<kNVFP4, 1, 1, false>(a, lay.total, s);
-    // 9..16 tokens: two 8-token column tiles, x staged in halves
-    cudaError_t e = L.M > 8 ? (L.fmt == kNVFP4 ? launch_t<kNVFP4, 2, 0, true>(a, lay.total, s)
-                                                : launch_t<kFP8, 2, 0, true>(a, lay.total, s))
-                            : (L.fmt == kNVFP4 ? launch_one_tile<kNVFP4>(a, lay.total, L.M, s)
-                                                : launch_one_tile<kFP8>(a, lay.total, L.M, s));
-    if (e != cudaSuccess) return e;
+    const bool lr = L.lora.ids != nullptr;
+    if (lr && (L.out_f32 || !L.out || L.lora.Rp > 64 || !split_lora_fits(L.fmt, L.M, L.K, L.lora.Rp, P)))
+        return cudaErrorInvalidValue;
+    cudaError_t e = L.fmt == kNVFP4 ? (lr ? launch_m<kNVFP4, true>(a, lay.total, L.M, s)
+                                          : launch_m<kNVFP4, false>(a, lay.total, L.M, s))
+                                    : (lr ? launch_m<kFP8, true>(a, lay.total, L.M, s)
+                                          : launch_m<kFP8, false>(a, lay.total, L.M, s));
+    if (e != cudaSuccess || (L.fmt == kNVFP4 && L.M == 1)) return e;
     RArgs r;
     r.part_elems = a.part_elems;
     r.part = L.part;
@@ -1165,8 +1478,9 @@ cudaError_t launch_split(const SplitLaunch& L, const SplitPlan& P, cudaStream_t 
     r.G = P.G;
     r.M = L.M;
     r.K = L.K;
+    r.lr = L.lora;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(L.M * ((L.K + 31) / 32)));
+    cfg.gridDim = dim3((unsigned)(L.M * ((L.K + (lr ? 63 : 31)) / (lr ? 64 : 32))));
     cfg.blockDim = dim3(kRedThr);
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -1174,6 +1488,9 @@ cudaError_t launch_split(const SplitLaunch& L, const SplitPlan& P, cudaStream_t 
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    if (lr)
+        return L.fmt == kNVFP4 ? cudaLaunchKernelEx(&cfg, gemv_split_reduce_lr_kernel<kNVFP4>, r)
+                               : cudaLaunchKernelEx(&cfg, gemv_split_reduce_lr_kernel<kFP8>, r);
     return L.fmt == kNVFP4 ? cudaLaunchKernelEx(&cfg, gemv_split_reduce_kernel<kNVFP4>, r)
                            : cudaLaunchKernelEx(&cfg, gemv_split_reduce_kernel<kFP8>, r);
 }

@@ -1,5 +1,6 @@
 // internal.h -- host-side structures shared by the qmlp translation units.
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -108,6 +109,9 @@ struct SplitPlan {
 };
 SplitPlan plan_split(int fmt, int K, int I, int num_sms);
 bool split_fits(int fmt, int M, int K, const SplitPlan& P);
+// Whether the decode kernel reduces its partials itself (schedule (a)).
+inline bool split_in_kernel(int fmt, int M) { return fmt == kNVFP4 && M == 1; }
+bool split_lora_fits(int fmt, int M, int K, int lora_r, const SplitPlan& P);
 size_t split_part_elems(int K, const SplitPlan& P);       // fp32 partials for M <= 16
 size_t split_codes_bytes(int fmt, const SplitPlan& P);     // down records, CTA-sliced
 // Down projection [K, I] into the CTA-sliced layout: local record u = w*LB + k
@@ -116,6 +120,18 @@ size_t split_codes_bytes(int fmt, const SplitPlan& P);     // down records, CTA-
 cudaError_t repack_nvfp4_split(const uint8_t* w, const uint8_t* scale, int N, int K, const SplitPlan& P,
                                uint8_t* wc, cudaStream_t s);
 cudaError_t repack_fp8_split(const uint8_t* w, int N, int K, const SplitPlan& P, uint8_t* wc, cudaStream_t s);
+// Low-rank adapters inside the decode kernel (see gemv_split.cu).
+struct SplitLora {
+    const int* ids = nullptr;   // [M] slots (null: no adapters)
+    const int* rank = nullptr;  // [slots]
+    const float* scale = nullptr;
+    int slots = 0, Rp = 0;
+    const float* v = nullptr;   // fp32 [M][2 Rp]: c A x of gate and up, written by the launch before
+    const __nv_bfloat16* b_gu = nullptr;  // [slots][2][I][Rp]
+    const __nv_bfloat16* a_d = nullptr;   // [slots][Rp][I]
+    const __nv_bfloat16* b_d = nullptr;   // [slots][K][Rp]
+    float* vd = nullptr;        // [G][M][Rp]: the CTAs' shares of A_d act
+};
 struct SplitLaunch {
     int fmt = 0, M = 0, K = 0, I = 0;
     GemvProj gate, up;               // GEMV layout with TWr = 16G, Lr = LA
@@ -130,7 +146,7 @@ struct SplitLaunch {
     const void* act_in = nullptr;    // optional bf16 [M, I]: the down projection consumes these (debug)
     float* dbg_g = nullptr;          // optional fp32 [M, I]: raw gate dot products (debug; with dbg_u)
     float* dbg_u = nullptr;          // optional fp32 [M, I]: raw up dot products (debug)
-    const float* add = nullptr;      // optional fp32 [M, 2I]: added to gate and up after the factor
+    SplitLora lora;
     float* part = nullptr;           // >= split_part_elems
     unsigned long long* ticket = nullptr;  // grid-barrier ticket counter (zeroed at create)
     int* err = nullptr;

@@ -532,12 +532,15 @@ QMLP_DEV float dot8(const uint4& a, const uint4& b, float s) {
     return s;
 }
 
-// v[m, j] = c A[slot(m)][j] . x[m]: a CTA a (row j, token m).
+// v[m, j] = c A[slot(m)][j] . x[m]: a CTA a (row j, token m). The next launch may
+// start at once or, `late`, once everything before this one has completed (see
+// gemv_split.cu).
 __global__ void __launch_bounds__(kThr) shrink_few_kernel(const LrFew a) {
-    pdl_launch_dependents();
     const int j = blockIdx.x, m = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (!a.late) pdl_launch_dependents();
     pdl_wait();
+    if (a.late) pdl_launch_dependents();
     const int slot = a.ids[m];
     const bool has = slot >= 0 && slot < a.slots && a.rank[slot] > j % a.Rp;
     float s = 0.0f;
@@ -786,10 +789,10 @@ cudaError_t expand_t(const LrExpand& a, int tiles, int zs, cudaStream_t s) {
 int lr_max_tiles(int M, int slots) { return M / kT + std::min(slots + 1, M) + 1; }
 
 // CTAs of a cluster that share a contraction of `steps`: a power of two up to
-// 8, while the grid stays under three CTAs an SM and each has two steps.
+// 8, while the grid stays under four CTAs an SM and each has two steps.
 static int lr_splits(int tiles, int steps, int num_sms) {
     int n = 1;
-    while (n < 8 && 2 * n * tiles <= 3 * num_sms && steps >= 4 * n) n *= 2;
+    while (n < 8 && 2 * n * tiles <= 4 * num_sms && steps >= 4 * n) n *= 2;
     return n;
 }
 
