@@ -6,8 +6,10 @@
 //   m = m b1 + g (1 - b1)
 //   v = v b2 + g g (1 - b2)
 //   p = p (1 - lr wd) - lr / (1 - b1^t) * m / ( sqrt(v) / sqrt(1 - b2^t) + eps )
-// All of it in fp32, each operation rounded once and none contracted, so that
-// a state does not depend on how the compiler fuses a product and a sum. p is
+// All of it in fp32, each operation of a state rounded once and none contracted,
+// so that a state does not depend on how the compiler fuses a product and a sum;
+// the update's quotient is the fast one (two units of the last place of a term
+// of the size of lr). p is
 // the fp32 master where there is one (then param = bf16(p) is written beside
 // it), else the parameter itself.
 //
@@ -129,11 +131,20 @@ QMLP_DEV void store8_codes(uint8_t* p, float* scale, int n, const float (&v)[kPe
     for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(v[i]));
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // bits order as the floats do
     const float s = __fmul_rn(top, 1.0f / 448.0f);
+    // v / s, correctly rounded where that can matter: a product with the
+    // reciprocal is within two units of the last place, so only a quotient that
+    // close to the middle of two codes (or under the normal codes, whose middles
+    // lie elsewhere) is divided out. (69M elements, both states: 229 -> 190 us.)
+    const float rs = __frcp_rn(s);
     float q[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        // no scale: zeros (and values under 448 of the smallest subnormal), or a NaN, which stays one
-        q[i] = s > 0.0f ? __fdiv_rn(v[i], s) : v[i];
+        q[i] = __fmul_rn(v[i], rs);
+        const uint32_t b = __float_as_uint(q[i]);
+        // normal codes keep 3 of 23 mantissa bits: the middle is 0x80000 of the other 20
+        if (((b + 4u - 0x80000u) & 0xFFFFFu) <= 8u || !(fabsf(q[i]) >= 0.016f && fabsf(q[i]) < 449.0f))
+            // no scale: zeros (and values under 448 of the smallest subnormal), or a NaN, which stays one
+            q[i] = s > 0.0f ? __fdiv_rn(v[i], s) : v[i];
         if (FLOOR && s > 0.0f && q[i] > 0.0f) q[i] = fmaxf(q[i], 0.001953125f);
     }
     uint32_t w[2];
@@ -176,7 +187,7 @@ QMLP_DEV void step8(const AdamWChunk& c, const AdamWStep& k, int at, int n) {
         v[i] = __fadd_rn(__fmul_rn(v[i], k.b2), __fmul_rn(__fmul_rn(gs, gs), k.omb2));
         r[i] = __fsqrt_rn(v[i]);
         const float d = __fadd_rn(__fmul_rn(r[i], k.rbc2), k.eps);
-        p[i] = __fsub_rn(__fmul_rn(p[i], k.decay), __fmul_rn(__fdiv_rn(m[i], d), k.step));
+        p[i] = __fsub_rn(__fmul_rn(p[i], k.decay), __fmul_rn(__fdividef(m[i], d), k.step));
     }
     if (MASTER) store8<VEC>(master, n, p);
     store8<VEC>(param, n, p);

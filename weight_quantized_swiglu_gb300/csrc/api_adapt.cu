@@ -46,6 +46,7 @@ struct qmlp_train_s {
     // ones into the adapter's images (T = 3), if all can be divided by.
     bool steps = true;
     int T = 2;
+    cudaEvent_t ev_img = nullptr;    // the images are there (side stream)
     uint8_t* img_gu = nullptr;       // images of B gate/up, B down; of A down, A gate/up
     uint8_t* img_d = nullptr;
     // FP8: the factors that d gate and d up carry (1 where a channel's is too
@@ -545,10 +546,28 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     const qmlp_lora_t* l = t->l;
     const int K = h->K, I = h->I, R = l->Rp;
     const bool ext = v.vgu.ext, fp8 = h->fmt == kFP8;
-    TRY(launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s));
+    // beside: the adapter's images, then down's weights
     TRY(beside(h, s, [&](cudaStream_t b) {
+        if (ad && ext) {
+            LrImage m = image_of(t, ad, v.vgu, I, true, 2, t->img_gu);
+            m.src[0] = bf(ad->gate_b);
+            m.src[1] = bf(ad->up_b);
+            m.sn = ad->rank;
+            m.sj = 1;
+            m.div[0] = t->eff;
+            m.div[1] = t->eff + I;
+            TRY(launch_lr_image(m, b));
+            m = image_of(t, ad, v.vd, K, false, 1, t->img_d);
+            m.src[0] = bf(ad->down_b);
+            m.sn = ad->rank;
+            m.sj = 1;
+            m.div[0] = h->gv[2].chs;
+            TRY(launch_lr_image(m, b));
+            TRY(cudaEventRecord(t->ev_img, b));
+        }
         return launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, b);
     }));
+    TRY(launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s));
     if (ad) {
         TRY(launch_lr_pack(pack_train(t, ad, false, !ext), s));
         LrShrink a = shrink_all(t, x, M, K, v.vgu);
@@ -559,24 +578,8 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
             a.half = R;
         }
         TRY(launch_lr_shrink(a, 2 * R, false, tiles_for(M), 1, h->num_sms, s));
-        if (ext) {
-            LrImage m = image_of(t, ad, v.vgu, I, true, 2, t->img_gu);
-            m.src[0] = bf(ad->gate_b);
-            m.src[1] = bf(ad->up_b);
-            m.sn = ad->rank;
-            m.sj = 1;
-            m.div[0] = t->eff;
-            m.div[1] = t->eff + I;
-            TRY(launch_lr_image(m, h->num_sms, s));
-            m = image_of(t, ad, v.vd, K, false, 1, t->img_d);
-            m.src[0] = bf(ad->down_b);
-            m.sn = ad->rank;
-            m.sj = 1;
-            m.div[0] = h->gv[2].chs;
-            TRY(launch_lr_image(m, h->num_sms, s));
-        } else {
-            TRY(expand_all(t, v.vgu, M, R, 2, l->b_gu, (size_t)I * R, I, false, s));
-        }
+        if (ext) TRY(cudaStreamWaitEvent(s, t->ev_img, 0));
+        else TRY(expand_all(t, v.vgu, M, R, 2, l->b_gu, (size_t)I * R, I, false, s));
     }
     GemmLaunch g = dq_gemm(t, M);
     g.epi = kEpiSwiGLU;
@@ -628,33 +631,34 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     // which lie along the contraction here; dout is then prescaled to fp16, so
     // that neither costs a rounding to 8 bits: dx was 2.8e-3 off with bf16
     // images, 2.3e-3 with these), then gate's and up's beside the first GEMM
-    TRY(launch_gemm_predecode_t(h->gm_d, t->mul_d, nullptr, fp8, t->img_t, t->img_t_bytes, s));
     TRY(beside(h, s, [&](cudaStream_t b) {
+        if (ad && ext_d) {
+            LrImage m = image_of(t, ad, wd, I, false, 1, t->img_d);
+            m.src[0] = bf(ad->down_a);
+            m.sn = 1;
+            m.sj = I;
+            TRY(launch_lr_image(m, b));
+        }
+        if (ad && ext) {
+            LrImage m = image_of(t, ad, wv, K, false, 2, t->img_gu);
+            m.src[0] = bf(ad->gate_a);
+            m.src[1] = bf(ad->up_a);
+            m.sn = 1;
+            m.sj = K;
+            TRY(launch_lr_image(m, b));
+            TRY(cudaEventRecord(t->ev_img, b));
+        }
         return launch_gemm_predecode_t(h->gm_gu, t->row, t->row ? t->row + I : nullptr, false, h->wdec, h->wdec_bytes, b);
     }));
+    TRY(launch_gemm_predecode_t(h->gm_d, t->mul_d, nullptr, fp8, t->img_t, t->img_t_bytes, s));
     if (ad) {
         TRY(launch_lr_pack(pack_train(t, ad, true, !ext_d || !ext), s));
         LrShrink a = shrink_all(t, dy, M, K, wd);
         a.w = l->b_d;
         if (ext_d) a.mul0 = 1.0f / h->gv[2].inv_g;
         TRY(launch_lr_shrink(a, R, true, tiles_for(M), 1, h->num_sms, s));
-        if (ext_d) {
-            LrImage m = image_of(t, ad, wd, I, false, 1, t->img_d);
-            m.src[0] = bf(ad->down_a);
-            m.sn = 1;
-            m.sj = I;
-            TRY(launch_lr_image(m, h->num_sms, s));
-        } else {
-            TRY(expand_all(t, wd, M, R, 1, l->a_d, 0, I, true, s));
-        }
-        if (ext) {
-            LrImage m = image_of(t, ad, wv, K, false, 2, t->img_gu);
-            m.src[0] = bf(ad->gate_a);
-            m.src[1] = bf(ad->up_a);
-            m.sn = 1;
-            m.sj = K;
-            TRY(launch_lr_image(m, h->num_sms, s));
-        }
+        if (!ext_d) TRY(expand_all(t, wd, M, R, 1, l->a_d, 0, I, true, s));
+        if (ext) TRY(cudaStreamWaitEvent(s, t->ev_img, 0));
     }
     // d act, and through the activation d gate and d up
     GemmLaunch g = dq_gemm(t, M);
@@ -835,9 +839,11 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
         if (e == cudaSuccess) e = cudaMemcpyAsync(t->mul_d, f.data(), K * sizeof(float), cudaMemcpyHostToDevice, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     }
+    if (e == cudaSuccess) e = cudaEventCreateWithFlags(&t->ev_img, cudaEventDisableTiming);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) {
         cudaStreamSynchronize(s);
+        if (t->ev_img) cudaEventDestroy(t->ev_img);
         qmlp_lora_destroy(t->l);
         t->mem.release();
         delete t;
@@ -850,6 +856,7 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
 void qmlp_train_destroy(qmlp_train_t* t) {
     if (!t) return;
     cudaDeviceSynchronize();
+    cudaEventDestroy(t->ev_img);
     qmlp_lora_destroy(t->l);
     t->mem.release();
     delete t;

@@ -248,6 +248,8 @@ QMLP_DEV void store16(__nv_bfloat16* dst, const uint32_t (&v)[8]) {
 template <int FMT, bool EXT>
 QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg, int nt, int first, int step) {
     // this warp's columns: 32 from each of first, first + step, ...
+    // 2^-sg, for the instances whose every factor is one product
+    const float pw = sg >= -126 && sg <= 126 ? __int_as_float((127 - sg) << 23) : scalbnf(1.0f, -sg);
     if (a.epi == kEpiSwiGLU) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 #pragma unroll 1
@@ -278,8 +280,8 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         float r4[4], g4[4], u4[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            g4[e] = scalbnf(g[h + 4 * j + e], -sg) * f4_at(fg, e) + f4_at(dg[j], e);
-                            u4[e] = scalbnf(u[h + 4 * j + e], -sg) * f4_at(fu, e) + f4_at(du[j], e);
+                            g4[e] = g[h + 4 * j + e] * pw * f4_at(fg, e) + f4_at(dg[j], e);
+                            u4[e] = u[h + 4 * j + e] * pw * f4_at(fu, e) + f4_at(du[j], e);
                             r4[e] = silu_f32(g4[e]) * u4[e];
                         }
                         if (a.gu_g) {
@@ -353,9 +355,9 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         float dg[4], du[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float d = scalbnf(y[h + 4 * j + e], -sg) * a.inv0 + f4_at(ad[j], e),
+                            const float d = y[h + 4 * j + e] * pw * a.inv0 + f4_at(ad[j], e),
                                         gv = f4_at(g4[j], e);
-                            const float sg1 = 1.0f / (1.0f + expf(-gv));
+                            const float sg1 = __fdividef(1.0f, 1.0f + expf(-gv));  // 0 past 2^126
                             du[e] = d * (gv * sg1) * f4_at(fu, e);
                             dg[e] = d * f4_at(u4[j], e) * (sg1 * (1.0f + gv * (1.0f - sg1))) * f4_at(fg, e);
                         }

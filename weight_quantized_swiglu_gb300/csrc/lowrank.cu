@@ -103,22 +103,28 @@ QMLP_DEV bool tile_of(const LrTokens& t, int i, int& slot, int& pos0, int& n) {
 QMLP_DEV void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-QMLP_DEV float4 sum_cluster(uint32_t addr, int n) {
-    float4 s = make_float4(0, 0, 0, 0);
-    for (int r = 0; r < n; ++r) {
-        uint32_t ra;
-        float4 v;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(r));
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                     : "r"(ra)
-                     : "memory");
-        s.x += v.x;
-        s.y += v.y;
-        s.z += v.z;
-        s.w += v.w;
+QMLP_DEV float4 sum_cluster(uint32_t addr, int n) {  // n <= 8
+    float4 v[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        v[r] = make_float4(0, 0, 0, 0);
+        if (r < n) {
+            uint32_t ra;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(addr), "r"(r));
+            asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                         : "=f"(v[r].x), "=f"(v[r].y), "=f"(v[r].z), "=f"(v[r].w)
+                         : "r"(ra)
+                         : "memory");
+        }
     }
-    return s;
+#pragma unroll
+    for (int r = 1; r < 8; ++r) {
+        v[0].x += v[r].x;
+        v[0].y += v[r].y;
+        v[0].z += v[r].z;
+        v[0].w += v[r].w;
+    }
+    return v[0];
 }
 
 // ---------------------------------------------------------------------------
@@ -675,9 +681,9 @@ __global__ void __launch_bounds__(256) pack_kernel(const LrPack a) {
     pdl_wait();
     const int p = a.first + blockIdx.y;  // 0..2: A of gate, up, down; 3..5: B
     const LrPackPart& q = a.part[p];
-    const long total = (long)q.rows * q.cols;
-    for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (long)gridDim.x * blockDim.x) {
-        const int row = (int)(i / q.cols), col = (int)(i % q.cols);
+    const uint32_t total = (uint32_t)q.rows * q.cols;  // at most 64 x 65536
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < total; i += gridDim.x * 256) {
+        const int row = (int)(i / (uint32_t)q.cols), col = (int)(i % (uint32_t)q.cols);
         // A: rows are the rank; B: columns are
         const bool in = q.src && (p < 3 ? row : col) < a.r;
         __nv_bfloat16 v = __float2bfloat16_rn(0.0f);
@@ -704,32 +710,32 @@ __global__ void __launch_bounds__(256) pack_kernel(const LrPack a) {
 __global__ void __launch_bounds__(256) image_kernel(const LrImage a) {
     pdl_launch_dependents();
     pdl_wait();
-    const long total = (long)a.tiles * a.ext * 2048;
-    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
-        const int p = (int)(i & 7), row = (int)(i >> 3) & 255, e = (int)((i >> 11) % a.ext), nt = (int)((i >> 11) / a.ext);
-        const int l = p ^ (row & 7);
-        const int side = a.interleaved ? row >> 7 : 0;
-        const int n = a.interleaved ? nt * 128 + (row & 127) : nt * 256 + row;
-        __align__(16) __nv_bfloat16 o[8];
+    const int sh = a.R == 16 ? 4 : a.R == 32 ? 5 : 6, two = a.parts - 1;
+    const int img = blockIdx.x >> 3, e = img % a.ext, nt = img / a.ext;  // a CTA 32 rows of an image
+    const int i = (blockIdx.x & 7) * 256 + threadIdx.x;
+    const int p = i & 7, row = i >> 3, l = p ^ (row & 7);
+    const int side = a.interleaved ? row >> 7 : 0;
+    const int n = a.interleaved ? nt * 128 + (row & 127) : nt * 256 + row;
+    const float div = a.T == 3 && n < a.N ? a.div[side][n] : 1.0f;
+    // the eight columns of a chunk lie in one word and part (R is 16 or more)
+    const int c = e * 64 + l * 8, wp = c >> sh, j0 = c & (a.R - 1);
+    const int w = wp >> two, part = wp & two;
+    const bool in = w < a.T && n < a.N && a.src[part] && (!a.interleaved || part == side);
+    const __nv_bfloat16* src = in ? a.src[part] + (size_t)n * a.sn + (size_t)j0 * a.sj : nullptr;
+    __align__(16) __nv_bfloat16 o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o[k] = in && j0 + k < a.r ? src[(size_t)k * a.sj] : __float2bfloat16_rn(0.0f);
+    if (a.T == 3) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const int c = e * 64 + l * 8 + k;
-            const int w = c / (a.parts * a.R), part = (c / a.R) % a.parts, j = c % a.R;
-            float v = 0.0f;
-            if (w < a.T && j < a.r && n < a.N && a.src[part] && (!a.interleaved || part == side)) {
-                v = __bfloat162float(a.src[part][(size_t)n * a.sn + (size_t)j * a.sj]);
-                if (a.T == 3) {
-                    v /= a.div[part][n];
-                    if (w == 2) v -= __bfloat162float(__float2bfloat16_rn(v));
-                }
-            }
+            float v = __fdividef(__bfloat162float(o[k]), div);
+            if (w == 2) v -= __bfloat162float(__float2bfloat16_rn(v));
             o[k] = __float2bfloat16_rn(v);
         }
-        *reinterpret_cast<uint4*>(a.img + i * 16) = *reinterpret_cast<const uint4*>(o);
     }
+    *reinterpret_cast<uint4*>(a.img + ((size_t)img * 2048 + i) * 16) = *reinterpret_cast<const uint4*>(o);
 }
 
-// cluster: CTAs of a cluster along y.
 template <typename K, typename A>
 cudaError_t launch_pdl(K kern, dim3 grid, int threads, int smem, const A& a, cudaStream_t s, int cluster = 1) {
     cudaLaunchConfig_t cfg = {};
@@ -855,9 +861,8 @@ cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, in
     return cudaPeekAtLastError();
 }
 
-cudaError_t launch_lr_image(const LrImage& a, int num_sms, cudaStream_t s) {
-    const long n = (long)a.tiles * a.ext * 2048;
-    return launch_pdl(image_kernel, dim3((unsigned)std::min<long>((n + 255) / 256, 8L * num_sms)), 256, 0, a, s);
+cudaError_t launch_lr_image(const LrImage& a, cudaStream_t s) {
+    return launch_pdl(image_kernel, dim3((unsigned)(a.tiles * a.ext * 8)), 256, 0, a, s);
 }
 
 cudaError_t launch_lr_pack(const LrPack& a, cudaStream_t s) {

@@ -136,7 +136,7 @@ struct LrImage {
     int tiles = 0, ext = 0;
     uint8_t* img = nullptr;
 };
-cudaError_t launch_lr_image(const LrImage& a, int num_sms, cudaStream_t s);
+cudaError_t launch_lr_image(const LrImage& a, cudaStream_t s);
 
 int lr_max_tiles(int M, int slots);
 cudaError_t launch_lr_tokgrad(const LrTokGrad& a, int nc, int zs, int num_sms, cudaStream_t s);
