@@ -428,6 +428,7 @@ qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M
         if (ex) {
             if (ex->between(s) != cudaSuccess) return QMLP_ERR_CUDA;
             g.add = ex->add_down;
+            g.split_tail = g.pair && g.wdec;
             g.ldadd = (size_t)h->K;
         }
         g.epi = out_f32 ? kEpiRaw : kEpiPlain;

@@ -471,6 +471,7 @@ GemmLaunch dq_gemm(const qmlp_train_s* t, int M) {
     g.wait_ns = h->wait_ns;
     g.withhold = h->withhold;
     g.images_ready = true;
+    g.split_tail = g.pair;
     return g;
 }
 
@@ -711,66 +712,37 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     else if (ad) add_terms(g, l->y, K);
     TRY(launch_gemm(g, h->num_sms, s));
     if (!gr) return cudaSuccess;
-    auto to = [](const void* p) { return static_cast<__nv_bfloat16*>(const_cast<void*>(p)); };
-    LrTokGrad q;
-    q.M = M;
-    q.r = ad->rank;
-    q.Rp = R;
-    auto v_of = [&](LrTokGrad& c, const Words& w) {
-        c.v = w.p;
-        c.ldv = w.ld;
-        c.v_word = w.nc;
+    // every gradient in one launch: B's = c dy^T (z A^T), A's = c (dy B)^T z
+    LrTokGrads all;
+    auto add = [&](const void* out, const void* z, const __nv_bfloat16* z_lo, int ldz, int D, const Words& w, int col,
+                   bool rows_d, float mul, const float* div) {
+        if (!out) return;
+        LrTokGrad& q = all.job[all.count++];
+        q.x = bf(z);
+        q.x_lo = z_lo;
+        q.ldx = ldz;
+        q.D = D;
+        q.M = M;
+        q.v = w.p + col;
+        q.ldv = w.ld;
+        q.v_word = w.nc;
+        q.rows_d = rows_d;
+        q.r = ad->rank;
+        q.out = static_cast<__nv_bfloat16*>(const_cast<void*>(out));
+        q.mul = mul;
+        q.div = div;
     };
-    // NVFP4's factors that v lacks as a GEMM's operand
-    const bool lack = ext && !fp8;
-    if (gr->down_b) {
-        LrTokGrad c = q;
-        c.x = dy;
-        c.ldx = c.D = K;
-        v_of(c, v.vd);
-        if (lack) c.mul[0] = h->gv[2].inv_g;
-        c.rows_d = true;
-        c.out[0] = to(gr->down_b);
-        TRY(launch_lr_tokgrad(c, R, 1, h->num_sms, s));
-    }
-    if (gr->down_a) {
-        LrTokGrad c = q;
-        c.x = v.act;
-        c.x_lo = v.act_lo;
-        c.ldx = c.D = I;
-        v_of(c, wd);
-        if (ext_d) c.mul[0] = h->gv[2].inv_g;
-        c.out[0] = to(gr->down_a);
-        TRY(launch_lr_tokgrad(c, R, 1, h->num_sms, s));
-    }
-    if (gr->gate_b || gr->up_b) {
-        LrTokGrad c = q;
-        c.x = t->dgu;
-        c.x_lo = lo;
-        c.ldx = (size_t)2 * I;
-        c.x_z = I;
-        c.D = I;
-        v_of(c, v.vgu);
-        c.rows_d = true;
-        c.out[0] = to(gr->gate_b);
-        c.out[1] = to(gr->up_b);
-        for (int i = 0; i < 2; ++i) {
-            // d gate carries the factor, and v lacks it where it is NVFP4's operand
-            c.div[i] = t->eff ? t->eff + (size_t)i * I : nullptr;
-            c.mul[i] = lack ? 1.0f : 1.0f / h->gv[i].inv_g;
-        }
-        TRY(launch_lr_tokgrad(c, R, 2, h->num_sms, s));
-    }
-    if (gr->gate_a || gr->up_a) {
-        LrTokGrad c = q;
-        c.x = static_cast<const __nv_bfloat16*>(x);
-        c.ldx = c.D = K;
-        v_of(c, wv);
-        c.out[0] = to(gr->gate_a);
-        c.out[1] = to(gr->up_a);
-        TRY(launch_lr_tokgrad(c, 2 * R, 1, h->num_sms, s));
-    }
-    return cudaSuccess;
+    // v lacks NVFP4's factor where it is a GEMM's operand; d gate and d up carry
+    // theirs (FP8: eff)
+    const float fd = ext && !fp8 ? h->gv[2].inv_g : 1.0f;
+    const float fg = ext && !fp8 ? 1.0f : 1.0f / h->gv[0].inv_g, fu = ext && !fp8 ? 1.0f : 1.0f / h->gv[1].inv_g;
+    add(gr->gate_b, t->dgu, lo, 2 * I, I, v.vgu, 0, true, fg, t->eff);
+    add(gr->up_b, t->dgu + I, lo ? lo + I : nullptr, 2 * I, I, v.vgu, R, true, fu, t->eff ? t->eff + I : nullptr);
+    add(gr->down_a, v.act, v.act_lo, I, I, wd, 0, false, ext_d ? h->gv[2].inv_g : 1.0f, nullptr);
+    add(gr->gate_a, x, nullptr, K, K, wv, 0, false, 1.0f, nullptr);
+    add(gr->up_a, x, nullptr, K, K, wv, R, false, 1.0f, nullptr);
+    add(gr->down_b, dy, nullptr, K, K, v.vd, 0, true, fd, nullptr);
+    return launch_lr_tokgrad(all, R, h->num_sms, s);
 }
 #undef TRY
 

@@ -157,6 +157,11 @@ struct Args {
     // further contraction steps of low-rank adapters (CTA pairs): activations
     // [M][64 ext] and images [Nt][ext], through tensor maps of their own
     int ext;
+    // CTA pairs, plain epilogue: the last `tail` tiles, which would leave most
+    // pairs idle for a tile's time, are split over the contraction, tail_splits
+    // pairs a tile, into ws [tail][tail_splits][256][256]; a kernel after this
+    // one adds them. (tail 0: none.)
+    int tail, tail_splits;
     void* out_lo;          // SwiGLU, SwiGLUGrad: optional, bf16 of what out's rounding leaves
 };
 
@@ -827,6 +832,20 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
     const int KS = a.Kd / BK;
     const int KT = EXT ? KS + a.ext : KS;  // with the adapters' steps
     const int units = Mt2 * Nt;  // n-tile-major, as the single-CTA kernel
+    // this pair's i-th piece of work: a tile, or its share of a split one
+    const int whole = EXT ? units - a.tail : units;
+    auto piece = [&](int i, int& u, int& k0, int& k1) {
+        u = pair + i * npairs;
+        k0 = 0;
+        k1 = KT;
+        if (!EXT || u < whole) return u < whole;
+        if (i * npairs != whole || pair >= a.tail * a.tail_splits) return false;
+        const int sp = pair % a.tail_splits;
+        u = whole + pair / a.tail_splits;
+        k0 = (int)((long)KT * sp / a.tail_splits);
+        k1 = (int)((long)KT * (sp + 1) / a.tail_splits);
+        return true;
+    };
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kL; ++s) {
@@ -861,12 +880,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
             if (PRE) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&bmap)) : "memory");
             int it = 0;
             bool ok = !PRE || rank == 0;  // PRE: the leader loads the stages of both CTAs
-            for (int u = pair; u < units && ok; u += npairs) {
+            int u, k0, k1;
+            for (int i = 0; ok && piece(i, u, k0, k1); ++i) {
                 const int nt = u / Mt2, mt2 = u % Mt2;
                 const uint8_t* blk = a.tiles + (size_t)nt * KS * raw_bytes<FMT>();
                 // error-path tests: the pair's very last k-step is never loaded
-                const int ks_stop = (a.withhold && u + npairs >= units) ? KT - 1 : KT;
-                for (int ks = 0; ks < ks_stop; ++ks, ++it) {
+                const int ks_stop = (a.withhold && u + npairs >= units) ? k1 - 1 : k1;
+                for (int ks = k0; ks < ks_stop; ++ks, ++it) {
                     const int s = it % kL;
                     if (it >= kL &&
                         !wait_or_abort(empty(s), (uint32_t)((it / kL - 1) & 1), abort_flag, a.err, 41, a.limit)) {
@@ -924,7 +944,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
         if (lane == 0) {
             int it = 0, tc = 0;
             bool ok = true, issued = false;
-            for (int u = pair; u < units && ok; u += npairs, ++tc) {
+            int u, k0, k1;
+            for (; ok && piece(tc, u, k0, k1); ++tc) {
                 const int buf = tc & 1, use = tc >> 1;
                 if (rank == 0) {
                     // ---------------- MMA issuer (leader) ----------------
@@ -937,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
                     }
                     tc_fence_after();
                     const uint32_t d_tmem = tmem + (uint32_t)(buf * BN);
-                    for (int ks = 0; ks < KT; ++ks, ++it) {
+                    for (int ks = k0; ks < k1; ++ks, ++it) {
                         const int s = it % kL, b = it % kBSd;
                         const bool ready =
                             wait_or_abort(full(s), (uint32_t)((it / kL) & 1), abort_flag, a.err, 44, a.limit) &&
@@ -956,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
                         for (int k = 0; k < BK / 16; ++k)
                             umma_f16_pair(d_tmem, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32),
                                           PRE && !(EXT && a.f16) ? kIdescPairBF16 : kIdescPair,
-                                          (ks != 0 || k != 0) ? 1u : 0u);
+                                          (ks != k0 || k != 0) ? 1u : 0u);
                         issued = true;
                         umma_commit_pair(empty(s));
                         if (!PRE) umma_commit_pair(bempty(b));
@@ -977,15 +998,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
             // every MMA that wrote either CTA's TMEM must be finished before
             // TMEM is freed: the leader's last commit reaches both done barriers
             if (rank == 0 && issued) umma_commit_pair(done_bar);
-            if (rank != 0 || issued) mbar_wait_bounded(done_bar, 0, kGemmWaitNs);
+            // (a pair that the split tiles leave without work has issued none)
+            if (((rank != 0 && tc > 0) || issued) && !mbar_wait_bounded(done_bar, 0, kGemmWaitNs)) atomicExch(a.err, 53);
         }
     } else if (warp < 2 + kGroups * kEpiWarps) {
         // ---------------- epilogue: this CTA's 128 tokens ----------------
         const int q = warp & 3;
         const int grp = (warp - 2) / kEpiWarps;
         const int row_in_tile = q * 32 + lane;
-        int tc = 0;
-        for (int u = pair; u < units; u += npairs, ++tc) {
+        int tc = 0, u, k0, k1;
+        for (; piece(tc, u, k0, k1); ++tc) {
             const int nt = u / Mt2, mt2 = u % Mt2;
             const int buf = tc & 1, use = tc >> 1;
             const bool ready = wait_or_abort(acc_full(buf), (uint32_t)(use & 1), abort_flag, a.err, 50, a.limit);
@@ -995,7 +1017,21 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
             const bool live = m < a.M;
             const int sg = live && a.sig ? a.sig[m] : 0;  // no prescale (null sig): bf16 operands
             const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
-            store_tile<FMT, EXT>(a, tbase, m, live, sg, nt, grp * 32, kGroups * 32);
+            if (EXT && u >= whole) {
+                float* ws = a.ws + (((size_t)pair * 2 + rank) * BM + row_in_tile) * BN;
+#pragma unroll 1
+                for (int c0 = grp * 32; c0 < BN; c0 += kGroups * 32) {
+                    float y[32];
+                    tmem_ld32(tbase + c0, y);
+                    if (live) {
+                        float4* dst = reinterpret_cast<float4*>(ws + c0);
+#pragma unroll
+                        for (int v = 0; v < 8; ++v) dst[v] = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+                    }
+                }
+            } else {
+                store_tile<FMT, EXT>(a, tbase, m, live, sg, nt, grp * 32, kGroups * 32);
+            }
             tc_fence_before();
             mbar_arrive(acc_empty(buf));
         }
@@ -1091,6 +1127,34 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const Args a) {
         if (a.add) y += a.add[(size_t)m * a.ldadd + n];
         *out = __float2bfloat16_rn(y);
     }
+}
+
+// The split tiles of a CTA-pair GEMM: out = bf16(factor * sum of the pairs'
+// shares, in order, + add). A thread four columns of a row.
+template <int FMT>
+__global__ void __launch_bounds__(256) tail_reduce_kernel(const Args a) {
+    const int Mt2 = (a.M + 2 * BM - 1) / (2 * BM), units = Mt2 * (a.N / BN);
+    const int i = blockIdx.x * 256 + threadIdx.x, q = i / (2 * BM * BN / 4), at = i % (2 * BM * BN / 4);
+    const int u = units - a.tail + q, nt = u / Mt2, row = at / (BN / 4);
+    const int m = (u % Mt2) * 2 * BM + row, n = nt * BN + (at % (BN / 4)) * 4;
+    if (m >= a.M) return;
+    const float4* ws = reinterpret_cast<const float4*>(a.ws) + (size_t)q * a.tail_splits * (2 * BM * BN / 4) + at;
+    float4 s = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+    for (int k = 0; k < a.tail_splits; ++k) {
+        const float4 v = __ldcg(ws + (size_t)k * (2 * BM * BN / 4));
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    const float4 f = factor4<FMT>(a.cs0, a.inv0, n);
+    const int sg = a.sig ? a.sig[m] : 0;
+    float4 d = make_float4(0, 0, 0, 0);
+    if (a.add) d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + n);
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)m * a.ldo + n) =
+        make_uint2(pack_bf16x2(scalbnf(s.x, -sg) * f.x + d.x, scalbnf(s.y, -sg) * f.y + d.y),
+                   pack_bf16x2(scalbnf(s.z, -sg) * f.z + d.z, scalbnf(s.w, -sg) * f.w + d.w));
 }
 
 // Dequantise-once prefill: every weight block of a projection -> its decoded
@@ -1382,7 +1446,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 // once: the pairs loop over the tiles).
 template <int FMT, bool PRE, bool EXT = false>
 cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const CUtensorMap& map2,
-                        const CUtensorMap& bmap2, const Args& a, int pairs_wanted, cudaStream_t s) {
+                        const CUtensorMap& bmap2, Args a, int pairs_wanted, int pairs_max, cudaStream_t s) {
     static int max_pairs = -1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -1406,8 +1470,26 @@ cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const C
         if (n < 1) return cudaErrorInvalidConfiguration;
         max_pairs = n;
     }
-    cfg.gridDim = dim3((unsigned)(2 * std::min(pairs_wanted, max_pairs)));
-    return cudaLaunchKernelEx(&cfg, gemm_pair_kernel<FMT, PRE, EXT>, map, bmap, map2, bmap2, a);
+    int pairs = std::min(pairs_wanted, max_pairs);
+    const bool split = EXT && a.tail && a.epi == kEpiPlain && a.ws;
+    a.tail = 0;
+    a.tail_splits = 1;
+    if (split) {
+        // tiles past the last whole round of all pairs, if they leave half of
+        // the pairs or more idle: split, at eight steps a share or more
+        const int units = ((a.M + 2 * BM - 1) / (2 * BM)) * (a.N / BN), all = std::min(max_pairs, pairs_max);
+        const int t = units % all, n = t ? std::min(all / t, (a.Kd / BK + a.ext) / 8) : 0;
+        if (n >= 2 && (size_t)t * n * 2 * BM * BN <= a.ws_elems) {
+            a.tail = t;
+            a.tail_splits = n;
+            pairs = all;
+        }
+    }
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_pair_kernel<FMT, PRE, EXT>, map, bmap, map2, bmap2, a);
+    if (e != cudaSuccess || !a.tail) return e;
+    tail_reduce_kernel<FMT><<<(unsigned)(a.tail * (2 * BM * BN / 4 / 256)), 256, 0, s>>>(a);
+    return cudaPeekAtLastError();
 }
 
 template <int FMT, bool PRE, bool EXT = false>
@@ -1566,6 +1648,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     if (P.fmt == kFP8 && (!P.cs0 || (P.interleaved && !P.cs1))) return cudaErrorInvalidValue;
     a.sig = bf ? nullptr : L.sig;
     a.f16 = L.f16 ? 1 : 0;
+    a.tail = L.split_tail ? 1 : 0;  // launch_pair plans it
     a.ext = L.ext;
     a.out = L.out;
     a.ldo = L.epi == kEpiSwiGLU ? P.N / 2 : (L.epi == kEpiRaw && P.interleaved ? P.N / 2 : P.N);
@@ -1579,7 +1662,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.gc0 = L.gc0;
     a.gc1 = L.gc1;
     a.out_lo = L.out_lo;
-    const bool grad = L.epi == kEpiSwiGLUGrad, ext = L.add || L.gu_g || grad || L.ext || (dq && L.f16);
+    const bool grad = L.epi == kEpiSwiGLUGrad, ext = L.add || L.gu_g || grad || L.ext || (dq && (L.f16 || L.split_tail));
     if (L.ext && (!L.pair || !dq || L.f16 || !L.ext_a || !L.ext_b)) return cudaErrorInvalidValue;
     if (ext && (L.epi == kEpiRaw || (L.pair && !dq) || L.ldadd % 4 || (grad && (!L.gu_g || L.ncols > P.N))))
         return cudaErrorInvalidValue;
@@ -1611,8 +1694,8 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
         if (L.M < kPairMinM) return cudaErrorInvalidValue;
         const int pairs = std::min(((L.M + 2 * BM - 1) / (2 * BM)) * (P.N / BN), std::max(num_sms, 2) / 2);
         if (!dq)
-            return P.fmt == kFP8 ? launch_pair<kFP8, false>(map, map, map, map, a, pairs, s)
-                                 : launch_pair<kNVFP4, false>(map, map, map, map, a, pairs, s);
+            return P.fmt == kFP8 ? launch_pair<kFP8, false>(map, map, map, map, a, pairs, std::max(num_sms, 2) / 2, s)
+                                 : launch_pair<kNVFP4, false>(map, map, map, map, a, pairs, std::max(num_sms, 2) / 2, s);
         // the decoded images as rows of 128 bytes, 128-row boxes (a CTA's
         // half of a k-step's image), no swizzle (the images carry it)
         CUtensorMap bmap;
@@ -1624,8 +1707,8 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
         if (!ext)
-            return P.fmt == kFP8 ? launch_pair<kFP8, true>(map, bmap, map, bmap, a, pairs, s)
-                                 : launch_pair<kNVFP4, true>(map, bmap, map, bmap, a, pairs, s);
+            return P.fmt == kFP8 ? launch_pair<kFP8, true>(map, bmap, map, bmap, a, pairs, std::max(num_sms, 2) / 2, s)
+                                 : launch_pair<kNVFP4, true>(map, bmap, map, bmap, a, pairs, std::max(num_sms, 2) / 2, s);
         CUtensorMap map2 = map, bmap2 = bmap;
         if (a.ext) {  // the adapters' steps: the same boxes over their own arrays
             const cuuint64_t edims[2] = {(cuuint64_t)a.ext * BK, (cuuint64_t)L.M};
@@ -1639,8 +1722,8 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
                 return cudaErrorInvalidValue;
         }
-        return P.fmt == kFP8 ? launch_pair<kFP8, true, true>(map, bmap, map2, bmap2, a, pairs, s)
-                             : launch_pair<kNVFP4, true, true>(map, bmap, map2, bmap2, a, pairs, s);
+        return P.fmt == kFP8 ? launch_pair<kFP8, true, true>(map, bmap, map2, bmap2, a, pairs, std::max(num_sms, 2) / 2, s)
+                             : launch_pair<kNVFP4, true, true>(map, bmap, map2, bmap2, a, pairs, std::max(num_sms, 2) / 2, s);
     }
     const int grid = std::min(tiles0 * a.splits, std::max(num_sms, 1));
     return P.fmt == kFP8 ? launch_fmt<kFP8>(map, a, ext, grid, s) : launch_fmt<kNVFP4>(map, a, ext, grid, s);

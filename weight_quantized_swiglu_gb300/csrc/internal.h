@@ -205,6 +205,7 @@ struct GemmLaunch {
     const float* gc0 = nullptr;
     const float* gc1 = nullptr;
     bool f16 = false;            // dequantise-once: images in fp16, activations prescaled to fp16 (into a16)
+    bool split_tail = false;     // CTA pairs, plain: the last tiles may be split over the contraction (into ws)
     int ext = 0;                 // CTA pairs: further contraction steps of 64, bf16: activations [M][64 ext]
     const void* ext_a = nullptr; // and stage images [N / 256][ext] (low-rank adapters)
     const void* ext_b = nullptr;

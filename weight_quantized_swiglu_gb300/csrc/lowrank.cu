@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kThr) expand_kernel(const LrExpand a) {
 
 // ---------------------------------------------------------------------------
 // z^T v over the tokens (the words of z in turn): a CTA takes 128 columns of z
-// (32 a warp) and NC of v; the tokens are split over the CTAs of a cluster. v in two words (2^-17): the gradients are bf16.
+// (32 a warp) and the NC of v; the tokens are split over the CTAs of a cluster;
+// one launch takes all gradients of an adapter, tile after tile. v in two words (2^-17): the gradients are bf16.
 // ---------------------------------------------------------------------------
 constexpr int kGD = 128;
 template <int NC>
@@ -409,18 +410,21 @@ struct GradSmem {
 };
 
 template <int NC>
-__global__ void __launch_bounds__(kThr) tokgrad_kernel(const LrTokGrad a) {
+__global__ void __launch_bounds__(kThr) tokgrad_kernel(const __grid_constant__ LrTokGrads jobs) {
     using S = GradSmem<NC>;
     extern __shared__ __align__(128) uint8_t smem[];
     pdl_launch_dependents();
     pdl_wait();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, z = blockIdx.z;
-    const int d0 = blockIdx.x * kGD;
+    int tile = blockIdx.x, job = 0;
+    while (tile >= jobs.tiles[job]) tile -= jobs.tiles[job++];
+    const LrTokGrad& a = jobs.job[job];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int d0 = tile * kGD;
     const int one = (a.M + 63) / 64, steps = a.x_lo ? 2 * one : one;
     const int s0 = (int)((long)steps * blockIdx.y / gridDim.y), s1 = (int)((long)steps * (blockIdx.y + 1) / gridDim.y);
-    const __nv_bfloat16* x = a.x + (size_t)z * a.x_z + d0;
+    const __nv_bfloat16* x = a.x + d0;
     const ptrdiff_t lo = a.x_lo ? a.x_lo - a.x : 0;
-    const __nv_bfloat16* v = a.v + z * NC;
+    const __nv_bfloat16* v = a.v;
     const uint32_t base = smem_u32(smem);
     auto load = [&](int step, int stage) {
         const uint32_t sx = base + stage * S::Stage, sv = sx + S::X;
@@ -486,14 +490,14 @@ __global__ void __launch_bounds__(kThr) tokgrad_kernel(const LrTokGrad a) {
     constexpr int kPitch = NC + 4;
     static_assert(kGD * kPitch * 4 <= S::Bytes, "the tile takes the stages' place");
     __syncthreads();
-    float* tile = reinterpret_cast<float*>(smem);  // [column of z][column of v]
+    float* sums = reinterpret_cast<float*>(smem);  // [column of z][column of v]
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < NC / 8; ++j)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                *reinterpret_cast<float2*>(tile + (warp * 32 + h * 16 + g + 8 * e) * kPitch + j * 8 + 2 * t) =
+                *reinterpret_cast<float2*>(sums + (warp * 32 + h * 16 + g + 8 * e) * kPitch + j * 8 + 2 * t) =
                     make_float2(acc[h][j][2 * e], acc[h][j][2 * e + 1]);
     if (ns > 1) cluster_sync();
     else __syncthreads();
@@ -505,21 +509,18 @@ __global__ void __launch_bounds__(kThr) tokgrad_kernel(const LrTokGrad a) {
         const int d = d0 + row;
         if (d >= a.D) continue;
         const uint32_t at = base + (row * kPitch + col) * 4;
-        const float4 s4 = ns > 1 ? sum_cluster(at, ns) : *reinterpret_cast<const float4*>(tile + row * kPitch + col);
+        const float4 s4 = ns > 1 ? sum_cluster(at, ns) : *reinterpret_cast<const float4*>(sums + row * kPitch + col);
         const float s[4] = {s4.x, s4.y, s4.z, s4.w};
         if (a.rows_d) {
-            if (!a.out[z]) continue;
-            const float f = a.div[z] ? a.div[z][d] : 1.0f;
+            const float f = a.div ? a.div[d] : 1.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if (col + e < a.r)
-                    a.out[z][(size_t)d * a.r + col + e] = __float2bfloat16_rn(a.div[z] ? s[e] / f : s[e] * a.mul[z]);
+                    a.out[(size_t)d * a.r + col + e] = __float2bfloat16_rn(a.div ? s[e] / f : s[e] * a.mul);
         } else {
-            const int part = col / a.Rp, j = col % a.Rp;
-            if (!a.out[part]) continue;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (j + e < a.r) a.out[part][(size_t)(j + e) * a.D + d] = __float2bfloat16_rn(s[e] * a.mul[part]);
+                if (col + e < a.r) a.out[(size_t)(col + e) * a.D + d] = __float2bfloat16_rn(s[e] * a.mul);
         }
     }
     if (ns > 1) cluster_sync();
@@ -820,7 +821,7 @@ cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, i
 }
 
 template <int NC>
-static cudaError_t tokgrad_t(const LrTokGrad& a, dim3 grid, cudaStream_t s) {
+static cudaError_t tokgrad_t(const LrTokGrads& a, dim3 grid, cudaStream_t s) {
     static bool attr = false;
     if (!attr) {
         const cudaError_t e = cudaFuncSetAttribute(tokgrad_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -830,14 +831,15 @@ static cudaError_t tokgrad_t(const LrTokGrad& a, dim3 grid, cudaStream_t s) {
     }
     return launch_pdl(tokgrad_kernel<NC>, grid, kThr, GradSmem<NC>::Bytes, a, s, (int)grid.y);
 }
-cudaError_t launch_lr_tokgrad(const LrTokGrad& a, int nc, int zs, int num_sms, cudaStream_t s) {
-    const int tiles = (a.D + kGD - 1) / kGD, splits = lr_splits(tiles * zs, (a.M + 63) / 64, num_sms);
-    const dim3 grid(tiles, splits, zs);
+cudaError_t launch_lr_tokgrad(LrTokGrads& a, int nc, int num_sms, cudaStream_t s) {
+    int tiles = 0;
+    for (int i = 0; i < a.count; ++i) tiles += a.tiles[i] = (a.job[i].D + kGD - 1) / kGD;
+    if (!tiles) return cudaSuccess;
+    const dim3 grid(tiles, lr_splits(tiles, (a.job[0].M + 63) / 64, 2 * num_sms), 1);
     switch (nc) {
         case 16: return tokgrad_t<16>(a, grid, s);
         case 32: return tokgrad_t<32>(a, grid, s);
         case 64: return tokgrad_t<64>(a, grid, s);
-        case 128: return tokgrad_t<128>(a, grid, s);
     }
     return cudaErrorInvalidValue;
 }

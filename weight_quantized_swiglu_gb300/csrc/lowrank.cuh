@@ -80,21 +80,26 @@ struct LrFew {
     float factor_all = 1.0f;
 };
 
-// out = z^T v over the tokens of one adapter, in bf16: with rows_d, out[z][d][r]
-// = B's gradient (part z of x and v); else out[j / Rp][j % Rp][d] = A's.
+// out = z^T v over the tokens of one adapter, in bf16: with rows_d, [D][r]
+// (a B's gradient), else [r][D] (an A's).
 struct LrTokGrad {
-    const __nv_bfloat16* x = nullptr;  // [M][ldx], D columns from z * x_z on
+    const __nv_bfloat16* x = nullptr;  // [M][ldx], D columns
     const __nv_bfloat16* x_lo = nullptr;  // optional second word of x
-    size_t ldx = 0, x_z = 0;
+    size_t ldx = 0;
     int D = 0, M = 0;
-    const __nv_bfloat16* v = nullptr;  // words of [M][ldv], columns z * NC on
+    const __nv_bfloat16* v = nullptr;  // [M][ldv], words v_word columns apart
     size_t v_word = 0;
     int ldv = 0;
     bool rows_d = false;
-    int r = 0, Rp = 0;
-    __nv_bfloat16* out[2] = {nullptr, nullptr};
-    const float* div[2] = {nullptr, nullptr};  // rows_d: the row's divisor; else mul
-    float mul[2] = {1.0f, 1.0f};
+    int r = 0;
+    __nv_bfloat16* out = nullptr;
+    const float* div = nullptr;  // rows_d: the row's divisor; else mul
+    float mul = 1.0f;
+};
+struct LrTokGrads {
+    LrTokGrad job[6];
+    int count = 0;
+    int tiles[6] = {0, 0, 0, 0, 0, 0};  // set by the launch
 };
 
 struct LrSwiGLU {
@@ -139,7 +144,7 @@ struct LrImage {
 cudaError_t launch_lr_image(const LrImage& a, cudaStream_t s);
 
 int lr_max_tiles(int M, int slots);
-cudaError_t launch_lr_tokgrad(const LrTokGrad& a, int nc, int zs, int num_sms, cudaStream_t s);
+cudaError_t launch_lr_tokgrad(LrTokGrads& a, int nc, int num_sms, cudaStream_t s);
 cudaError_t launch_lr_shrink(const LrShrink& a, int nc, bool trans, int tiles, int zs, int num_sms, cudaStream_t s);
 cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, int zs, cudaStream_t s);
 cudaError_t launch_lr_shrink_few(const LrFew& a, int M, cudaStream_t s);
