@@ -8,8 +8,8 @@
 //   p = p (1 - lr wd) - lr / (1 - b1^t) * m / ( sqrt(v) / sqrt(1 - b2^t) + eps )
 // All of it in fp32, each operation of a state rounded once and none contracted,
 // so that a state does not depend on how the compiler fuses a product and a sum;
-// the update's quotient is the fast one (two units of the last place of a term
-// of the size of lr). p is
+// the update's root and quotient are the fast ones (a few units of the last
+// place of a term of the size of lr). p is
 // the fp32 master where there is one (then param = bf16(p) is written beside
 // it), else the parameter itself.
 //
@@ -122,41 +122,62 @@ QMLP_DEV uint32_t e4m3x2(float a, float b) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
     return r;
 }
-// The block's codes: v / s, s = max|v| / 448 over the warp (zero: codes zero).
-// FLOOR: what is above zero keeps at least the smallest code.
-template <bool VEC, bool FLOOR>
-QMLP_DEV void store8_codes(uint8_t* p, float* scale, int n, const float (&v)[kPer]) {
+QMLP_DEV float sqrt_fast(float v) {  // within 2^-23
+    float r;
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// The block's codes of w: w / s, s = max|w| / 448 over the warp (zero: codes
+// zero). ROOT: w = sqrt(v), of which the correctly rounded one counts (its
+// maximum is the root of v's), and what is above zero keeps at least the
+// smallest code.
+//
+// The quotients are products with the reciprocal, and the roots fast ones: five
+// units of the last place off at most. Only where that can reach the middle of
+// two codes (or under the normal codes, whose middles lie elsewhere) are they
+// taken again, correctly rounded. A lane asks that once for its eight elements.
+// (69M elements, 384 tensors: 229 us with every root and quotient rounded, 212
+// with these.)
+template <bool VEC, bool ROOT>
+QMLP_DEV void store8_codes(uint8_t* p, float* scale, int n, const float (&v)[kPer], const float (&w)[kPer]) {
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) top = fmaxf(top, fabsf(v[i]));
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // bits order as the floats do
-    const float s = __fmul_rn(top, 1.0f / 448.0f);
-    // v / s, correctly rounded where that can matter: a product with the
-    // reciprocal is within two units of the last place, so only a quotient that
-    // close to the middle of two codes (or under the normal codes, whose middles
-    // lie elsewhere) is divided out. (69M elements, both states: 229 -> 190 us.)
-    const float rs = __frcp_rn(s);
+    if (ROOT) top = __fsqrt_rn(top);
+    const float s = __fmul_rn(top, 1.0f / 448.0f), rs = __frcp_rn(s);
     float q[kPer];
+    bool again = !(s > 0.0f);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        q[i] = __fmul_rn(v[i], rs);
+        q[i] = __fmul_rn(w[i], rs);
         const uint32_t b = __float_as_uint(q[i]);
-        // normal codes keep 3 of 23 mantissa bits: the middle is 0x80000 of the other 20
-        if (((b + 4u - 0x80000u) & 0xFFFFFu) <= 8u || !(fabsf(q[i]) >= 0.016f && fabsf(q[i]) < 449.0f))
-            // no scale: zeros (and values under 448 of the smallest subnormal), or a NaN, which stays one
-            q[i] = s > 0.0f ? __fdiv_rn(v[i], s) : v[i];
-        if (FLOOR && s > 0.0f && q[i] > 0.0f) q[i] = fmaxf(q[i], 0.001953125f);
+        // normal codes (from 2^-6) keep 3 of 23 mantissa bits: the middle is
+        // 0x80000 of the other 20. Zero is itself; 0.016 has room for the error
+        again |= ((b + 8u - 0x80000u) & 0xFFFFFu) <= 16u || !(fabsf(q[i]) >= 0.016f || q[i] == 0.0f);
     }
-    uint32_t w[2];
+    if (again) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16;
+        for (int i = 0; i < kPer; ++i) {
+            const float x = ROOT ? __fsqrt_rn(v[i]) : v[i];
+            // no scale: zeros (and values under 448 of the smallest subnormal), or a NaN, which stays one
+            q[i] = s > 0.0f ? __fdiv_rn(x, s) : x;
+        }
+    }
+    if (ROOT && s > 0.0f)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) q[i] = q[i] > 0.0f ? fmaxf(q[i], 0.001953125f) : q[i];
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) c[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16;
     if ((threadIdx.x & 31) == 0) *scale = s;
     if (VEC) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+            if (i < n) p[i] = (uint8_t)(c[i >> 2] >> (8 * (i & 3)));
     }
 }
 
@@ -185,15 +206,15 @@ QMLP_DEV void step8(const AdamWChunk& c, const AdamWStep& k, int at, int n) {
         const float gs = __fmul_rn(g[i], k.gscale);
         m[i] = __fadd_rn(__fmul_rn(m[i], k.b1), __fmul_rn(gs, k.omb1));
         v[i] = __fadd_rn(__fmul_rn(v[i], k.b2), __fmul_rn(__fmul_rn(gs, gs), k.omb2));
-        r[i] = __fsqrt_rn(v[i]);
+        r[i] = sqrt_fast(v[i]);
         const float d = __fadd_rn(__fmul_rn(r[i], k.rbc2), k.eps);
         p[i] = __fsub_rn(__fmul_rn(p[i], k.decay), __fmul_rn(__fdividef(m[i], d), k.step));
     }
     if (MASTER) store8<VEC>(master, n, p);
     store8<VEC>(param, n, p);
     if (S8) {
-        store8_codes<VEC, false>(static_cast<uint8_t*>(c.m) + at, c.m_scale + blk, n, m);
-        store8_codes<VEC, true>(static_cast<uint8_t*>(c.v) + at, c.v_scale + blk, n, r);
+        store8_codes<VEC, false>(static_cast<uint8_t*>(c.m) + at, c.m_scale + blk, n, m, m);
+        store8_codes<VEC, true>(static_cast<uint8_t*>(c.v) + at, c.v_scale + blk, n, v, r);
     } else {
         store8<VEC>(static_cast<float*>(c.m) + at, n, m);
         store8<VEC>(static_cast<float*>(c.v) + at, n, v);
@@ -201,7 +222,10 @@ QMLP_DEV void step8(const AdamWChunk& c, const AdamWStep& k, int at, int n) {
 }
 
 template <typename P, typename G, bool S8, bool MASTER>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const AdamWChunk* __restrict__ chunks, const AdamWStep k) {
+// Five CTAs an SM (8-bit states: 212 us with four, 202 with five, 209 with six;
+// the next chunk's words prefetched into registers: 243 and more, the issue slots
+// and the warps that hide the loads' latency count, not one warp's loads).
+__global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const AdamWChunk* __restrict__ chunks, const AdamWStep k) {
     const AdamWChunk c = chunks[blockIdx.x];
     const int at = threadIdx.x * kPer;  // within the chunk
     if ((at & ~(kAdamWBlock - 1)) >= c.n) return;  // the whole warp's block is past the end
