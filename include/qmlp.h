@@ -220,8 +220,9 @@ qmlp_status qmlp_debug_set_wait(qmlp_t* h, uint64_t limit_ns, int withhold_last_
 
 /*
  * Index checks. A library built with -DQMLP_DEBUG_BOUNDS (libqmlp_bounds.so;
- * the default build compiles the checks away) checks, in every kernel, the
- * index of each global access whose address comes from layout arithmetic or
+ * the default build compiles the checks away) checks, in every kernel of the
+ * dense block's and the routed experts' forward calls (not in those that
+ * adapters, training and AdamW add), the index of each global access whose address comes from layout arithmetic or
  * runtime data (weight-bank blocks and records, partial buffers, outputs,
  * route lists) against the size of its buffer. A failed check never traps:
  * the kernel records the first one and skips the access (a load reads zero,

@@ -401,7 +401,19 @@ qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M
     // fork follows everything already on s, so the previous call's down
     // GEMM has finished reading wdec2)
     const bool fork = g.wdec && stages == 3 && h->wdec2 && h->side;
-    if (fork && (launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s) != cudaSuccess ||
+    if (fork && ex) {
+        // with adapters, gate/up's images too, beside the adapters' products
+        if (cudaEventRecord(h->ev_fork, s) != cudaSuccess || cudaStreamWaitEvent(h->side, h->ev_fork, 0) != cudaSuccess ||
+            launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, h->side) != cudaSuccess ||
+            cudaEventRecord(ex->ev, h->side) != cudaSuccess ||
+            launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, h->side) != cudaSuccess ||
+            cudaEventRecord(h->ev_join, h->side) != cudaSuccess || ex->before(s) != cudaSuccess ||
+            cudaStreamWaitEvent(s, ex->ev, 0) != cudaSuccess)
+            return QMLP_ERR_CUDA;
+    } else if (ex && ex->before(s) != cudaSuccess) {
+        return QMLP_ERR_CUDA;
+    }
+    if (fork && !ex && (launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s) != cudaSuccess ||
                  cudaEventRecord(h->ev_fork, s) != cudaSuccess ||
                  cudaStreamWaitEvent(h->side, h->ev_fork, 0) != cudaSuccess ||
                  launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, h->side) != cudaSuccess ||

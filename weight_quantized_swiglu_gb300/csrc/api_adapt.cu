@@ -26,6 +26,7 @@ struct qmlp_lora_s {
     int* perm = nullptr;
     int4* tiles = nullptr;
     int* n_tiles = nullptr;
+    cudaEvent_t ev = nullptr;
     Owner mem;
 };
 
@@ -82,6 +83,16 @@ __global__ void __launch_bounds__(256) factors_kernel(const float* g, const floa
     const bool big = !(fabsf(f) < kLeastFactor);
     eff[i] = big ? f : 1.0f;
     row[i] = big ? 1.0f : f;
+}
+
+// No C++ exception leaves a C entry: what the host cannot allocate is OOM.
+template <typename F>
+qmlp_status guarded(F&& f) {
+    try {
+        return f();
+    } catch (...) {
+        return QMLP_ERR_OOM;
+    }
 }
 
 bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
@@ -270,52 +281,57 @@ extern "C" {
 // low-rank adapters
 // ---------------------------------------------------------------------------
 qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_rank, qmlp_stream_t stream) {
-    if (!out) return QMLP_ERR_INVALID_ARG;
-    *out = nullptr;
-    if (!h) return QMLP_ERR_INVALID_ARG;
-    if (slots < 1 || slots > kLrMaxSlots || max_rank < 1 || max_rank > kLrMaxRank) return QMLP_ERR_SHAPE;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    qmlp_lora_t* l = new qmlp_lora_t();
-    l->h = h;
-    l->slots = slots;
-    l->max_rank = max_rank;
-    l->Rp = max_rank <= 16 ? 16 : max_rank <= 32 ? 32 : 64;
-    const size_t K = h->K, I = h->I, R = l->Rp, S = slots, M = h->max_M;
-    const size_t tiles = (size_t)lr_max_tiles(h->max_M, slots);
-    cudaError_t e = cudaSuccess;
-    auto get = [&](auto** p, size_t count, bool zero) {
-        if (e != cudaSuccess) return;
-        const size_t bytes = count * sizeof(**p);
-        if ((e = l->mem.alloc(reinterpret_cast<void**>(p), bytes)) == cudaSuccess && zero) e = cudaMemsetAsync(*p, 0, bytes, s);
-    };
-    get(&l->a_gu, S * 2 * R * K, true);
-    get(&l->a_d, S * R * I, true);
-    get(&l->b_gu, S * 2 * I * R, true);
-    get(&l->b_d, S * K * R, true);
-    get(&l->scale, S, true);
-    get(&l->rank, S, true);
-    get(&l->v, (size_t)kLrFew * 2 * R, false);
-    get(&l->vw, kLrWords * M * 2 * R, false);
-    get(&l->y, M * std::max(2 * I, K), false);
-    get(&l->raw, (size_t)kMaxGemvM * (2 * I + K), false);
-    get(&l->vd, (size_t)std::max(1, h->sp.G) * kMaxGemvM * R, false);
-    get(&l->perm, M, false);
-    get(&l->tiles, tiles, false);
-    get(&l->n_tiles, 1, true);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) {
-        cudaStreamSynchronize(s);
-        l->mem.release();
-        delete l;
-        return from_cuda(e);
-    }
-    *out = l;
-    return QMLP_OK;
+    return guarded([&]() -> qmlp_status {
+        if (!out) return QMLP_ERR_INVALID_ARG;
+        *out = nullptr;
+        if (!h) return QMLP_ERR_INVALID_ARG;
+        if (slots < 1 || slots > kLrMaxSlots || max_rank < 1 || max_rank > kLrMaxRank) return QMLP_ERR_SHAPE;
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        qmlp_lora_t* l = new qmlp_lora_t();
+        l->h = h;
+        l->slots = slots;
+        l->max_rank = max_rank;
+        l->Rp = max_rank <= 16 ? 16 : max_rank <= 32 ? 32 : 64;
+        const size_t K = h->K, I = h->I, R = l->Rp, S = slots, M = h->max_M;
+        const size_t tiles = (size_t)lr_max_tiles(h->max_M, slots);
+        cudaError_t e = cudaSuccess;
+        auto get = [&](auto** p, size_t count, bool zero) {
+            if (e != cudaSuccess) return;
+            const size_t bytes = count * sizeof(**p);
+            if ((e = l->mem.alloc(reinterpret_cast<void**>(p), bytes)) == cudaSuccess && zero) e = cudaMemsetAsync(*p, 0, bytes, s);
+        };
+        get(&l->a_gu, S * 2 * R * K, true);
+        get(&l->a_d, S * R * I, true);
+        get(&l->b_gu, S * 2 * I * R, true);
+        get(&l->b_d, S * K * R, true);
+        get(&l->scale, S, true);
+        get(&l->rank, S, true);
+        get(&l->v, (size_t)kLrFew * 2 * R, false);
+        get(&l->vw, kLrWords * M * 2 * R, false);
+        get(&l->y, M * std::max(2 * I, K), false);
+        get(&l->raw, (size_t)kMaxGemvM * (2 * I + K), false);
+        get(&l->vd, (size_t)std::max(1, h->sp.G) * kMaxGemvM * R, false);
+        get(&l->perm, M, false);
+        get(&l->tiles, tiles, false);
+        get(&l->n_tiles, 1, true);
+        if (e == cudaSuccess) e = cudaEventCreateWithFlags(&l->ev, cudaEventDisableTiming);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        if (e != cudaSuccess) {
+            cudaStreamSynchronize(s);
+            if (l->ev) cudaEventDestroy(l->ev);
+            l->mem.release();
+            delete l;
+            return from_cuda(e);
+        }
+        *out = l;
+        return QMLP_OK;
+    });
 }
 
 void qmlp_lora_destroy(qmlp_lora_t* l) {
     if (!l) return;
     cudaDeviceSynchronize();
+    cudaEventDestroy(l->ev);
     l->mem.release();
     delete l;
 }
@@ -332,40 +348,45 @@ qmlp_status qmlp_lora_set(qmlp_lora_t* l, int slot, const qmlp_adapter* a, qmlp_
 
 qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids, int M, void* out,
                               qmlp_stream_t stream) {
-    if (!l || !x || !ids || !out) return QMLP_ERR_INVALID_ARG;
-    qmlp_t* h = l->h;
-    if (M < 1 || M > h->max_M) return QMLP_ERR_SHAPE;
-    if (!aligned16(x) || !aligned16(out) || !aligned(ids, 4)) return QMLP_ERR_ALIGNMENT;
-    const size_t xb = (size_t)M * h->K * 2, ab = (size_t)h->max_M * h->I * 2;
-    if (overlaps(out, xb, x, xb) || overlaps(out, xb, ids, (size_t)M * 4) || overlaps(out, xb, h->act, ab))
-        return QMLP_ERR_ALIAS;
-    if (fault("launch")) return QMLP_ERR_CUDA;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (!(h->has_gemm && M >= gemm_min_m(h))) {
-        const int block = h->sp.G ? split_max_m(h) : kMaxGemvM;
-        for (int m0 = 0; m0 < M; m0 += block) {
-            const qmlp_status st =
-                lora_block(l, static_cast<const uint8_t*>(x) + (size_t)m0 * h->K * 2, ids + m0, std::min(block, M - m0),
-                           static_cast<uint8_t*>(out) + (size_t)m0 * h->K * 2, s);
-            if (st != QMLP_OK) return st;
+    return guarded([&]() -> qmlp_status {
+        if (!l || !x || !ids || !out) return QMLP_ERR_INVALID_ARG;
+        qmlp_t* h = l->h;
+        if (M < 1 || M > h->max_M) return QMLP_ERR_SHAPE;
+        if (!aligned16(x) || !aligned16(out) || !aligned(ids, 4)) return QMLP_ERR_ALIGNMENT;
+        const size_t xb = (size_t)M * h->K * 2, ab = (size_t)h->max_M * h->I * 2;
+        if (overlaps(out, xb, x, xb) || overlaps(out, xb, ids, (size_t)M * 4) || overlaps(out, xb, h->act, ab))
+            return QMLP_ERR_ALIAS;
+        if (fault("launch")) return QMLP_ERR_CUDA;
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        if (!(h->has_gemm && M >= gemm_min_m(h))) {
+            const int block = h->sp.G ? split_max_m(h) : kMaxGemvM;
+            for (int m0 = 0; m0 < M; m0 += block) {
+                const qmlp_status st =
+                    lora_block(l, static_cast<const uint8_t*>(x) + (size_t)m0 * h->K * 2, ids + m0, std::min(block, M - m0),
+                               static_cast<uint8_t*>(out) + (size_t)m0 * h->K * 2, s);
+                if (st != QMLP_OK) return st;
+            }
+            return QMLP_OK;
         }
-        return QMLP_OK;
-    }
-    const bool few = M <= kLrFew;
-    auto terms = [&](bool down, const void* z, cudaStream_t st) {
-        cudaError_t e = few ? lora_shrink_few(l, down, z, ids, M, st) : lora_shrink(l, down, z, M, st);
-        if (e == cudaSuccess)
-            e = few ? lora_expand_few(l, down, ids, M, nullptr, nullptr, st) : lora_expand(l, down, M, st);
-        return e;
-    };
-    if (!few && launch_lr_plan(ids, M, l->slots, l->rank, l->perm, l->tiles, l->n_tiles, s) != cudaSuccess)
-        return QMLP_ERR_CUDA;
-    if (terms(false, x, s) != cudaSuccess) return QMLP_ERR_CUDA;
-    GemmTerms t;
-    t.add = l->y;
-    t.add_down = l->y;
-    t.between = [&](cudaStream_t st) { return terms(true, h->act, st); };
-    return run_gemm(h, QMLP_PATH_AUTO, 3, x, M, out, s, nullptr, &t);
+        const bool few = M <= kLrFew;
+        auto terms = [&](bool down, const void* z, cudaStream_t st) {
+            cudaError_t e = few ? lora_shrink_few(l, down, z, ids, M, st) : lora_shrink(l, down, z, M, st);
+            if (e == cudaSuccess)
+                e = few ? lora_expand_few(l, down, ids, M, nullptr, nullptr, st) : lora_expand(l, down, M, st);
+            return e;
+        };
+        GemmTerms t;
+        t.ev = l->ev;
+        t.before = [&](cudaStream_t st) {
+            const cudaError_t e =
+                few ? cudaSuccess : launch_lr_plan(ids, M, l->slots, l->rank, l->perm, l->tiles, l->n_tiles, st);
+            return e == cudaSuccess ? terms(false, x, st) : e;
+        };
+        t.add = l->y;
+        t.add_down = l->y;
+        t.between = [&](cudaStream_t st) { return terms(true, h->act, st); };
+        return run_gemm(h, QMLP_PATH_AUTO, 3, x, M, out, s, nullptr, &t);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -750,79 +771,81 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
 }  // extern "C++"
 
 qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_stream_t stream) {
-    if (!out) return QMLP_ERR_INVALID_ARG;
-    *out = nullptr;
-    if (!h) return QMLP_ERR_INVALID_ARG;
-    if (!h->has_gemm || !h->wdec || !h->side || max_rank < 1 || max_rank > kLrMaxRank) return QMLP_ERR_SHAPE;
-    for (int i = 0; i < 3; ++i)
-        if (h->fmt == kNVFP4 && !(fabsf(h->gv[i].inv_g) >= kLeastFactor)) return QMLP_ERR_INVALID_ARG;
-    qmlp_train_t* t = new qmlp_train_t();
-    t->h = h;
-    qmlp_status st = qmlp_lora_create(&t->l, h, 1, max_rank, stream);
-    if (st != QMLP_OK) {
-        delete t;
-        return st;
-    }
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const size_t I = h->I, K = h->K, M = h->max_M, R = t->l->Rp;
-    t->img_t_bytes = gemm_decoded_t_bytes((int)K, (int)I);
-    cudaError_t e = cudaSuccess;
-    auto get = [&](auto** p, size_t count) {
-        if (e == cudaSuccess) e = t->mem.alloc(reinterpret_cast<void**>(p), count * sizeof(**p));
-    };
-    get(&t->img_t, t->img_t_bytes);
-    get(&t->bq, 4 * I * R);
-    get(&t->dgu, M * 2 * I);
-    get(&t->dgu_lo, std::min<size_t>(M, kTwoWordM) * 2 * I);
-    get(&t->dv, words_room(M, 2 * (int)R));
-    get(&t->dvd, words_room(M, (int)R));
-    t->T = h->fmt == kFP8 ? 3 : 2;
-    // gate/up: I / 128 tiles, or K / 256 of the transposed; down: K / 256 or I / 256
-    const size_t tg = std::max(I / 128, K / 256), td = std::max(K / 256, (I + 255) / 256);
-    get(&t->img_gu, tg * (size_t)(word_ld(2 * (int)R, 3) / 64) * 32768);
-    get(&t->img_d, td * (size_t)(word_ld((int)R, 3) / 64) * 32768);
-    if (h->fmt == kFP8) {
-        get(&t->eff, 2 * I);
-        get(&t->row, 2 * I);
-        if (e == cudaSuccess) {
-            factors_kernel<<<(unsigned)((2 * I + 255) / 256), 256, 0, s>>>(h->gv[0].chs, h->gv[1].chs, (int)I, t->eff,
-                                                                          t->row);
-            e = cudaPeekAtLastError();
+    return guarded([&]() -> qmlp_status {
+        if (!out) return QMLP_ERR_INVALID_ARG;
+        *out = nullptr;
+        if (!h) return QMLP_ERR_INVALID_ARG;
+        if (!h->has_gemm || !h->wdec || !h->side || max_rank < 1 || max_rank > kLrMaxRank) return QMLP_ERR_SHAPE;
+        for (int i = 0; i < 3; ++i)
+            if (h->fmt == kNVFP4 && !(fabsf(h->gv[i].inv_g) >= kLeastFactor)) return QMLP_ERR_INVALID_ARG;
+        qmlp_train_t* t = new qmlp_train_t();
+        t->h = h;
+        qmlp_status st = qmlp_lora_create(&t->l, h, 1, max_rank, stream);
+        if (st != QMLP_OK) {
+            delete t;
+            return st;
         }
-    }
-    if (e == cudaSuccess && h->fmt == kFP8) {
-        // e4m3 (at most 448) times a factor under fac_d, times 2^6: under 2^15
-        std::vector<float> f(K), fg(2 * I);
-        e = cudaMemcpyAsync(fg.data(), h->gv[0].chs, I * sizeof(float), cudaMemcpyDeviceToHost, s);
-        if (e == cudaSuccess) e = cudaMemcpyAsync(fg.data() + I, h->gv[1].chs, I * sizeof(float), cudaMemcpyDeviceToHost, s);
-        if (e == cudaSuccess) e = cudaMemcpyAsync(f.data(), h->gv[2].chs, K * sizeof(float), cudaMemcpyDeviceToHost, s);
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        const size_t I = h->I, K = h->K, M = h->max_M, R = t->l->Rp;
+        t->img_t_bytes = gemm_decoded_t_bytes((int)K, (int)I);
+        cudaError_t e = cudaSuccess;
+        auto get = [&](auto** p, size_t count) {
+            if (e == cudaSuccess) e = t->mem.alloc(reinterpret_cast<void**>(p), count * sizeof(**p));
+        };
+        get(&t->img_t, t->img_t_bytes);
+        get(&t->bq, 4 * I * R);
+        get(&t->dgu, M * 2 * I);
+        get(&t->dgu_lo, std::min<size_t>(M, kTwoWordM) * 2 * I);
+        get(&t->dv, words_room(M, 2 * (int)R));
+        get(&t->dvd, words_room(M, (int)R));
+        t->T = h->fmt == kFP8 ? 3 : 2;
+        // gate/up: I / 128 tiles, or K / 256 of the transposed; down: K / 256 or I / 256
+        const size_t tg = std::max(I / 128, K / 256), td = std::max(K / 256, (I + 255) / 256);
+        get(&t->img_gu, tg * (size_t)(word_ld(2 * (int)R, 3) / 64) * 32768);
+        get(&t->img_d, td * (size_t)(word_ld((int)R, 3) / 64) * 32768);
+        if (h->fmt == kFP8) {
+            get(&t->eff, 2 * I);
+            get(&t->row, 2 * I);
+            if (e == cudaSuccess) {
+                factors_kernel<<<(unsigned)((2 * I + 255) / 256), 256, 0, s>>>(h->gv[0].chs, h->gv[1].chs, (int)I, t->eff,
+                                                                              t->row);
+                e = cudaPeekAtLastError();
+            }
+        }
+        if (e == cudaSuccess && h->fmt == kFP8) {
+            // e4m3 (at most 448) times a factor under fac_d, times 2^6: under 2^15
+            std::vector<float> f(K), fg(2 * I);
+            e = cudaMemcpyAsync(fg.data(), h->gv[0].chs, I * sizeof(float), cudaMemcpyDeviceToHost, s);
+            if (e == cudaSuccess) e = cudaMemcpyAsync(fg.data() + I, h->gv[1].chs, I * sizeof(float), cudaMemcpyDeviceToHost, s);
+            if (e == cudaSuccess) e = cudaMemcpyAsync(f.data(), h->gv[2].chs, K * sizeof(float), cudaMemcpyDeviceToHost, s);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+            for (float v : fg) t->steps = t->steps && fabsf(v) >= kLeastFactor;
+            for (float v : f) t->steps = t->steps && fabsf(v) >= kLeastFactor;
+            float top = 0.0f;
+            for (float v : f)
+                if (isfinite(v)) top = std::max(top, fabsf(v));
+            int ex = 0;
+            frexpf(top, &ex);
+            ex = std::max(-100, std::min(100, ex - 6));
+            t->fac_d = ldexpf(1.0f, ex);
+            for (float& v : f) v = ldexpf(v, -ex);
+            get(&t->mul_d, K);
+            if (e == cudaSuccess) e = cudaMemcpyAsync(t->mul_d, f.data(), K * sizeof(float), cudaMemcpyHostToDevice, s);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        }
+        if (e == cudaSuccess) e = cudaEventCreateWithFlags(&t->ev_img, cudaEventDisableTiming);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-        for (float v : fg) t->steps = t->steps && fabsf(v) >= kLeastFactor;
-        for (float v : f) t->steps = t->steps && fabsf(v) >= kLeastFactor;
-        float top = 0.0f;
-        for (float v : f)
-            if (isfinite(v)) top = std::max(top, fabsf(v));
-        int ex = 0;
-        frexpf(top, &ex);
-        ex = std::max(-100, std::min(100, ex - 6));
-        t->fac_d = ldexpf(1.0f, ex);
-        for (float& v : f) v = ldexpf(v, -ex);
-        get(&t->mul_d, K);
-        if (e == cudaSuccess) e = cudaMemcpyAsync(t->mul_d, f.data(), K * sizeof(float), cudaMemcpyHostToDevice, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
-    if (e == cudaSuccess) e = cudaEventCreateWithFlags(&t->ev_img, cudaEventDisableTiming);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e != cudaSuccess) {
-        cudaStreamSynchronize(s);
-        if (t->ev_img) cudaEventDestroy(t->ev_img);
-        qmlp_lora_destroy(t->l);
-        t->mem.release();
-        delete t;
-        return from_cuda(e);
-    }
-    *out = t;
-    return QMLP_OK;
+        if (e != cudaSuccess) {
+            cudaStreamSynchronize(s);
+            if (t->ev_img) cudaEventDestroy(t->ev_img);
+            qmlp_lora_destroy(t->l);
+            t->mem.release();
+            delete t;
+            return from_cuda(e);
+        }
+        *out = t;
+        return QMLP_OK;
+    });
 }
 
 void qmlp_train_destroy(qmlp_train_t* t) {
@@ -861,39 +884,41 @@ qmlp_status qmlp_train_forward(qmlp_train_t* t, const qmlp_adapter* adapter, con
 
 qmlp_status qmlp_train_backward(qmlp_train_t* t, const qmlp_adapter* adapter, const void* x, int M, const void* saved,
                                 const void* dout, void* dx, const qmlp_adapter* grads, qmlp_stream_t stream) {
-    if (!t || !x || !saved || !dout || !dx || (grads && !adapter)) return QMLP_ERR_INVALID_ARG;
-    const qmlp_status st = check_train(t, adapter, M);
-    if (st != QMLP_OK) return st;
-    if (!aligned16(x) || !aligned16(saved) || !aligned16(dout) || !aligned16(dx)) return QMLP_ERR_ALIGNMENT;
-    const size_t K = t->h->K, I = t->h->I, xb = (size_t)M * K * 2;
-    std::vector<Range> r;
-    auto add = [&](const void* p, size_t bytes, bool w) {
-        if (p) r.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, w});
-    };
-    add(x, xb, false);
-    add(dout, xb, false);
-    add(saved, saved_of(t, M, nullptr).bytes, false);
-    add(dx, xb, true);
-    if (adapter) {
-        const size_t rk = (size_t)adapter->rank * 2;
-        const size_t bytes[6] = {rk * K, rk * I, rk * K, rk * I, rk * I, rk * K};
-        const void* p[6] = {adapter->gate_a, adapter->gate_b, adapter->up_a, adapter->up_b, adapter->down_a, adapter->down_b};
-        for (int i = 0; i < 6; ++i) add(p[i], bytes[i], false);
-        if (grads) {
-            const void* g[6] = {grads->gate_a, grads->gate_b, grads->up_a, grads->up_b, grads->down_a, grads->down_b};
-            for (int i = 0; i < 6; ++i) {
-                if (g[i] && !p[i]) return QMLP_ERR_INVALID_ARG;
-                if (!aligned(g[i], 2)) return QMLP_ERR_ALIGNMENT;
-                add(g[i], bytes[i], true);
+    return guarded([&]() -> qmlp_status {
+        if (!t || !x || !saved || !dout || !dx || (grads && !adapter)) return QMLP_ERR_INVALID_ARG;
+        const qmlp_status st = check_train(t, adapter, M);
+        if (st != QMLP_OK) return st;
+        if (!aligned16(x) || !aligned16(saved) || !aligned16(dout) || !aligned16(dx)) return QMLP_ERR_ALIGNMENT;
+        const size_t K = t->h->K, I = t->h->I, xb = (size_t)M * K * 2;
+        std::vector<Range> r;
+        auto add = [&](const void* p, size_t bytes, bool w) {
+            if (p) r.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, w});
+        };
+        add(x, xb, false);
+        add(dout, xb, false);
+        add(saved, saved_of(t, M, nullptr).bytes, false);
+        add(dx, xb, true);
+        if (adapter) {
+            const size_t rk = (size_t)adapter->rank * 2;
+            const size_t bytes[6] = {rk * K, rk * I, rk * K, rk * I, rk * I, rk * K};
+            const void* p[6] = {adapter->gate_a, adapter->gate_b, adapter->up_a, adapter->up_b, adapter->down_a, adapter->down_b};
+            for (int i = 0; i < 6; ++i) add(p[i], bytes[i], false);
+            if (grads) {
+                const void* g[6] = {grads->gate_a, grads->gate_b, grads->up_a, grads->up_b, grads->down_a, grads->down_b};
+                for (int i = 0; i < 6; ++i) {
+                    if (g[i] && !p[i]) return QMLP_ERR_INVALID_ARG;
+                    if (!aligned(g[i], 2)) return QMLP_ERR_ALIGNMENT;
+                    add(g[i], bytes[i], true);
+                }
             }
         }
-    }
-    if (any_alias(r)) return QMLP_ERR_ALIAS;
-    if (fault("launch")) return QMLP_ERR_CUDA;
-    return train_backward(t, adapter, x, M, saved_of(t, M, saved), dout, dx, grads,
-                          reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? QMLP_OK
-               : QMLP_ERR_CUDA;
+        if (any_alias(r)) return QMLP_ERR_ALIAS;
+        if (fault("launch")) return QMLP_ERR_CUDA;
+        return train_backward(t, adapter, x, M, saved_of(t, M, saved), dout, dx, grads,
+                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? QMLP_OK
+                   : QMLP_ERR_CUDA;
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -901,87 +926,89 @@ qmlp_status qmlp_train_backward(qmlp_train_t* t, const qmlp_adapter* adapter, co
 // ---------------------------------------------------------------------------
 qmlp_status qmlp_adamw_create(qmlp_adamw_t** out, const qmlp_adamw_tensor* ts, int count, qmlp_dtype pdt,
                               qmlp_dtype gdt, qmlp_state state, qmlp_stream_t stream) {
-    if (!out) return QMLP_ERR_INVALID_ARG;
-    *out = nullptr;
-    if (!ts) return QMLP_ERR_INVALID_ARG;
-    if ((pdt != QMLP_DT_FP32 && pdt != QMLP_DT_BF16) || (gdt != QMLP_DT_FP32 && gdt != QMLP_DT_BF16) ||
-        (state != QMLP_STATE_FP32 && state != QMLP_STATE_8BIT))
-        return QMLP_ERR_INVALID_ARG;
-    if (count < 1) return QMLP_ERR_SHAPE;
-    const bool s8 = state == QMLP_STATE_8BIT, pb = pdt == QMLP_DT_BF16, gb = gdt == QMLP_DT_BF16;
-    const bool master = ts[0].master != nullptr;
-    if (master && !pb) return QMLP_ERR_INVALID_ARG;
-    const size_t pe = pb ? 2 : 4, ge = gb ? 2 : 4, se = s8 ? 1 : 4;
-    std::vector<Range> ranges;
-    int64_t total = 0;
-    for (int i = 0; i < count; ++i) {
-        const qmlp_adamw_tensor& t = ts[i];
-        if (!t.param || !t.grad || !t.m || !t.v || (t.master != nullptr) != master ||
-            (s8 && (!t.m_scale || !t.v_scale)) || (!s8 && (t.m_scale || t.v_scale)))
+    return guarded([&]() -> qmlp_status {
+        if (!out) return QMLP_ERR_INVALID_ARG;
+        *out = nullptr;
+        if (!ts) return QMLP_ERR_INVALID_ARG;
+        if ((pdt != QMLP_DT_FP32 && pdt != QMLP_DT_BF16) || (gdt != QMLP_DT_FP32 && gdt != QMLP_DT_BF16) ||
+            (state != QMLP_STATE_FP32 && state != QMLP_STATE_8BIT))
             return QMLP_ERR_INVALID_ARG;
-        if (t.n < 1 || t.n > ((int64_t)1 << 40)) return QMLP_ERR_SHAPE;
-        if (!aligned(t.param, pe) || !aligned(t.grad, ge) || !aligned(t.m, se) || !aligned(t.v, se) ||
-            !aligned(t.master, 4) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
-            return QMLP_ERR_ALIGNMENT;
-        total += (t.n + kAdamWChunk - 1) / kAdamWChunk;
-        if (total > 0x7fffffff) return QMLP_ERR_SHAPE;
-        auto add = [&](const void* p, size_t bytes, bool w) {
-            if (p) ranges.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, w});
-        };
-        const size_t n = (size_t)t.n, nb = (n + kAdamWBlock - 1) / kAdamWBlock;
-        add(t.param, n * pe, true);
-        add(t.master, n * 4, true);
-        add(t.grad, n * ge, false);
-        add(t.m, n * se, true);
-        add(t.v, n * se, true);
-        add(t.m_scale, nb * 4, true);
-        add(t.v_scale, nb * 4, true);
-    }
-    if (any_alias(ranges)) return QMLP_ERR_ALIAS;
-    int dev = 0, sms = 0;
-    qmlp_status st = check_device(&dev, &sms);
-    if (st != QMLP_OK) return st;
-    std::vector<AdamWChunk> table;
-    table.reserve((size_t)total);
-    for (int i = 0; i < count; ++i) {
-        const qmlp_adamw_tensor& t = ts[i];
-        const bool vec = aligned16(t.param) && aligned16(t.grad) && aligned16(t.master) &&
-                         aligned(t.m, s8 ? 8 : 16) && aligned(t.v, s8 ? 8 : 16);
-        for (int64_t at = 0; at < t.n; at += kAdamWChunk) {
-            AdamWChunk c;
-            c.param = static_cast<uint8_t*>(t.param) + at * pe;
-            c.master = master ? t.master + at : nullptr;
-            c.grad = static_cast<const uint8_t*>(t.grad) + at * ge;
-            c.m = static_cast<uint8_t*>(t.m) + at * se;
-            c.v = static_cast<uint8_t*>(t.v) + at * se;
-            c.m_scale = s8 ? t.m_scale + at / kAdamWBlock : nullptr;
-            c.v_scale = s8 ? t.v_scale + at / kAdamWBlock : nullptr;
-            c.n = (int)std::min<int64_t>(kAdamWChunk, t.n - at);
-            c.vec = vec ? 1 : 0;
-            table.push_back(c);
+        if (count < 1) return QMLP_ERR_SHAPE;
+        const bool s8 = state == QMLP_STATE_8BIT, pb = pdt == QMLP_DT_BF16, gb = gdt == QMLP_DT_BF16;
+        const bool master = ts[0].master != nullptr;
+        if (master && !pb) return QMLP_ERR_INVALID_ARG;
+        const size_t pe = pb ? 2 : 4, ge = gb ? 2 : 4, se = s8 ? 1 : 4;
+        std::vector<Range> ranges;
+        int64_t total = 0;
+        for (int i = 0; i < count; ++i) {
+            const qmlp_adamw_tensor& t = ts[i];
+            if (!t.param || !t.grad || !t.m || !t.v || (t.master != nullptr) != master ||
+                (s8 && (!t.m_scale || !t.v_scale)) || (!s8 && (t.m_scale || t.v_scale)))
+                return QMLP_ERR_INVALID_ARG;
+            if (t.n < 1 || t.n > ((int64_t)1 << 40)) return QMLP_ERR_SHAPE;
+            if (!aligned(t.param, pe) || !aligned(t.grad, ge) || !aligned(t.m, se) || !aligned(t.v, se) ||
+                !aligned(t.master, 4) || !aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))
+                return QMLP_ERR_ALIGNMENT;
+            total += (t.n + kAdamWChunk - 1) / kAdamWChunk;
+            if (total > 0x7fffffff) return QMLP_ERR_SHAPE;
+            auto add = [&](const void* p, size_t bytes, bool w) {
+                if (p) ranges.push_back({reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, w});
+            };
+            const size_t n = (size_t)t.n, nb = (n + kAdamWBlock - 1) / kAdamWBlock;
+            add(t.param, n * pe, true);
+            add(t.master, n * 4, true);
+            add(t.grad, n * ge, false);
+            add(t.m, n * se, true);
+            add(t.v, n * se, true);
+            add(t.m_scale, nb * 4, true);
+            add(t.v_scale, nb * 4, true);
         }
-    }
-    qmlp_adamw_t* h = new qmlp_adamw_t();
-    h->count = (long)table.size();
-    h->param_bf16 = pb;
-    h->master = master;
-    h->grad_bf16 = gb;
-    h->s8 = s8;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = h->mem.alloc(reinterpret_cast<void**>(&h->chunks), table.size() * sizeof(AdamWChunk));
-    if (e != cudaSuccess) st = from_cuda(e);
-    else if (cudaMemcpyAsync(h->chunks, table.data(), table.size() * sizeof(AdamWChunk), cudaMemcpyHostToDevice, s) !=
-                 cudaSuccess ||
-             cudaStreamSynchronize(s) != cudaSuccess)
-        st = QMLP_ERR_CUDA;
-    if (st != QMLP_OK) {
-        cudaStreamSynchronize(s);
-        h->mem.release();
-        delete h;
-        return st;
-    }
-    *out = h;
-    return QMLP_OK;
+        if (any_alias(ranges)) return QMLP_ERR_ALIAS;
+        int dev = 0, sms = 0;
+        qmlp_status st = check_device(&dev, &sms);
+        if (st != QMLP_OK) return st;
+        std::vector<AdamWChunk> table;
+        table.reserve((size_t)total);
+        for (int i = 0; i < count; ++i) {
+            const qmlp_adamw_tensor& t = ts[i];
+            const bool vec = aligned16(t.param) && aligned16(t.grad) && aligned16(t.master) &&
+                             aligned(t.m, s8 ? 8 : 16) && aligned(t.v, s8 ? 8 : 16);
+            for (int64_t at = 0; at < t.n; at += kAdamWChunk) {
+                AdamWChunk c;
+                c.param = static_cast<uint8_t*>(t.param) + at * pe;
+                c.master = master ? t.master + at : nullptr;
+                c.grad = static_cast<const uint8_t*>(t.grad) + at * ge;
+                c.m = static_cast<uint8_t*>(t.m) + at * se;
+                c.v = static_cast<uint8_t*>(t.v) + at * se;
+                c.m_scale = s8 ? t.m_scale + at / kAdamWBlock : nullptr;
+                c.v_scale = s8 ? t.v_scale + at / kAdamWBlock : nullptr;
+                c.n = (int)std::min<int64_t>(kAdamWChunk, t.n - at);
+                c.vec = vec ? 1 : 0;
+                table.push_back(c);
+            }
+        }
+        qmlp_adamw_t* h = new qmlp_adamw_t();
+        h->count = (long)table.size();
+        h->param_bf16 = pb;
+        h->master = master;
+        h->grad_bf16 = gb;
+        h->s8 = s8;
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        const cudaError_t e = h->mem.alloc(reinterpret_cast<void**>(&h->chunks), table.size() * sizeof(AdamWChunk));
+        if (e != cudaSuccess) st = from_cuda(e);
+        else if (cudaMemcpyAsync(h->chunks, table.data(), table.size() * sizeof(AdamWChunk), cudaMemcpyHostToDevice, s) !=
+                     cudaSuccess ||
+                 cudaStreamSynchronize(s) != cudaSuccess)
+            st = QMLP_ERR_CUDA;
+        if (st != QMLP_OK) {
+            cudaStreamSynchronize(s);
+            h->mem.release();
+            delete h;
+            return st;
+        }
+        *out = h;
+        return QMLP_OK;
+    });
 }
 
 void qmlp_adamw_destroy(qmlp_adamw_t* h) {

@@ -291,8 +291,8 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         }
                         if (a.gu_g) {
                             const size_t at = gu_at(m, col + h + 4 * j, a.ldo);
-                            a.gu_g[at] = make_float4(g4[0], g4[1], g4[2], g4[3]);
-                            a.gu_u[at] = make_float4(u4[0], u4[1], u4[2], u4[3]);
+                            __stcs(a.gu_g + at, make_float4(g4[0], g4[1], g4[2], g4[3]));
+                            __stcs(a.gu_u + at, make_float4(u4[0], u4[1], u4[2], u4[3]));
                         }
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {

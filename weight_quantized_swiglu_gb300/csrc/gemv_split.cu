@@ -260,9 +260,12 @@ QMLP_DEV float lr_fma8(const uint4& q, const float* v, float s) {
 // The adapter warps (tid 0 .. kLT - 1). s_v [M][2 Rp] floats, then 2 M ints,
 // and s_d [M][2][tslice] floats; bars: s_d written, act slice written, the share of A_d act written.
 QMLP_DEV void lr_warps(const SplitLora& lr, int M, int I, int tslice, int tid, float* s_v, float* s_d,
-                       const float* s_act, uint32_t bar0, uint64_t limit, int* err) {
+                       const float* s_act, uint32_t bar0, uint64_t limit, int* err, bool late) {
     const int R = lr.Rp, lane = tid & 31, i0 = blockIdx.x * tslice;
-    // every token's slot and rank once, and A_d's rows on the way to L2
+    // every token's slot and rank once, and A_d's rows on the way to L2. With
+    // schedule (b) this kernel may have started before the adapters and ids were
+    // written; with (a) all before the launch that writes v had completed
+    if (!late) pdl_wait();
     int* s_n8 = reinterpret_cast<int*>(s_v + M * 2 * R);
     int* s_slot = s_n8 + M;
     if (tid < M) s_n8[tid] = lr_slot(lr, tid, s_slot[tid]);
@@ -273,7 +276,7 @@ QMLP_DEV void lr_warps(const SplitLora& lr, int M, int I, int tslice, int tid, f
         const char* a0 = reinterpret_cast<const char*>(lr.a_d + ((size_t)s_slot[m] * R + j) * I + i0);
         for (int o = 0; o < 2 * tslice; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(a0 + o));
     }
-    pdl_wait();  // v is written
+    if (late) pdl_wait();  // v is written
     for (int i = tid; i < M * 2 * R; i += kLT) s_v[i] = __ldcg(lr.v + i);
     named_bar_sync(2, kLT);
     // B v: an item a (token, gate or up, row)
@@ -743,7 +746,9 @@ __global__ void __launch_bounds__(thr(LR), 1) gemv_split_kernel(const __grid_con
     __syncthreads();  // the last CTA-wide barrier: the producer never waits on the consumers
     // the next kernel's CTAs may start as SMs free up (set-up and launch
     // latency overlap this call's end); they wait before touching its buffers
-    pdl_launch_dependents();
+    // (schedule (b) with adapters: the reduce kernel reads ids and B_d before its
+    // own wait, so it may start only once this one has waited)
+    if (!(LR && SEP)) pdl_launch_dependents();
 
     if (warp == kW) {
         if (lane == 0) {
@@ -794,7 +799,7 @@ __global__ void __launch_bounds__(thr(LR), 1) gemv_split_kernel(const __grid_con
     if (LR && warp > kW) {
         float* s_d = reinterpret_cast<float*>(smem + a.lr_off);
         lr_warps(a.lr, M, a.I, a.T * 16, threadIdx.x - kThr, s_d + M * 2 * a.T * 16, s_d,
-                 reinterpret_cast<const float*>(smem + a.act_off), lr_bar, a.limit, a.err);
+                 reinterpret_cast<const float*>(smem + a.act_off), lr_bar, a.limit, a.err, kLate);
         return;
     }
 
@@ -810,6 +815,7 @@ __global__ void __launch_bounds__(thr(LR), 1) gemv_split_kernel(const __grid_con
     // it has completed (kLate: that one touches none of them, and let this one
     // start only once all before it had completed)
     if (!kLate) pdl_wait();
+    if (LR && SEP) pdl_launch_dependents();
 
     // ---------------- phase A: gate/up over this CTA's tiles ----------------
     if (NT == 2) {

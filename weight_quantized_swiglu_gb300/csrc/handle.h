@@ -169,12 +169,14 @@ inline qmlp::SplitLaunch split_launch(const qmlp_s* h, const void* x, int M) {
     return S;
 }
 
-// Terms of low-rank adapters that the GEMMs add: gate and up [M][2I], then,
-// once `between` has run on the workspace act, down's [M][K].
+// Terms of low-rank adapters that the GEMMs add: gate and up [M][2I], which
+// `before` computes, then, once `between` has run on the workspace act, down's
+// [M][K]. ev: an event for the images decoded beside `before`.
 struct GemmTerms {
     const float* add = nullptr;
     const float* add_down = nullptr;
-    std::function<cudaError_t(cudaStream_t)> between;
+    cudaEvent_t ev = nullptr;
+    std::function<cudaError_t(cudaStream_t)> before, between;
 };
 qmlp_status run_gemm(qmlp_s* h, qmlp_path path, int stages, const void* x, int M, void* out, cudaStream_t s,
                      float* out_f32, const GemmTerms* ex);
