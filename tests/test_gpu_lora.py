@@ -213,6 +213,33 @@ def test_stream_order_graph_and_a_changed_slot(torch, M):
     mlp.close()
 
 
+@pytest.mark.parametrize("fmt,rank", [("nvfp4", 16), ("nvfp4", 40), ("fp8", 7)])
+@pytest.mark.parametrize("pattern", ["runs", "each", "few", "none"])
+def test_long_batches(torch, fmt, rank, pattern):
+    """Enough tokens and a long enough contraction for the terms to be steps of
+    the GEMMs: slots whose tokens start and end inside tiles, tiles of several
+    slots and of none, and the same bytes from call to call and after other
+    calls."""
+    K, I, M = 4096, 1024, 1333
+    rng = np.random.default_rng(rank)
+    case = scaled_case(fmt, K, I, 38)
+    w = weights(case)
+    mlp = q.QuantMLP.from_case(case, max_M=1400)
+    lora = q.LoraMLP(mlp, 3, rank)
+    ads = {0: (adapter(rng, K, I, rank, gain=rank ** -0.5), 1.5), 2: (adapter(rng, K, I, max(1, rank - 3)), -0.25)}
+    for s, (d, c) in ads.items():
+        lora.set(s, on_device(torch, d, c))
+    xb, x = x_of(rng, M, K)
+    ids = {"runs": np.repeat([2, -1, 0, 1, 2], [300, 5, 640, 100, 288]), "each": rng.integers(-1, 4, M),
+           "few": np.where(np.arange(M) % 400 == 7, 2, 5), "none": np.full(M, -1)}[pattern]
+    out = run(torch, lora, mlp, xb, ids)
+    compare(out, reference(case, w, x, ids, ads), what=f"{fmt} {pattern}")
+    run(torch, lora, mlp, xb[:1000], rng.integers(0, 3, 1000))
+    assert np.array_equal(out, run(torch, lora, mlp, xb, ids))
+    lora.close()
+    mlp.close()
+
+
 def test_refusals(torch):
     case = gen.gen_dense_case("nvfp4", 256, 512, 1, 37)
     mlp = q.QuantMLP.from_case(case, max_M=16)

@@ -674,10 +674,11 @@ class AdamW:
         self.h = qmlp_adamw_create(ts, kinds[params[0].dtype], kinds[grads[0].dtype],
                                    STATE_8BIT if eight else STATE_FP32, stream)
         self._keep = lists
+        self._step = lib().qmlp_adamw_step
 
     def step(self, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step=1, grad_scale=1.0, stream=None):
         hyper = qmlp_adamw_hyper(lr, beta1, beta2, eps, weight_decay, grad_scale, step)
-        _chk(qmlp_adamw_step(self.h, hyper, stream), "qmlp_adamw_step")
+        _chk(self._step(self.h, hyper, _stream(stream)), "qmlp_adamw_step")
 
     def close(self):
         if getattr(self, "h", None):

@@ -425,6 +425,13 @@ qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M
         if (ex) {
             g.add = ex->add;
             g.ldadd = (size_t)2 * h->I;
+            g.ext = ex->ext;
+            g.ext_a = ex->v;
+            g.ext_b = ex->img;
+            g.ents = ex->ents;
+            g.ent_slot = ex->ent_slot;
+            g.entries = ex->entries;
+            g.slots = ex->slots;
         }
         g.w = h->gm_gu;
         g.a = x;
@@ -442,6 +449,9 @@ qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M
             g.add = ex->add_down;
             g.split_tail = g.pair && g.wdec;
             g.ldadd = (size_t)h->K;
+            g.ext = ex->ext_down;
+            g.ext_b = ex->img_down;
+            g.rows = ex->rows;
         }
         g.epi = out_f32 ? kEpiRaw : kEpiPlain;
         g.raw_sel = 0;

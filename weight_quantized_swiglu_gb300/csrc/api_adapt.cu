@@ -27,6 +27,17 @@ struct qmlp_lora_s {
     int4* tiles = nullptr;
     int* n_tiles = nullptr;
     cudaEvent_t ev = nullptr;
+    // From kDqMinM tokens on the terms may be further contraction steps of the
+    // GEMMs (see training's Words: T words, the factors divided out): tokens in
+    // slot order, the adapters' images made when they are set
+    bool steps = false;
+    int T = 2, e_gu = 0, e_d = 0;    // steps an entry
+    uint8_t* img_gu = nullptr;       // [slots][I / 128][e_gu] and [slots][K / 256][e_d] images of 32 KB
+    uint8_t* img_d = nullptr;
+    __nv_bfloat16* ev_v = nullptr;   // 256 rows an entry of 64 max(e_gu, e_d)
+    void* x_rows = nullptr;          // bf16 [max_M][K]
+    int2* ents = nullptr;
+    int* ent_slot = nullptr;
     Owner mem;
 };
 
@@ -64,6 +75,11 @@ struct qmlp_train_s {
 // rounding of their terms to show in a gradient; over more tokens it averages
 // out. (One token, rank 4: the gradient of A 5.4e-3 off with one word.)
 constexpr int kTwoWordM = 256;
+// Weights a projection from which a forward of fewer than kPairMinM tokens does
+// not decode them first (a step of 100 tokens, decoding against not: 5120 x 17408
+// 618 / 496 us, 2048 x 5632 205 / 202, 1024 x 2816 149 / 148; 60 tokens, 2048 x
+// 2048 146 / 158).
+constexpr size_t kFewWeights = (size_t)8 << 20;
 
 struct qmlp_adamw_s {
     AdamWChunk* chunks = nullptr;
@@ -111,6 +127,48 @@ bool any_alias(std::vector<Range>& r) {
         if (x.written) wend = std::max(wend, x.end);
     }
     return false;
+}
+
+// Where a call keeps c z A^T (or c dy B) of every token: bf16 words side by
+// side in rows of ld, nc columns a word. As further steps of a GEMM: T words
+// (the third again the first) and zeros up to a multiple of 64, with the parts'
+// factors divided out; else kLrWords words for the expand kernel.
+struct Words {
+    __nv_bfloat16* p = nullptr;
+    int nc = 0, ld = 0;
+    bool ext = false;
+    int T = 0;
+    int steps() const { return ld / 64; }
+};
+constexpr size_t kImage = 32768;                // bytes of a stage image
+constexpr size_t kMostImages = (size_t)4 << 30;  // bytes of images that the slots of a handle may hold
+int word_ld(int nc, int T) { return (nc * T + 63) / 64 * 64; }
+Words words_of(__nv_bfloat16* p, int nc, bool ext, int T) {
+    Words w;
+    w.p = p;
+    w.nc = nc;
+    w.ext = ext;
+    w.T = ext ? T : kLrWords;
+    w.ld = ext ? word_ld(nc, T) : nc * kLrWords;
+    return w;
+}
+size_t words_room(size_t M, int nc) { return M * std::max(word_ld(nc, 3), nc * kLrWords); }
+
+// Whether every factor of h's weights is large enough to divide by.
+cudaError_t factors_divide(const qmlp_t* h, bool* ok, cudaStream_t s) {
+    *ok = true;
+    const int n[3] = {h->I, h->I, h->K};
+    for (int i = 0; i < 3; ++i) {
+        std::vector<float> f(1, h->gv[i].inv_g);
+        if (h->fmt == kFP8) {
+            f.resize(n[i]);
+            cudaError_t e = cudaMemcpyAsync(f.data(), h->gv[i].chs, n[i] * sizeof(float), cudaMemcpyDeviceToHost, s);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+            if (e != cudaSuccess) return e;
+        }
+        for (float v : f) *ok = *ok && fabsf(v) >= kLeastFactor;
+    }
+    return cudaSuccess;
 }
 
 qmlp_status check_adapter(const qmlp_adapter* a, int max_rank) {
@@ -184,6 +242,77 @@ cudaError_t lora_expand(const qmlp_lora_s* l, bool down, int M, cudaStream_t s) 
     a.y = l->y;
     a.ldy = (size_t)(down ? 1 : 2) * a.N;
     return launch_lr_expand(a, l->Rp, false, lr_max_tiles(M, l->slots), down ? 1 : 2, s);
+}
+// The terms as steps of the GEMMs: z in slot order, v by entry.
+cudaError_t lora_shrink_steps(const qmlp_lora_s* l, bool down, const void* z, int M, cudaStream_t s) {
+    const qmlp_t* h = l->h;
+    LrShrink a;
+    a.tok = tokens_of(l, M);
+    a.tok.perm = nullptr;
+    a.x = static_cast<const __nv_bfloat16*>(z);
+    a.D = down ? h->I : h->K;
+    a.ldx = a.D;
+    a.w = down ? l->a_d : l->a_gu;
+    const int nc = (down ? 1 : 2) * l->Rp;
+    a.w_slot = (size_t)nc * a.D;
+    a.scale = l->scale;
+    a.v = l->ev_v;
+    a.v_word = nc;
+    a.ldv = word_ld(nc, l->T);
+    a.entries = true;
+    a.words = l->T;
+    a.again = l->T == 3;
+    a.pad = a.ldv - nc * l->T;
+    if (h->fmt == kNVFP4) {
+        a.mul0 = 1.0f / h->gv[down ? 2 : 0].inv_g;
+        a.mul1 = 1.0f / h->gv[down ? 2 : 1].inv_g;
+        a.half = l->Rp;
+    }
+    // the rows of an entry that are other slots'
+    const cudaError_t e =
+        cudaMemsetAsync(l->ev_v, 0, (size_t)lr_max_entries(M, l->slots) * 256 * a.ldv * sizeof(*l->ev_v), s);
+    return e != cudaSuccess ? e : launch_lr_shrink(a, nc, false, lr_max_tiles(M, l->slots), 1, h->num_sms, s);
+}
+// Whether a call takes them so: M tokens on the pair GEMM, and the entries that
+// the slots can make of them add at most 15% to the contraction (one or two steps
+// an entry for NVFP4 up to rank 32; the terms as an fp32 array cost 20% at rank
+// 64, 3001 tokens).
+bool lora_steps(const qmlp_lora_s* l, int M) {
+    if (!l->steps || M < kDqMinM) return false;
+    const long most = (long)lr_max_entries(M, l->slots) * l->e_gu;
+    return 100 * most <= 15L * (l->h->K / 64) * ((M + 255) / 256);
+}
+cudaError_t lora_images(const qmlp_lora_s* l, int slot, const qmlp_adapter* a, cudaStream_t s) {
+    const qmlp_t* h = l->h;
+    auto bf = [](const void* p) { return static_cast<const __nv_bfloat16*>(p); };
+    LrImage m;
+    m.r = a->rank;
+    m.R = l->Rp;
+    m.T = l->T;
+    m.sn = a->rank;
+    m.sj = 1;
+    m.parts = 2;
+    m.src[0] = bf(a->gate_b);
+    m.src[1] = bf(a->up_b);
+    m.div[0] = h->gv[0].chs;
+    m.div[1] = h->gv[1].chs;
+    m.N = h->I;
+    m.interleaved = 1;
+    m.tiles = h->I / 128;
+    m.ext = l->e_gu;
+    m.img = l->img_gu + (size_t)slot * m.tiles * m.ext * kImage;
+    const cudaError_t e = launch_lr_image(m, s);
+    if (e != cudaSuccess) return e;
+    m.parts = 1;
+    m.src[0] = bf(a->down_b);
+    m.src[1] = nullptr;
+    m.div[0] = h->gv[2].chs;
+    m.N = h->K;
+    m.interleaved = 0;
+    m.tiles = h->K / 256;
+    m.ext = l->e_d;
+    m.img = l->img_d + (size_t)slot * m.tiles * m.ext * kImage;
+    return launch_lr_image(m, s);
 }
 LrFew few_of(const qmlp_lora_s* l, bool down, const int32_t* ids) {
     LrFew a;
@@ -312,6 +441,22 @@ qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_ra
         get(&l->raw, (size_t)kMaxGemvM * (2 * I + K), false);
         get(&l->vd, (size_t)std::max(1, h->sp.G) * kMaxGemvM * R, false);
         get(&l->perm, M, false);
+        l->T = h->fmt == kFP8 ? 3 : 2;
+        l->e_gu = word_ld(2 * (int)R, l->T) / 64;
+        l->e_d = word_ld((int)R, l->T) / 64;
+        const size_t ig = S * (I / 128) * l->e_gu * kImage, id = S * (K / 256) * l->e_d * kImage;
+        bool ok = false;
+        if (e == cudaSuccess && h->wdec && h->side && ig + id <= kMostImages) e = factors_divide(h, &ok, s);
+        l->steps = ok;
+        if (l->steps) {
+            const size_t ents = (size_t)lr_max_entries((int)M, slots);
+            get(&l->img_gu, ig, false);
+            get(&l->img_d, id, false);
+            get(&l->ev_v, ents * 256 * 64 * std::max(l->e_gu, l->e_d), false);
+            get(reinterpret_cast<uint8_t**>(&l->x_rows), M * K * 2, false);
+            get(&l->ents, (M + 255) / 256, false);
+            get(&l->ent_slot, ents, false);
+        }
         get(&l->tiles, tiles, false);
         get(&l->n_tiles, 1, true);
         if (e == cudaSuccess) e = cudaEventCreateWithFlags(&l->ev, cudaEventDisableTiming);
@@ -343,7 +488,8 @@ qmlp_status qmlp_lora_set(qmlp_lora_t* l, int slot, const qmlp_adapter* a, qmlp_
     const qmlp_status st = check_adapter(a, l->max_rank);
     if (st != QMLP_OK) return st;
     if (fault("launch")) return QMLP_ERR_CUDA;
-    return launch_lr_pack(pack_of(l, slot, a), s) == cudaSuccess ? QMLP_OK : QMLP_ERR_CUDA;
+    if (launch_lr_pack(pack_of(l, slot, a), s) != cudaSuccess) return QMLP_ERR_CUDA;
+    return l->steps && lora_images(l, slot, a, s) != cudaSuccess ? QMLP_ERR_CUDA : QMLP_OK;
 }
 
 qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids, int M, void* out,
@@ -368,7 +514,7 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
             }
             return QMLP_OK;
         }
-        const bool few = M <= kLrFew;
+        const bool few = M <= kLrFew, steps = lora_steps(l, M);
         auto terms = [&](bool down, const void* z, cudaStream_t st) {
             cudaError_t e = few ? lora_shrink_few(l, down, z, ids, M, st) : lora_shrink(l, down, z, M, st);
             if (e == cudaSuccess)
@@ -377,9 +523,30 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
         };
         GemmTerms t;
         t.ev = l->ev;
+        if (steps) {
+            t.ext = l->e_gu;
+            t.ext_down = l->e_d;
+            t.v = l->ev_v;
+            t.img = l->img_gu;
+            t.img_down = l->img_d;
+            t.ents = l->ents;
+            t.ent_slot = l->ent_slot;
+            t.entries = lr_max_entries(M, l->slots);
+            t.slots = l->slots;
+            t.rows = l->perm;
+            t.before = [&](cudaStream_t st) {
+                cudaError_t e = launch_lr_plan(ids, M, l->slots, l->rank, l->perm, l->tiles, l->n_tiles, l->ents,
+                                               l->ent_slot, st);
+                if (e == cudaSuccess) e = launch_lr_gather(x, l->perm, M, h->K, l->x_rows, st);
+                return e == cudaSuccess ? lora_shrink_steps(l, false, l->x_rows, M, st) : e;
+            };
+            t.between = [&](cudaStream_t st) { return lora_shrink_steps(l, true, h->act, M, st); };
+            return run_gemm(h, QMLP_PATH_AUTO, 3, l->x_rows, M, out, s, nullptr, &t);
+        }
         t.before = [&](cudaStream_t st) {
-            const cudaError_t e =
-                few ? cudaSuccess : launch_lr_plan(ids, M, l->slots, l->rank, l->perm, l->tiles, l->n_tiles, st);
+            const cudaError_t e = few ? cudaSuccess
+                                      : launch_lr_plan(ids, M, l->slots, l->rank, l->perm, l->tiles, l->n_tiles, nullptr,
+                                                       nullptr, st);
             return e == cudaSuccess ? terms(false, x, st) : e;
         };
         t.add = l->y;
@@ -394,29 +561,6 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
 // ---------------------------------------------------------------------------
 extern "C++" {
 namespace {
-
-// Where a call keeps c z A^T (or c dy B) of every token: bf16 words side by
-// side in rows of ld, nc columns a word. As further steps of a GEMM: T words
-// (the third again the first) and zeros up to a multiple of 64, with the parts'
-// factors divided out; else kLrWords words for the expand kernel.
-struct Words {
-    __nv_bfloat16* p = nullptr;
-    int nc = 0, ld = 0;
-    bool ext = false;
-    int T = 0;
-    int steps() const { return ld / 64; }
-};
-int word_ld(int nc, int T) { return (nc * T + 63) / 64 * 64; }
-Words words_of(__nv_bfloat16* p, int nc, bool ext, int T) {
-    Words w;
-    w.p = p;
-    w.nc = nc;
-    w.ext = ext;
-    w.T = ext ? T : kLrWords;
-    w.ld = ext ? word_ld(nc, T) : nc * kLrWords;
-    return w;
-}
-size_t words_room(size_t M, int nc) { return M * std::max(word_ld(nc, 3), nc * kLrWords); }
 
 // What a forward keeps (see qmlp_train_saved_bytes).
 struct Saved {
@@ -449,13 +593,13 @@ Saved saved_of(const qmlp_train_s* t, int M, const void* base) {
 int tiles_for(int M) { return (M + kLrTile - 1) / kLrTile; }
 
 // v = c z W^T for every token (one adapter), W [nc][D] or, trans, [D][nc].
-LrShrink shrink_all(const qmlp_train_s* t, const void* z, int M, int D, const Words& w) {
+LrShrink shrink_all(const qmlp_adapter* ad, const void* z, int M, int D, const Words& w) {
     LrShrink a;
+    a.scale_all = ad->scale;
     a.tok.M = M;
     a.x = static_cast<const __nv_bfloat16*>(z);
     a.ldx = D;
     a.D = D;
-    a.scale = t->l->scale;
     a.v = w.p;
     a.v_word = w.nc;
     a.ldv = w.ld;
@@ -524,6 +668,14 @@ cudaError_t beside(qmlp_t* h, cudaStream_t s, F&& f) {
         if (try_e != cudaSuccess) return try_e;            \
     } while (0)
 
+// Whether the kernels can read the adapter's own arrays: the A's rows where
+// they start at 16 bytes, the B's where, besides, their rank is the padded one.
+bool own_a(const qmlp_adapter* a) { return aligned16(a->gate_a) && aligned16(a->up_a) && aligned16(a->down_a); }
+bool own_b(const qmlp_train_s* t, const qmlp_adapter* a) {
+    return a->rank == t->l->Rp && aligned16(a->gate_b) && aligned16(a->up_b) && aligned16(a->down_b) && a->gate_b &&
+           a->up_b && a->down_b;
+}
+
 // What the low-rank kernels read of the adapter, padded: the A parts for the
 // forward, the B parts (gate's and up's over the factor that their gradients
 // carry) for the backward pass; both where expand_all adds the other side.
@@ -568,6 +720,11 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     const qmlp_lora_t* l = t->l;
     const int K = h->K, I = h->I, R = l->Rp;
     const bool ext = v.vgu.ext, fp8 = h->fmt == kFP8;
+    bool own = false;
+    // few tokens: the decoder warps' GEMM, which reads the packed weights and no
+    // images (the backward pass has no such form: its weights lie transposed),
+    // unless the weights are so few that the twelve epilogue warps count
+    const bool dq = M >= kPairMinM || (size_t)K * I < kFewWeights;
     // beside: the adapter's images, then down's weights
     TRY(beside(h, s, [&](cudaStream_t b) {
         if (ad && ext) {
@@ -587,13 +744,21 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
             TRY(launch_lr_image(m, b));
             TRY(cudaEventRecord(t->ev_img, b));
         }
-        return launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, b);
+        return dq ? launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, b) : cudaSuccess;
     }));
-    TRY(launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s));
+    if (dq) TRY(launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s));
     if (ad) {
-        TRY(launch_lr_pack(pack_train(t, ad, false, !ext), s));
-        LrShrink a = shrink_all(t, x, M, K, v.vgu);
-        a.w = l->a_gu;
+        own = own_a(ad);
+        if (!own || !ext) TRY(launch_lr_pack(pack_train(t, ad, false, !ext), s));
+        LrShrink a = shrink_all(ad, x, M, K, v.vgu);
+        if (own) {
+            a.wa[0] = bf(ad->gate_a);
+            a.wa[1] = bf(ad->up_a);
+            a.r = ad->rank;
+            a.R = R;
+        } else {
+            a.w = l->a_gu;
+        }
         if (ext && !fp8) {
             a.mul0 = 1.0f / h->gv[0].inv_g;
             a.mul1 = 1.0f / h->gv[1].inv_g;
@@ -606,7 +771,7 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     GemmLaunch g = dq_gemm(t, M);
     g.epi = kEpiSwiGLU;
     g.w = h->gm_gu;
-    g.wdec = h->wdec;
+    g.wdec = dq ? h->wdec : nullptr;
     g.wdec_bytes = h->wdec_bytes;
     g.a = x;
     g.out = v.act;
@@ -619,9 +784,15 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     }
     TRY(launch_gemm(g, h->num_sms, s));
     if (ad) {
-        LrShrink a = shrink_all(t, v.act, M, I, v.vd);
+        LrShrink a = shrink_all(ad, v.act, M, I, v.vd);
         a.x_lo = v.act_lo;
-        a.w = l->a_d;
+        if (own) {
+            a.wa[0] = bf(ad->down_a);
+            a.r = ad->rank;
+            a.R = R;
+        } else {
+            a.w = l->a_d;
+        }
         if (ext && !fp8) a.mul0 = 1.0f / h->gv[2].inv_g;
         TRY(launch_lr_shrink(a, R, false, tiles_for(M), 1, h->num_sms, s));
         if (!ext) TRY(expand_all(t, v.vd, M, R, 1, l->b_d, 0, K, false, s));
@@ -630,7 +801,7 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     g = dq_gemm(t, M);
     g.epi = kEpiPlain;
     g.w = h->gm_d;
-    g.wdec = h->wdec2;
+    g.wdec = dq ? h->wdec2 : nullptr;
     g.wdec_bytes = h->wdec2_bytes;
     g.a = v.act;
     g.out = out;
@@ -647,6 +818,7 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     const bool fp8 = h->fmt == kFP8;
     // d act's GEMM of FP8 has fp16 operands: its adapter terms are added
     const bool ext = v.vgu.ext, ext_d = ext && !fp8;
+    bool own = false;
     const Words wd = words_of(t->dvd, R, ext_d, 2), wv = words_of(t->dv, 2 * R, ext, 2);
     const __nv_bfloat16* dy = static_cast<const __nv_bfloat16*>(dout);
     // the transposed images: down's (FP8: in fp16 with its per-channel factors,
@@ -674,9 +846,10 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     }));
     TRY(launch_gemm_predecode_t(h->gm_d, t->mul_d, nullptr, fp8, t->img_t, t->img_t_bytes, s));
     if (ad) {
-        TRY(launch_lr_pack(pack_train(t, ad, true, !ext_d || !ext), s));
-        LrShrink a = shrink_all(t, dy, M, K, wd);
-        a.w = l->b_d;
+        own = own_b(t, ad) && !fp8 && ext;
+        if (!own) TRY(launch_lr_pack(pack_train(t, ad, true, !ext_d || !ext), s));
+        LrShrink a = shrink_all(ad, dy, M, K, wd);
+        a.w = own ? bf(ad->down_b) : l->b_d;
         if (ext_d) a.mul0 = 1.0f / h->gv[2].inv_g;
         TRY(launch_lr_shrink(a, R, true, tiles_for(M), 1, h->num_sms, s));
         if (!ext_d) TRY(expand_all(t, wd, M, R, 1, l->a_d, 0, I, true, s));
@@ -709,13 +882,21 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     }
     TRY(launch_gemm(g, h->num_sms, s));
     if (ad) {
-        LrShrink a = shrink_all(t, t->dgu, M, I, wv);
+        LrShrink a = shrink_all(ad, t->dgu, M, I, wv);
         a.x_lo = lo;
         a.ldx = (size_t)2 * I;
         a.x_z = I;
-        a.w = t->bq;
-        a.w_lo = t->bq + (size_t)2 * I * R;
-        a.w_z = (size_t)I * R;
+        if (own) {  // d gate and d up carry NVFP4's factors: taken out of the products
+            a.w = bf(ad->gate_b);
+            a.w_z = (size_t)(bf(ad->up_b) - bf(ad->gate_b));
+            a.mul0 = 1.0f / h->gv[0].inv_g;
+            a.mul1 = 1.0f / h->gv[1].inv_g;
+            a.half = R;
+        } else {
+            a.w = t->bq;
+            a.w_lo = t->bq + (size_t)2 * I * R;
+            a.w_z = (size_t)I * R;
+        }
         TRY(launch_lr_shrink(a, R, true, tiles_for(M), 2, h->num_sms, s));
         if (!ext) TRY(expand_all(t, wv, M, 2 * R, 1, l->a_gu, 0, K, true, s));
     }
@@ -814,13 +995,11 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
         }
         if (e == cudaSuccess && h->fmt == kFP8) {
             // e4m3 (at most 448) times a factor under fac_d, times 2^6: under 2^15
-            std::vector<float> f(K), fg(2 * I);
-            e = cudaMemcpyAsync(fg.data(), h->gv[0].chs, I * sizeof(float), cudaMemcpyDeviceToHost, s);
-            if (e == cudaSuccess) e = cudaMemcpyAsync(fg.data() + I, h->gv[1].chs, I * sizeof(float), cudaMemcpyDeviceToHost, s);
-            if (e == cudaSuccess) e = cudaMemcpyAsync(f.data(), h->gv[2].chs, K * sizeof(float), cudaMemcpyDeviceToHost, s);
+            e = factors_divide(h, &t->steps, s);
+            std::vector<float> f(K);
+            if (e == cudaSuccess)
+                e = cudaMemcpyAsync(f.data(), h->gv[2].chs, K * sizeof(float), cudaMemcpyDeviceToHost, s);
             if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-            for (float v : fg) t->steps = t->steps && fabsf(v) >= kLeastFactor;
-            for (float v : f) t->steps = t->steps && fabsf(v) >= kLeastFactor;
             float top = 0.0f;
             for (float v : f)
                 if (isfinite(v)) top = std::max(top, fabsf(v));

@@ -154,9 +154,15 @@ struct Args {
     const float* gc0;
     const float* gc1;
     int f16;               // the images and activations are fp16 (activations prescaled, see sig)
-    // further contraction steps of low-rank adapters (CTA pairs): activations
-    // [M][64 ext] and images [Nt][ext], through tensor maps of their own
+    // further contraction steps of low-rank adapters (CTA pairs), `ext` of them an
+    // entry, through tensor maps of their own: entry e's activations are rows 256
+    // e.. of [..][64 ext], its images [Nt][ext] those of slot ent_slot[e]. A
+    // 256-token tile t has the entries ents[t] = {first, count}; without lists
+    // each has entry t and slot 0.
     int ext;
+    const int2* ents;
+    const int* ent_slot;
+    const int* rows;       // EXT, plain: optional, the output row of each token
     // CTA pairs, plain epilogue: the last `tail` tiles, which would leave most
     // pairs idle for a tile's time, are split over the contraction, tail_splits
     // pairs a tile, into ws [tail][tail_splits][256][256]; a kernel after this
@@ -406,8 +412,9 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                     pk[j / 2] = pack_bf16x2(scalbnf(y[j], -sg) * f.x, scalbnf(y[j + 1], -sg) * f.y);
                     pk[j / 2 + 1] = pack_bf16x2(scalbnf(y[j + 2], -sg) * f.z, scalbnf(y[j + 3], -sg) * f.w);
                 }
-                uint4* dst = reinterpret_cast<uint4*>(out + (size_t)m * a.ldo + nt * BN + c0);
-                if (QMLP_INB(nt * BN + c0 + 31, a.ldo, 12) && QMLP_INB(m, a.M, 12))
+                const int mo = EXT && a.rows ? __ldg(a.rows + m) : m;
+                uint4* dst = reinterpret_cast<uint4*>(out + (size_t)mo * a.ldo + nt * BN + c0);
+                if (QMLP_INB(nt * BN + c0 + 31, a.ldo, 12) && QMLP_INB(mo, a.M, 12))
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
                         dst[v] = make_uint4(pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
@@ -830,21 +837,35 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
     const int Mt2 = (a.M + 2 * BM - 1) / (2 * BM);  // 256-token tiles
     const int Nt = a.N / BN;
     const int KS = a.Kd / BK;
-    const int KT = EXT ? KS + a.ext : KS;  // with the adapters' steps
     const int units = Mt2 * Nt;  // n-tile-major, as the single-CTA kernel
-    // this pair's i-th piece of work: a tile, or its share of a split one
+    // this pair's i-th piece of work: a tile, or its share sp of a split one
     const int whole = EXT ? units - a.tail : units;
-    auto piece = [&](int i, int& u, int& k0, int& k1) {
+    auto piece = [&](int i, int& u, int& sp) {
         u = pair + i * npairs;
-        k0 = 0;
-        k1 = KT;
+        sp = -1;
         if (!EXT || u < whole) return u < whole;
         if (i * npairs != whole || pair >= a.tail * a.tail_splits) return false;
-        const int sp = pair % a.tail_splits;
+        sp = pair % a.tail_splits;
         u = whole + pair / a.tail_splits;
-        k0 = (int)((long)KT * sp / a.tail_splits);
-        k1 = (int)((long)KT * (sp + 1) / a.tail_splits);
         return true;
+    };
+    // its first adapter entry and its steps [k0, k1), the adapters' from KS on
+    auto steps = [&](int u, int sp, int& first, int& k0, int& k1) {
+        k0 = 0;
+        k1 = KS;
+        first = 0;
+        if (!EXT) return;
+        if (a.ext) {
+            const int t = u % Mt2;
+            const int2 e = a.ents ? __ldg(a.ents + t) : make_int2(t, 1);
+            first = e.x;
+            k1 += e.y * a.ext;
+        }
+        if (sp >= 0) {
+            const int n = k1;
+            k0 = (int)((long)n * sp / a.tail_splits);
+            k1 = (int)((long)n * (sp + 1) / a.tail_splits);
+        }
     };
 
     if (threadIdx.x == 0) {
@@ -880,8 +901,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
             if (PRE) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&bmap)) : "memory");
             int it = 0;
             bool ok = !PRE || rank == 0;  // PRE: the leader loads the stages of both CTAs
-            int u, k0, k1;
-            for (int i = 0; ok && piece(i, u, k0, k1); ++i) {
+            int u, sp, first, k0, k1;
+            for (int i = 0; ok && piece(i, u, sp); ++i) {
+                steps(u, sp, first, k0, k1);
                 const int nt = u / Mt2, mt2 = u % Mt2;
                 const uint8_t* blk = a.tiles + (size_t)nt * KS * raw_bytes<FMT>();
                 // error-path tests: the pair's very last k-step is never loaded
@@ -900,11 +922,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
                         // rows; the row swizzle has period 8) into CTA r
                         mbar_arrive_expect_tx(full(s), 2 * (kABytes + kR));
                         if (EXT && ks >= KS) {
-                            const int e = ks - KS, row = (nt * a.ext + e) * BN;
+                            const int e = (ks - KS) % a.ext, n = first + (ks - KS) / a.ext;
+                            const int slot = a.ents ? __ldg(a.ent_slot + n) : 0;
+                            const int row = ((slot * Nt + nt) * a.ext + e) * BN;
 #pragma unroll
                             for (uint32_t r = 0; r < 2; ++r) {
                                 tma_load_2d_pair(base_s + S::A + s * kABytes, r, &amap2, e * BK,
-                                                 mt2 * 2 * BM + (int)r * BM, full(s));
+                                                 n * 2 * BM + (int)r * BM, full(s));
                                 tma_load_2d_pair(base_s + S::Raw + s * kR, r, &bmap2, 0, row + (int)r * (BN / 2),
                                                  full(s));
                             }
@@ -944,10 +968,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
         if (lane == 0) {
             int it = 0, tc = 0;
             bool ok = true, issued = false;
-            int u, k0, k1;
-            for (; ok && piece(tc, u, k0, k1); ++tc) {
+            int u, sp, first, k0, k1;
+            for (; ok && piece(tc, u, sp); ++tc) {
                 const int buf = tc & 1, use = tc >> 1;
                 if (rank == 0) {
+                    steps(u, sp, first, k0, k1);
                     // ---------------- MMA issuer (leader) ----------------
                     if (use > 0 &&
                         (!wait_or_abort(acc_empty(buf), (uint32_t)((use - 1) & 1), abort_flag, a.err, 42, a.limit) ||
@@ -1006,8 +1031,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
         const int q = warp & 3;
         const int grp = (warp - 2) / kEpiWarps;
         const int row_in_tile = q * 32 + lane;
-        int tc = 0, u, k0, k1;
-        for (; piece(tc, u, k0, k1); ++tc) {
+        int tc = 0, u, sp;
+        for (; piece(tc, u, sp); ++tc) {
             const int nt = u / Mt2, mt2 = u % Mt2;
             const int buf = tc & 1, use = tc >> 1;
             const bool ready = wait_or_abort(acc_full(buf), (uint32_t)(use & 1), abort_flag, a.err, 50, a.limit);
@@ -1152,7 +1177,8 @@ __global__ void __launch_bounds__(256) tail_reduce_kernel(const Args a) {
     const int sg = a.sig ? a.sig[m] : 0;
     float4 d = make_float4(0, 0, 0, 0);
     if (a.add) d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + n);
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)m * a.ldo + n) =
+    const int mo = a.rows ? a.rows[m] : m;
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)mo * a.ldo + n) =
         make_uint2(pack_bf16x2(scalbnf(s.x, -sg) * f.x + d.x, scalbnf(s.y, -sg) * f.y + d.y),
                    pack_bf16x2(scalbnf(s.z, -sg) * f.z + d.z, scalbnf(s.w, -sg) * f.w + d.w));
 }
@@ -1650,6 +1676,10 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.f16 = L.f16 ? 1 : 0;
     a.tail = L.split_tail ? 1 : 0;  // launch_pair plans it
     a.ext = L.ext;
+    a.ents = L.ents;
+    a.ent_slot = L.ent_slot;
+    a.rows = L.rows;
+    if (L.rows && (L.epi != kEpiPlain || !L.pair || !dq)) return cudaErrorInvalidValue;
     a.out = L.out;
     a.ldo = L.epi == kEpiSwiGLU ? P.N / 2 : (L.epi == kEpiRaw && P.interleaved ? P.N / 2 : P.N);
     a.add = L.add;
@@ -1662,7 +1692,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.gc0 = L.gc0;
     a.gc1 = L.gc1;
     a.out_lo = L.out_lo;
-    const bool grad = L.epi == kEpiSwiGLUGrad, ext = L.add || L.gu_g || grad || L.ext || (dq && (L.f16 || L.split_tail));
+    const bool grad = L.epi == kEpiSwiGLUGrad, ext = L.add || L.gu_g || grad || L.ext || L.rows || (dq && (L.f16 || L.split_tail));
     if (L.ext && (!L.pair || !dq || L.f16 || !L.ext_a || !L.ext_b)) return cudaErrorInvalidValue;
     if (ext && (L.epi == kEpiRaw || (L.pair && !dq) || L.ldadd % 4 || (grad && (!L.gu_g || L.ncols > P.N))))
         return cudaErrorInvalidValue;
@@ -1711,9 +1741,9 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
                                  : launch_pair<kNVFP4, true>(map, bmap, map, bmap, a, pairs, std::max(num_sms, 2) / 2, s);
         CUtensorMap map2 = map, bmap2 = bmap;
         if (a.ext) {  // the adapters' steps: the same boxes over their own arrays
-            const cuuint64_t edims[2] = {(cuuint64_t)a.ext * BK, (cuuint64_t)L.M};
+            const cuuint64_t edims[2] = {(cuuint64_t)a.ext * BK, (cuuint64_t)(a.ents ? (size_t)L.entries * 2 * BM : L.M)};
             const cuuint64_t estrides[1] = {(cuuint64_t)a.ext * BK * 2};
-            const cuuint64_t ebdims[2] = {128, (cuuint64_t)(P.N / BN) * a.ext * BN};
+            const cuuint64_t ebdims[2] = {128, (cuuint64_t)(P.N / BN) * a.ext * BN * (a.ents ? L.slots : 1)};
             if (enc(&map2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(L.ext_a), edims, estrides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS ||

@@ -177,6 +177,13 @@ struct GemmTerms {
     const float* add_down = nullptr;
     cudaEvent_t ev = nullptr;
     std::function<cudaError_t(cudaStream_t)> before, between;
+    // or (tokens in the order of `rows`, x = their rows): further steps of the GEMMs
+    int ext = 0, ext_down = 0;
+    const void *v = nullptr, *img = nullptr, *img_down = nullptr;
+    const int2* ents = nullptr;
+    const int* ent_slot = nullptr;
+    int entries = 0, slots = 0;
+    const int* rows = nullptr;
 };
 qmlp_status run_gemm(qmlp_s* h, qmlp_path path, int stages, const void* x, int M, void* out, cudaStream_t s,
                      float* out_f32, const GemmTerms* ex);

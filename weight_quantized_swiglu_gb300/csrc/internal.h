@@ -209,6 +209,12 @@ struct GemmLaunch {
     int ext = 0;                 // CTA pairs: further contraction steps of 64, bf16: activations [M][64 ext]
     const void* ext_a = nullptr; // and stage images [N / 256][ext] (low-rank adapters)
     const void* ext_b = nullptr;
+    // several adapters: the entries of each 256-token tile {first, count}, their
+    // slots; ext_a then holds 256 rows an entry, ext_b the images slot by slot
+    const int2* ents = nullptr;
+    const int* ent_slot = nullptr;
+    int entries = 0, slots = 0;
+    const int* rows = nullptr;   // plain: the output row of each token
     void* out_lo = nullptr;      // with gu_g: optional, bf16 of what the rounding of out leaves
     bool images_ready = false;  // dequantise-once: wdec already holds w's images (no predecode launch)
 };

@@ -27,6 +27,8 @@ namespace {
 constexpr int kT = kLrTile;    // tokens of a tile
 constexpr int kThr = 128;      // 4 warps, 16 tokens each
 constexpr int kStep = 64;      // contraction length of a step
+constexpr int kPlanTable = 128;  // groups that the plan counts warp by warp
+constexpr int kLrMaxEnts = 256;  // 256-token tiles of the plan: 65536 tokens
 
 QMLP_DEV void cp16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -83,7 +85,8 @@ QMLP_DEV void split_bf16(float v, __nv_bfloat16 (&w)[NW]) {
 }
 
 // The tile of this CTA: slot, first position, tokens. False: no such tile.
-QMLP_DEV bool tile_of(const LrTokens& t, int i, int& slot, int& pos0, int& n) {
+QMLP_DEV bool tile_of(const LrTokens& t, int i, int& slot, int& pos0, int& n, int& entry0) {
+    entry0 = 0;
     if (!t.tiles) {
         slot = 0;
         pos0 = i * kT;
@@ -95,6 +98,7 @@ QMLP_DEV bool tile_of(const LrTokens& t, int i, int& slot, int& pos0, int& n) {
     slot = e.x;
     pos0 = e.y;
     n = e.z;
+    entry0 = e.w;
     return true;
 }
 
@@ -146,8 +150,8 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
     extern __shared__ __align__(128) uint8_t smem[];
     pdl_launch_dependents();
     pdl_wait();
-    int slot, pos0, n;
-    if (!tile_of(a.tok, blockIdx.x, slot, pos0, n) || slot < 0) return;
+    int slot, pos0, n, entry0;
+    if (!tile_of(a.tok, blockIdx.x, slot, pos0, n, entry0) || slot < 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int z = blockIdx.z;
     const __nv_bfloat16* x = a.x + (size_t)z * a.x_z;
@@ -191,8 +195,14 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
                 if (TWO) cp16(swt + S::W + sw<NC / 8>(r, c), w2 + off, live);
             } else {
                 const int r = k >> 3, c = k & 7, d = d0 + c * 8;
-                const bool live = d < a.D;
-                cp16(swt + sw<8>(r, c), w + (live ? (size_t)r * a.D + d : 0), live);
+                bool live = d < a.D;
+                const __nv_bfloat16* src = w + (size_t)r * a.D;
+                if (!a.w) {
+                    const int part = r >= a.R, j = r - part * a.R;
+                    src = a.wa[part] + (size_t)j * a.D;
+                    live = live && a.wa[part] && j < a.r;
+                }
+                cp16(swt + sw<8>(r, c), live ? src + d : x, live);
             }
         }
         cp_commit();
@@ -251,7 +261,7 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
                 make_float2(acc[j][2 * h], acc[j][2 * h + 1]);
     if (ns > 1) cluster_sync();
     else __syncthreads();
-    const float c = a.scale ? a.scale[slot] : 1.0f;
+    const float c = a.scale ? a.scale[slot] : a.scale_all;
     // this CTA's share of the rows, four columns a thread and round
     const int rows = kT / ns, r0 = blockIdx.y * rows;
     for (int i = tid; i < rows * (NC / 4); i += kThr) {
@@ -267,7 +277,9 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
             split_bf16(val[e], w[e]);
             if (a.again) w[e][2] = w[e][0];
         }
-        __nv_bfloat16* o = a.v + (size_t)(pos0 + row) * a.ldv + z * NC + col;
+        const int pos = pos0 + row;
+        __nv_bfloat16* line = a.v + (size_t)(a.entries ? (entry0 + (pos >> 8)) * 256 + (pos & 255) : pos) * a.ldv;
+        __nv_bfloat16* o = line + z * NC + col;
 #pragma unroll
         for (int k = 0; k < kLrWords; ++k)
             if (k < a.words) {
@@ -276,7 +288,7 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
             }
         // the columns past the words of a row that a GEMM reads whole
         for (int p = col + z * NC; p < a.pad; p += NC * gridDim.z)
-            *reinterpret_cast<uint2*>(a.v + (size_t)(pos0 + row) * a.ldv + a.ldv - a.pad + p) = make_uint2(0, 0);
+            *reinterpret_cast<uint2*>(line + a.ldv - a.pad + p) = make_uint2(0, 0);
     }
     if (ns > 1) cluster_sync();  // no CTA leaves while another reads its tile
 }
@@ -296,8 +308,8 @@ __global__ void __launch_bounds__(kThr) expand_kernel(const LrExpand a) {
     extern __shared__ __align__(128) uint8_t smem[];
     pdl_launch_dependents();
     pdl_wait();
-    int slot, pos0, n;
-    if (!tile_of(a.tok, blockIdx.x, slot, pos0, n)) return;
+    int slot, pos0, n, entry0;
+    if (!tile_of(a.tok, blockIdx.x, slot, pos0, n, entry0)) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int z = blockIdx.z;
     const int n0 = blockIdx.y * kNB, n1 = min(a.N, n0 + kNB);
@@ -612,14 +624,16 @@ __global__ void __launch_bounds__(256) swiglu_raw_kernel(const LrSwiGLU a) {
 
 // Tokens grouped by slot: perm holds the tokens slot by slot (those without an
 // adapter last), tiles the {slot or -1, first position, tokens} of at most 64.
-// One CTA; the order of a slot's tokens is left to the atomics (no result
-// depends on it).
+// One CTA; the order of a slot's tokens is left to the atomics where no result
+// depends on it.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids, int M, int slots,
                                                     const int* __restrict__ rank, int* perm, int4* tiles,
-                                                    int* n_tiles) {
+                                                    int* n_tiles, int2* ents, int* ent_slot) {
     __shared__ int cnt[kLrMaxSlots + 1], pos[kLrMaxSlots + 1];
-    __shared__ int wsum[2][32];
+    __shared__ int wsum[3][32];
+    __shared__ int first[kLrMaxEnts], last[kLrMaxEnts];
+    __shared__ int wcnt[32 * kPlanTable];
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -639,8 +653,15 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids,
     };
     for (int m = tid; m < (M + 31) / 32 * 32; m += 1024) claim(cnt, m < M ? group(m) : -1);
     __syncthreads();
-    // exclusive sums over the groups of tokens and of tiles, 1024 groups a round
-    int tok0 = 0, til0 = 0;
+    const int big = (M + 255) / 256;
+    if (ents)
+        for (int t = tid; t < big; t += 1024) first[t] = 0, last[t] = -1;
+    const int with = M - cnt[slots];  // tokens with an adapter: positions 0 .. with - 1
+    __syncthreads();
+    // exclusive sums over the groups of tokens, tiles and entries, 1024 groups a
+    // round. A group's entries: one for each 256 positions that it reaches into,
+    // which its first position has to be known for: a second scan
+    int tok0 = 0, til0 = 0, ent0 = 0;
     for (int b = 0; b <= slots; b += 1024) {
         const int i = b + tid;
         const int c = i <= slots ? cnt[i] : 0, tl = (c + kT - 1) / kT;
@@ -657,21 +678,95 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids,
             if (w < warp) bc += wsum[0][w], bt += wsum[1][w];
             ac += wsum[0][w], at += wsum[1][w];
         }
-        if (i <= slots) {
-            const int p0 = bc + sc - c;
-            pos[i] = p0;
-            for (int k = 0; k < tl; ++k)
-                tiles[bt + st - tl + k] = make_int4(i < slots ? i : -1, p0 + k * kT, min(kT, c - k * kT), 0);
+        const int p0 = bc + sc - c;
+        const int ne = ents && c && i < slots ? ((p0 + c - 1) >> 8) - (p0 >> 8) + 1 : 0;
+        int se = ne;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, se, o);
+            if (lane >= o) se += v;
         }
+        if (lane == 31) wsum[2][warp] = se;
+        __syncthreads();
+        int be = ent0, ae = 0;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) be += wsum[2][w];
+            ae += wsum[2][w];
+        }
+        if (i <= slots) {
+            pos[i] = p0;
+            const int e0 = be + se - ne;  // its first entry
+            for (int k = 0; k < tl; ++k)
+                tiles[bt + st - tl + k] =
+                    make_int4(i < slots ? i : -1, p0 + k * kT, min(kT, c - k * kT), e0 - (p0 >> 8));
+            for (int k = 0; k < ne; ++k) {
+                // positions are filled from 0 on: a tile's entries lie together,
+                // from the group at its first position to that at its last
+                const int t = (p0 >> 8) + k, lo = t * 256, hi = min(lo + 256, with) - 1;
+                ent_slot[e0 + k] = i;
+                if (p0 <= lo) first[t] = e0 + k;
+                if (p0 + c - 1 >= hi) last[t] = e0 + k;
+            }
+        }
+        ent0 += ae;
         tok0 += ac;
         til0 += at;
         __syncthreads();
     }
-    for (int m = tid; m < (M + 31) / 32 * 32; m += 1024) {
-        const int at = claim(pos, m < M ? group(m) : -1);
-        if (m < M) perm[at] = m;
+    if (!ents) {
+        for (int m = tid; m < (M + 31) / 32 * 32; m += 1024) {
+            const int at = claim(pos, m < M ? group(m) : -1);
+            if (m < M) perm[at] = m;
+        }
+        if (tid == 0) *n_tiles = til0;
+        return;
+    }
+    // With GEMM lists the order within a group is the tokens': the position
+    // decides which tile, and so which order of sums. For few groups the warps'
+    // counts of 1024 tokens are scanned together, for many the warps claim in turn
+    // (3001 tokens, 7 slots: 30 us in turn)
+    const bool table = slots < kPlanTable;
+    for (int b = 0; b < M; b += 1024) {
+        const int m = b + tid, gr = m < M ? group(m) : -1;
+        if (table) {
+            for (int i = tid; i < 32 * kPlanTable; i += 1024) wcnt[i] = 0;
+            __syncthreads();
+            const unsigned mask = __match_any_sync(0xffffffffu, gr);
+            if (gr >= 0 && lane == __ffs(mask) - 1) wcnt[warp * kPlanTable + gr] = __popc(mask);
+            __syncthreads();
+            if (tid <= slots) {
+                int at = pos[tid];
+                for (int w = 0; w < 32; ++w) {
+                    const int n = wcnt[w * kPlanTable + tid];
+                    wcnt[w * kPlanTable + tid] = at;
+                    at += n;
+                }
+                pos[tid] = at;
+            }
+            __syncthreads();
+            if (m < M) perm[wcnt[warp * kPlanTable + gr] + __popc(mask & ((1u << lane) - 1u))] = m;
+            __syncthreads();
+        } else {
+            for (int w = 0; w < 32 && b + w * 32 < M; ++w) {
+                if (w == warp) {
+                    const int at = claim(pos, gr);
+                    if (m < M) perm[at] = m;
+                }
+                __syncthreads();
+            }
+        }
     }
     if (tid == 0) *n_tiles = til0;
+    for (int t = tid; t < big; t += 1024) ents[t] = make_int2(first[t], last[t] - first[t] + 1);
+}
+
+__global__ void __launch_bounds__(256) gather_kernel(const uint4* __restrict__ x, const int* __restrict__ perm, int n16,
+                                                     uint4* rows) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint4* src = x + (size_t)perm[blockIdx.x] * n16;
+    uint4* dst = rows + (size_t)blockIdx.x * n16;
+    for (int i = threadIdx.x; i < n16; i += 256) dst[i] = src[i];
 }
 
 // One adapter into a slot's padded rows: A [r, D] -> [Rp][D], B [N, r] ->
@@ -857,9 +952,14 @@ cudaError_t launch_lr_swiglu_raw(const LrSwiGLU& a, cudaStream_t s) {
 }
 
 cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, int* perm, int4* tiles, int* n_tiles,
-                           cudaStream_t s) {
-    if (slots < 1 || slots > kLrMaxSlots) return cudaErrorInvalidValue;
-    plan_kernel<<<1, 1024, 0, s>>>(ids, M, slots, rank, perm, tiles, n_tiles);
+                           int2* ents, int* ent_slot, cudaStream_t s) {
+    if (slots < 1 || slots > kLrMaxSlots || (ents && M > 256 * kLrMaxEnts)) return cudaErrorInvalidValue;
+    plan_kernel<<<1, 1024, 0, s>>>(ids, M, slots, rank, perm, tiles, n_tiles, ents, ent_slot);
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_lr_gather(const void* x, const int* perm, int M, int K, void* rows, cudaStream_t s) {
+    gather_kernel<<<M, 256, 0, s>>>(static_cast<const uint4*>(x), perm, K / 8, static_cast<uint4*>(rows));
     return cudaPeekAtLastError();
 }
 

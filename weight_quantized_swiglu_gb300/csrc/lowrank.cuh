@@ -17,7 +17,7 @@ constexpr int kLrFew = 64;
 
 // Which tokens a tile holds: tiles null: one adapter, 64 consecutive tokens.
 struct LrTokens {
-    const int4* tiles = nullptr;  // {slot or -1, first position, tokens}
+    const int4* tiles = nullptr;  // {slot or -1, first position, tokens, entry of position p minus p / 256}
     const int* n_tiles = nullptr;
     const int* perm = nullptr;    // position -> token
     int M = 0;
@@ -32,11 +32,17 @@ struct LrShrink {
     const __nv_bfloat16* w = nullptr;     // slot and part strides in elements
     const __nv_bfloat16* w_lo = nullptr;  // second word of w, or null
     size_t w_slot = 0, w_z = 0;
-    const float* scale = nullptr;  // per slot
+    // or, not transposed, an adapter's own A's: row j of part p at wa[p] + j D, r
+    // rows (the columns from r to R of a part are zero)
+    const __nv_bfloat16* wa[2] = {nullptr, nullptr};
+    int r = 0, R = 0;
+    const float* scale = nullptr;  // per slot, or
+    float scale_all = 1.0f;
     __nv_bfloat16* v = nullptr;    // [position][ldv], columns z * NC on, word i at i * v_word elements
     size_t v_word = 0;
     int ldv = 0;
     int words = kLrWords;
+    bool entries = false;          // rows by GEMM entry: 256 entry(p) + p % 256 for position p
     bool again = false;            // the third word is the first once more
     int pad = 0;                   // columns at a row's end to fill with zeros
     float mul0 = 1.0f, mul1 = 1.0f;  // factors of the columns before and from `half` on
@@ -150,8 +156,13 @@ cudaError_t launch_lr_expand(const LrExpand& a, int rc, bool trans, int tiles, i
 cudaError_t launch_lr_shrink_few(const LrFew& a, int M, cudaStream_t s);
 cudaError_t launch_lr_expand_few(const LrFew& a, int M, int zs, cudaStream_t s);
 cudaError_t launch_lr_swiglu_raw(const LrSwiGLU& a, cudaStream_t s);
+// With ents: the GEMM's lists too, the entries {first, count} of each 256-token
+// tile and the entries' slots; at most lr_max_entries of them.
 cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, int* perm, int4* tiles, int* n_tiles,
-                           cudaStream_t s);
+                           int2* ents, int* ent_slot, cudaStream_t s);
+inline int lr_max_entries(int M, int slots) { return (M + 255) / 256 + std::min(slots, M); }
+// rows[p] = x[perm[p]] of K bf16 values (a multiple of 8).
+cudaError_t launch_lr_gather(const void* x, const int* perm, int M, int K, void* rows, cudaStream_t s);
 cudaError_t launch_lr_pack(const LrPack& a, cudaStream_t s);
 
 }  // namespace qmlp
