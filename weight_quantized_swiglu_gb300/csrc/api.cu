@@ -410,8 +410,13 @@ qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M
             cudaEventRecord(h->ev_join, h->side) != cudaSuccess || ex->before(s) != cudaSuccess ||
             cudaStreamWaitEvent(s, ex->ev, 0) != cudaSuccess)
             return QMLP_ERR_CUDA;
-    } else if (ex && ex->before(s) != cudaSuccess) {
-        return QMLP_ERR_CUDA;
+    } else if (ex) {
+        // the decoder warps' GEMM starts beside the adapters' products (see GemmLaunch::early)
+        if (!g.wdec) {
+            if (launch_gemm_prescale(x, M, h->K, h->a16, h->sig, h->num_sms, s) != cudaSuccess) return QMLP_ERR_CUDA;
+            g.prescaled = g.early = true;
+        }
+        if (ex->before(s) != cudaSuccess) return QMLP_ERR_CUDA;
     }
     if (fork && !ex && (launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s) != cudaSuccess ||
                  cudaEventRecord(h->ev_fork, s) != cudaSuccess ||
@@ -445,6 +450,8 @@ qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M
             g.wdec_bytes = h->wdec2_bytes;
         }
         if (ex) {
+            if (!g.wdec && launch_gemm_prescale(h->act, M, h->I, h->a16, h->sig, h->num_sms, s) != cudaSuccess)
+                return QMLP_ERR_CUDA;
             if (ex->between(s) != cudaSuccess) return QMLP_ERR_CUDA;
             g.add = ex->add_down;
             g.split_tail = g.pair && g.wdec;

@@ -747,6 +747,7 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
         return dq ? launch_gemm_predecode(h->gm_d, h->wdec2, h->wdec2_bytes, h->num_sms, b) : cudaSuccess;
     }));
     if (dq) TRY(launch_gemm_predecode(h->gm_gu, h->wdec, h->wdec_bytes, h->num_sms, s));
+    else TRY(launch_gemm_prescale(x, M, K, h->a16, h->sig, h->num_sms, s));
     if (ad) {
         own = own_a(ad);
         if (!own || !ext) TRY(launch_lr_pack(pack_train(t, ad, false, !ext), s));
@@ -773,6 +774,8 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     g.w = h->gm_gu;
     g.wdec = dq ? h->wdec : nullptr;
     g.wdec_bytes = h->wdec_bytes;
+    g.prescaled = !dq;
+    g.early = ad && !ext;
     g.a = x;
     g.out = v.act;
     g.gu_g = v.g;
@@ -783,6 +786,8 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
         else add_terms(g, l->y, (size_t)2 * I);
     }
     TRY(launch_gemm(g, h->num_sms, s));
+    TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
+    if (!dq) TRY(launch_gemm_prescale(v.act, M, I, h->a16, h->sig, h->num_sms, s));
     if (ad) {
         LrShrink a = shrink_all(ad, v.act, M, I, v.vd);
         a.x_lo = v.act_lo;
@@ -797,8 +802,9 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
         TRY(launch_lr_shrink(a, R, false, tiles_for(M), 1, h->num_sms, s));
         if (!ext) TRY(expand_all(t, v.vd, M, R, 1, l->b_d, 0, K, false, s));
     }
-    TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
     g = dq_gemm(t, M);
+    g.prescaled = !dq;
+    g.early = ad && !ext;
     g.epi = kEpiPlain;
     g.w = h->gm_d;
     g.wdec = dq ? h->wdec2 : nullptr;
@@ -845,6 +851,7 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
         return launch_gemm_predecode_t(h->gm_gu, t->row, t->row ? t->row + I : nullptr, false, h->wdec, h->wdec_bytes, b);
     }));
     TRY(launch_gemm_predecode_t(h->gm_d, t->mul_d, nullptr, fp8, t->img_t, t->img_t_bytes, s));
+    if (fp8) TRY(launch_gemm_prescale(dy, M, K, h->a16, h->sig, h->num_sms, s));
     if (ad) {
         own = own_b(t, ad) && !fp8 && ext;
         if (!own) TRY(launch_lr_pack(pack_train(t, ad, true, !ext_d || !ext), s));
@@ -860,7 +867,8 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     g.epi = kEpiSwiGLUGrad;
     g.w.fmt = kNVFP4;  // one factor for all columns
     g.w.inv_g0 = fp8 ? t->fac_d : h->gv[2].inv_g;
-    g.f16 = fp8;
+    g.f16 = g.prescaled = fp8;
+    g.early = ad && !ext_d;
     g.w.N = (I + 255) / 256 * 256;
     g.w.K = K;
     g.wdec = t->img_t;
@@ -881,6 +889,7 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
         else add_terms(g, l->y, I);
     }
     TRY(launch_gemm(g, h->num_sms, s));
+    TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
     if (ad) {
         LrShrink a = shrink_all(ad, t->dgu, M, I, wv);
         a.x_lo = lo;
@@ -900,8 +909,8 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
         TRY(launch_lr_shrink(a, R, true, tiles_for(M), 2, h->num_sms, s));
         if (!ext) TRY(expand_all(t, wv, M, 2 * R, 1, l->a_gu, 0, K, true, s));
     }
-    TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
     g = dq_gemm(t, M);
+    g.early = ad && !ext;
     g.epi = kEpiPlain;
     g.w.fmt = kNVFP4;
     g.w.N = K;

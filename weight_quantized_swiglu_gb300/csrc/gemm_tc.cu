@@ -159,6 +159,7 @@ struct Args {
     // e.. of [..][64 ext], its images [Nt][ext] those of slot ent_slot[e]. A
     // 256-token tile t has the entries ents[t] = {first, count}; without lists
     // each has entry t and slot 0.
+    int early;             // launched beside the kernels that write `add`
     int ext;
     const int2* ents;
     const int* ent_slot;
@@ -258,7 +259,9 @@ QMLP_DEV void store16(__nv_bfloat16* dst, const uint32_t (&v)[8]) {
 // EXT: the instances of low-rank adapters, which add their fp32 terms.
 template <int FMT, bool EXT>
 QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg, int nt, int first, int step) {
-    // this warp's columns: 32 from each of first, first + step, ...
+    // this warp's columns: 32 from each of first, first + step, ... (the adapters'
+    // terms may still be on their way when the main loop starts: Args::early)
+    if (EXT && a.early) pdl_wait();
     // 2^-sg, for the instances whose every factor is one product
     const float pw = sg >= -126 && sg <= 126 ? __int_as_float((127 - sg) << 23) : scalbnf(1.0f, -sg);
     if (a.epi == kEpiSwiGLU) {
@@ -1530,9 +1533,20 @@ cudaError_t launch_inst(const CUtensorMap& map, const Args& a, int grid, cudaStr
         if (e != cudaSuccess) return e;
         attr = true;
     }
-    if (a.splits > 1) gemm_kernel<FMT, true, PRE><<<grid, kThreads, bytes, s>>>(map, a);
-    else gemm_kernel<FMT, false, PRE, EXT><<<grid, kThreads, bytes, s>>>(map, a);
-    return cudaPeekAtLastError();
+    // early: the kernels before this one that write `add` may still run; nothing
+    // but the epilogue (or, split, the reduce kernel) needs them
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = a.early ? 1 : 0;
+    return a.splits > 1 ? cudaLaunchKernelEx(&cfg, gemm_kernel<FMT, true, PRE>, map, a)
+                        : cudaLaunchKernelEx(&cfg, gemm_kernel<FMT, false, PRE, EXT>, map, a);
 }
 
 // The projection's weight blocks -> their decoded images in wdec (= a.wdec,
@@ -1623,6 +1637,12 @@ cudaError_t repack_fp8_gemm(const uint8_t* w0, const uint8_t* w1, int N, int K, 
     return cudaPeekAtLastError();
 }
 
+cudaError_t launch_gemm_prescale(const void* a, int M, int K, void* a16, int* sig, int num_sms, cudaStream_t s) {
+    const int grid = std::min(M, 8 * std::max(num_sms, 1));
+    prescale_rows_kernel<<<grid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(a), static_cast<__half*>(a16), sig, M, K);
+    return cudaPeekAtLastError();
+}
+
 cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     const GemmProj& P = L.w;
     if (!gemm_supported(P.K, P.N) || L.M < 1 || !L.a16 || !L.sig) return cudaErrorInvalidValue;
@@ -1636,11 +1656,8 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
 
     // 1. per-token fp16 prescale of the activations (decoder-warp GEMMs,
     //    whose decoders write fp16 weights)
-    if (!dq || L.f16) {
-        const int pgrid = std::min(L.M, 8 * std::max(num_sms, 1));
-        prescale_rows_kernel<<<pgrid, 256, 0, s>>>(static_cast<const __nv_bfloat16*>(L.a),
-                                                    static_cast<__half*>(L.a16), L.sig, L.M, P.K);
-        cudaError_t e = cudaPeekAtLastError();
+    if ((!dq || L.f16) && !L.prescaled) {
+        const cudaError_t e = launch_gemm_prescale(L.a, L.M, P.K, L.a16, L.sig, num_sms, s);
         if (e != cudaSuccess) return e;
     }
 
@@ -1675,6 +1692,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.sig = bf ? nullptr : L.sig;
     a.f16 = L.f16 ? 1 : 0;
     a.tail = L.split_tail ? 1 : 0;  // launch_pair plans it
+    a.early = L.early && L.add && !L.pair;
     a.ext = L.ext;
     a.ents = L.ents;
     a.ent_slot = L.ent_slot;

@@ -197,6 +197,11 @@ struct GemmLaunch {
     uint8_t* wdec = nullptr;  // dequantise-once: decoded stage images of w (null: the decoder warps decode)
     size_t wdec_bytes = 0;    // bytes of wdec, >= gemm_decoded_bytes(w.N, w.K)
     const float* add = nullptr;  // fp32 [M][ldadd], added after the factor: gate's I columns then up's
+    // early: the kernels that write add are launched just before, each with
+    // programmatic dependent launch, behind one that is not; nothing else that the
+    // GEMM reads (prescaled activations, images) comes from them
+    bool early = false;
+    bool prescaled = false;      // a16 and sig are written (launch_gemm_prescale)
     size_t ldadd = 0;            // (SwiGLU), or the output's columns (plain, grad); low-rank adapters
     void* gu_g = nullptr;        // training: fp32 gate and up values, kept by SwiGLU and read by SwiGLUGrad,
     void* gu_u = nullptr;        // gemm_gu_bytes(M, I) each
@@ -219,6 +224,7 @@ struct GemmLaunch {
     bool images_ready = false;  // dequantise-once: wdec already holds w's images (no predecode launch)
 };
 constexpr int kPairMinM = 256;  // one 256-token tile of a CTA pair
+cudaError_t launch_gemm_prescale(const void* a, int M, int K, void* a16, int* sig, int num_sms, cudaStream_t s);
 cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s);
 size_t gemm_splitk_ws_elems(int num_sms);
 size_t gemm_decoded_bytes(int N, int K);  // bf16 stage images of an [N, K] projection (2 N K bytes)
