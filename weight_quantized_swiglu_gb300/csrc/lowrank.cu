@@ -578,18 +578,24 @@ __global__ void __launch_bounds__(kThr) shrink_few_kernel(const LrFew a) {
         a.v[(size_t)m * a.ncol + j] = has ? (red[0] + red[1] + red[2] + red[3]) * a.scale[slot] : 0.0f;
 }
 
-// y[m, n] = sum_j v[m, j] B[slot(m)][n][j]: a thread an n, the tokens in turn.
+// y[m, n] = sum_j v[m, j] B[slot(m)][n][j]: a thread an n, kFewTok tokens in turn
+// (so few CTAs that all are resident at once: the GEMM after them then starts
+// beside them).
+constexpr int kFewTok = 8;
 __global__ void __launch_bounds__(kThr) expand_few_kernel(const LrFew a) {
     pdl_launch_dependents();
-    const int n = blockIdx.x * kThr + threadIdx.x, z = blockIdx.z, m = blockIdx.y;
+    const int n = blockIdx.x * kThr + threadIdx.x, z = blockIdx.z, m0 = blockIdx.y * kFewTok;
     pdl_wait();
     if (n >= a.D) return;
-    const int slot = a.ids[m];
-    float s = 0.0f;
-    if (slot >= 0 && slot < a.slots && a.rank[slot] > 0) {
-        const uint4* b = reinterpret_cast<const uint4*>(a.w + (size_t)slot * a.w_slot + ((size_t)z * a.D + n) * a.Rp);
+    const float f = a.factor ? a.factor[n] : a.factor_all;
+#pragma unroll 2
+    for (int m = m0; m < min(a.M, m0 + kFewTok); ++m) {
+        const int slot = a.ids[m];
+        const int nr = slot >= 0 && slot < a.slots ? (a.rank[slot] + 7) / 8 : 0;
+        const uint4* b = reinterpret_cast<const uint4*>(a.w + (size_t)(nr ? slot : 0) * a.w_slot + ((size_t)z * a.D + n) * a.Rp);
         const float* v = a.v + (size_t)m * a.ncol + z * a.Rp;
-        const int nr = (a.rank[slot] + 7) / 8;
+        float s = 0.0f;
+#pragma unroll 2
         for (int i = 0; i < nr; ++i) {
             const uint4 q = __ldg(b + i);
             const uint32_t y[4] = {q.x, q.y, q.z, q.w};
@@ -599,12 +605,8 @@ __global__ void __launch_bounds__(kThr) expand_few_kernel(const LrFew a) {
                 s = fmaf(v[i * 8 + 2 * e + 1], __uint_as_float(y[e] & 0xFFFF0000u), s);
             }
         }
-    }
-    if (a.out) {
-        const float f = a.factor ? a.factor[n] : a.factor_all;
-        a.out[(size_t)m * a.D + n] = __float2bfloat16_rn(a.raw[(size_t)m * a.D + n] * f + s);
-    } else {
-        a.y[(size_t)m * a.ldy + (size_t)z * a.D + n] = s;
+        if (a.out) a.out[(size_t)m * a.D + n] = __float2bfloat16_rn(a.raw[(size_t)m * a.D + n] * f + s);
+        else a.y[(size_t)m * a.ldy + (size_t)z * a.D + n] = s;
     }
 }
 
@@ -943,7 +945,9 @@ cudaError_t launch_lr_shrink_few(const LrFew& a, int M, cudaStream_t s) {
     return launch_pdl(shrink_few_kernel, dim3(a.ncol, M), kThr, 0, a, s);
 }
 cudaError_t launch_lr_expand_few(const LrFew& a, int M, int zs, cudaStream_t s) {
-    return launch_pdl(expand_few_kernel, dim3((a.D + kThr - 1) / kThr, M, zs), kThr, 0, a, s);
+    LrFew b = a;
+    b.M = M;
+    return launch_pdl(expand_few_kernel, dim3((a.D + kThr - 1) / kThr, (M + kFewTok - 1) / kFewTok, zs), kThr, 0, b, s);
 }
 
 cudaError_t launch_lr_swiglu_raw(const LrSwiGLU& a, cudaStream_t s) {

@@ -71,6 +71,7 @@ struct LrFew {
     const int* rank = nullptr;
     const float* scale = nullptr;
     int slots = 0, Rp = 0;
+    int M = 0;  // expand: set by the launch
     bool late = false;
     const __nv_bfloat16* x = nullptr;  // shrink: [M][D]
     const __nv_bfloat16* w = nullptr;
