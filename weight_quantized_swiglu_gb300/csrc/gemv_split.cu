@@ -281,7 +281,7 @@ QMLP_DEV void lr_warps(const SplitLora& lr, int M, int I, int tslice, int tid, f
     named_bar_sync(2, kLT);
     // B v: an item a (token, gate or up, row)
     const int items = M * 2 * tslice;
-    constexpr int kU = 8;  // items whose rows are in flight together
+    constexpr int kU = 4;  // items whose rows are in flight together (more cost the consumers registers)
     for (int b = tid; b < items; b += kU * kLT) {
         float s[kU];
         const uint4* row[kU];
@@ -362,15 +362,13 @@ QMLP_DEV void lr_warps(const SplitLora& lr, int M, int I, int tslice, int tid, f
     }
     mbar_arrive(bar0 + 16);
 }
-// c A_d act of token m into s_vd[Rp] by `nthr` threads (a multiple of Rp, at
-// most 512; tmp holds as many floats): each adds every (nthr / Rp)-th CTA's
-// share, then the first Rp threads add those sums; the caller's barrier `sync`
-// stands between and after.
+// c A_d act of token m (its slot, its rank in eights) into s_vd[Rp] by `nthr`
+// threads (a multiple of Rp, at most 512; tmp holds as many floats): each adds
+// every (nthr / Rp)-th CTA's share, then up to eight lanes a value add those sums;
+// the caller's barrier `sync` stands between and after.
 template <typename Sync>
-QMLP_DEV void lr_down_sum(const SplitLora& lr, int G, int M, int m, int tid, int nthr, float* tmp, float* s_vd,
-                          const Sync& sync) {
-    int slot;
-    const int n8 = lr_slot(lr, m, slot);
+QMLP_DEV void lr_down_sum(const SplitLora& lr, int G, int M, int m, int slot, int n8, int tid, int nthr, float* tmp,
+                          float* s_vd, const Sync& sync) {
     const int j = tid % lr.Rp, b0 = tid / lr.Rp, nb = nthr / lr.Rp;
     float s = 0.0f;
     if (j < 8 * n8) {
@@ -380,21 +378,27 @@ QMLP_DEV void lr_down_sum(const SplitLora& lr, int G, int M, int m, int tid, int
     }
     tmp[tid] = s;
     sync();
-    if (tid < lr.Rp) {
+    const int gl = min(8, nb);  // lanes a value
+    if (tid < gl * lr.Rp) {
+        const int v = tid / gl;
         float t = 0.0f;
-        for (int b = 0; b < nb; ++b) t += tmp[b * lr.Rp + tid];
-        s_vd[tid] = n8 ? t * __ldg(lr.scale + slot) : 0.0f;
+        for (int b = tid % gl; b < nb; b += gl) t += tmp[b * lr.Rp + v];
+        const unsigned mask = __activemask();  // whole groups of lanes
+        for (int o = gl / 2; o > 0; o >>= 1) t += __shfl_xor_sync(mask, t, o);
+        if (tid % gl == 0) s_vd[v] = n8 ? t * __ldg(lr.scale + slot) : 0.0f;
     }
     sync();
 }
-// B_d[n] . s_vd
-QMLP_DEV float lr_down_dot(const SplitLora& lr, int K, int m, int n, const float* s_vd) {
-    int slot;
-    const int n8 = lr_slot(lr, m, slot);
+// B_d[n] . s_vd, the row's first 16 values in q0 and q1.
+QMLP_DEV float lr_down_dot(const SplitLora& lr, int K, int slot, int n8, int n, const uint4& q0, const uint4& q1,
+                           const float* s_vd) {
     float s = 0.0f;
-    const uint4* b = reinterpret_cast<const uint4*>(lr.b_d + ((size_t)(n8 ? slot : 0) * K + n) * lr.Rp);
+    if (!n8) return s;
+    s = lr_fma8(q0, s_vd, s);
+    if (n8 > 1) s = lr_fma8(q1, s_vd + 8, s);
+    const uint4* b = reinterpret_cast<const uint4*>(lr.b_d + ((size_t)slot * K + n) * lr.Rp);
 #pragma unroll 2
-    for (int i = 0; i < n8; ++i) s = lr_fma8(__ldg(b + i), s_vd + 8 * i, s);
+    for (int i = 2; i < n8; ++i) s = lr_fma8(__ldg(b + i), s_vd + 8 * i, s);
     return s;
 }
 // Its row on the way to L2.
@@ -1089,10 +1093,21 @@ __global__ void __launch_bounds__(thr(LR), 1) gemv_split_kernel(const __grid_con
     }
     // LR (one token): the sum of the CTAs' shares of A_d act, behind the scratch
     float* s_vd = red + (size_t)nu * kW * 32;
-    if (LR)
-        lr_down_sum(a.lr, a.G, M, 0, threadIdx.x, kCT, s_vd + 64, s_vd, [] { named_bar_sync(1, kCT); });
-    else
+    int lslot = 0, ln8 = 0;
+    uint4 bq0 = make_uint4(0, 0, 0, 0), bq1 = bq0;
+    if (LR) {
+        // B_d's row of this warp's (first) unit beside the shares
+        ln8 = lr_slot(a.lr, 0, lslot);
+        const int n = (blockIdx.x + warp * gridDim.x) * 32 + lane;
+        if (ln8 && warp < nu && n < a.K) {
+            const uint4* b = reinterpret_cast<const uint4*>(a.lr.b_d + ((size_t)lslot * a.K + n) * a.lr.Rp);
+            bq0 = __ldg(b);
+            bq1 = __ldg(b + 1);
+        }
+        lr_down_sum(a.lr, a.G, M, 0, lslot, ln8, threadIdx.x, kCT, s_vd + 64, s_vd, [] { named_bar_sync(1, kCT); });
+    } else {
         named_bar_sync(1, kCT);
+    }
     for (int i = warp; i < nu; i += kW) {
         const int u = blockIdx.x + i * gridDim.x;
         const int m = u / units_n, n = (u % units_n) * 32 + lane;
@@ -1105,7 +1120,14 @@ __global__ void __launch_bounds__(thr(LR), 1) gemv_split_kernel(const __grid_con
             } else {
                 const float sd = FMT == kNVFP4 ? a.invd : a.chsd[n];
                 float o = tot * sd;
-                if (LR) o += lr_down_dot(a.lr, a.K, m, n, s_vd);
+                if (LR) {
+                    if (i != warp && ln8) {
+                        const uint4* b = reinterpret_cast<const uint4*>(a.lr.b_d + ((size_t)lslot * a.K + n) * a.lr.Rp);
+                        bq0 = __ldg(b);
+                        bq1 = __ldg(b + 1);
+                    }
+                    o += lr_down_dot(a.lr, a.K, lslot, ln8, n, bq0, bq1, s_vd);
+                }
                 a.out[(size_t)m * a.K + n] = __float2bfloat16_rn(o);
             }
         }
@@ -1224,7 +1246,7 @@ __global__ void __launch_bounds__(kRedThr) gemv_split_reduce_lr_kernel(const __g
     }
     red[2 * grp][col] = s0;
     red[2 * grp + 1][col] = s1;
-    lr_down_sum(a.lr, a.G, a.M, m, threadIdx.x, kRedThr, s_tmp, s_vd, [] { __syncthreads(); });
+    lr_down_sum(a.lr, a.G, a.M, m, slot, n8, threadIdx.x, kRedThr, s_tmp, s_vd, [] { __syncthreads(); });
     float d = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
