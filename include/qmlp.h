@@ -429,8 +429,12 @@ typedef struct qmlp_lora_s qmlp_lora_t;
 
 /* Make `slots` empty adapter slots of ranks up to max_rank for the handle h,
  * which must outlive them. Holds slots * 3 (K + I) * R bf16 values, R = 16, 32
- * or 64 (max_rank rounded up), and a workspace for h's max_M tokens. The slots
- * share h's workspace: calls on them and on h go on one stream at a time.
+ * or 64 (max_rank rounded up), 4 max(2 I, K) bytes a token of h's max_M for the
+ * adapters' terms, and where h has the dequantise-once GEMM (and all its factors
+ * are at least 2^-60) the adapters once more as images for it (two to seven times
+ * the padded copies, up to 4 GiB; past that calls do without) and 2 K bytes a
+ * token. The slots share h's workspace: calls on them and on h go on one stream
+ * at a time.
  * Limits: 1 <= slots <= 1024, 1 <= max_rank <= 64. Synchronizes `stream`.
  * Errors: INVALID_ARG, SHAPE, OOM, CUDA. */
 qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_rank, qmlp_stream_t stream);
@@ -446,7 +450,8 @@ qmlp_status qmlp_lora_set(qmlp_lora_t* l, int slot, const qmlp_adapter* adapter,
  *  x   = device bf16 [M, K];  out = device bf16 [M, K]
  *  ids = device int32 [M]: the token's slot; a value outside [0, slots) or an
  *        empty slot: the block without an adapter (read on the device)
- * Allocates nothing; can be captured in a CUDA graph. 1 <= M <= h's max_M.
+ * Allocates nothing; can be captured in a CUDA graph (x and ids may change
+ * between replays). 1 <= M <= h's max_M. The same call gives the same bytes.
  * Errors: as qmlp_forward (ALIGNMENT: ids 4 bytes; ALIAS: out overlaps ids). */
 qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids, int M, void* out,
                               qmlp_stream_t stream);

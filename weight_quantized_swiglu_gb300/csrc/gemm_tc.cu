@@ -1173,6 +1173,8 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const Args a) {
     }
 }
 
+// (Down and dx, 2048 tokens of the 27B block: 160 tiles on 76 pairs, the last 8
+// shared by 72 pairs: 259 -> 197 us and 496 -> 377 us, with 5 us for this kernel.)
 // The split tiles of a CTA-pair GEMM: out = bf16(factor * sum of the pairs'
 // shares, in order, + add). A thread four columns of a row.
 template <int FMT>
@@ -1259,6 +1261,10 @@ __global__ void __launch_bounds__(256) predecode_kernel(const uint8_t* __restric
 // then up rows. mul0 / mul1: optional factors of the source rows (gate or the
 // projection's, and up's), rounded into the image, which is bf16 or, F16, fp16;
 // without them the decoded values are exact, as above. Columns past the source's are zero.
+// (27B-class NVFP4: gate/up 456 MB in 92 us, down 228 MB in 44; loads, two passes
+// through shared memory and the bulk copy of a CTA follow one another, six CTAs
+// an SM cover for that. With the image beside the decoded rows, three CTAs an SM:
+// 203 and 92 us.)
 struct PreT {
     const uint8_t* tiles;
     uint8_t* img;

@@ -18,7 +18,15 @@
 // does not depend on the tokens beside it.
 //
 // Bound by memory: z (or the wide output) passes once; the MMAs (mma.sync
-// m16n8k16) are far below the tensor cores' rate at these ranks.
+// m16n8k16) are below the tensor cores' rate at these ranks, but for the wide
+// products at rank 64, whose three words are 47 GFLOP for 3001 tokens of the
+// 27B-class block. Measured there (K 5120, I 17408):
+//   c A x, 8192 tokens, 32 columns: 25 us (84 MB); c dG B, 2 x 16 columns: 102 us
+//   (570 MB, 5.6 TB/s)
+//   B v as an fp32 array, 8192 tokens, rank 16: 240 us (1.14 GB, 4.8 TB/s); 3001
+//   tokens, rank 64: 128 us (the MMAs) -- hence the further GEMM steps, for which
+//   the image and the plan kernels below make the operands
+//   all six gradients, 8192 tokens, rank 16: 193 us (1.02 GB, 5.3 TB/s)
 #include "lowrank.cuh"
 
 namespace qmlp {
@@ -626,8 +634,8 @@ __global__ void __launch_bounds__(256) swiglu_raw_kernel(const LrSwiGLU a) {
 
 // Tokens grouped by slot: perm holds the tokens slot by slot (those without an
 // adapter last), tiles the {slot or -1, first position, tokens} of at most 64.
-// One CTA; the order of a slot's tokens is left to the atomics where no result
-// depends on it.
+// One CTA (3001 tokens, 7 slots: 8 us, 14 with the GEMM's lists); the order of a
+// slot's tokens is left to the atomics where no result depends on it.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids, int M, int slots,
                                                     const int* __restrict__ rank, int* perm, int4* tiles,
@@ -800,6 +808,7 @@ __global__ void __launch_bounds__(256) pack_kernel(const LrPack a) {
     }
 }
 
+// (4.5 MB of images of rank 16: 9 us.)
 // Stage images of an adapter's side of a GEMM's further steps: 256 rows of 64
 // columns each, 128-byte swizzled (16-byte chunk l of row n at l ^ (n & 7)). A
 // column is (word, part, j): with T = 2 words (the activations' v = h + l) both
