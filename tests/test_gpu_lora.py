@@ -240,6 +240,43 @@ def test_long_batches(torch, fmt, rank, pattern):
     mlp.close()
 
 
+@pytest.mark.parametrize("fmt,M", [("nvfp4", 1), ("nvfp4", 4), ("fp8", 3), ("nvfp4", 100), ("fp8", 800)])
+def test_waits_that_run_out_are_reported(torch, fmt, M):
+    """A weight step that is never loaded: the call ends by its bounded waits,
+    the handle reports it, and the next call is right again."""
+    K, I = 256, 512
+    rng = np.random.default_rng(39)
+    case = scaled_case(fmt, K, I, 39)
+    mlp = q.QuantMLP.from_case(case, max_M=800)
+    lora = q.LoraMLP(mlp, 2, 8)
+    ads = {1: (adapter(rng, K, I, 8), 1.0)}
+    lora.set(1, on_device(torch, *ads[1]))
+    xb, x = x_of(rng, M, K)
+    ids = np.ones(M, dtype=np.int64)
+    out = torch.empty((M, K), dtype=torch.int16, device="cuda")
+    mlp.set_wait(20_000_000, True)
+    lora.forward(to_dev(xb), torch.from_numpy(ids.astype(np.int32)).cuda(), out)
+    with pytest.raises(q.QmlpError) as e:
+        mlp.check()
+    assert e.value.status == 8
+    mlp.set_wait(0, False)
+    compare(run(torch, lora, mlp, xb, ids), reference(case, weights(case), x, ids, ads))
+    lora.close()
+    mlp.close()
+
+
+def test_ids_of_another_type_are_refused(torch):
+    mlp = q.QuantMLP.from_case(gen.gen_dense_case("nvfp4", 256, 512, 1, 40), max_M=8)
+    lora = q.LoraMLP(mlp, 1, 8)
+    x = torch.zeros((4, 256), dtype=torch.bfloat16, device="cuda")
+    for ids in (torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4, device="cuda"),
+                torch.zeros(8, dtype=torch.int32, device="cuda")[::2], torch.zeros(3, dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError):
+            lora.forward(x, ids, torch.empty_like(x))
+    lora.close()
+    mlp.close()
+
+
 def test_refusals(torch):
     case = gen.gen_dense_case("nvfp4", 256, 512, 1, 37)
     mlp = q.QuantMLP.from_case(case, max_M=16)

@@ -177,6 +177,40 @@ def test_forward_is_the_block_and_steps_repeat_bit_for_bit(torch):
     mlp.close()
 
 
+@pytest.mark.parametrize("M", [100, 600])
+def test_waits_that_run_out_are_reported(torch, M):
+    rng = np.random.default_rng(57)
+    case = scaled_case("nvfp4", 256, 512, 57)
+    mlp = q.QuantMLP.from_case(case, max_M=768)
+    t = q.TrainMLP(mlp, 8)
+    xb, x = x_of(rng, M, 256)
+    dyb, _ = x_of(rng, M, 256)
+    ad = on_device(torch, adapter(rng, 256, 512, 8), 1.0)
+    mlp.set_wait(20_000_000, True)
+    with pytest.raises(q.QmlpError) as e:
+        step(torch, t, xb, dyb, ad)
+    assert e.value.status == 8
+    mlp.set_wait(0, False)
+    compare_step(torch, t, case, weights(case), xb, x, rng, PARTS, 8, 1.0)
+    t.close()
+    mlp.close()
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "fp8"])
+def test_split_tiles(torch, fmt):
+    """Output tiles that the CTA pairs do not fill: shared over the contraction,
+    with pairs left without work, and with all pairs busy before them."""
+    rng = np.random.default_rng(58)
+    case = scaled_case(fmt, 1024, 4096, 58)
+    t = q.TrainMLP(q.QuantMLP.from_case(case, max_M=5000), 16)
+    w = weights(case)
+    for M, r in ((768, 16), (2049, 0), (4900, 5)):  # 12, 36 and 80 tiles of 256 x 256
+        xb, x = x_of(rng, M, 1024)
+        compare_step(torch, t, case, w, xb, x, rng, PARTS if r else (), r, 1.0)
+    t.close()
+    t.mlp.close()
+
+
 def test_refusals(torch):
     small = q.QuantMLP.from_case(gen.gen_dense_case("nvfp4", 256, 512, 1, 56), max_M=100)
     odd = q.QuantMLP.from_case(gen.gen_dense_case("nvfp4", 144, 208, 1, 56), max_M=768)

@@ -571,6 +571,9 @@ class LoraMLP:
     def forward(self, x, ids, out, M=None, stream=None):
         """x [M, K] bf16, ids [M] int32 (the token's slot; none: -1), out [M, K] bf16."""
         M = x.shape[0] if M is None else M
+        if not isinstance(ids, int) and (ids.element_size() != 4 or ids.is_floating_point() or not ids.is_contiguous()
+                                         or ids.numel() < M):
+            raise ValueError(f"LoraMLP: ids has to be a contiguous int32 tensor of {M} values")
         _chk(qmlp_lora_forward(self.h, x, ids, M, out, stream), "qmlp_lora_forward")
         return out
 

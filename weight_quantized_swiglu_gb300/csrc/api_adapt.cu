@@ -409,7 +409,10 @@ extern "C" {
 // ---------------------------------------------------------------------------
 // low-rank adapters
 // ---------------------------------------------------------------------------
-qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_rank, qmlp_stream_t stream) {
+// `inner`: the one slot of a training workspace, which makes the images of its own
+// calls and needs the added terms for few tokens alone unless `added`.
+static qmlp_status lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_rank, bool inner, bool added,
+                               qmlp_stream_t stream) {
     return guarded([&]() -> qmlp_status {
         if (!out) return QMLP_ERR_INVALID_ARG;
         *out = nullptr;
@@ -436,8 +439,8 @@ qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_ra
         get(&l->scale, S, true);
         get(&l->rank, S, true);
         get(&l->v, (size_t)kLrFew * 2 * R, false);
-        get(&l->vw, kLrWords * M * 2 * R, false);
-        get(&l->y, M * std::max(2 * I, K), false);
+        get(&l->vw, inner ? 16 : kLrWords * M * 2 * R, false);
+        get(&l->y, (inner && !added ? std::min<size_t>(M, kPairMinM) : M) * std::max(2 * I, K), false);
         get(&l->raw, (size_t)kMaxGemvM * (2 * I + K), false);
         get(&l->vd, (size_t)std::max(1, h->sp.G) * kMaxGemvM * R, false);
         get(&l->perm, M, false);
@@ -446,7 +449,7 @@ qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_ra
         l->e_d = word_ld((int)R, l->T) / 64;
         const size_t ig = S * (I / 128) * l->e_gu * kImage, id = S * (K / 256) * l->e_d * kImage;
         bool ok = false;
-        if (e == cudaSuccess && h->wdec && h->side && ig + id <= kMostImages) e = factors_divide(h, &ok, s);
+        if (e == cudaSuccess && !inner && h->wdec && h->side && ig + id <= kMostImages) e = factors_divide(h, &ok, s);
         l->steps = ok;
         if (l->steps) {
             const size_t ents = (size_t)lr_max_entries((int)M, slots);
@@ -471,6 +474,10 @@ qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_ra
         *out = l;
         return QMLP_OK;
     });
+}
+
+qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_rank, qmlp_stream_t stream) {
+    return lora_create(out, h, slots, max_rank, false, true, stream);
 }
 
 void qmlp_lora_destroy(qmlp_lora_t* l) {
@@ -970,12 +977,15 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
             if (h->fmt == kNVFP4 && !(fabsf(h->gv[i].inv_g) >= kLeastFactor)) return QMLP_ERR_INVALID_ARG;
         qmlp_train_t* t = new qmlp_train_t();
         t->h = h;
-        qmlp_status st = qmlp_lora_create(&t->l, h, 1, max_rank, stream);
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        qmlp_status st = from_cuda(factors_divide(h, &t->steps, s));
+        // FP8's d act, and every GEMM where the factors cannot be divided by, add
+        // the adapter's terms at any number of tokens
+        if (st == QMLP_OK) st = lora_create(&t->l, h, 1, max_rank, true, h->fmt == kFP8 || !t->steps, stream);
         if (st != QMLP_OK) {
             delete t;
             return st;
         }
-        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
         const size_t I = h->I, K = h->K, M = h->max_M, R = t->l->Rp;
         t->img_t_bytes = gemm_decoded_t_bytes((int)K, (int)I);
         cudaError_t e = cudaSuccess;
@@ -1004,10 +1014,8 @@ qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_
         }
         if (e == cudaSuccess && h->fmt == kFP8) {
             // e4m3 (at most 448) times a factor under fac_d, times 2^6: under 2^15
-            e = factors_divide(h, &t->steps, s);
             std::vector<float> f(K);
-            if (e == cudaSuccess)
-                e = cudaMemcpyAsync(f.data(), h->gv[2].chs, K * sizeof(float), cudaMemcpyDeviceToHost, s);
+            e = cudaMemcpyAsync(f.data(), h->gv[2].chs, K * sizeof(float), cudaMemcpyDeviceToHost, s);
             if (e == cudaSuccess) e = cudaStreamSynchronize(s);
             float top = 0.0f;
             for (float v : f)
