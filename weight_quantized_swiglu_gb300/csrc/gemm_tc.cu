@@ -628,6 +628,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             tc_fence_before();
             mbar_arrive(acc_empty(buf));
         }
+        // the reduce kernel reads `add` once this grid is complete, and this grid
+        // started beside the kernels that write it: only a wait in here puts
+        // their writes before that
+        if (SPLIT && a.early) pdl_wait();
     } else if (!PRE) {
         // ---------------- decoders ----------------
         const int d = threadIdx.x - (2 + kEpiWarps) * 32;  // 0 .. kDecThreads-1
