@@ -200,6 +200,35 @@ def test_small_roots_keep_a_code_and_the_next_update_stays_small(torch):
     o.close()
 
 
+@pytest.mark.parametrize("scale", [3e-38, 1e-38, 1e-39, 1e-40, 1e-42])
+def test_momenta_that_have_decayed_to_subnormal_scales(torch, scale):
+    """Without gradients m decays by beta1 a step, through scales whose
+    reciprocal is past fp32's range. Zeros stay zeros and the others keep nearest
+    codes: m rounds twice and the scale once more to a subnormal's step 2^-149."""
+    n = 512
+    d = make(torch, [n], torch.float32, torch.float32, True, False, 18)
+    d["grads"][0].zero_()
+    d["m"][0][::3] = 0
+    d["m_scale"][0].copy_(torch.tensor([scale, 5e-3 / 448], dtype=torch.float32))
+    m = (f64(d["m"][0]) * blocks(d["m_scale"][0], n)) * HYPER["beta1"]
+    o = q.AdamW(d["params"], d["grads"], d["m"], d["v"], m_scale=d["m_scale"], v_scale=d["v_scale"])
+    o.step(**HYPER)
+    torch.cuda.synchronize()
+    o.close()
+    tiny = 2.0 ** -149
+    c, s = f64(d["m"][0]), f64(d["m_scale"][0])
+    top = np.abs(m).reshape(2, 256).max(1)
+    assert np.all(np.abs(s - top / 448) <= 8 * U * top / 448 + tiny)
+    sb = np.repeat(s, 256)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        qv = np.where(sb > 0, m / sb, 0.0)
+        tol = np.where(sb > 0, (4 * U * np.abs(m) + 2 * tiny) / sb, 0.0)
+    qv = np.clip(qv, -448, 448)
+    assert np.all(c[m == 0] == 0)
+    assert np.all(np.abs(c - qv) <= e4m3_step(qv) / 2 + tol + 8 * U * np.abs(qv))
+    assert torch.isfinite(d["params"][0]).all()
+
+
 def test_not_finite_gradients_are_not_hidden(torch):
     d = make(torch, [512], torch.float32, torch.float32, True, False, 16)
     for t in d["m"] + d["v"] + d["m_scale"] + d["v_scale"]:

@@ -134,11 +134,12 @@ QMLP_DEV float sqrt_fast(float v) {  // within 2^-23
 // smallest code.
 //
 // The quotients are products with the reciprocal, and the roots fast ones: five
-// units of the last place off at most. Only where that can reach the middle of
-// two codes (or under the normal codes, whose middles lie elsewhere) are they
-// taken again, correctly rounded. A lane asks that once for its eight elements.
-// (69M elements, 384 tensors: 229 us with every root and quotient rounded, 212
-// with these.)
+// units of the last place off at most. So both ends of that error (2^-20 to each
+// side) are made codes, and only where they differ, or a root came to the code
+// zero, are root and quotient taken again, correctly rounded. A lane asks that
+// once for its eight elements. (69M elements, 384 tensors: 229 us with every
+// root and quotient rounded, 203 with the quotients' bits compared to the middles
+// of the codes, 190 with the two codes.)
 template <bool VEC, bool ROOT>
 QMLP_DEV void store8_codes(uint8_t* p, float* scale, int n, const float (&v)[kPer], const float (&w)[kPer]) {
     float top = 0.0f;
@@ -147,30 +148,31 @@ QMLP_DEV void store8_codes(uint8_t* p, float* scale, int n, const float (&v)[kPe
     top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // bits order as the floats do
     if (ROOT) top = __fsqrt_rn(top);
     const float s = __fmul_rn(top, 1.0f / 448.0f), rs = __frcp_rn(s);
-    float q[kPer];
-    bool again = !(s > 0.0f);
+    const float lo = __fmul_rn(rs, 1.0f - 9.5367431640625e-7f), hi = __fmul_rn(rs, 1.0f + 9.5367431640625e-7f);
+    uint32_t c[2], d[2];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        q[i] = __fmul_rn(w[i], rs);
-        const uint32_t b = __float_as_uint(q[i]);
-        // normal codes (from 2^-6) keep 3 of 23 mantissa bits: the middle is
-        // 0x80000 of the other 20. Zero is itself; 0.016 has room for the error
-        again |= ((b + 8u - 0x80000u) & 0xFFFFFu) <= 16u || !(fabsf(q[i]) >= 0.016f || q[i] == 0.0f);
+    for (int i = 0; i < 2; ++i) {
+        c[i] = e4m3x2(__fmul_rn(w[4 * i], lo), __fmul_rn(w[4 * i + 1], lo)) |
+               e4m3x2(__fmul_rn(w[4 * i + 2], lo), __fmul_rn(w[4 * i + 3], lo)) << 16;
+        d[i] = e4m3x2(__fmul_rn(w[4 * i], hi), __fmul_rn(w[4 * i + 1], hi)) |
+               e4m3x2(__fmul_rn(w[4 * i + 2], hi), __fmul_rn(w[4 * i + 3], hi)) << 16;
     }
+    // (under 2^-126 the reciprocal may be infinite: momenta that decay without gradients come there)
+    bool again = !(s >= 1.17549435e-38f) || c[0] != d[0] || c[1] != d[1];
+    if (ROOT)  // a byte that is zero
+        again |= (((c[0] - 0x01010101u) & ~c[0]) | ((c[1] - 0x01010101u) & ~c[1])) & 0x80808080u;
     if (again) {
+        float q[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const float x = ROOT ? __fsqrt_rn(v[i]) : v[i];
             // no scale: zeros (and values under 448 of the smallest subnormal), or a NaN, which stays one
             q[i] = s > 0.0f ? __fdiv_rn(x, s) : x;
+            if (ROOT && s > 0.0f && q[i] > 0.0f) q[i] = fmaxf(q[i], 0.001953125f);
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) c[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16;
     }
-    if (ROOT && s > 0.0f)
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) q[i] = q[i] > 0.0f ? fmaxf(q[i], 0.001953125f) : q[i];
-    uint32_t c[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) c[i] = e4m3x2(q[4 * i], q[4 * i + 1]) | e4m3x2(q[4 * i + 2], q[4 * i + 3]) << 16;
     if ((threadIdx.x & 31) == 0) *scale = s;
     if (VEC) {
         *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
@@ -222,7 +224,7 @@ QMLP_DEV void step8(const AdamWChunk& c, const AdamWStep& k, int at, int n) {
 }
 
 template <typename P, typename G, bool S8, bool MASTER>
-// Five CTAs an SM (8-bit states: 212 us with four, 202 with five, 209 with six;
+// Five CTAs an SM (8-bit states, with the middles compared: 212 us with four, 202 with five, 209 with six;
 // the next chunk's words prefetched into registers: 243 and more, the issue slots
 // and the warps that hide the loads' latency count, not one warp's loads).
 __global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const AdamWChunk* __restrict__ chunks, const AdamWStep k) {
