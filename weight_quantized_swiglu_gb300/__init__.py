@@ -154,10 +154,24 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_current_stream = None  # torch's current stream as a raw handle, of the current device
+
+
+def _find_current_stream():
+    import torch
+    raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and dev is not None:  # without the Stream object: 0.16 us, 3.0 with it
+        torch.cuda.init()
+        return lambda: raw(dev())
+    return lambda: torch.cuda.current_stream().cuda_stream
+
+
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
