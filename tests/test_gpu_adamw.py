@@ -152,6 +152,17 @@ def test_tensors_that_start_anywhere(torch, eight):
         [x.reshape(1) for x in before], [x.reshape(1) for x in after]))
 
 
+@pytest.mark.parametrize("offset", [0, 8])
+@pytest.mark.parametrize("pdt,gdt,master", [("float32", "bfloat16", False), ("bfloat16", "float32", True)])
+def test_more_chunks_than_the_gpu_holds_at_a_time(torch, pdt, gdt, master, offset):
+    """Many chunks, short ones among them; offset 8: 8-bit states that start on
+    8 bytes and not on 16."""
+    sizes = [2048 * 700 + 5] + [17, 4096, 3] * 40 + [2048 * 100 + 1031]
+    d = make(torch, sizes, getattr(torch, pdt), getattr(torch, gdt), True, master, 19, offset=offset)
+    assert offset == 0 or any(t.data_ptr() % 16 for t in d["m"])
+    check(torch, d, HYPER)
+
+
 def test_the_wide_and_the_narrow_path_agree_bit_for_bit(torch):
     n = 4096
     a = make(torch, [n], torch.float32, torch.float32, True, False, 13)

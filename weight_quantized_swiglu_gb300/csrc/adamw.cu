@@ -28,6 +28,8 @@
 // addresses come from one 64-byte entry of a table that is written when the
 // handle is made. Bound by memory: fp32 28 B an element (bf16 parameter, fp32
 // master, bf16 gradient and 8-bit states: 16 B).
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -223,12 +225,39 @@ QMLP_DEV void step8(const AdamWChunk& c, const AdamWStep& k, int at, int n) {
     }
 }
 
+// `bytes` (a multiple of 16) from p on their way to L2; only from a 16-byte
+// boundary, as the copy wants it (8-bit states may start on 8).
+QMLP_DEV void to_l2(const void* p, uint32_t bytes) {
+    if (bytes && !(reinterpret_cast<uintptr_t>(p) & 15))
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+constexpr int kResident = 5;  // CTAs an SM
+
+// Five CTAs an SM (8-bit states, with the middles compared: 212 us with four, 202
+// with five, 209 with six; the next chunk's words prefetched into registers: 243
+// and more). 8-bit states: a chunk is half the bytes of fp32's behind the same
+// two latencies, the table's entry and then the data, so one thread sends the
+// data of the chunk `ahead`, half of the GPU's resident CTAs on, to L2. (69M
+// elements, 384 tensors: 186 us without; 188 with half a CTA an SM ahead, 179 with
+// one and a half, 175 with two and a half, 174 with three, 177 with five, 178 with
+// ten. fp32 states, 150M elements: 591 without and with two and a half, 610 with
+// five, 781 with ten: they do without.)
 template <typename P, typename G, bool S8, bool MASTER>
-// Five CTAs an SM (8-bit states, with the middles compared: 212 us with four, 202 with five, 209 with six;
-// the next chunk's words prefetched into registers: 243 and more, the issue slots
-// and the warps that hide the loads' latency count, not one warp's loads).
-__global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const AdamWChunk* __restrict__ chunks, const AdamWStep k) {
+__global__ void __launch_bounds__(kThreads, kResident)
+    adamw_kernel(const AdamWChunk* __restrict__ chunks, const AdamWStep k, const unsigned ahead) {
     const AdamWChunk c = chunks[blockIdx.x];
+    if (S8 && threadIdx.x == 0 && blockIdx.x + ahead < gridDim.x) {
+        const AdamWChunk& f = chunks[blockIdx.x + ahead];
+        if (f.vec) {
+            const uint32_t n = (uint32_t)f.n & ~15u;  // whole 16 bytes of every type
+            if (MASTER) to_l2(f.master, n * 4);
+            else to_l2(f.param, n * (uint32_t)sizeof(P));
+            to_l2(f.grad, n * (uint32_t)sizeof(G));
+            to_l2(f.m, n);
+            to_l2(f.v, n);
+        }
+    }
     const int at = threadIdx.x * kPer;  // within the chunk
     if ((at & ~(kAdamWBlock - 1)) >= c.n) return;  // the whole warp's block is past the end
     const int n = min(max(c.n - at, 0), kPer);     // elements of this lane
@@ -238,26 +267,28 @@ __global__ void __launch_bounds__(kThreads, 5) adamw_kernel(const AdamWChunk* __
 }
 
 template <typename P, typename G, bool MASTER>
-cudaError_t launch_s(const AdamWChunk* chunks, long count, bool s8, const AdamWStep& k, cudaStream_t s) {
-    if (s8) adamw_kernel<P, G, true, MASTER><<<(unsigned)count, kThreads, 0, s>>>(chunks, k);
-    else adamw_kernel<P, G, false, MASTER><<<(unsigned)count, kThreads, 0, s>>>(chunks, k);
+cudaError_t launch_s(const AdamWChunk* chunks, long count, bool s8, const AdamWStep& k, unsigned ahead,
+                     cudaStream_t s) {
+    if (s8) adamw_kernel<P, G, true, MASTER><<<(unsigned)count, kThreads, 0, s>>>(chunks, k, ahead);
+    else adamw_kernel<P, G, false, MASTER><<<(unsigned)count, kThreads, 0, s>>>(chunks, k, ahead);
     return cudaPeekAtLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_adamw(const AdamWChunk* chunks, long count, bool param_bf16, bool master, bool grad_bf16, bool s8,
-                         const AdamWStep& k, cudaStream_t s) {
+                         const AdamWStep& k, int num_sms, cudaStream_t s) {
+    const unsigned ahead = (unsigned)(kResident * std::max(num_sms, 1) / 2);
     if (count < 1 || count > 0x7fffffffL) return cudaErrorInvalidValue;
     using B = __nv_bfloat16;
     if (!param_bf16)
-        return grad_bf16 ? launch_s<float, B, false>(chunks, count, s8, k, s)
-                         : launch_s<float, float, false>(chunks, count, s8, k, s);
+        return grad_bf16 ? launch_s<float, B, false>(chunks, count, s8, k, ahead, s)
+                         : launch_s<float, float, false>(chunks, count, s8, k, ahead, s);
     if (master)
-        return grad_bf16 ? launch_s<B, B, true>(chunks, count, s8, k, s)
-                         : launch_s<B, float, true>(chunks, count, s8, k, s);
-    return grad_bf16 ? launch_s<B, B, false>(chunks, count, s8, k, s)
-                     : launch_s<B, float, false>(chunks, count, s8, k, s);
+        return grad_bf16 ? launch_s<B, B, true>(chunks, count, s8, k, ahead, s)
+                         : launch_s<B, float, true>(chunks, count, s8, k, ahead, s);
+    return grad_bf16 ? launch_s<B, B, false>(chunks, count, s8, k, ahead, s)
+                     : launch_s<B, float, false>(chunks, count, s8, k, ahead, s);
 }
 
 }  // namespace qmlp

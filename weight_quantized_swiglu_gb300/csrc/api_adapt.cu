@@ -84,6 +84,7 @@ constexpr size_t kFewWeights = (size_t)8 << 20;
 struct qmlp_adamw_s {
     AdamWChunk* chunks = nullptr;
     long count = 0;
+    int num_sms = 0;
     bool param_bf16 = false, master = false, grad_bf16 = false, s8 = false;
     Owner mem;
 };
@@ -1185,6 +1186,7 @@ qmlp_status qmlp_adamw_create(qmlp_adamw_t** out, const qmlp_adamw_tensor* ts, i
         }
         qmlp_adamw_t* h = new qmlp_adamw_t();
         h->count = (long)table.size();
+        h->num_sms = sms;
         h->param_bf16 = pb;
         h->master = master;
         h->grad_bf16 = gb;
@@ -1230,7 +1232,7 @@ qmlp_status qmlp_adamw_step(qmlp_adamw_t* h, const qmlp_adamw_hyper* y, qmlp_str
     k.eps = (float)y->eps;
     k.decay = (float)(1.0 - y->lr * y->weight_decay);
     k.step = (float)(y->lr / (1.0 - pow(y->beta1, (double)y->step)));
-    return launch_adamw(h->chunks, h->count, h->param_bf16, h->master, h->grad_bf16, h->s8, k,
+    return launch_adamw(h->chunks, h->count, h->param_bf16, h->master, h->grad_bf16, h->s8, k, h->num_sms,
                         reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QMLP_OK
                : QMLP_ERR_CUDA;

@@ -333,7 +333,7 @@ struct AdamWStep {  // the constants of a step, fp32 of fp64 values
     float gscale, b1, omb1, b2, omb2, rbc2, eps, decay, step;
 };
 cudaError_t launch_adamw(const AdamWChunk* chunks, long count, bool param_bf16, bool master, bool grad_bf16, bool s8,
-                         const AdamWStep& k, cudaStream_t s);
+                         const AdamWStep& k, int num_sms, cudaStream_t s);
 
 // Index checks of a QMLP_DEBUG_BOUNDS build (common.cuh): each translation
 // unit's first failed check, (site << 48) | index, or 0; reading clears it.
