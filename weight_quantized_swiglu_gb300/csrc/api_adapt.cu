@@ -524,7 +524,7 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
         }
         const bool few = M <= kLrFew, steps = lora_steps(l, M);
         auto terms = [&](bool down, const void* z, cudaStream_t st) {
-            cudaError_t e = few ? lora_shrink_few(l, down, z, ids, M, st) : lora_shrink(l, down, z, M, st);
+            cudaError_t e = few ? lora_shrink_few(l, down, z, ids, M, st, true) : lora_shrink(l, down, z, M, st);
             if (e == cudaSuccess)
                 e = few ? lora_expand_few(l, down, ids, M, nullptr, nullptr, st) : lora_expand(l, down, M, st);
             return e;

@@ -198,8 +198,10 @@ struct GemmLaunch {
     size_t wdec_bytes = 0;    // bytes of wdec, >= gemm_decoded_bytes(w.N, w.K)
     const float* add = nullptr;  // fp32 [M][ldadd], added after the factor: gate's I columns then up's
     // early: the kernels that write add are launched just before, each with
-    // programmatic dependent launch, behind one that is not; nothing else that the
-    // GEMM reads (prescaled activations, images) comes from them
+    // programmatic dependent launch; nothing else that the GEMM reads (prescaled
+    // activations, images) comes from them. It reads those without a wait, so the
+    // first of these kernels lets the next one start only after its own wait, when
+    // all that came before has completed and is visible
     bool early = false;
     bool prescaled = false;      // a16 and sig are written (launch_gemm_prescale)
     size_t ldadd = 0;            // (SwiGLU), or the output's columns (plain, grad); low-rank adapters

@@ -156,8 +156,10 @@ template <int NC, bool TRANS, bool TWO>
 __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
     using S = ShrinkSmem<NC, TRANS, TWO>;
     extern __shared__ __align__(128) uint8_t smem[];
-    pdl_launch_dependents();
+    // (in this order: a GEMM launched early reads without a wait of its own what
+    // the launches before this one wrote, see GemmLaunch::early)
     pdl_wait();
+    pdl_launch_dependents();
     int slot, pos0, n, entry0;
     if (!tile_of(a.tok, blockIdx.x, slot, pos0, n, entry0) || slot < 0) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -560,8 +562,9 @@ QMLP_DEV float dot8(const uint4& a, const uint4& b, float s) {
 }
 
 // v[m, j] = c A[slot(m)][j] . x[m]: a CTA a (row j, token m). The next launch may
-// start at once or, `late`, once everything before this one has completed (see
-// gemv_split.cu).
+// start at once or, `late`, once everything before this one has completed: for
+// kernels that read what came before without a wait of their own (gemv_split.cu,
+// GemmLaunch::early).
 __global__ void __launch_bounds__(kThr) shrink_few_kernel(const LrFew a) {
     const int j = blockIdx.x, m = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
