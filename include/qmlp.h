@@ -480,8 +480,10 @@ typedef struct qmlp_train_s qmlp_train_t;
 qmlp_status qmlp_train_create(qmlp_train_t** out, qmlp_t* h, int max_rank, qmlp_stream_t stream);
 void qmlp_train_destroy(qmlp_train_t* t);
 
-/* Bytes of the buffer that a forward of M tokens fills for its backward pass
- * (about 10 M I); 0 where M is out of range. */
+/* Bytes of the buffer that a forward of M tokens fills for its backward pass:
+ * about 10 I a token (8 I of them for whole groups of 32 tokens) and 2 I more for
+ * each of the first 255; 0 where M is out of range. It grows with M: a buffer for
+ * M tokens serves any smaller number. */
 size_t qmlp_train_saved_bytes(qmlp_train_t* t, int M);
 
 /* The block as qmlp_lora_forward with one adapter for every token (NULL:

@@ -1,0 +1,79 @@
+"""What the adapter and training classes refuse before anything is launched:
+buffers that a kernel would read or write past their end. Stand-ins take the
+place of the CUDA tensors and of the library, so no GPU is needed."""
+import numpy as np
+import pytest
+
+import weight_quantized_swiglu_gb300 as q
+
+K, I, M = 256, 512, 20
+
+
+class Buffer:
+    """What the classes ask of a tensor."""
+
+    def __init__(self, shape, size=2, cuda=True, contiguous=True, floating=True, at=1 << 20):
+        self.shape, self.size, self.is_cuda, self.contiguous, self.floating, self.at = (
+            tuple(shape), size, cuda, contiguous, floating, at)
+
+    def numel(self):
+        return int(np.prod(self.shape))
+
+    def dim(self):
+        return len(self.shape)
+
+    def element_size(self):
+        return self.size
+
+    def is_contiguous(self):
+        return self.contiguous
+
+    def is_floating_point(self):
+        return self.floating
+
+    def data_ptr(self):
+        return self.at
+
+
+class Block:
+    K, I = K, I
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """The calls that reach the library."""
+    made = []
+    for name in ("qmlp_lora_forward", "qmlp_train_forward", "qmlp_train_backward"):
+        monkeypatch.setattr(q, name, lambda *a, _n=name: made.append(_n) or 0)
+    monkeypatch.setattr(q, "qmlp_train_saved_bytes", lambda h, m: 1000 * m)
+    return made
+
+
+def handle(cls):
+    h = cls.__new__(cls)
+    h.mlp, h.h = Block(), None
+    return h
+
+
+def rows(m=M, **kw):
+    return Buffer((m, K), **kw)
+
+
+def saved(nbytes=1000 * M, **kw):
+    return Buffer((nbytes,), size=1, **kw)
+
+
+def test_saved_buffers(calls):
+    t = handle(q.TrainMLP)
+    for good in (saved(), saved(1000 * M + 7), Buffer((250 * M,), size=4), 1 << 20):
+        t.forward(rows(), rows(), good)
+        t.backward(rows(), good, rows(), rows())
+    assert len(calls) == 8
+    for bad in (saved(1000 * M - 1), saved(cuda=False), saved(contiguous=False), Buffer((250 * M - 1,), size=4)):
+        with pytest.raises(ValueError, match="saved"):
+            t.forward(rows(), rows(), bad)
+        with pytest.raises(ValueError, match="saved"):
+            t.backward(rows(), bad, rows(), rows())
+    with pytest.raises(ValueError, match="saved"):  # M given apart from x
+        t.forward(rows(), rows(), saved(), M=M + 1)
+    assert len(calls) == 8

@@ -535,6 +535,13 @@ class MoeAWQ:
             pass
 
 
+def _device_buffer(who, name, t, nbytes):
+    """Refuse a tensor that a kernel would read or write past its end, or not
+    in the order of its elements."""
+    if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{who}: {name} has to be a contiguous CUDA tensor of {nbytes} bytes or more")
+
+
 class Adapter:
     """A low-rank adapter of the block: scale (alpha / r) and, for each adapted
     projection, A [r, in] and B [out, r], contiguous bf16 CUDA tensors of one
@@ -622,9 +629,15 @@ class TrainMLP:
         a.check(self.mlp.K, self.mlp.I)
         return a.c
 
+    def _saved(self, saved, M):
+        if not isinstance(saved, int):
+            _device_buffer("TrainMLP", "saved", saved, self.saved_bytes(M))
+
     def forward(self, x, out, saved, adapter: Adapter | None = None, M=None, stream=None):
-        """x, out [M, K] bf16; saved: saved_bytes(M) bytes on the device."""
+        """x, out [M, K] bf16; saved: saved_bytes(M) bytes on the device or more
+        (a buffer for the longest batch serves the shorter ones)."""
         M = x.shape[0] if M is None else M
+        self._saved(saved, M)
         _chk(qmlp_train_forward(self.h, self._adapter(adapter), x, M, out, saved, stream), "qmlp_train_forward")
         return out
 
@@ -633,6 +646,7 @@ class TrainMLP:
         """dout, dx [M, K] bf16; grads: the tensors that take the gradients of
         the adapter's parts (its scale is not used)."""
         M = x.shape[0] if M is None else M
+        self._saved(saved, M)
         _chk(qmlp_train_backward(self.h, self._adapter(adapter), x, M, saved, dout, dx, self._adapter(grads), stream),
              "qmlp_train_backward")
         return dx

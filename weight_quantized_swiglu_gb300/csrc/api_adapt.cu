@@ -590,7 +590,10 @@ Saved saved_of(const qmlp_train_s* t, int M, const void* base) {
     v.g = take(gemm_gu_bytes(M, (int)I));
     v.u = take(gemm_gu_bytes(M, (int)I));
     v.act = reinterpret_cast<__nv_bfloat16*>(take(m * I * 2));
-    v.act_lo = M < kTwoWordM ? reinterpret_cast<__nv_bfloat16*>(take(m * I * 2)) : nullptr;
+    // room for the second word at any M: a buffer for M tokens serves every
+    // smaller M too
+    uint8_t* lo = take(std::min<size_t>(m, kTwoWordM - 1) * I * 2);
+    v.act_lo = M < kTwoWordM ? reinterpret_cast<__nv_bfloat16*>(lo) : nullptr;
     const bool ext = t->steps && M >= kPairMinM;
     v.vgu = words_of(reinterpret_cast<__nv_bfloat16*>(take(words_room(m, 2 * (int)R) * 2)), 2 * (int)R, ext, t->T);
     v.vd = words_of(reinterpret_cast<__nv_bfloat16*>(take(words_room(m, (int)R) * 2)), (int)R, ext, t->T);
