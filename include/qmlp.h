@@ -499,8 +499,9 @@ qmlp_status qmlp_train_forward(qmlp_train_t* t, const qmlp_adapter* adapter, con
  * adapter (only read).
  *  dout = device bf16 [M, K];  dx = device bf16 [M, K]
  *  grads = where the gradients of the adapter's parts go: bf16, shaped and
- *          packed as the parts; a NULL part (or grads NULL) is not wanted.
- *          rank and scale are not read. Without an adapter: NULL.
+ *          packed as the parts, so of the adapter's rank; a NULL part (or grads
+ *          NULL) is not wanted. The rank and scale in it are not read. Without an
+ *          adapter: NULL.
  * Errors: as qmlp_train_forward (INVALID_ARG: gradients without an adapter or
  * of a part that it lacks). */
 qmlp_status qmlp_train_backward(qmlp_train_t* t, const qmlp_adapter* adapter, const void* x, int M, const void* saved,

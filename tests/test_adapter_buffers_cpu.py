@@ -77,3 +77,26 @@ def test_saved_buffers(calls):
     with pytest.raises(ValueError, match="saved"):  # M given apart from x
         t.forward(rows(), rows(), saved(), M=M + 1)
     assert len(calls) == 8
+
+
+def adapter_of(rank, parts=("gate", "up", "down")):
+    """An Adapter as its constructor leaves it, over stand-ins."""
+    a = q.Adapter.__new__(q.Adapter)
+    a.scale, a.parts = 1.0, {n: None for n in q.ADAPTER_PARTS}
+    for p in parts:
+        out, inp = {"gate": (I, K), "up": (I, K), "down": (K, I)}[p]
+        a.parts[p + "_a"], a.parts[p + "_b"] = Buffer((rank, inp)), Buffer((out, rank))
+    a.rank = rank if parts else 0
+    a.c = q.qmlp_adapter(a.rank, 1.0, *[None if t is None else t.data_ptr() for t in a.parts.values()])
+    return a
+
+
+def test_gradients_of_another_rank(calls):
+    t = handle(q.TrainMLP)
+    for grads in (adapter_of(16), adapter_of(16, ("up",)), adapter_of(3, ()), None):
+        t.backward(rows(), saved(), rows(), rows(), adapter=adapter_of(16), grads=grads)
+    assert len(calls) == 4
+    for rank in (1, 8, 15, 17, 32):
+        with pytest.raises(ValueError, match="rank"):
+            t.backward(rows(), saved(), rows(), rows(), adapter=adapter_of(16), grads=adapter_of(rank))
+    assert len(calls) == 4

@@ -647,6 +647,9 @@ class TrainMLP:
         the adapter's parts (its scale is not used)."""
         M = x.shape[0] if M is None else M
         self._saved(saved, M)
+        # (an Adapter without parts has no rank: no gradient is wanted)
+        if adapter is not None and grads is not None and grads.rank not in (0, adapter.rank):
+            raise ValueError(f"TrainMLP: gradients of rank {grads.rank} for an adapter of rank {adapter.rank}")
         _chk(qmlp_train_backward(self.h, self._adapter(adapter), x, M, saved, dout, dx, self._adapter(grads), stream),
              "qmlp_train_backward")
         return dx
