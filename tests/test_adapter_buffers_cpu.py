@@ -100,3 +100,49 @@ def test_gradients_of_another_rank(calls):
         with pytest.raises(ValueError, match="rank"):
             t.backward(rows(), saved(), rows(), rows(), adapter=adapter_of(16), grads=adapter_of(rank))
     assert len(calls) == 4
+
+
+def ids(n=M, **kw):
+    return Buffer((n,), **{"size": 4, "floating": False, **kw})
+
+
+BAD_ROWS = [rows(M - 1), rows(cuda=False), rows(contiguous=False), rows(size=1), Buffer((K,)), Buffer((M, K // 2)),
+            Buffer((M, 2 * K)), Buffer((M * K - 1,))]
+
+
+def test_serving_buffers(calls):
+    l = handle(q.LoraMLP)  # noqa: E741
+    good = [rows(), rows(M + 5), Buffer((M * K,)), Buffer((4, M // 4, K)), Buffer((M, 2 * K), size=1), 1 << 20]
+    for t in good:
+        l.forward(t, ids(), rows(), M=M)
+        l.forward(rows(), ids(), t)
+    l.forward(rows(), ids(M + 1), rows())
+    l.forward(rows(), 1 << 20, rows())
+    n = 2 * len(good) + 2
+    assert len(calls) == n
+    for t in BAD_ROWS:
+        with pytest.raises(ValueError, match="x "):
+            l.forward(t, ids(), rows(), M=M)
+        with pytest.raises(ValueError, match="out "):
+            l.forward(rows(), ids(), t)
+    with pytest.raises(ValueError, match="x "):  # one row of K values is not K tokens
+        l.forward(Buffer((K,)), ids(K), rows(K))
+    for t in (ids(cuda=False), ids(M - 1), ids(size=8), ids(floating=True), ids(contiguous=False)):
+        with pytest.raises(ValueError, match="ids"):
+            l.forward(rows(), t, rows())
+    assert len(calls) == n
+
+
+def test_training_buffers(calls):
+    t = handle(q.TrainMLP)
+    for bad in BAD_ROWS:
+        with pytest.raises(ValueError, match="x "):
+            t.forward(bad, rows(), saved(), M=M)
+        with pytest.raises(ValueError, match="out "):
+            t.forward(rows(), bad, saved())
+        for at in range(3):
+            a = [rows(), rows(), rows()]
+            a[at] = bad
+            with pytest.raises(ValueError, match=("x ", "dout ", "dx ")[at]):
+                t.backward(a[0], saved(), a[1], a[2], M=M)
+    assert not calls

@@ -542,6 +542,17 @@ def _device_buffer(who, name, t, nbytes):
         raise ValueError(f"{who}: {name} has to be a contiguous CUDA tensor of {nbytes} bytes or more")
 
 
+def _device_rows(who, M, K, **tensors):
+    """Refuse what is not M rows of K 16-bit values on the device (raw addresses
+    are the caller's)."""
+    for name, t in tensors.items():
+        if isinstance(t, int):
+            continue
+        _device_buffer(who, name, t, 2 * M * K)
+        if t.dim() > 1 and t.shape[-1] * t.element_size() != 2 * K:
+            raise ValueError(f"{who}: {name} has rows of {t.shape[-1]} values, {K} are wanted")
+
+
 class Adapter:
     """A low-rank adapter of the block: scale (alpha / r) and, for each adapted
     projection, A [r, in] and B [out, r], contiguous bf16 CUDA tensors of one
@@ -592,9 +603,10 @@ class LoraMLP:
     def forward(self, x, ids, out, M=None, stream=None):
         """x [M, K] bf16, ids [M] int32 (the token's slot; none: -1), out [M, K] bf16."""
         M = x.shape[0] if M is None else M
-        if not isinstance(ids, int) and (ids.element_size() != 4 or ids.is_floating_point() or not ids.is_contiguous()
-                                         or ids.numel() < M):
-            raise ValueError(f"LoraMLP: ids has to be a contiguous int32 tensor of {M} values")
+        _device_rows("LoraMLP", M, self.mlp.K, x=x, out=out)
+        if not isinstance(ids, int) and (not ids.is_cuda or ids.element_size() != 4 or ids.is_floating_point() or
+                                         not ids.is_contiguous() or ids.numel() < M):
+            raise ValueError(f"LoraMLP: ids has to be a contiguous int32 CUDA tensor of {M} values")
         _chk(qmlp_lora_forward(self.h, x, ids, M, out, stream), "qmlp_lora_forward")
         return out
 
@@ -638,6 +650,7 @@ class TrainMLP:
         (a buffer for the longest batch serves the shorter ones)."""
         M = x.shape[0] if M is None else M
         self._saved(saved, M)
+        _device_rows("TrainMLP", M, self.mlp.K, x=x, out=out)
         _chk(qmlp_train_forward(self.h, self._adapter(adapter), x, M, out, saved, stream), "qmlp_train_forward")
         return out
 
@@ -647,6 +660,7 @@ class TrainMLP:
         the adapter's parts (its scale is not used)."""
         M = x.shape[0] if M is None else M
         self._saved(saved, M)
+        _device_rows("TrainMLP", M, self.mlp.K, x=x, dout=dout, dx=dx)
         # (an Adapter without parts has no rank: no gradient is wanted)
         if adapter is not None and grads is not None and grads.rank not in (0, adapter.rank):
             raise ValueError(f"TrainMLP: gradients of rank {grads.rank} for an adapter of rank {adapter.rank}")
