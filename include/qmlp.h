@@ -411,6 +411,8 @@ qmlp_status qmlp_moe_m1_forward_noalloc(const qmlp_moe_desc* banks, const void* 
  *   g = sigma_g x Wg^T + c B_g A_g x   (u alike),  act = bf16(SiLU(g) u)
  *   out = bf16( sigma_d act Wd^T + c B_d A_d act )
  * with each token's own A, B and c. Sums are fp32, and c A z is held as fp32.
+ * Values of an adapter that are not finite reach the tokens that name it (as Inf
+ * or NaN) and no others.
  */
 /* One adapter: bf16 device arrays, any alignment of 2 bytes, any rank from 1.
  * A projection that is not adapted has both its pointers NULL. */

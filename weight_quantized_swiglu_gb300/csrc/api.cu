@@ -429,6 +429,7 @@ qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M
         g.epi = kEpiSwiGLU;
         if (ex) {
             g.add = ex->add;
+            g.add_rows = ex->add_rows;
             g.ldadd = (size_t)2 * h->I;
             g.ext = ex->ext;
             g.ext_a = ex->v;

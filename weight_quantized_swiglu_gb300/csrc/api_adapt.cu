@@ -38,6 +38,8 @@ struct qmlp_lora_s {
     void* x_rows = nullptr;          // bf16 [max_M][K]
     int2* ents = nullptr;
     int* ent_slot = nullptr;
+    int* odd = nullptr;              // [slots]: whether B has values that the images leave out
+    int* odd_rows = nullptr;         // [max_M], by position: its slot's
     Owner mem;
 };
 
@@ -204,6 +206,7 @@ LrPack pack_of(const qmlp_lora_s* l, int slot, const qmlp_adapter* a) {
     p.scale = a->scale;
     p.rank_out = l->rank + slot;
     p.scale_out = l->scale + slot;
+    p.odd_out = l->odd ? l->odd + slot : nullptr;
     return p;
 }
 
@@ -270,9 +273,30 @@ cudaError_t lora_shrink_steps(const qmlp_lora_s* l, bool down, const void* z, in
         a.half = l->Rp;
     }
     // the rows of an entry that are other slots'
-    const cudaError_t e =
+    cudaError_t e =
         cudaMemsetAsync(l->ev_v, 0, (size_t)lr_max_entries(M, l->slots) * 256 * a.ldv * sizeof(*l->ev_v), s);
-    return e != cudaSuccess ? e : launch_lr_shrink(a, nc, false, lr_max_tiles(M, l->slots), 1, h->num_sms, s);
+    if (e == cudaSuccess) e = launch_lr_shrink(a, nc, false, lr_max_tiles(M, l->slots), 1, h->num_sms, s);
+    if (e != cudaSuccess) return e;
+    LrOdd o;
+    o.tok = a.tok;
+    o.odd = l->odd;
+    o.v = l->ev_v;
+    o.ldv = a.ldv;
+    o.nc = nc;
+    o.w = down ? l->b_d : l->b_gu;
+    o.N = down ? h->K : h->I;
+    o.R = l->Rp;
+    o.w_slot = (size_t)(down ? 1 : 2) * o.N * o.R;
+    o.T = l->T;
+    o.div[0] = h->gv[down ? 2 : 0].chs;
+    o.div[1] = h->gv[1].chs;
+    if (h->fmt == kNVFP4) {
+        o.mul[0] = h->gv[down ? 2 : 0].inv_g;
+        o.mul[1] = h->gv[1].inv_g;
+    }
+    o.y = l->y;
+    o.ldy = (size_t)(down ? 1 : 2) * o.N;
+    return launch_lr_odd(o, lr_max_tiles(M, l->slots), down ? 1 : 2, s);
 }
 // Whether a call takes them so: M tokens on the pair GEMM, and the entries that
 // the slots can make of them add at most 15% to the contraction (one or two steps
@@ -302,6 +326,7 @@ cudaError_t lora_images(const qmlp_lora_s* l, int slot, const qmlp_adapter* a, c
     m.tiles = h->I / 128;
     m.ext = l->e_gu;
     m.img = l->img_gu + (size_t)slot * m.tiles * m.ext * kImage;
+    m.odd = l->odd + slot;
     const cudaError_t e = launch_lr_image(m, s);
     if (e != cudaSuccess) return e;
     m.parts = 1;
@@ -460,6 +485,8 @@ static qmlp_status lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_
             get(reinterpret_cast<uint8_t**>(&l->x_rows), M * K * 2, false);
             get(&l->ents, (M + 255) / 256, false);
             get(&l->ent_slot, ents, false);
+            get(&l->odd, S, true);
+            get(&l->odd_rows, M, false);
         }
         get(&l->tiles, tiles, false);
         get(&l->n_tiles, 1, true);
@@ -542,9 +569,11 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
             t.entries = lr_max_entries(M, l->slots);
             t.slots = l->slots;
             t.rows = l->perm;
+            t.add = t.add_down = l->y;
+            t.add_rows = l->odd_rows;
             t.before = [&](cudaStream_t st) {
                 cudaError_t e = launch_lr_plan(ids, M, l->slots, l->rank, l->perm, l->tiles, l->n_tiles, l->ents,
-                                               l->ent_slot, st);
+                                               l->ent_slot, l->odd, l->odd_rows, st);
                 if (e == cudaSuccess) e = launch_lr_gather(x, l->perm, M, h->K, l->x_rows, st);
                 return e == cudaSuccess ? lora_shrink_steps(l, false, l->x_rows, M, st) : e;
             };
@@ -554,7 +583,7 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
         t.before = [&](cudaStream_t st) {
             const cudaError_t e = few ? cudaSuccess
                                       : launch_lr_plan(ids, M, l->slots, l->rank, l->perm, l->tiles, l->n_tiles, nullptr,
-                                                       nullptr, st);
+                                                       nullptr, nullptr, nullptr, st);
             return e == cudaSuccess ? terms(false, x, st) : e;
         };
         t.add = l->y;

@@ -148,6 +148,7 @@ struct Args {
     // EXT instances (low-rank adapters and training)
     const float* add;      // optional fp32 [M][ldadd] added after the factor (gate then up columns, or the output's)
     size_t ldadd;
+    const int* add_rows;   // optional [M]: only to the rows whose value is not 0
     float4* gu_g;          // SwiGLU: optional, the gate and up values that act is made of, kept for the backward
     float4* gu_u;          //   pass; SwiGLUGrad: the values kept. [ceil(M / 32)][ldo / 4][32] quads (see gu_at)
     int ncols;             // SwiGLUGrad: I, the columns of each half of out (the last tile may reach past it)
@@ -266,6 +267,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
     if (EXT && a.early) pdl_wait();
     // 2^-sg, for the instances whose every factor is one product
     const float pw = sg >= -126 && sg <= 126 ? __int_as_float((127 - sg) << 23) : scalbnf(1.0f, -sg);
+    const bool adds = EXT && live && a.add && (!a.add_rows || __ldg(a.add_rows + m));
     if (a.epi == kEpiSwiGLU) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 #pragma unroll 1
@@ -282,7 +284,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         dg[j] = du[j] = make_float4(0, 0, 0, 0);
-                        if (a.add) {
+                        if (adds) {
                             const float* ad = a.add + (size_t)m * a.ldadd + col + h + 4 * j;
                             dg[j] = *reinterpret_cast<const float4*>(ad);
                             du[j] = *reinterpret_cast<const float4*>(ad + a.ldo);
@@ -359,8 +361,8 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         const size_t at = gu_at(m, col + h + 4 * j, a.ncols);
                         g4[j] = __ldcs(a.gu_g + at);
                         u4[j] = __ldcs(a.gu_u + at);
-                        ad[j] = a.add ? *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + col + h + 4 * j)
-                                      : make_float4(0, 0, 0, 0);
+                        ad[j] = adds ? *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + col + h + 4 * j)
+                                     : make_float4(0, 0, 0, 0);
                     }
                     uint32_t pg[8], pu[8], lg[8], lu[8];
 #pragma unroll
@@ -407,7 +409,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 f = factor4<FMT>(a.cs0, a.inv0, nt * BN + c0 + j);
-                    if (EXT && a.add) {
+                    if (adds) {
                         const float4 d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + nt * BN + c0 + j);
                         pk[j / 2] = pack_bf16x2(scalbnf(y[j], -sg) * f.x + d.x, scalbnf(y[j + 1], -sg) * f.y + d.y);
                         pk[j / 2 + 1] =
@@ -1201,7 +1203,7 @@ __global__ void __launch_bounds__(256) tail_reduce_kernel(const Args a) {
     const float4 f = factor4<FMT>(a.cs0, a.inv0, n);
     const int sg = a.sig ? a.sig[m] : 0;
     float4 d = make_float4(0, 0, 0, 0);
-    if (a.add) d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + n);
+    if (a.add && (!a.add_rows || a.add_rows[m])) d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + n);
     const int mo = a.rows ? a.rows[m] : m;
     *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)mo * a.ldo + n) =
         make_uint2(pack_bf16x2(scalbnf(s.x, -sg) * f.x + d.x, scalbnf(s.y, -sg) * f.y + d.y),
@@ -1728,6 +1730,8 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.ents = L.ents;
     a.ent_slot = L.ent_slot;
     a.rows = L.rows;
+    a.add_rows = L.add_rows;
+    if (L.add_rows && (!L.add || !L.pair)) return cudaErrorInvalidValue;
     if (L.rows && (L.epi != kEpiPlain || !L.pair || !dq)) return cudaErrorInvalidValue;
     a.out = L.out;
     a.ldo = L.epi == kEpiSwiGLU ? P.N / 2 : (L.epi == kEpiRaw && P.interleaved ? P.N / 2 : P.N);

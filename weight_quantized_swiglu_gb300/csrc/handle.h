@@ -184,6 +184,7 @@ struct GemmTerms {
     const int* ent_slot = nullptr;
     int entries = 0, slots = 0;
     const int* rows = nullptr;
+    const int* add_rows = nullptr;  // add and add_down: only to these tokens
 };
 qmlp_status run_gemm(qmlp_s* h, qmlp_path path, int stages, const void* x, int M, void* out, cudaStream_t s,
                      float* out_f32, const GemmTerms* ex);

@@ -222,6 +222,7 @@ struct GemmLaunch {
     const int* ent_slot = nullptr;
     int entries = 0, slots = 0;
     const int* rows = nullptr;   // plain: the output row of each token
+    const int* add_rows = nullptr;  // CTA pairs: only tokens whose value is not 0 get `add` (null: all)
     void* out_lo = nullptr;      // with gu_g: optional, bf16 of what the rounding of out leaves
     bool images_ready = false;  // dequantise-once: wdec already holds w's images (no predecode launch)
 };

@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(256) swiglu_raw_kernel(const LrSwiGLU a) {
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids, int M, int slots,
                                                     const int* __restrict__ rank, int* perm, int4* tiles,
-                                                    int* n_tiles, int2* ents, int* ent_slot) {
+                                                    int* n_tiles, int2* ents, int* ent_slot,
+                                                    const int* __restrict__ odd, int* odd_rows) {
     __shared__ int cnt[kLrMaxSlots + 1], pos[kLrMaxSlots + 1];
     __shared__ int wsum[3][32];
     __shared__ int first[kLrMaxEnts], last[kLrMaxEnts];
@@ -739,6 +740,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids,
     // counts of 1024 tokens are scanned together, for many the warps claim in turn
     // (3001 tokens, 7 slots: 30 us in turn)
     const bool table = slots < kPlanTable;
+    auto place = [&](int at, int m, int gr) {
+        perm[at] = m;
+        odd_rows[at] = gr < slots ? odd[gr] : 0;
+    };
     for (int b = 0; b < M; b += 1024) {
         const int m = b + tid, gr = m < M ? group(m) : -1;
         if (table) {
@@ -757,13 +762,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids,
                 pos[tid] = at;
             }
             __syncthreads();
-            if (m < M) perm[wcnt[warp * kPlanTable + gr] + __popc(mask & ((1u << lane) - 1u))] = m;
+            if (m < M) place(wcnt[warp * kPlanTable + gr] + __popc(mask & ((1u << lane) - 1u)), m, gr);
             __syncthreads();
         } else {
             for (int w = 0; w < 32 && b + w * 32 < M; ++w) {
                 if (w == warp) {
                     const int at = claim(pos, gr);
-                    if (m < M) perm[at] = m;
+                    if (m < M) place(at, m, gr);
                 }
                 __syncthreads();
             }
@@ -808,7 +813,18 @@ __global__ void __launch_bounds__(256) pack_kernel(const LrPack a) {
     if (blockIdx.y == 0 && blockIdx.x == 0 && threadIdx.x == 0) {
         *a.rank_out = a.r;
         *a.scale_out = a.scale;
+        if (a.odd_out) *a.odd_out = 0;
     }
+}
+
+// B's value as a step image holds it: over its row's factor (T = 3) or as it is.
+QMLP_DEV float step_value(__nv_bfloat16 b, float div, int T) {
+    const float v = __bfloat162float(b);
+    return T == 3 ? __fdividef(v, div) : v;
+}
+// Not finite, in bf16.
+QMLP_DEV bool odd_value(float v) {
+    return (__bfloat16_as_ushort(__float2bfloat16_rn(v)) & 0x7F80u) == 0x7F80u;
 }
 
 // (4.5 MB of images of rank 16: 9 us.)
@@ -835,15 +851,52 @@ __global__ void __launch_bounds__(256) image_kernel(const LrImage a) {
     __align__(16) __nv_bfloat16 o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) o[k] = in && j0 + k < a.r ? src[(size_t)k * a.sj] : __float2bfloat16_rn(0.0f);
-    if (a.T == 3) {
+    bool left = false;
+    if (a.T == 3 || a.odd) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            float v = __fdividef(__bfloat162float(o[k]), div);
+            float v = step_value(o[k], div, a.T);
+            if (a.odd && odd_value(v)) {
+                left = true;
+                v = 0.0f;
+            }
             if (w == 2) v -= __bfloat162float(__float2bfloat16_rn(v));
             o[k] = __float2bfloat16_rn(v);
         }
     }
+    if (left) *a.odd = 1;
     *reinterpret_cast<uint4*>(a.img + ((size_t)img * 2048 + i) * 16) = *reinterpret_cast<const uint4*>(o);
+}
+
+// The further steps of a 256-token tile multiply all its rows by the images of
+// every slot in it, the rows of other slots being zeros. A value of one request's
+// B that is not finite (Inf or NaN, or past bf16 over its row's factor) would make
+// those zeros NaN, so the images hold a zero in its place, and its terms, B v
+// value by value, come to its own tokens' rows alone: through y, which the GEMM's
+// epilogue adds where the plan has marked the row. Calls without such values pay
+// for an empty launch before each GEMM (2 us).
+__global__ void __launch_bounds__(kThr) odd_kernel(const LrOdd a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    int slot, pos0, n, entry0;
+    if (!tile_of(a.tok, blockIdx.x, slot, pos0, n, entry0) || slot < 0 || !a.odd[slot]) return;
+    const int z = blockIdx.z;
+    for (int c = blockIdx.y * kThr + threadIdx.x; c < a.N; c += gridDim.y * kThr) {
+        const __nv_bfloat16* b = a.w + (size_t)slot * a.w_slot + ((size_t)z * a.N + c) * a.R;
+        const float div = a.T == 3 ? a.div[z][c] : 1.0f;
+        uint64_t left = 0;
+        for (int j = 0; j < a.R; ++j) left |= (uint64_t)odd_value(step_value(b[j], div, a.T)) << j;
+        for (int r = 0; r < n; ++r) {
+            const int pos = pos0 + r;
+            const __nv_bfloat16* v = a.v + (size_t)((entry0 + (pos >> 8)) * 256 + (pos & 255)) * a.ldv + z * a.R;
+            float s = 0.0f;
+            for (uint64_t m = left; m; m &= m - 1) {
+                const int j = __ffsll((long long)m) - 1;
+                s = fmaf(__bfloat162float(b[j]), __bfloat162float(v[j]) + __bfloat162float(v[a.nc + j]), s);
+            }
+            a.y[(size_t)pos * a.ldy + (size_t)z * a.N + c] = s * a.mul[z];
+        }
+    }
 }
 
 template <typename K, typename A>
@@ -968,9 +1021,9 @@ cudaError_t launch_lr_swiglu_raw(const LrSwiGLU& a, cudaStream_t s) {
 }
 
 cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, int* perm, int4* tiles, int* n_tiles,
-                           int2* ents, int* ent_slot, cudaStream_t s) {
+                           int2* ents, int* ent_slot, const int* odd, int* odd_rows, cudaStream_t s) {
     if (slots < 1 || slots > kLrMaxSlots || (ents && M > 256 * kLrMaxEnts)) return cudaErrorInvalidValue;
-    plan_kernel<<<1, 1024, 0, s>>>(ids, M, slots, rank, perm, tiles, n_tiles, ents, ent_slot);
+    plan_kernel<<<1, 1024, 0, s>>>(ids, M, slots, rank, perm, tiles, n_tiles, ents, ent_slot, odd, odd_rows);
     return cudaPeekAtLastError();
 }
 
@@ -981,6 +1034,10 @@ cudaError_t launch_lr_gather(const void* x, const int* perm, int M, int K, void*
 
 cudaError_t launch_lr_image(const LrImage& a, cudaStream_t s) {
     return launch_pdl(image_kernel, dim3((unsigned)(a.tiles * a.ext * 8)), 256, 0, a, s);
+}
+
+cudaError_t launch_lr_odd(const LrOdd& a, int tiles, int parts, cudaStream_t s) {
+    return launch_pdl(odd_kernel, dim3((unsigned)tiles, 4, (unsigned)parts), kThr, 0, a, s);
 }
 
 cudaError_t launch_lr_pack(const LrPack& a, cudaStream_t s) {

@@ -136,6 +136,7 @@ struct LrPack {
     float scale = 0.0f;
     int* rank_out = nullptr;
     float* scale_out = nullptr;
+    int* odd_out = nullptr;  // optional: set to 0
 };
 
 struct LrImage {
@@ -147,8 +148,26 @@ struct LrImage {
     int interleaved = 0;  // tiles of 128 rows of part 0 and the same of part 1, each with its own columns
     int tiles = 0, ext = 0;
     uint8_t* img = nullptr;
+    int* odd = nullptr;   // optional: values that are not finite are left out (zeros), and 1 goes there
 };
 cudaError_t launch_lr_image(const LrImage& a, cudaStream_t s);
+
+// y = the terms of the values that a slot's images leave out, for the tokens of
+// the slots that have such values (see odd_kernel).
+struct LrOdd {
+    LrTokens tok;
+    const int* odd = nullptr;          // per slot
+    const __nv_bfloat16* v = nullptr;  // by GEMM entry, two words nc columns apart
+    int ldv = 0, nc = 0;
+    const __nv_bfloat16* w = nullptr;  // padded B's: [slot][part][N][R]
+    size_t w_slot = 0;
+    int N = 0, R = 0, T = 2;
+    const float* div[2] = {nullptr, nullptr};  // T = 3: the rows' factors
+    float mul[2] = {1.0f, 1.0f};               // what v's columns lack, by part
+    float* y = nullptr;                        // fp32 [position][ldy], columns part * N on
+    size_t ldy = 0;
+};
+cudaError_t launch_lr_odd(const LrOdd& a, int tiles, int parts, cudaStream_t s);
 
 int lr_max_tiles(int M, int slots);
 cudaError_t launch_lr_tokgrad(LrTokGrads& a, int nc, int num_sms, cudaStream_t s);
@@ -158,9 +177,10 @@ cudaError_t launch_lr_shrink_few(const LrFew& a, int M, cudaStream_t s);
 cudaError_t launch_lr_expand_few(const LrFew& a, int M, int zs, cudaStream_t s);
 cudaError_t launch_lr_swiglu_raw(const LrSwiGLU& a, cudaStream_t s);
 // With ents: the GEMM's lists too, the entries {first, count} of each 256-token
-// tile and the entries' slots; at most lr_max_entries of them.
+// tile and the entries' slots (at most lr_max_entries of them), and odd_rows, the
+// value of odd at each position's slot (0: no slot).
 cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, int* perm, int4* tiles, int* n_tiles,
-                           int2* ents, int* ent_slot, cudaStream_t s);
+                           int2* ents, int* ent_slot, const int* odd, int* odd_rows, cudaStream_t s);
 inline int lr_max_entries(int M, int slots) { return (M + 255) / 256 + std::min(slots, M); }
 // rows[p] = x[perm[p]] of K bf16 values (a multiple of 8).
 cudaError_t launch_lr_gather(const void* x, const int* perm, int M, int K, void* rows, cudaStream_t s);
