@@ -437,6 +437,9 @@ typedef struct qmlp_lora_s qmlp_lora_t;
  * the padded copies, up to 4 GiB; past that calls do without) and 2 K bytes a
  * token. The slots share h's workspace: calls on them and on h go on one stream
  * at a time.
+ * On a shard's handle (qmlp_create_shard) an adapter has the shard's rows of the
+ * gate and up B and its columns of the down A, and out is the rank's own term in
+ * bf16, as qmlp_forward's.
  * Limits: 1 <= slots <= 1024, 1 <= max_rank <= 64. Synchronizes `stream`.
  * Errors: INVALID_ARG, SHAPE, OOM, CUDA. */
 qmlp_status qmlp_lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_rank, qmlp_stream_t stream);
