@@ -1314,8 +1314,11 @@ cudaError_t launch_m(const Args& a, size_t smem, int M, cudaStream_t s) {
     // one token, (b) otherwise (see the top of the file).
     if constexpr (FMT == kNVFP4)
         if (M == 1) return launch_t<kNVFP4, 1, 1, false, LR>(a, smem, s);
-    // 9..16 tokens: two 8-token column tiles, x staged in halves
-    return M > 8 ? launch_t<FMT, 2, 0, true, LR>(a, smem, s) : launch_one_tile<FMT, LR>(a, smem, M, s);
+    if (M <= 8) return launch_one_tile<FMT, LR>(a, smem, M, s);
+    // 9..16 tokens: two 8-token column tiles, x staged in halves (NVFP4 with
+    // adapters takes the GEMM from 9 tokens on)
+    if constexpr (LR && FMT == kNVFP4) return cudaErrorInvalidValue;
+    else return launch_t<FMT, 2, 0, true, LR>(a, smem, s);
 }
 
 struct Layout {
