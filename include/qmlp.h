@@ -220,11 +220,11 @@ qmlp_status qmlp_debug_set_wait(qmlp_t* h, uint64_t limit_ns, int withhold_last_
 
 /*
  * Index checks. A library built with -DQMLP_DEBUG_BOUNDS (libqmlp_bounds.so;
- * the default build compiles the checks away) checks, in every kernel of the
- * dense block's and the routed experts' forward calls (not in those that
- * adapters, training and AdamW add), the index of each global access whose address comes from layout arithmetic or
+ * the default build compiles the checks away) checks, in every kernel, the
+ * index of each global access whose address comes from layout arithmetic or
  * runtime data (weight-bank blocks and records, partial buffers, outputs,
- * route lists) against the size of its buffer. A failed check never traps:
+ * route lists, the adapters' slots, tiles and rows) against the size of its
+ * buffer, as far as the library knows it. A failed check never traps:
  * the kernel records the first one and skips the access (a load reads zero,
  * a store is dropped, a bulk copy is taken from the start of its buffer), so
  * the call's outputs are then invalid but the device stays usable. This
@@ -237,7 +237,8 @@ int qmlp_debug_bounds_enabled(void);
  * check of any kernel since the last call: *site = the check's number
  * (per source file: 1-9 decode kernel, 11-19 tensor-core GEMM, 21-29 stream-K
  * and split-K decode kernels, 31-39 one-token routed experts, 41-49 grouped
- * routed experts, 51-59 tensor-parallel combine) and *index = the checked
+ * routed experts, 51-59 tensor-parallel combine, 61-69 low-rank products,
+ * 71-79 AdamW) and *index = the checked
  * index (low 48 bits), or 0 and 0. Returns OK, DEVICE_BOUNDS (a check
  * failed), INVALID_ARG (a NULL pointer) or CUDA. A default build always
  * reports OK. */

@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
     const AdamWChunk c = chunks[blockIdx.x];
     if (S8 && threadIdx.x == 0 && blockIdx.x + ahead < gridDim.x) {
         const AdamWChunk& f = chunks[blockIdx.x + ahead];
-        if (f.vec) {
+        if (f.vec && QMLP_INB(f.n - 1, kAdamWChunk, 71)) {
             const uint32_t n = (uint32_t)f.n & ~15u;  // whole 16 bytes of every type
             if (MASTER) to_l2(f.master, n * 4);
             else to_l2(f.param, n * (uint32_t)sizeof(P));
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(kThreads, kResident)
             to_l2(f.v, n);
         }
     }
+    if (!QMLP_INB(c.n - 1, kAdamWChunk, 71)) return;
     const int at = threadIdx.x * kPer;  // within the chunk
     if ((at & ~(kAdamWBlock - 1)) >= c.n) return;  // the whole warp's block is past the end
     const int n = min(max(c.n - at, 0), kPer);     // elements of this lane
@@ -290,5 +291,7 @@ cudaError_t launch_adamw(const AdamWChunk* chunks, long count, bool param_bf16, 
     return grad_bf16 ? launch_s<B, B, false>(chunks, count, s8, k, ahead, s)
                      : launch_s<B, float, false>(chunks, count, s8, k, ahead, s);
 }
+
+QMLP_BOUNDS_UNIT(adamw)
 
 }  // namespace qmlp

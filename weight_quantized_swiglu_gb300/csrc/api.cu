@@ -430,6 +430,7 @@ qmlp_status run_gemm(qmlp_t* h, qmlp_path path, int stages, const void* x, int M
         if (ex) {
             g.add = ex->add;
             g.add_rows = ex->add_rows;
+            g.add_elems = ex->add_elems;
             g.ldadd = (size_t)2 * h->I;
             g.ext = ex->ext;
             g.ext_a = ex->v;
@@ -760,7 +761,8 @@ qmlp_status qmlp_debug_bounds(int* site, unsigned long long* index) {
     cudaError_t (*const units[])(unsigned long long*) = {bounds_take_gemv_split, bounds_take_gemm_tc,
                                                           bounds_take_gemv_stream, bounds_take_gemv_dec,
                                                           bounds_take_moe_awq, bounds_take_moe_grouped,
-                                                          bounds_take_tp_shard};
+                                                          bounds_take_tp_shard, bounds_take_lowrank,
+                                                          bounds_take_adamw};
     unsigned long long first = 0;
     for (auto take : units) {
         unsigned long long v = 0;

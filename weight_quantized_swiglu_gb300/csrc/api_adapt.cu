@@ -1,6 +1,6 @@
-// api_adapt.cu -- the C ABI of training and serving adapters beside the
-// frozen quantized weights (declared in include/qmlp.h): AdamW over many
-// tensors. Argument checks, ownership and dispatch only, as api.cu.
+// api_adapt.cu -- the C ABI of serving adapters beside the frozen quantized
+// weights, of training through them, and of AdamW over many tensors (declared
+// in include/qmlp.h). Argument checks, ownership and dispatch only, as api.cu.
 #include <math.h>
 
 #include "handle.h"
@@ -21,6 +21,7 @@ struct qmlp_lora_s {
     float* v = nullptr;             // few tokens: [kLrFew][2 Rp]
     __nv_bfloat16* vw = nullptr;    // [kLrWords][max_M][2 Rp], by position
     float* y = nullptr;             // [max_M][max(2I, K)]: the adapters' terms
+    size_t y_elems = 0;
     float* raw = nullptr;           // [kMaxGemvM][2I + K]: projections without their factors
     float* vd = nullptr;            // [G][kMaxGemvM][Rp]: the decode CTAs' shares of A_d act
     int* perm = nullptr;
@@ -35,6 +36,7 @@ struct qmlp_lora_s {
     uint8_t* img_gu = nullptr;       // [slots][I / 128][e_gu] and [slots][K / 256][e_d] images of 32 KB
     uint8_t* img_d = nullptr;
     __nv_bfloat16* ev_v = nullptr;   // 256 rows an entry of 64 max(e_gu, e_d)
+    size_t ev_elems = 0;
     void* x_rows = nullptr;          // bf16 [max_M][K]
     int2* ents = nullptr;
     int* ent_slot = nullptr;
@@ -217,6 +219,7 @@ LrTokens tokens_of(const qmlp_lora_s* l, int M) {
     t.n_tiles = l->n_tiles;
     t.perm = l->perm;
     t.M = M;
+    t.slots = l->slots;
     return t;
 }
 cudaError_t lora_shrink(const qmlp_lora_s* l, bool down, const void* z, int M, cudaStream_t s) {
@@ -230,6 +233,7 @@ cudaError_t lora_shrink(const qmlp_lora_s* l, bool down, const void* z, int M, c
     a.scale = l->scale;
     a.v = l->vw;
     a.v_word = (size_t)l->h->max_M * 2 * l->Rp;
+    a.v_elems = a.v_word;  // of each word
     a.ldv = (down ? 1 : 2) * l->Rp;
     return launch_lr_shrink(a, a.ldv, false, lr_max_tiles(M, l->slots), 1, l->h->num_sms, s);
 }
@@ -244,6 +248,7 @@ cudaError_t lora_expand(const qmlp_lora_s* l, bool down, int M, cudaStream_t s) 
     a.w_z = (size_t)a.N * l->Rp;
     a.w_slot = (down ? 1 : 2) * a.w_z;
     a.y = l->y;
+    a.y_elems = l->y_elems;
     a.ldy = (size_t)(down ? 1 : 2) * a.N;
     return launch_lr_expand(a, l->Rp, false, lr_max_tiles(M, l->slots), down ? 1 : 2, s);
 }
@@ -261,6 +266,7 @@ cudaError_t lora_shrink_steps(const qmlp_lora_s* l, bool down, const void* z, in
     a.w_slot = (size_t)nc * a.D;
     a.scale = l->scale;
     a.v = l->ev_v;
+    a.v_elems = l->ev_elems;
     a.v_word = nc;
     a.ldv = word_ld(nc, l->T);
     a.entries = true;
@@ -281,6 +287,7 @@ cudaError_t lora_shrink_steps(const qmlp_lora_s* l, bool down, const void* z, in
     o.tok = a.tok;
     o.odd = l->odd;
     o.v = l->ev_v;
+    o.v_elems = l->ev_elems;
     o.ldv = a.ldv;
     o.nc = nc;
     o.w = down ? l->b_d : l->b_gu;
@@ -295,6 +302,7 @@ cudaError_t lora_shrink_steps(const qmlp_lora_s* l, bool down, const void* z, in
         o.mul[1] = h->gv[1].inv_g;
     }
     o.y = l->y;
+    o.y_elems = l->y_elems;
     o.ldy = (size_t)(down ? 1 : 2) * o.N;
     return launch_lr_odd(o, lr_max_tiles(M, l->slots), down ? 1 : 2, s);
 }
@@ -326,6 +334,7 @@ cudaError_t lora_images(const qmlp_lora_s* l, int slot, const qmlp_adapter* a, c
     m.tiles = h->I / 128;
     m.ext = l->e_gu;
     m.img = l->img_gu + (size_t)slot * m.tiles * m.ext * kImage;
+    m.img_bytes = (size_t)m.tiles * m.ext * kImage;
     m.odd = l->odd + slot;
     const cudaError_t e = launch_lr_image(m, s);
     if (e != cudaSuccess) return e;
@@ -338,6 +347,7 @@ cudaError_t lora_images(const qmlp_lora_s* l, int slot, const qmlp_adapter* a, c
     m.tiles = h->K / 256;
     m.ext = l->e_d;
     m.img = l->img_d + (size_t)slot * m.tiles * m.ext * kImage;
+    m.img_bytes = (size_t)m.tiles * m.ext * kImage;
     return launch_lr_image(m, s);
 }
 LrFew few_of(const qmlp_lora_s* l, bool down, const int32_t* ids) {
@@ -349,6 +359,8 @@ LrFew few_of(const qmlp_lora_s* l, bool down, const int32_t* ids) {
     a.Rp = l->Rp;
     a.ncol = (down ? 1 : 2) * l->Rp;
     a.v = l->v;
+    a.v_elems = (size_t)kLrFew * 2 * l->Rp;
+    a.y_elems = l->y_elems;
     return a;
 }
 cudaError_t lora_shrink_few(const qmlp_lora_s* l, bool down, const void* z, const int32_t* ids, int M, cudaStream_t s,
@@ -466,7 +478,8 @@ static qmlp_status lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_
         get(&l->rank, S, true);
         get(&l->v, (size_t)kLrFew * 2 * R, false);
         get(&l->vw, inner ? 16 : kLrWords * M * 2 * R, false);
-        get(&l->y, (inner && !added ? std::min<size_t>(M, kPairMinM) : M) * std::max(2 * I, K), false);
+        l->y_elems = (inner && !added ? std::min<size_t>(M, kPairMinM) : M) * std::max(2 * I, K);
+        get(&l->y, l->y_elems, false);
         get(&l->raw, (size_t)kMaxGemvM * (2 * I + K), false);
         get(&l->vd, (size_t)std::max(1, h->sp.G) * kMaxGemvM * R, false);
         get(&l->perm, M, false);
@@ -481,7 +494,8 @@ static qmlp_status lora_create(qmlp_lora_t** out, qmlp_t* h, int slots, int max_
             const size_t ents = (size_t)lr_max_entries((int)M, slots);
             get(&l->img_gu, ig, false);
             get(&l->img_d, id, false);
-            get(&l->ev_v, ents * 256 * 64 * std::max(l->e_gu, l->e_d), false);
+            l->ev_elems = ents * 256 * 64 * std::max(l->e_gu, l->e_d);
+            get(&l->ev_v, l->ev_elems, false);
             get(reinterpret_cast<uint8_t**>(&l->x_rows), M * K * 2, false);
             get(&l->ents, (M + 255) / 256, false);
             get(&l->ent_slot, ents, false);
@@ -570,6 +584,7 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
             t.slots = l->slots;
             t.rows = l->perm;
             t.add = t.add_down = l->y;
+            t.add_elems = l->y_elems;
             t.add_rows = l->odd_rows;
             t.before = [&](cudaStream_t st) {
                 cudaError_t e = launch_lr_plan(ids, M, l->slots, l->rank, l->perm, l->tiles, l->n_tiles, l->ents,
@@ -588,6 +603,7 @@ qmlp_status qmlp_lora_forward(qmlp_lora_t* l, const void* x, const int32_t* ids,
         };
         t.add = l->y;
         t.add_down = l->y;
+        t.add_elems = l->y_elems;
         t.between = [&](cudaStream_t st) { return terms(true, h->act, st); };
         return run_gemm(h, QMLP_PATH_AUTO, 3, x, M, out, s, nullptr, &t);
     });
@@ -641,6 +657,7 @@ LrShrink shrink_all(const qmlp_adapter* ad, const void* z, int M, int D, const W
     a.ldx = D;
     a.D = D;
     a.v = w.p;
+    a.v_elems = (size_t)M * w.ld;
     a.v_word = w.nc;
     a.ldv = w.ld;
     a.words = w.T;
@@ -660,6 +677,7 @@ cudaError_t expand_all(const qmlp_train_s* t, const Words& v, int M, int rc, int
     a.w_z = w_z;
     a.N = N;
     a.y = t->l->y;
+    a.y_elems = t->l->y_elems;
     a.ldy = (size_t)N * zs;
     return launch_lr_expand(a, rc, trans, tiles_for(M), zs, s);
 }
@@ -686,9 +704,10 @@ void extend(GemmLaunch& g, const Words& w, const uint8_t* img) {
     g.ext_a = w.p;
     g.ext_b = img;
 }
-void add_terms(GemmLaunch& g, const float* y, size_t ld) {
-    g.add = y;
+void add_terms(GemmLaunch& g, const qmlp_lora_t* l, size_t ld) {
+    g.add = l->y;
     g.ldadd = ld;
+    g.add_elems = l->y_elems;
 }
 
 // Work on the handle's side stream between the events: `fork` follows all that
@@ -751,6 +770,7 @@ LrImage image_of(const qmlp_train_s* t, const qmlp_adapter* a, const Words& w, i
     g.tiles = interleaved ? rows / 128 : (rows + 255) / 256;
     g.ext = w.steps();
     g.img = img;
+    g.img_bytes = (size_t)g.tiles * g.ext * kImage;
     return g;
 }
 
@@ -823,7 +843,7 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     if (ad) {
         g.out_lo = v.act_lo;
         if (ext) extend(g, v.vgu, t->img_gu);
-        else add_terms(g, l->y, (size_t)2 * I);
+        else add_terms(g, l, (size_t)2 * I);
     }
     TRY(launch_gemm(g, h->num_sms, s));
     TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
@@ -852,7 +872,7 @@ cudaError_t train_forward(qmlp_train_s* t, const qmlp_adapter* ad, const void* x
     g.a = v.act;
     g.out = out;
     if (ad && ext) extend(g, v.vd, t->img_d);
-    else if (ad) add_terms(g, l->y, K);
+    else if (ad) add_terms(g, l, K);
     return launch_gemm(g, h->num_sms, s);
 }
 
@@ -926,7 +946,7 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     if (ad) {
         g.out_lo = lo;
         if (ext_d) extend(g, wd, t->img_d);
-        else add_terms(g, l->y, I);
+        else add_terms(g, l, I);
     }
     TRY(launch_gemm(g, h->num_sms, s));
     TRY(cudaStreamWaitEvent(s, h->ev_join, 0));
@@ -960,7 +980,7 @@ cudaError_t train_backward(qmlp_train_s* t, const qmlp_adapter* ad, const void* 
     g.a = t->dgu;
     g.out = dx;
     if (ad && ext) extend(g, wv, t->img_gu);
-    else if (ad) add_terms(g, l->y, K);
+    else if (ad) add_terms(g, l, K);
     TRY(launch_gemm(g, h->num_sms, s));
     if (!gr) return cudaSuccess;
     // every gradient in one launch: B's = c dy^T (z A^T), A's = c (dy B)^T z

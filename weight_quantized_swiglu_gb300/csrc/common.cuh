@@ -181,9 +181,9 @@ QMLP_DEV void mbar_arrive(uint32_t bar) {
 // caller skips the access: a load reads zero, a store is dropped, a bulk copy
 // is taken from the start of its buffer so that its barrier still completes.
 // No check traps. The host reads and clears the words (qmlp_debug_bounds).
-// (The kernels of adapters, training and AdamW alone, lowrank.cu and adamw.cu,
-// have none.) Sites are numbered per file (gemv_split 1-9, gemm_tc 11-19, gemv_stream and
-// gemv_dec 21-29, moe_awq 31-39, moe_grouped 41-49, tp_shard 51-59).
+// Sites are numbered per file (gemv_split 1-9, gemm_tc 11-19, gemv_stream and
+// gemv_dec 21-29, moe_awq 31-39, moe_grouped 41-49, tp_shard 51-59, lowrank
+// 61-69, adamw 71-79).
 // ---------------------------------------------------------------------------
 #ifdef QMLP_DEBUG_BOUNDS
 static __device__ unsigned long long g_bounds_word;

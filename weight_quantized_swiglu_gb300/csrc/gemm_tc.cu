@@ -149,6 +149,9 @@ struct Args {
     const float* add;      // optional fp32 [M][ldadd] added after the factor (gate then up columns, or the output's)
     size_t ldadd;
     const int* add_rows;   // optional [M]: only to the rows whose value is not 0
+    size_t add_elems;      // index checks: floats of add, quads of gu_g and gu_u
+    size_t gu_quads;
+    int ext_rows;          // index checks: rows of the adapters' images
     float4* gu_g;          // SwiGLU: optional, the gate and up values that act is made of, kept for the backward
     float4* gu_u;          //   pass; SwiGLUGrad: the values kept. [ceil(M / 32)][ldo / 4][32] quads (see gu_at)
     int ncols;             // SwiGLUGrad: I, the columns of each half of out (the last tile may reach past it)
@@ -284,7 +287,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         dg[j] = du[j] = make_float4(0, 0, 0, 0);
-                        if (adds) {
+                        if (adds && QMLP_INB((size_t)m * a.ldadd + a.ldo + col + h + 4 * j + 3, a.add_elems, 19)) {
                             const float* ad = a.add + (size_t)m * a.ldadd + col + h + 4 * j;
                             dg[j] = *reinterpret_cast<const float4*>(ad);
                             du[j] = *reinterpret_cast<const float4*>(ad + a.ldo);
@@ -304,8 +307,10 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         }
                         if (a.gu_g) {
                             const size_t at = gu_at(m, col + h + 4 * j, a.ldo);
-                            __stcs(a.gu_g + at, make_float4(g4[0], g4[1], g4[2], g4[3]));
-                            __stcs(a.gu_u + at, make_float4(u4[0], u4[1], u4[2], u4[3]));
+                            if (QMLP_INB(at, a.gu_quads, 19)) {
+                                __stcs(a.gu_g + at, make_float4(g4[0], g4[1], g4[2], g4[3]));
+                                __stcs(a.gu_u + at, make_float4(u4[0], u4[1], u4[2], u4[3]));
+                            }
                         }
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
@@ -314,6 +319,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         }
                     }
                     const size_t at = (size_t)m * a.ldo + col + h;
+                    if (!QMLP_INB(col + h + 15, a.ldo, 12)) continue;
                     store16(out + at, pk);
                     if (a.out_lo) store16(reinterpret_cast<__nv_bfloat16*>(a.out_lo) + at, lo);
                 }
@@ -359,9 +365,10 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const size_t at = gu_at(m, col + h + 4 * j, a.ncols);
-                        g4[j] = __ldcs(a.gu_g + at);
-                        u4[j] = __ldcs(a.gu_u + at);
-                        ad[j] = adds ? *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + col + h + 4 * j)
+                        const bool in = QMLP_INB(at, a.gu_quads, 19);
+                        g4[j] = __ldcs(a.gu_g + (in ? at : 0));
+                        u4[j] = __ldcs(a.gu_u + (in ? at : 0));
+                        ad[j] = adds && QMLP_INB((size_t)m * a.ldadd + col + h + 4 * j + 3, a.add_elems, 19) ? *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + col + h + 4 * j)
                                      : make_float4(0, 0, 0, 0);
                     }
                     uint32_t pg[8], pu[8], lg[8], lu[8];
@@ -388,6 +395,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         }
                     }
                     const size_t at = (size_t)m * 2 * a.ncols + col + h;
+                    if (!QMLP_INB(col + h + 15, a.ncols, 12)) continue;
                     store16(out + at, pg);
                     store16(out + at + a.ncols, pu);
                     if (a.out_lo) {
@@ -409,7 +417,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
 #pragma unroll
                 for (int j = 0; j < 32; j += 4) {
                     const float4 f = factor4<FMT>(a.cs0, a.inv0, nt * BN + c0 + j);
-                    if (adds) {
+                    if (adds && QMLP_INB((size_t)m * a.ldadd + nt * BN + c0 + j + 3, a.add_elems, 19)) {
                         const float4 d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + nt * BN + c0 + j);
                         pk[j / 2] = pack_bf16x2(scalbnf(y[j], -sg) * f.x + d.x, scalbnf(y[j + 1], -sg) * f.y + d.y);
                         pk[j / 2 + 1] =
@@ -948,7 +956,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
                         if (EXT && ks >= KS) {
                             const int e = (ks - KS) % a.ext, n = first + (ks - KS) / a.ext;
                             const int slot = a.ents ? __ldg(a.ent_slot + n) : 0;
-                            const int row = ((slot * Nt + nt) * a.ext + e) * BN;
+                            int row = ((slot * Nt + nt) * a.ext + e) * BN;
+                            if (!QMLP_INB(row, a.ext_rows - BN + 1, 19)) row = 0;
 #pragma unroll
                             for (uint32_t r = 0; r < 2; ++r) {
                                 tma_load_2d_pair(base_s + S::A + s * kABytes, r, &amap2, e * BK,
@@ -1073,7 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
                 for (int c0 = grp * 32; c0 < BN; c0 += kGroups * 32) {
                     float y[32];
                     tmem_ld32(tbase + c0, y);
-                    if (live) {
+                    if (live && QMLP_INB(ws - a.ws + c0 + 31, a.ws_elems, 13)) {
                         float4* dst = reinterpret_cast<float4*>(ws + c0);
 #pragma unroll
                         for (int v = 0; v < 8; ++v) dst[v] = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
@@ -1163,7 +1172,7 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const Args a) {
         }
         const float fg = FMT == kNVFP4 ? a.inv0 : a.cs0[n], fu = FMT == kNVFP4 ? a.inv1 : a.cs1[n];
         float gv = scalbnf(g, -sg) * fg, uv = scalbnf(u, -sg) * fu;
-        if (a.add) {
+        if (a.add && QMLP_INB((size_t)m * a.ldadd + nout + n, a.add_elems, 19)) {
             gv += a.add[(size_t)m * a.ldadd + n];
             uv += a.add[(size_t)m * a.ldadd + nout + n];
         }
@@ -1174,7 +1183,7 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const Args a) {
             if (QMLP_INB((size_t)m * a.N + sp * plane + n, a.ws_elems, 14)) y += ws[sp * plane + n];
         const float f = FMT == kNVFP4 ? a.inv0 : a.cs0[n];
         y = scalbnf(y, -sg) * f;
-        if (a.add) y += a.add[(size_t)m * a.ldadd + n];
+        if (a.add && QMLP_INB((size_t)m * a.ldadd + n, a.add_elems, 19)) y += a.add[(size_t)m * a.ldadd + n];
         *out = __float2bfloat16_rn(y);
     }
 }
@@ -1194,6 +1203,7 @@ __global__ void __launch_bounds__(256) tail_reduce_kernel(const Args a) {
     float4 s = make_float4(0, 0, 0, 0);
 #pragma unroll 8
     for (int k = 0; k < a.tail_splits; ++k) {
+        if (!QMLP_INB((ws - reinterpret_cast<const float4*>(a.ws) + (size_t)k * (2 * BM * BN / 4)) * 4 + 3, a.ws_elems, 14)) break;
         const float4 v = __ldcg(ws + (size_t)k * (2 * BM * BN / 4));
         s.x += v.x;
         s.y += v.y;
@@ -1203,8 +1213,9 @@ __global__ void __launch_bounds__(256) tail_reduce_kernel(const Args a) {
     const float4 f = factor4<FMT>(a.cs0, a.inv0, n);
     const int sg = a.sig ? a.sig[m] : 0;
     float4 d = make_float4(0, 0, 0, 0);
-    if (a.add && (!a.add_rows || a.add_rows[m])) d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + n);
+    if (a.add && (!a.add_rows || a.add_rows[m]) && QMLP_INB((size_t)m * a.ldadd + n + 3, a.add_elems, 19)) d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + n);
     const int mo = a.rows ? a.rows[m] : m;
+    if (!QMLP_INB(mo, a.M, 12) || !QMLP_INB(n + 3, a.ldo, 12)) return;
     *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + (size_t)mo * a.ldo + n) =
         make_uint2(pack_bf16x2(scalbnf(s.x, -sg) * f.x + d.x, scalbnf(s.y, -sg) * f.y + d.y),
                    pack_bf16x2(scalbnf(s.z, -sg) * f.z + d.z, scalbnf(s.w, -sg) * f.w + d.w));
@@ -1279,7 +1290,7 @@ struct PreT {
     int half;       // interleaved: contraction steps of the gate half, else 0
     const float* mul0;
     const float* mul1;
-    size_t tiles_bytes;
+    size_t tiles_bytes, img_bytes;
 };
 constexpr int kPitchT = 256 + 8;  // 16-bit values of a decoded source row in shared memory
 constexpr int kSmemT = 64 * kPitchT * 2 + 128;
@@ -1370,7 +1381,7 @@ __global__ void __launch_bounds__(256) predecode_t_kernel(const PreT a) {
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && QMLP_INB(((size_t)rt * a.steps + cs + 1) * kBBytes - 1, a.img_bytes, 18)) {
         uint8_t* dst = a.img + ((size_t)rt * a.steps + cs) * kBBytes;
         asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(base_s),
                      "r"(kBBytes)
@@ -1634,6 +1645,7 @@ cudaError_t launch_gemm_predecode_t(const GemmProj& P, const float* mul0, const 
     a.mul0 = mul0;
     a.mul1 = mul1;
     a.tiles_bytes = gemm_tiles_bytes(P.fmt, P.N, P.K);
+    a.img_bytes = img_bytes;
     const dim3 grid((unsigned)a.steps, (unsigned)((P.K + BN - 1) / BN));
     static_assert(kSmemT <= 48 * 1024, "no attribute needed");
     if (P.fmt == kFP8 && f16) predecode_t_kernel<kFP8, true><<<grid, 256, kSmemT, s>>>(a);
@@ -1731,6 +1743,9 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.ent_slot = L.ent_slot;
     a.rows = L.rows;
     a.add_rows = L.add_rows;
+    a.add_elems = L.add_elems;
+    a.gu_quads = gemm_gu_bytes(L.M, L.epi == kEpiSwiGLUGrad ? L.ncols : P.N / 2) / sizeof(float4);
+    a.ext_rows = (P.N / BN) * L.ext * BN * (L.ents ? L.slots : 1);
     if (L.add_rows && (!L.add || !L.pair)) return cudaErrorInvalidValue;
     if (L.rows && (L.epi != kEpiPlain || !L.pair || !dq)) return cudaErrorInvalidValue;
     a.out = L.out;

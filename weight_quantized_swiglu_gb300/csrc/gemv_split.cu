@@ -358,7 +358,8 @@ QMLP_DEV void lr_warps(const SplitLora& lr, int M, int I, int tslice, int tid, f
         }
         s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
         s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
-        if ((lane & 3) == 0) lr.vd[((size_t)blockIdx.x * M + m) * R + j + (lane >> 2)] = s[0];
+        const size_t at = ((size_t)blockIdx.x * M + m) * R + j + (lane >> 2);
+        if ((lane & 3) == 0 && QMLP_INB(at, (size_t)gridDim.x * M * R, 9)) lr.vd[at] = s[0];
     }
     mbar_arrive(bar0 + 16);
 }

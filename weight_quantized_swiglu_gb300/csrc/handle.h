@@ -185,6 +185,7 @@ struct GemmTerms {
     int entries = 0, slots = 0;
     const int* rows = nullptr;
     const int* add_rows = nullptr;  // add and add_down: only to these tokens
+    size_t add_elems = 0;           // index checks: values that add and add_down hold
 };
 qmlp_status run_gemm(qmlp_s* h, qmlp_path path, int stages, const void* x, int M, void* out, cudaStream_t s,
                      float* out_f32, const GemmTerms* ex);

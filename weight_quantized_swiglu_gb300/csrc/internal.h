@@ -196,7 +196,10 @@ struct GemmLaunch {
     bool pair = false;        // the CTA-pair kernel (M >= kPairMinM; never split-K)
     uint8_t* wdec = nullptr;  // dequantise-once: decoded stage images of w (null: the decoder warps decode)
     size_t wdec_bytes = 0;    // bytes of wdec, >= gemm_decoded_bytes(w.N, w.K)
-    const float* add = nullptr;  // fp32 [M][ldadd], added after the factor: gate's I columns then up's
+    // fp32 [M][ldadd], added after the factor: gate's I columns then up's (SwiGLU),
+    // or the output's columns (plain, grad); the terms of low-rank adapters
+    const float* add = nullptr;
+    size_t ldadd = 0, add_elems = 0;  // add_elems: index checks
     // early: the kernels that write add are launched just before, each with
     // programmatic dependent launch; nothing else that the GEMM reads (prescaled
     // activations, images) comes from them. It reads those without a wait, so the
@@ -204,7 +207,6 @@ struct GemmLaunch {
     // all that came before has completed and is visible
     bool early = false;
     bool prescaled = false;      // a16 and sig are written (launch_gemm_prescale)
-    size_t ldadd = 0;            // (SwiGLU), or the output's columns (plain, grad); low-rank adapters
     void* gu_g = nullptr;        // training: fp32 gate and up values, kept by SwiGLU and read by SwiGLUGrad,
     void* gu_u = nullptr;        // gemm_gu_bytes(M, I) each
     int ncols = 0;               // SwiGLUGrad: I; out = [M][2I]
@@ -348,5 +350,7 @@ cudaError_t bounds_take_gemv_dec(unsigned long long* v);
 cudaError_t bounds_take_moe_awq(unsigned long long* v);
 cudaError_t bounds_take_moe_grouped(unsigned long long* v);
 cudaError_t bounds_take_tp_shard(unsigned long long* v);
+cudaError_t bounds_take_lowrank(unsigned long long* v);
+cudaError_t bounds_take_adamw(unsigned long long* v);
 
 }  // namespace qmlp

@@ -103,11 +103,18 @@ QMLP_DEV bool tile_of(const LrTokens& t, int i, int& slot, int& pos0, int& n, in
     }
     if (i >= *t.n_tiles) return false;
     const int4 e = t.tiles[i];
+    if (!QMLP_INB(e.x + 1, t.slots + 1, 61) || !QMLP_INB(e.z - 1, kT, 61) || !QMLP_INB(e.y, t.M - e.z + 1, 61)) return false;
     slot = e.x;
     pos0 = e.y;
     n = e.z;
     entry0 = e.w;
     return true;
+}
+
+// The token at a position (index checks: `bad` for one that does not exist).
+QMLP_DEV int token_at(const LrTokens& t, int pos, int bad) {
+    const int tok = t.perm ? t.perm[pos] : pos;
+    return QMLP_INB(tok, t.M, 62) ? tok : bad;
 }
 
 // The CTAs of a cluster (along y) hold partial sums of one tile in their shared
@@ -180,7 +187,7 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
     for (int i = 0; i < 4; ++i) {
         const int r = (tid >> 3) + 16 * i;
         xl[i] = r < n;
-        const int tok = xl[i] ? (a.tok.perm ? a.tok.perm[pos0 + r] : pos0 + r) : 0;
+        const int tok = xl[i] ? token_at(a.tok, pos0 + r, 0) : 0;
         xr[i] = x + (size_t)tok * a.ldx;
     }
     auto load = [&](int step, int stage) {
@@ -288,7 +295,9 @@ __global__ void __launch_bounds__(kThr) shrink_kernel(const LrShrink a) {
             if (a.again) w[e][2] = w[e][0];
         }
         const int pos = pos0 + row;
-        __nv_bfloat16* line = a.v + (size_t)(a.entries ? (entry0 + (pos >> 8)) * 256 + (pos & 255) : pos) * a.ldv;
+        const ptrdiff_t line0 = (ptrdiff_t)(a.entries ? (entry0 + (pos >> 8)) * 256 + (pos & 255) : pos) * a.ldv;
+        if (!QMLP_INB(line0, (ptrdiff_t)a.v_elems - a.ldv + 1, 63)) continue;
+        __nv_bfloat16* line = a.v + line0;
         __nv_bfloat16* o = line + z * NC + col;
 #pragma unroll
         for (int k = 0; k < kLrWords; ++k)
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(kThr) expand_kernel(const LrExpand a) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const int r = row0 + 8 * h;
-        tok[h] = r < n ? (a.tok.perm ? a.tok.perm[pos0 + r] : pos0 + r) : -1;
+        tok[h] = r < n ? token_at(a.tok, pos0 + r, -1) : -1;
     }
     auto load = [&](int p, int stage) {
         constexpr int kC = 64 * RC / 8;
@@ -410,7 +419,8 @@ __global__ void __launch_bounds__(kThr) expand_kernel(const LrExpand a) {
                     *reinterpret_cast<__nv_bfloat162*>(a.out + (size_t)tok[h] * a.N + col) =
                         __floats2bfloat162_rn(r.x * f0 + v0, r.y * f1 + v1);
                 } else {
-                    *reinterpret_cast<float2*>(a.y + (size_t)tok[h] * a.ldy + (size_t)z * a.N + col) = make_float2(v0, v1);
+                    const size_t at = (size_t)tok[h] * a.ldy + (size_t)z * a.N + col;
+                    if (QMLP_INB(at + 1, a.y_elems, 64)) *reinterpret_cast<float2*>(a.y + at) = make_float2(v0, v1);
                 }
             }
         }
@@ -537,12 +547,13 @@ __global__ void __launch_bounds__(kThr) tokgrad_kernel(const __grid_constant__ L
             const float f = a.div ? a.div[d] : 1.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (col + e < a.r)
+                if (col + e < a.r && QMLP_INB((size_t)d * a.r + col + e, (size_t)a.D * a.r, 68))
                     a.out[(size_t)d * a.r + col + e] = __float2bfloat16_rn(a.div ? s[e] / f : s[e] * a.mul);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (col + e < a.r) a.out[(size_t)(col + e) * a.D + d] = __float2bfloat16_rn(s[e] * a.mul);
+                if (col + e < a.r && QMLP_INB((size_t)(col + e) * a.D + d, (size_t)a.D * a.r, 68))
+                    a.out[(size_t)(col + e) * a.D + d] = __float2bfloat16_rn(s[e] * a.mul);
         }
     }
     if (ns > 1) cluster_sync();
@@ -585,7 +596,7 @@ __global__ void __launch_bounds__(kThr) shrink_few_kernel(const LrFew a) {
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (lane == 0) red[warp] = s;
     __syncthreads();
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0 && QMLP_INB((size_t)m * a.ncol + j, a.v_elems, 65))
         a.v[(size_t)m * a.ncol + j] = has ? (red[0] + red[1] + red[2] + red[3]) * a.scale[slot] : 0.0f;
 }
 
@@ -617,7 +628,8 @@ __global__ void __launch_bounds__(kThr) expand_few_kernel(const LrFew a) {
             }
         }
         if (a.out) a.out[(size_t)m * a.D + n] = __float2bfloat16_rn(a.raw[(size_t)m * a.D + n] * f + s);
-        else a.y[(size_t)m * a.ldy + (size_t)z * a.D + n] = s;
+        else if (QMLP_INB((size_t)m * a.ldy + (size_t)z * a.D + n, a.y_elems, 65))
+            a.y[(size_t)m * a.ldy + (size_t)z * a.D + n] = s;
     }
 }
 
@@ -643,7 +655,8 @@ __global__ void __launch_bounds__(256) swiglu_raw_kernel(const LrSwiGLU a) {
 __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids, int M, int slots,
                                                     const int* __restrict__ rank, int* perm, int4* tiles,
                                                     int* n_tiles, int2* ents, int* ent_slot,
-                                                    const int* __restrict__ odd, int* odd_rows) {
+                                                    const int* __restrict__ odd, int* odd_rows, int max_tiles,
+                                                    int max_ents) {
     __shared__ int cnt[kLrMaxSlots + 1], pos[kLrMaxSlots + 1];
     __shared__ int wsum[3][32];
     __shared__ int first[kLrMaxEnts], last[kLrMaxEnts];
@@ -710,10 +723,10 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids,
         if (i <= slots) {
             pos[i] = p0;
             const int e0 = be + se - ne;  // its first entry
-            for (int k = 0; k < tl; ++k)
+            for (int k = 0; k < tl && QMLP_INB(bt + st - tl + k, max_tiles, 66); ++k)
                 tiles[bt + st - tl + k] =
                     make_int4(i < slots ? i : -1, p0 + k * kT, min(kT, c - k * kT), e0 - (p0 >> 8));
-            for (int k = 0; k < ne; ++k) {
+            for (int k = 0; k < ne && QMLP_INB(e0 + k, max_ents, 66) && QMLP_INB((p0 >> 8) + k, big, 66); ++k) {
                 // positions are filled from 0 on: a tile's entries lie together,
                 // from the group at its first position to that at its last
                 const int t = (p0 >> 8) + k, lo = t * 256, hi = min(lo + 256, with) - 1;
@@ -730,7 +743,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids,
     if (!ents) {
         for (int m = tid; m < (M + 31) / 32 * 32; m += 1024) {
             const int at = claim(pos, m < M ? group(m) : -1);
-            if (m < M) perm[at] = m;
+            if (m < M && QMLP_INB(at, M, 66)) perm[at] = m;
         }
         if (tid == 0) *n_tiles = til0;
         return;
@@ -741,6 +754,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const int* __restrict__ ids,
     // (3001 tokens, 7 slots: 30 us in turn)
     const bool table = slots < kPlanTable;
     auto place = [&](int at, int m, int gr) {
+        if (!QMLP_INB(at, M, 66)) return;
         perm[at] = m;
         odd_rows[at] = gr < slots ? odd[gr] : 0;
     };
@@ -782,7 +796,8 @@ __global__ void __launch_bounds__(256) gather_kernel(const uint4* __restrict__ x
                                                      uint4* rows) {
     pdl_launch_dependents();
     pdl_wait();
-    const uint4* src = x + (size_t)perm[blockIdx.x] * n16;
+    const int tok = perm[blockIdx.x];
+    const uint4* src = x + (size_t)(QMLP_INB(tok, gridDim.x, 62) ? tok : 0) * n16;
     uint4* dst = rows + (size_t)blockIdx.x * n16;
     for (int i = threadIdx.x; i < n16; i += 256) dst[i] = src[i];
 }
@@ -865,7 +880,8 @@ __global__ void __launch_bounds__(256) image_kernel(const LrImage a) {
         }
     }
     if (left) *a.odd = 1;
-    *reinterpret_cast<uint4*>(a.img + ((size_t)img * 2048 + i) * 16) = *reinterpret_cast<const uint4*>(o);
+    if (QMLP_INB(((size_t)img * 2048 + i) * 16 + 15, a.img_bytes, 67))
+        *reinterpret_cast<uint4*>(a.img + ((size_t)img * 2048 + i) * 16) = *reinterpret_cast<const uint4*>(o);
 }
 
 // The further steps of a 256-token tile multiply all its rows by the images of
@@ -888,13 +904,16 @@ __global__ void __launch_bounds__(kThr) odd_kernel(const LrOdd a) {
         for (int j = 0; j < a.R; ++j) left |= (uint64_t)odd_value(step_value(b[j], div, a.T)) << j;
         for (int r = 0; r < n; ++r) {
             const int pos = pos0 + r;
-            const __nv_bfloat16* v = a.v + (size_t)((entry0 + (pos >> 8)) * 256 + (pos & 255)) * a.ldv + z * a.R;
+            const ptrdiff_t line = (ptrdiff_t)((entry0 + (pos >> 8)) * 256 + (pos & 255)) * a.ldv;
+            if (!QMLP_INB(line, (ptrdiff_t)a.v_elems - a.ldv + 1, 63)) continue;
+            const __nv_bfloat16* v = a.v + line + z * a.R;
             float s = 0.0f;
             for (uint64_t m = left; m; m &= m - 1) {
                 const int j = __ffsll((long long)m) - 1;
                 s = fmaf(__bfloat162float(b[j]), __bfloat162float(v[j]) + __bfloat162float(v[a.nc + j]), s);
             }
-            a.y[(size_t)pos * a.ldy + (size_t)z * a.N + c] = s * a.mul[z];
+            const size_t at = (size_t)pos * a.ldy + (size_t)z * a.N + c;
+            if (QMLP_INB(at, a.y_elems, 64)) a.y[at] = s * a.mul[z];
         }
     }
 }
@@ -1023,7 +1042,8 @@ cudaError_t launch_lr_swiglu_raw(const LrSwiGLU& a, cudaStream_t s) {
 cudaError_t launch_lr_plan(const int* ids, int M, int slots, const int* rank, int* perm, int4* tiles, int* n_tiles,
                            int2* ents, int* ent_slot, const int* odd, int* odd_rows, cudaStream_t s) {
     if (slots < 1 || slots > kLrMaxSlots || (ents && M > 256 * kLrMaxEnts)) return cudaErrorInvalidValue;
-    plan_kernel<<<1, 1024, 0, s>>>(ids, M, slots, rank, perm, tiles, n_tiles, ents, ent_slot, odd, odd_rows);
+    plan_kernel<<<1, 1024, 0, s>>>(ids, M, slots, rank, perm, tiles, n_tiles, ents, ent_slot, odd, odd_rows,
+                                   lr_max_tiles(M, slots), lr_max_entries(M, slots));
     return cudaPeekAtLastError();
 }
 
@@ -1044,5 +1064,7 @@ cudaError_t launch_lr_pack(const LrPack& a, cudaStream_t s) {
     pack_kernel<<<dim3(256, a.count), 256, 0, s>>>(a);
     return cudaPeekAtLastError();
 }
+
+QMLP_BOUNDS_UNIT(lowrank)
 
 }  // namespace qmlp

@@ -21,6 +21,7 @@ struct LrTokens {
     const int* n_tiles = nullptr;
     const int* perm = nullptr;    // position -> token
     int M = 0;
+    int slots = 1;                // index checks: slots that a tile may name
 };
 
 struct LrShrink {
@@ -45,6 +46,7 @@ struct LrShrink {
     bool entries = false;          // rows by GEMM entry: 256 entry(p) + p % 256 for position p
     bool again = false;            // the third word is the first once more
     int pad = 0;                   // columns at a row's end to fill with zeros
+    size_t v_elems = 0;            // index checks: values that v holds
     float mul0 = 1.0f, mul1 = 1.0f;  // factors of the columns before and from `half` on
     int half = 1 << 30;
 };
@@ -58,7 +60,7 @@ struct LrExpand {
     size_t w_slot = 0, w_z = 0;
     int N = 0;
     float* y = nullptr;  // fp32 [M][ldy], columns z * N on
-    size_t ldy = 0;
+    size_t ldy = 0, y_elems = 0;  // y_elems: index checks
     // or out = bf16(factor raw + y)
     __nv_bfloat16* out = nullptr;
     const float* raw = nullptr;     // fp32 [M][N]
@@ -80,7 +82,7 @@ struct LrFew {
     int ncol = 0;        // columns of v
     float* v = nullptr;  // [M][ncol]
     float* y = nullptr;  // expand: as LrExpand
-    size_t ldy = 0;
+    size_t ldy = 0, v_elems = 0, y_elems = 0;
     __nv_bfloat16* out = nullptr;
     const float* raw = nullptr;
     const float* factor = nullptr;
@@ -148,6 +150,7 @@ struct LrImage {
     int interleaved = 0;  // tiles of 128 rows of part 0 and the same of part 1, each with its own columns
     int tiles = 0, ext = 0;
     uint8_t* img = nullptr;
+    size_t img_bytes = 0; // index checks
     int* odd = nullptr;   // optional: values that are not finite are left out (zeros), and 1 goes there
 };
 cudaError_t launch_lr_image(const LrImage& a, cudaStream_t s);
@@ -165,7 +168,7 @@ struct LrOdd {
     const float* div[2] = {nullptr, nullptr};  // T = 3: the rows' factors
     float mul[2] = {1.0f, 1.0f};               // what v's columns lack, by part
     float* y = nullptr;                        // fp32 [position][ldy], columns part * N on
-    size_t ldy = 0;
+    size_t ldy = 0, v_elems = 0, y_elems = 0;
 };
 cudaError_t launch_lr_odd(const LrOdd& a, int tiles, int parts, cudaStream_t s);
 
