@@ -307,9 +307,13 @@ cudaError_t lora_shrink_steps(const qmlp_lora_s* l, bool down, const void* z, in
     return launch_lr_odd(o, lr_max_tiles(M, l->slots), down ? 1 : 2, s);
 }
 // Whether a call takes them so: M tokens on the pair GEMM, and the entries that
-// the slots can make of them add at most 15% to the contraction (one or two steps
-// an entry for NVFP4 up to rank 32; the terms as an fp32 array cost 20% at rank
-// 64, 3001 tokens).
+// the slots can make of them add at most 15% to gate/up's contraction (down's is
+// longer). Measured on the 27B-class shape, steps against an fp32 array, us: 3001
+// FP8 tokens of rank 64, 7 slots (12%) 1191 / 1302, 12 slots (15%) 1236 / 1300, 24
+// (23%) 1290 / 1325, 48 (38%) 1417 / 1338; 3001 NVFP4 tokens of rank 16, 64 slots
+// (8%) 1162 / 1241, 132 (15%) 1233 / 1271, 264 (29%) 1433 / 1404; 1024 FP8 tokens
+// of rank 32, 12 slots (15%) 537 / 564. They meet at about 25%; up to there the
+// slots' images cost memory that grows with them for the last 3%.
 bool lora_steps(const qmlp_lora_s* l, int M) {
     if (!l->steps || M < kDqMinM) return false;
     const long most = (long)lr_max_entries(M, l->slots) * l->e_gu;

@@ -368,8 +368,9 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         const bool in = QMLP_INB(at, a.gu_quads, 19);
                         g4[j] = __ldcs(a.gu_g + (in ? at : 0));
                         u4[j] = __ldcs(a.gu_u + (in ? at : 0));
-                        ad[j] = adds && QMLP_INB((size_t)m * a.ldadd + col + h + 4 * j + 3, a.add_elems, 19) ? *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + col + h + 4 * j)
-                                     : make_float4(0, 0, 0, 0);
+                        const size_t ai = (size_t)m * a.ldadd + col + h + 4 * j;
+                        ad[j] = adds && QMLP_INB(ai + 3, a.add_elems, 19) ? *reinterpret_cast<const float4*>(a.add + ai)
+                                                                          : make_float4(0, 0, 0, 0);
                     }
                     uint32_t pg[8], pu[8], lg[8], lu[8];
 #pragma unroll
