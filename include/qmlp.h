@@ -238,7 +238,7 @@ int qmlp_debug_bounds_enabled(void);
  * (per source file: 1-9 decode kernel, 11-19 tensor-core GEMM, 21-29 stream-K
  * and split-K decode kernels, 31-39 one-token routed experts, 41-49 grouped
  * routed experts, 51-59 tensor-parallel combine, 61-69 low-rank products,
- * 71-79 AdamW) and *index = the checked
+ * 71-79 AdamW, 81-89 norms) and *index = the checked
  * index (low 48 bits), or 0 and 0. Returns OK, DEVICE_BOUNDS (a check
  * failed), INVALID_ARG (a NULL pointer) or CUDA. A default build always
  * reports OK. */
@@ -568,6 +568,78 @@ void qmlp_adamw_destroy(qmlp_adamw_t* h);
  * Errors: INVALID_ARG (null; step < 1; beta outside [0, 1); a value that is
  * not finite), CUDA. */
 qmlp_status qmlp_adamw_step(qmlp_adamw_t* h, const qmlp_adamw_hyper* hyper, qmlp_stream_t stream);
+
+/*
+ * The norms before and after a block, fused with the block's gate, residual and
+ * residual scale: what stands between two blocks of a decoder layer in one pass.
+ * For every token, with z the block's output and r the residual stream:
+ *   n = z / rms(z) * (post_w + offset)     (post_w NULL: n = z)
+ *   h = r + scale * gate * n               (z NULL: h = r; residual NULL: r = 0)
+ *   y = h / rms(h) * (pre_w + offset)      rms(v) = sqrt(mean(v^2) + eps)
+ * The norm reads h before its rounding to the stream's type: h and y are rounded
+ * once each. Sums, with the squares, are fp32. The backward pass gives the
+ * gradients of z, r, both weights and the gate; sums over tokens are fp32 in an
+ * order that depends on the sizes alone: the same call gives the same bytes.
+ */
+/* What the gate has: nothing, a value a channel [K], a token [M] or an element [M, K]. */
+typedef enum { QMLP_GATE_NONE = 0, QMLP_GATE_CHANNEL = 1, QMLP_GATE_TOKEN = 2, QMLP_GATE_FULL = 3 } qmlp_gate;
+
+typedef struct {
+    int K;               /* 1 .. 16384                                              */
+    float eps;
+    float weight_offset; /* added to both weights (1 for weights kept about zero)   */
+    float scale;         /* of the block's output                                   */
+    qmlp_dtype dt;       /* z, out, gate a token / element, their gradients: BF16, FP16 */
+    qmlp_dtype rdt;      /* the residual stream and its gradients: dt or FP32        */
+    qmlp_dtype wdt;      /* weights, gate a channel, their gradients: dt or FP32     */
+    qmlp_gate gate;
+} qmlp_norm_desc;
+
+/* Device arrays, row-major and contiguous, of any alignment of their elements
+ * (stats: 8 bytes). Where K is a multiple of 8 and all are 16-byte aligned, rows
+ * are read 16 bytes at a time. */
+typedef struct {
+    const void* z;        /* [M, K], or NULL: no block, only the norm before         */
+    const void* residual; /* [M, K], or NULL                                         */
+    const void* post_w;   /* [K], or NULL: no norm after the block                   */
+    const void* pre_w;    /* [K], or NULL: no norm before the next one (no out)      */
+    const void* gate;     /* as the handle's gate; NULL without one or without z     */
+    void* residual_out;   /* h [M, K], or NULL; may be residual itself               */
+    void* out;            /* y [M, K], exactly where pre_w is                        */
+    float* stats;         /* [M][2]: 1/rms of z and h, for the backward pass, or NULL */
+} qmlp_norm_io;
+
+/* Gradients: of y (exactly where pre_w is) and of h behind (NULL: zero), read; the
+ * others written, NULL where not wanted. dresidual may be dresidual_out itself. */
+typedef struct {
+    const void* dout;
+    const void* dresidual_out;
+    void* dz;
+    void* dresidual;
+    void* dpost_w;
+    void* dpre_w;
+    void* dgate;
+} qmlp_norm_grads;
+
+typedef struct qmlp_norm_s qmlp_norm_t;
+
+/* Make a handle (it holds 24 K bytes an SM for the backward pass's column sums).
+ * Errors: INVALID_ARG (null, types, a value that is not finite), SHAPE,
+ * UNSUPPORTED_ARCH, OOM, CUDA. */
+qmlp_status qmlp_norm_create(qmlp_norm_t** out, const qmlp_norm_desc* desc, qmlp_stream_t stream);
+void qmlp_norm_destroy(qmlp_norm_t* h);
+
+/* Forward on M tokens. Allocates nothing; can be captured in a CUDA graph.
+ * Errors: INVALID_ARG (nothing to norm, post_w without z, a gate where the handle
+ * has none or none where it has one, out without pre_w or the reverse), SHAPE
+ * (M < 1), ALIGNMENT, ALIAS (an output overlaps another array), CUDA. */
+qmlp_status qmlp_norm_forward(qmlp_norm_t* h, const qmlp_norm_io* io, int M, qmlp_stream_t stream);
+
+/* Backward: io as the forward's, with the stats that it wrote (residual_out and
+ * out are not read). Errors: as the forward; INVALID_ARG also for no stats, no
+ * gradient to start from, or a gradient of what io lacks. */
+qmlp_status qmlp_norm_backward(qmlp_norm_t* h, const qmlp_norm_io* io, const qmlp_norm_grads* grads, int M,
+                               qmlp_stream_t stream);
 
 /* Human-readable name of a status ("QMLP_OK", ...). Never NULL. */
 const char* qmlp_status_str(qmlp_status s);

@@ -31,6 +31,7 @@ FMT_NVFP4, FMT_FP8_PC = 1, 2
 DT_BF16, DT_FP16, DT_FP32 = 1, 2, 3
 STATE_FP32, STATE_8BIT = 1, 2
 META_3B, META_4B = 3, 4
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 PATH_AUTO, PATH_GEMV, PATH_GEMM, PATH_GEMM_PAIR, PATH_GEMM_DQ = 0, 1, 2, 3, 4
 
 
@@ -72,6 +73,22 @@ class qmlp_adamw_hyper(ctypes.Structure):
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("grad_scale", ctypes.c_double),
                 ("step", ctypes.c_int64)]
+
+
+class qmlp_norm_desc(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int), ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+                ("scale", ctypes.c_float), ("dt", ctypes.c_int), ("rdt", ctypes.c_int), ("wdt", ctypes.c_int),
+                ("gate", ctypes.c_int)]
+
+
+class qmlp_norm_io(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("z", "residual", "post_w", "pre_w", "gate", "residual_out", "out",
+                                               "stats")]
+
+
+class qmlp_norm_grads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dout", "dresidual_out", "dz", "dresidual", "dpost_w", "dpre_w",
+                                               "dgate")]
 
 
 _lock = threading.Lock()
@@ -120,6 +137,10 @@ _SIGS = {
     "qmlp_adamw_create": ([ctypes.POINTER(_VP), ctypes.POINTER(qmlp_adamw_tensor), _I, _I, _I, _I, _VP], _I),
     "qmlp_adamw_destroy": ([_VP], None),
     "qmlp_adamw_step": ([_VP, ctypes.POINTER(qmlp_adamw_hyper), _VP], _I),
+    "qmlp_norm_create": ([ctypes.POINTER(_VP), ctypes.POINTER(qmlp_norm_desc), _VP], _I),
+    "qmlp_norm_destroy": ([_VP], None),
+    "qmlp_norm_forward": ([_VP, ctypes.POINTER(qmlp_norm_io), _I, _VP], _I),
+    "qmlp_norm_backward": ([_VP, ctypes.POINTER(qmlp_norm_io), ctypes.POINTER(qmlp_norm_grads), _I, _VP], _I),
     "qmlp_status_str": ([_I], ctypes.c_char_p),
     "qmlp_abi_version": ([], _I),
 }
@@ -381,6 +402,25 @@ def qmlp_adamw_destroy(h: int):
 
 def qmlp_adamw_step(h, hyper: qmlp_adamw_hyper, stream=None) -> int:
     return lib().qmlp_adamw_step(h, ctypes.byref(hyper), _stream(stream))
+
+
+def qmlp_norm_create(desc: qmlp_norm_desc, stream=None) -> int:
+    h = ctypes.c_void_p()
+    st = lib().qmlp_norm_create(ctypes.byref(h), ctypes.byref(desc), _stream(stream))
+    _chk(st, "qmlp_norm_create")
+    return h.value
+
+
+def qmlp_norm_destroy(h: int):
+    lib().qmlp_norm_destroy(h)
+
+
+def qmlp_norm_forward(h, io: qmlp_norm_io, M, stream=None) -> int:
+    return lib().qmlp_norm_forward(h, ctypes.byref(io), M, _stream(stream))
+
+
+def qmlp_norm_backward(h, io: qmlp_norm_io, grads: qmlp_norm_grads, M, stream=None) -> int:
+    return lib().qmlp_norm_backward(h, ctypes.byref(io), ctypes.byref(grads), M, _stream(stream))
 
 
 # ---- convenience handles ------------------------------------------------------
@@ -731,6 +771,103 @@ class AdamW:
     def close(self):
         if getattr(self, "h", None):
             qmlp_adamw_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _dtypes():
+    import torch
+    return {torch.bfloat16: DT_BF16, torch.float16: DT_FP16, torch.float32: DT_FP32}
+
+
+def _typed(who, name, t, dtype, shape):
+    """Refuse what is not a contiguous CUDA tensor of this type and shape, or of
+    the shape's elements in its order (raw addresses are the caller's)."""
+    if t is None or isinstance(t, int):
+        return
+    n = 1
+    for s in shape:
+        n *= s
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.numel() != n or t.shape[-1] != shape[-1]:
+        raise ValueError(f"{who}: {name} has to be a contiguous CUDA tensor of {dtype}, {tuple(shape)}")
+
+
+class BlockNorm:
+    """The norms before and after a block with its gate, residual and residual
+    scale (qmlp_norm_*):
+
+        n = z / rms(z) * (post_w + weight_offset);  h = residual + scale * gate * n
+        y = h / rms(h) * (pre_w + weight_offset)
+
+    dtype: bf16 or fp16 (z, out, a gate a token or an element); residual_dtype and
+    weight_dtype (weights, a gate a channel): dtype or fp32. gate: "none",
+    "channel" [K], "token" [M] or "full" [M, K]. Gradients have the types of what
+    they are gradients of. One object serves one stream at a time."""
+
+    def __init__(self, K, eps=1e-6, weight_offset=0.0, scale=1.0, dtype=None, residual_dtype=None, weight_dtype=None,
+                 gate="none", stream=None):
+        import torch
+        kinds, gates = _dtypes(), {"none": GATE_NONE, "channel": GATE_CHANNEL, "token": GATE_TOKEN, "full": GATE_FULL}
+        self.K, self.gate = K, gate
+        self.dt = torch.bfloat16 if dtype is None else dtype
+        self.rdt, self.wdt = residual_dtype or self.dt, weight_dtype or self.dt
+        if gate not in gates or any(t not in kinds for t in (self.dt, self.rdt, self.wdt)):
+            raise ValueError("BlockNorm: types are bf16, fp16 or fp32, gate is none, channel, token or full")
+        self.h = qmlp_norm_create(qmlp_norm_desc(K, eps, weight_offset, scale, kinds[self.dt], kinds[self.rdt],
+                                                 kinds[self.wdt], gates[gate]), stream)
+
+    def _check(self, M, **tensors):
+        rows, cols = (self.dt, (M, self.K)), (self.wdt, (self.K,))
+        gate = {"none": rows, "channel": cols, "token": (self.dt, (M,)), "full": rows}[self.gate]
+        kinds = {"z": rows, "residual": (self.rdt, (M, self.K)), "post_w": cols, "pre_w": cols, "gate": gate,
+                 "residual_out": (self.rdt, (M, self.K)), "out": rows, "dout": rows}
+        for n, t in tensors.items():
+            if n == "stats":
+                import torch
+                _typed("BlockNorm", n, t, torch.float32, (M, 2))
+            else:
+                dtype, shape = kinds[n] if n in kinds else kinds[n[1:]]
+                _typed("BlockNorm", n, t, dtype, shape)
+
+    def _rows(self, z, residual):
+        t = z if z is not None else residual
+        if t is None or isinstance(t, int):
+            raise ValueError("BlockNorm: M is wanted where neither z nor residual is a tensor")
+        return t.numel() // self.K
+
+    def forward(self, z=None, residual=None, post_w=None, pre_w=None, gate=None, residual_out=None, out=None,
+                stats=None, M=None, stream=None):
+        """Writes residual_out (h) and out (y); stats [M, 2] fp32 keeps what
+        backward needs. Returns (residual_out, out)."""
+        M = self._rows(z, residual) if M is None else M
+        t = dict(z=z, residual=residual, post_w=post_w, pre_w=pre_w, gate=gate, residual_out=residual_out, out=out,
+                 stats=stats)
+        self._check(M, **t)
+        _chk(qmlp_norm_forward(self.h, qmlp_norm_io(*[_ptr(a) for a in t.values()]), M, stream), "qmlp_norm_forward")
+        return residual_out, out
+
+    def backward(self, stats, z=None, residual=None, post_w=None, pre_w=None, gate=None, dout=None,
+                 dresidual_out=None, dz=None, dresidual=None, dpost_w=None, dpre_w=None, dgate=None, M=None,
+                 stream=None):
+        """From dout (y's gradient) and dresidual_out (h's, None: zero) the
+        gradients that are given: dz, dresidual, dpost_w, dpre_w, dgate."""
+        M = self._rows(z, residual) if M is None else M
+        t = dict(z=z, residual=residual, post_w=post_w, pre_w=pre_w, gate=gate, residual_out=None, out=None,
+                 stats=stats)
+        g = dict(dout=dout, dresidual_out=dresidual_out, dz=dz, dresidual=dresidual, dpost_w=dpost_w, dpre_w=dpre_w,
+                 dgate=dgate)
+        self._check(M, **t, **g)
+        _chk(qmlp_norm_backward(self.h, qmlp_norm_io(*[_ptr(a) for a in t.values()]),
+                                qmlp_norm_grads(*[_ptr(a) for a in g.values()]), M, stream), "qmlp_norm_backward")
+
+    def close(self):
+        if getattr(self, "h", None):
+            qmlp_norm_destroy(self.h)
             self.h = None
 
     def __del__(self):

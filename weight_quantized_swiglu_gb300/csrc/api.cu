@@ -31,21 +31,6 @@ static void release_handle(qmlp_s* h) {
     delete h;
 }
 
-struct qmlp_moe_s {
-    int E = 0, K = 0, I = 0, meta = 0, device = 0, num_sms = 0;
-    uint8_t *w13 = nullptr, *w13_meta = nullptr, *w2 = nullptr, *w2_meta = nullptr;
-    __half* act_ws = nullptr;
-    int* err = nullptr;
-    // multi-token workspace (qmlp_moe_reserve): routes = max_tokens * 16
-    int max_tokens = 1;
-    __half* g_act = nullptr;   // [routes, I]
-    __half* g_y = nullptr;     // [routes, K]
-    int* g_route = nullptr;    // [routes]
-    int4* g_groups = nullptr;  // [moe_grouped_max_groups(routes, E)]
-    int* g_ngroups = nullptr;
-    Owner mem;
-};
-
 extern "C" {
 
 const char* qmlp_status_str(qmlp_status s) {
@@ -762,7 +747,7 @@ qmlp_status qmlp_debug_bounds(int* site, unsigned long long* index) {
                                                           bounds_take_gemv_stream, bounds_take_gemv_dec,
                                                           bounds_take_moe_awq, bounds_take_moe_grouped,
                                                           bounds_take_tp_shard, bounds_take_lowrank,
-                                                          bounds_take_adamw};
+                                                          bounds_take_adamw,      bounds_take_norm};
     unsigned long long first = 0;
     for (auto take : units) {
         unsigned long long v = 0;

@@ -106,34 +106,6 @@ __global__ void __launch_bounds__(256) factors_kernel(const float* g, const floa
     row[i] = big ? 1.0f : f;
 }
 
-// No C++ exception leaves a C entry: what the host cannot allocate is OOM.
-template <typename F>
-qmlp_status guarded(F&& f) {
-    try {
-        return f();
-    } catch (...) {
-        return QMLP_ERR_OOM;
-    }
-}
-
-bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// Whether a written range overlaps any other one (ranges sorted in place).
-struct Range {
-    uintptr_t at, end;
-    bool written;
-};
-bool any_alias(std::vector<Range>& r) {
-    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.at < b.at; });
-    uintptr_t end = 0, wend = 0;  // the farthest end of any earlier range, and of any written one
-    for (const Range& x : r) {
-        if (x.at < wend || (x.written && x.at < end)) return true;
-        end = std::max(end, x.end);
-        if (x.written) wend = std::max(wend, x.end);
-    }
-    return false;
-}
-
 // Where a call keeps c z A^T (or c dy B) of every token: bf16 words side by
 // side in rows of ld, nc columns a word. As further steps of a GEMM: T words
 // (the third again the first) and zeros up to a multiple of 64, with the parts'

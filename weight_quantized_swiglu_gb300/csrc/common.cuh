@@ -183,7 +183,7 @@ QMLP_DEV void mbar_arrive(uint32_t bar) {
 // No check traps. The host reads and clears the words (qmlp_debug_bounds).
 // Sites are numbered per file (gemv_split 1-9, gemm_tc 11-19, gemv_stream and
 // gemv_dec 21-29, moe_awq 31-39, moe_grouped 41-49, tp_shard 51-59, lowrank
-// 61-69, adamw 71-79).
+// 61-69, adamw 71-79, norm 81-89, linear 91-99, moe_layer 101-109).
 // ---------------------------------------------------------------------------
 #ifdef QMLP_DEBUG_BOUNDS
 static __device__ unsigned long long g_bounds_word;

@@ -60,6 +60,34 @@ struct Owner {
     }
 };
 
+// No C++ exception leaves a C entry: what the host cannot allocate is OOM.
+template <typename F>
+qmlp_status guarded(F&& f) {
+    try {
+        return f();
+    } catch (...) {
+        return QMLP_ERR_OOM;
+    }
+}
+
+inline bool aligned(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Whether a written range overlaps any other one (ranges sorted in place).
+struct Range {
+    uintptr_t at, end;
+    bool written;
+};
+inline bool any_alias(std::vector<Range>& r) {
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.at < b.at; });
+    uintptr_t end = 0, wend = 0;  // the farthest end of any earlier range, and of any written one
+    for (const Range& x : r) {
+        if (x.at < wend || (x.written && x.at < end)) return true;
+        end = std::max(end, x.end);
+        if (x.written) wend = std::max(wend, x.end);
+    }
+    return false;
+}
+
 inline qmlp_status check_device(int* dev, int* num_sms) {
     cudaError_t e = cudaGetDevice(dev);
     if (e != cudaSuccess) return QMLP_ERR_CUDA;
@@ -73,6 +101,21 @@ inline qmlp_status check_device(int* dev, int* num_sms) {
 }
 
 }  // namespace qmlp
+
+struct qmlp_moe_s {
+    int E = 0, K = 0, I = 0, meta = 0, device = 0, num_sms = 0;
+    uint8_t *w13 = nullptr, *w13_meta = nullptr, *w2 = nullptr, *w2_meta = nullptr;
+    __half* act_ws = nullptr;
+    int* err = nullptr;
+    // multi-token workspace (qmlp_moe_reserve): routes = max_tokens * 16
+    int max_tokens = 1;
+    __half* g_act = nullptr;   // [routes, I]
+    __half* g_y = nullptr;     // [routes, K]
+    int* g_route = nullptr;    // [routes]
+    int4* g_groups = nullptr;  // [moe_grouped_max_groups(routes, E)]
+    int* g_ngroups = nullptr;
+    qmlp::Owner mem;
+};
 
 struct qmlp_s {
     int fmt = 0, K = 0, I = 0, max_M = 0, device = 0, num_sms = 0;

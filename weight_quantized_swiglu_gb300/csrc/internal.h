@@ -340,6 +340,30 @@ struct AdamWStep {  // the constants of a step, fp32 of fp64 values
 cudaError_t launch_adamw(const AdamWChunk* chunks, long count, bool param_bf16, bool master, bool grad_bf16, bool s8,
                          const AdamWStep& k, int num_sms, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// Norms before and after a block (norm.cu)
+// ---------------------------------------------------------------------------
+enum NormGate { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
+constexpr int kNormMaxK = 16384;
+struct NormArgs {
+    long M = 0;
+    int K = 0;
+    float eps = 0, rK = 0, offset = 0, scale = 1;  // rK: 1 / K
+    int gate_kind = kGateNone;
+    bool w_f32 = false;        // weights (and a channel gate) are fp32, else of z's type
+    bool vec = false;          // K % 8 == 0 and every pointer aligned for 8 elements at a time
+    const void *z = nullptr, *r = nullptr, *post_w = nullptr, *pre_w = nullptr, *gate = nullptr;
+    void *h = nullptr, *y = nullptr;
+    float2* stats = nullptr;   // [M] 1/rms of z and h
+    // backward
+    const void *dy = nullptr, *dh = nullptr;
+    void *dz = nullptr, *dr = nullptr, *dpost = nullptr, *dpre = nullptr, *dgate = nullptr;
+    float* part = nullptr;     // [shares][3][K]: the CTAs' column sums (null: none is wanted)
+    int shares = 0;
+    size_t elems = 0, part_elems = 0;  // index checks: M K; floats of part
+};
+cudaError_t launch_norm(const NormArgs& a, bool t_f16, bool r_f32, bool backward, cudaStream_t s);
+
 // Index checks of a QMLP_DEBUG_BOUNDS build (common.cuh): each translation
 // unit's first failed check, (site << 48) | index, or 0; reading clears it.
 // The default build returns 0.
@@ -352,5 +376,6 @@ cudaError_t bounds_take_moe_grouped(unsigned long long* v);
 cudaError_t bounds_take_tp_shard(unsigned long long* v);
 cudaError_t bounds_take_lowrank(unsigned long long* v);
 cudaError_t bounds_take_adamw(unsigned long long* v);
+cudaError_t bounds_take_norm(unsigned long long* v);
 
 }  // namespace qmlp
