@@ -238,7 +238,8 @@ int qmlp_debug_bounds_enabled(void);
  * (per source file: 1-9 decode kernel, 11-19 tensor-core GEMM, 21-29 stream-K
  * and split-K decode kernels, 31-39 one-token routed experts, 41-49 grouped
  * routed experts, 51-59 tensor-parallel combine, 61-69 low-rank products,
- * 71-79 AdamW, 81-89 norms) and *index = the checked
+ * 71-79 AdamW, 81-89 norms, 91-99 linear,
+ * 101-109 mixture-of-experts layer) and *index = the checked
  * index (low 48 bits), or 0 and 0. Returns OK, DEVICE_BOUNDS (a check
  * failed), INVALID_ARG (a NULL pointer) or CUDA. A default build always
  * reports OK. */
@@ -640,6 +641,105 @@ qmlp_status qmlp_norm_forward(qmlp_norm_t* h, const qmlp_norm_io* io, int M, qml
  * gradient to start from, or a gradient of what io lacks. */
 qmlp_status qmlp_norm_backward(qmlp_norm_t* h, const qmlp_norm_io* io, const qmlp_norm_grads* grads, int M,
                                qmlp_stream_t stream);
+
+/*
+ * One projection with 4-bit weights and group scales, for the projections beside
+ * the MLP (attention's, an output head's):
+ *   y[m, n] = c sum_k x[m, k] W[n, k] + bias[n]
+ *   NVFP4: W[n, k] = E2M1(code) E4M3(scale[n, k / 16]), c = fp32(1 / global_scale)
+ *   INT4:  W[n, k] = (code - zero[n, k / group]) scale[n, k / group], c = 1
+ * Sums are fp32 and y is rounded once, to the type of the output.
+ */
+typedef enum { QMLP_LINEAR_NVFP4 = 1, QMLP_LINEAR_INT4 = 2 } qmlp_linear_format;
+
+/* Arrays in host or device memory, read only by qmlp_linear_create, in the
+ * checkpoint's order: two codes a byte, the low nibble the even k. */
+typedef struct {
+    qmlp_linear_format fmt;
+    int N;                /* outputs, 1 .. 2^20                                    */
+    int K;                /* inputs, a multiple of 16 and of group, 16 .. 65536    */
+    int max_M;            /* most tokens of a call, 1 .. 65536                     */
+    int group;            /* INT4: 32, 64 or 128; NVFP4: 16                        */
+    const uint8_t* w;     /* u8 [N, K/2]                                           */
+    const void* scale;    /* NVFP4: E4M3 [N, K/16]; INT4: fp16 [N, K/group]        */
+    const uint8_t* zero;  /* INT4: u8 [N, K/group]; NVFP4: NULL                    */
+    float global_scale;   /* NVFP4                                                 */
+    const float* bias;    /* fp32 [N], or NULL                                     */
+} qmlp_linear_desc;
+
+typedef struct qmlp_linear_s qmlp_linear_t;
+
+/* Make a handle: copies the weights into memory of its own, reordered for the
+ * kernels (packed as they are), and makes the workspace of calls of up to max_M
+ * tokens. Synchronizes `stream`.
+ * Errors: INVALID_ARG, SHAPE, UNSUPPORTED_ARCH, OOM, CUDA. */
+qmlp_status qmlp_linear_create(qmlp_linear_t** out, const qmlp_linear_desc* desc, qmlp_stream_t stream);
+void qmlp_linear_destroy(qmlp_linear_t* h);
+
+/* y = x W^T + bias on M tokens.
+ *  x   = device [M, K], bf16 or fp16 per xdt
+ *  out = device [M, N], bf16, fp16 or fp32 per odt
+ * Allocates nothing; can be captured in a CUDA graph. The same call gives the same
+ * bytes. One handle serves one stream at a time.
+ * Errors: INVALID_ARG, ALIGNMENT (16 bytes), ALIAS, SHAPE (M < 1 or over max_M),
+ * CUDA. */
+qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt, int M, void* out, qmlp_dtype odt,
+                                qmlp_stream_t stream);
+
+/*
+ * A whole mixture-of-experts layer over the banks of a routed-expert handle: router,
+ * selection, routed and shared experts, weighted sum. For every token x, with E
+ * routed experts and the last `shared` of the handle's experts shared ones:
+ *   l[e] = router[e] . x;   p = softmax(l) or sigmoid(l)
+ *   the topk experts with the largest p[e] (+ bias[e]) are selected, ties to the
+ *   lowest e (a NaN ranks below every number);
+ *   w[e] = route_scale p[e], over the sum of the selected p where renorm is set
+ *   a shared expert's w is 1, or sigmoid(shared_gate . x)
+ *   out = sum of w[e] W2[e] (SiLU(g) u),  g, u = the halves of W13[e] x
+ * (a shared expert of n times the width is n shared experts of the handle's I).
+ * Up to 16 tokens whose x fits in shared memory (2 K bytes a token) run as one
+ * kernel: sums are fp32, the intermediate is rounded once to fp16 times a power of
+ * two of the token and expert, out once. More tokens run the router, the selection
+ * and the kernels of qmlp_moe_forward, with its roundings of the stages to fp16.
+ */
+typedef enum { QMLP_SCORE_SOFTMAX = 1, QMLP_SCORE_SIGMOID = 2 } qmlp_score;
+
+typedef struct {
+    const void* router;      /* [E, K], host or device, copied; E = the handle's E - shared */
+    qmlp_dtype rdt;          /* type of router and shared_gate: BF16, FP16 or FP32          */
+    const float* bias;       /* fp32 [E] that selection (not w) adds to p, or NULL          */
+    const void* shared_gate; /* [shared, K], or NULL: w = 1                                 */
+    int shared;              /* >= 0                                                        */
+    int topk;                /* 1 .. E; topk + shared <= 16                                 */
+    qmlp_score score;
+    int renorm;
+    float route_scale;
+    int max_tokens;          /* of a call                                                   */
+} qmlp_moe_layer_desc;
+
+typedef struct qmlp_moe_layer_s qmlp_moe_layer_t;
+
+/* Make a layer over the handle's banks (which must outlive it and whose workspace
+ * for more than 16 tokens it shares: calls on both go on one stream at a time).
+ * Reserves max_tokens on the handle (qmlp_moe_reserve and its limits), copies the
+ * router. E <= 1024. Synchronizes `stream`.
+ * Errors: INVALID_ARG, SHAPE, OOM, CUDA. */
+qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const qmlp_moe_layer_desc* desc,
+                                  qmlp_stream_t stream);
+void qmlp_moe_layer_destroy(qmlp_moe_layer_t* h);
+
+/* The layer on M tokens.
+ *  x   = device [M, K], bf16 or fp16 per xdt;  out = device [M, K] of type odt
+ *  ids, weights = device int32 / fp32 [M, topk]: the selected experts, largest
+ *        first, and their w; either may be NULL
+ * Allocates nothing; can be captured in a CUDA graph. The same call gives the same
+ * bytes. The one-kernel form is a cooperative launch with a CTA an SM: it starts
+ * when the whole GPU has room, and its grid barriers wait 2 s at most (then out is
+ * not valid and qmlp_moe_layer_check returns QMLP_ERR_DEVICE_TIMEOUT).
+ * Errors: INVALID_ARG, ALIGNMENT (16 bytes; ids and weights 4), ALIAS, SHAPE, CUDA. */
+qmlp_status qmlp_moe_layer_forward(qmlp_moe_layer_t* h, const void* x, qmlp_dtype xdt, int M, void* out, qmlp_dtype odt,
+                                   int32_t* ids, float* weights, qmlp_stream_t stream);
+qmlp_status qmlp_moe_layer_check(qmlp_moe_layer_t* h, qmlp_stream_t stream);
 
 /* Human-readable name of a status ("QMLP_OK", ...). Never NULL. */
 const char* qmlp_status_str(qmlp_status s);

@@ -31,6 +31,8 @@ FMT_NVFP4, FMT_FP8_PC = 1, 2
 DT_BF16, DT_FP16, DT_FP32 = 1, 2, 3
 STATE_FP32, STATE_8BIT = 1, 2
 META_3B, META_4B = 3, 4
+SCORE_SOFTMAX, SCORE_SIGMOID = 1, 2
+LINEAR_NVFP4, LINEAR_INT4 = 1, 2
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 PATH_AUTO, PATH_GEMV, PATH_GEMM, PATH_GEMM_PAIR, PATH_GEMM_DQ = 0, 1, 2, 3, 4
 
@@ -91,6 +93,19 @@ class qmlp_norm_grads(ctypes.Structure):
                                                "dgate")]
 
 
+class qmlp_linear_desc(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int), ("N", ctypes.c_int), ("K", ctypes.c_int), ("max_M", ctypes.c_int),
+                ("group", ctypes.c_int), ("w", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("global_scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
+class qmlp_moe_layer_desc(ctypes.Structure):
+    _fields_ = [("router", ctypes.c_void_p), ("rdt", ctypes.c_int), ("bias", ctypes.c_void_p),
+                ("shared_gate", ctypes.c_void_p), ("shared", ctypes.c_int), ("topk", ctypes.c_int),
+                ("score", ctypes.c_int), ("renorm", ctypes.c_int), ("route_scale", ctypes.c_float),
+                ("max_tokens", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -141,6 +156,13 @@ _SIGS = {
     "qmlp_norm_destroy": ([_VP], None),
     "qmlp_norm_forward": ([_VP, ctypes.POINTER(qmlp_norm_io), _I, _VP], _I),
     "qmlp_norm_backward": ([_VP, ctypes.POINTER(qmlp_norm_io), ctypes.POINTER(qmlp_norm_grads), _I, _VP], _I),
+    "qmlp_linear_create": ([ctypes.POINTER(_VP), ctypes.POINTER(qmlp_linear_desc), _VP], _I),
+    "qmlp_linear_destroy": ([_VP], None),
+    "qmlp_linear_forward": ([_VP, _VP, _I, _I, _VP, _I, _VP], _I),
+    "qmlp_moe_layer_create": ([ctypes.POINTER(_VP), _VP, ctypes.POINTER(qmlp_moe_layer_desc), _VP], _I),
+    "qmlp_moe_layer_destroy": ([_VP], None),
+    "qmlp_moe_layer_forward": ([_VP, _VP, _I, _I, _VP, _I, _VP, _VP, _VP], _I),
+    "qmlp_moe_layer_check": ([_VP, _VP], _I),
     "qmlp_status_str": ([_I], ctypes.c_char_p),
     "qmlp_abi_version": ([], _I),
 }
@@ -421,6 +443,40 @@ def qmlp_norm_forward(h, io: qmlp_norm_io, M, stream=None) -> int:
 
 def qmlp_norm_backward(h, io: qmlp_norm_io, grads: qmlp_norm_grads, M, stream=None) -> int:
     return lib().qmlp_norm_backward(h, ctypes.byref(io), ctypes.byref(grads), M, _stream(stream))
+
+
+def qmlp_linear_create(desc: qmlp_linear_desc, stream=None) -> int:
+    h = ctypes.c_void_p()
+    st = lib().qmlp_linear_create(ctypes.byref(h), ctypes.byref(desc), _stream(stream))
+    _chk(st, "qmlp_linear_create")
+    return h.value
+
+
+def qmlp_linear_destroy(h: int):
+    lib().qmlp_linear_destroy(h)
+
+
+def qmlp_linear_forward(h, x, xdt, M, out, odt, stream=None) -> int:
+    return lib().qmlp_linear_forward(h, _ptr(x), xdt, M, _ptr(out), odt, _stream(stream))
+
+
+def qmlp_moe_layer_create(moe, desc: qmlp_moe_layer_desc, stream=None) -> int:
+    h = ctypes.c_void_p()
+    st = lib().qmlp_moe_layer_create(ctypes.byref(h), moe, ctypes.byref(desc), _stream(stream))
+    _chk(st, "qmlp_moe_layer_create")
+    return h.value
+
+
+def qmlp_moe_layer_destroy(h: int):
+    lib().qmlp_moe_layer_destroy(h)
+
+
+def qmlp_moe_layer_forward(h, x, xdt, M, out, odt, ids=None, weights=None, stream=None) -> int:
+    return lib().qmlp_moe_layer_forward(h, _ptr(x), xdt, M, _ptr(out), odt, _ptr(ids), _ptr(weights), _stream(stream))
+
+
+def qmlp_moe_layer_check(h, stream=None) -> int:
+    return lib().qmlp_moe_layer_check(h, _stream(stream))
 
 
 # ---- convenience handles ------------------------------------------------------
@@ -868,6 +924,125 @@ class BlockNorm:
     def close(self):
         if getattr(self, "h", None):
             qmlp_norm_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class QuantLinear:
+    """One projection y = x W^T + bias with 4-bit weights and group scales
+    (qmlp_linear_*): "nvfp4" (w u8 [N, K/2], scale E4M3 [N, K/16], global_scale) or
+    "int4" (w, scale fp16 [N, K/group], zero u8 [N, K/group]; group 32, 64 or 128).
+    The low nibble of a byte is the even k. bias: fp32 [N] or None. Arrays may be
+    numpy arrays (host) or torch CUDA tensors; they are copied at construction."""
+
+    def __init__(self, fmt, N, K, max_M, w, scale, zero=None, group=None, global_scale=1.0, bias=None, stream=None):
+        if fmt not in ("nvfp4", "int4"):
+            raise ValueError("QuantLinear: fmt is nvfp4 or int4")
+        group = (16 if fmt == "nvfp4" else 128) if group is None else group
+        self.N, self.K, self.max_M = N, K, max_M
+        cells = N * (K // group) if group > 0 else 0
+        want = {"w": (w, N * (K // 2)), "scale": (scale, cells * (1 if fmt == "nvfp4" else 2)), "zero": (zero, cells),
+                "bias": (bias, 4 * N)}
+        keep, ptr = [], {}
+        for n, (a, nbytes) in want.items():
+            ptr[n] = None
+            if a is None:
+                continue
+            if isinstance(a, int):
+                ptr[n] = a
+                continue
+            size = a.nbytes if isinstance(a, np.ndarray) else a.numel() * a.element_size()
+            if size != nbytes or (not isinstance(a, np.ndarray) and not a.is_contiguous()):
+                raise ValueError(f"QuantLinear: {n} has to be contiguous, of {nbytes} bytes")
+            ptr[n], owner = _host_or_dev(a)
+            keep.append(owner)
+        self.h = qmlp_linear_create(
+            qmlp_linear_desc(LINEAR_NVFP4 if fmt == "nvfp4" else LINEAR_INT4, N, K, max_M, group, ptr["w"],
+                             ptr["scale"], ptr["zero"], float(global_scale), ptr["bias"]), stream)
+        self._forward, self._kinds = lib().qmlp_linear_forward, _dtypes()
+
+    def forward(self, x, out, M=None, stream=None):
+        """x [M, K] bf16 or fp16, out [M, N] bf16, fp16 or fp32."""
+        M = x.numel() // self.K if M is None else M
+        if (not x.is_cuda or not out.is_cuda or not x.is_contiguous() or not out.is_contiguous() or
+                x.numel() < M * self.K or out.numel() < M * self.N or x.shape[-1] != self.K or
+                out.shape[-1] != self.N or self._kinds.get(x.dtype, DT_FP32) == DT_FP32 or
+                out.dtype not in self._kinds):
+            raise ValueError(f"QuantLinear: x has to be [{M}, {self.K}] and out [{M}, {self.N}], contiguous CUDA "
+                             f"tensors of bf16 or fp16 (out: or fp32)")
+        _chk(self._forward(self.h, x.data_ptr(), self._kinds[x.dtype], M, out.data_ptr(), self._kinds[out.dtype],
+                           _stream(stream)), "qmlp_linear_forward")
+        return out
+
+    def close(self):
+        if getattr(self, "h", None):
+            qmlp_linear_destroy(self.h)
+            self.h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class MoeLayer:
+    """A whole mixture-of-experts layer over a MoeAWQ's banks (qmlp_moe_layer_*):
+    router [E, K] (bf16, fp16 or fp32), softmax or sigmoid scores, topk experts by
+    score (+ bias, fp32 [E]), weights renormed over the selected ones and scaled; the
+    last `shared` of the MoeAWQ's experts are always used, with weight 1 or
+    sigmoid(shared_gate x) (shared_gate [shared, K], of the router's type). The
+    MoeAWQ has to stay open while this object is."""
+
+    def __init__(self, moe: MoeAWQ, router, topk, score="softmax", bias=None, renorm=True, route_scale=1.0, shared=0,
+                 shared_gate=None, max_tokens=1, stream=None):
+        import torch
+        self._kinds = _dtypes()
+        scores = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+        E, K = moe.E - shared, moe.K
+        if score not in scores or router.dtype not in self._kinds:
+            raise ValueError("MoeLayer: scores are softmax or sigmoid, the router bf16, fp16 or fp32")
+        for n, t, shape, dtype in (("router", router, (E, K), router.dtype), ("bias", bias, (E,), torch.float32),
+                                   ("shared_gate", shared_gate, (shared, K), router.dtype)):
+            if t is not None and (tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous()):
+                raise ValueError(f"MoeLayer: {n} has to be contiguous, {shape}, {dtype}")
+        self.moe, self.K, self.topk, self.max_tokens = moe, K, topk, max_tokens
+        self.h = qmlp_moe_layer_create(
+            moe.h, qmlp_moe_layer_desc(_ptr(router), self._kinds[router.dtype], _ptr(bias), _ptr(shared_gate), shared,
+                                       topk, scores[score], 1 if renorm else 0, route_scale, max_tokens), stream)
+        self._forward = lib().qmlp_moe_layer_forward
+
+    def forward(self, x, out, ids=None, weights=None, M=None, stream=None):
+        """x [M, K] bf16 or fp16, out [M, K] bf16, fp16 or fp32; ids (int32) and
+        weights (fp32) [M, topk] take the selected experts and their weights."""
+        M = x.numel() // self.K if M is None else M
+        if (not x.is_cuda or not out.is_cuda or not x.is_contiguous() or not out.is_contiguous() or
+                x.numel() < M * self.K or out.numel() < M * self.K or x.shape[-1] != self.K or
+                out.shape[-1] != self.K or self._kinds.get(x.dtype, DT_FP32) == DT_FP32 or
+                out.dtype not in self._kinds):
+            raise ValueError(f"MoeLayer: x and out have to be [{M}, {self.K}], contiguous CUDA tensors of bf16 or "
+                             f"fp16 (out: or fp32)")
+        for n, t, fp in (("ids", ids, False), ("weights", weights, True)):
+            if t is not None and (not t.is_cuda or not t.is_contiguous() or t.numel() < M * self.topk or
+                                  t.element_size() != 4 or t.is_floating_point() != fp):
+                raise ValueError(f"MoeLayer: {n} has to be a contiguous {'fp32' if fp else 'int32'} CUDA tensor of "
+                                 f"{M * self.topk} values")
+        _chk(self._forward(self.h, x.data_ptr(), self._kinds[x.dtype], M, out.data_ptr(), self._kinds[out.dtype],
+                           None if ids is None else ids.data_ptr(), None if weights is None else weights.data_ptr(),
+                           _stream(stream)), "qmlp_moe_layer_forward")
+        return out
+
+    def check(self, stream=None):
+        _chk(qmlp_moe_layer_check(self.h, stream), "qmlp_moe_layer_check")
+
+    def close(self):
+        if getattr(self, "h", None):
+            qmlp_moe_layer_destroy(self.h)
             self.h = None
 
     def __del__(self):

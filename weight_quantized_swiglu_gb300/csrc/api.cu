@@ -747,7 +747,8 @@ qmlp_status qmlp_debug_bounds(int* site, unsigned long long* index) {
                                                           bounds_take_gemv_stream, bounds_take_gemv_dec,
                                                           bounds_take_moe_awq, bounds_take_moe_grouped,
                                                           bounds_take_tp_shard, bounds_take_lowrank,
-                                                          bounds_take_adamw,      bounds_take_norm};
+                                                          bounds_take_adamw,      bounds_take_norm,
+                                                          bounds_take_linear,     bounds_take_moe_layer};
     unsigned long long first = 0;
     for (auto take : units) {
         unsigned long long v = 0;
@@ -991,17 +992,8 @@ qmlp_status qmlp_moe_reserve(qmlp_moe_t* h, int max_tokens, qmlp_stream_t stream
     return QMLP_OK;
 }
 
-qmlp_status qmlp_moe_forward(qmlp_moe_t* h, const void* x, qmlp_dtype xdt, const int32_t* ids, const float* rw,
-                             int topk, int M, void* out, qmlp_stream_t stream) {
-    if (!h || !x || !ids || !rw || !out) return QMLP_ERR_INVALID_ARG;
-    if (M < 1 || M > h->max_tokens) return QMLP_ERR_SHAPE;
-    if (M == 1) return moe_run(h, x, xdt, ids, rw, topk, out, nullptr, nullptr, nullptr, stream);
-    if (xdt != QMLP_DT_BF16 && xdt != QMLP_DT_FP16) return QMLP_ERR_INVALID_ARG;
-    if (topk < 1 || topk > 16) return QMLP_ERR_SHAPE;
-    if (!aligned16(x) || !aligned16(out) || !aligned16(ids) || !aligned16(rw)) return QMLP_ERR_ALIGNMENT;
-    const size_t xb = (size_t)M * h->K * 2, rb = (size_t)M * topk * 4;
-    if (overlaps(out, xb, x, xb) || overlaps(out, xb, ids, rb) || overlaps(out, xb, rw, rb)) return QMLP_ERR_ALIAS;
-    if (fault("launch")) return QMLP_ERR_CUDA;
+extern "C++" cudaError_t moe_grouped(qmlp_moe_s* h, const void* x, bool x_bf16, const int32_t* ids, const float* rw, int topk,
+                                     int M, void* out, int odt, cudaStream_t s) {
     MoeGroupedLaunch L;
     L.num_sms = h->num_sms;
     L.E = h->E;
@@ -1015,16 +1007,34 @@ qmlp_status qmlp_moe_forward(qmlp_moe_t* h, const void* x, qmlp_dtype xdt, const
     L.w2 = h->w2;
     L.w2_meta = h->w2_meta;
     L.x = x;
-    L.x_is_bf16 = xdt == QMLP_DT_BF16;
+    L.x_is_bf16 = x_bf16;
     L.ids = ids;
     L.rw = rw;
-    L.out = static_cast<__half*>(out);
+    L.out = out;
+    L.odt = odt;
     L.act_ws = h->g_act;
     L.y_ws = h->g_y;
     L.route_list = h->g_route;
     L.groups = h->g_groups;
     L.n_groups = h->g_ngroups;
-    return launch_moe_grouped(L, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? QMLP_OK : QMLP_ERR_CUDA;
+    return launch_moe_grouped(L, s);
+}
+
+qmlp_status qmlp_moe_forward(qmlp_moe_t* h, const void* x, qmlp_dtype xdt, const int32_t* ids, const float* rw,
+                             int topk, int M, void* out, qmlp_stream_t stream) {
+    if (!h || !x || !ids || !rw || !out) return QMLP_ERR_INVALID_ARG;
+    if (M < 1 || M > h->max_tokens) return QMLP_ERR_SHAPE;
+    if (M == 1) return moe_run(h, x, xdt, ids, rw, topk, out, nullptr, nullptr, nullptr, stream);
+    if (xdt != QMLP_DT_BF16 && xdt != QMLP_DT_FP16) return QMLP_ERR_INVALID_ARG;
+    if (topk < 1 || topk > 16) return QMLP_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(out) || !aligned16(ids) || !aligned16(rw)) return QMLP_ERR_ALIGNMENT;
+    const size_t xb = (size_t)M * h->K * 2, rb = (size_t)M * topk * 4;
+    if (overlaps(out, xb, x, xb) || overlaps(out, xb, ids, rb) || overlaps(out, xb, rw, rb)) return QMLP_ERR_ALIAS;
+    if (fault("launch")) return QMLP_ERR_CUDA;
+    return moe_grouped(h, x, xdt == QMLP_DT_BF16, ids, rw, topk, M, out, 2, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? QMLP_OK
+               : QMLP_ERR_CUDA;
 }
 
 qmlp_status qmlp_moe_check(qmlp_moe_t* h, qmlp_stream_t stream) {

@@ -1,5 +1,6 @@
 // api_layer.cu -- the C ABI of the operators around the quantized blocks of a
-// decoder layer (declared in include/qmlp.h): the norms before and after a block.
+// decoder layer (declared in include/qmlp.h): the norms before and after a block,
+// one projection with 4-bit weights, a whole mixture-of-experts layer.
 // Argument checks, ownership and dispatch only, as api.cu.
 #include <math.h>
 
@@ -15,9 +16,26 @@ struct qmlp_norm_s {
     Owner mem;
 };
 
+struct qmlp_linear_s {
+    int group = 16, N = 0, K = 0, max_M = 0, num_sms = 0;
+    uint8_t* w = nullptr;
+    size_t w_bytes = 0;
+    float factor = 1.0f;
+    float* bias = nullptr;
+    Owner mem;
+};
+
+struct qmlp_moe_layer_s {
+    qmlp_moe_t* moe = nullptr;
+    int max_tokens = 0;
+    MoeLayerArgs a;  // everything but the call's own
+    Owner mem;
+};
+
 namespace {
 
 size_t dt_bytes(qmlp_dtype t) { return t == QMLP_DT_FP32 ? 4 : 2; }
+int dt_code(qmlp_dtype t) { return t == QMLP_DT_FP32 ? 0 : t == QMLP_DT_BF16 ? 1 : 2; }
 bool half_type(qmlp_dtype t) { return t == QMLP_DT_BF16 || t == QMLP_DT_FP16; }
 // fp32 or the other 16-bit type
 bool same_or_fp32(qmlp_dtype t, qmlp_dtype of) { return t == of || t == QMLP_DT_FP32; }
@@ -201,6 +219,220 @@ qmlp_status qmlp_norm_backward(qmlp_norm_t* h, const qmlp_norm_io* io, const qml
         return from_cuda(launch_norm(a, d.dt == QMLP_DT_FP16, d.rdt == QMLP_DT_FP32, true,
                                      reinterpret_cast<cudaStream_t>(stream)));
     });
+}
+
+// ---------------------------------------------------------------------------
+// One projection with 4-bit weights and group scales
+// ---------------------------------------------------------------------------
+qmlp_status qmlp_linear_create(qmlp_linear_t** out, const qmlp_linear_desc* d, qmlp_stream_t stream) {
+    return guarded([&]() -> qmlp_status {
+        if (!out) return QMLP_ERR_INVALID_ARG;
+        *out = nullptr;
+        if (!d || !d->w || !d->scale || (d->fmt != QMLP_LINEAR_NVFP4 && d->fmt != QMLP_LINEAR_INT4))
+            return QMLP_ERR_INVALID_ARG;
+        const bool nv = d->fmt == QMLP_LINEAR_NVFP4;
+        if ((d->zero != nullptr) == nv || (nv ? d->group != 16 : d->group != 32 && d->group != 64 && d->group != 128))
+            return QMLP_ERR_INVALID_ARG;
+        if (d->N < 1 || d->N > (1 << 20) || d->K < 16 || d->K > 65536 || d->K % d->group || d->max_M < 1 ||
+            d->max_M > 65536)
+            return QMLP_ERR_SHAPE;
+        int dev = 0, sms = 0;
+        qmlp_status st = check_device(&dev, &sms);
+        if (st != QMLP_OK) return st;
+        qmlp_linear_t* h = new qmlp_linear_t();
+        Owner tmp;  // the checkpoint's arrays on the device, while they are reordered
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        h->group = d->group;
+        h->N = d->N;
+        h->K = d->K;
+        h->max_M = d->max_M;
+        h->num_sms = sms;
+        h->factor = nv ? (float)(1.0 / (double)d->global_scale) : 1.0f;
+        h->w_bytes = linear_bytes(d->group, d->N, d->K);
+        const size_t rows = (size_t)d->N, groups = rows * (d->K / d->group);
+        cudaError_t e = cudaSuccess;
+        auto stage = [&](const void* src, size_t bytes) -> void* {
+            void* p = nullptr;
+            if (src && e == cudaSuccess && (e = tmp.alloc(&p, bytes)) == cudaSuccess)
+                e = cudaMemcpyAsync(p, src, bytes, cudaMemcpyDefault, s);
+            return p;
+        };
+        const void* w = stage(d->w, rows * (d->K / 2));
+        const void* sc = stage(d->scale, groups * (nv ? 1 : 2));
+        const void* z = stage(d->zero, groups);
+        if (e == cudaSuccess) e = h->mem.alloc(reinterpret_cast<void**>(&h->w), h->w_bytes);
+        if (e == cudaSuccess && d->bias) {
+            e = h->mem.alloc(reinterpret_cast<void**>(&h->bias), rows * 4);
+            if (e == cudaSuccess) e = cudaMemcpyAsync(h->bias, d->bias, rows * 4, cudaMemcpyDefault, s);
+        }
+        if (e == cudaSuccess)
+            e = repack_linear(d->group, static_cast<const uint8_t*>(w), sc, static_cast<const uint8_t*>(z), d->N, d->K,
+                              h->w, s);
+        const cudaError_t e2 = cudaStreamSynchronize(s);
+        tmp.release();
+        if (e == cudaSuccess) e = e2;
+        if (e != cudaSuccess) {
+            h->mem.release();
+            delete h;
+            return from_cuda(e);
+        }
+        *out = h;
+        return QMLP_OK;
+    });
+}
+
+void qmlp_linear_destroy(qmlp_linear_t* h) {
+    if (!h) return;
+    cudaDeviceSynchronize();
+    h->mem.release();
+    delete h;
+}
+
+qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt, int M, void* out, qmlp_dtype odt,
+                                qmlp_stream_t stream) {
+    if (!h || !x || !out || !half_type(xdt) || (!half_type(odt) && odt != QMLP_DT_FP32)) return QMLP_ERR_INVALID_ARG;
+    if (M < 1 || M > h->max_M) return QMLP_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(out)) return QMLP_ERR_ALIGNMENT;
+    if (overlaps(out, (size_t)M * h->N * dt_bytes(odt), x, (size_t)M * h->K * 2)) return QMLP_ERR_ALIAS;
+    if (fault("launch")) return QMLP_ERR_CUDA;
+    LinearArgs a;
+    a.M = M;
+    a.N = h->N;
+    a.K = h->K;
+    a.w = h->w;
+    a.w_bytes = h->w_bytes;
+    a.factor = h->factor;
+    a.bias = h->bias;
+    a.x = x;
+    a.x_bf16 = xdt == QMLP_DT_BF16;
+    a.out = out;
+    a.odt = dt_code(odt);
+    return from_cuda(launch_linear(h->group, a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// A whole mixture-of-experts layer
+// ---------------------------------------------------------------------------
+qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const qmlp_moe_layer_desc* d,
+                                  qmlp_stream_t stream) {
+    return guarded([&]() -> qmlp_status {
+        if (!out) return QMLP_ERR_INVALID_ARG;
+        *out = nullptr;
+        if (!moe || !d || !d->router || (!half_type(d->rdt) && d->rdt != QMLP_DT_FP32) ||
+            (d->score != QMLP_SCORE_SOFTMAX && d->score != QMLP_SCORE_SIGMOID) || !isfinite(d->route_scale) ||
+            (d->shared_gate && d->shared < 1))
+            return QMLP_ERR_INVALID_ARG;
+        const int E = moe->E - d->shared, nsel = d->topk + d->shared;
+        if (d->shared < 0 || E < 1 || E > kMoeLayerMaxE || d->topk < 1 || d->topk > E || nsel > 16 ||
+            d->max_tokens < 1 || d->max_tokens > (1 << 20))
+            return QMLP_ERR_SHAPE;
+        cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        if (d->max_tokens > 1) {
+            const qmlp_status st = qmlp_moe_reserve(moe, d->max_tokens, stream);
+            if (st != QMLP_OK) return st;
+        }
+        qmlp_moe_layer_t* h = new qmlp_moe_layer_t();
+        h->moe = moe;
+        h->max_tokens = d->max_tokens;
+        MoeLayerArgs& a = h->a;
+        a.E = E;
+        a.S = d->shared;
+        a.K = moe->K;
+        a.I = moe->I;
+        a.topk = d->topk;
+        a.softmax = d->score == QMLP_SCORE_SOFTMAX;
+        a.renorm = d->renorm != 0;
+        a.rscale = d->route_scale;
+        a.rdt = dt_code(d->rdt);
+        a.w13 = moe->w13;
+        a.w13_meta = moe->w13_meta;
+        a.w2 = moe->w2;
+        a.w2_meta = moe->w2_meta;
+        const size_t few = (size_t)std::min(d->max_tokens, kMoeLayerFew) * nsel, rows = (size_t)d->max_tokens;
+        a.logit_elems = rows * (E + a.S);
+        a.act_elems = few * a.I;
+        a.w13_bytes = moe_w13_bank_bytes(moe->E, a.I, a.K);
+        a.w13_meta_bytes = moe_w13_meta_bank_bytes(moe->E, a.I, a.K, moe->meta);
+        a.w2_bytes = (size_t)moe->E * a.K * (a.I / 2);
+        a.w2_meta_bytes = (size_t)moe->E * a.K * (a.I / 32) * moe->meta;
+        cudaError_t e = cudaSuccess;
+        auto make = [&](size_t bytes, const void* src) -> void* {
+            void* p = nullptr;
+            if (e == cudaSuccess && (e = h->mem.alloc(&p, bytes)) == cudaSuccess && src)
+                e = cudaMemcpyAsync(p, src, bytes, cudaMemcpyDefault, s);
+            return p;
+        };
+        const size_t re = dt_bytes(d->rdt) * a.K;
+        a.router = make(re * E, d->router);
+        if (d->shared_gate) a.sgate = make(re * a.S, d->shared_gate);
+        if (d->bias) a.bias = static_cast<float*>(make((size_t)E * 4, d->bias));
+        a.logits = static_cast<float*>(make(a.logit_elems * 4, nullptr));
+        a.ids = static_cast<int32_t*>(make(rows * nsel * 4, nullptr));
+        a.weights = static_cast<float*>(make(rows * nsel * 4, nullptr));
+        a.act = static_cast<float*>(make(a.act_elems * 4, nullptr));
+        a.amax = static_cast<int*>(make(few * 4, nullptr));
+        uint8_t* words = static_cast<uint8_t*>(make(16, nullptr));
+        if (e == cudaSuccess) e = cudaMemsetAsync(words, 0, 16, s);
+        a.ticket = reinterpret_cast<unsigned long long*>(words);
+        a.err = reinterpret_cast<int*>(words + 8);
+        const cudaError_t e2 = cudaStreamSynchronize(s);
+        if (e == cudaSuccess) e = e2;
+        if (e != cudaSuccess) {
+            h->mem.release();
+            delete h;
+            return from_cuda(e);
+        }
+        *out = h;
+        return QMLP_OK;
+    });
+}
+
+void qmlp_moe_layer_destroy(qmlp_moe_layer_t* h) {
+    if (!h) return;
+    cudaDeviceSynchronize();
+    h->mem.release();
+    delete h;
+}
+
+qmlp_status qmlp_moe_layer_forward(qmlp_moe_layer_t* h, const void* x, qmlp_dtype xdt, int M, void* out, qmlp_dtype odt,
+                                   int32_t* ids, float* weights, qmlp_stream_t stream) {
+    if (!h || !x || !out || !half_type(xdt) || (!half_type(odt) && odt != QMLP_DT_FP32)) return QMLP_ERR_INVALID_ARG;
+    if (M < 1 || M > h->max_tokens) return QMLP_ERR_SHAPE;
+    if (!aligned16(x) || !aligned16(out) || !aligned(ids, 4) || !aligned(weights, 4)) return QMLP_ERR_ALIGNMENT;
+    MoeLayerArgs a = h->a;
+    const size_t n = (size_t)M * a.K, c = (size_t)M * a.topk * 4;
+    const void* p[4] = {out, x, ids, weights};
+    const size_t bytes[4] = {n * dt_bytes(odt), n * 2, c, c};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if (p[i] && p[j] && overlaps(p[i], bytes[i], p[j], bytes[j])) return QMLP_ERR_ALIAS;
+    if (fault("launch")) return QMLP_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    a.M = M;
+    a.x = x;
+    a.x_bf16 = xdt == QMLP_DT_BF16;
+    a.out = out;
+    a.odt = dt_code(odt);
+    a.ids_out = ids;
+    a.w_out = weights;
+    if (moe_layer_few(M, a.K, a.E, std::min(a.E, M * a.topk) + a.S))
+        return from_cuda(launch_moe_layer_few(a, h->moe->meta, h->moe->num_sms, s));
+    cudaError_t e = launch_moe_router(a, s);
+    if (e == cudaSuccess)
+        e = moe_grouped(h->moe, x, a.x_bf16, a.ids, a.weights, a.topk + a.S, M, out, a.odt, s);
+    return from_cuda(e);
+}
+
+qmlp_status qmlp_moe_layer_check(qmlp_moe_layer_t* h, qmlp_stream_t stream) {
+    if (!h) return QMLP_ERR_INVALID_ARG;
+    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return QMLP_ERR_CUDA;
+    int v = 0;
+    if (cudaMemcpy(&v, h->a.err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return QMLP_ERR_CUDA;
+    if (v != 0) {
+        cudaMemset(h->a.err, 0, sizeof(int));
+        return QMLP_ERR_DEVICE_TIMEOUT;
+    }
+    return QMLP_OK;
 }
 
 }  // extern "C"

@@ -117,6 +117,11 @@ struct qmlp_moe_s {
     qmlp::Owner mem;
 };
 
+// The grouped routed experts on M tokens (reserved for); odt: type of out (0 fp32,
+// 1 bf16, 2 fp16).
+cudaError_t moe_grouped(qmlp_moe_s* h, const void* x, bool x_bf16, const int32_t* ids, const float* rw, int topk, int M,
+                        void* out, int odt, cudaStream_t s);
+
 struct qmlp_s {
     int fmt = 0, K = 0, I = 0, max_M = 0, device = 0, num_sms = 0;
     qmlp::GemvProj gv[3];  // gate, up, down

@@ -280,7 +280,8 @@ struct MoeGroupedLaunch {
     int x_is_bf16;
     const int32_t* ids;            // [M, topk]
     const float* rw;               // [M, topk]
-    __half* out;                   // [M, K]
+    void* out;                     // [M, K]
+    int odt = 2;                   // type of out: 0 fp32, 1 bf16, 2 fp16
     __half* act_ws;                // [>= M*topk, I]
     __half* y_ws;                  // [>= M*topk, K]
     int* route_list;               // [>= M*topk]
@@ -364,6 +365,65 @@ struct NormArgs {
 };
 cudaError_t launch_norm(const NormArgs& a, bool t_f16, bool r_f32, bool backward, cudaStream_t s);
 
+// ---------------------------------------------------------------------------
+// One projection with 4-bit weights and group scales (linear.cu)
+// ---------------------------------------------------------------------------
+constexpr int kLinearChunk = 128;  // k of a record of 16 rows
+// Bytes of a record: codes, then scales and zeros of its groups (group 16: NVFP4)
+constexpr int linear_rec_bytes(int group) {
+    return 16 * kLinearChunk / 2 + 16 * (kLinearChunk / group) * (group == 16 ? 1 : 3);
+}
+size_t linear_bytes(int group, int N, int K);
+cudaError_t repack_linear(int group, const uint8_t* w, const void* scale, const uint8_t* zero, int N, int K, uint8_t* out,
+                          cudaStream_t s);
+struct LinearArgs {
+    int M = 0, N = 0, K = 0;
+    const uint8_t* w = nullptr;   // records [N / 16][K / 128], rounded up
+    size_t w_bytes = 0;
+    float factor = 1.0f;          // NVFP4: 1 / global
+    const float* bias = nullptr;  // fp32 [N], or null
+    const void* x = nullptr;      // [M, K], bf16 or fp16
+    bool x_bf16 = true;
+    void* out = nullptr;          // [M, N]
+    int odt = 0;                  // 0 fp32, 1 bf16, 2 fp16
+};
+cudaError_t launch_linear(int group, const LinearArgs& a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// A whole mixture-of-experts layer (moe_layer.cu)
+// ---------------------------------------------------------------------------
+constexpr int kMoeLayerFew = 16;     // tokens that the one-kernel form takes at most
+constexpr int kMoeLayerMaxE = 1024;  // routed experts
+struct MoeLayerArgs {
+    int M = 0, E = 0, S = 0, K = 0, I = 0, topk = 0;  // E routed experts, S shared ones behind them in the banks
+    bool softmax = true, renorm = true;
+    float rscale = 1.0f;
+    int rdt = 1;                    // router and shared gates: 0 fp32, 1 bf16, 2 fp16
+    const void* router = nullptr;   // [E, K]
+    const void* sgate = nullptr;    // [S, K], or null
+    const float* bias = nullptr;    // [E], or null
+    const uint8_t *w13 = nullptr, *w13_meta = nullptr, *w2 = nullptr, *w2_meta = nullptr;  // the handle's banks
+    const void* x = nullptr;        // [M, K]
+    bool x_bf16 = true;
+    void* out = nullptr;            // [M, K]
+    int odt = 1;                    // 0 fp32, 1 bf16, 2 fp16
+    int32_t* ids_out = nullptr;     // [M, topk], or null
+    float* w_out = nullptr;
+    float* logits = nullptr;        // [max_tokens][E + S]
+    int32_t* ids = nullptr;         // more tokens: [M][topk + S]
+    float* weights = nullptr;
+    float* act = nullptr;           // few tokens: [M (topk + S)][I]
+    int* amax = nullptr;            // [M (topk + S)]: bits of the largest |act|
+    unsigned long long* ticket = nullptr;
+    int* err = nullptr;
+    uint64_t limit = 0;
+    int slots = 0;                  // experts that M tokens can name, at most
+    size_t w13_bytes = 0, w13_meta_bytes = 0, w2_bytes = 0, w2_meta_bytes = 0, logit_elems = 0, act_elems = 0;
+};
+bool moe_layer_few(int M, int K, int E, int slots);
+cudaError_t launch_moe_layer_few(MoeLayerArgs a, int meta_bytes, int num_sms, cudaStream_t s);
+cudaError_t launch_moe_router(const MoeLayerArgs& a, cudaStream_t s);
+
 // Index checks of a QMLP_DEBUG_BOUNDS build (common.cuh): each translation
 // unit's first failed check, (site << 48) | index, or 0; reading clears it.
 // The default build returns 0.
@@ -377,5 +437,7 @@ cudaError_t bounds_take_tp_shard(unsigned long long* v);
 cudaError_t bounds_take_lowrank(unsigned long long* v);
 cudaError_t bounds_take_adamw(unsigned long long* v);
 cudaError_t bounds_take_norm(unsigned long long* v);
+cudaError_t bounds_take_linear(unsigned long long* v);
+cudaError_t bounds_take_moe_layer(unsigned long long* v);
 
 }  // namespace qmlp

@@ -65,7 +65,8 @@ struct GArgs {
     int meta_al4;
     const int32_t* ids;  // [M, topk]
     const float* rw;     // [M, topk]
-    __half* out;         // [M, K]
+    void* out;           // [M, K], fp16 or as odt says
+    int odt;             // 0 fp32, 1 bf16, 2 fp16
     __half* act_ws;      // [M * topk, I]
     __half* y_ws;        // [M * topk, K]
     int* route_list;     // [M * topk]: route indices sorted by expert
@@ -544,12 +545,25 @@ __global__ void __launch_bounds__(kCombThr) moe_combine_kernel(const GArgs a) {
             for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[r], __half2float(h[e]), acc[e]);
         }
     }
+    const size_t at = (size_t)tok * a.K + n;
+    if (!QMLP_INB(at + 7, (size_t)a.M * a.K, 49)) return;
+    if (a.odt == 0) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+        o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        return;
+    }
     uint4 o;
-    __half* oh = reinterpret_cast<__half*>(&o);
+    if (a.odt == 1) {
+        __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(&o);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) oh[e] = __float2half_rn(acc[e]);
-    if (QMLP_INB((size_t)tok * a.K + n + 7, (size_t)a.M * a.K, 49))
-        *reinterpret_cast<uint4*>(a.out + (size_t)tok * a.K + n) = o;
+        for (int e = 0; e < 8; ++e) ob[e] = __float2bfloat16_rn(acc[e]);
+    } else {
+        __half* oh = reinterpret_cast<__half*>(&o);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) oh[e] = __float2half_rn(acc[e]);
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = o;
 }
 
 cudaLaunchConfig_t pdl_cfg(dim3 grid, dim3 block, size_t smem, cudaStream_t s, cudaLaunchAttribute* at) {
@@ -616,6 +630,7 @@ cudaError_t launch_moe_grouped(const MoeGroupedLaunch& L, cudaStream_t s) {
     a.ids = L.ids;
     a.rw = L.rw;
     a.out = L.out;
+    a.odt = L.odt;
     a.act_ws = L.act_ws;
     a.y_ws = L.y_ws;
     a.route_list = L.route_list;
