@@ -699,7 +699,8 @@ qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt,
  * (a shared expert of n times the width is n shared experts of the handle's I).
  * Up to 16 tokens whose x fits in shared memory (2 K bytes a token) run as one
  * kernel: sums are fp32, the intermediate is rounded once to fp16 times a power of
- * two of the token and expert, out once. More tokens run the router, the selection
+ * two of the token and expert, out once; a token's result does not depend on the
+ * others of the call. More tokens run the router, the selection
  * and the kernels of qmlp_moe_forward, with its roundings of the stages to fp16.
  */
 typedef enum { QMLP_SCORE_SOFTMAX = 1, QMLP_SCORE_SIGMOID = 2 } qmlp_score;
