@@ -97,6 +97,58 @@ def test_few_tokens(torch, case):
     lin.close()
 
 
+MANY = [  # format, group, N, K, tokens, x, out, bias
+    ("nvfp4", 16, 1000, 1040, (20, 64, 65, 255, 256, 300), "bf16", "bf16", True),
+    ("nvfp4", 16, 256, 5120, (40, 513), "fp16", "fp32", False),
+    ("int4", 32, 5120, 608, (24, 100, 257), "bf16", "fp16", False),
+    ("int4", 64, 77, 17408, (33, 64, 400), "fp16", "bf16", True),
+    ("int4", 128, 2050, 2048, (31, 200, 1000), "bf16", "fp32", True),
+    ("int4", 32, 40, 65536, (64, 256), "bf16", "fp32", False),
+    ("int4", 128, 5120, 4096, (2000,), "bf16", "bf16", False),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(map(str, c)))
+def test_many_tokens(torch, case):
+    """From 256 tokens on an INT4 weight is rounded to fp16: 2^-11 of its size."""
+    fmt, G, N, K, tokens, xt, ot, has_bias = case
+    T = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+    a, v = weights(fmt, N, K, G, N + K)
+    bias = np.random.default_rng(1).normal(size=N).astype(np.float32) if has_bias else None
+    lin = q.QuantLinear(fmt, N, K, max(tokens), global_scale=0.3 if fmt == "nvfp4" else 1.0, bias=bias, **a)
+    factor = 1.0 / np.float64(np.float32(0.3)) if fmt == "nvfp4" else 1.0
+    g = torch.Generator(device="cuda").manual_seed(K)
+    for M in tokens:
+        x = torch.randn((M, K), generator=g, device="cuda").to(T[xt])
+        out = torch.full((M, N), 7.0, device="cuda", dtype=T[ot])
+        lin.forward(x, out)
+        again = torch.empty_like(out)
+        lin.forward(x, again)
+        lin.check()
+        assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
+        check(torch, x, v, out, factor, bias, 2.0 ** -11 if M >= 256 and fmt == "int4" else 0.0)
+    lin.close()
+
+
+def test_weights_in_several_slabs(torch):
+    """A projection whose images pass 1 GiB: the rows at the slabs' ends."""
+    N, K, M = 70001, 8192, 300
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.randint(0, 256, (N, K // 2), generator=g, device="cuda", dtype=torch.uint8)
+    s = torch.rand((N, K // 128), generator=g, device="cuda").half() * 0.01
+    z = torch.randint(0, 16, (N, K // 128), generator=g, device="cuda", dtype=torch.uint8)
+    lin = q.QuantLinear("int4", N, K, M, w, s, zero=z, group=128)
+    x = torch.randn((M, K), generator=g, device="cuda").to(torch.bfloat16)
+    out = torch.empty((M, N), device="cuda")
+    lin.forward(x, out)
+    lin.check()
+    rows = [*range(0, 40), *range(65500, 65600), *range(69960, 70001)]
+    c = torch.stack((w[rows] & 15, w[rows] >> 4), -1).flatten(1).double()
+    v = (c - z[rows].double().repeat_interleave(128, 1)) * s[rows].double().repeat_interleave(128, 1)
+    check(torch, x, v.cpu().numpy(), out[:, rows].contiguous(), more=2.0 ** -11)
+    lin.close()
+
+
 def test_single_weights_and_any_zero(torch):
     """One-hot tokens return single weights, exactly; zeros over the whole byte."""
     for fmt, G, zmax in (("nvfp4", 16, 0), ("int4", 32, 256), ("int4", 128, 256)):

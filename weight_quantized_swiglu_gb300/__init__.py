@@ -159,6 +159,7 @@ _SIGS = {
     "qmlp_linear_create": ([ctypes.POINTER(_VP), ctypes.POINTER(qmlp_linear_desc), _VP], _I),
     "qmlp_linear_destroy": ([_VP], None),
     "qmlp_linear_forward": ([_VP, _VP, _I, _I, _VP, _I, _VP], _I),
+    "qmlp_linear_check": ([_VP, _VP], _I),
     "qmlp_moe_layer_create": ([ctypes.POINTER(_VP), _VP, ctypes.POINTER(qmlp_moe_layer_desc), _VP], _I),
     "qmlp_moe_layer_destroy": ([_VP], None),
     "qmlp_moe_layer_forward": ([_VP, _VP, _I, _I, _VP, _I, _VP, _VP, _VP], _I),
@@ -458,6 +459,10 @@ def qmlp_linear_destroy(h: int):
 
 def qmlp_linear_forward(h, x, xdt, M, out, odt, stream=None) -> int:
     return lib().qmlp_linear_forward(h, _ptr(x), xdt, M, _ptr(out), odt, _stream(stream))
+
+
+def qmlp_linear_check(h, stream=None) -> int:
+    return lib().qmlp_linear_check(h, _stream(stream))
 
 
 def qmlp_moe_layer_create(moe, desc: qmlp_moe_layer_desc, stream=None) -> int:
@@ -978,6 +983,9 @@ class QuantLinear:
         _chk(self._forward(self.h, x.data_ptr(), self._kinds[x.dtype], M, out.data_ptr(), self._kinds[out.dtype],
                            _stream(stream)), "qmlp_linear_forward")
         return out
+
+    def check(self, stream=None):
+        _chk(qmlp_linear_check(self.h, stream), "qmlp_linear_check")
 
     def close(self):
         if getattr(self, "h", None):

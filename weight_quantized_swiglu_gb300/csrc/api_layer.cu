@@ -22,8 +22,22 @@ struct qmlp_linear_s {
     size_t w_bytes = 0;
     float factor = 1.0f;
     float* bias = nullptr;
+    // max_M >= kLinearGemmM: the tensor-core GEMM, `slab` rows of W at a time
+    int slab = 0;
+    float* factors = nullptr;  // [N rounded up to 256]
+    uint8_t* img = nullptr;
+    size_t img_bytes = 0;
+    void* a16 = nullptr;       // fp16 [max_M, K]: bf16 tokens times a power of two each
+    int* sig = nullptr;        // [max_M]
+    float* ws = nullptr;       // shares of split tiles
+    int* err = nullptr;
     Owner mem;
 };
+
+// Fewest tokens that the GEMM takes (see qmlp_linear_forward).
+constexpr int kLinearGemmM = 256;
+static_assert(kLinearGemmM >= kPairMinM, "the GEMM on CTA pairs");
+constexpr size_t kLinearImages = (size_t)1 << 30;  // bytes of images that a handle holds at most
 
 struct qmlp_moe_layer_s {
     qmlp_moe_t* moe = nullptr;
@@ -39,6 +53,17 @@ int dt_code(qmlp_dtype t) { return t == QMLP_DT_FP32 ? 0 : t == QMLP_DT_BF16 ? 1
 bool half_type(qmlp_dtype t) { return t == QMLP_DT_BF16 || t == QMLP_DT_FP16; }
 // fp32 or the other 16-bit type
 bool same_or_fp32(qmlp_dtype t, qmlp_dtype of) { return t == of || t == QMLP_DT_FP32; }
+
+// Waits for the stream, reports and clears a recorded give-up of a bounded wait.
+qmlp_status check_word(int* err, qmlp_stream_t stream) {
+    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return QMLP_ERR_CUDA;
+    int v = 0;
+    if (!err) return QMLP_OK;
+    if (cudaMemcpy(&v, err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return QMLP_ERR_CUDA;
+    if (v == 0) return QMLP_OK;
+    cudaMemset(err, 0, sizeof(int));
+    return QMLP_ERR_DEVICE_TIMEOUT;
+}
 
 Range range(const void* p, size_t bytes, bool written) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(p);
@@ -268,6 +293,19 @@ qmlp_status qmlp_linear_create(qmlp_linear_t** out, const qmlp_linear_desc* d, q
         if (e == cudaSuccess)
             e = repack_linear(d->group, static_cast<const uint8_t*>(w), sc, static_cast<const uint8_t*>(z), d->N, d->K,
                               h->w, s);
+        if (d->max_M >= kLinearGemmM) {
+            const int padded = (d->N + 255) / 256 * 256, Kp = (d->K + 63) / 64 * 64;
+            h->slab = (int)std::max<size_t>(256, std::min<size_t>(padded, kLinearImages / (2 * (size_t)Kp) / 256 * 256));
+            h->img_bytes = gemm_decoded_bytes(h->slab, Kp);
+            const size_t need[6] = {(size_t)padded * 4, h->img_bytes, (size_t)d->max_M * d->K * 2, (size_t)d->max_M * 4,
+                                    gemm_splitk_ws_elems(sms) * 4, 16};
+            void** dst[6] = {reinterpret_cast<void**>(&h->factors), reinterpret_cast<void**>(&h->img), &h->a16,
+                             reinterpret_cast<void**>(&h->sig), reinterpret_cast<void**>(&h->ws),
+                             reinterpret_cast<void**>(&h->err)};
+            for (int i = 0; i < 6 && e == cudaSuccess; ++i) e = h->mem.alloc(dst[i], need[i]);
+            if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 16, s);
+            if (e == cudaSuccess) e = launch_linear_factors(d->group, sc, d->N, d->K, h->factor, h->factors, padded, s);
+        }
         const cudaError_t e2 = cudaStreamSynchronize(s);
         tmp.release();
         if (e == cudaSuccess) e = e2;
@@ -307,7 +345,50 @@ qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt,
     a.x_bf16 = xdt == QMLP_DT_BF16;
     a.out = out;
     a.odt = dt_code(odt);
-    return from_cuda(launch_linear(h->group, a, h->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (M < kLinearGemmM || !h->img) return from_cuda(launch_linear(h->group, a, h->num_sms, s));
+    // many tokens: the weights decoded once into stage images, rows of W in slabs
+    const int Kp = (h->K + 63) / 64 * 64;
+    for (int n0 = 0; n0 < h->N; n0 += h->slab) {
+        const int rows = std::min(h->slab, (h->N - n0 + 255) / 256 * 256), cols = std::min(h->slab, h->N - n0);
+        cudaError_t e = launch_linear_images(h->group, h->w, h->w_bytes, h->factors, h->N, h->K, n0, rows, h->img,
+                                             h->img_bytes, s);
+        if (e != cudaSuccess) return from_cuda(e);
+        GemmLaunch g;
+        g.epi = kEpiOut;
+        g.w.fmt = kFP8;
+        g.w.N = rows;
+        g.w.K = Kp;
+        g.w.cs0 = h->factors + n0;
+        g.a = x;
+        g.M = M;
+        g.out = static_cast<uint8_t*>(out) + (size_t)n0 * dt_bytes(odt);
+        g.ldo = h->N;
+        g.ncols = cols;
+        g.odt = a.odt;
+        g.bias = h->bias ? h->bias + n0 : nullptr;
+        g.ka = h->K;
+        // (the activations are scaled once, before the first slab)
+        g.unscaled = !a.x_bf16;
+        g.prescaled = !a.x_bf16 || n0 > 0;
+        g.a16 = a.x_bf16 ? h->a16 : const_cast<void*>(x);
+        g.sig = h->sig;
+        g.err = h->err;
+        g.ws = h->ws;
+        g.pair = true;
+        g.wdec = h->img;
+        g.wdec_bytes = h->img_bytes;
+        g.f16 = true;
+        g.split_tail = true;
+        g.images_ready = true;
+        if ((e = launch_gemm(g, h->num_sms, s)) != cudaSuccess) return from_cuda(e);
+    }
+    return QMLP_OK;
+}
+
+qmlp_status qmlp_linear_check(qmlp_linear_t* h, qmlp_stream_t stream) {
+    if (!h) return QMLP_ERR_INVALID_ARG;
+    return check_word(h->err, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -425,14 +506,7 @@ qmlp_status qmlp_moe_layer_forward(qmlp_moe_layer_t* h, const void* x, qmlp_dtyp
 
 qmlp_status qmlp_moe_layer_check(qmlp_moe_layer_t* h, qmlp_stream_t stream) {
     if (!h) return QMLP_ERR_INVALID_ARG;
-    if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return QMLP_ERR_CUDA;
-    int v = 0;
-    if (cudaMemcpy(&v, h->a.err, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return QMLP_ERR_CUDA;
-    if (v != 0) {
-        cudaMemset(h->a.err, 0, sizeof(int));
-        return QMLP_ERR_DEVICE_TIMEOUT;
-    }
-    return QMLP_OK;
+    return check_word(h->a.err, stream);
 }
 
 }  // extern "C"

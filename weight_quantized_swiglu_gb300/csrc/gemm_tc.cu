@@ -176,6 +176,8 @@ struct Args {
     // one adds them. (tail 0: none.)
     int tail, tail_splits;
     void* out_lo;          // SwiGLU, SwiGLUGrad: optional, bf16 of what out's rounding leaves
+    int odt;               // kEpiOut: type of out (0 fp32, 1 bf16, 2 fp16); ncols: its columns
+    const float* bias;     // kEpiOut: optional, [ncols]
 };
 
 // Quad (columns col..col+3) of row m in the gate / up values kept for the
@@ -260,6 +262,46 @@ QMLP_DEV uint32_t pack_bf16x2(float lo, float hi) {
 QMLP_DEV void store16(__nv_bfloat16* dst, const uint32_t (&v)[8]) {
     reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+}
+
+// kEpiOut: n values of row m from column col on, whole vectors where out has the
+// room and the alignment for them.
+template <int N>
+QMLP_DEV void store_any(const Args& a, int m, int col, const float (&v)[N]) {
+    const size_t at = (size_t)m * a.ldo + col;
+    if (!QMLP_INB(m, a.M, 12)) return;
+    if (a.odt == 0) {
+        float* o = static_cast<float*>(a.out) + at;
+        if (col + N <= a.ncols && (a.ldo & 3) == 0) {
+#pragma unroll
+            for (int j = 0; j < N; j += 4) *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (col + j < a.ncols) o[j] = v[j];
+        }
+        return;
+    }
+    uint32_t p[N / 2];
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) {
+        if (a.odt == 1) {
+            p[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+        } else {
+            const __half2 h = __floats2half2_rn(v[2 * j], v[2 * j + 1]);
+            p[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+    if (col + N <= a.ncols && (a.ldo & 7) == 0 && N % 8 == 0) {
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j)
+            reinterpret_cast<uint4*>(o)[j] = make_uint4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (col + j < a.ncols) o[j] = (uint16_t)(p[j / 2] >> (16 * (j & 1)));
+    }
 }
 
 // EXT: the instances of low-rank adapters, which add their fp32 terms.
@@ -405,6 +447,25 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                         store16(lo + a.ncols, lu);
                     }
                 }
+            }
+        }
+    } else if (EXT && a.epi == kEpiOut) {
+#pragma unroll 1
+        for (int c0 = first; c0 < BN; c0 += step) {
+            float y[32];
+            tmem_ld32(tbase + c0, y);
+            const int col = nt * BN + c0;
+            if (live && col < a.ncols) {
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 f = factor4<FMT>(a.cs0, a.inv0, col + j);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[j + e] = y[j + e] * pw * f4_at(f, e);
+                        if (a.bias && col + j + e < a.ncols) y[j + e] += __ldg(a.bias + col + j + e);
+                    }
+                }
+                store_any<32>(a, m, col, y);
             }
         }
     } else if (a.epi == kEpiPlain) {
@@ -1213,6 +1274,16 @@ __global__ void __launch_bounds__(256) tail_reduce_kernel(const Args a) {
     }
     const float4 f = factor4<FMT>(a.cs0, a.inv0, n);
     const int sg = a.sig ? a.sig[m] : 0;
+    if (a.epi == kEpiOut) {
+        if (n >= a.ncols) return;
+        const float pw = scalbnf(1.0f, -sg);
+        float v[4] = {s.x * pw * f.x, s.y * pw * f.y, s.z * pw * f.z, s.w * pw * f.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (a.bias && n + e < a.ncols) v[e] += a.bias[n + e];
+        store_any<4>(a, m, n, v);
+        return;
+    }
     float4 d = make_float4(0, 0, 0, 0);
     if (a.add && (!a.add_rows || a.add_rows[m]) && QMLP_INB((size_t)m * a.ldadd + n + 3, a.add_elems, 19)) d = *reinterpret_cast<const float4*>(a.add + (size_t)m * a.ldadd + n);
     const int mo = a.rows ? a.rows[m] : m;
@@ -1540,7 +1611,7 @@ cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const C
         max_pairs = n;
     }
     int pairs = std::min(pairs_wanted, max_pairs);
-    const bool split = EXT && a.tail && a.epi == kEpiPlain && a.ws;
+    const bool split = EXT && a.tail && (a.epi == kEpiPlain || a.epi == kEpiOut) && a.ws;
     a.tail = 0;
     a.tail_splits = 1;
     if (split) {
@@ -1698,15 +1769,16 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     // 1. per-token fp16 prescale of the activations (decoder-warp GEMMs,
     //    whose decoders write fp16 weights)
     if ((!dq || L.f16) && !L.prescaled) {
-        const cudaError_t e = launch_gemm_prescale(L.a, L.M, P.K, L.a16, L.sig, num_sms, s);
+        const cudaError_t e = launch_gemm_prescale(L.a, L.M, L.ka ? L.ka : P.K, L.a16, L.sig, num_sms, s);
         if (e != cudaSuccess) return e;
     }
 
     // 2. tensor map of the MMA's activations: [M rows, K] row-major, box 64 x
     //    128 (fp16 prescaled, or the bf16 input itself)
     CUtensorMap map;
-    const cuuint64_t dims[2] = {(cuuint64_t)P.K, (cuuint64_t)L.M};
-    const cuuint64_t strides[1] = {(cuuint64_t)P.K * 2};
+    const int ka = L.ka ? L.ka : P.K;
+    const cuuint64_t dims[2] = {(cuuint64_t)ka, (cuuint64_t)L.M};
+    const cuuint64_t strides[1] = {(cuuint64_t)ka * 2};
     const cuuint32_t box[2] = {(cuuint32_t)BK, (cuuint32_t)BM};
     const cuuint32_t estr[2] = {1, 1};
     const bool bf = dq && !L.f16;
@@ -1730,7 +1802,10 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.cs0 = P.cs0;
     a.cs1 = P.cs1;
     if (P.fmt == kFP8 && (!P.cs0 || (P.interleaved && !P.cs1))) return cudaErrorInvalidValue;
-    a.sig = bf ? nullptr : L.sig;
+    a.sig = bf || L.unscaled ? nullptr : L.sig;
+    a.odt = L.odt;
+    a.bias = L.bias;
+    if (L.epi == kEpiOut && (!L.pair || !dq || !L.f16 || !L.images_ready || P.fmt != kFP8)) return cudaErrorInvalidValue;
     a.f16 = L.f16 ? 1 : 0;
     a.tail = L.split_tail ? 1 : 0;  // launch_pair plans it
     // Training's SwiGLU GEMMs stream as much through L2 as their operands: in groups
@@ -1751,6 +1826,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     if (L.rows && (L.epi != kEpiPlain || !L.pair || !dq)) return cudaErrorInvalidValue;
     a.out = L.out;
     a.ldo = L.epi == kEpiSwiGLU ? P.N / 2 : (L.epi == kEpiRaw && P.interleaved ? P.N / 2 : P.N);
+    if (L.epi == kEpiOut) a.ldo = L.ldo;
     a.add = L.add;
     a.ldadd = L.ldadd;
     a.gu_g = static_cast<float4*>(L.gu_g);
@@ -1763,7 +1839,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.out_lo = L.out_lo;
     const bool grad = L.epi == kEpiSwiGLUGrad, ext = L.add || L.gu_g || grad || L.ext || L.rows || (dq && (L.f16 || L.split_tail));
     if (L.ext && (!L.pair || !dq || L.f16 || !L.ext_a || !L.ext_b)) return cudaErrorInvalidValue;
-    if (ext && (L.epi == kEpiRaw || (L.pair && !dq) || L.ldadd % 4 || (grad && (!L.gu_g || L.ncols > P.N))))
+    if (ext && (L.epi == kEpiRaw || (L.pair && !dq) || L.ldadd % 4 || (grad && (!L.gu_g || L.ncols > P.N)) || (L.epi == kEpiOut && L.ncols > P.N)))
         return cudaErrorInvalidValue;
     a.err = L.err;
     a.limit = L.wait_ns ? L.wait_ns : kGemmWaitNs;

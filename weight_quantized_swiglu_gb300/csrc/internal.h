@@ -21,7 +21,8 @@ enum GemvEpi {
     kEpiSwiGLU = 0,  // two projections (gate, up) -> act = bf16(SiLU(g)*u)
     kEpiPlain = 1,   // one projection -> bf16(sigma * acc)
     kEpiRaw = 2,     // one projection -> fp32 acc (no scale), debug
-    kEpiSwiGLUGrad = 3  // d act -> [d gate | d up] (GEMM, training)
+    kEpiSwiGLUGrad = 3, // d act -> [d gate | d up] (GEMM, training)
+    kEpiOut = 4         // one projection, factor a row -> bf16, fp16 or fp32, + bias, any number of columns (GEMM)
 };
 
 // One projection [N, K] in the GEMV ("fragment-native") layout: one record
@@ -227,6 +228,12 @@ struct GemmLaunch {
     const int* add_rows = nullptr;  // CTA pairs: only tokens whose value is not 0 get `add` (null: all)
     void* out_lo = nullptr;      // with gu_g: optional, bf16 of what the rounding of out leaves
     bool images_ready = false;  // dequantise-once: wdec already holds w's images (no predecode launch)
+    // kEpiOut (CTA pairs, f16 images, w.fmt FP8: a factor a row): out = [M][ldo] of odt
+    // (0 fp32, 1 bf16, 2 fp16), the first ncols of w.N columns written, + bias
+    int ldo = 0, odt = 1;
+    const float* bias = nullptr;
+    int ka = 0;                 // row length of a (0: w.K): k past it is zero
+    bool unscaled = false;      // a16 is fp16 as it came: no exponents
 };
 constexpr int kPairMinM = 256;  // one 256-token tile of a CTA pair
 cudaError_t launch_gemm_prescale(const void* a, int M, int K, void* a16, int* sig, int num_sms, cudaStream_t s);
@@ -388,6 +395,14 @@ struct LinearArgs {
     int odt = 0;                  // 0 fp32, 1 bf16, 2 fp16
 };
 cudaError_t launch_linear(int group, const LinearArgs& a, int num_sms, cudaStream_t s);
+// Stage images of the tensor-core GEMM (fp16, rows times 2^-exponent of their factor)
+// of rows n0.. (a multiple of 256) of the records: N rows padded to 256, K to 64. The
+// factors of all rows: c, for INT4 times a power of two that keeps a row's images in
+// fp16's range.
+cudaError_t launch_linear_images(int group, const uint8_t* w, size_t w_bytes, const float* factors, int N, int K, int n0,
+                                 int rows, uint8_t* img, size_t img_bytes, cudaStream_t s);
+cudaError_t launch_linear_factors(int group, const void* scale, int N, int K, float c, float* factors, int padded,
+                                  cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // A whole mixture-of-experts layer (moe_layer.cu)

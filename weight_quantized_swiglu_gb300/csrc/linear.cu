@@ -4,7 +4,7 @@
 //   INT4:  W = (code - zero[n, k / G]) scale[n, k / G], G = 32, 64 or 128, c = 1
 // for a few tokens (here) or many (images for the tensor-core GEMM, below).
 //
-// Few tokens (at most 16): bound by the weights' bytes, each read once.
+// Few tokens (at most 64 a launch): the weights are read once.
 //  * Weights are laid out once, in records of 16 rows x 128 k (kRec bytes: codes
 //    in the order in which the lanes of an mma.sync m16n8k16 take them as the A
 //    operand, then the groups' scales). k is summed in any order that both
@@ -179,6 +179,14 @@ QMLP_DEV float peer_f32(const float* p, int rank) {
     return v;
 }
 
+QMLP_DEV int peer_s32(const int* p, int rank) {
+    uint32_t ra;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(ra) : "memory");
+    return v;
+}
+
 QMLP_DEV void store_out(const LinearArgs& a, int m, int n, float v) {
     const size_t at = (size_t)m * a.N + n;
     if (!QMLP_INB(at, (size_t)a.M * a.N, 92)) return;
@@ -190,13 +198,18 @@ QMLP_DEV void store_out(const LinearArgs& a, int m, int n, float v) {
 
 // Grid (splits, CTAs of a split), cluster (splits, 1). Shared memory: x, the
 // warps' sums (two buffers), this CTA's sums of its tiles where k is split.
+// Buffers of the warps' sums: with two, one barrier a tile is enough.
+template <int NT>
+constexpr int red_bufs() { return NT <= 2 ? 2 : 1; }
+template <int NT>
+constexpr int few_ctas() { return NT == 1 ? 3 : NT == 8 ? 1 : 2; }
+
 template <int G, int NT>
-__global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) linear_few_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(kW * 32, few_ctas<NT>()) linear_few_kernel(const LinearArgs a) {
     using R = Rec<G>;
     constexpr int kC = 8 * NT;  // columns
     extern __shared__ __align__(16) uint4 xsm[];
-    __shared__ float s_max[16];
-    __shared__ int s_sig[16];
+    __shared__ int s_max[kC], s_sig[kC];
     const int S = gridDim.x, rank = blockIdx.x, M = a.M, K = a.K;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int Kc = (K + kCh - 1) / kCh, Nt = (a.N + 15) / 16;
@@ -204,8 +217,8 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) linear_few_kernel(co
     const int kc0 = rank * cps, nch = min(cps, Kc - kc0);  // this one's
     const int cpw = (cps + kW - 1) / kW;
     const int c0 = warp * cpw, cw = max(0, min(cpw, nch - c0));  // this warp's
-    float* red = reinterpret_cast<float*>(xsm + (size_t)cps * 16 * M);  // [2][kW][16][kC]
-    float* own = red + 2 * kW * 16 * kC;                                // [tiles][16][kC]
+    float* red = reinterpret_cast<float*>(xsm + (size_t)cps * 16 * M);  // [buffers][kW][16][kC]
+    float* own = red + red_bufs<NT>() * kW * 16 * kC;                   // [tiles][16][kC]
     const int tiles = (Nt - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
 
     // the first records are on their way before anything else
@@ -230,54 +243,60 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) linear_few_kernel(co
         for (int d = 0; d < kD; ++d) fetch(fr[d]);
 
     // x of this CTA's k, in the order of the steps: slot ((c 4 + i) M + m) 4 + t has
-    // k = 128 c + 32 i + 4 t.. (four) and 16 further (four) of token m
-    const int k0 = kc0 * kCh, kn = nch * kCh;
-    if (a.x_bf16) {
-        for (int m = warp; m < M; m += kW) {
-            const uint2* row = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.x) + (size_t)m * K);
-            float mx = 0.0f;
-            for (int i = k0 / 4 + lane; i < min(K, k0 + kn) / 4; i += 32) {
-                const uint2 v = __ldg(row + i);
-                mx = fmaxf(mx, fmaxf(fmaxf(fabsf(__uint_as_float(v.x << 16)), fabsf(__uint_as_float(v.x & 0xFFFF0000u))),
-                                     fmaxf(fabsf(__uint_as_float(v.y << 16)), fabsf(__uint_as_float(v.y & 0xFFFF0000u)))));
-            }
+    // k = 128 c + 32 i + 4 t.. (four) and 16 further (four) of token m. A thread
+    // stays with one token: its largest value falls out of the copy, and the copy is
+    // scaled in place once the row's exponent is known (M = 1, K = 5120: the kernel
+    // took 10.3 us with a pass over x for the largest value before the copy)
+    constexpr int kMp = NT == 1 ? 8 : 8 * NT;  // (M = 1: all threads on its row)
+    const int mp = NT == 1 && M == 1 ? 1 : kMp;
+    const int k0 = kc0 * kCh, xt = threadIdx.x & 3, xm = (threadIdx.x >> 2) % mp, hop_c = kW * 8 / mp;
+    if (threadIdx.x < kC) s_max[threadIdx.x] = 0;
+    __syncthreads();
+    if (xm < M) {
+        float mx = 0.0f;
+        const uint16_t* row = static_cast<const uint16_t*>(a.x) + (size_t)xm * K;
+#pragma unroll 4
+        for (int ci = (threadIdx.x >> 2) / mp; ci < nch * 4; ci += hop_c) {
+            const int k = k0 + 32 * ci + 4 * xt;
+            uint2 v[2];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) s_max[m] = mx;
+            for (int h = 0; h < 2; ++h)  // K is a multiple of 16
+                v[h] = k + 16 * h < K ? __ldg(reinterpret_cast<const uint2*>(row + k + 16 * h)) : make_uint2(0, 0);
+            if (a.x_bf16)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    mx = fmaxf(mx, fmaxf(fmaxf(fabsf(__uint_as_float(v[h].x << 16)), fabsf(__uint_as_float(v[h].x & 0xFFFF0000u))),
+                                         fmaxf(fabsf(__uint_as_float(v[h].y << 16)), fabsf(__uint_as_float(v[h].y & 0xFFFF0000u)))));
+            xsm[(ci * M + xm) * 4 + xt] = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
         }
+        if (a.x_bf16) atomicMax(s_max + xm, __float_as_int(mx));
+    }
+    if (a.x_bf16) {
         if (S > 1) lin_cluster_sync();
         else __syncthreads();
-    }
-    if (threadIdx.x < M) {
-        float mx = 0.0f;
-        if (a.x_bf16)
-            for (int r = 0; r < S; ++r) mx = fmaxf(mx, S > 1 ? peer_f32(s_max + threadIdx.x, r) : s_max[threadIdx.x]);
-        s_sig[threadIdx.x] = prescale_exponent(mx);
-        if (!a.x_bf16) s_sig[threadIdx.x] = 0;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < nch * 16 * M; i += blockDim.x) {
-        const int tt = i & 3, m = (i >> 2) % M, ci = (i >> 2) / M;  // ci = 4 c + step pair
-        const int k = k0 + 32 * ci + 4 * tt;
-        uint32_t v[4] = {0, 0, 0, 0};
-        const uint16_t* row = static_cast<const uint16_t*>(a.x) + (size_t)m * K;
+        if (threadIdx.x < M) {
+            int mx = 0;
+            for (int r = 0; r < S; ++r) mx = max(mx, S > 1 ? peer_s32(s_max + threadIdx.x, r) : s_max[threadIdx.x]);
+            s_sig[threadIdx.x] = prescale_exponent(__int_as_float(mx));
+        }
+        __syncthreads();
+        if (xm < M) {
+            const int sg = s_sig[xm];
+            for (int ci = (threadIdx.x >> 2) / mp; ci < nch * 4; ci += hop_c) {
+                uint4& slot = xsm[(ci * M + xm) * 4 + xt];
+                const uint4 u = slot;
+                uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            if (k + 16 * h < K) {  // K is a multiple of 16
-                const uint2 p = __ldg(reinterpret_cast<const uint2*>(row + k + 16 * h));
-                v[2 * h] = p.x;
-                v[2 * h + 1] = p.y;
-            }
-        if (a.x_bf16) {
-            const int sg = s_sig[m];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __half2 hv = __floats2half2_rn(scalbnf(__uint_as_float(v[j] << 16), sg),
-                                                     scalbnf(__uint_as_float(v[j] & 0xFFFF0000u), sg));
-                v[j] = *reinterpret_cast<const uint32_t*>(&hv);
+                for (int j = 0; j < 4; ++j) {
+                    const __half2 hv = __floats2half2_rn(scalbnf(__uint_as_float(v[j] << 16), sg),
+                                                         scalbnf(__uint_as_float(v[j] & 0xFFFF0000u), sg));
+                    v[j] = *reinterpret_cast<const uint32_t*>(&hv);
+                }
+                slot = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
-        xsm[i] = make_uint4(v[0], v[1], v[2], v[3]);
+    } else if (threadIdx.x < M) {
+        s_sig[threadIdx.x] = 0;
     }
     __syncthreads();
 
@@ -292,7 +311,8 @@ __global__ void __launch_bounds__(kW * 32, NT == 1 ? 3 : 2) linear_few_kernel(co
     // the warps' sums of a tile -> out, or this CTA's share of it
     int tile = 0;
     auto finish = [&] {
-        float* rb = red + (tile & 1) * kW * 16 * kC;
+        float* rb = red + (red_bufs<NT>() > 1 ? (tile & 1) * kW * 16 * kC : 0);
+        if (red_bufs<NT>() == 1) __syncthreads();  // the sums of the tile before are read
         float* mine = rb + warp * 16 * kC;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -395,6 +415,84 @@ __global__ void __launch_bounds__(256) repack_linear_kernel(const uint8_t* __res
     }
 }
 
+// Records -> stage images: a warp a record (16 rows x 128 k), each lane the four k
+// of its two rows that it has of a step, 8 bytes of an image row at a time.
+template <int G>
+__global__ void __launch_bounds__(256) linear_images_kernel(const uint8_t* __restrict__ w, size_t w_bytes,
+                                                            const float* __restrict__ factors, int Nt, int Kc, int KS,
+                                                            int tile0, long recs, uint8_t* __restrict__ img,
+                                                            size_t img_bytes) {
+    using R = Rec<G>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    for (long rec = (long)blockIdx.x * 8 + (threadIdx.x >> 5); rec < recs; rec += (long)gridDim.x * 8) {
+        const int kc = (int)(rec % Kc), lt = (int)(rec / Kc), tile = tile0 + lt;  // 16 rows, from the images' first
+        Frag<G> f;
+        const bool in = tile < Nt;
+        const size_t at = ((size_t)(in ? tile : 0) * Kc + kc) * R::kBytes;
+        if (in && QMLP_INB(at + R::kBytes - 1, w_bytes, 93)) load_frag<G>(f, w + at, lane);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = lt * 16 + g + 8 * h, n = row & 255;
+            // INT4: the images hold (code - zero) scale over the row's factor, a power of two
+            const float rf = R::kNv || !in ? 1.0f : 1.0f / factors[tile * 16 + g + 8 * h];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // steps 2i, 2i + 1
+                uint32_t a[4] = {0, 0, 0, 0};
+                if (in) {
+                    if constexpr (R::kNv) {
+                        e2m1x4_to_f16x2x4(word_of(f.c[h], i), a[0], a[1], a[2], a[3]);
+                        const uint32_t sp = e4m3x2_to_f16x2((f.s[h][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
+                        const uint32_t lo = dup_lo16(sp), hi = dup_hi16(sp);
+                        a[0] = hmul2_u32(a[0], lo);
+                        a[1] = hmul2_u32(a[1], lo);
+                        a[2] = hmul2_u32(a[2], hi);
+                        a[3] = hmul2_u32(a[3], hi);
+                    } else {
+                        const int q = i * R::kPer / 4;
+                        const uint32_t z1 = zero2(f.z[h], q);
+                        int4x8(word_of(f.c[h], i), z1, hadd2u(z1, 0x63806380u), a);
+                        const float s =
+                            rf * __half2float(__ushort_as_half((unsigned short)(f.s[h][q >> 1] >> (16 * (q & 1)))));
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&a[p]));
+                            const __half2 o = __floats2half2_rn(v.x * s, v.y * s);
+                            a[p] = *reinterpret_cast<const uint32_t*>(&o);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int ks = 2 * kc + (i >> 1);                          // 64-k step
+                    const int ch = 2 * (2 * (i & 1) + u) + (t >> 1);           // 16-byte chunk of its row
+                    if (ks < KS) {
+                        const size_t o = ((size_t)(row >> 8) * KS + ks) * 32768 + n * 128 + ((ch ^ (n & 7)) << 4) + 8 * (t & 1);
+                        if (QMLP_INB(o + 7, img_bytes, 94)) *reinterpret_cast<uint2*>(img + o) = make_uint2(a[2 * u], a[2 * u + 1]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+// The factors of the images' rows, padded with ones.
+__global__ void __launch_bounds__(256) linear_factors_kernel(const __half* __restrict__ scale, int groups, int N, float c,
+                                                             float* __restrict__ factors, int padded) {
+    const int lane = threadIdx.x & 31;
+    for (int n = blockIdx.x * 8 + (threadIdx.x >> 5); n < padded; n += gridDim.x * 8) {
+        float f = n < N ? c : 1.0f;
+        if (scale && n < N) {
+            float mx = 0.0f;
+            for (int i = lane; i < groups; i += 32) mx = fmaxf(mx, fabsf(__half2float(scale[(size_t)n * groups + i])));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            // the largest scale to [2^5, 2^6): 255 of it stay below fp16's largest
+            f = scalbnf(1.0f, 9 - prescale_exponent(mx));
+        }
+        if (lane == 0) factors[n] = f;
+    }
+}
+
 template <int G, int NT>
 cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     constexpr int kC = 8 * NT;
@@ -407,8 +505,8 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     while (S > 1 && (S - 1) * ((Kc + S - 1) / S) >= Kc) S /= 2;  // every CTA has some of k
     if (xbytes(S) > kSmemMax - 64 * 1024) return cudaErrorInvalidValue;
     // as many CTAs as fit at once, each on an even share of the tiles
-    const size_t fixed = xbytes(S) + 2 * kW * 16 * kC * sizeof(float);
-    const int fit = (int)std::max<size_t>(1, std::min<size_t>(NT == 1 ? 3 : 2, kSmemMax / (fixed + 2048)));
+    const size_t fixed = xbytes(S) + red_bufs<NT>() * kW * 16 * kC * sizeof(float);
+    const int fit = (int)std::max<size_t>(1, std::min<size_t>(few_ctas<NT>(), kSmemMax / (fixed + 2048)));
     int gy = std::max(1, std::min(Nt, num_sms * fit / S));
     int tiles = (Nt + gy - 1) / gy;
     // a split's sums of all its tiles wait in shared memory
@@ -440,17 +538,22 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
 
 template <int G>
 cudaError_t launch_g(LinearArgs a, int num_sms, cudaStream_t s) {
-    // more tokens than a launch takes: several
+    // several launches of as many tokens each as one takes: 64, or what a cluster's
+    // shared memory has room for
     const size_t ob = a.odt == 0 ? 4 : 2;
     const int M = a.M;
-    // (where the x of sixteen does not fit in a cluster's shared memory: eight)
-    const int step = (size_t)((a.K + 8 * kCh - 1) / (8 * kCh)) * 256 * 16 > kSmemMax - 64 * 1024 ? 8 : 16;
+    int most = 64;
+    while (most > 8 && (size_t)((a.K + 8 * kCh - 1) / (8 * kCh)) * 256 * most > kSmemMax - 64 * 1024) most /= 2;
+    const int blocks = (M + most - 1) / most, step = ((M + blocks - 1) / blocks + 7) / 8 * 8;
     for (int m = 0; m < M; m += step) {
         LinearArgs b = a;
         b.M = std::min(step, M - m);
         b.x = static_cast<const uint8_t*>(a.x) + (size_t)m * a.K * 2;
         b.out = static_cast<uint8_t*>(a.out) + (size_t)m * a.N * ob;
-        const cudaError_t e = b.M <= 8 ? launch_few<G, 1>(b, num_sms, s) : launch_few<G, 2>(b, num_sms, s);
+        const cudaError_t e = b.M <= 8    ? launch_few<G, 1>(b, num_sms, s)
+                              : b.M <= 16 ? launch_few<G, 2>(b, num_sms, s)
+                              : b.M <= 32 ? launch_few<G, 4>(b, num_sms, s)
+                                          : launch_few<G, 8>(b, num_sms, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -475,6 +578,28 @@ cudaError_t repack_linear(int group, const uint8_t* w, const void* scale, const 
         case 128: repack_linear_kernel<128><<<grid, 256, 0, s>>>(w, sc, zero, N, K, Kc, items, out); break;
         default: return cudaErrorInvalidValue;
     }
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_linear_images(int group, const uint8_t* w, size_t w_bytes, const float* factors, int N, int K, int n0,
+                                 int rows, uint8_t* img, size_t img_bytes, cudaStream_t s) {
+    const int Kc = (K + kCh - 1) / kCh, KS = (K + 63) / 64, Nt = (N + 15) / 16;
+    const long recs = (long)(rows / 16) * Kc;
+    const unsigned grid = (unsigned)std::min<long>((recs + 7) / 8, 1 << 20);
+    switch (group) {
+        case 16: linear_images_kernel<16><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, img, img_bytes); break;
+        case 32: linear_images_kernel<32><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, img, img_bytes); break;
+        case 64: linear_images_kernel<64><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, img, img_bytes); break;
+        case 128: linear_images_kernel<128><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, img, img_bytes); break;
+        default: return cudaErrorInvalidValue;
+    }
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_linear_factors(int group, const void* scale, int N, int K, float c, float* factors, int padded,
+                                  cudaStream_t s) {
+    linear_factors_kernel<<<(unsigned)std::min((padded + 7) / 8, 65535), 256, 0, s>>>(
+        group == 16 ? nullptr : static_cast<const __half*>(scale), K / group, N, c, factors, padded);
     return cudaPeekAtLastError();
 }
 
