@@ -30,7 +30,7 @@ struct qmlp_linear_s {
     void* a16 = nullptr;       // fp16 [max_M, K]: bf16 tokens times a power of two each
     int* sig = nullptr;        // [max_M]
     float* ws = nullptr;       // shares of split tiles
-    int* err = nullptr;
+    int* err = nullptr;        // device error word
     Owner mem;
 };
 
@@ -286,6 +286,8 @@ qmlp_status qmlp_linear_create(qmlp_linear_t** out, const qmlp_linear_desc* d, q
         const void* sc = stage(d->scale, groups * (nv ? 1 : 2));
         const void* z = stage(d->zero, groups);
         if (e == cudaSuccess) e = h->mem.alloc(reinterpret_cast<void**>(&h->w), h->w_bytes);
+        if (e == cudaSuccess) e = h->mem.alloc(reinterpret_cast<void**>(&h->err), 16);
+        if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 16, s);
         if (e == cudaSuccess && d->bias) {
             e = h->mem.alloc(reinterpret_cast<void**>(&h->bias), rows * 4);
             if (e == cudaSuccess) e = cudaMemcpyAsync(h->bias, d->bias, rows * 4, cudaMemcpyDefault, s);
@@ -297,13 +299,11 @@ qmlp_status qmlp_linear_create(qmlp_linear_t** out, const qmlp_linear_desc* d, q
             const int padded = (d->N + 255) / 256 * 256, Kp = (d->K + 63) / 64 * 64;
             h->slab = (int)std::max<size_t>(256, std::min<size_t>(padded, kLinearImages / (2 * (size_t)Kp) / 256 * 256));
             h->img_bytes = gemm_decoded_bytes(h->slab, Kp);
-            const size_t need[6] = {(size_t)padded * 4, h->img_bytes, (size_t)d->max_M * d->K * 2, (size_t)d->max_M * 4,
-                                    gemm_splitk_ws_elems(sms) * 4, 16};
-            void** dst[6] = {reinterpret_cast<void**>(&h->factors), reinterpret_cast<void**>(&h->img), &h->a16,
-                             reinterpret_cast<void**>(&h->sig), reinterpret_cast<void**>(&h->ws),
-                             reinterpret_cast<void**>(&h->err)};
-            for (int i = 0; i < 6 && e == cudaSuccess; ++i) e = h->mem.alloc(dst[i], need[i]);
-            if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 16, s);
+            const size_t need[5] = {(size_t)padded * 4, h->img_bytes, (size_t)d->max_M * d->K * 2, (size_t)d->max_M * 4,
+                                    gemm_splitk_ws_elems(sms) * 4};
+            void** dst[5] = {reinterpret_cast<void**>(&h->factors), reinterpret_cast<void**>(&h->img), &h->a16,
+                             reinterpret_cast<void**>(&h->sig), reinterpret_cast<void**>(&h->ws)};
+            for (int i = 0; i < 5 && e == cudaSuccess; ++i) e = h->mem.alloc(dst[i], need[i]);
             if (e == cudaSuccess) e = launch_linear_factors(d->group, sc, d->N, d->K, h->factor, h->factors, padded, s);
         }
         const cudaError_t e2 = cudaStreamSynchronize(s);
@@ -345,6 +345,7 @@ qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt,
     a.x_bf16 = xdt == QMLP_DT_BF16;
     a.out = out;
     a.odt = dt_code(odt);
+    a.err = h->err;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (M < kLinearGemmM || !h->img) return from_cuda(launch_linear(h->group, a, h->num_sms, s));
     // many tokens: the weights decoded once into stage images, rows of W in slabs

@@ -393,6 +393,7 @@ struct LinearArgs {
     bool x_bf16 = true;
     void* out = nullptr;          // [M, N]
     int odt = 0;                  // 0 fp32, 1 bf16, 2 fp16
+    int* err = nullptr;           // device error word
 };
 cudaError_t launch_linear(int group, const LinearArgs& a, int num_sms, cudaStream_t s);
 // Stage images of the tensor-core GEMM (fp16, rows times 2^-exponent of their factor)

@@ -18,10 +18,14 @@
 //    multiplied out and all of k summed by the MMAs. INT4: code - zero is an
 //    integer, exact in fp16; a group's sum is taken by itself and multiplied by
 //    its scale in fp32, so no weight is ever rounded.
-//  * A CTA takes 16 rows at a time, its eight warps an eighth of its k each; the
-//    warps' sums are added in their order. A cluster of up to eight CTAs splits k
-//    where x would not fit in shared memory or the rows are too few for the GPU;
-//    its CTAs add their sums through distributed shared memory, in their order.
+//  * A producer warp keeps a ring of records in shared memory full with bulk copies
+//    (loads into registers, two records a warp, ran at one record's latency after
+//    the other: 4.2 TB/s at 128000 x 5120). Its CTA's warps each take a record of the
+//    ring at a time: a tile of 16 rows to several warps that share its k and whose
+//    sums are added in their order, or a warp a tile.
+//  * A cluster of up to eight CTAs splits k where x would not fit in shared memory or
+//    the rows are too few for the GPU; its CTAs add their sums through distributed
+//    shared memory, in their order.
 #include <algorithm>
 
 #include "common.cuh"
@@ -31,10 +35,10 @@ namespace qmlp {
 namespace {
 
 constexpr int kCh = kLinearChunk;   // k of a record
-constexpr int kW = 8;               // warps of a CTA
-constexpr int kD = 2;               // records a warp has in flight
-constexpr int kXBytes = 48 * 1024;  // shared memory that a CTA should spend on x at most
-constexpr int kSmemMax = 220 * 1024;
+constexpr int kPitch = 20;          // rows of a column of the warps' sums, padded
+constexpr int kSmemMax = 226 * 1024;
+constexpr int kMaxStages = 16;
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s
 
 // Kinds of weights: NVFP4 (group 16) or INT4 with its group.
 template <int G>
@@ -47,104 +51,134 @@ struct Rec {
     static_assert(kBytes % 16 == 0 && kBytes == linear_rec_bytes(G), "records of whole 16 bytes");
 };
 
-// A lane's part of a record: codes of rows g and g + 8, and their scales.
+// A lane's part of a record: codes of rows g and g + 8, and their scales and zeros,
+// which lie together for the two rows: [8 g][2 rows][kPer].
 template <int G>
 struct Frag {
     uint4 c[2];
-    uint32_t s[2][G >= 64 ? 1 : 2];  // NVFP4: 8 E4M3; INT4: the groups' fp16 scales
-    uint32_t z[2];                   // INT4: the groups' zeros, a byte each
+    uint32_t s[2][G >= 64 ? 1 : 2];  // NVFP4: 8 E4M3; INT4: the groups' fp16 scales (G = 128: both rows in s[0])
+    uint32_t z[2];                   // INT4: the groups' zeros, a byte each (G >= 64: both rows in z[0])
 };
+QMLP_DEV uint4 lds4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+QMLP_DEV uint2 lds2(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+QMLP_DEV uint32_t lds1(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+    return v;
+}
+QMLP_DEV uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+    return v;
+}
+// at: the lane's codes of row g; sc: its g's scales, ze: zeros (shared memory).
 template <int G>
-QMLP_DEV void load_frag(Frag<G>& f, const uint8_t* rec, int lane) {
-    using R = Rec<G>;
-    const int g = lane >> 2;
-    f.c[0] = ldg_stream_u4(reinterpret_cast<const uint4*>(rec) + lane);
-    f.c[1] = ldg_stream_u4(reinterpret_cast<const uint4*>(rec + 512) + lane);
-    const uint8_t* sc = rec + 1024;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int row = g + 8 * h;
-        if constexpr (G <= 32) {
-            const uint2 v = ldg_stream_u2(reinterpret_cast<const uint2*>(sc) + row);
-            f.s[h][0] = v.x;
-            f.s[h][1] = v.y;
-        } else if constexpr (G == 64) {
-            f.s[h][0] = __ldg(reinterpret_cast<const unsigned int*>(sc) + row);
-        } else {
-            f.s[h][0] = __ldg(reinterpret_cast<const unsigned short*>(sc) + row);
+QMLP_DEV void load_frag(Frag<G>& f, uint32_t at, uint32_t sc, uint32_t ze) {
+    f.c[0] = lds4(at);
+    f.c[1] = lds4(at + 512);
+    if constexpr (G <= 32) {
+        const uint4 v = lds4(sc);
+        f.s[0][0] = v.x, f.s[0][1] = v.y, f.s[1][0] = v.z, f.s[1][1] = v.w;
+        if constexpr (G == 32) {
+            const uint2 z = lds2(ze);
+            f.z[0] = z.x, f.z[1] = z.y;
         }
-        if constexpr (G == 32) f.z[h] = __ldg(reinterpret_cast<const unsigned int*>(sc + R::kScales) + row);
-        else if constexpr (G == 64) f.z[h] = __ldg(reinterpret_cast<const unsigned short*>(sc + R::kScales) + row);
-        else if constexpr (G == 128) f.z[h] = __ldg(sc + R::kScales + row);
+    } else if constexpr (G == 64) {
+        const uint2 v = lds2(sc);
+        f.s[0][0] = v.x, f.s[1][0] = v.y;
+        f.z[0] = lds1(ze);
+    } else {
+        f.s[0][0] = lds1(sc);
+        f.z[0] = lds16(ze);
     }
+}
+// fp16 scale of row half h and group q, in place 0 or 1 of its word.
+template <int G>
+QMLP_DEV __half scale_of(const Frag<G>& f, int h, int q) {
+    const uint32_t w = G == 128 ? f.s[0][0] : f.s[h][q >> 1];
+    const __half2 p = *reinterpret_cast<const __half2*>(&w);
+    return (G == 128 ? h : q & 1) ? __high2half(p) : __low2half(p);
 }
 
 QMLP_DEV uint32_t word_of(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-QMLP_DEV uint32_t hfma2u(uint32_t a, uint32_t b, uint32_t c) {
-    uint32_t d;
-    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
-}
-QMLP_DEV uint32_t hadd2u(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
-// Zero of group i (byte i of z) as {-(1024 + z)} twice: 0xE400 is -1024, whose last
-// place is one.
+QMLP_DEV __half2 h2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+QMLP_DEV uint32_t u2(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+// Byte i of z as {-(1024 + z)} twice: 0xE400 is -1024, whose last place is one.
 QMLP_DEV uint32_t zero2(uint32_t z, int i) { return __byte_perm(z, 0xE4E4E4E4u, 0x4040u | (uint32_t)(i | i << 8)); }
+template <int G>
+QMLP_DEV uint32_t zero_of(const Frag<G>& f, int h, int q) {
+    return G == 32 ? zero2(f.z[h], q) : zero2(f.z[0], G == 64 ? 2 * h + q : h);
+}
 // Eight codes (two steps of a row) less their zero: nibbles p and p + 4 of the word
 // are pair p; 0x6400 | q is 1024 + q, 0x6400 | 16 q is 1024 + 16 q; both steps exact.
-QMLP_DEV void int4x8(uint32_t w, uint32_t z1, uint32_t z16, uint32_t (&p)[4]) {
+// z1 = -(1024 + z), z16 = -(64 + z).
+QMLP_DEV void int4x8(uint32_t w, __half2 z1, __half2 z16, uint32_t (&p)[4]) {
     const uint32_t v = w >> 8;
-    p[0] = hadd2u((w & 0x000F000Fu) | 0x64006400u, z1);
-    p[1] = hfma2u((w & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, z16);
-    p[2] = hadd2u((v & 0x000F000Fu) | 0x64006400u, z1);
-    p[3] = hfma2u((v & 0x00F000F0u) | 0x64006400u, 0x2C002C00u, z16);
+    const __half2 six = h2(0x2C002C00u);  // 1/16
+    p[0] = u2(__hadd2(h2((w & 0x000F000Fu) | 0x64006400u), z1));
+    p[1] = u2(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), six, z16));
+    p[2] = u2(__hadd2(h2((v & 0x000F000Fu) | 0x64006400u), z1));
+    p[3] = u2(__hfma2(h2((v & 0x00F000F0u) | 0x64006400u), six, z16));
+}
+// Eight E2M1 codes (two steps of a row) times the E4M3 scales of their two groups
+// (sp, as fp16): pair p is byte p of the word.
+QMLP_DEV void e2m1x8(uint32_t w, __half2 sp, uint32_t (&p)[4]) {
+    e2m1x4_to_f16x2x4(w, p[0], p[1], p[2], p[3]);
+    const __half2 lo = __low2half2(sp), hi = __high2half2(sp);
+    p[0] = u2(__hmul2(h2(p[0]), lo));
+    p[1] = u2(__hmul2(h2(p[1]), lo));
+    p[2] = u2(__hmul2(h2(p[2]), hi));
+    p[3] = u2(__hmul2(h2(p[3]), hi));
 }
 
-// One record times NT tiles of eight tokens. xb: this lane's x of the record, a
-// uint4 a pair of steps and tile, `xs` apart (tiles: their own pointers).
+// One record times NT tiles of eight tokens. xb: the record's x in shared memory, xn
+// this lane's place in it for each tile, 16 bytes a pair of steps, `xs` apart. With one tile
+// the steps go to two accumulators in turn: a warp's MMAs would
+// otherwise wait for one another.
+template <int NT>
+constexpr int chains() { return NT == 1 ? 2 : 1; }
 template <int G, int NT>
-QMLP_DEV void mma_record(const Frag<G>& f, const uint4* const (&xb)[NT], int xs, float (&acc)[NT][4]) {
+QMLP_DEV void mma_record(const Frag<G>& f, uint32_t xb, uint32_t xs, const uint32_t (&xn)[NT],
+                         float (&acc)[chains<NT>()][NT][4]) {
     using R = Rec<G>;
+    constexpr int kO = chains<NT>() - 1;
     if constexpr (R::kNv) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // two steps: groups 2i and 2i + 1 of both rows
             uint32_t a[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                e2m1x4_to_f16x2x4(word_of(f.c[h], i), a[h][0], a[h][1], a[h][2], a[h][3]);
-                const uint32_t sp = e4m3x2_to_f16x2((f.s[h][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-                const uint32_t lo = dup_lo16(sp), hi = dup_hi16(sp);
-                a[h][0] = hmul2_u32(a[h][0], lo);
-                a[h][1] = hmul2_u32(a[h][1], lo);
-                a[h][2] = hmul2_u32(a[h][2], hi);
-                a[h][3] = hmul2_u32(a[h][3], hi);
+                uint32_t s01, s23;
+                e4m3x4_to_f16x2x2(f.s[h][i >> 1], s01, s23);
+                e2m1x8(word_of(f.c[h], i), h2((i & 1) ? s23 : s01), a[h]);
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const uint4 x = xb[n][i * xs];
-                mma_f16_16816(acc[n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                mma_f16_16816(acc[n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                const uint4 x = lds4(xb + xn[n] + i * xs);
+                mma_f16_16816(acc[0][n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                mma_f16_16816(acc[kO][n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
             }
         }
     } else {
 #pragma unroll
         for (int q = 0; q < R::kPer; ++q) {
-            uint32_t z1[2], z16[2];
+            __half2 z1[2], z16[2];
             float s[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                z1[h] = zero2(f.z[h], q);
-                z16[h] = hadd2u(z1[h], 0x63806380u);  // -(1024 + z) + 960 = -(64 + z)
-                s[h] = __half2float(__ushort_as_half((unsigned short)(f.s[h][q >> 1] >> (16 * (q & 1)))));
+                z1[h] = h2(zero_of<G>(f, h, q));
+                z16[h] = __hadd2(z1[h], h2(0x63806380u));  // -(1024 + z) + 960
+                s[h] = __half2float(scale_of<G>(f, h, q));
             }
-            float d[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+            float d[chains<NT>()][NT][4];
 #pragma unroll
             for (int i = q * (4 / R::kPer); i < (q + 1) * (4 / R::kPer); ++i) {
                 uint32_t a[2][4];
@@ -152,18 +186,19 @@ QMLP_DEV void mma_record(const Frag<G>& f, const uint4* const (&xb)[NT], int xs,
                 for (int h = 0; h < 2; ++h) int4x8(word_of(f.c[h], i), z1[h], z16[h], a[h]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const uint4 x = xb[n][i * xs];
-                    mma_f16_16816(d[n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                    mma_f16_16816(d[n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                    const uint4 x = lds4(xb + xn[n] + i * xs);
+                    const bool first = i == q * (4 / R::kPer);
+                    if (first) mma_f16_16816_zc(d[0][n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                    else mma_f16_16816(d[0][n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                    if (first && kO > 0) mma_f16_16816_zc(d[kO][n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                    else mma_f16_16816(d[kO][n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(s[0], d[n][0], acc[n][0]);
-                acc[n][1] = fmaf(s[0], d[n][1], acc[n][1]);
-                acc[n][2] = fmaf(s[1], d[n][2], acc[n][2]);
-                acc[n][3] = fmaf(s[1], d[n][3], acc[n][3]);
-            }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[0][n][e] = fmaf(s[e >> 1], kO ? d[0][n][e] + d[kO][n][e] : d[0][n][e], acc[0][n][e]);
         }
     }
 }
@@ -171,14 +206,44 @@ QMLP_DEV void mma_record(const Frag<G>& f, const uint4* const (&xb)[NT], int xs,
 QMLP_DEV void lin_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-QMLP_DEV float peer_f32(const float* p, int rank) {
+QMLP_DEV void peer_arrive(uint32_t bar, uint32_t rank) {
     uint32_t ra;
-    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(bar), "r"(rank));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(ra) : "memory");
+}
+// Bounded wait for a phase of a barrier that CTAs of the cluster arrive on.
+QMLP_DEV bool wait_peers(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+    auto once = [&] {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    if (once()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!once())
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    return true;
+}
+QMLP_DEV float4 peer_f4(const float* p, int rank) {
+    uint32_t ra;
+    float4 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra) : "memory");
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(ra));
     return v;
 }
-
+QMLP_DEV void add4(float4& a, const float4& b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
 QMLP_DEV int peer_s32(const int* p, int rank) {
     uint32_t ra;
     int v;
@@ -187,81 +252,174 @@ QMLP_DEV int peer_s32(const int* p, int rank) {
     return v;
 }
 
-QMLP_DEV void store_out(const LinearArgs& a, int m, int n, float v) {
+// Output n of token m from its sum, which is times 2^sig.
+QMLP_DEV void store1(const LinearArgs& a, int m, int n, float s, int sig) {
+    const float p0 = __int_as_float((127 - (sig >> 1)) << 23), p1 = __int_as_float((127 - sig + (sig >> 1)) << 23);
     const size_t at = (size_t)m * a.N + n;
-    if (!QMLP_INB(at, (size_t)a.M * a.N, 92)) return;
+    if (n >= a.N || !QMLP_INB(at, (size_t)a.M * a.N, 92)) return;
+    float v = s * p0 * p1 * a.factor;
     if (a.bias) v += __ldg(a.bias + n);
     if (a.odt == 0) static_cast<float*>(a.out)[at] = v;
     else if (a.odt == 1) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
     else static_cast<__half*>(a.out)[at] = __float2half_rn(v);
 }
+// Outputs n..n + 3.
+QMLP_DEV void store4(const LinearArgs& a, int m, int n, const float4& s, int sig) {
+    const float p0 = __int_as_float((127 - (sig >> 1)) << 23), p1 = __int_as_float((127 - sig + (sig >> 1)) << 23);
+    float v[4] = {s.x, s.y, s.z, s.w};
+    const size_t at = (size_t)m * a.N + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        v[e] = v[e] * p0 * p1 * a.factor;
+        if (a.bias && n + e < a.N) v[e] += __ldg(a.bias + n + e);
+    }
+    if (n + 3 < a.N && (a.N & 3) == 0) {
+        if (!QMLP_INB(at + 3, (size_t)a.M * a.N, 92)) return;
+        if (a.odt == 0) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else if (a.odt == 1) {
+            __nv_bfloat162 p[2] = {__floats2bfloat162_rn(v[0], v[1]), __floats2bfloat162_rn(v[2], v[3])};
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) = *reinterpret_cast<const uint2*>(p);
+        } else {
+            __half2 p[2] = {__floats2half2_rn(v[0], v[1]), __floats2half2_rn(v[2], v[3])};
+            *reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + at) = *reinterpret_cast<const uint2*>(p);
+        }
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (n + e >= a.N || !QMLP_INB(at + e, (size_t)a.M * a.N, 92)) continue;
+        if (a.odt == 0) static_cast<float*>(a.out)[at + e] = v[e];
+        else if (a.odt == 1) static_cast<__nv_bfloat16*>(a.out)[at + e] = __float2bfloat16_rn(v[e]);
+        else static_cast<__half*>(a.out)[at + e] = __float2half_rn(v[e]);
+    }
+}
 
-// Grid (splits, CTAs of a split), cluster (splits, 1). Shared memory: x, the
-// warps' sums (two buffers), this CTA's sums of its tiles where k is split.
-// Buffers of the warps' sums: with two, one barrier a tile is enough.
+// How a launch of the few-token kernel is cut.
+struct FewPlan {
+    int S;        // CTAs of a cluster: splits of k
+    int wpt;      // warps that share a tile of 16 rows (its k), W / wpt tiles a group
+    int gy;       // clusters
+    int stages;   // ring stages of W records
+    int batch;    // groups whose sums wait in shared memory (S > 1)
+};
+// Consumer warps of a CTA, and CTAs an SM. Measured at ... see launch_few.
 template <int NT>
-constexpr int red_bufs() { return NT <= 2 ? 2 : 1; }
+constexpr int few_warps() { return NT == 4 ? 16 : 8; }
 template <int NT>
-constexpr int few_ctas() { return NT == 1 ? 3 : NT == 8 ? 1 : 2; }
+constexpr int few_ctas() { return NT <= 2 ? 2 : 1; }
+template <int NT>
+constexpr int red_bufs() { return NT <= 2 ? 2 : 1; }  // with two, one barrier a group is enough
 
+// Grid (S, gy), clusters of S. A producer warp copies the groups' records into a
+// ring in shared memory (bulk copies: the weights do not depend on anything before
+// this launch, so they start at once), W warps consume them. Shared memory: x, the
+// ring, the warps' sums, this CTA's sums of a batch of groups where k is split.
 template <int G, int NT>
-__global__ void __launch_bounds__(kW * 32, few_ctas<NT>()) linear_few_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
+    linear_few_kernel(const LinearArgs a, const FewPlan P) {
     using R = Rec<G>;
-    constexpr int kC = 8 * NT;  // columns
-    extern __shared__ __align__(16) uint4 xsm[];
+    constexpr int kC = 8 * NT, W = few_warps<NT>(), kT = W * 32, kRec = R::kBytes, kStage = W * kRec;
+    extern __shared__ __align__(128) uint8_t few_sm[];
     __shared__ int s_max[kC], s_sig[kC];
-    const int S = gridDim.x, rank = blockIdx.x, M = a.M, K = a.K;
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
+    const int S = P.S, rank = blockIdx.x, M = a.M, K = a.K;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int Kc = (K + kCh - 1) / kCh, Nt = (a.N + 15) / 16;
     const int cps = (Kc + S - 1) / S;                     // records of k a CTA
     const int kc0 = rank * cps, nch = min(cps, Kc - kc0);  // this one's
-    const int cpw = (cps + kW - 1) / kW;
-    const int c0 = warp * cpw, cw = max(0, min(cpw, nch - c0));  // this warp's
-    float* red = reinterpret_cast<float*>(xsm + (size_t)cps * 16 * M);  // [buffers][kW][16][kC]
-    float* own = red + red_bufs<NT>() * kW * 16 * kC;                   // [tiles][16][kC]
-    const int tiles = (Nt - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y;
-
-    // the first records are on their way before anything else
-    const uint8_t* base = a.w + (size_t)(kc0 + c0) * R::kBytes;
-    const size_t tile_bytes = (size_t)Kc * R::kBytes, hop = tile_bytes * gridDim.y;
-    const uint8_t* next = base + (size_t)blockIdx.y * tile_bytes;  // record that is loaded next
-    int nc = 0, nt = 0;                                            // its place in the slice, its tile
-    auto fetch = [&](Frag<G>& f) {
-        if (nt < tiles) {
-            if (QMLP_INB(next - a.w + R::kBytes - 1, a.w_bytes, 91)) load_frag<G>(f, next, lane);
-            next += R::kBytes;
-            if (++nc == cw) {
-                nc = 0;
-                ++nt;
-                next += hop - (size_t)cw * R::kBytes;
-            }
+    const int wpt = P.wpt, TG = W / wpt, groups = (Nt + TG - 1) / TG, steps = (cps + wpt - 1) / wpt;
+    uint4* xsm = reinterpret_cast<uint4*>(few_sm);
+    uint8_t* ring = few_sm + (size_t)cps * 256 * M;
+    float* red = reinterpret_cast<float*>(ring + (size_t)P.stages * kStage);     // [buffers][W][kC][kPitch], wpt > 1
+    float* own = red + (wpt > 1 ? red_bufs<NT>() * W * kC * kPitch : 0);           // [batch][TG][kC][16], S > 1
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    const uint32_t peers = bar0 + 8u * (2 * kMaxStages);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < P.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), W);
         }
-    };
-    Frag<G> fr[kD];
-    if (cw > 0)
-#pragma unroll
-        for (int d = 0; d < kD; ++d) fetch(fr[d]);
+        mbar_init(peers, (uint32_t)S);
+        fence_mbar_init();
+    }
+    if (threadIdx.x < kC) s_max[threadIdx.x] = s_sig[threadIdx.x] = 0;
+    if (S > 1) lin_cluster_sync();  // the peers' barriers are there
+    else __syncthreads();
+    pdl_launch_dependents();
 
-    // x of this CTA's k, in the order of the steps: slot ((c 4 + i) M + m) 4 + t has
+    if (warp == W) {
+        // ---------------- producer ----------------
+        if (lane == 0) {
+            int it = 0;
+            bool ok = true;
+            for (int gr = blockIdx.y; gr < groups && ok; gr += gridDim.y) {
+                const int tiles = min(TG, Nt - gr * TG);
+                const uint8_t* src = a.w + ((size_t)gr * TG * Kc + kc0) * kRec;
+                for (int st = 0; st < steps; ++st, ++it) {
+                    const int s = it % P.stages;
+                    if (it >= P.stages && !mbar_wait_bounded(empty(s), (uint32_t)((it / P.stages - 1) & 1), kWaitNs)) {
+                        atomicExch(a.err, 91);
+                        ok = false;
+                        break;
+                    }
+                    const int n = max(0, min(wpt, nch - st * wpt));
+                    const uint32_t bytes = (uint32_t)(n * kRec);
+                    mbar_arrive_expect_tx(full(s), bytes * tiles);
+                    if (n > 0)
+                        for (int j = 0; j < tiles; ++j) {
+                            const uint8_t* p = src + ((size_t)j * Kc + st * wpt) * kRec;
+                            if (!QMLP_INB(p - a.w + bytes - 1, a.w_bytes, 91)) p = a.w;
+                            bulk_g2s(smem_u32(ring + (size_t)s * kStage + (size_t)j * wpt * kRec), p, bytes, full(s));
+                        }
+                }
+            }
+            // copies still in flight (only after a wait that ran out): wait for each
+            // stage's last one
+            if (!ok)
+                for (int q = it - 1; q >= 0 && q >= it - P.stages; --q)
+                    mbar_wait_bounded(full(q % P.stages), (uint32_t)((q / P.stages) & 1), kWaitNs);
+        }
+        __syncwarp();
+        if (S > 1) lin_cluster_sync();  // see the end
+        return;
+    }
+
+    // ---------------- x ----------------
+    // of this CTA's k, in the order of the steps: slot ((c 4 + i) M + m) 4 + t has
     // k = 128 c + 32 i + 4 t.. (four) and 16 further (four) of token m. A thread
     // stays with one token: its largest value falls out of the copy, and the copy is
-    // scaled in place once the row's exponent is known (M = 1, K = 5120: the kernel
-    // took 10.3 us with a pass over x for the largest value before the copy)
-    constexpr int kMp = NT == 1 ? 8 : 8 * NT;  // (M = 1: all threads on its row)
-    const int mp = NT == 1 && M == 1 ? 1 : kMp;
-    const int k0 = kc0 * kCh, xt = threadIdx.x & 3, xm = (threadIdx.x >> 2) % mp, hop_c = kW * 8 / mp;
-    if (threadIdx.x < kC) s_max[threadIdx.x] = 0;
-    __syncthreads();
+    // scaled in place once the row's exponent is known.
+    pdl_wait();  // x is written, and out may be
+    // What the consumers of the cluster's CTAs wrote to their shared memory is
+    // visible to all of them (the producers have no part in it: they wait for the
+    // consumers, who would wait for them).
+    bool ok = true;
+    int meets = 0;
+    auto meet = [&] {
+        named_bar_sync(1, kT);
+        if ((int)threadIdx.x < S) peer_arrive(peers, threadIdx.x);
+        if (ok && !wait_peers(peers, (uint32_t)(meets & 1), kWaitNs)) {
+            atomicExch(a.err, 93);
+            ok = false;
+        }
+        ++meets;
+        named_bar_sync(1, kT);
+    };
+    const int mp = NT == 1 && M == 1 ? 1 : kC;  // (M = 1: all threads on its row)
+    const int k0 = kc0 * kCh, xt = threadIdx.x & 3, xm = (threadIdx.x >> 2) % mp, hop = kT / 4 / mp;
     if (xm < M) {
         float mx = 0.0f;
         const uint16_t* row = static_cast<const uint16_t*>(a.x) + (size_t)xm * K;
 #pragma unroll 4
-        for (int ci = (threadIdx.x >> 2) / mp; ci < nch * 4; ci += hop_c) {
+        for (int ci = (threadIdx.x >> 2) / mp; ci < nch * 4; ci += hop) {
             const int k = k0 + 32 * ci + 4 * xt;
             uint2 v[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)  // K is a multiple of 16
-                v[h] = k + 16 * h < K ? __ldg(reinterpret_cast<const uint2*>(row + k + 16 * h)) : make_uint2(0, 0);
+                v[h] = k + 16 * h < K ? *reinterpret_cast<const uint2*>(row + k + 16 * h) : make_uint2(0, 0);
             if (a.x_bf16)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -269,103 +427,146 @@ __global__ void __launch_bounds__(kW * 32, few_ctas<NT>()) linear_few_kernel(con
                                          fmaxf(fabsf(__uint_as_float(v[h].y << 16)), fabsf(__uint_as_float(v[h].y & 0xFFFF0000u)))));
             xsm[(ci * M + xm) * 4 + xt] = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
         }
-        if (a.x_bf16) atomicMax(s_max + xm, __float_as_int(mx));
+        if (a.x_bf16) {  // lanes of the same token first
+            const uint32_t on = __activemask();
+            mx = fmaxf(mx, __shfl_xor_sync(on, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(on, mx, 2));
+            if (mp == 1)
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(on, mx, o));
+            if (mp == 1 ? lane == 0 : xt == 0) atomicMax(s_max + xm, __float_as_int(mx));
+        }
     }
     if (a.x_bf16) {
-        if (S > 1) lin_cluster_sync();
-        else __syncthreads();
+        if (S > 1) meet();
+        else named_bar_sync(1, kT);
         if (threadIdx.x < M) {
             int mx = 0;
             for (int r = 0; r < S; ++r) mx = max(mx, S > 1 ? peer_s32(s_max + threadIdx.x, r) : s_max[threadIdx.x]);
             s_sig[threadIdx.x] = prescale_exponent(__int_as_float(mx));
         }
-        __syncthreads();
+        named_bar_sync(1, kT);
         if (xm < M) {
+            // 2^sig in two factors: it may pass fp32's range, they do not
             const int sg = s_sig[xm];
-            for (int ci = (threadIdx.x >> 2) / mp; ci < nch * 4; ci += hop_c) {
+            const float p0 = __int_as_float((127 + (sg >> 1)) << 23), p1 = __int_as_float((127 + sg - (sg >> 1)) << 23);
+            for (int ci = (threadIdx.x >> 2) / mp; ci < nch * 4; ci += hop) {
                 uint4& slot = xsm[(ci * M + xm) * 4 + xt];
                 const uint4 u = slot;
                 uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const __half2 hv = __floats2half2_rn(scalbnf(__uint_as_float(v[j] << 16), sg),
-                                                         scalbnf(__uint_as_float(v[j] & 0xFFFF0000u), sg));
+                    const __half2 hv = __floats2half2_rn(__uint_as_float(v[j] << 16) * p0 * p1,
+                                                         __uint_as_float(v[j] & 0xFFFF0000u) * p0 * p1);
                     v[j] = *reinterpret_cast<const uint32_t*>(&hv);
                 }
                 slot = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
-    } else if (threadIdx.x < M) {
-        s_sig[threadIdx.x] = 0;
     }
-    __syncthreads();
+    named_bar_sync(1, kT);
 
-    const uint4* xw[NT];
+    // ---------------- consumers ----------------
+    const int wi = warp % wpt, wt = warp / wpt;  // place in the tile's k, tile of the group
+    uint32_t xn[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xw[n] = xsm + (size_t)c0 * 16 * M + min(8 * n + g, M - 1) * 4 + t;
-    float acc[NT][4];
+    for (int n = 0; n < NT; ++n) xn[n] = (uint32_t)((min(8 * n + g, M - 1) * 4 + t) * 16);
+    const uint32_t x0 = smem_u32(xsm) + (uint32_t)(wi * 256 * M), xstep = (uint32_t)(wpt * 256 * M), xs = (uint32_t)(64 * M);
+    // this warp's record of the ring's current stage, and that stage's barriers
+    const uint32_t ring0 = smem_u32(ring) + (uint32_t)(warp * kRec), ring_end = ring0 + (uint32_t)(P.stages * kStage);
+    uint32_t slot = ring0, fb = full(0), parity = 0;
+    uint64_t lim = kWaitNs;
+    const int nst = nch > wi ? (nch - wi + wpt - 1) / wpt : 0;  // steps that this warp has a record in
+    int done = 0, b0 = blockIdx.y;  // groups done, the batch's first
+    for (int gr = blockIdx.y; gr < groups; gr += gridDim.y, ++done) {
+        float acc[chains<NT>()][NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+        for (int c = 0; c < chains<NT>(); ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
-    // the warps' sums of a tile -> out, or this CTA's share of it
-    int tile = 0;
-    auto finish = [&] {
-        float* rb = red + (red_bufs<NT>() > 1 ? (tile & 1) * kW * 16 * kC : 0);
-        if (red_bufs<NT>() == 1) __syncthreads();  // the sums of the tile before are read
-        float* mine = rb + warp * 16 * kC;
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            *reinterpret_cast<float2*>(mine + g * kC + 8 * n + 2 * t) = make_float2(acc[n][0], acc[n][1]);
-            *reinterpret_cast<float2*>(mine + (g + 8) * kC + 8 * n + 2 * t) = make_float2(acc[n][2], acc[n][3]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
-        }
-        __syncthreads();
-        const int row = threadIdx.x & 15, j = (int)blockIdx.y + tile * (int)gridDim.y;
-        for (int m = threadIdx.x >> 4; m < M; m += kW * 2) {
-            float v = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kW; ++w) v += rb[(w * 16 + row) * kC + m];
-            if (S > 1) own[(tile * 16 + row) * kC + m] = v;
-            else if (16 * j + row < a.N) store_out(a, m, 16 * j + row, scalbnf(v, -s_sig[m]) * a.factor);
-        }
-        ++tile;
-    };
-    if (cw > 0) {
-        const int total = tiles * cw;
-        int c = 0;
-        for (int i = 0; i < total; i += kD) {
-#pragma unroll
-            for (int d = 0; d < kD; ++d) {
-                if (i + d < total) {
-                    const uint4* xb[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) xb[n] = xw[n] + (size_t)c * 16 * M;
-                    mma_record<G, NT>(fr[d], xb, 4 * M, acc);
-                    fetch(fr[d]);
-                    if (++c == cw) {
-                        c = 0;
-                        finish();
-                    }
-                }
+                for (int e = 0; e < 4; ++e) acc[c][n][e] = 0.0f;
+        const int mst = gr * TG + wt < Nt ? nst : 0;
+        uint32_t xb = x0;
+#pragma unroll 1
+        for (int st = 0; st < steps; ++st, xb += xstep) {
+            if (!mbar_try_wait(fb, parity) && !mbar_wait_bounded(fb, parity, lim)) {
+                atomicExch(a.err, 92);  // (what is then read lies in the ring; out is not valid)
+                lim = 0;
             }
+            Frag<G> f;
+            const bool has = st < mst;
+            if (has) load_frag<G>(f, slot + lane * 16, slot + 1024 + g * (R::kScales / 8), slot + 1024 + R::kScales + g * (R::kZeros / 8));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(fb + 8u * kMaxStages);
+            slot += kStage;
+            fb += 8;
+            if (slot == ring_end) {
+                slot = ring0;
+                fb = full(0);
+                parity ^= 1;
+            }
+            if (has) mma_record<G, NT>(f, xb, xs, xn, acc);
         }
-    } else {
-        while (tile < tiles) finish();
-    }
-    if (S > 1) {
-        lin_cluster_sync();  // every CTA's shares are written
-        const int per = (tiles * 16 * M + S - 1) / S;
-        for (int i = rank * per + threadIdx.x; i < min(tiles * 16 * M, (rank + 1) * per); i += blockDim.x) {
-            const int row = i & 15, m = (i >> 4) % M, tl = (i >> 4) / M;
-            const int n = 16 * ((int)blockIdx.y + tl * (int)gridDim.y) + row;
-            float v = 0.0f;
-            for (int r = 0; r < S; ++r) v += peer_f32(own + (tl * 16 + row) * kC + m, r);
-            if (n < a.N) store_out(a, m, n, scalbnf(v, -s_sig[m]) * a.factor);
+#pragma unroll
+        for (int c = 1; c < chains<NT>(); ++c)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[0][n][e] += acc[c][n][e];
+        float* ob = own + (size_t)(done % P.batch) * TG * kC * 16;
+        if (wpt > 1) {
+            float* rb = red + (red_bufs<NT>() > 1 ? (done & 1) * W * kC * kPitch : 0);
+            if (red_bufs<NT>() == 1) named_bar_sync(1, kT);  // the sums of the group before are read
+            // [warp][column][kPitch rows]: 20 puts the 32 lanes on 32 banks
+            float* mine = rb + warp * kC * kPitch;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[(8 * n + 2 * t + (e & 1)) * kPitch + g + 4 * (e & 2)] = acc[0][n][e];
+            named_bar_sync(1, kT);
+            for (int i = threadIdx.x; i < 4 * M * TG; i += kT) {  // four rows of a token
+                const int r4 = (i & 3) * 4, m = (i >> 2) % M, j = (i >> 2) / M;
+                float4 v = make_float4(0, 0, 0, 0);
+                for (int w = 0; w < wpt; ++w)
+                    add4(v, *reinterpret_cast<const float4*>(rb + ((j * wpt + w) * kC + m) * kPitch + r4));
+                if (S > 1) *reinterpret_cast<float4*>(ob + (j * kC + m) * 16 + r4) = v;
+                else store4(a, m, 16 * (gr * TG + j) + r4, v, s_sig[m]);
+            }
+        } else if (S > 1) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ob[(warp * kC + 8 * n + 2 * t + (e & 1)) * 16 + g + 4 * (e & 2)] = acc[0][n][e];
+        } else {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int m = 8 * n + 2 * t + (e & 1);
+                    if (m < M) store1(a, m, 16 * (gr * TG + warp) + g + 4 * (e & 2), acc[0][n][e], s_sig[m]);
+                }
         }
-        lin_cluster_sync();  // none leaves while another reads its shares
+        // a batch of groups is done: the cluster's sums in order
+        if (S > 1 && ((done + 1) % P.batch == 0 || gr + (int)gridDim.y >= groups)) {
+            meet();  // every CTA's sums are written
+            const int nb = done % P.batch + 1, items = nb * TG * 4 * M, per = (items + S - 1) / S;
+            for (int i = rank * per + threadIdx.x; i < min(items, (rank + 1) * per); i += kT) {
+                const int r4 = (i & 3) * 4, m = (i >> 2) % M, j = (i >> 2) / M;
+                float4 p[8], v = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < S) p[r] = peer_f4(own + ((size_t)j * kC + m) * 16 + r4, r);
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < S) add4(v, p[r]);
+                store4(a, m, 16 * ((b0 + j / TG * (int)gridDim.y) * TG + j % TG) + r4, v, s_sig[m]);
+            }
+            meet();  // none writes its next sums while another reads
+            b0 = gr + gridDim.y;
+        }
     }
+    if (S > 1) lin_cluster_sync();  // no CTA leaves while another may read its sums
 }
 
 // Checkpoint rows -> records (one thread a lane's 16 bytes of a row half, the
@@ -398,17 +599,18 @@ __global__ void __launch_bounds__(256) repack_linear_kernel(const uint8_t* __res
         }
         reinterpret_cast<uint4*>(dst + 512 * h)[lane] = make_uint4(o[0], o[1], o[2], o[3]);
         if (t == 0) {
-            const int r = g + 8 * h, groups = K / G;
+            const int groups = K / G;
             for (int q = 0; q < R::kPer; ++q) {
                 const int gi = kc * R::kPer + q;
                 const bool in = row < (size_t)N && gi < groups;
                 const size_t at = row * groups + gi;
+                const int to = (2 * g + h) * R::kPer + q;
                 if (R::kNv) {
-                    dst[1024 + r * R::kPer + q] = in ? scale[at] : 0;
+                    dst[1024 + to] = in ? scale[at] : 0;
                 } else {
-                    reinterpret_cast<uint16_t*>(dst + 1024)[r * R::kPer + q] =
+                    reinterpret_cast<uint16_t*>(dst + 1024)[to] =
                         in ? reinterpret_cast<const uint16_t*>(scale)[at] : (uint16_t)0;
-                    dst[1024 + R::kScales + r * R::kPer + q] = in ? zero[at] : 0;
+                    dst[1024 + R::kScales + to] = in ? zero[at] : 0;
                 }
             }
         }
@@ -426,10 +628,28 @@ __global__ void __launch_bounds__(256) linear_images_kernel(const uint8_t* __res
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     for (long rec = (long)blockIdx.x * 8 + (threadIdx.x >> 5); rec < recs; rec += (long)gridDim.x * 8) {
         const int kc = (int)(rec % Kc), lt = (int)(rec / Kc), tile = tile0 + lt;  // 16 rows, from the images' first
-        Frag<G> f;
         const bool in = tile < Nt;
         const size_t at = ((size_t)(in ? tile : 0) * Kc + kc) * R::kBytes;
-        if (in && QMLP_INB(at + R::kBytes - 1, w_bytes, 93)) load_frag<G>(f, w + at, lane);
+        uint32_t f[2][4], s[2][G <= 32 ? 2 : 1], z[2] = {0, 0};  // codes; scales and zeros of rows g and g + 8
+        if (!QMLP_INB(at + R::kBytes - 1, w_bytes, 93)) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint4 c = ldg_stream_u4(reinterpret_cast<const uint4*>(w + at + 512 * h) + lane);
+            f[h][0] = c.x, f[h][1] = c.y, f[h][2] = c.z, f[h][3] = c.w;
+            const uint8_t* sp = w + at + 1024 + (2 * g + h) * (R::kScales / 16);
+            const uint8_t* zp = w + at + 1024 + R::kScales + (2 * g + h) * R::kPer;
+            if constexpr (G <= 32) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(sp));
+                s[h][0] = v.x, s[h][1] = v.y;
+                if constexpr (G == 32) z[h] = __ldg(reinterpret_cast<const unsigned int*>(zp));
+            } else if constexpr (G == 64) {
+                s[h][0] = __ldg(reinterpret_cast<const unsigned int*>(sp));
+                z[h] = __ldg(reinterpret_cast<const unsigned short*>(zp));
+            } else {
+                s[h][0] = __ldg(reinterpret_cast<const unsigned short*>(sp));
+                z[h] = __ldg(zp);
+            }
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int row = lt * 16 + g + 8 * h, n = row & 255;
@@ -440,23 +660,19 @@ __global__ void __launch_bounds__(256) linear_images_kernel(const uint8_t* __res
                 uint32_t a[4] = {0, 0, 0, 0};
                 if (in) {
                     if constexpr (R::kNv) {
-                        e2m1x4_to_f16x2x4(word_of(f.c[h], i), a[0], a[1], a[2], a[3]);
-                        const uint32_t sp = e4m3x2_to_f16x2((f.s[h][i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-                        const uint32_t lo = dup_lo16(sp), hi = dup_hi16(sp);
-                        a[0] = hmul2_u32(a[0], lo);
-                        a[1] = hmul2_u32(a[1], lo);
-                        a[2] = hmul2_u32(a[2], hi);
-                        a[3] = hmul2_u32(a[3], hi);
+                        uint32_t s01, s23;
+                        e4m3x4_to_f16x2x2(s[h][i >> 1], s01, s23);
+                        e2m1x8(f[h][i], h2((i & 1) ? s23 : s01), a);
                     } else {
                         const int q = i * R::kPer / 4;
-                        const uint32_t z1 = zero2(f.z[h], q);
-                        int4x8(word_of(f.c[h], i), z1, hadd2u(z1, 0x63806380u), a);
-                        const float s =
-                            rf * __half2float(__ushort_as_half((unsigned short)(f.s[h][q >> 1] >> (16 * (q & 1)))));
+                        const __half2 z1 = h2(zero2(z[h], q));
+                        int4x8(f[h][i], z1, __hadd2(z1, h2(0x63806380u)), a);
+                        const float sc =
+                            rf * __half2float(__ushort_as_half((unsigned short)(s[h][q >> 1] >> (16 * (q & 1)))));
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
                             const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&a[p]));
-                            const __half2 o = __floats2half2_rn(v.x * s, v.y * s);
+                            const __half2 o = __floats2half2_rn(v.x * sc, v.y * sc);
                             a[p] = *reinterpret_cast<const uint32_t*>(&o);
                         }
                     }
@@ -493,27 +709,48 @@ __global__ void __launch_bounds__(256) linear_factors_kernel(const __half* __res
     }
 }
 
+// Bytes of x that one of S CTAs holds for M tokens.
+size_t few_x_bytes(int K, int M, int S) {
+    const int Kc = (K + kCh - 1) / kCh;
+    return (size_t)((Kc + S - 1) / S) * 256 * M;
+}
+
 template <int G, int NT>
 cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
-    constexpr int kC = 8 * NT;
+    constexpr int kC = 8 * NT, W = few_warps<NT>(), kStage = W * Rec<G>::kBytes;
     const int Kc = (a.K + kCh - 1) / kCh, Nt = (a.N + 15) / 16;
-    // k is split where x of one CTA would be too large, then as long as the GPU
-    // has room for twice the CTAs and every warp keeps a record or more
-    int S = 1;
-    auto xbytes = [&](int sp) { return (size_t)((Kc + sp - 1) / sp) * 256 * a.M; };
-    while (S < 8 && (xbytes(S) > kXBytes || ((long)Nt * S * 2 <= 2L * num_sms && Kc >= 2 * S * kW))) S *= 2;
-    while (S > 1 && (S - 1) * ((Kc + S - 1) / S) >= Kc) S /= 2;  // every CTA has some of k
-    if (xbytes(S) > kSmemMax - 64 * 1024) return cudaErrorInvalidValue;
-    // as many CTAs as fit at once, each on an even share of the tiles
-    const size_t fixed = xbytes(S) + red_bufs<NT>() * kW * 16 * kC * sizeof(float);
-    const int fit = (int)std::max<size_t>(1, std::min<size_t>(few_ctas<NT>(), kSmemMax / (fixed + 2048)));
-    int gy = std::max(1, std::min(Nt, num_sms * fit / S));
-    int tiles = (Nt + gy - 1) / gy;
-    // a split's sums of all its tiles wait in shared memory
-    const int most = (int)((kSmemMax / fit - fixed) / (16 * kC * sizeof(float)));
-    if (S > 1 && tiles > most) tiles = std::max(1, most);
-    gy = (Nt + tiles - 1) / tiles;
-    const size_t smem = fixed + (S > 1 ? (size_t)tiles * 16 * kC * sizeof(float) : 0);
+    FewPlan P;
+    // k is split where x would take more than its part of shared memory, and while
+    // the GPU has room for twice the CTAs and a warp keeps two records or more
+    const size_t xmost = kSmemMax / few_ctas<NT>() * 2 / 5;
+    P.S = 1;
+    auto tile_groups = [&](int wpt) { return (Nt + W / wpt - 1) / (W / wpt); };
+    while (P.S < 8 && few_x_bytes(a.K, a.M, P.S) > xmost) P.S *= 2;
+    // a tile's k is shared by as many warps as leave enough groups for the GPU
+    P.wpt = NT <= 2 ? W : 1;
+    while (P.wpt > 1 && ((Kc + P.S - 1) / P.S < 2 * P.wpt || tile_groups(P.wpt / 2) * P.S >= 8 * num_sms)) P.wpt /= 2;
+    while (P.S < 8 && tile_groups(P.wpt) * P.S * 2 <= num_sms * few_ctas<NT>() && Kc >= 4 * P.S * P.wpt) P.S *= 2;
+    while (P.S > 1 && (P.S - 1) * ((Kc + P.S - 1) / P.S) >= Kc) P.S /= 2;  // every CTA has some of k
+    const int TG = W / P.wpt, groups = tile_groups(P.wpt);
+    const size_t x = few_x_bytes(a.K, a.M, P.S);
+    const size_t red = P.wpt > 1 ? (size_t)red_bufs<NT>() * W * kC * kPitch * 4 : 0;
+    const size_t group_own = P.S > 1 ? (size_t)TG * kC * 16 * 4 : 0;
+    const size_t room = kSmemMax / few_ctas<NT>() - 2048;
+    if (x + red + group_own + 2 * kStage > kSmemMax - 2048) return cudaErrorInvalidValue;
+    const bool one = x + red + group_own + 3 * kStage > room;  // one CTA an SM then
+    const size_t all = one ? kSmemMax - 2048 : room;
+    const int fit = one ? 1 : few_ctas<NT>();
+    P.gy = std::max(1, std::min(groups, num_sms * fit / P.S));
+    const int mine = (groups + P.gy - 1) / P.gy;
+    P.gy = (groups + mine - 1) / mine;
+    P.batch = 1;
+    if (P.S > 1) {  // a quarter of what is left for the sums that wait
+        const size_t left = all - x - red - 2 * kStage;
+        P.batch = (int)std::max<size_t>(1, std::min<size_t>(mine, left / 4 / group_own));
+    }
+    const size_t fixed = x + red + group_own * P.batch;
+    P.stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(2, (all - fixed) / kStage));
+    const size_t smem = fixed + (size_t)P.stages * kStage;
     static bool attr = false;
     if (!attr) {
         const cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -522,18 +759,20 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
         attr = true;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)S, (unsigned)gy);
-    cfg.blockDim = dim3(kW * 32);
+    cfg.gridDim = dim3((unsigned)P.S, (unsigned)P.gy);
+    cfg.blockDim = dim3((W + 1) * 32);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)S;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)P.S;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = S > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, linear_few_kernel<G, NT>, a);
+    cfg.numAttrs = P.S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, linear_few_kernel<G, NT>, a, P);
 }
 
 template <int G>
@@ -543,7 +782,8 @@ cudaError_t launch_g(LinearArgs a, int num_sms, cudaStream_t s) {
     const size_t ob = a.odt == 0 ? 4 : 2;
     const int M = a.M;
     int most = 64;
-    while (most > 8 && (size_t)((a.K + 8 * kCh - 1) / (8 * kCh)) * 256 * most > kSmemMax - 64 * 1024) most /= 2;
+    // (the ring, and a group's sums of 64 tokens, need 100 KB at most)
+    while (most > 8 && few_x_bytes(a.K, most, 8) > kSmemMax - 104 * 1024) most /= 2;
     const int blocks = (M + most - 1) / most, step = ((M + blocks - 1) / blocks + 7) / 8 * 8;
     for (int m = 0; m < M; m += step) {
         LinearArgs b = a;
