@@ -31,6 +31,8 @@ struct qmlp_linear_s {
     int* sig = nullptr;        // [max_M]
     float* ws = nullptr;       // shares of split tiles
     int* err = nullptr;        // device error word
+    void* xf = nullptr;        // few tokens: x in the order of the products
+    size_t xf_bytes = 0;
     Owner mem;
 };
 
@@ -288,6 +290,11 @@ qmlp_status qmlp_linear_create(qmlp_linear_t** out, const qmlp_linear_desc* d, q
         if (e == cudaSuccess) e = h->mem.alloc(reinterpret_cast<void**>(&h->w), h->w_bytes);
         if (e == cudaSuccess) e = h->mem.alloc(reinterpret_cast<void**>(&h->err), 16);
         if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, 16, s);
+        if (d->max_M > kLinearFew) {
+            h->xf_bytes = linear_x_bytes(d->K, d->max_M);
+            if (e == cudaSuccess) e = h->mem.alloc(&h->xf, h->xf_bytes);
+            if (e == cudaSuccess) e = h->mem.alloc(reinterpret_cast<void**>(&h->sig), (size_t)d->max_M * 4);
+        }
         if (e == cudaSuccess && d->bias) {
             e = h->mem.alloc(reinterpret_cast<void**>(&h->bias), rows * 4);
             if (e == cudaSuccess) e = cudaMemcpyAsync(h->bias, d->bias, rows * 4, cudaMemcpyDefault, s);
@@ -299,11 +306,11 @@ qmlp_status qmlp_linear_create(qmlp_linear_t** out, const qmlp_linear_desc* d, q
             const int padded = (d->N + 255) / 256 * 256, Kp = (d->K + 63) / 64 * 64;
             h->slab = (int)std::max<size_t>(256, std::min<size_t>(padded, kLinearImages / (2 * (size_t)Kp) / 256 * 256));
             h->img_bytes = gemm_decoded_bytes(h->slab, Kp);
-            const size_t need[5] = {(size_t)padded * 4, h->img_bytes, (size_t)d->max_M * d->K * 2, (size_t)d->max_M * 4,
+            const size_t need[4] = {(size_t)padded * 4, h->img_bytes, (size_t)d->max_M * d->K * 2,
                                     gemm_splitk_ws_elems(sms) * 4};
-            void** dst[5] = {reinterpret_cast<void**>(&h->factors), reinterpret_cast<void**>(&h->img), &h->a16,
-                             reinterpret_cast<void**>(&h->sig), reinterpret_cast<void**>(&h->ws)};
-            for (int i = 0; i < 5 && e == cudaSuccess; ++i) e = h->mem.alloc(dst[i], need[i]);
+            void** dst[4] = {reinterpret_cast<void**>(&h->factors), reinterpret_cast<void**>(&h->img), &h->a16,
+                             reinterpret_cast<void**>(&h->ws)};
+            for (int i = 0; i < 4 && e == cudaSuccess; ++i) e = h->mem.alloc(dst[i], need[i]);
             if (e == cudaSuccess) e = launch_linear_factors(d->group, sc, d->N, d->K, h->factor, h->factors, padded, s);
         }
         const cudaError_t e2 = cudaStreamSynchronize(s);
@@ -346,6 +353,9 @@ qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt,
     a.out = out;
     a.odt = dt_code(odt);
     a.err = h->err;
+    a.xf = h->xf;
+    a.xf_elems = h->xf_bytes / 16;
+    a.sig = h->sig;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (M < kLinearGemmM || !h->img) return from_cuda(launch_linear(h->group, a, h->num_sms, s));
     // many tokens: the weights decoded once into stage images, rows of W in slabs

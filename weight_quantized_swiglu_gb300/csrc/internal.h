@@ -394,7 +394,13 @@ struct LinearArgs {
     void* out = nullptr;          // [M, N]
     int odt = 0;                  // 0 fp32, 1 bf16, 2 fp16
     int* err = nullptr;           // device error word
+    void* xf = nullptr;           // workspace of more than kLinearFew tokens: linear_x_bytes
+    size_t xf_elems = 0;          // its 16-byte pieces
+    int* sig = nullptr;           // [max_M] exponents of the tokens
 };
+constexpr int kLinearFew = 8;   // tokens whose x stays in shared memory
+constexpr int kLinearMid = 64;  // tokens of a launch above
+size_t linear_x_bytes(int K, int M);
 cudaError_t launch_linear(int group, const LinearArgs& a, int num_sms, cudaStream_t s);
 // Stage images of the tensor-core GEMM (fp16, rows times 2^-exponent of their factor)
 // of rows n0.. (a multiple of 256) of the records: N rows padded to 256, K to 64. The

@@ -117,16 +117,22 @@ template <int G>
 QMLP_DEV uint32_t zero_of(const Frag<G>& f, int h, int q) {
     return G == 32 ? zero2(f.z[h], q) : zero2(f.z[0], G == 64 ? 2 * h + q : h);
 }
+// (w & mask) | magic in one instruction (the compiler took two)
+QMLP_DEV uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
+    return d;
+}
 // Eight codes (two steps of a row) less their zero: nibbles p and p + 4 of the word
 // are pair p; 0x6400 | q is 1024 + q, 0x6400 | 16 q is 1024 + 16 q; both steps exact.
 // z1 = -(1024 + z), z16 = -(64 + z).
 QMLP_DEV void int4x8(uint32_t w, __half2 z1, __half2 z16, uint32_t (&p)[4]) {
     const uint32_t v = w >> 8;
     const __half2 six = h2(0x2C002C00u);  // 1/16
-    p[0] = u2(__hadd2(h2((w & 0x000F000Fu) | 0x64006400u), z1));
-    p[1] = u2(__hfma2(h2((w & 0x00F000F0u) | 0x64006400u), six, z16));
-    p[2] = u2(__hadd2(h2((v & 0x000F000Fu) | 0x64006400u), z1));
-    p[3] = u2(__hfma2(h2((v & 0x00F000F0u) | 0x64006400u), six, z16));
+    p[0] = u2(__hadd2(h2(and_or(w, 0x000F000Fu, 0x64006400u)), z1));
+    p[1] = u2(__hfma2(h2(and_or(w, 0x00F000F0u, 0x64006400u)), six, z16));
+    p[2] = u2(__hadd2(h2(and_or(v, 0x000F000Fu, 0x64006400u)), z1));
+    p[3] = u2(__hfma2(h2(and_or(v, 0x00F000F0u, 0x64006400u)), six, z16));
 }
 // Eight E2M1 codes (two steps of a row) times the E4M3 scales of their two groups
 // (sp, as fp16): pair p is byte p of the word.
@@ -139,17 +145,12 @@ QMLP_DEV void e2m1x8(uint32_t w, __half2 sp, uint32_t (&p)[4]) {
     p[3] = u2(__hmul2(h2(p[3]), hi));
 }
 
-// One record times NT tiles of eight tokens. xb: the record's x in shared memory, xn
-// this lane's place in it for each tile, 16 bytes a pair of steps, `xs` apart. With one tile
-// the steps go to two accumulators in turn: a warp's MMAs would
-// otherwise wait for one another.
-template <int NT>
-constexpr int chains() { return NT == 1 ? 2 : 1; }
-template <int G, int NT>
-QMLP_DEV void mma_record(const Frag<G>& f, uint32_t xb, uint32_t xs, const uint32_t (&xn)[NT],
-                         float (&acc)[chains<NT>()][NT][4]) {
+// One record times one tile of eight tokens. xb: this lane's x of the record in shared
+// memory, 16 bytes a pair of steps, `xs` apart. The steps go to two accumulators in
+// turn: a warp's MMAs would otherwise wait for one another.
+template <int G, bool ONE>
+QMLP_DEV void mma_record(const Frag<G>& f, uint32_t xb, uint32_t xs, float (&acc)[2][4]) {
     using R = Rec<G>;
-    constexpr int kO = chains<NT>() - 1;
     if constexpr (R::kNv) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // two steps: groups 2i and 2i + 1 of both rows
@@ -160,12 +161,9 @@ QMLP_DEV void mma_record(const Frag<G>& f, uint32_t xb, uint32_t xs, const uint3
                 e4m3x4_to_f16x2x2(f.s[h][i >> 1], s01, s23);
                 e2m1x8(word_of(f.c[h], i), h2((i & 1) ? s23 : s01), a[h]);
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint4 x = lds4(xb + xn[n] + i * xs);
-                mma_f16_16816(acc[0][n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                mma_f16_16816(acc[kO][n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
-            }
+            const uint4 x = lds4(xb + i * xs);
+            mma_f16_16816(acc[0], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+            mma_f16_16816(acc[1], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
         }
     } else {
 #pragma unroll
@@ -178,27 +176,68 @@ QMLP_DEV void mma_record(const Frag<G>& f, uint32_t xb, uint32_t xs, const uint3
                 z16[h] = __hadd2(z1[h], h2(0x63806380u));  // -(1024 + z) + 960
                 s[h] = __half2float(scale_of<G>(f, h, q));
             }
-            float d[chains<NT>()][NT][4];
+            float d[2][4];
 #pragma unroll
             for (int i = q * (4 / R::kPer); i < (q + 1) * (4 / R::kPer); ++i) {
                 uint32_t a[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) int4x8(word_of(f.c[h], i), z1[h], z16[h], a[h]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const uint4 x = lds4(xb + xn[n] + i * xs);
-                    const bool first = i == q * (4 / R::kPer);
-                    if (first) mma_f16_16816_zc(d[0][n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                    else mma_f16_16816(d[0][n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                    if (first && kO > 0) mma_f16_16816_zc(d[kO][n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
-                    else mma_f16_16816(d[kO][n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                const uint4 x = lds4(xb + i * xs);
+                if (i == q * (4 / R::kPer)) {
+                    mma_f16_16816_zc(d[0], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                    mma_f16_16816_zc(d[1], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                } else {
+                    mma_f16_16816(d[0], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                    mma_f16_16816(d[1], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
                 }
             }
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int e = 0; e < 4; e += ONE ? 2 : 1) acc[0][e] = fmaf(s[e >> 1], d[0][e] + d[1][e], acc[0][e]);
+        }
+    }
+}
+// One record times NT tiles; INT4's sums of 32 k are scaled one by one, which keeps
+// few of them in registers. xn: this lane's place in the record's x (xb) by tile.
+template <int G, int NT>
+QMLP_DEV void mma_record_tiles(const Frag<G>& f, uint32_t xb, uint32_t xs, const uint32_t (&xn)[NT], float (&acc)[NT][4]) {
+    using R = Rec<G>;
+    __half2 z1[2], z16[2];
+    float s[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[0][n][e] = fmaf(s[e >> 1], kO ? d[0][n][e] + d[kO][n][e] : d[0][n][e], acc[0][n][e]);
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a[2][4];
+        if constexpr (R::kNv) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t s01, s23;
+                e4m3x4_to_f16x2x2(f.s[h][i >> 1], s01, s23);
+                e2m1x8(word_of(f.c[h], i), h2((i & 1) ? s23 : s01), a[h]);
+            }
+        } else {
+            if (i % (4 / R::kPer) == 0)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int q = i / (4 / R::kPer);
+                    z1[h] = h2(zero_of<G>(f, h, q));
+                    z16[h] = __hadd2(z1[h], h2(0x63806380u));
+                    s[h] = __half2float(scale_of<G>(f, h, q));
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) int4x8(word_of(f.c[h], i), z1[h], z16[h], a[h]);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const uint4 x = lds4(xb + xn[n] + i * xs);
+            if constexpr (R::kNv) {
+                mma_f16_16816(acc[n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                mma_f16_16816(acc[n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+            } else {
+                float d[4];
+                mma_f16_16816_zc(d, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                mma_f16_16816(d, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] = fmaf(s[e >> 1], d[e], acc[n][e]);
+            }
         }
     }
 }
@@ -244,6 +283,18 @@ QMLP_DEV void add4(float4& a, const float4& b) {
     a.z += b.z;
     a.w += b.w;
 }
+// The sum over the S CTAs of a cluster of what they have at p, in their order.
+QMLP_DEV float4 peer_sum(const float* p, int S) {
+    float4 q[8], v = make_float4(0, 0, 0, 0);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+        if (r < S) q[r] = peer_f4(p, r);
+#pragma unroll
+    for (int r = 0; r < 8; ++r)
+        if (r < S) add4(v, q[r]);
+    return v;
+}
+
 QMLP_DEV int peer_s32(const int* p, int rank) {
     uint32_t ra;
     int v;
@@ -252,18 +303,7 @@ QMLP_DEV int peer_s32(const int* p, int rank) {
     return v;
 }
 
-// Output n of token m from its sum, which is times 2^sig.
-QMLP_DEV void store1(const LinearArgs& a, int m, int n, float s, int sig) {
-    const float p0 = __int_as_float((127 - (sig >> 1)) << 23), p1 = __int_as_float((127 - sig + (sig >> 1)) << 23);
-    const size_t at = (size_t)m * a.N + n;
-    if (n >= a.N || !QMLP_INB(at, (size_t)a.M * a.N, 92)) return;
-    float v = s * p0 * p1 * a.factor;
-    if (a.bias) v += __ldg(a.bias + n);
-    if (a.odt == 0) static_cast<float*>(a.out)[at] = v;
-    else if (a.odt == 1) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(a.out)[at] = __float2half_rn(v);
-}
-// Outputs n..n + 3.
+// Outputs n..n + 3 of token m from their sums, which are times 2^sig.
 QMLP_DEV void store4(const LinearArgs& a, int m, int n, const float4& s, int sig) {
     const float p0 = __int_as_float((127 - (sig >> 1)) << 23), p1 = __int_as_float((127 - sig + (sig >> 1)) << 23);
     float v[4] = {s.x, s.y, s.z, s.w};
@@ -295,35 +335,79 @@ QMLP_DEV void store4(const LinearArgs& a, int m, int n, const float4& s, int sig
     }
 }
 
-// How a launch of the few-token kernel is cut.
-struct FewPlan {
-    int S;        // CTAs of a cluster: splits of k
-    int wpt;      // warps that share a tile of 16 rows (its k), W / wpt tiles a group
-    int gy;       // clusters
-    int stages;   // ring stages of W records
-    int batch;    // groups whose sums wait in shared memory (S > 1)
+// The meeting of the consumers of a cluster's CTAs: what they wrote to their shared
+// memory is visible to all of them behind it (the producers have no part in it: they
+// wait for the consumers, who would wait for them). Bounded.
+struct Peers {
+    uint32_t bar;
+    int S, threads, count;
+    int* err;
+    bool ok;
+    QMLP_DEV void meet() {
+        named_bar_sync(1, threads);
+        if ((int)threadIdx.x < S) peer_arrive(bar, threadIdx.x);
+        if (ok && !wait_peers(bar, (uint32_t)(count & 1), kWaitNs)) {
+            atomicExch(err, 93);
+            ok = false;
+        }
+        ++count;
+        named_bar_sync(1, threads);
+    }
 };
-// Consumer warps of a CTA, and CTAs an SM. Measured at ... see launch_few.
-template <int NT>
-constexpr int few_warps() { return NT == 4 ? 16 : 8; }
-template <int NT>
-constexpr int few_ctas() { return NT <= 2 ? 2 : 1; }
-template <int NT>
-constexpr int red_bufs() { return NT <= 2 ? 2 : 1; }  // with two, one barrier a group is enough
 
-// Grid (S, gy), clusters of S. A producer warp copies the groups' records into a
-// ring in shared memory (bulk copies: the weights do not depend on anything before
-// this launch, so they start at once), W warps consume them. Shared memory: x, the
-// ring, the warps' sums, this CTA's sums of a batch of groups where k is split.
-template <int G, int NT>
-__global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
+// A consumer's place in the ring of stages.
+struct Place {
+    uint32_t slot, first, end, stage, fb, fb0, parity;
+    bool late;
+    QMLP_DEV void wait(int* err) {
+        if (mbar_try_wait(fb, parity)) return;
+        if (!mbar_wait_bounded(fb, parity, late ? 0 : kWaitNs)) {
+            atomicExch(err, 92);  // (what is then read lies in the ring; out is not valid)
+            late = true;
+        }
+    }
+    QMLP_DEV void release_and_step(int lane) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fb + 8u * kMaxStages);
+        slot += stage;
+        fb += 8;
+        if (slot == end) {
+            slot = first;
+            fb = fb0;
+            parity ^= 1;
+        }
+    }
+};
+
+// How a launch is cut.
+struct FewPlan {
+    int S;       // CTAs of a cluster: splits of k
+    int wpt;     // few: warps that share a tile of 16 rows (its k), W / wpt tiles a group
+    int tg;      // mid: tiles of a group
+    int gy;      // clusters
+    int stages;  // of the ring
+    int batch;   // few: groups whose sums wait in shared memory (S > 1)
+};
+// Warps and CTAs an SM, one token and two to eight.
+template <bool ONE>
+constexpr int few_warps() { return ONE ? 8 : 16; }
+template <bool ONE>
+constexpr int few_ctas() { return ONE ? 3 : 1; }
+
+// At most eight tokens. Grid (S, gy), clusters of S. A producer warp copies the
+// groups' records into a ring in shared memory (bulk copies: the weights do not
+// depend on anything before this launch, so they start at once), W warps consume
+// them. Shared memory: x, the ring, the warps' sums (two buffers: one barrier a group
+// is enough), this CTA's sums of a batch of groups where k is split.
+template <int G, bool ONE>
+__global__ void __launch_bounds__((few_warps<ONE>() + 1) * 32, few_ctas<ONE>())
     linear_few_kernel(const LinearArgs a, const FewPlan P) {
     using R = Rec<G>;
-    constexpr int kC = 8 * NT, W = few_warps<NT>(), kT = W * 32, kRec = R::kBytes, kStage = W * kRec;
+    constexpr int kC = ONE ? 1 : 8, W = few_warps<ONE>(), kT = W * 32, kRec = R::kBytes, kStage = W * kRec;
     extern __shared__ __align__(128) uint8_t few_sm[];
-    __shared__ int s_max[kC], s_sig[kC];
+    __shared__ int s_max[8], s_sig[8];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
-    const int S = P.S, rank = blockIdx.x, M = a.M, K = a.K;
+    const int S = P.S, rank = blockIdx.x, M = ONE ? 1 : a.M, K = a.K;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int Kc = (K + kCh - 1) / kCh, Nt = (a.N + 15) / 16;
     const int cps = (Kc + S - 1) / S;                     // records of k a CTA
@@ -331,8 +415,8 @@ __global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
     const int wpt = P.wpt, TG = W / wpt, groups = (Nt + TG - 1) / TG, steps = (cps + wpt - 1) / wpt;
     uint4* xsm = reinterpret_cast<uint4*>(few_sm);
     uint8_t* ring = few_sm + (size_t)cps * 256 * M;
-    float* red = reinterpret_cast<float*>(ring + (size_t)P.stages * kStage);     // [buffers][W][kC][kPitch], wpt > 1
-    float* own = red + (wpt > 1 ? red_bufs<NT>() * W * kC * kPitch : 0);           // [batch][TG][kC][16], S > 1
+    float* red = reinterpret_cast<float*>(ring + (size_t)P.stages * kStage);  // [2][W][kC][kPitch], wpt > 1
+    float* own = red + (wpt > 1 ? 2 * W * kC * kPitch : 0);                    // [batch][TG][kC][16], S > 1
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
@@ -345,7 +429,7 @@ __global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
         mbar_init(peers, (uint32_t)S);
         fence_mbar_init();
     }
-    if (threadIdx.x < kC) s_max[threadIdx.x] = s_sig[threadIdx.x] = 0;
+    if (threadIdx.x < 8) s_max[threadIdx.x] = s_sig[threadIdx.x] = 0;
     if (S > 1) lin_cluster_sync();  // the peers' barriers are there
     else __syncthreads();
     pdl_launch_dependents();
@@ -393,29 +477,15 @@ __global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
     // stays with one token: its largest value falls out of the copy, and the copy is
     // scaled in place once the row's exponent is known.
     pdl_wait();  // x is written, and out may be
-    // What the consumers of the cluster's CTAs wrote to their shared memory is
-    // visible to all of them (the producers have no part in it: they wait for the
-    // consumers, who would wait for them).
-    bool ok = true;
-    int meets = 0;
-    auto meet = [&] {
-        named_bar_sync(1, kT);
-        if ((int)threadIdx.x < S) peer_arrive(peers, threadIdx.x);
-        if (ok && !wait_peers(peers, (uint32_t)(meets & 1), kWaitNs)) {
-            atomicExch(a.err, 93);
-            ok = false;
-        }
-        ++meets;
-        named_bar_sync(1, kT);
-    };
-    const int mp = NT == 1 && M == 1 ? 1 : kC;  // (M = 1: all threads on its row)
-    const int k0 = kc0 * kCh, xt = threadIdx.x & 3, xm = (threadIdx.x >> 2) % mp, hop = kT / 4 / mp;
+    Peers cluster{peers, S, kT, 0, a.err, true};
+    const int xt = threadIdx.x & 3, xm = ONE ? 0 : (threadIdx.x >> 2) & 7, hop = ONE ? kT / 4 : kT / 32;
+    const int ci0 = ONE ? threadIdx.x >> 2 : threadIdx.x >> 5;
     if (xm < M) {
         float mx = 0.0f;
         const uint16_t* row = static_cast<const uint16_t*>(a.x) + (size_t)xm * K;
 #pragma unroll 4
-        for (int ci = (threadIdx.x >> 2) / mp; ci < nch * 4; ci += hop) {
-            const int k = k0 + 32 * ci + 4 * xt;
+        for (int ci = ci0; ci < nch * 4; ci += hop) {
+            const int k = kc0 * kCh + 32 * ci + 4 * xt;
             uint2 v[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h)  // K is a multiple of 16
@@ -429,16 +499,13 @@ __global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
         }
         if (a.x_bf16) {  // lanes of the same token first
             const uint32_t on = __activemask();
-            mx = fmaxf(mx, __shfl_xor_sync(on, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(on, mx, 2));
-            if (mp == 1)
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(on, mx, o));
-            if (mp == 1 ? lane == 0 : xt == 0) atomicMax(s_max + xm, __float_as_int(mx));
+            for (int o = 1; o < (ONE ? 32 : 4); o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(on, mx, o));
+            if (ONE ? lane == 0 : xt == 0) atomicMax(s_max + xm, __float_as_int(mx));
         }
     }
     if (a.x_bf16) {
-        if (S > 1) meet();
+        if (S > 1) cluster.meet();
         else named_bar_sync(1, kT);
         if (threadIdx.x < M) {
             int mx = 0;
@@ -450,16 +517,14 @@ __global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
             // 2^sig in two factors: it may pass fp32's range, they do not
             const int sg = s_sig[xm];
             const float p0 = __int_as_float((127 + (sg >> 1)) << 23), p1 = __int_as_float((127 + sg - (sg >> 1)) << 23);
-            for (int ci = (threadIdx.x >> 2) / mp; ci < nch * 4; ci += hop) {
+            for (int ci = ci0; ci < nch * 4; ci += hop) {
                 uint4& slot = xsm[(ci * M + xm) * 4 + xt];
                 const uint4 u = slot;
                 uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __half2 hv = __floats2half2_rn(__uint_as_float(v[j] << 16) * p0 * p1,
-                                                         __uint_as_float(v[j] & 0xFFFF0000u) * p0 * p1);
-                    v[j] = *reinterpret_cast<const uint32_t*>(&hv);
-                }
+                for (int j = 0; j < 4; ++j)
+                    v[j] = u2(__floats2half2_rn(__uint_as_float(v[j] << 16) * p0 * p1,
+                                                __uint_as_float(v[j] & 0xFFFF0000u) * p0 * p1));
                 slot = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
@@ -468,62 +533,39 @@ __global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
 
     // ---------------- consumers ----------------
     const int wi = warp % wpt, wt = warp / wpt;  // place in the tile's k, tile of the group
-    uint32_t xn[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) xn[n] = (uint32_t)((min(8 * n + g, M - 1) * 4 + t) * 16);
-    const uint32_t x0 = smem_u32(xsm) + (uint32_t)(wi * 256 * M), xstep = (uint32_t)(wpt * 256 * M), xs = (uint32_t)(64 * M);
-    // this warp's record of the ring's current stage, and that stage's barriers
-    const uint32_t ring0 = smem_u32(ring) + (uint32_t)(warp * kRec), ring_end = ring0 + (uint32_t)(P.stages * kStage);
-    uint32_t slot = ring0, fb = full(0), parity = 0;
-    uint64_t lim = kWaitNs;
+    const uint32_t x0 = smem_u32(xsm) + (uint32_t)(wi * 256 * M + (min(g, M - 1) * 4 + t) * 16);
+    const uint32_t xstep = (uint32_t)(wpt * 256 * M), xs = (uint32_t)(64 * M);
+    const uint32_t at0 = smem_u32(ring) + (uint32_t)(warp * kRec);
+    Place at{at0, at0, at0 + (uint32_t)(P.stages * kStage), (uint32_t)kStage, full(0), full(0), 0, false};
     const int nst = nch > wi ? (nch - wi + wpt - 1) / wpt : 0;  // steps that this warp has a record in
     int done = 0, b0 = blockIdx.y;  // groups done, the batch's first
     for (int gr = blockIdx.y; gr < groups; gr += gridDim.y, ++done) {
-        float acc[chains<NT>()][NT][4];
+        float acc[2][4];
 #pragma unroll
-        for (int c = 0; c < chains<NT>(); ++c)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[c][n][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) acc[0][e] = acc[1][e] = 0.0f;
         const int mst = gr * TG + wt < Nt ? nst : 0;
         uint32_t xb = x0;
 #pragma unroll 1
         for (int st = 0; st < steps; ++st, xb += xstep) {
-            if (!mbar_try_wait(fb, parity) && !mbar_wait_bounded(fb, parity, lim)) {
-                atomicExch(a.err, 92);  // (what is then read lies in the ring; out is not valid)
-                lim = 0;
-            }
+            at.wait(a.err);
             Frag<G> f;
             const bool has = st < mst;
-            if (has) load_frag<G>(f, slot + lane * 16, slot + 1024 + g * (R::kScales / 8), slot + 1024 + R::kScales + g * (R::kZeros / 8));
-            __syncwarp();
-            if (lane == 0) mbar_arrive(fb + 8u * kMaxStages);
-            slot += kStage;
-            fb += 8;
-            if (slot == ring_end) {
-                slot = ring0;
-                fb = full(0);
-                parity ^= 1;
-            }
-            if (has) mma_record<G, NT>(f, xb, xs, xn, acc);
+            if (has)
+                load_frag<G>(f, at.slot + lane * 16, at.slot + 1024 + g * (R::kScales / 8),
+                             at.slot + 1024 + R::kScales + g * (R::kZeros / 8));
+            at.release_and_step(lane);
+            if (has) mma_record<G, ONE>(f, xb, xs, acc);
         }
 #pragma unroll
-        for (int c = 1; c < chains<NT>(); ++c)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[0][n][e] += acc[c][n][e];
+        for (int e = 0; e < 4; ++e) acc[0][e] += acc[1][e];
         float* ob = own + (size_t)(done % P.batch) * TG * kC * 16;
         if (wpt > 1) {
-            float* rb = red + (red_bufs<NT>() > 1 ? (done & 1) * W * kC * kPitch : 0);
-            if (red_bufs<NT>() == 1) named_bar_sync(1, kT);  // the sums of the group before are read
+            float* rb = red + (done & 1) * W * kC * kPitch;
             // [warp][column][kPitch rows]: 20 puts the 32 lanes on 32 banks
             float* mine = rb + warp * kC * kPitch;
+            if (!ONE || t == 0)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) mine[(8 * n + 2 * t + (e & 1)) * kPitch + g + 4 * (e & 2)] = acc[0][n][e];
+                for (int e = 0; e < 4; e += ONE ? 2 : 1) mine[(ONE ? 0 : 2 * t + (e & 1)) * kPitch + g + 4 * (e & 2)] = acc[0][e];
             named_bar_sync(1, kT);
             for (int i = threadIdx.x; i < 4 * M * TG; i += kT) {  // four rows of a token
                 const int r4 = (i & 3) * 4, m = (i >> 2) % M, j = (i >> 2) / M;
@@ -533,40 +575,234 @@ __global__ void __launch_bounds__((few_warps<NT>() + 1) * 32, few_ctas<NT>())
                 if (S > 1) *reinterpret_cast<float4*>(ob + (j * kC + m) * 16 + r4) = v;
                 else store4(a, m, 16 * (gr * TG + j) + r4, v, s_sig[m]);
             }
-        } else if (S > 1) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ob[(warp * kC + 8 * n + 2 * t + (e & 1)) * 16 + g + 4 * (e & 2)] = acc[0][n][e];
         } else {
+            // the warp's own tile: through its place in `own`, four rows of a token at a time
+            float* mine = ob + warp * kC * 16;
+            __syncwarp();
+            if (!ONE || t == 0)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int m = 8 * n + 2 * t + (e & 1);
-                    if (m < M) store1(a, m, 16 * (gr * TG + warp) + g + 4 * (e & 2), acc[0][n][e], s_sig[m]);
-                }
+                for (int e = 0; e < 4; e += ONE ? 2 : 1) mine[(ONE ? 0 : 2 * t + (e & 1)) * 16 + g + 4 * (e & 2)] = acc[0][e];
+            __syncwarp();
+            if (S == 1 && lane < 4 * M)
+                store4(a, lane >> 2, 16 * (gr * TG + warp) + (lane & 3) * 4,
+                       *reinterpret_cast<const float4*>(mine + (lane >> 2) * 16 + (lane & 3) * 4), s_sig[lane >> 2]);
         }
         // a batch of groups is done: the cluster's sums in order
         if (S > 1 && ((done + 1) % P.batch == 0 || gr + (int)gridDim.y >= groups)) {
-            meet();  // every CTA's sums are written
+            cluster.meet();  // every CTA's sums are written
             const int nb = done % P.batch + 1, items = nb * TG * 4 * M, per = (items + S - 1) / S;
             for (int i = rank * per + threadIdx.x; i < min(items, (rank + 1) * per); i += kT) {
                 const int r4 = (i & 3) * 4, m = (i >> 2) % M, j = (i >> 2) / M;
-                float4 p[8], v = make_float4(0, 0, 0, 0);
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < S) p[r] = peer_f4(own + ((size_t)j * kC + m) * 16 + r4, r);
-#pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < S) add4(v, p[r]);
+                const float4 v = peer_sum(own + ((size_t)j * kC + m) * 16 + r4, S);
                 store4(a, m, 16 * ((b0 + j / TG * (int)gridDim.y) * TG + j % TG) + r4, v, s_sig[m]);
             }
-            meet();  // none writes its next sums while another reads
+            cluster.meet();  // none writes its next sums while another reads
             b0 = gr + gridDim.y;
         }
     }
     if (S > 1) lin_cluster_sync();  // no CTA leaves while another may read its sums
+}
+
+// Nine to 64 tokens: x does not stay in shared memory but comes through the ring with
+// the weights, in the order of the steps as linear_x_kernel wrote it. A warp takes a
+// tile of 16 rows, up to 16 of them a group, and all of them the same k: a stage is CS
+// records of each of the group's tiles and the x of their k.
+template <int NT>
+constexpr int mid_chunks() { return NT == 8 ? 1 : 2; }  // CS: 36 KB of weights a stage, 18 with 64 tokens
+constexpr int kMidWarps = 16;
+
+template <int G, int NT>
+__global__ void __launch_bounds__((kMidWarps + 1) * 32, 1) linear_mid_kernel(const LinearArgs a, const FewPlan P) {
+    using R = Rec<G>;
+    constexpr int kC = 8 * NT, W = kMidWarps, kT = W * 32, kRec = R::kBytes, CS = mid_chunks<NT>();
+    extern __shared__ __align__(128) uint8_t few_sm[];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
+    const int S = P.S, rank = blockIdx.x, M = a.M, K = a.K;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int Kc = (K + kCh - 1) / kCh, Nt = (a.N + 15) / 16, TG = P.tg, groups = (Nt + TG - 1) / TG;
+    const int cps = (Kc + S - 1) / S, kc0 = rank * cps, nch = min(cps, Kc - kc0), steps = (cps + CS - 1) / CS;
+    const int xbytes = 256 * M, stage = TG * CS * kRec + CS * xbytes;
+    float* own = reinterpret_cast<float*>(few_sm + (size_t)P.stages * stage);  // [W][kC][16]
+    const uint32_t bar0 = smem_u32(bars), ring = smem_u32(few_sm);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    const uint32_t peers = bar0 + 8u * (2 * kMaxStages);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < P.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), W);
+        }
+        mbar_init(peers, (uint32_t)S);
+        fence_mbar_init();
+    }
+    if (S > 1) lin_cluster_sync();
+    else __syncthreads();
+    pdl_launch_dependents();
+
+    if (warp == W) {
+        // ---------------- producer ----------------
+        if (lane == 0) {
+            const uint8_t* xf = static_cast<const uint8_t*>(a.xf) + (size_t)kc0 * xbytes;
+            const int all = (groups - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y * steps;
+            // the first stages' weights, then, once x is there, their x
+            auto weights = [&](int it) {
+                const int s = it % P.stages, st = it % steps, gr = blockIdx.y + it / steps * gridDim.y;
+                const int n = max(0, min(CS, nch - st * CS)), tiles = min(TG, Nt - gr * TG);
+                mbar_arrive_expect_tx(full(s), (uint32_t)(n * (kRec * tiles + xbytes)));
+                if (n > 0)
+                    for (int j = 0; j < tiles; ++j) {
+                        const uint8_t* p = a.w + (((size_t)gr * TG + j) * Kc + kc0 + st * CS) * kRec;
+                        if (!QMLP_INB(p - a.w + n * kRec - 1, a.w_bytes, 91)) p = a.w;
+                        bulk_g2s(ring + (uint32_t)(s * stage + j * CS * kRec), p, (uint32_t)(n * kRec), full(s));
+                    }
+            };
+            auto tokens = [&](int it) {
+                const int s = it % P.stages, st = it % steps, n = max(0, min(CS, nch - st * CS));
+                if (n > 0)
+                    bulk_g2s(ring + (uint32_t)(s * stage + TG * CS * kRec), xf + (size_t)st * CS * xbytes,
+                             (uint32_t)(n * xbytes), full(s));
+            };
+            int it = 0;
+            const int early = min(all, P.stages);
+            for (; it < early; ++it) weights(it);
+            pdl_wait();
+            for (int q = 0; q < early; ++q) tokens(q);
+            bool ok = true;
+            for (; it < all; ++it) {
+                if (!mbar_wait_bounded(empty(it % P.stages), (uint32_t)((it / P.stages - 1) & 1), kWaitNs)) {
+                    atomicExch(a.err, 91);
+                    ok = false;
+                    break;
+                }
+                weights(it);
+                tokens(it);
+            }
+            if (!ok)
+                for (int q = it - 1; q >= 0 && q >= it - P.stages; --q)
+                    mbar_wait_bounded(full(q % P.stages), (uint32_t)((q / P.stages) & 1), kWaitNs);
+        }
+        __syncwarp();
+        if (S > 1) lin_cluster_sync();
+        return;
+    }
+
+    // ---------------- consumers ----------------
+    pdl_wait();  // the exponents are written, and out may be
+    Peers cluster{peers, S, kT, 0, a.err, true};
+    uint32_t xn[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xn[n] = (uint32_t)((min(8 * n + g, M - 1) * 4 + t) * 16);
+    const uint32_t xs = (uint32_t)(64 * M), xat = (uint32_t)(TG * CS * kRec - warp * CS * kRec);
+    const uint32_t at0 = ring + (uint32_t)(warp * CS * kRec);
+    Place at{at0, at0, at0 + (uint32_t)(P.stages * stage), (uint32_t)stage, full(0), full(0), 0, false};
+    for (int gr = blockIdx.y; gr < groups; gr += gridDim.y) {
+        const bool on = warp < TG && gr * TG + warp < Nt;
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+#pragma unroll 1
+        for (int st = 0; st < steps; ++st) {
+            at.wait(a.err);
+#pragma unroll
+            for (int c = 0; c < CS; ++c)
+                if (on && st * CS + c < nch) {
+                    const uint32_t rec = at.slot + c * kRec;
+                    Frag<G> f;
+                    load_frag<G>(f, rec + lane * 16, rec + 1024 + g * (R::kScales / 8),
+                                 rec + 1024 + R::kScales + g * (R::kZeros / 8));
+                    mma_record_tiles<G, NT>(f, at.slot + xat + c * xbytes, xs, xn, acc);
+                }
+            at.release_and_step(lane);
+        }
+        // the tile's sums, [token][16 rows]
+        float* mine = own + warp * kC * 16;
+        __syncwarp();
+        if (on)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mine[(8 * n + 2 * t + (e & 1)) * 16 + g + 4 * (e & 2)] = acc[n][e];
+        __syncwarp();
+        if (S == 1) {
+            if (on)
+                for (int i = lane; i < 4 * M; i += 32)
+                    store4(a, i >> 2, 16 * (gr * TG + warp) + (i & 3) * 4,
+                           *reinterpret_cast<const float4*>(mine + (i >> 2) * 16 + (i & 3) * 4), __ldcg(a.sig + (i >> 2)));
+        } else {
+            cluster.meet();  // every CTA's sums are written
+            const int tiles = min(TG, Nt - gr * TG), items = tiles * 4 * M, per = (items + S - 1) / S;
+            for (int i = rank * per + threadIdx.x; i < min(items, (rank + 1) * per); i += kT) {
+                const int r4 = (i & 3) * 4, m = (i >> 2) % M, j = (i >> 2) / M;
+                store4(a, m, 16 * (gr * TG + j) + r4, peer_sum(own + ((size_t)j * kC + m) * 16 + r4, S), __ldcg(a.sig + m));
+            }
+            cluster.meet();
+        }
+    }
+    if (S > 1) lin_cluster_sync();
+}
+
+// x -> fp16 in the order of the steps, [record of k][pair of steps][token][t] of 16
+// bytes (see linear_few_kernel), and the tokens' exponents. A CTA a token.
+__global__ void __launch_bounds__(256) linear_x_kernel(const LinearArgs a) {
+    __shared__ int s_max;
+    const int m = blockIdx.x, M = a.M, K = a.K, n = (K + kCh - 1) / kCh * 16;  // 16-byte pieces of the token
+    if (threadIdx.x == 0) s_max = 0;
+    pdl_wait();
+    pdl_launch_dependents();  // (only now: what comes next waits for this kernel alone)
+    const uint16_t* row = static_cast<const uint16_t*>(a.x) + (size_t)m * K;
+    uint4* out = static_cast<uint4*>(a.xf);
+    auto piece = [&](int i) {  // i = 4 ci + t
+        const int k = 32 * (i >> 2) + 4 * (i & 3);
+        uint2 v[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) v[h] = k + 16 * h < K ? *reinterpret_cast<const uint2*>(row + k + 16 * h) : make_uint2(0, 0);
+        return make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
+    };
+    constexpr int kKeep = 4;  // pieces a thread keeps between the two passes
+    uint4 keep[kKeep];
+    float mx = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j) {
+        const int i = threadIdx.x + j * 256;
+        keep[j] = i < n ? piece(i) : make_uint4(0, 0, 0, 0);
+    }
+    auto largest = [&](const uint4& v) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[j] << 16)), fabsf(__uint_as_float(w[j] & 0xFFFF0000u))));
+    };
+    int sg = 0;
+    __syncthreads();
+    if (a.x_bf16) {
+#pragma unroll
+        for (int j = 0; j < kKeep; ++j) largest(keep[j]);
+#pragma unroll 4
+        for (int i = threadIdx.x + kKeep * 256; i < n; i += 256) largest(piece(i));
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if ((threadIdx.x & 31) == 0) atomicMax(&s_max, __float_as_int(mx));
+        __syncthreads();
+        sg = prescale_exponent(__int_as_float(s_max));
+    }
+    if (threadIdx.x == 0) a.sig[m] = sg;
+    const float p0 = __int_as_float((127 + (sg >> 1)) << 23), p1 = __int_as_float((127 + sg - (sg >> 1)) << 23);
+    auto put = [&](int i, const uint4& u) {
+        uint32_t v[4] = {u.x, u.y, u.z, u.w};
+        if (a.x_bf16)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = u2(__floats2half2_rn(__uint_as_float(v[j] << 16) * p0 * p1, __uint_as_float(v[j] & 0xFFFF0000u) * p0 * p1));
+        const size_t at = ((size_t)(i >> 2) * M + m) * 4 + (i & 3);
+        if (QMLP_INB(at, a.xf_elems, 95)) out[at] = make_uint4(v[0], v[1], v[2], v[3]);
+    };
+#pragma unroll
+    for (int j = 0; j < kKeep; ++j)
+        if (threadIdx.x + j * 256 < n) put(threadIdx.x + j * 256, keep[j]);
+#pragma unroll 4
+    for (int i = threadIdx.x + kKeep * 256; i < n; i += 256) put(i, piece(i));
 }
 
 // Checkpoint rows -> records (one thread a lane's 16 bytes of a row half, the
@@ -715,31 +951,49 @@ size_t few_x_bytes(int K, int M, int S) {
     return (size_t)((Kc + S - 1) / S) * 256 * M;
 }
 
-template <int G, int NT>
+cudaLaunchConfig_t few_config(const FewPlan& P, int threads, size_t smem, cudaStream_t s, cudaLaunchAttribute* at) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)P.S, (unsigned)P.gy);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = (unsigned)P.S;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = P.S > 1 ? 2 : 1;
+    return cfg;
+}
+
+template <int G, bool ONE>
 cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
-    constexpr int kC = 8 * NT, W = few_warps<NT>(), kStage = W * Rec<G>::kBytes;
+    constexpr int kC = ONE ? 1 : 8, W = few_warps<ONE>(), kStage = W * Rec<G>::kBytes, kCtas = few_ctas<ONE>();
     const int Kc = (a.K + kCh - 1) / kCh, Nt = (a.N + 15) / 16;
-    FewPlan P;
-    // k is split where x would take more than its part of shared memory, and while
-    // the GPU has room for twice the CTAs and a warp keeps two records or more
-    const size_t xmost = kSmemMax / few_ctas<NT>() * 2 / 5;
+    const size_t room = kSmemMax / kCtas - 2048;  // of a CTA where the SM has all its CTAs
+    FewPlan P = {};
+    // k is split where x would take more than half of that, and where a warp would
+    // have 16 records of a tile and more while half of the GPU has none (a cluster's
+    // barriers cost 1.4 us: 1024 x 5120, 4.3 us without, 5.7 with two CTAs)
     P.S = 1;
-    auto tile_groups = [&](int wpt) { return (Nt + W / wpt - 1) / (W / wpt); };
-    while (P.S < 8 && few_x_bytes(a.K, a.M, P.S) > xmost) P.S *= 2;
-    // a tile's k is shared by as many warps as leave enough groups for the GPU
-    P.wpt = NT <= 2 ? W : 1;
-    while (P.wpt > 1 && ((Kc + P.S - 1) / P.S < 2 * P.wpt || tile_groups(P.wpt / 2) * P.S >= 8 * num_sms)) P.wpt /= 2;
-    while (P.S < 8 && tile_groups(P.wpt) * P.S * 2 <= num_sms * few_ctas<NT>() && Kc >= 4 * P.S * P.wpt) P.S *= 2;
+    while (P.S < 8 && few_x_bytes(a.K, a.M, P.S) > room / 2) P.S *= 2;
+    while (P.S < 8 && (long)Nt * P.S * 2 <= (long)num_sms * kCtas && Kc >= 16 * P.S * W) P.S *= 2;
     while (P.S > 1 && (P.S - 1) * ((Kc + P.S - 1) / P.S) >= Kc) P.S /= 2;  // every CTA has some of k
+    // a tile's k is shared by as many warps as have two records or more of it, by
+    // fewer (a barrier a group) as long as every CTA has two groups
+    auto tile_groups = [&](int wpt) { return (Nt + W / wpt - 1) / (W / wpt); };
+    P.wpt = W;
+    while (P.wpt > 1 && ((Kc + P.S - 1) / P.S < 2 * P.wpt || tile_groups(P.wpt / 2) * P.S >= 2 * kCtas * num_sms)) P.wpt /= 2;
     const int TG = W / P.wpt, groups = tile_groups(P.wpt);
     const size_t x = few_x_bytes(a.K, a.M, P.S);
-    const size_t red = P.wpt > 1 ? (size_t)red_bufs<NT>() * W * kC * kPitch * 4 : 0;
-    const size_t group_own = P.S > 1 ? (size_t)TG * kC * 16 * 4 : 0;
-    const size_t room = kSmemMax / few_ctas<NT>() - 2048;
+    const size_t red = P.wpt > 1 ? (size_t)2 * W * kC * kPitch * 4 : 0;
+    const size_t group_own = P.S > 1 || P.wpt == 1 ? (size_t)TG * kC * 16 * 4 : 0;
     if (x + red + group_own + 2 * kStage > kSmemMax - 2048) return cudaErrorInvalidValue;
-    const bool one = x + red + group_own + 3 * kStage > room;  // one CTA an SM then
+    const bool one = x + red + group_own + 2 * kStage > room;  // one CTA an SM then
     const size_t all = one ? kSmemMax - 2048 : room;
-    const int fit = one ? 1 : few_ctas<NT>();
+    const int fit = one ? 1 : kCtas;
     P.gy = std::max(1, std::min(groups, num_sms * fit / P.S));
     const int mine = (groups + P.gy - 1) / P.gy;
     P.gy = (groups + mine - 1) / mine;
@@ -750,56 +1004,76 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     }
     const size_t fixed = x + red + group_own * P.batch;
     P.stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(2, (all - fixed) / kStage));
-    const size_t smem = fixed + (size_t)P.stages * kStage;
     static bool attr = false;
     if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        const cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<G, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    kSmemMax);
         if (e != cudaSuccess) return e;
         attr = true;
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)P.S, (unsigned)P.gy);
-    cfg.blockDim = dim3((W + 1) * 32);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)P.S;
-    at[1].val.clusterDim.y = 1;
-    at[1].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = P.S > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, linear_few_kernel<G, NT>, a, P);
+    const cudaLaunchConfig_t cfg = few_config(P, (W + 1) * 32, fixed + (size_t)P.stages * kStage, s, at);
+    return cudaLaunchKernelEx(&cfg, linear_few_kernel<G, ONE>, a, P);
+}
+
+template <int G, int NT>
+cudaError_t launch_mid(const LinearArgs& a, int num_sms, cudaStream_t s) {
+    constexpr int kC = 8 * NT, CS = mid_chunks<NT>(), kRec = Rec<G>::kBytes;
+    const int Kc = (a.K + kCh - 1) / kCh, Nt = (a.N + 15) / 16;
+    FewPlan P = {};
+    // a CTA an SM, with eight tiles or more of its cluster's k where there are enough
+    P.S = 1;
+    while (P.S < 8 && Nt * P.S * 2 <= 12 * num_sms && Kc >= 4 * P.S * CS) P.S *= 2;
+    while (P.S > 1 && (P.S - 1) * ((Kc + P.S - 1) / P.S) >= Kc) P.S /= 2;
+    const int clusters = std::max(1, num_sms / P.S);
+    P.tg = std::min(kMidWarps, (Nt + clusters - 1) / clusters);
+    const int groups = (Nt + P.tg - 1) / P.tg;
+    P.gy = std::min(groups, clusters);
+    const size_t stage = (size_t)P.tg * CS * kRec + (size_t)CS * 256 * a.M, own = (size_t)kMidWarps * kC * 16 * 4;
+    P.stages = (int)std::min<size_t>(kMaxStages, (kSmemMax - 2048 - own) / stage);
+    if (P.stages < 2) return cudaErrorInvalidValue;
+    static bool attr = false;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(linear_mid_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kSmemMax);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    cudaLaunchAttribute at[2];
+    FewPlan X = {};
+    X.S = 1;
+    cudaLaunchConfig_t cfg = few_config(X, 256, 0, s, at);
+    cfg.gridDim = dim3((unsigned)a.M);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, linear_x_kernel, a);
+    if (e != cudaSuccess) return e;
+    cfg = few_config(P, (kMidWarps + 1) * 32, own + (size_t)P.stages * stage, s, at);
+    return cudaLaunchKernelEx(&cfg, linear_mid_kernel<G, NT>, a, P);
 }
 
 template <int G>
 cudaError_t launch_g(LinearArgs a, int num_sms, cudaStream_t s) {
-    // several launches of as many tokens each as one takes: 64, or what a cluster's
-    // shared memory has room for
+    if (a.M == 1) return launch_few<G, true>(a, num_sms, s);
+    if (a.M <= kLinearFew) return launch_few<G, false>(a, num_sms, s);
+    // 64 tokens a launch, or as evenly as that many launches allow
     const size_t ob = a.odt == 0 ? 4 : 2;
-    const int M = a.M;
-    int most = 64;
-    // (the ring, and a group's sums of 64 tokens, need 100 KB at most)
-    while (most > 8 && few_x_bytes(a.K, most, 8) > kSmemMax - 104 * 1024) most /= 2;
-    const int blocks = (M + most - 1) / most, step = ((M + blocks - 1) / blocks + 7) / 8 * 8;
+    const int M = a.M, blocks = (M + kLinearMid - 1) / kLinearMid, step = ((M + blocks - 1) / blocks + 7) / 8 * 8;
     for (int m = 0; m < M; m += step) {
         LinearArgs b = a;
         b.M = std::min(step, M - m);
         b.x = static_cast<const uint8_t*>(a.x) + (size_t)m * a.K * 2;
         b.out = static_cast<uint8_t*>(a.out) + (size_t)m * a.N * ob;
-        const cudaError_t e = b.M <= 8    ? launch_few<G, 1>(b, num_sms, s)
-                              : b.M <= 16 ? launch_few<G, 2>(b, num_sms, s)
-                              : b.M <= 32 ? launch_few<G, 4>(b, num_sms, s)
-                                          : launch_few<G, 8>(b, num_sms, s);
+        const cudaError_t e = b.M <= 8    ? launch_mid<G, 1>(b, num_sms, s)
+                              : b.M <= 16 ? launch_mid<G, 2>(b, num_sms, s)
+                              : b.M <= 32 ? launch_mid<G, 4>(b, num_sms, s)
+                                          : launch_mid<G, 8>(b, num_sms, s);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
 
 }  // namespace
+
+size_t linear_x_bytes(int K, int M) { return few_x_bytes(K, std::min(M, kLinearMid), 1); }
 
 size_t linear_bytes(int group, int N, int K) {
     return (size_t)((N + 15) / 16) * ((K + kCh - 1) / kCh) * linear_rec_bytes(group);
