@@ -435,37 +435,36 @@ __global__ void __launch_bounds__((few_warps<ONE>() + 1) * 32, few_ctas<ONE>())
     pdl_launch_dependents();
 
     if (warp == W) {
-        // ---------------- producer ----------------
-        if (lane == 0) {
-            int it = 0;
-            bool ok = true;
-            for (int gr = blockIdx.y; gr < groups && ok; gr += gridDim.y) {
-                const int tiles = min(TG, Nt - gr * TG);
-                const uint8_t* src = a.w + ((size_t)gr * TG * Kc + kc0) * kRec;
-                for (int st = 0; st < steps; ++st, ++it) {
-                    const int s = it % P.stages;
-                    if (it >= P.stages && !mbar_wait_bounded(empty(s), (uint32_t)((it / P.stages - 1) & 1), kWaitNs)) {
-                        atomicExch(a.err, 91);
-                        ok = false;
-                        break;
-                    }
-                    const int n = max(0, min(wpt, nch - st * wpt));
-                    const uint32_t bytes = (uint32_t)(n * kRec);
-                    mbar_arrive_expect_tx(full(s), bytes * tiles);
-                    if (n > 0)
-                        for (int j = 0; j < tiles; ++j) {
-                            const uint8_t* p = src + ((size_t)j * Kc + st * wpt) * kRec;
-                            if (!QMLP_INB(p - a.w + bytes - 1, a.w_bytes, 91)) p = a.w;
-                            bulk_g2s(smem_u32(ring + (size_t)s * kStage + (size_t)j * wpt * kRec), p, bytes, full(s));
-                        }
+        // ---------------- producer: a lane a tile ----------------
+        int it = 0;
+        bool ok = true;
+        for (int gr = blockIdx.y; gr < groups && ok; gr += gridDim.y) {
+            const int tiles = min(TG, Nt - gr * TG);
+            const uint8_t* src = a.w + (((size_t)gr * TG + lane) * Kc + kc0) * kRec;
+            for (int st = 0; st < steps; ++st, ++it) {
+                const int s = it % P.stages;
+                if (it >= P.stages &&
+                    !__all_sync(0xffffffffu, mbar_wait_bounded(empty(s), (uint32_t)((it / P.stages - 1) & 1), kWaitNs))) {
+                    if (lane == 0) atomicExch(a.err, 91);
+                    ok = false;
+                    break;
+                }
+                const int n = max(0, min(wpt, nch - st * wpt));
+                const uint32_t bytes = (uint32_t)(n * kRec);
+                if (lane == 0) mbar_arrive_expect_tx(full(s), bytes * tiles);
+                __syncwarp();
+                if (n > 0 && lane < tiles) {
+                    const uint8_t* p = src + (size_t)st * wpt * kRec;
+                    if (!QMLP_INB(p - a.w + bytes - 1, a.w_bytes, 91)) p = a.w;
+                    bulk_g2s(smem_u32(ring + (size_t)s * kStage + (size_t)lane * wpt * kRec), p, bytes, full(s));
                 }
             }
-            // copies still in flight (only after a wait that ran out): wait for each
-            // stage's last one
-            if (!ok)
-                for (int q = it - 1; q >= 0 && q >= it - P.stages; --q)
-                    mbar_wait_bounded(full(q % P.stages), (uint32_t)((q / P.stages) & 1), kWaitNs);
         }
+        // copies still in flight (only after a wait that ran out): wait for each
+        // stage's last one
+        if (!ok)
+            for (int q = it - 1; q >= 0 && q >= it - P.stages; --q)
+                mbar_wait_bounded(full(q % P.stages), (uint32_t)((q / P.stages) & 1), kWaitNs);
         __syncwarp();
         if (S > 1) lin_cluster_sync();  // see the end
         return;
@@ -605,11 +604,11 @@ __global__ void __launch_bounds__((few_warps<ONE>() + 1) * 32, few_ctas<ONE>())
 
 // Nine to 64 tokens: x does not stay in shared memory but comes through the ring with
 // the weights, in the order of the steps as linear_x_kernel wrote it. A warp takes a
-// tile of 16 rows, up to 16 of them a group, and all of them the same k: a stage is CS
+// tile of 16 rows, up to 15 of them a group, and all of them the same k: a stage is CS
 // records of each of the group's tiles and the x of their k.
 template <int NT>
 constexpr int mid_chunks() { return NT == 8 ? 1 : 2; }  // CS: 36 KB of weights a stage, 18 with 64 tokens
-constexpr int kMidWarps = 16;
+constexpr int kMidWarps = 15;  // with the producer four a scheduler: 128 registers each
 
 template <int G, int NT>
 __global__ void __launch_bounds__((kMidWarps + 1) * 32, 1) linear_mid_kernel(const LinearArgs a, const FewPlan P) {
@@ -640,47 +639,45 @@ __global__ void __launch_bounds__((kMidWarps + 1) * 32, 1) linear_mid_kernel(con
     pdl_launch_dependents();
 
     if (warp == W) {
-        // ---------------- producer ----------------
-        if (lane == 0) {
-            const uint8_t* xf = static_cast<const uint8_t*>(a.xf) + (size_t)kc0 * xbytes;
-            const int all = (groups - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y * steps;
-            // the first stages' weights, then, once x is there, their x
-            auto weights = [&](int it) {
-                const int s = it % P.stages, st = it % steps, gr = blockIdx.y + it / steps * gridDim.y;
-                const int n = max(0, min(CS, nch - st * CS)), tiles = min(TG, Nt - gr * TG);
-                mbar_arrive_expect_tx(full(s), (uint32_t)(n * (kRec * tiles + xbytes)));
-                if (n > 0)
-                    for (int j = 0; j < tiles; ++j) {
-                        const uint8_t* p = a.w + (((size_t)gr * TG + j) * Kc + kc0 + st * CS) * kRec;
-                        if (!QMLP_INB(p - a.w + n * kRec - 1, a.w_bytes, 91)) p = a.w;
-                        bulk_g2s(ring + (uint32_t)(s * stage + j * CS * kRec), p, (uint32_t)(n * kRec), full(s));
-                    }
-            };
-            auto tokens = [&](int it) {
-                const int s = it % P.stages, st = it % steps, n = max(0, min(CS, nch - st * CS));
-                if (n > 0)
-                    bulk_g2s(ring + (uint32_t)(s * stage + TG * CS * kRec), xf + (size_t)st * CS * xbytes,
-                             (uint32_t)(n * xbytes), full(s));
-            };
-            int it = 0;
-            const int early = min(all, P.stages);
-            for (; it < early; ++it) weights(it);
-            pdl_wait();
-            for (int q = 0; q < early; ++q) tokens(q);
-            bool ok = true;
-            for (; it < all; ++it) {
-                if (!mbar_wait_bounded(empty(it % P.stages), (uint32_t)((it / P.stages - 1) & 1), kWaitNs)) {
-                    atomicExch(a.err, 91);
-                    ok = false;
-                    break;
-                }
-                weights(it);
-                tokens(it);
+        // ---------------- producer: a lane a tile ----------------
+        const uint8_t* xf = static_cast<const uint8_t*>(a.xf) + (size_t)kc0 * xbytes;
+        const int all = (groups - (int)blockIdx.y + (int)gridDim.y - 1) / (int)gridDim.y * steps;
+        // the first stages' weights, then, once x is there, their x
+        auto weights = [&](int it) {
+            const int s = it % P.stages, st = it % steps, gr = blockIdx.y + it / steps * gridDim.y;
+            const int n = max(0, min(CS, nch - st * CS)), tiles = min(TG, Nt - gr * TG);
+            if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)(n * (kRec * tiles + xbytes)));
+            __syncwarp();
+            if (n > 0 && lane < tiles) {
+                const uint8_t* p = a.w + (((size_t)gr * TG + lane) * Kc + kc0 + st * CS) * kRec;
+                if (!QMLP_INB(p - a.w + n * kRec - 1, a.w_bytes, 91)) p = a.w;
+                bulk_g2s(ring + (uint32_t)(s * stage + lane * CS * kRec), p, (uint32_t)(n * kRec), full(s));
             }
-            if (!ok)
-                for (int q = it - 1; q >= 0 && q >= it - P.stages; --q)
-                    mbar_wait_bounded(full(q % P.stages), (uint32_t)((q / P.stages) & 1), kWaitNs);
+        };
+        auto tokens = [&](int it) {
+            const int s = it % P.stages, st = it % steps, n = max(0, min(CS, nch - st * CS));
+            if (n > 0 && lane == 0)
+                bulk_g2s(ring + (uint32_t)(s * stage + TG * CS * kRec), xf + (size_t)st * CS * xbytes, (uint32_t)(n * xbytes),
+                         full(s));
+        };
+        int it = 0;
+        const int early = min(all, P.stages);
+        for (; it < early; ++it) weights(it);
+        pdl_wait();
+        for (int q = 0; q < early; ++q) tokens(q);
+        bool ok = true;
+        for (; it < all; ++it) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(it % P.stages), (uint32_t)((it / P.stages - 1) & 1), kWaitNs))) {
+                if (lane == 0) atomicExch(a.err, 91);
+                ok = false;
+                break;
+            }
+            weights(it);
+            tokens(it);
         }
+        if (!ok)
+            for (int q = it - 1; q >= 0 && q >= it - P.stages; --q)
+                mbar_wait_bounded(full(q % P.stages), (uint32_t)((q / P.stages) & 1), kWaitNs);
         __syncwarp();
         if (S > 1) lin_cluster_sync();
         return;
@@ -981,11 +978,16 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     while (P.S < 8 && few_x_bytes(a.K, a.M, P.S) > room / 2) P.S *= 2;
     while (P.S < 8 && (long)Nt * P.S * 2 <= (long)num_sms * kCtas && Kc >= 16 * P.S * W) P.S *= 2;
     while (P.S > 1 && (P.S - 1) * ((Kc + P.S - 1) / P.S) >= Kc) P.S /= 2;  // every CTA has some of k
-    // a tile's k is shared by as many warps as have two records or more of it, by
-    // fewer (a barrier a group) as long as every CTA has two groups
+    // a tile's k is shared by as many warps as have two records or more of it: a copy
+    // of the ring is their records of one tile, and small copies are slow (128000 x
+    // 5120, one token: 78 us with eight records a copy, 84 with two or four, 112 with
+    // one). Sixteen warps: by eight where that leaves every CTA two groups (17408 x
+    // 5120, eight tokens: 17.3 us, 20.8 with sixteen).
     auto tile_groups = [&](int wpt) { return (Nt + W / wpt - 1) / (W / wpt); };
     P.wpt = W;
-    while (P.wpt > 1 && ((Kc + P.S - 1) / P.S < 2 * P.wpt || tile_groups(P.wpt / 2) * P.S >= 2 * kCtas * num_sms)) P.wpt /= 2;
+    while (P.wpt > 1 && ((Kc + P.S - 1) / P.S < 2 * P.wpt ||
+                         (P.wpt > 8 && tile_groups(P.wpt / 2) * P.S >= 2 * kCtas * num_sms)))
+        P.wpt /= 2;
     const int TG = W / P.wpt, groups = tile_groups(P.wpt);
     const size_t x = few_x_bytes(a.K, a.M, P.S);
     const size_t red = P.wpt > 1 ? (size_t)2 * W * kC * kPitch * 4 : 0;
