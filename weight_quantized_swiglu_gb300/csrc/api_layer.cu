@@ -435,13 +435,16 @@ qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const
         a.softmax = d->score == QMLP_SCORE_SOFTMAX;
         a.renorm = d->renorm != 0;
         a.rscale = d->route_scale;
-        a.rdt = dt_code(d->rdt);
+        a.sgate = d->shared_gate != nullptr;
+        a.planes = d->rdt == QMLP_DT_FP32 ? 2 : 1;
+        a.rtiles = (E + (a.sgate ? a.S : 0) + 15) / 16;
+        a.rfrag_elems = (size_t)a.planes * a.rtiles * (a.K / 32) * 64;
         a.w13 = moe->w13;
         a.w13_meta = moe->w13_meta;
         a.w2 = moe->w2;
         a.w2_meta = moe->w2_meta;
         const size_t few = (size_t)std::min(d->max_tokens, kMoeLayerFew) * nsel, rows = (size_t)d->max_tokens;
-        a.logit_elems = rows * (E + a.S);
+        a.logit_elems = std::max(rows, (size_t)kMoeRouterSplits * std::min(d->max_tokens, kMoeLayerFew)) * (E + a.S);
         a.act_elems = few * a.I;
         a.w13_bytes = moe_w13_bank_bytes(moe->E, a.I, a.K);
         a.w13_meta_bytes = moe_w13_meta_bank_bytes(moe->E, a.I, a.K, moe->meta);
@@ -455,8 +458,20 @@ qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const
             return p;
         };
         const size_t re = dt_bytes(d->rdt) * a.K;
-        a.router = make(re * E, d->router);
-        if (d->shared_gate) a.sgate = make(re * a.S, d->shared_gate);
+        Owner tmp;  // the router as given, while it is laid out
+        auto stage = [&](size_t bytes, const void* src) -> void* {
+            void* p = nullptr;
+            if (src && e == cudaSuccess && (e = tmp.alloc(&p, bytes)) == cudaSuccess)
+                e = cudaMemcpyAsync(p, src, bytes, cudaMemcpyDefault, s);
+            return p;
+        };
+        const void* w = stage(re * E, d->router);
+        const void* sg = stage(re * a.S, d->shared_gate);
+        uint4* frag = static_cast<uint4*>(make(a.rfrag_elems * 16, nullptr));
+        int* rexp = static_cast<int*>(make((size_t)a.rtiles * 16 * 4, nullptr));
+        if (e == cudaSuccess) e = launch_router_layout(a, w, sg, dt_code(d->rdt), frag, rexp, s);
+        a.rfrag = frag;
+        a.rexp = rexp;
         if (d->bias) a.bias = static_cast<float*>(make((size_t)E * 4, d->bias));
         a.logits = static_cast<float*>(make(a.logit_elems * 4, nullptr));
         a.ids = static_cast<int32_t*>(make(rows * nsel * 4, nullptr));
@@ -468,6 +483,7 @@ qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const
         a.ticket = reinterpret_cast<unsigned long long*>(words);
         a.err = reinterpret_cast<int*>(words + 8);
         const cudaError_t e2 = cudaStreamSynchronize(s);
+        tmp.release();
         if (e == cudaSuccess) e = e2;
         if (e != cudaSuccess) {
             h->mem.release();
@@ -507,7 +523,7 @@ qmlp_status qmlp_moe_layer_forward(qmlp_moe_layer_t* h, const void* x, qmlp_dtyp
     a.odt = dt_code(odt);
     a.ids_out = ids;
     a.w_out = weights;
-    if (moe_layer_few(M, a.K, a.E, std::min(a.E, M * a.topk) + a.S))
+    if (moe_layer_few(M, a.K, a.I, a.E, a.S, a.topk, h->moe->meta))
         return from_cuda(launch_moe_layer_few(a, h->moe->meta, h->moe->num_sms, s));
     cudaError_t e = launch_moe_router(a, s);
     if (e == cudaSuccess)

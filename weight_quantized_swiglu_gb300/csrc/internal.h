@@ -420,9 +420,13 @@ struct MoeLayerArgs {
     int M = 0, E = 0, S = 0, K = 0, I = 0, topk = 0;  // E routed experts, S shared ones behind them in the banks
     bool softmax = true, renorm = true;
     float rscale = 1.0f;
-    int rdt = 1;                    // router and shared gates: 0 fp32, 1 bf16, 2 fp16
-    const void* router = nullptr;   // [E, K]
-    const void* sgate = nullptr;    // [S, K], or null
+    // router and shared gates as fragments (router_frag_kernel): planes of fp16 words,
+    // tiles of 16 rows; the rows' exponents [16 rtiles]
+    const uint4* rfrag = nullptr;
+    const int* rexp = nullptr;
+    size_t rfrag_elems = 0;
+    int planes = 1, rtiles = 0;
+    bool sgate = false;             // the shared experts have gates: rows E..E + S - 1
     const float* bias = nullptr;    // [E], or null
     const uint8_t *w13 = nullptr, *w13_meta = nullptr, *w2 = nullptr, *w2_meta = nullptr;  // the handle's banks
     const void* x = nullptr;        // [M, K]
@@ -431,7 +435,7 @@ struct MoeLayerArgs {
     int odt = 1;                    // 0 fp32, 1 bf16, 2 fp16
     int32_t* ids_out = nullptr;     // [M, topk], or null
     float* w_out = nullptr;
-    float* logits = nullptr;        // [max_tokens][E + S]
+    float* logits = nullptr;        // [max_tokens][E + S], few tokens: one such array a split of k
     int32_t* ids = nullptr;         // more tokens: [M][topk + S]
     float* weights = nullptr;
     float* act = nullptr;           // few tokens: [M (topk + S)][I]
@@ -442,7 +446,10 @@ struct MoeLayerArgs {
     int slots = 0;                  // experts that M tokens can name, at most
     size_t w13_bytes = 0, w13_meta_bytes = 0, w2_bytes = 0, w2_meta_bytes = 0, logit_elems = 0, act_elems = 0;
 };
-bool moe_layer_few(int M, int K, int E, int slots);
+constexpr int kMoeRouterSplits = 8;  // splits of the router's k over CTAs, at most
+bool moe_layer_few(int M, int K, int I, int E, int S, int topk, int meta_bytes);
+cudaError_t launch_router_layout(const MoeLayerArgs& a, const void* w, const void* sg, int type, uint4* frag, int* rexp,
+                                 cudaStream_t s);
 cudaError_t launch_moe_layer_few(MoeLayerArgs a, int meta_bytes, int num_sms, cudaStream_t s);
 cudaError_t launch_moe_router(const MoeLayerArgs& a, cudaStream_t s);
 

@@ -14,7 +14,12 @@
 // Few tokens (at most 16): one cooperative kernel, a CTA an SM, in three parts with
 // a grid barrier between them. With one token all of it is latency: the reads of
 // each part depend on the part before.
-//  1. Router: a row for five warps; x goes to shared memory meanwhile.
+//  1. x goes to shared memory as fp16 in the order of the MMAs (bf16 times a power of
+//     two a token: exact within 2^29 of its largest value), and the router is a
+//     product on the same MMAs: its rows are kept as fp16 times a power of two a row
+//     (bf16, fp16: exact within 2^29 of the row's largest; fp32: two fp16 words, 22
+//     bits), in fragments. Sixteen rows a CTA, k split over CTAs and warps; the
+//     CTAs' shares of a logit are added in order by who reads them.
 //  2. Every CTA selects by itself (a warp a token, from the logits in L2), lists
 //     the experts that any token named, and takes its share of their (expert,
 //     eight gate and eight up rows) tiles, ten warps a tile as in moe_awq.cu. All
@@ -26,8 +31,12 @@
 //     2^-11 of a value at most, the only rounding between x and out), W2 times it;
 //     a token's choices are added in their order, fp32. So a token's result does
 //     not depend on the other tokens of the call.
-// More tokens: the same router and selection as two kernels, then the grouped
-// kernels (moe_grouped.cu) with the shared experts as further routes.
+// The weights of parts 2 and 3 come through a ring in shared memory that a producer
+// warp fills with bulk copies: a W13 tile is one run of codes and one of records in
+// the bank, 16 rows of W2 likewise. W2's first ones are on their way before the second
+// barrier. (Where the ring does not fit beside x, the warps load for themselves.)
+// More tokens: router and selection as two kernels, then the grouped kernels
+// (moe_grouped.cu) with the shared experts as further routes.
 #include <algorithm>
 
 #include "common.cuh"
@@ -36,26 +45,39 @@
 namespace qmlp {
 namespace {
 
-constexpr int kTeams = 2;                           // tiles that a CTA has in hand
+constexpr int kTeams = 2;                           // W13 tiles that a CTA has in hand
 constexpr int kWarps = kTeams * kMoeKSplit;         // 20
-constexpr int kThreads = kWarps * 32;
-constexpr int kRowTeams = 4;                        // router rows that a CTA has in hand
-constexpr int kRowWarps = kWarps / kRowTeams;       // 5
-constexpr int kC13 = 4;                             // 64-k chunks that a W13 warp loads at once
-constexpr int kG2 = 10;                             // k16 groups that a W2 warp loads at once
+constexpr int kThreads = kWarps * 32;               // and a producer warp
+constexpr int kC13 = 4;                             // 64-k chunks that a W13 warp takes at once
+constexpr int kG2 = 10;                             // k16 groups that a W2 warp takes at once
+constexpr int kMaxStages = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;         // 2 s
-constexpr int kSmemMax = 224 * 1024;
+constexpr int kSmemMax = 225 * 1024;
 constexpr uint16_t kNone = 0xFFFF;
 
-// Bytes of the shared-memory tables (slots: experts that the tokens can name).
+QMLP_DEV uint32_t u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
+
+// Splits of the router's k over CTAs.
+__host__ __device__ inline int router_splits(int rows, int K, int ctas) {
+    const int tiles = (rows + 15) / 16;
+    int s = ctas / (tiles > 0 ? tiles : 1);
+    if (s > kMoeRouterSplits) s = kMoeRouterSplits;
+    while (s > 1 && K / 32 < 2 * s) --s;
+    return s < 1 ? 1 : s;
+}
+
+// Shared memory of the kernel (slots: experts that the tokens can name).
 struct Layout {
-    int x, coef, ridx, expo, slot_e, mask, sel_e, sel_w, part, bytes;
+    int x, coef, ridx, expo, slot_e, mask, sel_e, sel_w, part, part_bytes, ring;
+    int stage, stages;  // bytes of a ring stage (0: no ring), stages
+    int n2, sp;         // W2: experts of a stage, parts of I that different warps take
+    int bytes;
 };
-__host__ __device__ inline Layout layout(int M, int K, int E, int slots, int NT) {
+__host__ __device__ inline Layout layout(int M, int K, int I, int E, int nsel, int slots, int MB, int NT) {
     Layout l;
-    auto up = [](int b) { return (b + 15) / 16 * 16; };
+    auto up = [](int b) { return (b + 127) / 128 * 128; };
     int at = 0;
-    l.x = at, at += M * K * 2;
+    l.x = at, at += up(M * K * 2);
     l.coef = at, at += up(slots * M * 4);
     l.ridx = at, at += up(slots * M * 2);
     l.expo = at, at += up(slots * M);
@@ -63,8 +85,21 @@ __host__ __device__ inline Layout layout(int M, int K, int E, int slots, int NT)
     l.mask = at, at += up(E * 4);
     l.sel_e = at, at += 16 * 16 * 4;
     l.sel_w = at, at += 16 * 16 * 4;
-    l.part = at, at += 2 * kWarps * 16 * 8 * NT * 4;  // (parts 1 and 3 need less)
-    l.bytes = at;
+    l.part = at, l.part_bytes = 2 * kWarps * 16 * 8 * NT * 4, at += l.part_bytes;
+    l.ring = at;
+    const int item13 = (int)(kMoeKSplit * (moe_w13_block_bytes(K) + moe_w13_meta_block_bytes(K, MB)));
+    const int item2 = 16 * (I / 2) + 16 * (I / 32) * MB;
+    l.stage = up(item13 > item2 ? item13 : item2);
+    l.stages = (kSmemMax - at) / l.stage;
+    if (l.stages > kMaxStages) l.stages = kMaxStages;
+    if (l.stages < 2) l.stage = l.stages = 0;
+    l.n2 = l.stage ? l.stage / item2 : slots;
+    if (l.n2 > 32) l.n2 = 32;
+    // where the experts of a stage are few, parts of I go to different warps
+    l.sp = 1;
+    const int per = l.n2 < slots ? l.n2 : slots;
+    while (l.sp < 8 && 2 * l.sp * per <= kWarps && I / 32 >= 4 * l.sp && M * nsel * 2 * l.sp * 64 <= l.part_bytes) l.sp *= 2;
+    l.bytes = at + l.stage * l.stages;
     return l;
 }
 
@@ -101,29 +136,6 @@ QMLP_DEV float wsum(float v) {
     return v;
 }
 
-// Row `row` of the router, then of the shared gates, times up to 16 tokens, over
-// the chunks of 8 k of `threads` threads: this thread's sums.
-QMLP_DEV void row_dots(const MoeLayerArgs& a, const void* x, int M, int row, int tid, int threads, float (&acc)[16]) {
-#pragma unroll
-    for (int m = 0; m < 16; ++m) acc[m] = 0.0f;
-    const bool sh = row >= a.E;
-    const void* w = sh ? a.sgate : a.router;
-    const size_t base = (size_t)(sh ? row - a.E : row) * a.K;
-    for (int c = tid; c < a.K / 8; c += threads) {
-        float wv[8];
-        load8t(w, a.rdt, base + 8 * c, wv);
-#pragma unroll
-        for (int m = 0; m < 16; ++m) {
-            if (m < M) {
-                float xv[8];
-                load8t(x, a.x_bf16 ? 1 : 2, (size_t)m * a.K + 8 * c, xv);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[m] = fmaf(wv[e], xv[e], acc[m]);
-            }
-        }
-    }
-}
-
 // A float as an unsigned number of the same order, above 1; NaN is 1, the lowest.
 QMLP_DEV uint32_t order_key(float v) {
     if (v != v) return 1u;
@@ -132,20 +144,30 @@ QMLP_DEV uint32_t order_key(float v) {
     return max(k, 2u);
 }
 
-// One warp selects for one token: logits l[0..E) (then the shared gates'), its
-// choices to sel_e / sel_w in order (the shared experts after the routed ones).
+// One warp selects for one token: its logits are the sums of `splits` shares, `hop`
+// apart, from l on (E routed experts, then the shared gates). Its choices go to
+// sel_e / sel_w in order, the shared experts after the routed ones.
 template <int NPL>
-QMLP_DEV void select(const MoeLayerArgs& a, const float* l, int lane, int* sel_e, float* sel_w) {
+QMLP_DEV void select(const MoeLayerArgs& a, const float* l, int splits, size_t hop, int lane, int* sel_e, float* sel_w) {
     float v[NPL];
     float mx = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const int e = i * 32 + lane;
         v[i] = e < a.E ? __ldcg(l + e) : -INFINITY;
-        mx = fmaxf(mx, v[i]);
     }
-    float lsh = 0.0f;
-    if (a.sgate && lane < a.S) lsh = __ldcg(l + a.E + lane);
+    float lsh = a.sgate && lane < a.S ? __ldcg(l + a.E + lane) : 0.0f;
+    for (int s = 1; s < splits; ++s) {
+        const float* ls = l + s * hop;
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) {
+            const int e = i * 32 + lane;
+            if (e < a.E) v[i] += __ldcg(ls + e);
+        }
+        if (a.sgate && lane < a.S) lsh += __ldcg(ls + a.E + lane);
+    }
+#pragma unroll
+    for (int i = 0; i < NPL; ++i) mx = fmaxf(mx, v[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     float total = 1.0f;  // softmax, without renorming or with a bias: p itself is wanted
@@ -162,47 +184,121 @@ QMLP_DEV void select(const MoeLayerArgs& a, const float* l, int lane, int* sel_e
     for (int i = 0; i < NPL; ++i) {
         const int e = i * 32 + lane;
         // without a bias the logits have the scores' order
-        key[i] = e < a.E ? order_key(a.bias ? score(v[i]) + __ldg(a.bias + e) : v[i]) : 0u;
+        float k = v[i];
+        if (a.bias && e < a.E) k = score(k) + __ldg(a.bias + e);
+        key[i] = e < a.E ? order_key(k) : 0u;
     }
-    float mine = 0.0f;  // lane r: the score of choice r
+    float mine = 0.0f;  // lane r: the logit of choice r
     for (int r = 0; r < a.topk; ++r) {
         uint32_t best = 0;
         int at = 0;
+        float val = 0.0f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i)
             if (key[i] > best) {
                 best = key[i];
                 at = i;
+                val = v[i];
             }
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
         const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
-        float s = 0.0f;
-        if ((int)(e & 31u) == lane) {
+        val = __shfl_sync(0xffffffffu, val, (int)(e & 31u));
+        const int gone = (int)(e & 31u) == lane ? (int)(e >> 5) : -1;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i)
-                if (i == (int)(e >> 5)) {
-                    s = score(v[i]);
-                    key[i] = 0u;
-                }
-        }
-        s = __shfl_sync(0xffffffffu, s, (int)(e & 31u));
+        for (int i = 0; i < NPL; ++i)
+            if (i == gone) key[i] = 0u;
         if (lane == r) {
-            mine = s;
+            mine = val;
             sel_e[r] = (int)e;
         }
     }
-    const float sum = a.renorm ? wsum(lane < a.topk ? mine : 0.0f) : 1.0f;
-    if (lane < a.topk) sel_w[lane] = mine / sum * a.rscale;
+    const float p = lane < a.topk ? score(mine) : 0.0f;
+    const float sum = a.renorm ? wsum(p) : 1.0f;
+    if (lane < a.topk) sel_w[lane] = p / sum * a.rscale;
     if (lane < a.S) {
         sel_e[a.topk + lane] = a.E + lane;
         sel_w[a.topk + lane] = a.sgate ? 1.0f / (1.0f + expf(-lsh)) : 1.0f;
     }
 }
-QMLP_DEV void select_any(const MoeLayerArgs& a, const float* l, int lane, int* sel_e, float* sel_w) {
-    if (a.E <= 64) select<2>(a, l, lane, sel_e, sel_w);
-    else if (a.E <= 256) select<8>(a, l, lane, sel_e, sel_w);
-    else if (a.E <= 512) select<16>(a, l, lane, sel_e, sel_w);
-    else select<32>(a, l, lane, sel_e, sel_w);
+QMLP_DEV void select_any(const MoeLayerArgs& a, const float* l, int splits, size_t hop, int lane, int* sel_e, float* sel_w) {
+    if (a.E <= 64) select<2>(a, l, splits, hop, lane, sel_e, sel_w);
+    else if (a.E <= 256) select<8>(a, l, splits, hop, lane, sel_e, sel_w);
+    else if (a.E <= 512) select<16>(a, l, splits, hop, lane, sel_e, sel_w);
+    else select<32>(a, l, splits, hop, lane, sel_e, sel_w);
+}
+
+// Sixteen rows of the router times NT tiles of eight tokens over pairs of steps
+// (32 k) j0 + w, w + hop, ... < j1, both planes of an fp32 router: fragments of 1 KB a
+// pair, [plane][tile][pair][2][lane] of 16 bytes.
+template <int NT>
+QMLP_DEV void router_tile(const MoeLayerArgs& a, const uint4* xsm, int M, int tile, int j0, int j1, int hop, int lane,
+                          float (&d)[NT][4]) {
+    const int g = lane >> 2, t = lane & 3, n32 = a.K / 32;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+    for (int pl = 0; pl < a.planes; ++pl) {
+        const uint4* f = a.rfrag + ((size_t)(pl * a.rtiles + tile) * n32) * 64 + lane;
+#pragma unroll 2
+        for (int j = j0; j < j1; j += hop) {
+            if (!QMLP_INB((size_t)(f - a.rfrag) + (size_t)j * 64 + 32, a.rfrag_elems, 105)) continue;
+            const uint4 a0 = __ldg(f + (size_t)j * 64), a1 = __ldg(f + (size_t)j * 64 + 32);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 x = xsm[(j * M + min(8 * n + g, M - 1)) * 4 + t];
+                mma_f16_16816(d[n], a0.x, a0.y, a0.z, a0.w, x.x, x.y);
+                mma_f16_16816(d[n], a1.x, a1.y, a1.z, a1.w, x.z, x.w);
+            }
+        }
+    }
+}
+// x [M, K] -> fp16 in the order of the MMAs, by `threads` threads: slot (j M + m) 4 + t
+// has, of the pair j of steps (32 k), k pairs 2t.. and 8 + 2t.. of token m, then the
+// same of the second step; the tokens' exponents to sig. A thread stays with a token:
+// the row's largest value falls out of the copy, which is then scaled in place.
+template <typename Sync>
+QMLP_DEV void stage_x(const MoeLayerArgs& a, const void* x, int M, uint4* xsm, int* s_max, int* sig, int threads, Sync sync) {
+    const int K = a.K, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = threads >> 5;
+    const int wpt = max(1, nw / M);  // warps a token
+    if (threadIdx.x < 16) s_max[threadIdx.x] = 0;
+    sync();
+    uint32_t* xw = reinterpret_cast<uint32_t*>(xsm);
+    for (int m = warp / wpt; m < M; m += nw / wpt) {
+        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + (size_t)m * K);
+        float mx = 0.0f;
+#pragma unroll 4
+        for (int q = (warp % wpt) * 32 + lane; q < K / 8; q += 32 * wpt) {
+            const uint4 v = row[q];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            // words 4 q'.. of a pair's 16: word i of them to slot t = i, place q'
+            const int at = ((q >> 2) * M + m) * 16 + (q & 3);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xw[at + 4 * i] = w[i];
+                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
+            }
+        }
+        if (a.x_bf16) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (lane == 0) atomicMax(s_max + m, __float_as_int(mx));
+        }
+    }
+    sync();
+    if (threadIdx.x < 16) sig[threadIdx.x] = a.x_bf16 ? prescale_exponent(__int_as_float(s_max[threadIdx.x])) : 0;
+    if (a.x_bf16)
+        for (int i = threadIdx.x; i < K / 8 * M; i += threads) {
+            const int sg = prescale_exponent(__int_as_float(s_max[(i >> 2) % M]));
+            const float p0 = __int_as_float((127 + (sg >> 1)) << 23), p1 = __int_as_float((127 + sg - (sg >> 1)) << 23);
+            const uint4 u = xsm[i];
+            uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = u32(__floats2half2_rn(__uint_as_float(v[j] << 16) * p0 * p1, __uint_as_float(v[j] & 0xFFFF0000u) * p0 * p1));
+            xsm[i] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    sync();
 }
 
 // ---------------------------------------------------------------------------
@@ -240,29 +336,25 @@ struct Batch13 {
     uint32_t c[kC13][2][2];  // [chunk][gate, up][unit]
     uint32_t m[kC13][2][2];
 };
+// codes, meta: the warp's block of codes and of records; at: its first chunk.
 template <int MB>
-QMLP_DEV void load13(Batch13<MB>& b, const MoeLayerArgs& a, size_t blk, int at, int lane) {
-    const int g = lane >> 2, np = moe_w13_pairs(a.K), ms = moe_w13_meta_stride(a.K, MB);
-    const uint8_t* codes = a.w13 + blk * moe_w13_block_bytes(a.K);
-    if (!QMLP_INB((blk + 1) * moe_w13_block_bytes(a.K) - 1, a.w13_bytes, 101) ||
-        !QMLP_INB((blk + 1) * moe_w13_meta_block_bytes(a.K, MB) - 1, a.w13_meta_bytes, 102))
-        return;
+QMLP_DEV void load13(Batch13<MB>& b, const uint8_t* codes, const uint8_t* meta, int np, int ms, int at, int lane) {
+    const int g = lane >> 2;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
 #pragma unroll
         for (int pi = 0; pi < kC13 / 2; ++pi) {
             const int pp = at / 2 + pi;
             uint4 u = make_uint4(0, 0, 0, 0);
-            if (pp < np) u = __ldg(reinterpret_cast<const uint4*>(codes + (size_t)(q * np + pp) * 512) + lane);
+            if (pp < np) u = *(reinterpret_cast<const uint4*>(codes + (q * np + pp) * 512) + lane);
             b.c[2 * pi][q][0] = u.x;
             b.c[2 * pi][q][1] = u.y;
             b.c[2 * pi + 1][q][0] = u.z;
             b.c[2 * pi + 1][q][1] = u.w;
         }
-        const uint8_t* slot =
-            a.w13_meta + blk * moe_w13_meta_block_bytes(a.K, MB) + (q * 8 + g) * ms + (size_t)at * 2 * MB;
+        const uint8_t* slot = meta + (q * 8 + g) * ms + at * 2 * MB;
         if (MB == 4) {
-            const uint4 m0 = __ldg(reinterpret_cast<const uint4*>(slot)), m1 = __ldg(reinterpret_cast<const uint4*>(slot) + 1);
+            const uint4 m0 = *reinterpret_cast<const uint4*>(slot), m1 = *(reinterpret_cast<const uint4*>(slot) + 1);
             const uint32_t mr[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
             for (int i = 0; i < kC13; ++i) b.m[i][q][0] = mr[2 * i], b.m[i][q][1] = mr[2 * i + 1];
@@ -270,7 +362,7 @@ QMLP_DEV void load13(Batch13<MB>& b, const MoeLayerArgs& a, size_t blk, int at, 
             uint32_t mr[3 * kC13 / 2 + 1];
 #pragma unroll
             for (int j = 0; j < 3 * kC13 / 4; ++j) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(slot) + j);
+                const uint2 v = *(reinterpret_cast<const uint2*>(slot) + j);
                 mr[2 * j] = v.x;
                 mr[2 * j + 1] = v.y;
             }
@@ -291,28 +383,21 @@ template <int MB>
 struct Batch2 {
     uint32_t c[kG2 / 2][2], m[kG2 / 2][2];
 };
+// codes, meta: rows n0.. of the expert; u0, u1: units of 32 k.
 template <int MB>
-QMLP_DEV void load2(Batch2<MB>& b, const MoeLayerArgs& a, int e, int n0, int gb, int lane) {
-    const int g = lane >> 2, t = lane & 3, gpr = a.I / 32;
-    const size_t row0 = (size_t)e * a.K + n0 + g;
-    if (!QMLP_INB((row0 + 9) * (a.I / 2) - 1, a.w2_bytes, 103) ||
-        !QMLP_INB((row0 + 9) * gpr * MB - 1, a.w2_meta_bytes, 104))
-        return;
+QMLP_DEV void load2(Batch2<MB>& b, const uint8_t* codes, const uint8_t* meta, int I, int u0, int u1, int lane) {
+    const int g = lane >> 2, t = lane & 3, gpr = I / 32;
 #pragma unroll
     for (int i = 0; i < kG2 / 2; ++i) {
-        const int u = gb / 2 + i;  // unit of 32 k
         b.c[i][0] = b.c[i][1] = b.m[i][0] = b.m[i][1] = 0u;
-        if (u < gpr) {
+        if (u0 + i < u1) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const size_t row = row0 + 8 * h;
-                b.c[i][h] = __ldg(reinterpret_cast<const unsigned int*>(a.w2 + row * (a.I / 2) + 16 * u) + t);
-                const uint8_t* mp = a.w2_meta + (row * gpr + u) * MB;
-                if (MB == 4) {
-                    b.m[i][h] = __ldg(reinterpret_cast<const unsigned int*>(mp));
-                } else {
-                    b.m[i][h] = (uint32_t)__ldg(mp) | (uint32_t)__ldg(mp + 1) << 8 | (uint32_t)__ldg(mp + 2) << 16;
-                }
+                const int row = g + 8 * h;
+                b.c[i][h] = *(reinterpret_cast<const unsigned int*>(codes + row * (I / 2) + 16 * (u0 + i)) + t);
+                const uint8_t* mp = meta + (row * gpr + u0 + i) * MB;
+                if (MB == 4) b.m[i][h] = *reinterpret_cast<const unsigned int*>(mp);
+                else b.m[i][h] = (uint32_t)mp[0] | (uint32_t)mp[1] << 8 | (uint32_t)mp[2] << 16;
             }
         }
     }
@@ -353,14 +438,84 @@ QMLP_DEV void store_any(void* p, int type, size_t at, float v) {
     else static_cast<__half*>(p)[at] = __float2half_rn(v);
 }
 
+// Part 3's share of one expert: its rows n0.. (codes, meta) times the tokens' act over
+// units u0..u1 of 32 k, times the weights, to part (choice r of the call: r 16 + row).
 template <int MB, int NT>
-__global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const MoeLayerArgs a) {
+QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t* meta, int u0, int u1, const uint16_t* ridx,
+                      const int8_t* expo, const float* coef, float* part, int lane) {
+    const int M = a.M, I = a.I, g = lane >> 2, t = lane & 3;
+    float d[NT][4];
+    int col[NT];
+    float up[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int m = 8 * n + g;
+        col[n] = m < M ? ridx[m] : kNone;
+        up[n] = m < M ? __int_as_float((127 + expo[m]) << 23) : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+    }
+    for (int ub = u0; ub < u1; ub += kG2 / 2) {
+        uint32_t xb[NT][kG2][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float* row = a.act + (size_t)(col[n] == kNone ? 0 : col[n]) * I + 32 * ub + 2 * t;
+#pragma unroll
+            for (int i = 0; i < kG2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float2 v = make_float2(0.0f, 0.0f);
+                    if (ub + i / 2 < u1 && col[n] != kNone &&
+                        QMLP_INB((size_t)(row - a.act) + 16 * i + 8 * h + 1, a.act_elems, 107))
+                        v = __ldcg(reinterpret_cast<const float2*>(row + 16 * i + 8 * h));
+                    xb[n][i][h] = u32(__floats2half2_rn(v.x * up[n], v.y * up[n]));
+                }
+        }
+        Batch2<MB> b;
+        load2<MB>(b, codes, meta, I, ub, u1, lane);
+#pragma unroll
+        for (int i = 0; i < kG2 / 2; ++i) {
+            if (ub + i < u1) {
+                uint32_t s2[2], b2[2], f[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    meta2<MB>(b.m[i][h], s2[h], b2[h]);
+                    f[h][0] = pair_of<0>(b.c[i][h], s2[h], b2[h]);
+                    f[h][1] = pair_of<1>(b.c[i][h], s2[h], b2[h]);
+                    f[h][2] = pair_of<2>(b.c[i][h], s2[h], b2[h]);
+                    f[h][3] = pair_of<3>(b.c[i][h], s2[h], b2[h]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma_f16_16816(d[n], f[0][0], f[1][0], f[0][1], f[1][1], xb[n][2 * i][0], xb[n][2 * i][1]);
+                    mma_f16_16816(d[n], f[0][2], f[1][2], f[0][3], f[1][3], xb[n][2 * i + 1][0], xb[n][2 * i + 1][1]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int m = 8 * n + 2 * t + e;
+            const int r = m < M ? ridx[m] : kNone;
+            if (r != kNone) {  // a choice of token m: its rows g and g + 8
+                const float w = coef[m];
+                part[r * 16 + g] = w * d[n][e];
+                part[r * 16 + g + 8] = w * d[n][2 + e];
+            }
+        }
+}
+
+template <int MB, int NT, bool RING>
+__global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLayerArgs a) {
     constexpr int kC = 8 * NT;
-    extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int s_pass, s_n, s_sig[16], s_cnt[kWarps];
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ int s_pass, s_n, s_max[16], s_sig[16], s_cnt[kWarps];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
     const int M = a.M, K = a.K, I = a.I, rows = a.E + (a.sgate ? a.S : 0), nsel = a.topk + a.S;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const Layout L = layout(M, K, a.E, a.slots, NT);
+    const Layout L = layout(M, K, I, a.E, nsel, a.slots, MB, NT);
     uint4* xsm = reinterpret_cast<uint4*>(sm + L.x);
     float* coef = reinterpret_cast<float*>(sm + L.coef);          // [slot][M]
     uint16_t* ridx = reinterpret_cast<uint16_t*>(sm + L.ridx);    // [slot][M]: row of act
@@ -370,65 +525,48 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const MoeLayerAr
     int* sel_e = reinterpret_cast<int*>(sm + L.sel_e);            // [16][16]
     float* sel_w = reinterpret_cast<float*>(sm + L.sel_w);
     float* part = reinterpret_cast<float*>(sm + L.part);
-
-    // ---------------- 1: router ----------------
-    {
-        const int rt = warp / kRowWarps, tid = threadIdx.x - rt * kRowWarps * 32;
-        for (int row = blockIdx.x + rt * gridDim.x; row < rows; row += kRowTeams * gridDim.x) {
-            float acc[16];
-            row_dots(a, a.x, M, row, tid, kRowWarps * 32, acc);
-            float* pr = part + rt * kRowWarps * 16;
-#pragma unroll
-            for (int m = 0; m < 16; ++m)
-                if (m < M) {
-                    const float s = wsum(acc[m]);
-                    if (lane == 0) pr[(warp % kRowWarps) * 16 + m] = s;
-                }
-            named_bar_sync(1 + rt, kRowWarps * 32);
-            if (tid < M) {
-                float s = 0.0f;
-                for (int w = 0; w < kRowWarps; ++w) s += pr[w * 16 + tid];
-                if (QMLP_INB((size_t)tid * (a.E + a.S) + row, a.logit_elems, 105)) a.logits[(size_t)tid * (a.E + a.S) + row] = s;
-            }
-            named_bar_sync(1 + rt, kRowWarps * 32);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
+    const int splits = router_splits(rows, K, gridDim.x), ctile = (rows + 15) / 16;
+    const size_t hop = (size_t)M * (a.E + a.S);  // between the splits' shares of the logits
+    if (RING && threadIdx.x == 0) {
+        for (int s = 0; s < L.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), kMoeKSplit);  // a team; W2's stages: every warp, see below
         }
+        fence_mbar_init();
     }
-    // the largest |act| of each row of act, for part 2
+
+    // ---------------- 1: x, router ----------------
     for (int i = blockIdx.x * kThreads + threadIdx.x; i < M * nsel; i += gridDim.x * kThreads) a.amax[i] = 0;
     for (int e = threadIdx.x; e < a.E; e += kThreads) mask[e] = 0;
-    // x -> fp16 in the order of the MMAs: slot ((c 2 + jj) M + m) 4 + t has, of chunk
-    // c (64 k) and its steps 2jj and 2jj + 1, k pairs 2t.. and 8 + 2t.. of token m
-    if (a.x_bf16) {
-        for (int m = warp; m < M; m += kWarps) {
-            float mx = 0.0f;
-            for (int c = lane; c < K / 8; c += 32) {
-                float v[8];
-                load8t(a.x, 1, (size_t)m * K + 8 * c, v);
+    if (warp < kWarps) {
+        stage_x(a, a.x, M, xsm, s_max, s_sig, kThreads, [] { named_bar_sync(1, kThreads); });
+        const int n32 = K / 32;
+        for (int u = blockIdx.x; u < ctile * splits; u += gridDim.x) {
+            const int tile = u / splits, sp = u % splits;
+            const int j0 = (int)((long)sp * n32 / splits), j1 = (int)((long)(sp + 1) * n32 / splits);
+            float d[NT][4];
+            router_tile<NT>(a, xsm, M, tile, j0 + warp, j1, kWarps, lane, d);
+            if (u != (int)blockIdx.x) named_bar_sync(1, kThreads);  // the sums before are read
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+            for (int n = 0; n < NT; ++n) {
+                *reinterpret_cast<float2*>(part + (warp * 16 + g) * kC + 8 * n + 2 * t) = make_float2(d[n][0], d[n][1]);
+                *reinterpret_cast<float2*>(part + (warp * 16 + g + 8) * kC + 8 * n + 2 * t) = make_float2(d[n][2], d[n][3]);
             }
+            named_bar_sync(1, kThreads);
+            for (int i = threadIdx.x; i < 16 * M; i += kThreads) {
+                const int r = i & 15, m = i >> 4, row = tile * 16 + r;
+                if (row < rows) {
+                    float v = 0.0f;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) s_sig[m] = prescale_exponent(mx);
-        }
-    } else if (threadIdx.x < 16) {
-        s_sig[threadIdx.x] = 0;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < (K / 64) * 2 * M * 4; i += kThreads) {
-        const int tt = i & 3, m = (i >> 2) % M, cj = (i >> 2) / M;
-        const uint32_t* row = static_cast<const uint32_t*>(a.x) + (size_t)m * (K / 2) + cj * 16 + tt;
-        uint32_t v[4] = {__ldg(row), __ldg(row + 4), __ldg(row + 8), __ldg(row + 12)};
-        if (a.x_bf16) {
-            const int sg = s_sig[m];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const __half2 h = __floats2half2_rn(scalbnf(__uint_as_float(v[j] << 16), sg),
-                                                    scalbnf(__uint_as_float(v[j] & 0xFFFF0000u), sg));
-                v[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    for (int w = 0; w < kWarps; ++w) v += part[(w * 16 + r) * kC + m];
+                    const size_t at = sp * hop + (size_t)m * (a.E + a.S) + row;
+                    if (QMLP_INB(at, a.logit_elems, 105)) a.logits[at] = scalbnf(v, -s_sig[m] - a.rexp[row]);
+                }
             }
         }
-        xsm[i] = make_uint4(v[0], v[1], v[2], v[3]);
     }
     if (!grid_barrier(a, &s_pass)) {
         if (threadIdx.x == 0) atomicAdd(a.ticket, 1ull);  // the second barrier's count
@@ -436,76 +574,168 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const MoeLayerAr
     }
 
     // ---------------- 2: selection, W13 ----------------
-    if (warp < M) select_any(a, a.logits + (size_t)warp * (a.E + a.S), lane, sel_e + warp * 16, sel_w + warp * 16);
+    if (warp < M) select_any(a, a.logits + (size_t)warp * (a.E + a.S), splits, hop, lane, sel_e + warp * 16, sel_w + warp * 16);
     __syncthreads();
-    for (int i = threadIdx.x; i < M * a.topk; i += kThreads) atomicOr(&mask[sel_e[(i / a.topk) * 16 + i % a.topk]], 1u << (i / a.topk));
-    __syncthreads();
-    // the experts named, in their order, then the shared ones
-    const int per = (a.E + kWarps - 1) / kWarps;  // experts a warp, its lanes side by side
-    {
-        int n = 0;
-        for (int b = 0; b < per; b += 32) {
-            const int e = warp * per + b + lane;
-            n += __popc(__ballot_sync(0xffffffffu, b + lane < per && e < a.E && mask[e] != 0));
+    int slots;
+    if (M == 1) {  // the choices are the list
+        slots = nsel;
+        if ((int)threadIdx.x < nsel) {
+            slot_e[threadIdx.x] = sel_e[threadIdx.x];
+            ridx[threadIdx.x] = (uint16_t)threadIdx.x;
+            coef[threadIdx.x] = sel_w[threadIdx.x];
         }
-        if (lane == 0) s_cnt[warp] = n;
-    }
-    __syncthreads();
-    {
-        int at = 0;
-        for (int w = 0; w < warp; ++w) at += s_cnt[w];
-        for (int b = 0; b < per; b += 32) {
-            const int e = warp * per + b + lane;
-            const bool on = b + lane < per && e < a.E && mask[e] != 0;
-            const uint32_t vote = __ballot_sync(0xffffffffu, on);
-            if (on) {
-                const int s = at + __popc(vote & ((1u << lane) - 1));
-                slot_e[s] = e;
-                mask[e] = (uint32_t)s;
+    } else {
+        for (int i = threadIdx.x; i < M * a.topk; i += kThreads + 32)
+            atomicOr(&mask[sel_e[(i / a.topk) * 16 + i % a.topk]], 1u << (i / a.topk));
+        __syncthreads();
+        // the experts named, in their order, then the shared ones: experts a warp, its
+        // lanes side by side
+        const int per = (a.E + kWarps - 1) / kWarps;
+        if (warp < kWarps) {
+            int n = 0;
+            for (int b = 0; b < per; b += 32) {
+                const int e = warp * per + b + lane;
+                n += __popc(__ballot_sync(0xffffffffu, b + lane < per && e < a.E && mask[e] != 0));
             }
-            at += __popc(vote);
+            if (lane == 0) s_cnt[warp] = n;
         }
-        if (warp == kWarps - 1 && lane == 0) s_n = at;
-    }
-    __syncthreads();
-    const int named = s_n, slots = named + a.S;
-    for (int i = threadIdx.x; i < slots * M; i += kThreads) {
-        ridx[i] = kNone;
-        coef[i] = 0.0f;
-    }
-    for (int j = threadIdx.x; j < a.S; j += kThreads) slot_e[named + j] = a.E + j;
-    __syncthreads();
-    for (int i = threadIdx.x; i < M * nsel; i += kThreads) {
-        const int m = i / nsel, r = i % nsel, e = sel_e[m * 16 + r];
-        const int s = r < a.topk ? (int)mask[e] : named + r - a.topk;
-        ridx[s * M + m] = (uint16_t)i;
-        coef[s * M + m] = sel_w[m * 16 + r];
-        if (blockIdx.x == 0 && r < a.topk) {
-            if (a.ids_out) a.ids_out[m * a.topk + r] = e;
-            if (a.w_out) a.w_out[m * a.topk + r] = sel_w[m * 16 + r];
+        __syncthreads();
+        if (warp < kWarps) {
+            int at = 0;
+            for (int w = 0; w < warp; ++w) at += s_cnt[w];
+            for (int b = 0; b < per; b += 32) {
+                const int e = warp * per + b + lane;
+                const bool on = b + lane < per && e < a.E && mask[e] != 0;
+                const uint32_t vote = __ballot_sync(0xffffffffu, on);
+                if (on) {
+                    const int s = at + __popc(vote & ((1u << lane) - 1));
+                    slot_e[s] = e;
+                    mask[e] = (uint32_t)s;
+                }
+                at += __popc(vote);
+            }
+            if (warp == kWarps - 1 && lane == 0) s_n = at;
+        }
+        __syncthreads();
+        const int named = s_n;
+        slots = named + a.S;
+        for (int i = threadIdx.x; i < slots * M; i += kThreads + 32) {
+            ridx[i] = kNone;
+            coef[i] = 0.0f;
+        }
+        for (int j = threadIdx.x; j < a.S; j += kThreads + 32) slot_e[named + j] = a.E + j;
+        __syncthreads();
+        for (int i = threadIdx.x; i < M * nsel; i += kThreads + 32) {
+            const int m = i / nsel, r = i % nsel;
+            const int s = r < a.topk ? (int)mask[sel_e[m * 16 + r]] : named + r - a.topk;
+            ridx[s * M + m] = (uint16_t)i;
+            coef[s * M + m] = sel_w[m * 16 + r];
         }
     }
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < M * a.topk; i += kThreads + 32) {
+            const int m = i / a.topk, r = i % a.topk;
+            if (a.ids_out) a.ids_out[i] = sel_e[m * 16 + r];
+            if (a.w_out) a.w_out[i] = sel_w[m * 16 + r];
+        }
     __syncthreads();
-    {
+
+    const int no = I / 8, items = slots * no, np = moe_w13_pairs(K), ms = moe_w13_meta_stride(K, MB), cpw = moe_w13_cpw(K);
+    const int cb = (int)moe_w13_block_bytes(K), mb = (int)moe_w13_meta_block_bytes(K, MB);  // a warp's blocks
+    const int cb2 = 16 * (I / 2), mb2 = 16 * (I / 32) * MB;                                  // 16 rows of W2
+    const int n13 = items > (int)blockIdx.x ? (items - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;  // this CTA's tiles
+    const int tiles2 = K / 16 > (int)blockIdx.x ? (K / 16 - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+    const int st2 = (slots + L.n2 - 1) / L.n2, n2 = tiles2 * st2;  // stages of W2: an expert group of a tile each
+    // ---------------- the producer's side of the ring ----------------
+    bool ok = true;
+    auto claim = [&](int it) {  // stage it % L.stages is free
+        if (it < L.stages) return true;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty(it % L.stages), (uint32_t)((it / L.stages - 1) & 1), a.limit))) {
+            if (lane == 0) atomicExch(a.err, 102);
+            ok = false;
+        }
+        return ok;
+    };
+    auto send13 = [&](int it) {
+        const int s = it % L.stages, item = blockIdx.x + it * gridDim.x;
+        const size_t blk = ((size_t)slot_e[item / no] * no + item % no) * kMoeKSplit;
+        if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)(kMoeKSplit * (cb + mb)));
+        __syncwarp();
+        const uint32_t dst = smem_u32(sm + L.ring) + (uint32_t)(s * L.stage);
+        if (lane == 0) {
+            const uint8_t* p = a.w13 + blk * cb;
+            if (!QMLP_INB((blk + kMoeKSplit) * cb - 1, a.w13_bytes, 101)) p = a.w13;
+            bulk_g2s(dst, p, (uint32_t)(kMoeKSplit * cb), full(s));
+        } else if (lane == 1) {
+            const uint8_t* p = a.w13_meta + blk * mb;
+            if (!QMLP_INB((blk + kMoeKSplit) * mb - 1, a.w13_meta_bytes, 102)) p = a.w13_meta;
+            bulk_g2s(dst + (uint32_t)(kMoeKSplit * cb), p, (uint32_t)(kMoeKSplit * mb), full(s));
+        }
+    };
+    auto send2 = [&](int it) {  // it counts on from W13's
+        const int s = it % L.stages, j = it - n13, s0 = j % st2 * L.n2, n = min(L.n2, slots - s0);
+        const int tile = blockIdx.x + j / st2 * gridDim.x;
+        if (lane == 0) mbar_arrive_expect_tx(full(s), (uint32_t)(n * (cb2 + mb2)));
+        __syncwarp();
+        if (lane < n) {
+            const size_t row = (size_t)slot_e[s0 + lane] * K + 16 * tile;
+            const uint32_t dst = smem_u32(sm + L.ring) + (uint32_t)(s * L.stage + lane * (cb2 + mb2));
+            const uint8_t *p = a.w2 + row * (I / 2), *q = a.w2_meta + row * (I / 32) * MB;
+            if (!QMLP_INB((row + 16) * (I / 2) - 1, a.w2_bytes, 103)) p = a.w2;
+            if (!QMLP_INB((row + 16) * (I / 32) * MB - 1, a.w2_meta_bytes, 104)) q = a.w2_meta;
+            bulk_g2s(dst, p, (uint32_t)cb2, full(s));
+            bulk_g2s(dst + (uint32_t)cb2, q, (uint32_t)mb2, full(s));
+        }
+    };
+    int sent = 0;
+    if (RING && warp == kWarps) {
+        for (; sent < n13 && claim(sent); ++sent) send13(sent);
+        // what fits of W2 (every stage of W13 is consumed before the barrier)
+        for (; ok && sent < n13 + min(n2, L.stages) && claim(sent); ++sent) send2(sent);
+    }
+    bool late = false;
+    auto arrived = [&](int it) {
+        const uint32_t bar = full(it % L.stages), par = (uint32_t)((it / L.stages) & 1);
+        if (mbar_try_wait(bar, par)) return;
+        if (!mbar_wait_bounded(bar, par, late ? 0 : a.limit)) {
+            atomicExch(a.err, 103);  // (what is then read lies in the ring; out is not valid)
+            late = true;
+        }
+    };
+
+    if (warp < kWarps) {
         const int team = warp / kMoeKSplit, ks = warp % kMoeKSplit, tid = threadIdx.x - team * kMoeKSplit * 32;
-        const int no = I / 8, items = slots * no, stride = kTeams * gridDim.x;
-        const int Kc = K / 64, cpw = moe_w13_cpw(K), c0 = ks * cpw, nc = max(0, min(Kc, c0 + cpw) - c0);
+        const int Kc = K / 64, c0 = ks * cpw, nc = max(0, min(Kc, c0 + cpw) - c0);
         Batch13<MB> b;
-        int item = blockIdx.x + team * gridDim.x;
-        auto block = [&](int it) { return ((size_t)slot_e[it / no] * no + it % no) * kMoeKSplit + ks; };
-        if (item < items && nc > 0) load13<MB>(b, a, block(item), 0, lane);
-        for (int turn = 0; item < items; item += stride, turn ^= 1) {
-            const int s = item / no, oct = item % no;
+        int turn = 0;
+        for (int it = team; it < n13; it += kTeams, turn ^= 1) {
+            const int item = blockIdx.x + it * gridDim.x, s = item / no, oct = item % no;
+            const size_t blk = ((size_t)slot_e[s] * no + oct) * kMoeKSplit + ks;
+            const uint8_t *codes = a.w13 + blk * cb, *meta = a.w13_meta + blk * mb;
+            if (RING) {
+                arrived(it);
+                codes = sm + L.ring + (it % L.stages) * L.stage + ks * cb;
+                meta = sm + L.ring + (it % L.stages) * L.stage + kMoeKSplit * cb + ks * mb;
+            }
             float d[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
-            for (int cb = 0; cb < nc; cb += kC13) {
-                if (cb > 0) load13<MB>(b, a, block(item), cb, lane);
+            for (int ch = 0; ch < nc; ch += kC13) {
+                if (RING) {
+                    load13<MB>(b, sm + L.ring + (it % L.stages) * L.stage + ks * cb,
+                               sm + L.ring + (it % L.stages) * L.stage + kMoeKSplit * cb + ks * mb, np, ms, ch, lane);
+                } else if (QMLP_INB((blk + 1) * cb - 1, a.w13_bytes, 101) && QMLP_INB((blk + 1) * mb - 1, a.w13_meta_bytes, 102)) {
+                    load13<MB>(b, codes, meta, np, ms, ch, lane);
+                }
+                if (RING && ch + kC13 >= nc) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(empty(it % L.stages));
+                }
 #pragma unroll
                 for (int i = 0; i < kC13; ++i) {
-                    if (cb + i < nc) {
+                    if (ch + i < nc) {
                         uint32_t s2[2][2], b2[2][2];
 #pragma unroll
                         for (int q = 0; q < 2; ++q)
@@ -523,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const MoeLayerAr
                             }
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                const uint4 x = xsm[(((c0 + cb + i) * 2 + h) * M + min(8 * n + g, M - 1)) * 4 + t];
+                                const uint4 x = xsm[(((c0 + ch + i) * 2 + h) * M + min(8 * n + g, M - 1)) * 4 + t];
                                 mma_f16_16816(d[n], f[0][0], f[1][0], f[0][1], f[1][1], x.x, x.y);
                                 mma_f16_16816(d[n], f[0][2], f[1][2], f[0][3], f[1][3], x.z, x.w);
                             }
@@ -531,8 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const MoeLayerAr
                     }
                 }
             }
-            // the next tile's weights are on their way while this one's sums are added
-            if (item + stride < items && nc > 0) load13<MB>(b, a, block(item + stride), 0, lane);
+            if (RING && nc == 0 && lane == 0) mbar_arrive(empty(it % L.stages));
             float* pt = part + ((turn * kTeams + team) * kMoeKSplit) * 16 * kC;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -542,7 +771,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const MoeLayerAr
             named_bar_sync(1 + team, kMoeKSplit * 32);
             if (tid < 8 * kC) {
                 const int row = tid & 7, m = tid >> 3;
-                float v = 0.0f;
                 if (m < M && ridx[s * M + m] != kNone) {
                     float hg = 0.0f, hu = 0.0f;
 #pragma unroll
@@ -551,22 +779,34 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const MoeLayerAr
                         hu += pt[(w * 16 + 8 + row) * kC + m];
                     }
                     const int sg = s_sig[m], r = ridx[s * M + m];
-                    v = silu_f32(scalbnf(hg, -sg)) * scalbnf(hu, -sg);
+                    const float v = silu_f32(scalbnf(hg, -sg)) * scalbnf(hu, -sg);
                     if (QMLP_INB((size_t)r * I + 8 * oct + row, a.act_elems, 106)) a.act[(size_t)r * I + 8 * oct + row] = v;
-                    v = fabsf(v);
                     // the eight rows of a token are neighbours in a warp; the largest
                     // of them does not depend on the order of the tiles
-                    uint32_t top = __float_as_uint(v);
-                    const uint32_t lanes = 0xFFu << (lane & 24);
-                    top = __reduce_max_sync(lanes, top);
+                    const uint32_t top = __reduce_max_sync(0xFFu << (lane & 24), __float_as_uint(fabsf(v)));
                     if (row == 0) atomicMax(a.amax + r, (int)top);
                 }
             }
         }
     }
-    if (!grid_barrier(a, &s_pass)) return;
+    if (!grid_barrier(a, &s_pass)) {
+        // (copies in flight end before the CTA does)
+        if (RING && warp == kWarps)
+            for (int q = sent - 1; q >= 0 && q >= sent - L.stages; --q)
+                mbar_wait_bounded(full(q % L.stages), (uint32_t)((q / L.stages) & 1), a.limit);
+        return;
+    }
 
     // ---------------- 3: W2 and the weighted sum ----------------
+    if (warp == kWarps) {
+        if (RING) {
+            for (; ok && sent < n13 + n2 && claim(sent); ++sent) send2(sent);
+            if (!ok)
+                for (int q = sent - 1; q >= 0 && q >= sent - L.stages; --q)
+                    mbar_wait_bounded(full(q % L.stages), (uint32_t)((q / L.stages) & 1), a.limit);
+        }
+        return;
+    }
     for (int i = threadIdx.x; i < slots * M; i += kThreads) {
         int e = 0;
         if (ridx[i] != kNone) {
@@ -575,104 +815,65 @@ __global__ void __launch_bounds__(kThreads, 1) moe_layer_kernel(const MoeLayerAr
         }
         expo[i] = (int8_t)e;
     }
-    __syncthreads();
-    const int ng = I / 16;
-    for (int tile = blockIdx.x; tile < K / 16; tile += gridDim.x) {
-        __syncthreads();  // the sums of the tile before are read
-        for (int s = warp; s < slots; s += kWarps) {
-            int col[NT];
-            float up[NT];
-            const float* row[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int m = 8 * n + g;
-                col[n] = m < M ? ridx[s * M + m] : kNone;
-                up[n] = m < M ? __int_as_float((127 + expo[s * M + m]) << 23) : 1.0f;
-                row[n] = a.act + (size_t)(col[n] == kNone ? 0 : col[n]) * I;
-            }
-            float d[NT][4];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
-            for (int gb = 0; gb < ng; gb += kG2) {
-                Batch2<MB> b;
-                load2<MB>(b, a, slot_e[s], 16 * tile, gb, lane);
-                uint32_t xb[NT][kG2][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < kG2; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float2 v = make_float2(0.0f, 0.0f);
-                            if (gb + i < ng && col[n] != kNone &&
-                                QMLP_INB((size_t)col[n] * I + 16 * (gb + i) + 8 * h + 2 * t + 1, a.act_elems, 107))
-                                v = __ldcg(reinterpret_cast<const float2*>(row[n] + 16 * (gb + i) + 8 * h + 2 * t));
-                            const __half2 p = __floats2half2_rn(v.x * up[n], v.y * up[n]);
-                            xb[n][i][h] = *reinterpret_cast<const uint32_t*>(&p);
-                        }
-#pragma unroll
-                for (int i = 0; i < kG2 / 2; ++i) {
-                    if (gb + 2 * i < ng) {
-                        uint32_t s2[2], b2[2], f[2][4];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            meta2<MB>(b.m[i][h], s2[h], b2[h]);
-                            f[h][0] = pair_of<0>(b.c[i][h], s2[h], b2[h]);
-                            f[h][1] = pair_of<1>(b.c[i][h], s2[h], b2[h]);
-                            f[h][2] = pair_of<2>(b.c[i][h], s2[h], b2[h]);
-                            f[h][3] = pair_of<3>(b.c[i][h], s2[h], b2[h]);
-                        }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_f16_16816(d[n], f[0][0], f[1][0], f[0][1], f[1][1], xb[n][2 * i][0], xb[n][2 * i][1]);
-                            mma_f16_16816(d[n], f[0][2], f[1][2], f[0][3], f[1][3], xb[n][2 * i + 1][0],
-                                          xb[n][2 * i + 1][1]);
-                        }
-                    }
+    named_bar_sync(1, kThreads);
+    const int nu = I / 32, prow = M * nsel;
+    for (int tl = 0; tl < tiles2; ++tl) {
+        const int tile = blockIdx.x + tl * gridDim.x;
+        for (int j = 0; j < st2; ++j) {
+            const int it = n13 + tl * st2 + j, s0 = j * L.n2, n = min(L.n2, slots - s0);
+            if (RING) arrived(it);
+            for (int u = warp; u < n * L.sp; u += kWarps) {
+                const int s = s0 + u / L.sp, ip = u % L.sp, u0 = ip * nu / L.sp, u1 = (ip + 1) * nu / L.sp;
+                float* pp = part + ip * prow * 16;
+                if (RING) {
+                    const uint8_t* codes = sm + L.ring + (it % L.stages) * L.stage + (u / L.sp) * (cb2 + mb2);
+                    w2_unit<MB, NT>(a, codes, codes + cb2, u0, u1, ridx + s * M, expo + s * M, coef + s * M, pp, lane);
+                } else {
+                    const size_t row = (size_t)slot_e[s] * K + 16 * tile;
+                    if (QMLP_INB((row + 16) * (I / 2) - 1, a.w2_bytes, 103) &&
+                        QMLP_INB((row + 16) * (I / 32) * MB - 1, a.w2_meta_bytes, 104))
+                        w2_unit<MB, NT>(a, a.w2 + row * (I / 2), a.w2_meta + row * (I / 32) * MB, u0, u1, ridx + s * M,
+                                        expo + s * M, coef + s * M, pp, lane);
                 }
             }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int m = 8 * n + 2 * t + e;
-                    const int r = m < M ? ridx[s * M + m] : kNone;
-                    if (r != kNone) {  // a choice of token m: its rows g and g + 8
-                        const float w = coef[s * M + m];
-                        part[r * 16 + g] = w * d[n][e];
-                        part[r * 16 + g + 8] = w * d[n][2 + e];
-                    }
-                }
+            if (RING) {  // ten arrivals a stage: one for two warps
+                named_bar_sync(2 + warp / 2, 64);
+                if (lane == 0 && (warp & 1) == 0) mbar_arrive(empty(it % L.stages));
+            }
         }
-        __syncthreads();
+        named_bar_sync(1, kThreads);
         for (int i = threadIdx.x; i < 16 * M; i += kThreads) {
             const int r = i & 15, m = i >> 4;
             float v = 0.0f;
-            for (int c = 0; c < nsel; ++c) v += part[(m * nsel + c) * 16 + r];
+            for (int c = 0; c < nsel; ++c)
+                for (int ip = 0; ip < L.sp; ++ip) v += part[((ip * prow) + m * nsel + c) * 16 + r];
             store_any(a.out, a.odt, (size_t)m * K + 16 * tile + r, v);
         }
+        named_bar_sync(1, kThreads);
     }
 }
 
 // ---------------------------------------------------------------------------
 // More tokens: router and selection for the grouped kernels
 // ---------------------------------------------------------------------------
-// One CTA eight rows (a warp a row) for 16 tokens.
+// Eight tokens and eight tiles of rows a CTA, a warp a tile.
 __global__ void __launch_bounds__(256) router_kernel(const MoeLayerArgs a) {
-    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int m0 = blockIdx.y * 16, M = min(16, a.M - m0);
-    if (row >= a.E + (a.sgate ? a.S : 0)) return;
-    float acc[16];
-    row_dots(a, static_cast<const uint16_t*>(a.x) + (size_t)m0 * a.K, M, row, lane, 32, acc);
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ int s_max[16], s_sig[16];
+    uint4* xsm = reinterpret_cast<uint4*>(sm);
+    const int m0 = blockIdx.y * 8, M = min(8, a.M - m0), rows = a.E + (a.sgate ? a.S : 0);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    stage_x(a, static_cast<const uint16_t*>(a.x) + (size_t)m0 * a.K, M, xsm, s_max, s_sig, 256, [] { __syncthreads(); });
+    const int tile = blockIdx.x * 8 + warp;
+    if (tile * 16 >= rows) return;
+    float d[1][4];
+    router_tile<1>(a, xsm, M, tile, 0, a.K / 32, 1, lane, d);
 #pragma unroll
-    for (int m = 0; m < 16; ++m)
-        if (m < M) {
-            const float s = wsum(acc[m]);
-            const size_t at = (size_t)(m0 + m) * (a.E + a.S) + row;
-            if (lane == 0 && QMLP_INB(at, a.logit_elems, 108)) a.logits[at] = s;
-        }
+    for (int e = 0; e < 4; ++e) {
+        const int row = tile * 16 + g + 4 * (e & 2), m = 2 * t + (e & 1);
+        const size_t at = (size_t)(m0 + m) * (a.E + a.S) + row;
+        if (row < rows && m < M && QMLP_INB(at, a.logit_elems, 108)) a.logits[at] = scalbnf(d[0][e], -s_sig[m] - a.rexp[row]);
+    }
 }
 // A warp a token.
 __global__ void __launch_bounds__(128) select_kernel(const MoeLayerArgs a) {
@@ -680,7 +881,7 @@ __global__ void __launch_bounds__(128) select_kernel(const MoeLayerArgs a) {
     __shared__ float sw[4][16];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, m = blockIdx.x * 4 + w, nsel = a.topk + a.S;
     if (m >= a.M) return;
-    select_any(a, a.logits + (size_t)m * (a.E + a.S), lane, se[w], sw[w]);
+    select_any(a, a.logits + (size_t)m * (a.E + a.S), 1, 0, lane, se[w], sw[w]);
     __syncwarp();
     if (lane < nsel) {
         a.ids[(size_t)m * nsel + lane] = se[w][lane];
@@ -692,18 +893,66 @@ __global__ void __launch_bounds__(128) select_kernel(const MoeLayerArgs a) {
     }
 }
 
-template <int MB, int NT>
+// The router (and shared gates) [rows, K] of a type -> fragments, and the rows'
+// exponents. A warp a row for the exponent, then a thread a 16-byte piece.
+__global__ void __launch_bounds__(256) router_exp_kernel(const void* w, const void* sg, int type, int E, int rows, int K, int* rexp,
+                                                         int padded) {
+    const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= padded) return;
+    float mx = 0.0f;
+    if (row < rows)
+        for (int c = lane; c < K / 8; c += 32) {
+            float v[8];
+            load8t(row < E ? w : sg, type, (size_t)(row < E ? row : row - E) * K + 8 * c, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+        }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (lane == 0) rexp[row] = prescale_exponent(mx);
+}
+__global__ void __launch_bounds__(256) router_frag_kernel(const void* w, const void* sg, int type, int E, int rows, int K,
+                                                          const int* rexp, int tiles, int planes, uint4* out) {
+    const size_t n32 = K / 32, items = (size_t)planes * tiles * n32 * 64;
+    for (size_t it = (size_t)blockIdx.x * 256 + threadIdx.x; it < items; it += (size_t)gridDim.x * 256) {
+        const int lane = (int)(it & 31), st = (int)(it >> 5) & 1, g = lane >> 2, t = lane & 3;
+        const size_t rest = it >> 6;
+        const int j = (int)(rest % n32), tile = (int)(rest / n32 % tiles), pl = (int)(rest / n32 / tiles);
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {  // rows g, g + 8 at k 2t.., then at 8 + 2t..
+            const int row = tile * 16 + g + 8 * (q & 1), k = 32 * j + 16 * st + 8 * (q >> 1) + 2 * t;
+            float v[2] = {0.0f, 0.0f};
+            if (row < rows) {
+                const void* p = row < E ? w : sg;
+                const size_t at = (size_t)(row < E ? row : row - E) * K + k;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float f = type == 0   ? static_cast<const float*>(p)[at + e]
+                                    : type == 1 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + e])
+                                                : __half2float(static_cast<const __half*>(p)[at + e]);
+                    v[e] = scalbnf(f, rexp[row]);
+                    if (pl) v[e] -= __half2float(__float2half_rn(v[e]));  // what the first plane leaves
+                }
+            }
+            o[q] = u32(__floats2half2_rn(v[0], v[1]));
+        }
+        out[it] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+}
+
+template <int MB, int NT, bool RING>
 cudaError_t launch_few(const MoeLayerArgs& a, int bytes, int num_sms, cudaStream_t s) {
     static bool attr = false;
     if (!attr) {
         const cudaError_t e =
-            cudaFuncSetAttribute(moe_layer_kernel<MB, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+            cudaFuncSetAttribute(moe_layer_kernel<MB, NT, RING>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
         if (e != cudaSuccess) return e;
         attr = true;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)num_sms);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads + 32);
     cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = s;
     cudaLaunchAttribute at[1];
@@ -711,32 +960,58 @@ cudaError_t launch_few(const MoeLayerArgs& a, int bytes, int num_sms, cudaStream
     at[0].val.cooperative = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_layer_kernel<MB, NT>, a);
+    return cudaLaunchKernelEx(&cfg, moe_layer_kernel<MB, NT, RING>, a);
+}
+
+Layout layout_of(int M, int K, int I, int E, int S, int topk, int MB) {
+    return layout(M, K, I, E, topk + S, std::min(E, M * topk) + S, MB, M <= 8 ? 1 : 2);
 }
 
 }  // namespace
 
-bool moe_layer_few(int M, int K, int E, int slots) {
-    return M <= kMoeLayerFew && E <= kMoeLayerMaxE &&
-           layout(M, K, E, slots, M <= 8 ? 1 : 2).bytes <= kSmemMax;
+bool moe_layer_few(int M, int K, int I, int E, int S, int topk, int meta_bytes) {
+    return M <= kMoeLayerFew && layout_of(M, K, I, E, S, topk, meta_bytes).bytes <= kSmemMax;
 }
 
 cudaError_t launch_moe_layer_few(MoeLayerArgs a, int meta_bytes, int num_sms, cudaStream_t s) {
     a.slots = std::min(a.E, a.M * a.topk) + a.S;
     a.limit = kWaitNs;
-    const int bytes = layout(a.M, a.K, a.E, a.slots, a.M <= 8 ? 1 : 2).bytes;
-    if (bytes > kSmemMax) return cudaErrorInvalidValue;
-    if (meta_bytes == 4)
-        return a.M <= 8 ? launch_few<4, 1>(a, bytes, num_sms, s) : launch_few<4, 2>(a, bytes, num_sms, s);
-    return a.M <= 8 ? launch_few<3, 1>(a, bytes, num_sms, s) : launch_few<3, 2>(a, bytes, num_sms, s);
+    const Layout l = layout_of(a.M, a.K, a.I, a.E, a.S, a.topk, meta_bytes);
+    if (l.bytes > kSmemMax) return cudaErrorInvalidValue;
+    const int n = l.bytes;
+    if (l.stage) {
+        if (meta_bytes == 4) return a.M <= 8 ? launch_few<4, 1, true>(a, n, num_sms, s) : launch_few<4, 2, true>(a, n, num_sms, s);
+        return a.M <= 8 ? launch_few<3, 1, true>(a, n, num_sms, s) : launch_few<3, 2, true>(a, n, num_sms, s);
+    }
+    if (meta_bytes == 4) return a.M <= 8 ? launch_few<4, 1, false>(a, n, num_sms, s) : launch_few<4, 2, false>(a, n, num_sms, s);
+    return a.M <= 8 ? launch_few<3, 1, false>(a, n, num_sms, s) : launch_few<3, 2, false>(a, n, num_sms, s);
 }
 
 cudaError_t launch_moe_router(const MoeLayerArgs& a, cudaStream_t s) {
-    const int rows = a.E + (a.sgate ? a.S : 0);
-    router_kernel<<<dim3((unsigned)((rows + 7) / 8), (unsigned)((a.M + 15) / 16)), 256, 0, s>>>(a);
+    const int tiles = (a.E + (a.sgate ? a.S : 0) + 15) / 16;
+    const size_t smem = (size_t)std::min(8, a.M) * a.K * 2;
+    static bool attr = false;
+    if (!attr) {
+        const cudaError_t e = cudaFuncSetAttribute(router_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+        if (e != cudaSuccess) return e;
+        attr = true;
+    }
+    if (smem > kSmemMax) return cudaErrorInvalidValue;
+    router_kernel<<<dim3((unsigned)((tiles + 7) / 8), (unsigned)((a.M + 7) / 8)), 256, smem, s>>>(a);
     const cudaError_t e = cudaPeekAtLastError();
     if (e != cudaSuccess) return e;
     select_kernel<<<(unsigned)((a.M + 3) / 4), 128, 0, s>>>(a);
+    return cudaPeekAtLastError();
+}
+
+cudaError_t launch_router_layout(const MoeLayerArgs& a, const void* w, const void* sg, int type, uint4* frag, int* rexp,
+                                 cudaStream_t s) {
+    const int rows = a.E + (sg ? a.S : 0), padded = a.rtiles * 16;
+    router_exp_kernel<<<(unsigned)((padded + 7) / 8), 256, 0, s>>>(w, sg, type, a.E, rows, a.K, rexp, padded);
+    const cudaError_t e = cudaPeekAtLastError();
+    if (e != cudaSuccess) return e;
+    router_frag_kernel<<<(unsigned)std::min<size_t>((a.rfrag_elems + 255) / 256, 65535), 256, 0, s>>>(
+        w, sg, type, a.E, rows, a.K, rexp, a.rtiles, a.planes, frag);
     return cudaPeekAtLastError();
 }
 
