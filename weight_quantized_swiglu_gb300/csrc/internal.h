@@ -446,7 +446,7 @@ struct MoeLayerArgs {
     int slots = 0;                  // experts that M tokens can name, at most
     size_t w13_bytes = 0, w13_meta_bytes = 0, w2_bytes = 0, w2_meta_bytes = 0, logit_elems = 0, act_elems = 0;
 };
-constexpr int kMoeRouterSplits = 8;  // splits of the router's k over CTAs, at most
+constexpr int kMoeRouterSplits = 4;  // splits of the router's k over CTAs, at most
 bool moe_layer_few(int M, int K, int I, int E, int S, int topk, int meta_bytes);
 cudaError_t launch_router_layout(const MoeLayerArgs& a, const void* w, const void* sg, int type, uint4* frag, int* rexp,
                                  cudaStream_t s);

@@ -57,6 +57,15 @@ constexpr uint16_t kNone = 0xFFFF;
 
 QMLP_DEV uint32_t u32(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 
+// What the warps of a token's selection share.
+struct Pick {
+    uint32_t top[32];  // largest keys of 32 groups of experts
+    uint32_t key[32];  // candidates: key, expert, logit
+    int e[32];
+    float l[32];
+    float part[16];
+    int n;
+};
 // Splits of the router's k over CTAs.
 __host__ __device__ inline int router_splits(int rows, int K, int ctas) {
     const int tiles = (rows + 15) / 16;
@@ -68,7 +77,7 @@ __host__ __device__ inline int router_splits(int rows, int K, int ctas) {
 
 // Shared memory of the kernel (slots: experts that the tokens can name).
 struct Layout {
-    int x, coef, ridx, expo, slot_e, mask, sel_e, sel_w, part, part_bytes, ring;
+    int x, coef, ridx, slot_e, mask, sel_e, sel_w, cand, part, part_bytes, ring;
     int stage, stages;  // bytes of a ring stage (0: no ring), stages
     int n2, sp;         // W2: experts of a stage, parts of I that different warps take
     int bytes;
@@ -80,11 +89,11 @@ __host__ __device__ inline Layout layout(int M, int K, int I, int E, int nsel, i
     l.x = at, at += up(M * K * 2);
     l.coef = at, at += up(slots * M * 4);
     l.ridx = at, at += up(slots * M * 2);
-    l.expo = at, at += up(slots * M);
     l.slot_e = at, at += up(slots * 4);
     l.mask = at, at += up(E * 4);
     l.sel_e = at, at += 16 * 16 * 4;
     l.sel_w = at, at += 16 * 16 * 4;
+    l.cand = at, at += up(M * (int)sizeof(Pick));  // (what follows is read 8 and copied 16 bytes at a time)
     l.part = at, l.part_bytes = 2 * kWarps * 16 * 8 * NT * 4, at += l.part_bytes;
     l.ring = at;
     const int item13 = (int)(kMoeKSplit * (moe_w13_block_bytes(K) + moe_w13_meta_block_bytes(K, MB)));
@@ -98,7 +107,7 @@ __host__ __device__ inline Layout layout(int M, int K, int I, int E, int nsel, i
     // where the experts of a stage are few, parts of I go to different warps
     l.sp = 1;
     const int per = l.n2 < slots ? l.n2 : slots;
-    while (l.sp < 8 && 2 * l.sp * per <= kWarps && I / 32 >= 4 * l.sp && M * nsel * 2 * l.sp * 64 <= l.part_bytes) l.sp *= 2;
+    while (l.sp < 8 && 2 * l.sp * per <= kWarps && I / 32 >= 4 * l.sp && 2 * M * nsel * 2 * l.sp * 64 <= l.part_bytes) l.sp *= 2;
     l.bytes = at + l.stage * l.stages;
     return l;
 }
@@ -144,87 +153,128 @@ QMLP_DEV uint32_t order_key(float v) {
     return max(k, 2u);
 }
 
-// One warp selects for one token: its logits are the sums of `splits` shares, `hop`
-// apart, from l on (E routed experts, then the shared gates). Its choices go to
-// sel_e / sel_w in order, the shared experts after the routed ones.
-template <int NPL>
-QMLP_DEV void select(const MoeLayerArgs& a, const float* l, int splits, size_t hop, int lane, int* sel_e, float* sel_w) {
-    float v[NPL];
-    float mx = -INFINITY;
+// Selection for M tokens from their logits lg (rows of E routed experts, then the
+// shared gates; shared or global memory) by `wt` warps a token (a power of two): to
+// sel_e / sel_w [token][16] in order, the shared experts after the routed ones.
+// The topk-th largest of the 32 groups' largest keys is at most the topk-th largest
+// key: only the keys from it on are candidates, seldom more than 32 of them, one a lane
+// then, whose rank is how many are above it. One token is all latency: its experts go
+// over 16 warps, and the code is loops instead of registers (512 experts: 5.8 us by one
+// warp in topk rounds of a warp-wide maximum, 5.3 by one warp with candidates).
+// sync: a barrier of all warps that call it.
+template <typename Sync>
+QMLP_DEV void select_tokens(const MoeLayerArgs& a, const float* lg, int M, int wt, Pick* picks, int* sel_e, float* sel_w, Sync sync) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, m = warp / wt, w = warp % wt;
+    const bool on = m < M;
+    const float* l = lg + (size_t)(on ? m : 0) * (a.E + a.S);
+    Pick& c = picks[on ? m : 0];
+    const int e0 = w * 32 + lane, hop = wt * 32, E = on ? a.E : 0;
+    if (on && w == 0 && lane == 0) c.n = 0;
+    float mx = 0.0f, total = 1.0f;
+    if (a.softmax && (!a.renorm || a.bias)) {  // p itself is wanted
+        mx = -INFINITY;
+        for (int e = e0; e < E; e += hop) mx = fmaxf(mx, l[e]);
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = i * 32 + lane;
-        v[i] = e < a.E ? __ldcg(l + e) : -INFINITY;
-    }
-    float lsh = a.sgate && lane < a.S ? __ldcg(l + a.E + lane) : 0.0f;
-    for (int s = 1; s < splits; ++s) {
-        const float* ls = l + s * hop;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = i * 32 + lane;
-            if (e < a.E) v[i] += __ldcg(ls + e);
-        }
-        if (a.sgate && lane < a.S) lsh += __ldcg(ls + a.E + lane);
-    }
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) mx = fmaxf(mx, v[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    float total = 1.0f;  // softmax, without renorming or with a bias: p itself is wanted
-    if (a.softmax && (!a.renorm || a.bias)) {
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (on && lane == 0) c.part[w] = mx;
+        sync();
+        for (int i = 0; i < wt; ++i) mx = fmaxf(mx, c.part[i]);
         float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (i * 32 + lane < a.E) s += expf(v[i] - mx);
-        total = wsum(s);
+        for (int e = e0; e < E; e += hop) s += expf(l[e] - mx);
+        s = wsum(s);
+        sync();
+        if (on && lane == 0) c.part[w] = s;
+        sync();
+        total = 0.0f;
+        for (int i = 0; i < wt; ++i) total += c.part[i];
     }
     auto score = [&](float t) { return a.softmax ? expf(t - mx) / total : 1.0f / (1.0f + expf(-t)); };
-    uint32_t key[NPL];
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = i * 32 + lane;
-        // without a bias the logits have the scores' order
-        float k = v[i];
-        if (a.bias && e < a.E) k = score(k) + __ldg(a.bias + e);
-        key[i] = e < a.E ? order_key(k) : 0u;
-    }
-    float mine = 0.0f;  // lane r: the logit of choice r
-    for (int r = 0; r < a.topk; ++r) {
-        uint32_t best = 0;
-        int at = 0;
-        float val = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-                val = v[i];
-            }
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(at * 32 + lane) : 0xffffffffu);
-        val = __shfl_sync(0xffffffffu, val, (int)(e & 31u));
-        const int gone = (int)(e & 31u) == lane ? (int)(e >> 5) : -1;
-#pragma unroll
-        for (int i = 0; i < NPL; ++i)
-            if (i == gone) key[i] = 0u;
-        if (lane == r) {
-            mine = val;
-            sel_e[r] = (int)e;
+    // without a bias the logits have the scores' order
+    auto key_of = [&](int e) {
+        const float t = l[e];
+        return order_key(a.bias ? score(t) + __ldg(a.bias + e) : t);
+    };
+    uint32_t best = 0;
+#pragma unroll 4
+    for (int e = e0; e < E; e += hop) best = max(best, key_of(e));
+    for (int o = 1; o < wt; o <<= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+    if (on && lane % wt == 0) c.top[w * (32 / wt) + lane / wt] = best;
+    sync();
+    {
+        const uint32_t mine = c.top[lane];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t o = c.top[j];
+            rank += o > mine || (o == mine && j < lane);
         }
+        const uint32_t at = __ballot_sync(0xffffffffu, rank == a.topk - 1);
+        const uint32_t least = max(__shfl_sync(0xffffffffu, mine, __ffs(at) - 1), 1u);
+#pragma unroll 4
+        for (int e = e0; e < E; e += hop) {
+            const uint32_t k = key_of(e);
+            if (k >= least) {
+                const int pos = atomicAdd(&c.n, 1);
+                if (pos < 32) {
+                    c.key[pos] = k;
+                    c.e[pos] = e;
+                    c.l[pos] = l[e];
+                }
+            }
+        }
+    }
+    sync();
+    if (!on || w != 0) return;
+    int* se = sel_e + m * 16;
+    float* sw = sel_w + m * 16;
+    float mine = 0.0f;  // lane r: the logit of choice r
+    const int n = c.n;
+    if (n <= 32) {
+        const uint32_t k = lane < n ? c.key[lane] : 0u;
+        const int e = lane < n ? c.e[lane] : 0;
+        const float f = c.l[lane];
+        int rank = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += c.key[j] > k || (c.key[j] == k && c.e[j] < e);
+        __syncwarp();
+        if (lane < n && rank < a.topk) {
+            se[rank] = e;
+            c.l[rank] = f;
+        }
+        __syncwarp();
+        mine = c.l[lane];
+    } else {  // (many equal ones) round after round
+        for (int r = 0; r < a.topk; ++r) {
+            uint32_t top = 0;
+            int at = 0;
+            for (int e = lane; e < E; e += 32) {
+                const uint32_t k = key_of(e);
+                bool taken = false;
+                for (int q = 0; q < r; ++q) taken = taken || se[q] == e;
+                if (!taken && k > top) {
+                    top = k;
+                    at = e;
+                }
+            }
+            const uint32_t all = __reduce_max_sync(0xffffffffu, top);
+            const uint32_t e = __reduce_min_sync(0xffffffffu, top == all ? (uint32_t)at : 0xffffffffu);
+            if (lane == 0) se[r] = (int)e;
+            __syncwarp();
+            if (lane == r) mine = l[e];
+        }
+    }
+    if (a.softmax && a.renorm && !a.bias) {  // (any shift will do: the largest selected logit)
+        mx = lane < a.topk ? mine : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
     const float p = lane < a.topk ? score(mine) : 0.0f;
     const float sum = a.renorm ? wsum(p) : 1.0f;
-    if (lane < a.topk) sel_w[lane] = p / sum * a.rscale;
+    if (lane < a.topk) sw[lane] = p / sum * a.rscale;
     if (lane < a.S) {
-        sel_e[a.topk + lane] = a.E + lane;
-        sel_w[a.topk + lane] = a.sgate ? 1.0f / (1.0f + expf(-lsh)) : 1.0f;
+        se[a.topk + lane] = a.E + lane;
+        sw[a.topk + lane] = a.sgate ? 1.0f / (1.0f + expf(-l[a.E + lane])) : 1.0f;
     }
-}
-QMLP_DEV void select_any(const MoeLayerArgs& a, const float* l, int splits, size_t hop, int lane, int* sel_e, float* sel_w) {
-    if (a.E <= 64) select<2>(a, l, splits, hop, lane, sel_e, sel_w);
-    else if (a.E <= 256) select<8>(a, l, splits, hop, lane, sel_e, sel_w);
-    else if (a.E <= 512) select<16>(a, l, splits, hop, lane, sel_e, sel_w);
-    else select<32>(a, l, splits, hop, lane, sel_e, sel_w);
 }
 
 // Sixteen rows of the router times NT tiles of eight tokens over pairs of steps
@@ -322,10 +372,16 @@ QMLP_DEV void meta2(uint32_t m, uint32_t& s2, uint32_t& b2) {
     s2 = s | (s << 16);
     b2 = b | (b << 16);
 }
+// (m & 0x00F0000F) | 0x64006400 in one instruction (the compiler took two)
+QMLP_DEV uint32_t pair_bits(uint32_t m) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(m), "r"(0x00F0000Fu), "r"(0x64006400u));
+    return d;
+}
 template <int T>  // byte T of the word
 QMLP_DEV uint32_t pair_of(uint32_t w, uint32_t s2, uint32_t b2) {
     const uint32_t m = __byte_perm(w, 0u, (uint32_t)(T | 4 << 4 | T << 8 | 4 << 12));
-    const uint32_t q = lfma2((m & 0x00F0000Fu) | 0x64006400u, 0x2C003C00u, 0xD400E400u);
+    const uint32_t q = lfma2(pair_bits(m), 0x2C003C00u, 0xD400E400u);
     return lfma2(q, s2, b2);
 }
 
@@ -438,20 +494,33 @@ QMLP_DEV void store_any(void* p, int type, size_t at, float v) {
     else static_cast<__half*>(p)[at] = __float2half_rn(v);
 }
 
+// Eight bytes that other CTAs wrote, where `on`: else zeros, without a branch.
+QMLP_DEV float2 ldcg2_if(const float* p, bool on) {
+    float2 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tmov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
+        "@p ld.global.cg.v2.f32 {%0, %1}, [%2];\n\t}"
+        : "=&f"(v.x), "=&f"(v.y)
+        : "l"(p), "r"((uint32_t)on));
+    return v;
+}
 // Part 3's share of one expert: its rows n0.. (codes, meta) times the tokens' act over
 // units u0..u1 of 32 k, times the weights, to part (choice r of the call: r 16 + row).
+// All loads of act and of its largest value go out at once.
 template <int MB, int NT>
 QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t* meta, int u0, int u1, const uint16_t* ridx,
-                      const int8_t* expo, const float* coef, float* part, int lane) {
+                      const float* coef, float* part, int lane) {
     const int M = a.M, I = a.I, g = lane >> 2, t = lane & 3;
-    float d[NT][4];
-    int col[NT];
-    float up[NT];
+    float d[NT][4], up[NT];
+    int ex[NT];
+    const float* row[NT];
+    bool on[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int m = 8 * n + g;
-        col[n] = m < M ? ridx[m] : kNone;
-        up[n] = m < M ? __int_as_float((127 + expo[m]) << 23) : 1.0f;
+        const int m = 8 * n + g, r = m < M ? ridx[m] : kNone;
+        on[n] = r != kNone && QMLP_INB((size_t)(r + 1) * I - 1, a.act_elems, 107);
+        row[n] = a.act + (size_t)(on[n] ? r : 0) * I + 2 * t;
+        ex[n] = on[n] ? __ldcg(a.amax + r) : 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
     }
@@ -459,17 +528,20 @@ QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t
         uint32_t xb[NT][kG2][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const float* row = a.act + (size_t)(col[n] == kNone ? 0 : col[n]) * I + 32 * ub + 2 * t;
+            float2 v[kG2][2];
 #pragma unroll
             for (int i = 0; i < kG2; ++i)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float2 v = make_float2(0.0f, 0.0f);
-                    if (ub + i / 2 < u1 && col[n] != kNone &&
-                        QMLP_INB((size_t)(row - a.act) + 16 * i + 8 * h + 1, a.act_elems, 107))
-                        v = __ldcg(reinterpret_cast<const float2*>(row + 16 * i + 8 * h));
-                    xb[n][i][h] = u32(__floats2half2_rn(v.x * up[n], v.y * up[n]));
-                }
+                for (int h = 0; h < 2; ++h)
+                    v[i][h] = ldcg2_if(row[n] + 32 * ub + 16 * i + 8 * h, on[n] && ub + i / 2 < u1);
+            if (ub == u0) {
+                ex[n] = max(-113, min(126, prescale_exponent(__int_as_float(ex[n]))));
+                up[n] = __int_as_float((127 + ex[n]) << 23);
+            }
+#pragma unroll
+            for (int i = 0; i < kG2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) xb[n][i][h] = u32(__floats2half2_rn(v[i][h].x * up[n], v[i][h].y * up[n]));
         }
         Batch2<MB> b;
         load2<MB>(b, codes, meta, I, ub, u1, lane);
@@ -497,10 +569,10 @@ QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int m = 8 * n + 2 * t + e;
+            const int m = 8 * n + 2 * t + e, back = __shfl_sync(0xffffffffu, ex[n], (2 * t + e) * 4);
             const int r = m < M ? ridx[m] : kNone;
             if (r != kNone) {  // a choice of token m: its rows g and g + 8
-                const float w = coef[m];
+                const float w = coef[m] * __int_as_float((127 - back) << 23);
                 part[r * 16 + g] = w * d[n][e];
                 part[r * 16 + g + 8] = w * d[n][2 + e];
             }
@@ -519,16 +591,17 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
     uint4* xsm = reinterpret_cast<uint4*>(sm + L.x);
     float* coef = reinterpret_cast<float*>(sm + L.coef);          // [slot][M]
     uint16_t* ridx = reinterpret_cast<uint16_t*>(sm + L.ridx);    // [slot][M]: row of act
-    int8_t* expo = reinterpret_cast<int8_t*>(sm + L.expo);        // [slot][M]
     int* slot_e = reinterpret_cast<int*>(sm + L.slot_e);
     uint32_t* mask = reinterpret_cast<uint32_t*>(sm + L.mask);    // [E]: tokens that named it, then its slot
     int* sel_e = reinterpret_cast<int*>(sm + L.sel_e);            // [16][16]
     float* sel_w = reinterpret_cast<float*>(sm + L.sel_w);
+    Pick* picks = reinterpret_cast<Pick*>(sm + L.cand);           // [M]
     float* part = reinterpret_cast<float*>(sm + L.part);
     const uint32_t bar0 = smem_u32(bars);
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
-    const int splits = router_splits(rows, K, gridDim.x), ctile = (rows + 15) / 16;
+    // (one split where the logits have no room in shared memory)
+    const int splits = M * (a.E + a.S) * 4 <= L.part_bytes ? router_splits(rows, K, gridDim.x) : 1, ctile = (rows + 15) / 16;
     const size_t hop = (size_t)M * (a.E + a.S);  // between the splits' shares of the logits
     if (RING && threadIdx.x == 0) {
         for (int s = 0; s < L.stages; ++s) {
@@ -574,7 +647,29 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
     }
 
     // ---------------- 2: selection, W13 ----------------
-    if (warp < M) select_any(a, a.logits + (size_t)warp * (a.E + a.S), splits, hop, lane, sel_e + warp * 16, sel_w + warp * 16);
+    {
+        // the logits: the splits' shares in order, in shared memory where there is room
+        const int all = M * (a.E + a.S);
+        const bool room = all * 4 <= L.part_bytes;
+        float* lg = room ? part : a.logits;
+        if (warp < kWarps && room) {
+#pragma unroll 2
+            for (int i = threadIdx.x; i < all; i += kThreads) {
+                float v[kMoeRouterSplits];
+#pragma unroll
+                for (int s = 0; s < kMoeRouterSplits; ++s) v[s] = s < splits ? __ldcg(a.logits + s * hop + i) : 0.0f;
+#pragma unroll
+                for (int s = 1; s < kMoeRouterSplits; ++s)
+                    if (s < splits) v[0] += v[s];
+                part[i] = v[0];
+            }
+        }
+        if (warp < kWarps) {
+            named_bar_sync(1, kThreads);
+            select_tokens(a, lg, M, M == 1 ? 16 : M == 2 ? 8 : M <= 4 ? 4 : M <= 8 ? 2 : 1, picks, sel_e, sel_w,
+                          [] { named_bar_sync(1, kThreads); });
+        }
+    }
     __syncthreads();
     int slots;
     if (M == 1) {  // the choices are the list
@@ -807,47 +902,44 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
         }
         return;
     }
-    for (int i = threadIdx.x; i < slots * M; i += kThreads) {
-        int e = 0;
-        if (ridx[i] != kNone) {
-            e = max(-113, min(126, prescale_exponent(__int_as_float(__ldcg(a.amax + ridx[i])))));
-            coef[i] *= __int_as_float((127 - e) << 23);
-        }
-        expo[i] = (int8_t)e;
-    }
-    named_bar_sync(1, kThreads);
     const int nu = I / 32, prow = M * nsel;
-    for (int tl = 0; tl < tiles2; ++tl) {
-        const int tile = blockIdx.x + tl * gridDim.x;
-        for (int j = 0; j < st2; ++j) {
-            const int it = n13 + tl * st2 + j, s0 = j * L.n2, n = min(L.n2, slots - s0);
-            if (RING) arrived(it);
-            for (int u = warp; u < n * L.sp; u += kWarps) {
-                const int s = s0 + u / L.sp, ip = u % L.sp, u0 = ip * nu / L.sp, u1 = (ip + 1) * nu / L.sp;
-                float* pp = part + ip * prow * 16;
-                if (RING) {
-                    const uint8_t* codes = sm + L.ring + (it % L.stages) * L.stage + (u / L.sp) * (cb2 + mb2);
-                    w2_unit<MB, NT>(a, codes, codes + cb2, u0, u1, ridx + s * M, expo + s * M, coef + s * M, pp, lane);
-                } else {
-                    const size_t row = (size_t)slot_e[s] * K + 16 * tile;
-                    if (QMLP_INB((row + 16) * (I / 2) - 1, a.w2_bytes, 103) &&
-                        QMLP_INB((row + 16) * (I / 32) * MB - 1, a.w2_meta_bytes, 104))
-                        w2_unit<MB, NT>(a, a.w2 + row * (I / 2), a.w2_meta + row * (I / 32) * MB, u0, u1, ridx + s * M,
-                                        expo + s * M, coef + s * M, pp, lane);
+    int first = 0;  // the warp that takes the next unit: the units of all stages go round
+    for (int tl = 0; tl < tiles2; tl += 2) {  // two tiles between barriers
+        const int nt = min(2, tiles2 - tl);
+        for (int q = 0; q < nt; ++q)
+            for (int j = 0; j < st2; ++j) {
+                const int tile = blockIdx.x + (tl + q) * gridDim.x;
+                const int it = n13 + (tl + q) * st2 + j, s0 = j * L.n2, n = min(L.n2, slots - s0);
+                const uint8_t* stage = sm + L.ring + (RING ? it % L.stages * L.stage : 0);
+                if (RING) arrived(it);
+                int u = warp - first;
+                for (u += u < 0 ? kWarps : 0; u < n * L.sp; u += kWarps) {
+                    const int s = s0 + u / L.sp, ip = u % L.sp, u0 = ip * nu / L.sp, u1 = (ip + 1) * nu / L.sp;
+                    float* pp = part + (q * L.sp + ip) * prow * 16;
+                    if (RING) {
+                        const uint8_t* codes = stage + (u / L.sp) * (cb2 + mb2);
+                        w2_unit<MB, NT>(a, codes, codes + cb2, u0, u1, ridx + s * M, coef + s * M, pp, lane);
+                    } else {
+                        const size_t row = (size_t)slot_e[s] * K + 16 * tile;
+                        if (QMLP_INB((row + 16) * (I / 2) - 1, a.w2_bytes, 103) &&
+                            QMLP_INB((row + 16) * (I / 32) * MB - 1, a.w2_meta_bytes, 104))
+                            w2_unit<MB, NT>(a, a.w2 + row * (I / 2), a.w2_meta + row * (I / 32) * MB, u0, u1, ridx + s * M,
+                                            coef + s * M, pp, lane);
+                    }
+                }
+                first = (first + n * L.sp) % kWarps;
+                if (RING) {  // ten arrivals a stage: one for two warps
+                    named_bar_sync(2 + warp / 2, 64);
+                    if (lane == 0 && (warp & 1) == 0) mbar_arrive(empty(it % L.stages));
                 }
             }
-            if (RING) {  // ten arrivals a stage: one for two warps
-                named_bar_sync(2 + warp / 2, 64);
-                if (lane == 0 && (warp & 1) == 0) mbar_arrive(empty(it % L.stages));
-            }
-        }
         named_bar_sync(1, kThreads);
-        for (int i = threadIdx.x; i < 16 * M; i += kThreads) {
-            const int r = i & 15, m = i >> 4;
+        for (int i = threadIdx.x; i < 16 * M * nt; i += kThreads) {
+            const int r = i & 15, m = (i >> 4) % M, q = (i >> 4) / M;
             float v = 0.0f;
             for (int c = 0; c < nsel; ++c)
-                for (int ip = 0; ip < L.sp; ++ip) v += part[((ip * prow) + m * nsel + c) * 16 + r];
-            store_any(a.out, a.odt, (size_t)m * K + 16 * tile + r, v);
+                for (int ip = 0; ip < L.sp; ++ip) v += part[((q * L.sp + ip) * prow + m * nsel + c) * 16 + r];
+            store_any(a.out, a.odt, (size_t)m * K + 16 * (blockIdx.x + (tl + q) * gridDim.x) + r, v);
         }
         named_bar_sync(1, kThreads);
     }
@@ -879,9 +971,10 @@ __global__ void __launch_bounds__(256) router_kernel(const MoeLayerArgs a) {
 __global__ void __launch_bounds__(128) select_kernel(const MoeLayerArgs a) {
     __shared__ int se[4][16];
     __shared__ float sw[4][16];
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, m = blockIdx.x * 4 + w, nsel = a.topk + a.S;
+    __shared__ Pick picks[4];
+    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, m0 = blockIdx.x * 4, m = m0 + w, nsel = a.topk + a.S;
+    select_tokens(a, a.logits + (size_t)m0 * (a.E + a.S), min(4, a.M - m0), 1, picks, &se[0][0], &sw[0][0], [] { __syncwarp(); });
     if (m >= a.M) return;
-    select_any(a, a.logits + (size_t)m * (a.E + a.S), 1, 0, lane, se[w], sw[w]);
     __syncwarp();
     if (lane < nsel) {
         a.ids[(size_t)m * nsel + lane] = se[w][lane];
