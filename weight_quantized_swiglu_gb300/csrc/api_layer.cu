@@ -478,6 +478,8 @@ qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const
         a.weights = static_cast<float*>(make(rows * nsel * 4, nullptr));
         a.act = static_cast<float*>(make(a.act_elems * 4, nullptr));
         a.amax = static_cast<int*>(make(few * 4, nullptr));
+        a.act16_elems = a.act_elems / 8;
+        a.act16 = static_cast<uint4*>(make(a.act16_elems * 16, nullptr));
         uint8_t* words = static_cast<uint8_t*>(make(16, nullptr));
         if (e == cudaSuccess) e = cudaMemsetAsync(words, 0, 16, s);
         a.ticket = reinterpret_cast<unsigned long long*>(words);

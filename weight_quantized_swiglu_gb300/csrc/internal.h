@@ -440,6 +440,8 @@ struct MoeLayerArgs {
     float* weights = nullptr;
     float* act = nullptr;           // few tokens: [M (topk + S)][I]
     int* amax = nullptr;            // [M (topk + S)]: bits of the largest |act|
+    uint4* act16 = nullptr;         // act in fp16, in the order of the products
+    size_t act16_elems = 0;
     unsigned long long* ticket = nullptr;
     int* err = nullptr;
     uint64_t limit = 0;

@@ -48,8 +48,6 @@ namespace {
 constexpr int kTeams = 2;                           // W13 tiles that a CTA has in hand
 constexpr int kWarps = kTeams * kMoeKSplit;         // 20
 constexpr int kThreads = kWarps * 32;               // and a producer warp
-constexpr int kC13 = 4;                             // 64-k chunks that a W13 warp takes at once
-constexpr int kG2 = 10;                             // k16 groups that a W2 warp takes at once
 constexpr int kMaxStages = 8;
 constexpr uint64_t kWaitNs = 2000000000ull;         // 2 s
 constexpr int kSmemMax = 225 * 1024;
@@ -77,7 +75,7 @@ __host__ __device__ inline int router_splits(int rows, int K, int ctas) {
 
 // Shared memory of the kernel (slots: experts that the tokens can name).
 struct Layout {
-    int x, coef, ridx, slot_e, mask, sel_e, sel_w, cand, part, part_bytes, ring;
+    int x, coef, ridx, slot_e, mask, sel_e, sel_w, cand, part, part_bytes, act16, ring;
     int stage, stages;  // bytes of a ring stage (0: no ring), stages
     int n2, sp;         // W2: experts of a stage, parts of I that different warps take
     int bytes;
@@ -95,6 +93,8 @@ __host__ __device__ inline Layout layout(int M, int K, int I, int E, int nsel, i
     l.sel_w = at, at += 16 * 16 * 4;
     l.cand = at, at += up(M * (int)sizeof(Pick));  // (what follows is read 8 and copied 16 bytes at a time)
     l.part = at, l.part_bytes = 2 * kWarps * 16 * 8 * NT * 4, at += l.part_bytes;
+    l.act16 = -1;  // fp16 act of the routes, where it is small (else in device memory)
+    if (M * nsel * I * 2 <= 32 * 1024) l.act16 = at, at += up(M * nsel * I * 2);
     l.ring = at;
     const int item13 = (int)(kMoeKSplit * (moe_w13_block_bytes(K) + moe_w13_meta_block_bytes(K, MB)));
     const int item2 = 16 * (I / 2) + 16 * (I / 32) * MB;
@@ -303,9 +303,17 @@ QMLP_DEV void router_tile(const MoeLayerArgs& a, const uint4* xsm, int M, int ti
         }
     }
 }
-// x [M, K] -> fp16 in the order of the MMAs, by `threads` threads: slot (j M + m) 4 + t
-// has, of the pair j of steps (32 k), k pairs 2t.. and 8 + 2t.. of token m, then the
-// same of the second step; the tokens' exponents to sig. A thread stays with a token:
+// The order of a lane's eight k of a unit of 32, for A and B alike: a byte of the
+// lane-sliced banks holds two neighbours, and the codes are taken as nibbles p and p +
+// 4 of the word, so pairs (2t, 16 + 2t), (2t + 1, 17 + 2t), (8 + 2t, 24 + 2t),
+// (9 + 2t, 25 + 2t); the first two are one MMA's, the others the next one's.
+// From v[i] = k 8 i + 2t and its neighbour (packed halves) to that order.
+QMLP_DEV uint4 unit_order(uint32_t v0, uint32_t v1, uint32_t v2, uint32_t v3) {
+    return make_uint4(__byte_perm(v0, v2, 0x5410), __byte_perm(v0, v2, 0x7632), __byte_perm(v1, v3, 0x5410),
+                      __byte_perm(v1, v3, 0x7632));
+}
+// x [M, K] -> fp16 in that order, by `threads` threads: slot (j M + m) 4 + t has unit j
+// of token m for lanes t; the tokens' exponents to sig. A thread stays with a token:
 // the row's largest value falls out of the copy, which is then scaled in place.
 template <typename Sync>
 QMLP_DEV void stage_x(const MoeLayerArgs& a, const void* x, int M, uint4* xsm, int* s_max, int* sig, int threads, Sync sync) {
@@ -321,7 +329,7 @@ QMLP_DEV void stage_x(const MoeLayerArgs& a, const void* x, int M, uint4* xsm, i
         for (int q = (warp % wpt) * 32 + lane; q < K / 8; q += 32 * wpt) {
             const uint4 v = row[q];
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            // words 4 q'.. of a pair's 16: word i of them to slot t = i, place q'
+            // k 8 i'.. of the unit: word t of them to slot t, place i'
             const int at = ((q >> 2) * M + m) * 16 + (q & 3);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -337,125 +345,72 @@ QMLP_DEV void stage_x(const MoeLayerArgs& a, const void* x, int M, uint4* xsm, i
     }
     sync();
     if (threadIdx.x < 16) sig[threadIdx.x] = a.x_bf16 ? prescale_exponent(__int_as_float(s_max[threadIdx.x])) : 0;
-    if (a.x_bf16)
-        for (int i = threadIdx.x; i < K / 8 * M; i += threads) {
+    for (int i = threadIdx.x; i < K / 8 * M; i += threads) {
+        const uint4 u = xsm[i];
+        uint32_t v[4] = {u.x, u.y, u.z, u.w};
+        if (a.x_bf16) {
             const int sg = prescale_exponent(__int_as_float(s_max[(i >> 2) % M]));
             const float p0 = __int_as_float((127 + (sg >> 1)) << 23), p1 = __int_as_float((127 + sg - (sg >> 1)) << 23);
-            const uint4 u = xsm[i];
-            uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 v[j] = u32(__floats2half2_rn(__uint_as_float(v[j] << 16) * p0 * p1, __uint_as_float(v[j] & 0xFFFF0000u) * p0 * p1));
-            xsm[i] = make_uint4(v[0], v[1], v[2], v[3]);
         }
+        xsm[i] = unit_order(v[0], v[1], v[2], v[3]);
+    }
     sync();
 }
 
 // ---------------------------------------------------------------------------
-// Weight decode, as moe_awq.cu: {half_fma(q_lo, s, b), half_fma(q_hi, s, b)}
+// Weight decode with the values of moe_awq.cu: half_fma(q, s, b)
 // ---------------------------------------------------------------------------
 QMLP_DEV uint32_t lfma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-template <int MB>
-QMLP_DEV void meta2(uint32_t m, uint32_t& s2, uint32_t& b2) {
-    const uint32_t s = m & 0xFFFFu;
-    uint32_t b;
-    if (MB == 4) {
-        b = m >> 16;
-    } else {
-        const float bf = -(float)((m >> 16) & 0xFFu) * __half2float(__ushort_as_half((unsigned short)s));
-        b = __half_as_ushort(__float2half_rn(bf));
-    }
-    s2 = s | (s << 16);
-    b2 = b | (b << 16);
-}
-// (m & 0x00F0000F) | 0x64006400 in one instruction (the compiler took two)
-QMLP_DEV uint32_t pair_bits(uint32_t m) {
+QMLP_DEV uint32_t ladd2(uint32_t a, uint32_t b) {
     uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(m), "r"(0x00F0000Fu), "r"(0x64006400u));
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-template <int T>  // byte T of the word
-QMLP_DEV uint32_t pair_of(uint32_t w, uint32_t s2, uint32_t b2) {
-    const uint32_t m = __byte_perm(w, 0u, (uint32_t)(T | 4 << 4 | T << 8 | 4 << 12));
-    const uint32_t q = lfma2(pair_bits(m), 0x2C003C00u, 0xD400E400u);
-    return lfma2(q, s2, b2);
+// {scale, scale} and {bias, bias} of a record: the bias is stored (4 bytes) or
+// half(-zero scale): -(1024 + z) + 1024 is exact, and the product rounds once.
+template <int MB>
+QMLP_DEV void meta2(uint32_t m, uint32_t& s2, uint32_t& b2) {
+    s2 = __byte_perm(m, 0, 0x1010);
+    if (MB == 4) b2 = __byte_perm(m, 0, 0x3232);
+    else b2 = hmul2_u32(ladd2(__byte_perm(m, 0xE4E4E4E4u, 0x4242), 0x64006400u), s2);
 }
-
-// A warp's batch of a W13 tile: its four chunks' codes and records (lane-sliced
-// banks in warp blocks, internal.h).
-template <int MB>
-struct Batch13 {
-    uint32_t c[kC13][2][2];  // [chunk][gate, up][unit]
-    uint32_t m[kC13][2][2];
-};
-// codes, meta: the warp's block of codes and of records; at: its first chunk.
-template <int MB>
-QMLP_DEV void load13(Batch13<MB>& b, const uint8_t* codes, const uint8_t* meta, int np, int ms, int at, int lane) {
-    const int g = lane >> 2;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-        for (int pi = 0; pi < kC13 / 2; ++pi) {
-            const int pp = at / 2 + pi;
-            uint4 u = make_uint4(0, 0, 0, 0);
-            if (pp < np) u = *(reinterpret_cast<const uint4*>(codes + (q * np + pp) * 512) + lane);
-            b.c[2 * pi][q][0] = u.x;
-            b.c[2 * pi][q][1] = u.y;
-            b.c[2 * pi + 1][q][0] = u.z;
-            b.c[2 * pi + 1][q][1] = u.w;
-        }
-        const uint8_t* slot = meta + (q * 8 + g) * ms + at * 2 * MB;
-        if (MB == 4) {
-            const uint4 m0 = *reinterpret_cast<const uint4*>(slot), m1 = *(reinterpret_cast<const uint4*>(slot) + 1);
-            const uint32_t mr[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
-#pragma unroll
-            for (int i = 0; i < kC13; ++i) b.m[i][q][0] = mr[2 * i], b.m[i][q][1] = mr[2 * i + 1];
-        } else {
-            uint32_t mr[3 * kC13 / 2 + 1];
-#pragma unroll
-            for (int j = 0; j < 3 * kC13 / 4; ++j) {
-                const uint2 v = *(reinterpret_cast<const uint2*>(slot) + j);
-                mr[2 * j] = v.x;
-                mr[2 * j + 1] = v.y;
-            }
-            mr[3 * kC13 / 2] = 0u;
-#pragma unroll
-            for (int i = 0; i < kC13; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int o = 3 * (2 * i + h);
-                    b.m[i][q][h] = __funnelshift_r(mr[o / 4], mr[o / 4 + 1], 8 * (o % 4)) & 0xFFFFFFu;
-                }
-        }
-    }
+// (w & mask) | magic in one instruction (the compiler took two)
+QMLP_DEV uint32_t and_or(uint32_t w, uint32_t mask) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(0x64006400u));
+    return d;
 }
-
-// A warp's batch of W2: rows g and g + 8 of 16, kG2 groups of 16 k.
-template <int MB>
-struct Batch2 {
-    uint32_t c[kG2 / 2][2], m[kG2 / 2][2];
-};
-// codes, meta: rows n0.. of the expert; u0, u1: units of 32 k.
-template <int MB>
-QMLP_DEV void load2(Batch2<MB>& b, const uint8_t* codes, const uint8_t* meta, int I, int u0, int u1, int lane) {
-    const int g = lane >> 2, t = lane & 3, gpr = I / 32;
+// A lane's word of a unit (eight weights of a row) in the order above: nibbles p and p +
+// 4 are pair p; 0x6400 | q is 1024 + q, 0x6400 | 16 q is 1024 + 16 q; q comes out exact
+// and half_fma rounds once. (Byte by byte, PRMT and LOP3 for two weights: 8 integer
+// instructions a word instead of 5.)
+QMLP_DEV void word_weights(uint32_t w, uint32_t s2, uint32_t b2, uint32_t (&f)[4]) {
+    const uint32_t v = w >> 8;
+    f[0] = lfma2(ladd2(and_or(w, 0x000F000Fu), 0xE400E400u), s2, b2);
+    f[1] = lfma2(lfma2(and_or(w, 0x00F000F0u), 0x2C002C00u, 0xD400D400u), s2, b2);
+    f[2] = lfma2(ladd2(and_or(v, 0x000F000Fu), 0xE400E400u), s2, b2);
+    f[3] = lfma2(lfma2(and_or(v, 0x00F000F0u), 0x2C002C00u, 0xD400D400u), s2, b2);
+}
+// One unit of 32 k of sixteen rows (words and records of rows g and g + 8) times NT
+// tiles of tokens.
+template <int MB, int NT>
+QMLP_DEV void unit_mma(uint32_t w0, uint32_t w8, uint32_t m0, uint32_t m8, const uint4 (&x)[NT], float (&d)[NT][4]) {
+    uint32_t s2, b2, f0[4], f8[4];
+    meta2<MB>(m0, s2, b2);
+    word_weights(w0, s2, b2, f0);
+    meta2<MB>(m8, s2, b2);
+    word_weights(w8, s2, b2, f8);
 #pragma unroll
-    for (int i = 0; i < kG2 / 2; ++i) {
-        b.c[i][0] = b.c[i][1] = b.m[i][0] = b.m[i][1] = 0u;
-        if (u0 + i < u1) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int row = g + 8 * h;
-                b.c[i][h] = *(reinterpret_cast<const unsigned int*>(codes + row * (I / 2) + 16 * (u0 + i)) + t);
-                const uint8_t* mp = meta + (row * gpr + u0 + i) * MB;
-                if (MB == 4) b.m[i][h] = *reinterpret_cast<const unsigned int*>(mp);
-                else b.m[i][h] = (uint32_t)mp[0] | (uint32_t)mp[1] << 8 | (uint32_t)mp[2] << 16;
-            }
-        }
+    for (int n = 0; n < NT; ++n) {
+        mma_f16_16816(d[n], f0[0], f8[0], f0[1], f8[1], x[n].x, x[n].y);
+        mma_f16_16816(d[n], f0[2], f8[2], f0[3], f8[3], x[n].z, x[n].w);
     }
 }
 
@@ -494,85 +449,86 @@ QMLP_DEV void store_any(void* p, int type, size_t at, float v) {
     else static_cast<__half*>(p)[at] = __float2half_rn(v);
 }
 
-// Eight bytes that other CTAs wrote, where `on`: else zeros, without a branch.
-QMLP_DEV float2 ldcg2_if(const float* p, bool on) {
-    float2 v;
+// Sixteen bytes of device memory, where `on`: else zeros, without a branch.
+QMLP_DEV uint4 ldcg4_if(const uint4* p, bool on) {
+    uint4 v;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tmov.f32 %0, 0f00000000;\n\tmov.f32 %1, 0f00000000;\n\t"
-        "@p ld.global.cg.v2.f32 {%0, %1}, [%2];\n\t}"
-        : "=&f"(v.x), "=&f"(v.y)
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\t"
+        "mov.b32 %3, 0;\n\t@p ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
         : "l"(p), "r"((uint32_t)on));
     return v;
 }
-// Part 3's share of one expert: its rows n0.. (codes, meta) times the tokens' act over
-// units u0..u1 of 32 k, times the weights, to part (choice r of the call: r 16 + row).
-// All loads of act and of its largest value go out at once.
-template <int MB, int NT>
-QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t* meta, int u0, int u1, const uint16_t* ridx,
-                      const float* coef, float* part, int lane) {
-    const int M = a.M, I = a.I, g = lane >> 2, t = lane & 3;
-    float d[NT][4], up[NT];
-    int ex[NT];
-    const float* row[NT];
+// The exponent that a row of act is scaled by, from the bits of its largest value.
+QMLP_DEV int act_exponent(int bits) { return max(-113, min(126, prescale_exponent(__int_as_float(bits)))); }
+
+// act (fp32, rows of I) -> fp16 times the row's power of two, in the order of the
+// MMAs: piece (r I / 32 + unit) 4 + t, to `out` (shared or device memory), by threads
+// i0, i0 + hop, ...
+QMLP_DEV void convert_act(const MoeLayerArgs& a, int rows, uint4* out, size_t out_elems, int i0, int hop) {
+    const int nu = a.I / 32;
+#pragma unroll 2
+    for (int i = i0; i < rows * nu * 4; i += hop) {
+        const int t = i & 3, r = (i >> 2) / nu;
+        const float* p = a.act + (size_t)(i >> 2) * 32 + 2 * t;
+        if (!QMLP_INB((size_t)(i >> 2) * 32 + 31, a.act_elems, 107) || !QMLP_INB(i, out_elems, 109)) continue;
+        float2 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __ldcg(reinterpret_cast<const float2*>(p + 8 * j));
+        const float up = __int_as_float((127 + act_exponent(__ldcg(a.amax + r))) << 23);
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = u32(__floats2half2_rn(v[j].x * up, v[j].y * up));
+        out[i] = unit_order(h[0], h[1], h[2], h[3]);
+    }
+}
+
+// Part 3's share of one expert: sixteen rows (codes, meta) times the tokens' act (fp16,
+// converted; SH: in shared memory) over units u0..u1 of 32 k, times the weights, to
+// part (choice r of the call: r 16 + row).
+template <int MB, int NT, bool SH>
+QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t* meta, const uint4* act16, int u0, int u1,
+                      const uint16_t* ridx, const float* coef, float* part, int lane) {
+    const int M = a.M, I = a.I, nu = I / 32, g = lane >> 2, t = lane & 3;
+    float d[NT][4];
+    const uint4* row[NT];
     bool on[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int m = 8 * n + g, r = m < M ? ridx[m] : kNone;
-        on[n] = r != kNone && QMLP_INB((size_t)(r + 1) * I - 1, a.act_elems, 107);
-        row[n] = a.act + (size_t)(on[n] ? r : 0) * I + 2 * t;
-        ex[n] = on[n] ? __ldcg(a.amax + r) : 0;
+        on[n] = r != kNone;
+        row[n] = act16 + (size_t)(on[n] ? r : 0) * nu * 4 + t;
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
     }
-    for (int ub = u0; ub < u1; ub += kG2 / 2) {
-        uint32_t xb[NT][kG2][2];
+    const uint8_t *c0 = codes + g * (I / 2) + 4 * t, *c8 = c0 + 4 * I;
+    const uint8_t *m0 = meta + g * nu * MB, *m8 = m0 + 8 * nu * MB;
+#pragma unroll 4
+    for (int u = u0; u < u1; ++u) {
+        uint4 x[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float2 v[kG2][2];
-#pragma unroll
-            for (int i = 0; i < kG2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    v[i][h] = ldcg2_if(row[n] + 32 * ub + 16 * i + 8 * h, on[n] && ub + i / 2 < u1);
-            if (ub == u0) {
-                ex[n] = max(-113, min(126, prescale_exponent(__int_as_float(ex[n]))));
-                up[n] = __int_as_float((127 + ex[n]) << 23);
-            }
-#pragma unroll
-            for (int i = 0; i < kG2; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) xb[n][i][h] = u32(__floats2half2_rn(v[i][h].x * up[n], v[i][h].y * up[n]));
+            if (SH) x[n] = on[n] ? row[n][u * 4] : make_uint4(0, 0, 0, 0);
+            else x[n] = ldcg4_if(row[n] + u * 4, on[n]);
         }
-        Batch2<MB> b;
-        load2<MB>(b, codes, meta, I, ub, u1, lane);
-#pragma unroll
-        for (int i = 0; i < kG2 / 2; ++i) {
-            if (ub + i < u1) {
-                uint32_t s2[2], b2[2], f[2][4];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    meta2<MB>(b.m[i][h], s2[h], b2[h]);
-                    f[h][0] = pair_of<0>(b.c[i][h], s2[h], b2[h]);
-                    f[h][1] = pair_of<1>(b.c[i][h], s2[h], b2[h]);
-                    f[h][2] = pair_of<2>(b.c[i][h], s2[h], b2[h]);
-                    f[h][3] = pair_of<3>(b.c[i][h], s2[h], b2[h]);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    mma_f16_16816(d[n], f[0][0], f[1][0], f[0][1], f[1][1], xb[n][2 * i][0], xb[n][2 * i][1]);
-                    mma_f16_16816(d[n], f[0][2], f[1][2], f[0][3], f[1][3], xb[n][2 * i + 1][0], xb[n][2 * i + 1][1]);
-                }
-            }
+        uint32_t r0, r8;
+        if (MB == 4) {
+            r0 = *reinterpret_cast<const uint32_t*>(m0 + u * 4);
+            r8 = *reinterpret_cast<const uint32_t*>(m8 + u * 4);
+        } else {
+            r0 = (uint32_t)m0[u * 3] | (uint32_t)m0[u * 3 + 1] << 8 | (uint32_t)m0[u * 3 + 2] << 16;
+            r8 = (uint32_t)m8[u * 3] | (uint32_t)m8[u * 3 + 1] << 8 | (uint32_t)m8[u * 3 + 2] << 16;
         }
+        unit_mma<MB, NT>(*reinterpret_cast<const uint32_t*>(c0 + 16 * u), *reinterpret_cast<const uint32_t*>(c8 + 16 * u), r0,
+                         r8, x, d);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int m = 8 * n + 2 * t + e, back = __shfl_sync(0xffffffffu, ex[n], (2 * t + e) * 4);
-            const int r = m < M ? ridx[m] : kNone;
+            const int m = 8 * n + 2 * t + e, r = m < M ? ridx[m] : kNone;
             if (r != kNone) {  // a choice of token m: its rows g and g + 8
-                const float w = coef[m] * __int_as_float((127 - back) << 23);
+                const float w = coef[m];
                 part[r * 16 + g] = w * d[n][e];
                 part[r * 16 + g + 8] = w * d[n][2 + e];
             }
@@ -641,8 +597,10 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
             }
         }
     }
+    // (a barrier that ran out: the CTA still counts for those that it will not reach)
+    const unsigned long long further = L.act16 < 0 ? 2ull : 1ull;
     if (!grid_barrier(a, &s_pass)) {
-        if (threadIdx.x == 0) atomicAdd(a.ticket, 1ull);  // the second barrier's count
+        if (threadIdx.x == 0) atomicAdd(a.ticket, further);
         return;
     }
 
@@ -801,62 +759,60 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
     if (warp < kWarps) {
         const int team = warp / kMoeKSplit, ks = warp % kMoeKSplit, tid = threadIdx.x - team * kMoeKSplit * 32;
         const int Kc = K / 64, c0 = ks * cpw, nc = max(0, min(Kc, c0 + cpw) - c0);
-        Batch13<MB> b;
         int turn = 0;
         for (int it = team; it < n13; it += kTeams, turn ^= 1) {
             const int item = blockIdx.x + it * gridDim.x, s = item / no, oct = item % no;
-            const size_t blk = ((size_t)slot_e[s] * no + oct) * kMoeKSplit + ks;
-            const uint8_t *codes = a.w13 + blk * cb, *meta = a.w13_meta + blk * mb;
+            const uint8_t *codes, *meta;
+            bool in = true;
             if (RING) {
                 arrived(it);
                 codes = sm + L.ring + (it % L.stages) * L.stage + ks * cb;
                 meta = sm + L.ring + (it % L.stages) * L.stage + kMoeKSplit * cb + ks * mb;
+            } else {
+                const size_t blk = ((size_t)slot_e[s] * no + oct) * kMoeKSplit + ks;
+                codes = a.w13 + blk * cb;
+                meta = a.w13_meta + blk * mb;
+                in = QMLP_INB((blk + 1) * cb - 1, a.w13_bytes, 101) && QMLP_INB((blk + 1) * mb - 1, a.w13_meta_bytes, 102);
             }
             float d[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
-            for (int ch = 0; ch < nc; ch += kC13) {
-                if (RING) {
-                    load13<MB>(b, sm + L.ring + (it % L.stages) * L.stage + ks * cb,
-                               sm + L.ring + (it % L.stages) * L.stage + kMoeKSplit * cb + ks * mb, np, ms, ch, lane);
-                } else if (QMLP_INB((blk + 1) * cb - 1, a.w13_bytes, 101) && QMLP_INB((blk + 1) * mb - 1, a.w13_meta_bytes, 102)) {
-                    load13<MB>(b, codes, meta, np, ms, ch, lane);
+            // pairs of 64-k chunks: four units of the gate row g and of the up row g
+            const uint4* cp = reinterpret_cast<const uint4*>(codes) + lane;
+            const uint8_t* mp = meta + g * ms;
+#pragma unroll 2
+            for (int pr = 0; pr < (nc + 1) / 2; ++pr) {
+                if (!in) break;
+                const uint4 cg = cp[pr * 32], cu = cp[(np + pr) * 32];
+                const uint32_t wg[4] = {cg.x, cg.y, cg.z, cg.w}, wu[4] = {cu.x, cu.y, cu.z, cu.w};
+                uint32_t rg[4], ru[4];
+                if (MB == 4) {
+                    const uint4 p = *reinterpret_cast<const uint4*>(mp + pr * 16), q = *reinterpret_cast<const uint4*>(mp + 8 * ms + pr * 16);
+                    rg[0] = p.x, rg[1] = p.y, rg[2] = p.z, rg[3] = p.w;
+                    ru[0] = q.x, ru[1] = q.y, ru[2] = q.z, ru[3] = q.w;
+                } else {
+                    const uint32_t *p = reinterpret_cast<const uint32_t*>(mp + pr * 12), *q = reinterpret_cast<const uint32_t*>(mp + 8 * ms + pr * 12);
+                    const uint32_t a0 = p[0], a1 = p[1], a2 = p[2], e0 = q[0], e1 = q[1], e2 = q[2];
+                    rg[0] = a0, rg[1] = __funnelshift_r(a0, a1, 24), rg[2] = __funnelshift_r(a1, a2, 16), rg[3] = a2 >> 8;
+                    ru[0] = e0, ru[1] = __funnelshift_r(e0, e1, 24), ru[2] = __funnelshift_r(e1, e2, 16), ru[3] = e2 >> 8;
                 }
-                if (RING && ch + kC13 >= nc) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(empty(it % L.stages));
-                }
 #pragma unroll
-                for (int i = 0; i < kC13; ++i) {
-                    if (ch + i < nc) {
-                        uint32_t s2[2][2], b2[2][2];
+                for (int h = 0; h < 4; ++h) {
+                    if (2 * pr + (h >> 1) < nc) {
+                        uint4 x[NT];
 #pragma unroll
-                        for (int q = 0; q < 2; ++q)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) meta2<MB>(b.m[i][q][h], s2[q][h], b2[q][h]);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {  // steps 2h and 2h + 1: record h
-                            uint32_t f[2][4];
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                f[q][0] = pair_of<0>(b.c[i][q][h], s2[q][h], b2[q][h]);
-                                f[q][1] = pair_of<1>(b.c[i][q][h], s2[q][h], b2[q][h]);
-                                f[q][2] = pair_of<2>(b.c[i][q][h], s2[q][h], b2[q][h]);
-                                f[q][3] = pair_of<3>(b.c[i][q][h], s2[q][h], b2[q][h]);
-                            }
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                const uint4 x = xsm[(((c0 + ch + i) * 2 + h) * M + min(8 * n + g, M - 1)) * 4 + t];
-                                mma_f16_16816(d[n], f[0][0], f[1][0], f[0][1], f[1][1], x.x, x.y);
-                                mma_f16_16816(d[n], f[0][2], f[1][2], f[0][3], f[1][3], x.z, x.w);
-                            }
-                        }
+                        for (int n = 0; n < NT; ++n)
+                            x[n] = xsm[(((c0 + 2 * pr) * 2 + h) * M + min(8 * n + g, M - 1)) * 4 + t];
+                        unit_mma<MB, NT>(wg[h], wu[h], rg[h], ru[h], x, d);
                     }
                 }
             }
-            if (RING && nc == 0 && lane == 0) mbar_arrive(empty(it % L.stages));
+            if (RING) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty(it % L.stages));
+            }
             float* pt = part + ((turn * kTeams + team) * kMoeKSplit) * 16 * kC;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -885,11 +841,23 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
         }
     }
     if (!grid_barrier(a, &s_pass)) {
+        if (threadIdx.x == 0 && further > 1) atomicAdd(a.ticket, 1ull);
         // (copies in flight end before the CTA does)
         if (RING && warp == kWarps)
             for (int q = sent - 1; q >= 0 && q >= sent - L.stages; --q)
                 mbar_wait_bounded(full(q % L.stages), (uint32_t)((q / L.stages) & 1), a.limit);
         return;
+    }
+
+    if (L.act16 < 0) {  // act has no room in shared memory: converted once, a third barrier
+        if (warp < kWarps)
+            convert_act(a, M * nsel, a.act16, a.act16_elems, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
+        if (!grid_barrier(a, &s_pass)) {
+            if (RING && warp == kWarps)
+                for (int q = sent - 1; q >= 0 && q >= sent - L.stages; --q)
+                    mbar_wait_bounded(full(q % L.stages), (uint32_t)((q / L.stages) & 1), a.limit);
+            return;
+        }
     }
 
     // ---------------- 3: W2 and the weighted sum ----------------
@@ -903,6 +871,14 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
         return;
     }
     const int nu = I / 32, prow = M * nsel;
+    for (int i = threadIdx.x; i < slots * M; i += kThreads)
+        if (ridx[i] != kNone) coef[i] *= __int_as_float((127 - act_exponent(__ldcg(a.amax + ridx[i]))) << 23);
+    const uint4* act16 = a.act16;
+    if (L.act16 >= 0) {  // every CTA for itself
+        convert_act(a, prow, reinterpret_cast<uint4*>(sm + L.act16), (size_t)prow * nu * 4, threadIdx.x, kThreads);
+        act16 = reinterpret_cast<const uint4*>(sm + L.act16);
+    }
+    named_bar_sync(1, kThreads);
     int first = 0;  // the warp that takes the next unit: the units of all stages go round
     for (int tl = 0; tl < tiles2; tl += 2) {  // two tiles between barriers
         const int nt = min(2, tiles2 - tl);
@@ -916,16 +892,23 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
                 for (u += u < 0 ? kWarps : 0; u < n * L.sp; u += kWarps) {
                     const int s = s0 + u / L.sp, ip = u % L.sp, u0 = ip * nu / L.sp, u1 = (ip + 1) * nu / L.sp;
                     float* pp = part + (q * L.sp + ip) * prow * 16;
+                    const uint8_t *codes, *meta;
+                    bool in = true;
                     if (RING) {
-                        const uint8_t* codes = stage + (u / L.sp) * (cb2 + mb2);
-                        w2_unit<MB, NT>(a, codes, codes + cb2, u0, u1, ridx + s * M, coef + s * M, pp, lane);
+                        codes = stage + (u / L.sp) * (cb2 + mb2);
+                        meta = codes + cb2;
                     } else {
                         const size_t row = (size_t)slot_e[s] * K + 16 * tile;
-                        if (QMLP_INB((row + 16) * (I / 2) - 1, a.w2_bytes, 103) &&
-                            QMLP_INB((row + 16) * (I / 32) * MB - 1, a.w2_meta_bytes, 104))
-                            w2_unit<MB, NT>(a, a.w2 + row * (I / 2), a.w2_meta + row * (I / 32) * MB, u0, u1, ridx + s * M,
-                                            coef + s * M, pp, lane);
+                        codes = a.w2 + row * (I / 2);
+                        meta = a.w2_meta + row * (I / 32) * MB;
+                        in = QMLP_INB((row + 16) * (I / 2) - 1, a.w2_bytes, 103) &&
+                             QMLP_INB((row + 16) * (I / 32) * MB - 1, a.w2_meta_bytes, 104);
                     }
+                    if (!in) continue;
+                    if (L.act16 >= 0)
+                        w2_unit<MB, NT, true>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, lane);
+                    else
+                        w2_unit<MB, NT, false>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, lane);
                 }
                 first = (first + n * L.sp) % kWarps;
                 if (RING) {  // ten arrivals a stage: one for two warps
@@ -1013,17 +996,17 @@ __global__ void __launch_bounds__(256) router_frag_kernel(const void* w, const v
         const int j = (int)(rest % n32), tile = (int)(rest / n32 % tiles), pl = (int)(rest / n32 / tiles);
         uint32_t o[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {  // rows g, g + 8 at k 2t.., then at 8 + 2t..
-            const int row = tile * 16 + g + 8 * (q & 1), k = 32 * j + 16 * st + 8 * (q >> 1) + 2 * t;
+        for (int q = 0; q < 4; ++q) {  // rows g, g + 8 of pair 2 st, then of 2 st + 1 (unit_order)
+            const int row = tile * 16 + g + 8 * (q & 1), k = 32 * j + 8 * st + 2 * t + (q >> 1);
             float v[2] = {0.0f, 0.0f};
             if (row < rows) {
                 const void* p = row < E ? w : sg;
                 const size_t at = (size_t)(row < E ? row : row - E) * K + k;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = type == 0   ? static_cast<const float*>(p)[at + e]
-                                    : type == 1 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + e])
-                                                : __half2float(static_cast<const __half*>(p)[at + e]);
+                for (int e = 0; e < 2; ++e) {  // k and k + 16
+                    const float f = type == 0   ? static_cast<const float*>(p)[at + 16 * e]
+                                    : type == 1 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at + 16 * e])
+                                                : __half2float(static_cast<const __half*>(p)[at + 16 * e]);
                     v[e] = scalbnf(f, rexp[row]);
                     if (pl) v[e] -= __half2float(__float2half_rn(v[e]));  // what the first plane leaves
                 }
