@@ -747,7 +747,7 @@ qmlp_status qmlp_debug_bounds(int* site, unsigned long long* index) {
                                                           bounds_take_gemv_stream, bounds_take_gemv_dec,
                                                           bounds_take_moe_awq, bounds_take_moe_grouped,
                                                           bounds_take_tp_shard, bounds_take_lowrank,
-                                                          bounds_take_adamw,      bounds_take_norm,
+                                                          bounds_take_adamw,      bounds_take_norm,       bounds_take_norm_f16,
                                                           bounds_take_linear,     bounds_take_moe_layer};
     unsigned long long first = 0;
     for (auto take : units) {

@@ -112,6 +112,7 @@ qmlp_status norm_call(const qmlp_norm_t* h, const qmlp_norm_io* io, int M, bool 
     a.gate = io->gate;
     a.stats = reinterpret_cast<float2*>(io->stats);
     a.elems = n;
+    a.num_sms = h->num_sms;
     const size_t gn = d.gate == QMLP_GATE_CHANNEL ? (size_t)d.K : d.gate == QMLP_GATE_TOKEN ? (size_t)M : n;
     qmlp_status st = QMLP_OK;
     auto add = [&](const void* p, qmlp_dtype t, size_t k, bool w) {
@@ -192,7 +193,7 @@ qmlp_status qmlp_norm_forward(qmlp_norm_t* h, const qmlp_norm_io* io, int M, qml
         if (fault("launch")) return QMLP_ERR_CUDA;
         c.a.h = io->residual_out;
         c.a.y = io->out;
-        c.a.vec = c.aligned_all && h->d.K % 8 == 0;
+        c.a.vec = c.aligned_all;
         return from_cuda(launch_norm(c.a, h->d.dt == QMLP_DT_FP16, h->d.rdt == QMLP_DT_FP32, false,
                                      reinterpret_cast<cudaStream_t>(stream)));
     });
@@ -242,7 +243,7 @@ qmlp_status qmlp_norm_backward(qmlp_norm_t* h, const qmlp_norm_io* io, const qml
         a.shares = h->shares;
         a.part = g->dpost_w || g->dpre_w || (g->dgate && d.gate == QMLP_GATE_CHANNEL) ? h->part : nullptr;
         a.part_elems = (size_t)h->shares * 3 * d.K;
-        a.vec = c.aligned_all && d.K % 8 == 0;
+        a.vec = c.aligned_all;
         return from_cuda(launch_norm(a, d.dt == QMLP_DT_FP16, d.rdt == QMLP_DT_FP32, true,
                                      reinterpret_cast<cudaStream_t>(stream)));
     });

@@ -349,7 +349,7 @@ cudaError_t launch_adamw(const AdamWChunk* chunks, long count, bool param_bf16, 
                          const AdamWStep& k, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
-// Norms before and after a block (norm.cu)
+// Norms before and after a block (norm.cuh)
 // ---------------------------------------------------------------------------
 enum NormGate { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
 constexpr int kNormMaxK = 16384;
@@ -359,7 +359,7 @@ struct NormArgs {
     float eps = 0, rK = 0, offset = 0, scale = 1;  // rK: 1 / K
     int gate_kind = kGateNone;
     bool w_f32 = false;        // weights (and a channel gate) are fp32, else of z's type
-    bool vec = false;          // K % 8 == 0 and every pointer aligned for 8 elements at a time
+    bool vec = false;          // every pointer is 16-byte aligned
     const void *z = nullptr, *r = nullptr, *post_w = nullptr, *pre_w = nullptr, *gate = nullptr;
     void *h = nullptr, *y = nullptr;
     float2* stats = nullptr;   // [M] 1/rms of z and h
@@ -367,9 +367,20 @@ struct NormArgs {
     const void *dy = nullptr, *dh = nullptr;
     void *dz = nullptr, *dr = nullptr, *dpost = nullptr, *dpre = nullptr, *dgate = nullptr;
     float* part = nullptr;     // [shares][3][K]: the CTAs' column sums (null: none is wanted)
-    int shares = 0;
+    int shares = 0, num_sms = 0;
     size_t elems = 0, part_elems = 0;  // index checks: M K; floats of part
 };
+// A kernel's limit of dynamic shared memory, raised once a device (`done`: a bit each).
+template <typename F>
+cudaError_t smem_once(F* kernel, int bytes, unsigned long& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done |= 1ul << dev;
+    return e;
+}
+cudaError_t launch_norm_f16(const NormArgs& a, bool r_f32, bool backward, cudaStream_t s);
 cudaError_t launch_norm(const NormArgs& a, bool t_f16, bool r_f32, bool backward, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
@@ -468,6 +479,7 @@ cudaError_t bounds_take_tp_shard(unsigned long long* v);
 cudaError_t bounds_take_lowrank(unsigned long long* v);
 cudaError_t bounds_take_adamw(unsigned long long* v);
 cudaError_t bounds_take_norm(unsigned long long* v);
+cudaError_t bounds_take_norm_f16(unsigned long long* v);
 cudaError_t bounds_take_linear(unsigned long long* v);
 cudaError_t bounds_take_moe_layer(unsigned long long* v);
 

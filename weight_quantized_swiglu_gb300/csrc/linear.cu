@@ -1006,13 +1006,8 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     }
     const size_t fixed = x + red + group_own * P.batch;
     P.stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(2, (all - fixed) / kStage));
-    static bool attr = false;
-    if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_few_kernel<G, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kSmemMax);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static unsigned long done = 0;
+    if (const cudaError_t e = smem_once(linear_few_kernel<G, ONE>, kSmemMax, done); e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     const cudaLaunchConfig_t cfg = few_config(P, (W + 1) * 32, fixed + (size_t)P.stages * kStage, s, at);
     return cudaLaunchKernelEx(&cfg, linear_few_kernel<G, ONE>, a, P);
@@ -1034,13 +1029,8 @@ cudaError_t launch_mid(const LinearArgs& a, int num_sms, cudaStream_t s) {
     const size_t stage = (size_t)P.tg * CS * kRec + (size_t)CS * 256 * a.M, own = (size_t)kMidWarps * kC * 16 * 4;
     P.stages = (int)std::min<size_t>(kMaxStages, (kSmemMax - 2048 - own) / stage);
     if (P.stages < 2) return cudaErrorInvalidValue;
-    static bool attr = false;
-    if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(linear_mid_kernel<G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kSmemMax);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static unsigned long done = 0;
+    if (const cudaError_t e = smem_once(linear_mid_kernel<G, NT>, kSmemMax, done); e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     FewPlan X = {};
     X.S = 1;

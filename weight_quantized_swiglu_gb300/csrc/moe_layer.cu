@@ -1019,13 +1019,8 @@ __global__ void __launch_bounds__(256) router_frag_kernel(const void* w, const v
 
 template <int MB, int NT, bool RING>
 cudaError_t launch_few(const MoeLayerArgs& a, int bytes, int num_sms, cudaStream_t s) {
-    static bool attr = false;
-    if (!attr) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(moe_layer_kernel<MB, NT, RING>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static unsigned long done = 0;
+    if (const cudaError_t e = smem_once(moe_layer_kernel<MB, NT, RING>, kSmemMax, done); e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)num_sms);
     cfg.blockDim = dim3(kThreads + 32);
@@ -1066,12 +1061,8 @@ cudaError_t launch_moe_layer_few(MoeLayerArgs a, int meta_bytes, int num_sms, cu
 cudaError_t launch_moe_router(const MoeLayerArgs& a, cudaStream_t s) {
     const int tiles = (a.E + (a.sgate ? a.S : 0) + 15) / 16;
     const size_t smem = (size_t)std::min(8, a.M) * a.K * 2;
-    static bool attr = false;
-    if (!attr) {
-        const cudaError_t e = cudaFuncSetAttribute(router_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    static unsigned long done = 0;
+    if (const cudaError_t e = smem_once(router_kernel, kSmemMax, done); e != cudaSuccess) return e;
     if (smem > kSmemMax) return cudaErrorInvalidValue;
     router_kernel<<<dim3((unsigned)((tiles + 7) / 8), (unsigned)((a.M + 7) / 8)), 256, smem, s>>>(a);
     const cudaError_t e = cudaPeekAtLastError();
