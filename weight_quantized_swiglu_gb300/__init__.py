@@ -846,18 +846,6 @@ def _dtypes():
     return {torch.bfloat16: DT_BF16, torch.float16: DT_FP16, torch.float32: DT_FP32}
 
 
-def _typed(who, name, t, dtype, shape):
-    """Refuse what is not a contiguous CUDA tensor of this type and shape, or of
-    the shape's elements in its order (raw addresses are the caller's)."""
-    if t is None or isinstance(t, int):
-        return
-    n = 1
-    for s in shape:
-        n *= s
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.numel() != n or t.shape[-1] != shape[-1]:
-        raise ValueError(f"{who}: {name} has to be a contiguous CUDA tensor of {dtype}, {tuple(shape)}")
-
-
 class BlockNorm:
     """The norms before and after a block with its gate, residual and residual
     scale (qmlp_norm_*):
@@ -881,19 +869,25 @@ class BlockNorm:
             raise ValueError("BlockNorm: types are bf16, fp16 or fp32, gate is none, channel, token or full")
         self.h = qmlp_norm_create(qmlp_norm_desc(K, eps, weight_offset, scale, kinds[self.dt], kinds[self.rdt],
                                                  kinds[self.wdt], gates[gate]), stream)
+        # type, whether a token has its own, last dimension (0: M)
+        rows, stream_rows, cols = (self.dt, True, K), (self.rdt, True, K), (self.wdt, False, K)
+        args = dict(z=rows, residual=stream_rows, post_w=cols, pre_w=cols, residual_out=stream_rows, out=rows,
+                    gate={"channel": cols, "token": (self.dt, False, 0)}.get(gate, rows))
+        self._args = {**args, "dout": args["out"], "stats": (torch.float32, True, 2),
+                      **{"d" + n: k for n, k in args.items() if n != "out"}}
+        self._forward, self._backward = lib().qmlp_norm_forward, lib().qmlp_norm_backward
 
-    def _check(self, M, **tensors):
-        rows, cols = (self.dt, (M, self.K)), (self.wdt, (self.K,))
-        gate = {"none": rows, "channel": cols, "token": (self.dt, (M,)), "full": rows}[self.gate]
-        kinds = {"z": rows, "residual": (self.rdt, (M, self.K)), "post_w": cols, "pre_w": cols, "gate": gate,
-                 "residual_out": (self.rdt, (M, self.K)), "out": rows, "dout": rows}
-        for n, t in tensors.items():
-            if n == "stats":
-                import torch
-                _typed("BlockNorm", n, t, torch.float32, (M, 2))
-            else:
-                dtype, shape = kinds[n] if n in kinds else kinds[n[1:]]
-                _typed("BlockNorm", n, t, dtype, shape)
+    def _addr(self, n, t, M):
+        """The address of argument n; refuses what is not a contiguous CUDA tensor of
+        its type and shape (raw addresses are the caller's)."""
+        if t is None or isinstance(t, int):
+            return t
+        dtype, rows, last = self._args[n]
+        if (t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or
+                t.numel() != (M * last if rows else last or M) or t.dim() == 0 or t.size(-1) != (last or M)):
+            shape = ((M, last) if rows else (last or M,))
+            raise ValueError(f"BlockNorm: {n} has to be a contiguous CUDA tensor of {dtype}, {shape}")
+        return t.data_ptr()
 
     def _rows(self, z, residual):
         t = z if z is not None else residual
@@ -906,10 +900,11 @@ class BlockNorm:
         """Writes residual_out (h) and out (y); stats [M, 2] fp32 keeps what
         backward needs. Returns (residual_out, out)."""
         M = self._rows(z, residual) if M is None else M
-        t = dict(z=z, residual=residual, post_w=post_w, pre_w=pre_w, gate=gate, residual_out=residual_out, out=out,
-                 stats=stats)
-        self._check(M, **t)
-        _chk(qmlp_norm_forward(self.h, qmlp_norm_io(*[_ptr(a) for a in t.values()]), M, stream), "qmlp_norm_forward")
+        addr = self._addr
+        io = qmlp_norm_io(addr("z", z, M), addr("residual", residual, M), addr("post_w", post_w, M),
+                          addr("pre_w", pre_w, M), addr("gate", gate, M), addr("residual_out", residual_out, M),
+                          addr("out", out, M), addr("stats", stats, M))
+        _chk(self._forward(self.h, io, M, _stream(stream)), "qmlp_norm_forward")
         return residual_out, out
 
     def backward(self, stats, z=None, residual=None, post_w=None, pre_w=None, gate=None, dout=None,
@@ -918,13 +913,13 @@ class BlockNorm:
         """From dout (y's gradient) and dresidual_out (h's, None: zero) the
         gradients that are given: dz, dresidual, dpost_w, dpre_w, dgate."""
         M = self._rows(z, residual) if M is None else M
-        t = dict(z=z, residual=residual, post_w=post_w, pre_w=pre_w, gate=gate, residual_out=None, out=None,
-                 stats=stats)
-        g = dict(dout=dout, dresidual_out=dresidual_out, dz=dz, dresidual=dresidual, dpost_w=dpost_w, dpre_w=dpre_w,
-                 dgate=dgate)
-        self._check(M, **t, **g)
-        _chk(qmlp_norm_backward(self.h, qmlp_norm_io(*[_ptr(a) for a in t.values()]),
-                                qmlp_norm_grads(*[_ptr(a) for a in g.values()]), M, stream), "qmlp_norm_backward")
+        addr = self._addr
+        io = qmlp_norm_io(addr("z", z, M), addr("residual", residual, M), addr("post_w", post_w, M),
+                          addr("pre_w", pre_w, M), addr("gate", gate, M), None, None, addr("stats", stats, M))
+        grads = qmlp_norm_grads(addr("dout", dout, M), addr("dresidual_out", dresidual_out, M), addr("dz", dz, M),
+                                addr("dresidual", dresidual, M), addr("dpost_w", dpost_w, M),
+                                addr("dpre_w", dpre_w, M), addr("dgate", dgate, M))
+        _chk(self._backward(self.h, io, grads, M, _stream(stream)), "qmlp_norm_backward")
 
     def close(self):
         if getattr(self, "h", None):
