@@ -884,7 +884,7 @@ class BlockNorm:
             return t
         dtype, rows, last = self._args[n]
         if (t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or
-                t.numel() != (M * last if rows else last or M) or t.dim() == 0 or t.size(-1) != (last or M)):
+                t.numel() != (M * last if rows else last or M) or t.dim() == 0 or t.shape[-1] != (last or M)):
             shape = ((M, last) if rows else (last or M,))
             raise ValueError(f"BlockNorm: {n} has to be a contiguous CUDA tensor of {dtype}, {shape}")
         return t.data_ptr()

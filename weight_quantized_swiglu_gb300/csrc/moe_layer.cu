@@ -73,6 +73,8 @@ __host__ __device__ inline int router_splits(int rows, int K, int ctas) {
     return s < 1 ? 1 : s;
 }
 
+// W2's rows of I / 2 bytes would meet on a bank: four units at a time (w2_quads).
+__host__ __device__ inline bool quads(int I) { return I % 128 == 0; }
 // Shared memory of the kernel (slots: experts that the tokens can name).
 struct Layout {
     int x, coef, ridx, slot_e, mask, sel_e, sel_w, cand, part, part_bytes, act16, ring;
@@ -321,21 +323,21 @@ QMLP_DEV void stage_x(const MoeLayerArgs& a, const void* x, int M, uint4* xsm, i
     const int wpt = max(1, nw / M);  // warps a token
     if (threadIdx.x < 16) s_max[threadIdx.x] = 0;
     sync();
-    uint32_t* xw = reinterpret_cast<uint32_t*>(xsm);
     for (int m = warp / wpt; m < M; m += nw / wpt) {
-        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + (size_t)m * K);
+        const uint32_t* row = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(x) + (size_t)m * K);
         float mx = 0.0f;
 #pragma unroll 4
         for (int q = (warp % wpt) * 32 + lane; q < K / 8; q += 32 * wpt) {
-            const uint4 v = row[q];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            // k 8 i'.. of the unit: word t of them to slot t, place i'
-            const int at = ((q >> 2) * M + m) * 16 + (q & 3);
+            // lane t of unit j: word t of its four pieces (16 bytes in four places at once
+            // met on a bank: 8 tokens of 2560 4.1 us)
+            const int j = q >> 2, t = q & 3;
+            uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                xw[at + 4 * i] = w[i];
+            for (int i = 0; i < 4; ++i) w[i] = row[16 * j + 4 * i + t];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
                 mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-            }
+            xsm[(j * M + m) * 4 + t] = a.x_bf16 ? make_uint4(w[0], w[1], w[2], w[3]) : unit_order(w[0], w[1], w[2], w[3]);
         }
         if (a.x_bf16) {
 #pragma unroll
@@ -345,18 +347,21 @@ QMLP_DEV void stage_x(const MoeLayerArgs& a, const void* x, int M, uint4* xsm, i
     }
     sync();
     if (threadIdx.x < 16) sig[threadIdx.x] = a.x_bf16 ? prescale_exponent(__int_as_float(s_max[threadIdx.x])) : 0;
-    for (int i = threadIdx.x; i < K / 8 * M; i += threads) {
-        const uint4 u = xsm[i];
-        uint32_t v[4] = {u.x, u.y, u.z, u.w};
-        if (a.x_bf16) {
-            const int sg = prescale_exponent(__int_as_float(s_max[(i >> 2) % M]));
+    if (a.x_bf16)  // a thread's own pieces again
+        for (int m = warp / wpt; m < M; m += nw / wpt) {
+            const int sg = prescale_exponent(__int_as_float(s_max[m]));
             const float p0 = __int_as_float((127 + (sg >> 1)) << 23), p1 = __int_as_float((127 + sg - (sg >> 1)) << 23);
+#pragma unroll 2
+            for (int q = (warp % wpt) * 32 + lane; q < K / 8; q += 32 * wpt) {
+                uint4* at = xsm + ((q >> 2) * M + m) * 4 + (q & 3);
+                const uint4 u = *at;
+                uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = u32(__floats2half2_rn(__uint_as_float(v[j] << 16) * p0 * p1, __uint_as_float(v[j] & 0xFFFF0000u) * p0 * p1));
+                for (int j = 0; j < 4; ++j)
+                    v[j] = u32(__floats2half2_rn(__uint_as_float(v[j] << 16) * p0 * p1, __uint_as_float(v[j] & 0xFFFF0000u) * p0 * p1));
+                *at = unit_order(v[0], v[1], v[2], v[3]);
+            }
         }
-        xsm[i] = unit_order(v[0], v[1], v[2], v[3]);
-    }
     sync();
 }
 
@@ -400,18 +405,29 @@ QMLP_DEV void word_weights(uint32_t w, uint32_t s2, uint32_t b2, uint32_t (&f)[4
 }
 // One unit of 32 k of sixteen rows (words and records of rows g and g + 8) times NT
 // tiles of tokens.
-template <int MB, int NT>
-QMLP_DEV void unit_mma(uint32_t w0, uint32_t w8, uint32_t m0, uint32_t m8, const uint4 (&x)[NT], float (&d)[NT][4]) {
-    uint32_t s2, b2, f0[4], f8[4];
-    meta2<MB>(m0, s2, b2);
-    word_weights(w0, s2, b2, f0);
-    meta2<MB>(m8, s2, b2);
-    word_weights(w8, s2, b2, f8);
+template <int NT>
+QMLP_DEV void words_mma(uint32_t w0, uint32_t w8, uint32_t s0, uint32_t b0, uint32_t s8, uint32_t b8, const uint4 (&x)[NT],
+                        float (&d)[NT][4]) {
+    uint32_t f0[4], f8[4];
+    word_weights(w0, s0, b0, f0);
+    word_weights(w8, s8, b8, f8);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         mma_f16_16816(d[n], f0[0], f8[0], f0[1], f8[1], x[n].x, x[n].y);
         mma_f16_16816(d[n], f0[2], f8[2], f0[3], f8[3], x[n].z, x[n].w);
     }
+}
+template <int MB, int NT>
+QMLP_DEV void unit_mma(uint32_t w0, uint32_t w8, uint32_t m0, uint32_t m8, const uint4 (&x)[NT], float (&d)[NT][4]) {
+    uint32_t s0, b0, s8, b8;
+    meta2<MB>(m0, s0, b0);
+    meta2<MB>(m8, s8, b8);
+    words_mma<NT>(w0, w8, s0, b0, s8, b8, x, d);
+}
+template <int MB>
+QMLP_DEV uint32_t record(const uint8_t* p) {
+    if (MB == 4) return *reinterpret_cast<const uint32_t*>(p);
+    return (uint32_t)p[0] | (uint32_t)p[1] << 8 | (uint32_t)p[2] << 16;
 }
 
 QMLP_DEV unsigned long long ld_acq(const unsigned long long* p) {
@@ -465,11 +481,13 @@ QMLP_DEV int act_exponent(int bits) { return max(-113, min(126, prescale_exponen
 // act (fp32, rows of I) -> fp16 times the row's power of two, in the order of the
 // MMAs: piece (r I / 32 + unit) 4 + t, to `out` (shared or device memory), by threads
 // i0, i0 + hop, ...
+template <bool QUAD>
 QMLP_DEV void convert_act(const MoeLayerArgs& a, int rows, uint4* out, size_t out_elems, int i0, int hop) {
+    const bool quad = QUAD && quads(a.I);
     const int nu = a.I / 32;
-#pragma unroll 2
+#pragma unroll 4
     for (int i = i0; i < rows * nu * 4; i += hop) {
-        const int t = i & 3, r = (i >> 2) / nu;
+        const int t = i & 3, r = (i >> 2) / nu, u = (i >> 2) % nu;
         const float* p = a.act + (size_t)(i >> 2) * 32 + 2 * t;
         if (!QMLP_INB((size_t)(i >> 2) * 32 + 31, a.act_elems, 107) || !QMLP_INB(i, out_elems, 109)) continue;
         float2 v[4];
@@ -479,8 +497,25 @@ QMLP_DEV void convert_act(const MoeLayerArgs& a, int rows, uint4* out, size_t ou
         uint32_t h[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) h[j] = u32(__floats2half2_rn(v[j].x * up, v[j].y * up));
-        out[i] = unit_order(h[0], h[1], h[2], h[3]);
+        // (of four units: lane t's pieces are unit t's, see w2_quads)
+        out[quad ? i + 3 * (t - (u & 3)) : i] = unit_order(h[0], h[1], h[2], h[3]);
     }
+}
+
+// A unit's results, times the weights, to part.
+template <int NT>
+QMLP_DEV void unit_out(const float (&d)[NT][4], int M, int t, int g, const uint16_t* ridx, const float* coef, float* part) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int m = 8 * n + 2 * t + e, r = m < M ? ridx[m] : kNone;
+            if (r != kNone) {  // a choice of token m: its rows g and g + 8
+                const float w = coef[m];
+                part[r * 16 + g] = w * d[n][e];
+                part[r * 16 + g + 8] = w * d[n][2 + e];
+            }
+        }
 }
 
 // Part 3's share of one expert: sixteen rows (codes, meta) times the tokens' act (fp16,
@@ -522,17 +557,52 @@ QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t
         unit_mma<MB, NT>(*reinterpret_cast<const uint32_t*>(c0 + 16 * u), *reinterpret_cast<const uint32_t*>(c8 + 16 * u), r0,
                          r8, x, d);
     }
+    unit_out<NT>(d, M, t, g, ridx, coef, part);
+}
+
+// The same with act in device memory, four units at a time: lane t takes unit u + t whole, a
+// word of it a step, one read of 16 bytes a row and a record for the four. (A word a unit
+// has four or eight rows on one bank where I is a multiple of 128: 4 tokens of 64 experts
+// of 4096 x 1024 103 us instead of 87; elsewhere it is ahead, I = 704 84 to 88 us.) act lies
+// in that order, and is asked for PF steps ahead.
+template <int MB, int NT>
+QMLP_DEV void w2_quads(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t* meta, const uint4* act16, int u0, int u1,
+                       const uint16_t* ridx, const float* coef, float* part, int lane) {
+    constexpr int PF = NT == 1 ? 4 : 2;
+    const int M = a.M, I = a.I, nu = I / 32, g = lane >> 2, t = lane & 3;
+    float d[NT][4];
+    const uint4* row[NT];
+    bool on[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        const int m = 8 * n + g, r = m < M ? ridx[m] : kNone;
+        on[n] = r != kNone;
+        row[n] = act16 + (size_t)(on[n] ? r : 0) * nu * 4 + t;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int m = 8 * n + 2 * t + e, r = m < M ? ridx[m] : kNone;
-            if (r != kNone) {  // a choice of token m: its rows g and g + 8
-                const float w = coef[m];
-                part[r * 16 + g] = w * d[n][e];
-                part[r * 16 + g + 8] = w * d[n][2 + e];
-            }
+        for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+    }
+    const uint8_t *c0 = codes + g * (I / 2) + 16 * t, *c8 = c0 + 4 * I;
+    const uint8_t *m0 = meta + (g * nu + t) * MB, *m8 = m0 + 8 * nu * MB;
+    uint4 x[PF][NT];
+#pragma unroll
+    for (int j = 0; j < PF; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[j][n] = ldcg4_if(row[n] + (u0 + j) * 4, on[n] && u0 < u1);
+#pragma unroll 1
+    for (int u = u0; u < u1; u += 4) {
+        const uint4 p = *reinterpret_cast<const uint4*>(c0 + 16 * u), q = *reinterpret_cast<const uint4*>(c8 + 16 * u);
+        const uint32_t w0[4] = {p.x, p.y, p.z, p.w}, w8[4] = {q.x, q.y, q.z, q.w};
+        uint32_t s0, b0, s8, b8;
+        meta2<MB>(record<MB>(m0 + u * MB), s0, b0);
+        meta2<MB>(record<MB>(m8 + u * MB), s8, b8);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            words_mma<NT>(w0[j], w8[j], s0, b0, s8, b8, x[j % PF], d);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) x[j % PF][n] = ldcg4_if(row[n] + (u + j + PF) * 4, on[n] && u + j + PF < u1);
         }
+    }
+    unit_out<NT>(d, M, t, g, ridx, coef, part);
 }
 
 template <int MB, int NT, bool RING>
@@ -611,7 +681,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
         const bool room = all * 4 <= L.part_bytes;
         float* lg = room ? part : a.logits;
         if (warp < kWarps && room) {
-#pragma unroll 2
+#pragma unroll 4
             for (int i = threadIdx.x; i < all; i += kThreads) {
                 float v[kMoeRouterSplits];
 #pragma unroll
@@ -851,7 +921,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
 
     if (L.act16 < 0) {  // act has no room in shared memory: converted once, a third barrier
         if (warp < kWarps)
-            convert_act(a, M * nsel, a.act16, a.act16_elems, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
+            convert_act<true>(a, M * nsel, a.act16, a.act16_elems, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
         if (!grid_barrier(a, &s_pass)) {
             if (RING && warp == kWarps)
                 for (int q = sent - 1; q >= 0 && q >= sent - L.stages; --q)
@@ -871,12 +941,19 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
         return;
     }
     const int nu = I / 32, prow = M * nsel;
-    for (int i = threadIdx.x; i < slots * M; i += kThreads)
-        if (ridx[i] != kNone) coef[i] *= __int_as_float((127 - act_exponent(__ldcg(a.amax + ridx[i]))) << 23);
+    const bool quad = L.act16 < 0 && quads(I);
+    const int step = quad ? 4 : 1;
+    const int first_r = (int)threadIdx.x < slots * M ? ridx[threadIdx.x] : kNone;
+    const int first_max = first_r != kNone ? __ldcg(a.amax + first_r) : 0;  // (on its way while act is converted)
     const uint4* act16 = a.act16;
     if (L.act16 >= 0) {  // every CTA for itself
-        convert_act(a, prow, reinterpret_cast<uint4*>(sm + L.act16), (size_t)prow * nu * 4, threadIdx.x, kThreads);
+        convert_act<false>(a, prow, reinterpret_cast<uint4*>(sm + L.act16), (size_t)prow * nu * 4, threadIdx.x, kThreads);
         act16 = reinterpret_cast<const uint4*>(sm + L.act16);
+    }
+    for (int i = threadIdx.x; i < slots * M; i += kThreads) {
+        const int r = ridx[i];
+        if (r == kNone) continue;
+        coef[i] *= __int_as_float((127 - act_exponent(i == (int)threadIdx.x ? first_max : __ldcg(a.amax + r))) << 23);
     }
     named_bar_sync(1, kThreads);
     int first = 0;  // the warp that takes the next unit: the units of all stages go round
@@ -890,7 +967,8 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
                 if (RING) arrived(it);
                 int u = warp - first;
                 for (u += u < 0 ? kWarps : 0; u < n * L.sp; u += kWarps) {
-                    const int s = s0 + u / L.sp, ip = u % L.sp, u0 = ip * nu / L.sp, u1 = (ip + 1) * nu / L.sp;
+                    const int s = s0 + u / L.sp, ip = u % L.sp, u0 = ip * (nu / step) / L.sp * step;
+                    const int u1 = ip + 1 < L.sp ? (ip + 1) * (nu / step) / L.sp * step : nu;
                     float* pp = part + (q * L.sp + ip) * prow * 16;
                     const uint8_t *codes, *meta;
                     bool in = true;
@@ -905,7 +983,9 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
                              QMLP_INB((row + 16) * (I / 32) * MB - 1, a.w2_meta_bytes, 104);
                     }
                     if (!in) continue;
-                    if (L.act16 >= 0)
+                    if (quad)
+                        w2_quads<MB, NT>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, lane);
+                    else if (L.act16 >= 0)
                         w2_unit<MB, NT, true>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, lane);
                     else
                         w2_unit<MB, NT, false>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, lane);
