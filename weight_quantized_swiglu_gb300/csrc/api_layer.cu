@@ -36,9 +36,6 @@ struct qmlp_linear_s {
     Owner mem;
 };
 
-// Fewest tokens that the GEMM takes (see qmlp_linear_forward).
-constexpr int kLinearGemmM = 256;
-static_assert(kLinearGemmM >= kPairMinM, "the GEMM on CTA pairs");
 constexpr size_t kLinearImages = (size_t)1 << 30;  // bytes of images that a handle holds at most
 
 struct qmlp_moe_layer_s {
@@ -358,7 +355,7 @@ qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt,
     a.xf_elems = h->xf_bytes / 16;
     a.sig = h->sig;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (M < kLinearGemmM || !h->img) return from_cuda(launch_linear(h->group, a, h->num_sms, s));
+    if (M < kLinearGemmM) return from_cuda(launch_linear(h->group, a, h->num_sms, s));
     // many tokens: the weights decoded once into stage images, rows of W in slabs
     const int Kp = (h->K + 63) / 64 * 64;
     for (int n0 = 0; n0 < h->N; n0 += h->slab) {

@@ -1866,7 +1866,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     // 256-token tiles on CTA pairs (every weight row decoded once per 256
     // tokens), when asked for
     if (L.pair) {
-        if (L.M < kPairMinM) return cudaErrorInvalidValue;
+        if (L.M < (L.epi == kEpiOut ? kLinearGemmM : kPairMinM)) return cudaErrorInvalidValue;
         const int pairs = std::min(((L.M + 2 * BM - 1) / (2 * BM)) * (P.N / BN), std::max(num_sms, 2) / 2);
         if (!dq)
             return P.fmt == kFP8 ? launch_pair<kFP8, false>(map, map, map, map, a, pairs, std::max(num_sms, 2) / 2, s)

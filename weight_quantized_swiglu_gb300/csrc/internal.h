@@ -236,6 +236,11 @@ struct GemmLaunch {
     bool unscaled = false;      // a16 is fp16 as it came: no exponents
 };
 constexpr int kPairMinM = 256;  // one 256-token tile of a CTA pair
+// Fewest tokens of one projection that the GEMM takes, a 256-token tile of them in part:
+// its time hardly depends on their number (17408 x 5120 81 us from 65 to 255 tokens; launches
+// of 64 tokens each 80 us at 128, 120 at 192; 5120 x 5120 36 to 73 us, 1024 x 5120 22 to 58
+// at 130), one launch of up to 64 takes half of it.
+constexpr int kLinearGemmM = 65;
 cudaError_t launch_gemm_prescale(const void* a, int M, int K, void* a16, int* sig, int num_sms, cudaStream_t s);
 cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s);
 size_t gemm_splitk_ws_elems(int num_sms);
@@ -410,7 +415,7 @@ struct LinearArgs {
     int* sig = nullptr;           // [max_M] exponents of the tokens
 };
 constexpr int kLinearFew = 8;   // tokens whose x stays in shared memory
-constexpr int kLinearMid = 64;  // tokens of a launch above
+constexpr int kLinearMid = 64;  // tokens of linear_mid_kernel; more are the GEMM's
 size_t linear_x_bytes(int K, int M);
 cudaError_t launch_linear(int group, const LinearArgs& a, int num_sms, cudaStream_t s);
 // Stage images of the tensor-core GEMM (fp16, rows times 2^-exponent of their factor)

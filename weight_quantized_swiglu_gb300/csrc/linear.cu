@@ -4,7 +4,7 @@
 //   INT4:  W = (code - zero[n, k / G]) scale[n, k / G], G = 32, 64 or 128, c = 1
 // for a few tokens (here) or many (images for the tensor-core GEMM, below).
 //
-// Few tokens (at most 64 a launch): the weights are read once.
+// Few tokens (at most 64): the weights are read once.
 //  * Weights are laid out once, in records of 16 rows x 128 k (kRec bytes: codes
 //    in the order in which the lanes of an mma.sync m16n8k16 take them as the A
 //    operand, then the groups' scales). k is summed in any order that both
@@ -1043,24 +1043,12 @@ cudaError_t launch_mid(const LinearArgs& a, int num_sms, cudaStream_t s) {
 }
 
 template <int G>
-cudaError_t launch_g(LinearArgs a, int num_sms, cudaStream_t s) {
+cudaError_t launch_g(const LinearArgs& a, int num_sms, cudaStream_t s) {
     if (a.M == 1) return launch_few<G, true>(a, num_sms, s);
     if (a.M <= kLinearFew) return launch_few<G, false>(a, num_sms, s);
-    // 64 tokens a launch, or as evenly as that many launches allow
-    const size_t ob = a.odt == 0 ? 4 : 2;
-    const int M = a.M, blocks = (M + kLinearMid - 1) / kLinearMid, step = ((M + blocks - 1) / blocks + 7) / 8 * 8;
-    for (int m = 0; m < M; m += step) {
-        LinearArgs b = a;
-        b.M = std::min(step, M - m);
-        b.x = static_cast<const uint8_t*>(a.x) + (size_t)m * a.K * 2;
-        b.out = static_cast<uint8_t*>(a.out) + (size_t)m * a.N * ob;
-        const cudaError_t e = b.M <= 8    ? launch_mid<G, 1>(b, num_sms, s)
-                              : b.M <= 16 ? launch_mid<G, 2>(b, num_sms, s)
-                              : b.M <= 32 ? launch_mid<G, 4>(b, num_sms, s)
-                                          : launch_mid<G, 8>(b, num_sms, s);
-        if (e != cudaSuccess) return e;
-    }
-    return cudaSuccess;
+    if (a.M > kLinearMid) return cudaErrorInvalidValue;  // (the GEMM's)
+    if (a.M <= 16) return launch_mid<G, 2>(a, num_sms, s);
+    return a.M <= 32 ? launch_mid<G, 4>(a, num_sms, s) : launch_mid<G, 8>(a, num_sms, s);
 }
 
 }  // namespace
