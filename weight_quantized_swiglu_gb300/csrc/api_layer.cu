@@ -256,7 +256,8 @@ qmlp_status qmlp_linear_create(qmlp_linear_t** out, const qmlp_linear_desc* d, q
         if (!d || !d->w || !d->scale || (d->fmt != QMLP_LINEAR_NVFP4 && d->fmt != QMLP_LINEAR_INT4))
             return QMLP_ERR_INVALID_ARG;
         const bool nv = d->fmt == QMLP_LINEAR_NVFP4;
-        if ((d->zero != nullptr) == nv || (nv ? d->group != 16 : d->group != 32 && d->group != 64 && d->group != 128))
+        if ((d->zero != nullptr) == nv || (nv ? d->group != 16 : d->group != 32 && d->group != 64 && d->group != 128) ||
+            (nv && (d->global_scale == 0.0f || !isfinite(d->global_scale))))
             return QMLP_ERR_INVALID_ARG;
         if (d->N < 1 || d->N > (1 << 20) || d->K < 16 || d->K > 65536 || d->K % d->group || d->max_M < 1 ||
             d->max_M > 65536)
