@@ -684,7 +684,8 @@ void qmlp_linear_destroy(qmlp_linear_t* h);
  * Up to 64 tokens every product is exact. From 65 on the weights are decoded once a
  * call into images of the tensor-core GEMM (at most 1 GiB held by a handle made for
  * 65 tokens or more, in turn for larger projections), in which an INT4 weight is
- * rounded once to fp16; NVFP4's are exact in it.
+ * rounded once to fp16; NVFP4's are exact in it. Into an fp32 out what that rounding
+ * leaves is added by a second product.
  * Errors: INVALID_ARG, ALIGNMENT (16 bytes), ALIAS, SHAPE (M < 1 or over max_M),
  * CUDA. */
 qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt, int M, void* out, qmlp_dtype odt,
@@ -705,7 +706,7 @@ qmlp_status qmlp_linear_check(qmlp_linear_t* h, qmlp_stream_t stream);
  * (a shared expert of n times the width is n shared experts of the handle's I).
  * Up to 16 tokens whose x fits in shared memory (2 K bytes a token) run as one
  * kernel: sums are fp32, the intermediate is rounded once to fp16 times a power of
- * two of the token and expert, out once; a token's result does not depend on the
+ * two of the token and expert (to two fp16 for an fp32 out), out once; a token's result does not depend on the
  * others of the call. More tokens run the router, the selection
  * and the kernels of qmlp_moe_forward, with its roundings of the stages to fp16.
  */

@@ -110,7 +110,8 @@ MANY = [  # format, group, N, K, tokens, x, out, bias
 
 @pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(map(str, c)))
 def test_many_tokens(torch, case):
-    """From 65 tokens on an INT4 weight is rounded to fp16: 2^-11 of its size."""
+    """From 65 tokens on an INT4 weight is rounded to fp16, 2^-11 of its size; with an fp32
+    out nothing of it is left out."""
     fmt, G, N, K, tokens, xt, ot, has_bias = case
     T = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
     a, v = weights(fmt, N, K, G, N + K)
@@ -126,7 +127,7 @@ def test_many_tokens(torch, case):
         lin.forward(x, again)
         lin.check()
         assert torch.equal(out.view(torch.uint8), again.view(torch.uint8))
-        check(torch, x, v, out, factor, bias, 2.0 ** -11 if M >= 65 and fmt == "int4" else 0.0)
+        check(torch, x, v, out, factor, bias, 2.0 ** -11 if M >= 65 and fmt == "int4" and ot != "fp32" else 0.0)
     lin.close()
 
 
@@ -145,7 +146,7 @@ def test_weights_in_several_slabs(torch):
     rows = [*range(0, 40), *range(65500, 65600), *range(69960, 70001)]
     c = torch.stack((w[rows] & 15, w[rows] >> 4), -1).flatten(1).double()
     v = (c - z[rows].double().repeat_interleave(128, 1)) * s[rows].double().repeat_interleave(128, 1)
-    check(torch, x, v.cpu().numpy(), out[:, rows].contiguous(), more=2.0 ** -11)
+    check(torch, x, v.cpu().numpy(), out[:, rows].contiguous())
     lin.close()
 
 

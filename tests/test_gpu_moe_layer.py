@@ -7,8 +7,8 @@ output for that selection. Bounds, from the arithmetic (u = 2^-24):
   a renormed one by four times, with 32 u for exp, the quotients and the sums.
 * g and u: K u of their terms' sizes, and for bf16 tokens 2^-38 of the largest |x|
   (what the scaling to fp16 leaves); act: 1.1 |u| dg + |SiLU(g)| du + 16 u |act|
-  (SiLU's slope is at most 1.1), then fp16's half step, 2^-11, and 2^-38 of the
-  largest |act| of the token and expert below fp16's normal numbers.
+  (SiLU's slope is at most 1.1), then fp16's half step, 2^-11 (two of them with an fp32
+  out, 2^-22), and 2^-38 of the   largest |act| of the token and expert below fp16's normal numbers.
 * the sum over I and the experts: (I + 64) u of its terms' sizes.
 With more than 16 tokens, or where x does not fit in shared memory, g, u, act and
 each expert's y are rounded to fp16 (2^-11 of their size, at least 2^-25)."""
@@ -107,7 +107,8 @@ def verify(bank, x, router, sgate, bias, cfg, ids, weights, out, half, bf16, few
             silu = g * sigmoid(g)
             act = silu * u
             ea = 1.1 * eg * (np.abs(u) + eu) + np.abs(silu) * eu + 16 * U * np.abs(act)
-            ea = ea + h16 * (np.abs(act) + ea) + (2.0 ** -38 * np.abs(act).max() if few else 2.0 ** -25)
+            ha = 2.0 ** -22 if few and half < 2.0 ** -20 else h16
+            ea = ea + ha * (np.abs(act) + ea) + (2.0 ** -38 * np.abs(act).max() if few else 2.0 ** -25)
             y, ey = w2 @ act, np.abs(w2) @ (ea + (I + 64) * U * np.abs(act))
             if not few:
                 ey = ey + h16 * (np.abs(y) + ey) + 2.0 ** -25

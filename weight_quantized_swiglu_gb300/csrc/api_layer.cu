@@ -361,7 +361,7 @@ qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt,
     const int Kp = (h->K + 63) / 64 * 64;
     for (int n0 = 0; n0 < h->N; n0 += h->slab) {
         const int rows = std::min(h->slab, (h->N - n0 + 255) / 256 * 256), cols = std::min(h->slab, h->N - n0);
-        cudaError_t e = launch_linear_images(h->group, h->w, h->w_bytes, h->factors, h->N, h->K, n0, rows, h->img,
+        cudaError_t e = launch_linear_images(h->group, h->w, h->w_bytes, h->factors, h->N, h->K, n0, rows, false, h->img,
                                              h->img_bytes, s);
         if (e != cudaSuccess) return from_cuda(e);
         GemmLaunch g;
@@ -391,6 +391,14 @@ qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt,
         g.f16 = true;
         g.split_tail = true;
         g.images_ready = true;
+        if ((e = launch_gemm(g, h->num_sms, s)) != cudaSuccess) return from_cuda(e);
+        if (h->group == 16 || a.odt != 0) continue;
+        // INT4 into fp32: what the images' rounding to fp16 left, a second product on top
+        e = launch_linear_images(h->group, h->w, h->w_bytes, h->factors, h->N, h->K, n0, rows, true, h->img, h->img_bytes, s);
+        if (e != cudaSuccess) return from_cuda(e);
+        g.bias = nullptr;
+        g.prescaled = true;
+        g.onto = true;
         if ((e = launch_gemm(g, h->num_sms, s)) != cudaSuccess) return from_cuda(e);
     }
     return QMLP_OK;
@@ -477,7 +485,7 @@ qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const
         a.weights = static_cast<float*>(make(rows * nsel * 4, nullptr));
         a.act = static_cast<float*>(make(a.act_elems * 4, nullptr));
         a.amax = static_cast<int*>(make(few * 4, nullptr));
-        a.act16_elems = a.act_elems / 8;
+        a.act16_elems = a.act_elems / 8 * 2;  // (twice: what rounding to fp16 leaves)
         a.act16 = static_cast<uint4*>(make(a.act16_elems * 16, nullptr));
         uint8_t* words = static_cast<uint8_t*>(make(16, nullptr));
         if (e == cudaSuccess) e = cudaMemsetAsync(words, 0, 16, s);

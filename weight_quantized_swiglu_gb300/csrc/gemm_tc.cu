@@ -178,6 +178,7 @@ struct Args {
     void* out_lo;          // SwiGLU, SwiGLUGrad: optional, bf16 of what out's rounding leaves
     int odt;               // kEpiOut: type of out (0 fp32, 1 bf16, 2 fp16); ncols: its columns
     const float* bias;     // kEpiOut: optional, [ncols]
+    int onto;              // kEpiOut, fp32: added to what out holds
 };
 
 // Quad (columns col..col+3) of row m in the gate / up values kept for the
@@ -274,11 +275,18 @@ QMLP_DEV void store_any(const Args& a, int m, int col, const float (&v)[N]) {
         float* o = static_cast<float*>(a.out) + at;
         if (col + N <= a.ncols && (a.ldo & 3) == 0) {
 #pragma unroll
-            for (int j = 0; j < N; j += 4) *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            for (int j = 0; j < N; j += 4) {
+                float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                if (a.onto) {
+                    const float4 h = *reinterpret_cast<const float4*>(o + j);
+                    w.x += h.x, w.y += h.y, w.z += h.z, w.w += h.w;
+                }
+                *reinterpret_cast<float4*>(o + j) = w;
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (col + j < a.ncols) o[j] = v[j];
+                if (col + j < a.ncols) o[j] = a.onto ? o[j] + v[j] : v[j];
         }
         return;
     }
@@ -1805,6 +1813,7 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
     a.sig = bf || L.unscaled ? nullptr : L.sig;
     a.odt = L.odt;
     a.bias = L.bias;
+    a.onto = L.onto ? 1 : 0;
     if (L.epi == kEpiOut && (!L.pair || !dq || !L.f16 || !L.images_ready || P.fmt != kFP8)) return cudaErrorInvalidValue;
     a.f16 = L.f16 ? 1 : 0;
     a.tail = L.split_tail ? 1 : 0;  // launch_pair plans it

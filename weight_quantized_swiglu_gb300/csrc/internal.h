@@ -234,6 +234,7 @@ struct GemmLaunch {
     const float* bias = nullptr;
     int ka = 0;                 // row length of a (0: w.K): k past it is zero
     bool unscaled = false;      // a16 is fp16 as it came: no exponents
+    bool onto = false;          // kEpiOut, fp32: added to what out holds
 };
 constexpr int kPairMinM = 256;  // one 256-token tile of a CTA pair
 // Fewest tokens of one projection that the GEMM takes, a 256-token tile of them in part:
@@ -421,9 +422,9 @@ cudaError_t launch_linear(int group, const LinearArgs& a, int num_sms, cudaStrea
 // Stage images of the tensor-core GEMM (fp16, rows times 2^-exponent of their factor)
 // of rows n0.. (a multiple of 256) of the records: N rows padded to 256, K to 64. The
 // factors of all rows: c, for INT4 times a power of two that keeps a row's images in
-// fp16's range.
+// fp16's range. rest: of INT4 what the images' rounding to fp16 leaves.
 cudaError_t launch_linear_images(int group, const uint8_t* w, size_t w_bytes, const float* factors, int N, int K, int n0,
-                                 int rows, uint8_t* img, size_t img_bytes, cudaStream_t s);
+                                 int rows, bool rest, uint8_t* img, size_t img_bytes, cudaStream_t s);
 cudaError_t launch_linear_factors(int group, const void* scale, int N, int K, float c, float* factors, int padded,
                                   cudaStream_t s);
 

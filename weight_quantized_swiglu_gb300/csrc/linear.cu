@@ -855,7 +855,7 @@ __global__ void __launch_bounds__(256) repack_linear_kernel(const uint8_t* __res
 template <int G>
 __global__ void __launch_bounds__(256) linear_images_kernel(const uint8_t* __restrict__ w, size_t w_bytes,
                                                             const float* __restrict__ factors, int Nt, int Kc, int KS,
-                                                            int tile0, long recs, uint8_t* __restrict__ img,
+                                                            int tile0, long recs, bool rest, uint8_t* __restrict__ img,
                                                             size_t img_bytes) {
     using R = Rec<G>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -904,8 +904,13 @@ __global__ void __launch_bounds__(256) linear_images_kernel(const uint8_t* __res
                             rf * __half2float(__ushort_as_half((unsigned short)(s[h][q >> 1] >> (16 * (q & 1)))));
 #pragma unroll
                         for (int p = 0; p < 4; ++p) {
-                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&a[p]));
-                            const __half2 o = __floats2half2_rn(v.x * sc, v.y * sc);
+                            float2 v = __half22float2(*reinterpret_cast<const __half2*>(&a[p]));
+                            v.x *= sc, v.y *= sc;  // exact: 8 bits times 11
+                            __half2 o = __floats2half2_rn(v.x, v.y);
+                            if (rest) {  // what that leaves, exact as well (nothing of what is not finite)
+                                const float2 r = __half22float2(o);
+                                o = __floats2half2_rn(isfinite(r.x) ? v.x - r.x : 0.0f, isfinite(r.y) ? v.y - r.y : 0.0f);
+                            }
                             a[p] = *reinterpret_cast<const uint32_t*>(&o);
                         }
                     }
@@ -1076,15 +1081,15 @@ cudaError_t repack_linear(int group, const uint8_t* w, const void* scale, const 
 }
 
 cudaError_t launch_linear_images(int group, const uint8_t* w, size_t w_bytes, const float* factors, int N, int K, int n0,
-                                 int rows, uint8_t* img, size_t img_bytes, cudaStream_t s) {
+                                 int rows, bool rest, uint8_t* img, size_t img_bytes, cudaStream_t s) {
     const int Kc = (K + kCh - 1) / kCh, KS = (K + 63) / 64, Nt = (N + 15) / 16;
     const long recs = (long)(rows / 16) * Kc;
     const unsigned grid = (unsigned)std::min<long>((recs + 7) / 8, 1 << 20);
     switch (group) {
-        case 16: linear_images_kernel<16><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, img, img_bytes); break;
-        case 32: linear_images_kernel<32><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, img, img_bytes); break;
-        case 64: linear_images_kernel<64><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, img, img_bytes); break;
-        case 128: linear_images_kernel<128><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, img, img_bytes); break;
+        case 16: linear_images_kernel<16><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, rest, img, img_bytes); break;
+        case 32: linear_images_kernel<32><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, rest, img, img_bytes); break;
+        case 64: linear_images_kernel<64><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, rest, img, img_bytes); break;
+        case 128: linear_images_kernel<128><<<grid, 256, 0, s>>>(w, w_bytes, factors, Nt, Kc, KS, n0 / 16, recs, rest, img, img_bytes); break;
         default: return cudaErrorInvalidValue;
     }
     return cudaPeekAtLastError();

@@ -28,7 +28,8 @@
 //     fp32, a row a (token, choice).
 //  3. A warp a (16 output rows, expert): act as fp16 times a power of two of the
 //     (token, expert) (its largest value, known now, goes to [2^14, 2^15): off by
-//     2^-11 of a value at most, the only rounding between x and out), W2 times it;
+//     2^-11 of a value at most, the only rounding between x and out; with an fp32 out
+//     what that leaves is taken as well, another fp16), W2 times it;
 //     a token's choices are added in their order, fp32. So a token's result does
 //     not depend on the other tokens of the call.
 // The weights of parts 2 and 3 come through a ring in shared memory that a producer
@@ -82,7 +83,7 @@ struct Layout {
     int n2, sp;         // W2: experts of a stage, parts of I that different warps take
     int bytes;
 };
-__host__ __device__ inline Layout layout(int M, int K, int I, int E, int nsel, int slots, int MB, int NT) {
+__host__ __device__ inline Layout layout(int M, int K, int I, int E, int nsel, int slots, int MB, int NT, bool lo) {
     Layout l;
     auto up = [](int b) { return (b + 127) / 128 * 128; };
     int at = 0;
@@ -95,8 +96,9 @@ __host__ __device__ inline Layout layout(int M, int K, int I, int E, int nsel, i
     l.sel_w = at, at += 16 * 16 * 4;
     l.cand = at, at += up(M * (int)sizeof(Pick));  // (what follows is read 8 and copied 16 bytes at a time)
     l.part = at, l.part_bytes = 2 * kWarps * 16 * 8 * NT * 4, at += l.part_bytes;
-    l.act16 = -1;  // fp16 act of the routes, where it is small (else in device memory)
-    if (M * nsel * I * 2 <= 32 * 1024) l.act16 = at, at += up(M * nsel * I * 2);
+    l.act16 = -1;  // fp16 act of the routes (lo: and what it leaves), where it is small (else in device memory)
+    const int act = M * nsel * I * (lo ? 4 : 2);
+    if (act <= 32 * 1024) l.act16 = at, at += up(act);
     l.ring = at;
     const int item13 = (int)(kMoeKSplit * (moe_w13_block_bytes(K) + moe_w13_meta_block_bytes(K, MB)));
     const int item2 = 16 * (I / 2) + 16 * (I / 32) * MB;
@@ -405,9 +407,10 @@ QMLP_DEV void word_weights(uint32_t w, uint32_t s2, uint32_t b2, uint32_t (&f)[4
 }
 // One unit of 32 k of sixteen rows (words and records of rows g and g + 8) times NT
 // tiles of tokens.
-template <int NT>
+// LO: xl, what x's rounding left, as well.
+template <int NT, bool LO = false>
 QMLP_DEV void words_mma(uint32_t w0, uint32_t w8, uint32_t s0, uint32_t b0, uint32_t s8, uint32_t b8, const uint4 (&x)[NT],
-                        float (&d)[NT][4]) {
+                        const uint4 (&xl)[NT], float (&d)[NT][4]) {
     uint32_t f0[4], f8[4];
     word_weights(w0, s0, b0, f0);
     word_weights(w8, s8, b8, f8);
@@ -415,14 +418,19 @@ QMLP_DEV void words_mma(uint32_t w0, uint32_t w8, uint32_t s0, uint32_t b0, uint
     for (int n = 0; n < NT; ++n) {
         mma_f16_16816(d[n], f0[0], f8[0], f0[1], f8[1], x[n].x, x[n].y);
         mma_f16_16816(d[n], f0[2], f8[2], f0[3], f8[3], x[n].z, x[n].w);
+        if (LO) {
+            mma_f16_16816(d[n], f0[0], f8[0], f0[1], f8[1], xl[n].x, xl[n].y);
+            mma_f16_16816(d[n], f0[2], f8[2], f0[3], f8[3], xl[n].z, xl[n].w);
+        }
     }
 }
-template <int MB, int NT>
-QMLP_DEV void unit_mma(uint32_t w0, uint32_t w8, uint32_t m0, uint32_t m8, const uint4 (&x)[NT], float (&d)[NT][4]) {
+template <int MB, int NT, bool LO = false>
+QMLP_DEV void unit_mma(uint32_t w0, uint32_t w8, uint32_t m0, uint32_t m8, const uint4 (&x)[NT], const uint4 (&xl)[NT],
+                       float (&d)[NT][4]) {
     uint32_t s0, b0, s8, b8;
     meta2<MB>(m0, s0, b0);
     meta2<MB>(m8, s8, b8);
-    words_mma<NT>(w0, w8, s0, b0, s8, b8, x, d);
+    words_mma<NT, LO>(w0, w8, s0, b0, s8, b8, x, xl, d);
 }
 template <int MB>
 QMLP_DEV uint32_t record(const uint8_t* p) {
@@ -481,7 +489,7 @@ QMLP_DEV int act_exponent(int bits) { return max(-113, min(126, prescale_exponen
 // act (fp32, rows of I) -> fp16 times the row's power of two, in the order of the
 // MMAs: piece (r I / 32 + unit) 4 + t, to `out` (shared or device memory), by threads
 // i0, i0 + hop, ...
-template <bool QUAD>
+template <bool QUAD, bool LO>
 QMLP_DEV void convert_act(const MoeLayerArgs& a, int rows, uint4* out, size_t out_elems, int i0, int hop) {
     const bool quad = QUAD && quads(a.I);
     const int nu = a.I / 32;
@@ -489,16 +497,26 @@ QMLP_DEV void convert_act(const MoeLayerArgs& a, int rows, uint4* out, size_t ou
     for (int i = i0; i < rows * nu * 4; i += hop) {
         const int t = i & 3, r = (i >> 2) / nu, u = (i >> 2) % nu;
         const float* p = a.act + (size_t)(i >> 2) * 32 + 2 * t;
-        if (!QMLP_INB((size_t)(i >> 2) * 32 + 31, a.act_elems, 107) || !QMLP_INB(i, out_elems, 109)) continue;
+        if (!QMLP_INB((size_t)(i >> 2) * 32 + 31, a.act_elems, 107) || !QMLP_INB((LO ? rows * nu * 4 : 0) + i, out_elems, 109)) continue;
         float2 v[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[j] = __ldcg(reinterpret_cast<const float2*>(p + 8 * j));
         const float up = __int_as_float((127 + act_exponent(__ldcg(a.amax + r))) << 23);
-        uint32_t h[4];
+        uint32_t h[4], l[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = u32(__floats2half2_rn(v[j].x * up, v[j].y * up));
+        for (int j = 0; j < 4; ++j) {
+            const float2 w = make_float2(v[j].x * up, v[j].y * up);
+            const __half2 q = __floats2half2_rn(w.x, w.y);
+            h[j] = u32(q);
+            if (LO) {  // (nothing of what is not finite)
+                const float2 f = __half22float2(q);
+                l[j] = u32(__floats2half2_rn(isfinite(f.x) ? w.x - f.x : 0.0f, isfinite(f.y) ? w.y - f.y : 0.0f));
+            }
+        }
         // (of four units: lane t's pieces are unit t's, see w2_quads)
-        out[quad ? i + 3 * (t - (u & 3)) : i] = unit_order(h[0], h[1], h[2], h[3]);
+        const int at = quad ? i + 3 * (t - (u & 3)) : i;
+        out[at] = unit_order(h[0], h[1], h[2], h[3]);
+        if (LO) out[rows * nu * 4 + at] = unit_order(l[0], l[1], l[2], l[3]);
     }
 }
 
@@ -521,9 +539,9 @@ QMLP_DEV void unit_out(const float (&d)[NT][4], int M, int t, int g, const uint1
 // Part 3's share of one expert: sixteen rows (codes, meta) times the tokens' act (fp16,
 // converted; SH: in shared memory) over units u0..u1 of 32 k, times the weights, to
 // part (choice r of the call: r 16 + row).
-template <int MB, int NT, bool SH>
+template <int MB, int NT, bool SH, bool LO>
 QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t* meta, const uint4* act16, int u0, int u1,
-                      const uint16_t* ridx, const float* coef, float* part, int lane) {
+                      const uint16_t* ridx, const float* coef, float* part, size_t lo, int lane) {
     const int M = a.M, I = a.I, nu = I / 32, g = lane >> 2, t = lane & 3;
     float d[NT][4];
     const uint4* row[NT];
@@ -540,11 +558,14 @@ QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t
     const uint8_t *m0 = meta + g * nu * MB, *m8 = m0 + 8 * nu * MB;
 #pragma unroll 4
     for (int u = u0; u < u1; ++u) {
-        uint4 x[NT];
+        uint4 x[NT], xl[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if (SH) x[n] = on[n] ? row[n][u * 4] : make_uint4(0, 0, 0, 0);
             else x[n] = ldcg4_if(row[n] + u * 4, on[n]);
+            if (!LO) continue;
+            if (SH) xl[n] = on[n] ? row[n][lo + u * 4] : make_uint4(0, 0, 0, 0);
+            else xl[n] = ldcg4_if(row[n] + lo + u * 4, on[n]);
         }
         uint32_t r0, r8;
         if (MB == 4) {
@@ -554,8 +575,8 @@ QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t
             r0 = (uint32_t)m0[u * 3] | (uint32_t)m0[u * 3 + 1] << 8 | (uint32_t)m0[u * 3 + 2] << 16;
             r8 = (uint32_t)m8[u * 3] | (uint32_t)m8[u * 3 + 1] << 8 | (uint32_t)m8[u * 3 + 2] << 16;
         }
-        unit_mma<MB, NT>(*reinterpret_cast<const uint32_t*>(c0 + 16 * u), *reinterpret_cast<const uint32_t*>(c8 + 16 * u), r0,
-                         r8, x, d);
+        unit_mma<MB, NT, LO>(*reinterpret_cast<const uint32_t*>(c0 + 16 * u), *reinterpret_cast<const uint32_t*>(c8 + 16 * u), r0,
+                         r8, x, xl, d);
     }
     unit_out<NT>(d, M, t, g, ridx, coef, part);
 }
@@ -565,10 +586,10 @@ QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t
 // has four or eight rows on one bank where I is a multiple of 128: 4 tokens of 64 experts
 // of 4096 x 1024 103 us instead of 87; elsewhere it is ahead, I = 704 84 to 88 us.) act lies
 // in that order, and is asked for PF steps ahead.
-template <int MB, int NT>
+template <int MB, int NT, bool LO>
 QMLP_DEV void w2_quads(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t* meta, const uint4* act16, int u0, int u1,
-                       const uint16_t* ridx, const float* coef, float* part, int lane) {
-    constexpr int PF = NT == 1 ? 4 : 2;
+                       const uint16_t* ridx, const float* coef, float* part, size_t lo, int lane) {
+    constexpr int PF = 4 / (NT * (LO ? 2 : 1));
     const int M = a.M, I = a.I, nu = I / 32, g = lane >> 2, t = lane & 3;
     float d[NT][4];
     const uint4* row[NT];
@@ -583,11 +604,16 @@ QMLP_DEV void w2_quads(const MoeLayerArgs& a, const uint8_t* codes, const uint8_
     }
     const uint8_t *c0 = codes + g * (I / 2) + 16 * t, *c8 = c0 + 4 * I;
     const uint8_t *m0 = meta + (g * nu + t) * MB, *m8 = m0 + 8 * nu * MB;
-    uint4 x[PF][NT];
+    uint4 x[PF][NT], xl[PF][NT];
+    auto ask = [&](int u, uint4 (&v)[NT], uint4 (&vl)[NT]) {
 #pragma unroll
-    for (int j = 0; j < PF; ++j)
+        for (int n = 0; n < NT; ++n) {
+            v[n] = ldcg4_if(row[n] + u * 4, on[n] && u < u1);
+            if (LO) vl[n] = ldcg4_if(row[n] + lo + u * 4, on[n] && u < u1);
+        }
+    };
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[j][n] = ldcg4_if(row[n] + (u0 + j) * 4, on[n] && u0 < u1);
+    for (int j = 0; j < PF; ++j) ask(u0 + j, x[j], xl[j]);
 #pragma unroll 1
     for (int u = u0; u < u1; u += 4) {
         const uint4 p = *reinterpret_cast<const uint4*>(c0 + 16 * u), q = *reinterpret_cast<const uint4*>(c8 + 16 * u);
@@ -597,15 +623,14 @@ QMLP_DEV void w2_quads(const MoeLayerArgs& a, const uint8_t* codes, const uint8_
         meta2<MB>(record<MB>(m8 + u * MB), s8, b8);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            words_mma<NT>(w0[j], w8[j], s0, b0, s8, b8, x[j % PF], d);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) x[j % PF][n] = ldcg4_if(row[n] + (u + j + PF) * 4, on[n] && u + j + PF < u1);
+            words_mma<NT, LO>(w0[j], w8[j], s0, b0, s8, b8, x[j % PF], xl[j % PF], d);
+            ask(u + j + PF, x[j % PF], xl[j % PF]);
         }
     }
     unit_out<NT>(d, M, t, g, ridx, coef, part);
 }
 
-template <int MB, int NT, bool RING>
+template <int MB, int NT, bool RING, bool LO>
 __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLayerArgs a) {
     constexpr int kC = 8 * NT;
     extern __shared__ __align__(128) uint8_t sm[];
@@ -613,7 +638,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
     const int M = a.M, K = a.K, I = a.I, rows = a.E + (a.sgate ? a.S : 0), nsel = a.topk + a.S;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const Layout L = layout(M, K, I, a.E, nsel, a.slots, MB, NT);
+    const Layout L = layout(M, K, I, a.E, nsel, a.slots, MB, NT, LO);
     uint4* xsm = reinterpret_cast<uint4*>(sm + L.x);
     float* coef = reinterpret_cast<float*>(sm + L.coef);          // [slot][M]
     uint16_t* ridx = reinterpret_cast<uint16_t*>(sm + L.ridx);    // [slot][M]: row of act
@@ -875,7 +900,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             x[n] = xsm[(((c0 + 2 * pr) * 2 + h) * M + min(8 * n + g, M - 1)) * 4 + t];
-                        unit_mma<MB, NT>(wg[h], wu[h], rg[h], ru[h], x, d);
+                        unit_mma<MB, NT>(wg[h], wu[h], rg[h], ru[h], x, x, d);
                     }
                 }
             }
@@ -921,7 +946,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
 
     if (L.act16 < 0) {  // act has no room in shared memory: converted once, a third barrier
         if (warp < kWarps)
-            convert_act<true>(a, M * nsel, a.act16, a.act16_elems, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
+            convert_act<true, LO>(a, M * nsel, a.act16, a.act16_elems, blockIdx.x * kThreads + threadIdx.x, gridDim.x * kThreads);
         if (!grid_barrier(a, &s_pass)) {
             if (RING && warp == kWarps)
                 for (int q = sent - 1; q >= 0 && q >= sent - L.stages; --q)
@@ -947,7 +972,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
     const int first_max = first_r != kNone ? __ldcg(a.amax + first_r) : 0;  // (on its way while act is converted)
     const uint4* act16 = a.act16;
     if (L.act16 >= 0) {  // every CTA for itself
-        convert_act<false>(a, prow, reinterpret_cast<uint4*>(sm + L.act16), (size_t)prow * nu * 4, threadIdx.x, kThreads);
+        convert_act<false, LO>(a, prow, reinterpret_cast<uint4*>(sm + L.act16), (size_t)prow * nu * (LO ? 8 : 4), threadIdx.x, kThreads);
         act16 = reinterpret_cast<const uint4*>(sm + L.act16);
     }
     for (int i = threadIdx.x; i < slots * M; i += kThreads) {
@@ -984,11 +1009,11 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
                     }
                     if (!in) continue;
                     if (quad)
-                        w2_quads<MB, NT>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, lane);
+                        w2_quads<MB, NT, LO>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, (size_t)prow * nu * 4, lane);
                     else if (L.act16 >= 0)
-                        w2_unit<MB, NT, true>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, lane);
+                        w2_unit<MB, NT, true, LO>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, (size_t)prow * nu * 4, lane);
                     else
-                        w2_unit<MB, NT, false>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, lane);
+                        w2_unit<MB, NT, false, LO>(a, codes, meta, act16, u0, u1, ridx + s * M, coef + s * M, pp, (size_t)prow * nu * 4, lane);
                 }
                 first = (first + n * L.sp) % kWarps;
                 if (RING) {  // ten arrivals a stage: one for two warps
@@ -1097,10 +1122,10 @@ __global__ void __launch_bounds__(256) router_frag_kernel(const void* w, const v
     }
 }
 
-template <int MB, int NT, bool RING>
+template <int MB, int NT, bool RING, bool LO>
 cudaError_t launch_few(const MoeLayerArgs& a, int bytes, int num_sms, cudaStream_t s) {
     static unsigned long done = 0;
-    if (const cudaError_t e = smem_once(moe_layer_kernel<MB, NT, RING>, kSmemMax, done); e != cudaSuccess) return e;
+    if (const cudaError_t e = smem_once(moe_layer_kernel<MB, NT, RING, LO>, kSmemMax, done); e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)num_sms);
     cfg.blockDim = dim3(kThreads + 32);
@@ -1111,31 +1136,34 @@ cudaError_t launch_few(const MoeLayerArgs& a, int bytes, int num_sms, cudaStream
     at[0].val.cooperative = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, moe_layer_kernel<MB, NT, RING>, a);
+    return cudaLaunchKernelEx(&cfg, moe_layer_kernel<MB, NT, RING, LO>, a);
 }
 
-Layout layout_of(int M, int K, int I, int E, int S, int topk, int MB) {
-    return layout(M, K, I, E, topk + S, std::min(E, M * topk) + S, MB, M <= 8 ? 1 : 2);
+Layout layout_of(int M, int K, int I, int E, int S, int topk, int MB, bool lo) {
+    return layout(M, K, I, E, topk + S, std::min(E, M * topk) + S, MB, M <= 8 ? 1 : 2, lo);
+}
+template <int MB, bool LO>
+cudaError_t launch_few_of(const MoeLayerArgs& a, const Layout& l, int num_sms, cudaStream_t s) {
+    if (l.bytes > kSmemMax) return cudaErrorInvalidValue;
+    if (l.stage)
+        return a.M <= 8 ? launch_few<MB, 1, true, LO>(a, l.bytes, num_sms, s) : launch_few<MB, 2, true, LO>(a, l.bytes, num_sms, s);
+    return a.M <= 8 ? launch_few<MB, 1, false, LO>(a, l.bytes, num_sms, s) : launch_few<MB, 2, false, LO>(a, l.bytes, num_sms, s);
 }
 
 }  // namespace
 
 bool moe_layer_few(int M, int K, int I, int E, int S, int topk, int meta_bytes) {
-    return M <= kMoeLayerFew && layout_of(M, K, I, E, S, topk, meta_bytes).bytes <= kSmemMax;
+    return M <= kMoeLayerFew && layout_of(M, K, I, E, S, topk, meta_bytes, false).bytes <= kSmemMax &&
+           layout_of(M, K, I, E, S, topk, meta_bytes, true).bytes <= kSmemMax;
 }
 
 cudaError_t launch_moe_layer_few(MoeLayerArgs a, int meta_bytes, int num_sms, cudaStream_t s) {
     a.slots = std::min(a.E, a.M * a.topk) + a.S;
     a.limit = kWaitNs;
-    const Layout l = layout_of(a.M, a.K, a.I, a.E, a.S, a.topk, meta_bytes);
-    if (l.bytes > kSmemMax) return cudaErrorInvalidValue;
-    const int n = l.bytes;
-    if (l.stage) {
-        if (meta_bytes == 4) return a.M <= 8 ? launch_few<4, 1, true>(a, n, num_sms, s) : launch_few<4, 2, true>(a, n, num_sms, s);
-        return a.M <= 8 ? launch_few<3, 1, true>(a, n, num_sms, s) : launch_few<3, 2, true>(a, n, num_sms, s);
-    }
-    if (meta_bytes == 4) return a.M <= 8 ? launch_few<4, 1, false>(a, n, num_sms, s) : launch_few<4, 2, false>(a, n, num_sms, s);
-    return a.M <= 8 ? launch_few<3, 1, false>(a, n, num_sms, s) : launch_few<3, 2, false>(a, n, num_sms, s);
+    const bool lo = a.odt == 0;
+    const Layout l = layout_of(a.M, a.K, a.I, a.E, a.S, a.topk, meta_bytes, lo);
+    if (meta_bytes == 4) return lo ? launch_few_of<4, true>(a, l, num_sms, s) : launch_few_of<4, false>(a, l, num_sms, s);
+    return lo ? launch_few_of<3, true>(a, l, num_sms, s) : launch_few_of<3, false>(a, l, num_sms, s);
 }
 
 cudaError_t launch_moe_router(const MoeLayerArgs& a, cudaStream_t s) {
