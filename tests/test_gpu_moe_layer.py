@@ -8,7 +8,7 @@ output for that selection. Bounds, from the arithmetic (u = 2^-24):
 * g and u: K u of their terms' sizes, and for bf16 tokens 2^-38 of the largest |x|
   (what the scaling to fp16 leaves); act: 1.1 |u| dg + |SiLU(g)| du + 16 u |act|
   (SiLU's slope is at most 1.1), then fp16's half step, 2^-11 (two of them with an fp32
-  out, 2^-22), and 2^-38 of the   largest |act| of the token and expert below fp16's normal numbers.
+  out, 2^-22), and 2^-38 of the largest |act| of the token and expert below fp16's normal numbers.
 * the sum over I and the experts: (I + 64) u of its terms' sizes.
 With more than 16 tokens, or where x does not fit in shared memory, g, u, act and
 each expert's y are rounded to fp16 (2^-11 of their size, at least 2^-25)."""

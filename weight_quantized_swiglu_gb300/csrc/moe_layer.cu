@@ -520,6 +520,15 @@ QMLP_DEV void convert_act(const MoeLayerArgs& a, int rows, uint4* out, size_t ou
     }
 }
 
+// The MMAs' accumulators to sums of their own (LO): an MMA cuts off what passes its last
+// bit, always downward in size, and a chain of 128 of them was 1.4e-6 off, eight at a time 5e-7.
+template <int NT>
+QMLP_DEV void flush(float (&d)[NT][4], float (&sum)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[n][e] += d[n][e], d[n][e] = 0.0f;
+}
 // A unit's results, times the weights, to part.
 template <int NT>
 QMLP_DEV void unit_out(const float (&d)[NT][4], int M, int t, int g, const uint16_t* ridx, const float* coef, float* part) {
@@ -543,7 +552,7 @@ template <int MB, int NT, bool SH, bool LO>
 QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t* meta, const uint4* act16, int u0, int u1,
                       const uint16_t* ridx, const float* coef, float* part, size_t lo, int lane) {
     const int M = a.M, I = a.I, nu = I / 32, g = lane >> 2, t = lane & 3;
-    float d[NT][4];
+    float d[NT][4], sum[NT][4];
     const uint4* row[NT];
     bool on[NT];
 #pragma unroll
@@ -552,7 +561,7 @@ QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t
         on[n] = r != kNone;
         row[n] = act16 + (size_t)(on[n] ? r : 0) * nu * 4 + t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) d[n][e] = sum[n][e] = 0.0f;
     }
     const uint8_t *c0 = codes + g * (I / 2) + 4 * t, *c8 = c0 + 4 * I;
     const uint8_t *m0 = meta + g * nu * MB, *m8 = m0 + 8 * nu * MB;
@@ -577,8 +586,10 @@ QMLP_DEV void w2_unit(const MoeLayerArgs& a, const uint8_t* codes, const uint8_t
         }
         unit_mma<MB, NT, LO>(*reinterpret_cast<const uint32_t*>(c0 + 16 * u), *reinterpret_cast<const uint32_t*>(c8 + 16 * u), r0,
                          r8, x, xl, d);
+        if (LO && (u & 1)) flush<NT>(d, sum);
     }
-    unit_out<NT>(d, M, t, g, ridx, coef, part);
+    if (LO) flush<NT>(d, sum);
+    unit_out<NT>(LO ? sum : d, M, t, g, ridx, coef, part);
 }
 
 // The same with act in device memory, four units at a time: lane t takes unit u + t whole, a
@@ -591,7 +602,7 @@ QMLP_DEV void w2_quads(const MoeLayerArgs& a, const uint8_t* codes, const uint8_
                        const uint16_t* ridx, const float* coef, float* part, size_t lo, int lane) {
     constexpr int PF = 4 / (NT * (LO ? 2 : 1));
     const int M = a.M, I = a.I, nu = I / 32, g = lane >> 2, t = lane & 3;
-    float d[NT][4];
+    float d[NT][4], sum[NT][4];
     const uint4* row[NT];
     bool on[NT];
 #pragma unroll
@@ -600,7 +611,7 @@ QMLP_DEV void w2_quads(const MoeLayerArgs& a, const uint8_t* codes, const uint8_
         on[n] = r != kNone;
         row[n] = act16 + (size_t)(on[n] ? r : 0) * nu * 4 + t;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) d[n][e] = sum[n][e] = 0.0f;
     }
     const uint8_t *c0 = codes + g * (I / 2) + 16 * t, *c8 = c0 + 4 * I;
     const uint8_t *m0 = meta + (g * nu + t) * MB, *m8 = m0 + 8 * nu * MB;
@@ -625,9 +636,10 @@ QMLP_DEV void w2_quads(const MoeLayerArgs& a, const uint8_t* codes, const uint8_
         for (int j = 0; j < 4; ++j) {
             words_mma<NT, LO>(w0[j], w8[j], s0, b0, s8, b8, x[j % PF], xl[j % PF], d);
             ask(u + j + PF, x[j % PF], xl[j % PF]);
+            if (LO && (j & 1)) flush<NT>(d, sum);
         }
     }
-    unit_out<NT>(d, M, t, g, ridx, coef, part);
+    unit_out<NT>(LO ? sum : d, M, t, g, ridx, coef, part);
 }
 
 template <int MB, int NT, bool RING, bool LO>
@@ -869,11 +881,11 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
                 meta = a.w13_meta + blk * mb;
                 in = QMLP_INB((blk + 1) * cb - 1, a.w13_bytes, 101) && QMLP_INB((blk + 1) * mb - 1, a.w13_meta_bytes, 102);
             }
-            float d[NT][4];
+            float d[NT][4], sum[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) d[n][e] = sum[n][e] = 0.0f;
             // pairs of 64-k chunks: four units of the gate row g and of the up row g
             const uint4* cp = reinterpret_cast<const uint4*>(codes) + lane;
             const uint8_t* mp = meta + g * ms;
@@ -903,16 +915,18 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
                         unit_mma<MB, NT>(wg[h], wu[h], rg[h], ru[h], x, x, d);
                     }
                 }
+                if (LO) flush<NT>(d, sum);
             }
             if (RING) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty(it % L.stages));
             }
+            float (&v)[NT][4] = LO ? sum : d;
             float* pt = part + ((turn * kTeams + team) * kMoeKSplit) * 16 * kC;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                *reinterpret_cast<float2*>(pt + (ks * 16 + g) * kC + 8 * n + 2 * t) = make_float2(d[n][0], d[n][1]);
-                *reinterpret_cast<float2*>(pt + (ks * 16 + g + 8) * kC + 8 * n + 2 * t) = make_float2(d[n][2], d[n][3]);
+                *reinterpret_cast<float2*>(pt + (ks * 16 + g) * kC + 8 * n + 2 * t) = make_float2(v[n][0], v[n][1]);
+                *reinterpret_cast<float2*>(pt + (ks * 16 + g + 8) * kC + 8 * n + 2 * t) = make_float2(v[n][2], v[n][3]);
             }
             named_bar_sync(1 + team, kMoeKSplit * 32);
             if (tid < 8 * kC) {
