@@ -197,12 +197,14 @@ QMLP_DEV void mma_record(const Frag<G>& f, uint32_t xb, uint32_t xs, float (&acc
     }
 }
 // One record times NT tiles; INT4's sums of 32 k are scaled one by one, which keeps
-// few of them in registers. xn: this lane's place in the record's x (xb) by tile.
-template <int G, int NT>
+// few of them in registers. NVFP4's are all of k's, or (SUM, for an fp32 out) a record's:
+// an MMA cuts off what passes its last bit, and chains over k = 17408 were 1.3e-6 off (64
+// tokens of 17408 x 5120 take 54 us with it, 40 without). xn: this lane's place in the record's x (xb) by tile.
+template <int G, int NT, bool SUM>
 QMLP_DEV void mma_record_tiles(const Frag<G>& f, uint32_t xb, uint32_t xs, const uint32_t (&xn)[NT], float (&acc)[NT][4]) {
     using R = Rec<G>;
     __half2 z1[2], z16[2];
-    float s[2];
+    float s[2], sum[SUM ? NT : 1][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t a[2][4];
@@ -229,8 +231,13 @@ QMLP_DEV void mma_record_tiles(const Frag<G>& f, uint32_t xb, uint32_t xs, const
         for (int n = 0; n < NT; ++n) {
             const uint4 x = lds4(xb + xn[n] + i * xs);
             if constexpr (R::kNv) {
-                mma_f16_16816(acc[n], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                mma_f16_16816(acc[n], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                float (&d)[4] = SUM ? sum[n] : acc[n];
+                if (SUM && i == 0) mma_f16_16816_zc(d, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                else mma_f16_16816(d, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                mma_f16_16816(d, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                if (SUM && i == 3)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[n][e] += sum[n][e];
             } else {
                 float d[4];
                 mma_f16_16816_zc(d, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
@@ -610,7 +617,7 @@ template <int NT>
 constexpr int mid_chunks() { return NT == 8 ? 1 : 2; }  // CS: 36 KB of weights a stage, 18 with 64 tokens
 constexpr int kMidWarps = 15;  // with the producer four a scheduler: 128 registers each
 
-template <int G, int NT>
+template <int G, int NT, bool SUM>
 __global__ void __launch_bounds__((kMidWarps + 1) * 32, 1) linear_mid_kernel(const LinearArgs a, const FewPlan P) {
     using R = Rec<G>;
     constexpr int kC = 8 * NT, W = kMidWarps, kT = W * 32, kRec = R::kBytes, CS = mid_chunks<NT>();
@@ -709,7 +716,7 @@ __global__ void __launch_bounds__((kMidWarps + 1) * 32, 1) linear_mid_kernel(con
                     Frag<G> f;
                     load_frag<G>(f, rec + lane * 16, rec + 1024 + g * (R::kScales / 8),
                                  rec + 1024 + R::kScales + g * (R::kZeros / 8));
-                    mma_record_tiles<G, NT>(f, at.slot + xat + c * xbytes, xs, xn, acc);
+                    mma_record_tiles<G, NT, SUM>(f, at.slot + xat + c * xbytes, xs, xn, acc);
                 }
             at.release_and_step(lane);
         }
@@ -1018,7 +1025,7 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, linear_few_kernel<G, ONE>, a, P);
 }
 
-template <int G, int NT>
+template <int G, int NT, bool SUM>
 cudaError_t launch_mid(const LinearArgs& a, int num_sms, cudaStream_t s) {
     constexpr int kC = 8 * NT, CS = mid_chunks<NT>(), kRec = Rec<G>::kBytes;
     const int Kc = (a.K + kCh - 1) / kCh, Nt = (a.N + 15) / 16;
@@ -1035,7 +1042,7 @@ cudaError_t launch_mid(const LinearArgs& a, int num_sms, cudaStream_t s) {
     P.stages = (int)std::min<size_t>(kMaxStages, (kSmemMax - 2048 - own) / stage);
     if (P.stages < 2) return cudaErrorInvalidValue;
     static unsigned long done = 0;
-    if (const cudaError_t e = smem_once(linear_mid_kernel<G, NT>, kSmemMax, done); e != cudaSuccess) return e;
+    if (const cudaError_t e = smem_once(linear_mid_kernel<G, NT, SUM>, kSmemMax, done); e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     FewPlan X = {};
     X.S = 1;
@@ -1044,16 +1051,21 @@ cudaError_t launch_mid(const LinearArgs& a, int num_sms, cudaStream_t s) {
     cudaError_t e = cudaLaunchKernelEx(&cfg, linear_x_kernel, a);
     if (e != cudaSuccess) return e;
     cfg = few_config(P, (kMidWarps + 1) * 32, own + (size_t)P.stages * stage, s, at);
-    return cudaLaunchKernelEx(&cfg, linear_mid_kernel<G, NT>, a, P);
+    return cudaLaunchKernelEx(&cfg, linear_mid_kernel<G, NT, SUM>, a, P);
 }
 
+template <int G, bool SUM>
+cudaError_t launch_tiles(const LinearArgs& a, int num_sms, cudaStream_t s) {
+    if (a.M <= 16) return launch_mid<G, 2, SUM>(a, num_sms, s);
+    return a.M <= 32 ? launch_mid<G, 4, SUM>(a, num_sms, s) : launch_mid<G, 8, SUM>(a, num_sms, s);
+}
 template <int G>
 cudaError_t launch_g(const LinearArgs& a, int num_sms, cudaStream_t s) {
     if (a.M == 1) return launch_few<G, true>(a, num_sms, s);
     if (a.M <= kLinearFew) return launch_few<G, false>(a, num_sms, s);
     if (a.M > kLinearMid) return cudaErrorInvalidValue;  // (the GEMM's)
-    if (a.M <= 16) return launch_mid<G, 2>(a, num_sms, s);
-    return a.M <= 32 ? launch_mid<G, 4>(a, num_sms, s) : launch_mid<G, 8>(a, num_sms, s);
+    if (Rec<G>::kNv && a.odt == 0) return launch_tiles<G, Rec<G>::kNv>(a, num_sms, s);
+    return launch_tiles<G, false>(a, num_sms, s);
 }
 
 }  // namespace
