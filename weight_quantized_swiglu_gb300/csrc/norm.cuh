@@ -442,24 +442,56 @@ QMLP_DEV uint4 lds16(uint32_t a) {
 QMLP_DEV void sts16(uint32_t a, const uint4& v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+// Two fp32 values in a register pair: one instruction for both (4096 x 4096 with an
+// element's gate, backward: 61 us, one by one 63, 533 instructions a warp and row of 256
+// values; 16384 x 1024 55 to 58 us).
+typedef unsigned long long f2;
+QMLP_DEV f2 pair(float a, float b) {
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+QMLP_DEV f2 both(float a) { return pair(a, a); }
+QMLP_DEV float2 two(f2 v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+QMLP_DEV f2 fma2(f2 a, f2 b, f2 c) {
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+QMLP_DEV f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+QMLP_DEV f2 add2(f2 a, f2 b) {
+    f2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+QMLP_DEV float sum2(f2 v) {
+    const float2 t = two(v);
+    return t.x + t.y;
+}
 template <typename E>
-QMLP_DEV void get8(uint32_t at, float (&v)[8]) {
+QMLP_DEV void get8(uint32_t at, f2 (&v)[4]) {
     const uint4 a = lds16(at);
     if constexpr (sizeof(E) == 4) {
         const uint4 b = lds16(at + 512);
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+        v[0] = pair(__uint_as_float(a.x), __uint_as_float(a.y)), v[1] = pair(__uint_as_float(a.z), __uint_as_float(a.w));
+        v[2] = pair(__uint_as_float(b.x), __uint_as_float(b.y)), v[3] = pair(__uint_as_float(b.z), __uint_as_float(b.w));
     } else {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (std::is_same<E, __half>::value) {
                 const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                v[2 * i] = f.x, v[2 * i + 1] = f.y;
+                v[i] = pair(f.x, f.y);
             } else {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+                v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
             }
         }
     }
@@ -528,8 +560,8 @@ struct Walk {
             put8(w0 + (i * 4 + 2) * 512, B);
         }
     }
-    QMLP_DEV void getA(int i, float (&v)[8]) const { get8<float>(w0 + (i * 4) * 512, v); }
-    QMLP_DEV void getB(int i, float (&v)[8]) const { get8<float>(w0 + (i * 4 + 2) * 512, v); }
+    QMLP_DEV void getA(int i, f2 (&v)[4]) const { get8<float>(w0 + (i * 4) * 512, v); }
+    QMLP_DEV void getB(int i, f2 (&v)[4]) const { get8<float>(w0 + (i * 4 + 2) * 512, v); }
     static constexpr uint32_t place(int p, int i, int piece) { return ((p * NC + i) * L::row + piece) * 512; }
     // The stream's chunk of a row at p: fp32 comes as the warp's 1024 bytes in a row (a
     // thread's two halves of its own 32 are half sectors both).
@@ -593,11 +625,17 @@ struct Walk {
         return s;
     }
     template <typename E>
-    QMLP_DEV void get(uint32_t s, int p, int i, int piece, float (&v)[8]) const {
+    QMLP_DEV void get(uint32_t s, int p, int i, int piece, f2 (&v)[4]) const {
         get8<E>(s + place(p, i, piece), v);
     }
     template <typename E>
-    QMLP_DEV void store(void* p, size_t row, int i, const float (&v)[8]) const {
+    QMLP_DEV void store(void* p, size_t row, int i, const f2 (&x)[4]) const {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 t = two(x[e]);
+            v[2 * e] = t.x, v[2 * e + 1] = t.y;
+        }
         E* dst = static_cast<E*>(p) + row + col(i);
         if (all[i]) {
             stv<E, 8>(dst, v);
@@ -631,66 +669,72 @@ __global__ void __launch_bounds__(kForwardThreads) norm_forward_rows_kernel(cons
             gt[p] = a.gate_kind == kGateToken && row[p] ? (float)static_cast<const T*>(a.gate)[m + p * hop] : 1.0f;
         }
         const uint32_t s = k.arrived(st, S);
-        float h[RP][NC][8], ss[RP], rz[RP], rh[RP];
+        f2 h[RP][NC][4], sq[RP];
+        float ss[RP], rz[RP], rh[RP];
 #pragma unroll
-        for (int p = 0; p < RP; ++p) ss[p] = 0.0f, rz[p] = rh[p] = 1.0f;
+        for (int p = 0; p < RP; ++p) sq[p] = both(0.0f), rz[p] = rh[p] = 1.0f;
         if (post) {
 #pragma unroll
-            for (int p = 0; p < RP; ++p)
+            for (int p = 0; p < RP; ++p) {
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
                     if (k.ok[i]) {
-                        float v[8];
+                        f2 v[4];
                         k.template get<T>(s, p, i, 0, v);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) ss[p] = fmaf(v[e], v[e], ss[p]);
+                        for (int e = 0; e < 4; ++e) sq[p] = fma2(v[e], v[e], sq[p]);
                     }
+                ss[p] = sum2(sq[p]);
+            }
             group_sum<RP>(ss, buf, turn, tg, k.rg);
 #pragma unroll
-            for (int p = 0; p < RP; ++p) rz[p] = rsqrtf(ss[p] * a.rK + a.eps), ss[p] = 0.0f;
+            for (int p = 0; p < RP; ++p) rz[p] = rsqrtf(ss[p] * a.rK + a.eps), sq[p] = both(0.0f);
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             if (!k.ok[i]) continue;
-            float A[8];
+            f2 A[4];
             if (k.hz) k.getA(i, A);
 #pragma unroll
             for (int p = 0; p < RP; ++p) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) h[p][i][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) h[p][i][e] = both(0.0f);
                 if (k.hr) k.template get<R>(s, p, i, L::res, h[p][i]);
                 if (k.hz) {
-                    float v[8];
-                    const float f = rz[p] * gt[p];
+                    f2 v[4];
+                    const f2 f = both(rz[p] * gt[p]);
                     k.template get<T>(s, p, i, 0, v);
                     if (k.full) {
-                        float g[8];
+                        f2 g[4];
                         k.template get<T>(s, p, i, L::gate, g);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] *= g[e];
+                        for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], g[e]);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) h[p][i][e] = fmaf(v[e] * f, A[e], h[p][i][e]);
+                    for (int e = 0; e < 4; ++e) h[p][i][e] = fma2(mul2(v[e], f), A[e], h[p][i][e]);
                 }
                 if (a.h && row[p]) k.template store<R>(a.h, (size_t)(m + p * hop) * a.K, i, h[p][i]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) ss[p] = fmaf(h[p][i][e], h[p][i][e], ss[p]);
+                for (int e = 0; e < 4; ++e) sq[p] = fma2(h[p][i][e], h[p][i][e], sq[p]);
             }
         }
         if (pre) {
+#pragma unroll
+            for (int p = 0; p < RP; ++p) ss[p] = sum2(sq[p]);
             group_sum<RP>(ss, buf, turn, tg, k.rg);
 #pragma unroll
             for (int p = 0; p < RP; ++p) rh[p] = rsqrtf(ss[p] * a.rK + a.eps);
 #pragma unroll
             for (int i = 0; i < NC; ++i) {
                 if (!k.ok[i]) continue;
-                float B[8];
+                f2 B[4];
                 k.getB(i, B);
 #pragma unroll
                 for (int p = 0; p < RP; ++p) {
-                    float v[8];
+                    f2 v[4];
+                    const f2 f = both(rh[p]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = h[p][i][e] * rh[p] * B[e];
+                    for (int e = 0; e < 4; ++e) v[e] = mul2(mul2(h[p][i][e], f), B[e]);
                     if (row[p]) k.template store<T>(a.y, (size_t)(m + p * hop) * a.K, i, v);
                 }
             }
@@ -717,11 +761,11 @@ __global__ void __launch_bounds__(NC == 1 && RP == 1 ? 640 : 512) norm_backward_
     pdl_launch_dependents();  // (the columns' kernel: it waits for this one's end)
     for (int i = 0; i + 1 < S; ++i) k.fetch_rows(first + i * RP * hop, hop, i);
     k.fetch_weights();
-    float D[NC][8], P[NC][8];  // columns' sums of t dH zh (times an element's gate) and of dy hh
+    f2 D[NC][4], P[NC][4];  // columns' sums of t dH zh (times an element's gate) and of dy hh
 #pragma unroll
     for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) D[i][e] = P[i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) D[i][e] = P[i][e] = both(0.0f);
     int st = 0, turn = 0;
     for (long m = first; m < a.M; m += RP * hop) {
         k.fetch_rows(m + (S - 1) * RP * hop, hop, st ? st - 1 : S - 1);
@@ -735,55 +779,60 @@ __global__ void __launch_bounds__(NC == 1 && RP == 1 ? 640 : 512) norm_backward_
             gt[p] = token && row[p] ? (float)static_cast<const T*>(a.gate)[m + p * hop] : 1.0f;
         }
         const uint32_t s = k.arrived(st, S);
-        float x[RP][NC][8], y[RP][NC][8], c[3 * RP];  // hh; dh + dy B / rms
+        f2 x[RP][NC][4], y[RP][NC][4], c2[3 * RP];  // hh; dh + dy B / rms
+        float c[3 * RP];
 #pragma unroll
-        for (int j = 0; j < 3 * RP; ++j) c[j] = 0.0f;
+        for (int j = 0; j < 3 * RP; ++j) c2[j] = both(0.0f);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             if (!k.ok[i]) continue;
-            float A[8], B[8];
+            f2 A[4], B[4];
             if (k.hz) k.getA(i, A);
             if (pre) k.getB(i, B);
 #pragma unroll
             for (int p = 0; p < RP; ++p) {
-                float q[8], v[8];
+                f2 q[4], v[4];
                 if (k.hz) {
+                    const f2 f = both(rz[p]);
                     k.template get<T>(s, p, i, 0, q);
                     if (k.full) {
                         k.template get<T>(s, p, i, L::gate, v);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) q[e] *= v[e];
+                        for (int e = 0; e < 4; ++e) q[e] = mul2(q[e], v[e]);
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) q[e] *= rz[p] * A[e];
+                    for (int e = 0; e < 4; ++e) q[e] = mul2(mul2(q[e], f), A[e]);
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[p][i][e] = 0.0f;
+                for (int e = 0; e < 4; ++e) y[p][i][e] = both(0.0f);
                 if (k.hd) k.template get<R>(s, p, i, L::dh, y[p][i]);
                 if (pre) {
-                    float (&h)[8] = x[p][i];
+                    f2 (&h)[4] = x[p][i];
+                    const f2 g = both(gt[p]), f = both(rh[p]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) h[e] = 0.0f;
+                    for (int e = 0; e < 4; ++e) h[e] = both(0.0f);
                     if (k.hr) k.template get<R>(s, p, i, L::res, h);
                     if (k.hz)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) h[e] = fmaf(gt[p], q[e], h[e]);
+                        for (int e = 0; e < 4; ++e) h[e] = fma2(g, q[e], h[e]);
                     k.template get<T>(s, p, i, L::dy, v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        h[e] *= rh[p];
-                        P[i][e] = fmaf(v[e], h[e], P[i][e]);
-                        v[e] *= B[e];
-                        c[3 * p] = fmaf(v[e], h[e], c[3 * p]);
-                        y[p][i][e] = fmaf(v[e], rh[p], y[p][i][e]);
-                        if (k.hz) c[3 * p + 2] = fmaf(h[e], q[e], c[3 * p + 2]);
+                    for (int e = 0; e < 4; ++e) {
+                        h[e] = mul2(h[e], f);
+                        P[i][e] = fma2(v[e], h[e], P[i][e]);
+                        v[e] = mul2(v[e], B[e]);
+                        c2[3 * p] = fma2(v[e], h[e], c2[3 * p]);
+                        y[p][i][e] = fma2(v[e], f, y[p][i][e]);
+                        if (k.hz) c2[3 * p + 2] = fma2(h[e], q[e], c2[3 * p + 2]);
                     }
                 }
                 if (k.hz)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) c[3 * p + 1] = fmaf(y[p][i][e], q[e], c[3 * p + 1]);
+                    for (int e = 0; e < 4; ++e) c2[3 * p + 1] = fma2(y[p][i][e], q[e], c2[3 * p + 1]);
             }
         }
+#pragma unroll
+        for (int j = 0; j < 3 * RP; ++j) c[j] = sum2(c2[j]);
         group_sum<3 * RP>(c, buf, turn, tg, k.rg);
         float mr[RP], back[RP];
 #pragma unroll
@@ -796,34 +845,36 @@ __global__ void __launch_bounds__(NC == 1 && RP == 1 ? 640 : 512) norm_backward_
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             if (!k.ok[i]) continue;
-            float A[8];
+            f2 A[4];
             if (k.hz) k.getA(i, A);
 #pragma unroll
             for (int p = 0; p < RP; ++p) {
-                float (&d)[8] = y[p][i];
+                f2 (&d)[4] = y[p][i];
                 const size_t at = (size_t)(m + p * hop) * K;
-                if (pre)
+                if (pre) {
+                    const f2 f = both(-mr[p]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] = fmaf(-x[p][i][e], mr[p], d[e]);
+                    for (int e = 0; e < 4; ++e) d[e] = fma2(x[p][i][e], f, d[e]);
+                }
                 if (a.dr && row[p]) k.template store<R>(a.dr, at, i, d);
                 if (!k.hz) continue;
-                float z[8], t[8];
+                f2 z[4], t[4];
                 k.template get<T>(s, p, i, 0, z);
-                const float f = rz[p] * gt[p], zb = rz[p] * back[p];
+                const f2 f = both(rz[p] * gt[p]), zb = both(-rz[p] * back[p]), r = both(rz[p]);
                 if (k.full) {
                     if (a.dgate && row[p]) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) t[e] = d[e] * (z[e] * rz[p] * A[e]);
+                        for (int e = 0; e < 4; ++e) t[e] = mul2(d[e], mul2(mul2(z[e], r), A[e]));
                         k.template store<T>(a.dgate, at, i, t);
                     }
                     k.template get<T>(s, p, i, L::gate, t);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) d[e] *= t[e];
+                    for (int e = 0; e < 4; ++e) d[e] = mul2(d[e], t[e]);
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    D[i][e] = fmaf(d[e], z[e] * f, D[i][e]);
-                    t[e] = fmaf(d[e] * A[e], f, -(z[e] * zb));
+                for (int e = 0; e < 4; ++e) {
+                    D[i][e] = fma2(d[e], mul2(z[e], f), D[i][e]);
+                    t[e] = fma2(mul2(d[e], A[e]), f, mul2(z[e], zb));
                 }
                 if (a.dz && row[p]) k.template store<T>(a.dz, at, i, t);
             }
@@ -848,9 +899,11 @@ __global__ void __launch_bounds__(NC == 1 && RP == 1 ? 640 : 512) norm_backward_
                     if (c < 0 || c >= K) continue;
                     const float gate = channel ? k.weight1(a.gate, c) : 1.0f;
                     const float w = channel && a.post_w ? k.weight1(a.post_w, c) + a.offset : 1.0f;
-                    sum[c] = (g ? sum[c] : 0.0f) + a.scale * gate * D[i][e];
-                    sum[K + c] = (g ? sum[K + c] : 0.0f) + P[i][e];
-                    if (channel) sum[2 * K + c] = (g ? sum[2 * K + c] : 0.0f) + a.scale * w * D[i][e];
+                    const float2 d2 = two(D[i][e >> 1]), p2 = two(P[i][e >> 1]);
+                    const float dv = e & 1 ? d2.y : d2.x, pv = e & 1 ? p2.y : p2.x;
+                    sum[c] = (g ? sum[c] : 0.0f) + a.scale * gate * dv;
+                    sum[K + c] = (g ? sum[K + c] : 0.0f) + pv;
+                    if (channel) sum[2 * K + c] = (g ? sum[2 * K + c] : 0.0f) + a.scale * w * dv;
                 }
         __syncthreads();
     }
@@ -959,8 +1012,8 @@ bool rows_try(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
     }
     return true;
 }
-// The first form that fits: two rows at a time (16384 x 1024, backward 64 -> 58 us; 4096
-// x 4096 with an element's gate 81 -> 63 us), one, sixteen values a thread.
+// The first form that fits: two rows at a time (16384 x 1024, backward 58 us, one 64; 4096
+// x 4096 with an element's gate 63 and 81), one, sixteen values a thread.
 template <typename T, typename R, int G, bool BWD>
 bool rows_g(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
     if constexpr (G != kAny) {
@@ -977,12 +1030,12 @@ bool launch_rows(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
 
 // Backward, the kernels that walk over rows wherever they fit. Forward a row a CTA (up to
 // 1024 columns: a warp) hides a row's latencies behind other rows' as well and has no
-// weights to lay out: it is ahead for few rows and for an fp32 stream (512 x 5120 7.9 to
-// 8.6 us; fp32 2048 x 5120 26 to 30, 8192 x 5120 91 to 102; 16384 x 512 17.9 to 18.6),
-// behind otherwise (2048 x 5120 23.7 to 21.6 us, 16384 x 1024 46 to 29, 4096 x 4096 with an
-// element's gate 47 to 37, 2048 x 8192 46 to 36). Rows of no multiple of eight values have
-// the walks, or a value at a time (301 x 2571 8.3 to 9.8 us, backward 16 to 25; 4096 x 3333
-// 43 to 48 and 64 to 198).
+// weights to lay out: it is ahead for few rows and for an fp32 stream (512 x 5120 8.0 to
+// 8.6 us; fp32 2048 x 5120 26 to 30, 8192 x 5120 91 to 102; 16384 x 512 17.7 to 18.6),
+// behind otherwise (2048 x 5120 23.7 to 21.2 us, 16384 x 1024 46 to 29, 4096 x 4096 with an
+// element's gate 47 to 36, 2048 x 8192 46 to 36). Rows of no multiple of eight values have
+// the walks, or a value at a time (301 x 2571 7.8 to 9.8 us, backward 16 to 25; 4096 x 3333
+// 43 to 48 and 61 to 198).
 template <typename T, typename R>
 cudaError_t launch_tr(const NormArgs& a, bool backward, cudaStream_t s) {
     const int K = a.K;
