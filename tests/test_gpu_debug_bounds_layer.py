@@ -60,7 +60,7 @@ def _linear(torch, fmt, N, K, G, tokens):
     return _bytes(torch, *outs)
 
 
-def _moe(torch, E, S, K, I, topk, meta, tokens):
+def _moe(torch, E, S, K, I, topk, meta, tokens, dtype="bf16"):
     from test_gpu_moe_layer import Bank
     moe = Bank(E + S, K, I, meta, E).handle()
     g = torch.Generator(device="cuda").manual_seed(K)
@@ -69,7 +69,8 @@ def _moe(torch, E, S, K, I, topk, meta, tokens):
     outs = []
     for M in tokens:
         x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
-        out, ids = torch.empty_like(x), torch.empty((M, topk), dtype=torch.int32, device="cuda")
+        out = torch.empty((M, K), device="cuda", dtype=torch.float32 if dtype == "fp32" else torch.bfloat16)
+        ids = torch.empty((M, topk), dtype=torch.int32, device="cuda")
         layer.forward(x, out, ids=ids)
         outs += [out, ids]
     layer.check()
@@ -90,7 +91,8 @@ def cases():
               ("nvfp4", 17, 48, 16, (1, 8, 9))):
         out[f"linear {a[0]} {a[1]}"] = lambda t, a=a: _linear(t, *a)
     for a in ((512, 1, 640, 160, 10, 4, (1, 4, 16, 40)), (30, 0, 4096, 1024, 2, 4, (16, 1)),
-              (12, 1, 8192, 64, 3, 4, (1, 12)), (7, 2, 320, 96, 7, 3, (1, 9, 17)), (40, 1, 512, 256, 6, 4, (3, 16))):
+              (12, 1, 8192, 64, 3, 4, (1, 12)), (7, 2, 320, 96, 7, 3, (1, 9, 17)), (40, 1, 512, 256, 6, 4, (3, 16)),
+              (31, 0, 4096, 1024, 2, 4, (16, 5, 1), "fp32"), (8, 2, 320, 96, 7, 3, (1, 9, 17), "fp32")):
         out[f"moe {a[0]} {a[2]}"] = lambda t, a=a: _moe(t, *a)
     return out
 
