@@ -328,18 +328,28 @@ QMLP_DEV void stage_x(const MoeLayerArgs& a, const void* x, int M, uint4* xsm, i
     for (int m = warp / wpt; m < M; m += nw / wpt) {
         const uint32_t* row = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(x) + (size_t)m * K);
         float mx = 0.0f;
-#pragma unroll 4
-        for (int q = (warp % wpt) * 32 + lane; q < K / 8; q += 32 * wpt) {
-            // lane t of unit j: word t of its four pieces (16 bytes in four places at once
-            // met on a bank: 8 tokens of 2560 4.1 us)
-            const int j = q >> 2, t = q & 3;
-            uint32_t w[4];
+        // lane t of unit j: word t of its four pieces (16 bytes in four places at once met on
+        // a bank: 8 tokens of 2560 4.1 us). All loads of a batch are under way together (the
+        // rest of an unrolled loop goes one by one).
+        constexpr int kBatch = 6;
+        for (int q0 = (warp % wpt) * 32 + lane; q0 < K / 8; q0 += 32 * wpt * kBatch) {
+            uint32_t w[kBatch][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = row[16 * j + 4 * i + t];
+            for (int b = 0; b < kBatch; ++b) {
+                const int q = q0 + 32 * wpt * b, at = 16 * (q >> 2) + (q & 3);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xFFFF0000u))));
-            xsm[(j * M + m) * 4 + t] = a.x_bf16 ? make_uint4(w[0], w[1], w[2], w[3]) : unit_order(w[0], w[1], w[2], w[3]);
+                for (int i = 0; i < 4; ++i) w[b][i] = q < K / 8 ? row[at + 4 * i] : 0u;
+            }
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int q = q0 + 32 * wpt * b;
+                if (q >= K / 8) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(w[b][i] << 16)), fabsf(__uint_as_float(w[b][i] & 0xFFFF0000u))));
+                xsm[((q >> 2) * M + m) * 4 + (q & 3)] = a.x_bf16 ? make_uint4(w[b][0], w[b][1], w[b][2], w[b][3])
+                                                                 : unit_order(w[b][0], w[b][1], w[b][2], w[b][3]);
+            }
         }
         if (a.x_bf16) {
 #pragma unroll
@@ -493,30 +503,40 @@ template <bool QUAD, bool LO>
 QMLP_DEV void convert_act(const MoeLayerArgs& a, int rows, uint4* out, size_t out_elems, int i0, int hop) {
     const bool quad = QUAD && quads(a.I);
     const int nu = a.I / 32;
-#pragma unroll 4
-    for (int i = i0; i < rows * nu * 4; i += hop) {
-        const int t = i & 3, r = (i >> 2) / nu, u = (i >> 2) % nu;
-        const float* p = a.act + (size_t)(i >> 2) * 32 + 2 * t;
-        if (!QMLP_INB((size_t)(i >> 2) * 32 + 31, a.act_elems, 107) || !QMLP_INB((LO ? rows * nu * 4 : 0) + i, out_elems, 109)) continue;
-        float2 v[4];
+    constexpr int kBatch = LO ? 2 : 3;  // (88 rows of 160: all loads under way together)
+    for (int b0 = i0; b0 < rows * nu * 4; b0 += hop * kBatch) {
+        float2 v[kBatch][4];
+        int top[kBatch];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __ldcg(reinterpret_cast<const float2*>(p + 8 * j));
-        const float up = __int_as_float((127 + act_exponent(__ldcg(a.amax + r))) << 23);
-        uint32_t h[4], l[4];
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = b0 + b * hop, t = i & 3;
+            const bool in = i < rows * nu * 4 && QMLP_INB((size_t)(i >> 2) * 32 + 31, a.act_elems, 107);
+            const float* p = a.act + (size_t)(in ? i >> 2 : 0) * 32 + 2 * t;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 w = make_float2(v[j].x * up, v[j].y * up);
-            const __half2 q = __floats2half2_rn(w.x, w.y);
-            h[j] = u32(q);
-            if (LO) {  // (nothing of what is not finite)
-                const float2 f = __half22float2(q);
-                l[j] = u32(__floats2half2_rn(isfinite(f.x) ? w.x - f.x : 0.0f, isfinite(f.y) ? w.y - f.y : 0.0f));
-            }
+            for (int j = 0; j < 4; ++j) v[b][j] = in ? __ldcg(reinterpret_cast<const float2*>(p + 8 * j)) : make_float2(0.0f, 0.0f);
+            top[b] = in ? __ldcg(a.amax + (i >> 2) / nu) : 0;
         }
-        // (of four units: lane t's pieces are unit t's, see w2_quads)
-        const int at = quad ? i + 3 * (t - (u & 3)) : i;
-        out[at] = unit_order(h[0], h[1], h[2], h[3]);
-        if (LO) out[rows * nu * 4 + at] = unit_order(l[0], l[1], l[2], l[3]);
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int i = b0 + b * hop, t = i & 3, u = (i >> 2) % nu;
+            if (i >= rows * nu * 4 || !QMLP_INB((LO ? rows * nu * 4 : 0) + i, out_elems, 109)) continue;
+            const float up = __int_as_float((127 + act_exponent(top[b])) << 23);
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 w = make_float2(v[b][j].x * up, v[b][j].y * up);
+                const __half2 q = __floats2half2_rn(w.x, w.y);
+                h[j] = u32(q);
+                if (LO) {  // (nothing of what is not finite)
+                    const float2 f = __half22float2(q);
+                    l[j] = u32(__floats2half2_rn(isfinite(f.x) ? w.x - f.x : 0.0f, isfinite(f.y) ? w.y - f.y : 0.0f));
+                }
+            }
+            // (of four units: lane t's pieces are unit t's, see w2_quads)
+            const int at = quad ? i + 3 * (t - (u & 3)) : i;
+            out[at] = unit_order(h[0], h[1], h[2], h[3]);
+            if (LO) out[rows * nu * 4 + at] = unit_order(l[0], l[1], l[2], l[3]);
+        }
     }
 }
 
@@ -718,15 +738,21 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
         const bool room = all * 4 <= L.part_bytes;
         float* lg = room ? part : a.logits;
         if (warp < kWarps && room) {
-#pragma unroll 4
-            for (int i = threadIdx.x; i < all; i += kThreads) {
-                float v[kMoeRouterSplits];
+            constexpr int kBatch = 7;  // (8 tokens of 512 experts: all loads under way together)
+            for (int i0 = threadIdx.x; i0 < all; i0 += kThreads * kBatch) {
+                float v[kBatch][kMoeRouterSplits];
 #pragma unroll
-                for (int s = 0; s < kMoeRouterSplits; ++s) v[s] = s < splits ? __ldcg(a.logits + s * hop + i) : 0.0f;
+                for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-                for (int s = 1; s < kMoeRouterSplits; ++s)
-                    if (s < splits) v[0] += v[s];
-                part[i] = v[0];
+                    for (int s = 0; s < kMoeRouterSplits; ++s)
+                        v[b][s] = s < splits && i0 + b * kThreads < all ? __ldcg(a.logits + s * hop + i0 + b * kThreads) : 0.0f;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+                    for (int s = 1; s < kMoeRouterSplits; ++s)
+                        if (s < splits) v[b][0] += v[b][s];
+                    if (i0 + b * kThreads < all) part[i0 + b * kThreads] = v[b][0];
+                }
             }
         }
         if (warp < kWarps) {
