@@ -880,13 +880,14 @@ class BlockNorm:
     def _addr(self, n, t, M):
         """The address of argument n; refuses what is not a contiguous CUDA tensor of
         its type and shape (raw addresses are the caller's)."""
-        if t is None or isinstance(t, int):
+        if t is None or type(t) is int:
             return t
         dtype, rows, last = self._args[n]
-        if (t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or
-                t.numel() != (M * last if rows else last or M) or t.dim() == 0 or t.shape[-1] != (last or M)):
-            shape = ((M, last) if rows else (last or M,))
-            raise ValueError(f"BlockNorm: {n} has to be a contiguous CUDA tensor of {dtype}, {shape}")
+        last = last or M
+        if (t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != (M * last if rows else last) or
+                (t.shape or (0,))[-1] != last):
+            raise ValueError(f"BlockNorm: {n} has to be a contiguous CUDA tensor of {dtype}, "
+                             f"{(M, last) if rows else (last,)}")
         return t.data_ptr()
 
     def _rows(self, z, residual):
