@@ -26,6 +26,35 @@ namespace {
 
 constexpr int kWarps = 8;  // rows (warps) of a CTA where a warp takes a row
 
+template <typename T>
+QMLP_DEV void open8(const uint4& a, float (&v)[8]) {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __half>::value) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+        } else {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+// V values of T as they lie in memory.
+template <typename T, int V>
+struct Packed {
+    T v;
+    QMLP_DEV void zero() { v = (T)0.0f; }
+    QMLP_DEV void load(const T* p) { v = *p; }
+    QMLP_DEV void open(float (&f)[V]) const { f[0] = (float)v; }
+};
+template <typename T>
+struct Packed<T, 8> {
+    uint4 v;
+    QMLP_DEV void zero() { v = make_uint4(0, 0, 0, 0); }
+    QMLP_DEV void load(const T* p) { v = *reinterpret_cast<const uint4*>(p); }
+    QMLP_DEV void open(float (&f)[8]) const { open8<T>(v, f); }
+};
 template <typename T, int V>
 QMLP_DEV void ldv(const T* p, float (&v)[V]) {
     if constexpr (V == 1) {
@@ -44,18 +73,7 @@ QMLP_DEV void ldv(const T* p, float (&v)[V]) {
             v[i] = a.x, v[i + 1] = a.y, v[i + 2] = a.z, v[i + 3] = a.w;
         }
     } else {
-        const uint4 a = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (std::is_same<T, __half>::value) {
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                v[2 * i] = f.x, v[2 * i + 1] = f.y;
-            } else {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-        }
+        open8<T>(*reinterpret_cast<const uint4*>(p), v);
     }
 }
 QMLP_DEV void put(float* p, float v) { *p = v; }
@@ -128,8 +146,9 @@ QMLP_DEV int column(int i) {
     return (WARP ? i * 32 + (int)(threadIdx.x & 31) : i * (int)blockDim.x + (int)threadIdx.x) * V;
 }
 
-template <typename T, typename R, int V, int NC, bool WARP>
-__global__ void __launch_bounds__(WARP ? kWarps * 32 : 1024) norm_forward_kernel(const NormArgs a) {
+// TIGHT: 32 registers a thread.
+template <typename T, typename R, int V, int NC, bool WARP, bool TIGHT>
+__global__ void __launch_bounds__(WARP ? kWarps * 32 : 1024, TIGHT ? 2 : 1) norm_forward_kernel(const NormArgs a) {
     __shared__ float buf[2][1][32];
     int turn = 0;
     const long m = WARP ? (long)blockIdx.x * kWarps + (threadIdx.x >> 5) : (long)blockIdx.x;
@@ -138,15 +157,17 @@ __global__ void __launch_bounds__(WARP ? kWarps * 32 : 1024) norm_forward_kernel
     const size_t at = (size_t)m * K;
     const T* z = static_cast<const T*>(a.z) + at;
     const R* r = static_cast<const R*>(a.r) + at;
-    float h[NC][V], zv[NC][V];
+    float h[NC][V];
+    Packed<T, V> zp[NC];  // (as it came: registers)
     float ss[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
         const int c = column<V, WARP>(i);
 #pragma unroll
-        for (int e = 0; e < V; ++e) h[i][e] = zv[i][e] = 0.0f;
+        for (int e = 0; e < V; ++e) h[i][e] = 0.0f;
+        zp[i].zero();
         if (c < K && QMLP_INB(at + c + V - 1, a.elems, 81)) {
-            if (a.z) ldv<T, V>(z + c, zv[i]);
+            if (a.z) zp[i].load(z + c);
             if (a.r) ldv<R, V>(r + c, h[i]);
         }
     }
@@ -154,9 +175,12 @@ __global__ void __launch_bounds__(WARP ? kWarps * 32 : 1024) norm_forward_kernel
     if (a.z) {
         if (a.post_w) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
+            for (int i = 0; i < NC; ++i) {
+                float v[V];
+                zp[i].open(v);
 #pragma unroll
-                for (int e = 0; e < V; ++e) ss[0] = fmaf(zv[i][e], zv[i][e], ss[0]);
+                for (int e = 0; e < V; ++e) ss[0] = fmaf(v[e], v[e], ss[0]);
+            }
             row_sum<WARP, 1>(ss, buf, turn);
             rz = rsqrtf(ss[0] * a.rK + a.eps);
         }
@@ -166,13 +190,14 @@ __global__ void __launch_bounds__(WARP ? kWarps * 32 : 1024) norm_forward_kernel
         for (int i = 0; i < NC; ++i) {
             const int c = column<V, WARP>(i);
             if (c < K) {
-                float w[V], g[V];
+                float w[V], g[V], v[V];
+                zp[i].open(v);
                 if (a.post_w) ldw<T, V>(a.post_w, a.w_f32, c, w);
                 if (a.gate_kind == kGateChannel) ldw<T, V>(a.gate, a.w_f32, c, g);
                 if (a.gate_kind == kGateFull) ldv<T, V>(static_cast<const T*>(a.gate) + at + c, g);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    float n = zv[i][e];
+                    float n = v[e];
                     if (a.post_w) n = n * rz * (w[e] + a.offset);
                     if (a.gate_kind == kGateChannel || a.gate_kind == kGateFull) n *= g[e];
                     h[i][e] = fmaf(s, n, h[i][e]);
@@ -950,10 +975,10 @@ cudaError_t launch_columns(const NormArgs& a, int shares, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, norm_columns_kernel<T>, a, shares);
 }
 
-template <typename T, typename R, int V, int NC, bool WARP>
+template <typename T, typename R, int V, int NC, bool WARP, bool TIGHT = false>
 cudaError_t launch_forward(const NormArgs& a, int threads, cudaStream_t s) {
     const unsigned grid = (unsigned)(WARP ? (a.M + kWarps - 1) / kWarps : a.M);
-    norm_forward_kernel<T, R, V, NC, WARP><<<grid, WARP ? kWarps * 32 : threads, 0, s>>>(a);
+    norm_forward_kernel<T, R, V, NC, WARP, TIGHT><<<grid, WARP ? kWarps * 32 : threads, 0, s>>>(a);
     return cudaPeekAtLastError();
 }
 template <typename T, typename R, int V, int NC, bool WARP>
@@ -1029,13 +1054,14 @@ bool launch_rows(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
 }
 
 // Backward, the kernels that walk over rows wherever they fit. Forward a row a CTA (up to
-// 1024 columns: a warp) hides a row's latencies behind other rows' as well and has no
-// weights to lay out: it is ahead for few rows and for an fp32 stream (512 x 5120 8.0 to
-// 8.6 us; fp32 2048 x 5120 26 to 30, 8192 x 5120 91 to 102; 16384 x 512 17.7 to 18.6),
-// behind otherwise (2048 x 5120 23.7 to 21.2 us, 16384 x 1024 46 to 29, 4096 x 4096 with an
-// element's gate 47 to 36, 2048 x 8192 46 to 36). Rows of no multiple of eight values have
-// the walks, or a value at a time (301 x 2571 7.8 to 9.8 us, backward 16 to 25; 4096 x 3333
-// 43 to 48 and 61 to 198).
+// 256 columns: a warp), which hides a row's latencies behind other rows'. From four rows an
+// SM on it may take 32 registers, so that an SM is full of threads (8192 x 5120 with an fp32
+// stream 84 us, 95 with the 42 it would like, 102 walking; 8192 x 4096 64 to 81; with fewer
+// rows the spilled ones show, 512 x 5120 8.1 to 8.8). Walking is ahead for very many rows
+// of a 16-bit stream (8192 x 5120 64 us to 70, 8192 x 2048 27.5 to 28.1; 4096 x 4096 32 to 30),
+// a warp a row is behind from 512 columns on (16384 x 512 17.5 us to 15.2, 2048 x 1024 8.8 to
+// 5.8). Rows of no multiple of eight values have the walks, or a value at a time (301 x
+// 2571 7.8 to 9.8 us, backward 16 to 25; 4096 x 3333 43 to 48 and 61 to 198).
 template <typename T, typename R>
 cudaError_t launch_tr(const NormArgs& a, bool backward, cudaStream_t s) {
     const int K = a.K;
@@ -1048,12 +1074,13 @@ cudaError_t launch_tr(const NormArgs& a, bool backward, cudaStream_t s) {
         if (K <= 8192) return launch_backward<T, R, 1, 8, false>(a, up((K + 7) / 8), s);
         return launch_backward<T, R, 1, 16, false>(a, up((K + 15) / 16), s);
     }
-    const bool walk = K % 8 || (sizeof(R) == 2 && K > 512 && a.M >= 8L * a.num_sms);
+    const bool walk = K % 8 || (sizeof(R) == 2 && K > 1024 && a.M >= 32L * a.num_sms);
     if (a.vec && walk && launch_rows<T, R, false>(a, s, e)) return e;
     if (a.vec && K % 8 == 0) {
-        if (K <= 512) return launch_forward<T, R, 8, 2, true>(a, 0, s);
-        if (K <= 1024) return launch_forward<T, R, 8, 4, true>(a, 0, s);
-        if (K <= 8192) return launch_forward<T, R, 8, 1, false>(a, up(K / 8), s);
+        if (K <= 256) return launch_forward<T, R, 8, 1, true>(a, 0, s);
+        if (K <= 8192)
+            return a.M >= 4L * a.num_sms ? launch_forward<T, R, 8, 1, false, true>(a, up(K / 8), s)
+                                         : launch_forward<T, R, 8, 1, false>(a, up(K / 8), s);
         return launch_forward<T, R, 8, 2, false>(a, up((K / 8 + 1) / 2), s);
     }
     if (K <= 256) return launch_forward<T, R, 1, 8, true>(a, 0, s);
