@@ -407,7 +407,9 @@ __global__ void __launch_bounds__(WARP ? kWarps * 32 : 1024) norm_backward_kerne
 // G: kAny, or z, the residual and both norms are there and no element has
 // its own gate (kScalar) or every one has (kFull).
 // ---------------------------------------------------------------------------
-constexpr int kForwardThreads = 768;
+// (768: 4096 x 3333, whose rows take 448 threads, 42 us instead of 30; 1024: 31, and 8192 x
+// 5120 69 instead of 66, by their fewer registers)
+constexpr int kForwardThreads = 896;
 constexpr int kAny = 0, kScalar = 1, kFull = 2;
 // 16 bytes on their way, the first n of them from memory, zeros behind
 QMLP_DEV void cp16(uint32_t dst, const void* src, int n) {
@@ -1057,11 +1059,11 @@ bool launch_rows(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
 // 256 columns: a warp), which hides a row's latencies behind other rows'. From four rows an
 // SM on it may take 32 registers, so that an SM is full of threads (8192 x 5120 with an fp32
 // stream 84 us, 95 with the 42 it would like, 102 walking; 8192 x 4096 64 to 81; with fewer
-// rows the spilled ones show, 512 x 5120 8.1 to 8.8). Walking is ahead for very many rows
-// of a 16-bit stream (8192 x 5120 64 us to 70, 8192 x 2048 27.5 to 28.1; 4096 x 4096 32 to 30),
+// rows the spilled ones show, 512 x 5120 8.1 to 8.8). Walking is ahead for very many long
+// rows of a 16-bit stream (8192 x 5120 66 us to 70; 8192 x 2048 28 both, 4096 x 4096 32 to 30),
 // a warp a row is behind from 512 columns on (16384 x 512 17.5 us to 15.2, 2048 x 1024 8.8 to
 // 5.8). Rows of no multiple of eight values have the walks, or a value at a time (301 x
-// 2571 7.8 to 9.8 us, backward 16 to 25; 4096 x 3333 43 to 48 and 61 to 198).
+// 2571 7.5 to 9.8 us, backward 16 to 25; 4096 x 3333 30 to 48 and 61 to 198).
 template <typename T, typename R>
 cudaError_t launch_tr(const NormArgs& a, bool backward, cudaStream_t s) {
     const int K = a.K;
@@ -1074,7 +1076,7 @@ cudaError_t launch_tr(const NormArgs& a, bool backward, cudaStream_t s) {
         if (K <= 8192) return launch_backward<T, R, 1, 8, false>(a, up((K + 7) / 8), s);
         return launch_backward<T, R, 1, 16, false>(a, up((K + 15) / 16), s);
     }
-    const bool walk = K % 8 || (sizeof(R) == 2 && K > 1024 && a.M >= 32L * a.num_sms);
+    const bool walk = K % 8 || (sizeof(R) == 2 && K > 4096 && a.M >= 32L * a.num_sms);
     if (a.vec && walk && launch_rows<T, R, false>(a, s, e)) return e;
     if (a.vec && K % 8 == 0) {
         if (K <= 256) return launch_forward<T, R, 8, 1, true>(a, 0, s);
