@@ -169,6 +169,8 @@ __global__ void __launch_bounds__(WARP ? kWarps * 32 : 1024, TIGHT ? 2 : 1) norm
         if (c < K && QMLP_INB(at + c + V - 1, a.elems, 81)) {
             if (a.z) zp[i].load(z + c);
             if (a.r) ldv<R, V>(r + c, h[i]);
+            if (a.gate_kind == kGateFull && a.post_w)  // (into L2 while the row is summed: 4096 x 4096 36.1 -> 34.5 us)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const T*>(a.gate) + at + c));
         }
     }
     float rz = 1.0f, rh = 1.0f;
@@ -1060,7 +1062,7 @@ bool launch_rows(const NormArgs& a, cudaStream_t s, cudaError_t& e) {
 // SM on it may take 32 registers, so that an SM is full of threads (8192 x 5120 with an fp32
 // stream 84 us, 95 with the 42 it would like, 102 walking; 8192 x 4096 64 to 81; with fewer
 // rows the spilled ones show, 512 x 5120 8.1 to 8.8). Walking is ahead for very many long
-// rows of a 16-bit stream (8192 x 5120 66 us to 70; 8192 x 2048 28 both, 4096 x 4096 32 to 30),
+// rows of a 16-bit stream (8192 x 5120 66 us to 70; 8192 x 2048 28 both, 4096 x 4096 32 to 29.5),
 // a warp a row is behind from 512 columns on (16384 x 512 17.5 us to 15.2, 2048 x 1024 8.8 to
 // 5.8). Rows of no multiple of eight values have the walks, or a value at a time (301 x
 // 2571 7.5 to 9.8 us, backward 16 to 25; 4096 x 3333 30 to 48 and 61 to 198).
