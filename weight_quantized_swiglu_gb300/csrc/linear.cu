@@ -396,7 +396,7 @@ struct FewPlan {
     int batch;   // few: groups whose sums wait in shared memory (S > 1)
 };
 // Warps and CTAs an SM, one token and two to eight (5120 x 5120 / 17408 x 5120 / 128000 x
-// 5120 NVFP4: one token 7.0 / 15.7 / 78 us, with 16 warps in one CTA 7.6 / 14.1 / 84; eight
+// 5120 NVFP4: one token 6.9 / 15.4 / 76 us, with 16 warps in one CTA 7.6 / 14.1 / 84; eight
 // tokens 10.9 / 17.3 / 86, with 8 warps in two CTAs 12.1 / 22.6 / 111).
 template <bool ONE>
 constexpr int few_warps() { return ONE ? 8 : 16; }
@@ -1012,7 +1012,10 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     const int fit = one ? 1 : kCtas;
     P.gy = std::max(1, std::min(groups, num_sms * fit / P.S));
     const int mine = (groups + P.gy - 1) / P.gy;
-    P.gy = (groups + mine - 1) / mine;
+    // Single CTAs fill every place, some with a group less (8192 x 5120 9.3 us; as many to
+    // each in fewer CTAs 10.8). Clusters get as many each: the GPU does not hold as many
+    // of them as its SMs would (5120 x 17408, eight tokens, S = 8: 21.4 us, 35.6 with all).
+    if (P.S > 1) P.gy = (groups + mine - 1) / mine;
     P.batch = 1;
     if (P.S > 1) {  // a quarter of what is left for the sums that wait
         const size_t left = all - x - red - 2 * kStage;
