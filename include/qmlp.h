@@ -704,11 +704,12 @@ qmlp_status qmlp_linear_check(qmlp_linear_t* h, qmlp_stream_t stream);
  *   a shared expert's w is 1, or sigmoid(shared_gate . x)
  *   out = sum of w[e] W2[e] (SiLU(g) u),  g, u = the halves of W13[e] x
  * (a shared expert of n times the width is n shared experts of the handle's I).
- * Up to 16 tokens whose x fits in shared memory (2 K bytes a token) run as one
- * kernel: sums are fp32, the intermediate is rounded once to fp16 times a power of
- * two of the token and expert (to two fp16 for an fp32 out), out once; a token's result does not depend on the
- * others of the call. More tokens run the router, the selection
- * and the kernels of qmlp_moe_forward, with its roundings of the stages to fp16.
+ * Sums are fp32, the intermediate is rounded once, to fp16 times a power of two of the
+ * token and expert (to two fp16 for an fp32 out), and out once: values have fp32's range
+ * up to out's type. A token's result does not depend on the others of the call. Up to 16
+ * tokens whose x fits in shared memory (2 K bytes a token) run as one kernel; more run
+ * the router, the selection and the kernels of qmlp_moe_forward, without that entry
+ * point's roundings of the stages to fp16.
  */
 typedef enum { QMLP_SCORE_SOFTMAX = 1, QMLP_SCORE_SIGMOID = 2 } qmlp_score;
 
@@ -729,8 +730,9 @@ typedef struct qmlp_moe_layer_s qmlp_moe_layer_t;
 
 /* Make a layer over the handle's banks (which must outlive it and whose workspace
  * for more than 16 tokens it shares: calls on both go on one stream at a time).
- * Reserves max_tokens on the handle (qmlp_moe_reserve and its limits), copies the
- * router. E <= 1024. Synchronizes `stream`.
+ * Reserves max_tokens on the handle (qmlp_moe_reserve and its limits; with more than
+ * eight selected and shared experts a token a larger workspace, 4 bytes for each of
+ * them and each of K + I values), copies the router. E <= 1024. Synchronizes `stream`.
  * Errors: INVALID_ARG, SHAPE, OOM, CUDA. */
 qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const qmlp_moe_layer_desc* desc,
                                   qmlp_stream_t stream);

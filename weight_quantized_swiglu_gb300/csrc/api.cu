@@ -833,7 +833,7 @@ qmlp_status qmlp_moe_create(qmlp_moe_t** out, const qmlp_moe_desc* d, qmlp_strea
     *out = nullptr;
     if (!d || !d->w13 || !d->w13_meta || !d->w2 || !d->w2_meta) return QMLP_ERR_INVALID_ARG;
     if (d->meta != QMLP_META_3B && d->meta != QMLP_META_4B) return QMLP_ERR_INVALID_ARG;
-    if (d->E < 1 || d->K < 64 || d->K > 16384 || d->K % 64 || d->I < 32 || d->I > 1024 || d->I % 32)
+    if (d->E < 1 || d->K < 64 || d->K > 16384 || d->K % 64 || d->I < 32 || d->I > kMoeMaxI || d->I % 32)
         return QMLP_ERR_SHAPE;
     int dev = 0, sms = 0;
     qmlp_status st = check_device(&dev, &sms);
@@ -958,18 +958,18 @@ qmlp_status qmlp_moe_debug_stages(qmlp_moe_t* h, const void* x, qmlp_dtype xdt, 
     return moe_run(h, x, xdt, ids, rw, topk, out, gu, act, y, stream);
 }
 
-qmlp_status qmlp_moe_reserve(qmlp_moe_t* h, int max_tokens, qmlp_stream_t stream) {
-    if (!h) return QMLP_ERR_INVALID_ARG;
+extern "C++" qmlp_status moe_reserve(qmlp_moe_s* h, int max_tokens, size_t bytes, cudaStream_t s) {
     if (max_tokens < 1 || max_tokens > (1 << 20)) return QMLP_ERR_SHAPE;
-    if (max_tokens <= h->max_tokens) return QMLP_OK;
+    if (max_tokens <= h->max_tokens && bytes <= h->g_bytes) return QMLP_OK;
     if (h->K > kMoeGroupedMaxK || h->E > kMoeGroupedMaxE) return QMLP_ERR_SHAPE;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    max_tokens = std::max(max_tokens, h->max_tokens);
+    bytes = std::max(bytes, h->g_bytes);
     if (cudaStreamSynchronize(s) != cudaSuccess) return QMLP_ERR_CUDA;
     const size_t routes = (size_t)max_tokens * 16;
     void *act = nullptr, *y = nullptr, *rl = nullptr, *gr = nullptr, *ng = nullptr;
     cudaError_t e;
-    if ((e = h->mem.alloc(&act, routes * h->I * sizeof(__half))) != cudaSuccess ||
-        (e = h->mem.alloc(&y, routes * h->K * sizeof(__half))) != cudaSuccess ||
+    if ((e = h->mem.alloc(&act, max_tokens * bytes * h->I)) != cudaSuccess ||
+        (e = h->mem.alloc(&y, max_tokens * bytes * h->K)) != cudaSuccess ||
         (e = h->mem.alloc(&rl, routes * sizeof(int))) != cudaSuccess ||
         (e = h->mem.alloc(&gr, moe_grouped_max_groups((int)routes, h->E) * sizeof(int4))) != cudaSuccess ||
         (e = h->mem.alloc(&ng, 16)) != cudaSuccess) {
@@ -983,8 +983,9 @@ qmlp_status qmlp_moe_reserve(qmlp_moe_t* h, int max_tokens, qmlp_stream_t stream
         return from_cuda(e);
     }
     // the previous (smaller) workspace stays owned by the handle until destroy
-    h->g_act = static_cast<__half*>(act);
-    h->g_y = static_cast<__half*>(y);
+    h->g_act = act;
+    h->g_y = y;
+    h->g_bytes = bytes;
     h->g_route = static_cast<int*>(rl);
     h->g_groups = static_cast<int4*>(gr);
     h->g_ngroups = static_cast<int*>(ng);
@@ -992,8 +993,13 @@ qmlp_status qmlp_moe_reserve(qmlp_moe_t* h, int max_tokens, qmlp_stream_t stream
     return QMLP_OK;
 }
 
+qmlp_status qmlp_moe_reserve(qmlp_moe_t* h, int max_tokens, qmlp_stream_t stream) {
+    if (!h) return QMLP_ERR_INVALID_ARG;
+    return moe_reserve(h, max_tokens, h->g_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
 extern "C++" cudaError_t moe_grouped(qmlp_moe_s* h, const void* x, bool x_bf16, const int32_t* ids, const float* rw, int topk,
-                                     int M, void* out, int odt, cudaStream_t s) {
+                                     int M, void* out, int odt, int* amax, cudaStream_t s) {
     MoeGroupedLaunch L;
     L.num_sms = h->num_sms;
     L.E = h->E;
@@ -1012,8 +1018,15 @@ extern "C++" cudaError_t moe_grouped(qmlp_moe_s* h, const void* x, bool x_bf16, 
     L.rw = rw;
     L.out = out;
     L.odt = odt;
-    L.act_ws = h->g_act;
-    L.y_ws = h->g_y;
+    if (amax) {
+        if (h->g_bytes < (size_t)topk * 4) return cudaErrorInvalidValue;
+        L.act32 = static_cast<float*>(h->g_act);
+        L.y32 = static_cast<float*>(h->g_y);
+        L.amax = amax;
+    } else {
+        L.act_ws = static_cast<__half*>(h->g_act);
+        L.y_ws = static_cast<__half*>(h->g_y);
+    }
     L.route_list = h->g_route;
     L.groups = h->g_groups;
     L.n_groups = h->g_ngroups;
@@ -1031,8 +1044,8 @@ qmlp_status qmlp_moe_forward(qmlp_moe_t* h, const void* x, qmlp_dtype xdt, const
     const size_t xb = (size_t)M * h->K * 2, rb = (size_t)M * topk * 4;
     if (overlaps(out, xb, x, xb) || overlaps(out, xb, ids, rb) || overlaps(out, xb, rw, rb)) return QMLP_ERR_ALIAS;
     if (fault("launch")) return QMLP_ERR_CUDA;
-    return moe_grouped(h, x, xdt == QMLP_DT_BF16, ids, rw, topk, M, out, 2, reinterpret_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
+    return moe_grouped(h, x, xdt == QMLP_DT_BF16, ids, rw, topk, M, out, 2, nullptr,
+                       reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? QMLP_OK
                : QMLP_ERR_CUDA;
 }

@@ -427,7 +427,7 @@ qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const
             return QMLP_ERR_SHAPE;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
         if (d->max_tokens > 1) {
-            const qmlp_status st = qmlp_moe_reserve(moe, d->max_tokens, stream);
+            const qmlp_status st = moe_reserve(moe, d->max_tokens, std::max<size_t>(moe->g_bytes, 4 * (size_t)nsel), s);
             if (st != QMLP_OK) return st;
         }
         qmlp_moe_layer_t* h = new qmlp_moe_layer_t();
@@ -484,7 +484,7 @@ qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const
         a.ids = static_cast<int32_t*>(make(rows * nsel * 4, nullptr));
         a.weights = static_cast<float*>(make(rows * nsel * 4, nullptr));
         a.act = static_cast<float*>(make(a.act_elems * 4, nullptr));
-        a.amax = static_cast<int*>(make(few * 4, nullptr));
+        a.amax = static_cast<int*>(make(rows * nsel * 4, nullptr));
         a.act16_elems = a.act_elems / 8 * 2;  // (twice: what rounding to fp16 leaves)
         a.act16 = static_cast<uint4*>(make(a.act16_elems * 16, nullptr));
         uint8_t* words = static_cast<uint8_t*>(make(16, nullptr));
@@ -536,7 +536,7 @@ qmlp_status qmlp_moe_layer_forward(qmlp_moe_layer_t* h, const void* x, qmlp_dtyp
         return from_cuda(launch_moe_layer_few(a, h->moe->meta, h->moe->num_sms, s));
     cudaError_t e = launch_moe_router(a, s);
     if (e == cudaSuccess)
-        e = moe_grouped(h->moe, x, a.x_bf16, a.ids, a.weights, a.topk + a.S, M, out, a.odt, s);
+        e = moe_grouped(h->moe, x, a.x_bf16, a.ids, a.weights, a.topk + a.S, M, out, a.odt, a.amax, s);
     return from_cuda(e);
 }
 

@@ -111,6 +111,9 @@ QMLP_DEV int prescale_exponent(float maxabs) {
     const int e = b ? b - 126 : (32 - __clz(bits)) - 149;
     return 15 - e;
 }
+// The exponent that a row of fp32 values is scaled by before it is rounded to fp16, from
+// the bits of its largest one; both 2^e and 2^-e are normal fp32 numbers.
+QMLP_DEV int act_exponent(int bits) { return max(-113, min(126, prescale_exponent(__int_as_float(bits)))); }
 
 // ---------------------------------------------------------------------------
 // mbarrier + bulk-async (TMA) copies

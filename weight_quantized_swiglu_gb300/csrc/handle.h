@@ -107,20 +107,25 @@ struct qmlp_moe_s {
     uint8_t *w13 = nullptr, *w13_meta = nullptr, *w2 = nullptr, *w2_meta = nullptr;
     __half* act_ws = nullptr;
     int* err = nullptr;
-    // multi-token workspace (qmlp_moe_reserve): routes = max_tokens * 16
+    // multi-token workspace (moe_reserve): routes = max_tokens * 16
     int max_tokens = 1;
-    __half* g_act = nullptr;   // [routes, I]
-    __half* g_y = nullptr;     // [routes, K]
+    size_t g_bytes = 16 * sizeof(__half);  // of a token and column in the two below
+    void* g_act = nullptr;     // fp16 [routes, I], or fewer routes in fp32
+    void* g_y = nullptr;       // fp16 [routes, K], or fewer routes in fp32
     int* g_route = nullptr;    // [routes]
     int4* g_groups = nullptr;  // [moe_grouped_max_groups(routes, E)]
     int* g_ngroups = nullptr;
     qmlp::Owner mem;
 };
 
-// The grouped routed experts on M tokens (reserved for); odt: type of out (0 fp32,
-// 1 bf16, 2 fp16).
+// Makes the workspace of calls of max_tokens tokens, with `bytes` (of all its routes)
+// for a token and column, where the handle does not have it.
+qmlp_status moe_reserve(qmlp_moe_s* h, int max_tokens, size_t bytes, cudaStream_t s);
+// The grouped routed experts on M tokens (reserved for). amax null: the stages in fp16,
+// out too. Else [M, topk] zeros: the stages in fp32 and scaled (reserved with 4 topk
+// bytes or more), out of type odt (0 fp32, 1 bf16, 2 fp16).
 cudaError_t moe_grouped(qmlp_moe_s* h, const void* x, bool x_bf16, const int32_t* ids, const float* rw, int topk, int M,
-                        void* out, int odt, cudaStream_t s);
+                        void* out, int odt, int* amax, cudaStream_t s);
 
 struct qmlp_s {
     int fmt = 0, K = 0, I = 0, max_M = 0, device = 0, num_sms = 0;

@@ -280,6 +280,7 @@ struct MoeLaunch {
 cudaError_t launch_moe(const MoeLaunch& L, int num_sms, cudaStream_t s);
 
 // M tokens, routes grouped by expert (see moe_grouped.cu).
+constexpr int kMoeMaxI = 1024;         // of a routed-expert handle
 constexpr int kMoeGroupedMaxK = 8192;  // x of a group's 8 tokens is staged in shared memory
 constexpr int kMoeGroupedMaxE = 8192;  // the routing CTA keeps 4 ints per expert in shared memory
 struct MoeGroupedLaunch {
@@ -294,9 +295,14 @@ struct MoeGroupedLaunch {
     const int32_t* ids;            // [M, topk]
     const float* rw;               // [M, topk]
     void* out;                     // [M, K]
-    int odt = 2;                   // type of out: 0 fp32, 1 bf16, 2 fp16
-    __half* act_ws;                // [>= M*topk, I]
-    __half* y_ws;                  // [>= M*topk, K]
+    int odt = 2;                   // type of out: 0 fp32, 1 bf16, 2 fp16 (without act32: 2)
+    __half* act_ws = nullptr;      // [>= M*topk, I]
+    __half* y_ws = nullptr;        // [>= M*topk, K]
+    // instead, stages that are not limited to fp16's range (the mixture-of-experts
+    // layer): the same in fp32, and [>= M*topk] zeros
+    float* act32 = nullptr;
+    float* y32 = nullptr;
+    int* amax = nullptr;
     int* route_list;               // [>= M*topk]
     int4* groups;                  // [>= moe_grouped_max_groups(M*topk, E)]
     int* n_groups;                 // one int
@@ -456,7 +462,7 @@ struct MoeLayerArgs {
     int32_t* ids = nullptr;         // more tokens: [M][topk + S]
     float* weights = nullptr;
     float* act = nullptr;           // few tokens: [M (topk + S)][I]
-    int* amax = nullptr;            // [M (topk + S)]: bits of the largest |act|
+    int* amax = nullptr;            // [max_tokens (topk + S)]: bits of the largest |act|
     uint4* act16 = nullptr;         // act in fp16, in the order of the products
     size_t act16_elems = 0;
     unsigned long long* ticket = nullptr;

@@ -35,6 +35,14 @@
 //  * moe_combine_kernel: one thread per (token, 8 output elements, one
 //    16-byte load per route) adds the token's valid routes in router order
 //    (fmaf, fp32), like the one-token W2 stage.
+//  * For the mixture-of-experts layer (Stage kScaled) nothing between x and
+//    out is limited to fp16's range: g, u, act and y are fp32, and W2's kernel
+//    takes act to fp16 times a power of two of the route, whose largest |act|
+//    W13's kernel has left in memory -- one rounding, 2^-11 of a value at most,
+//    as in the layer's one-kernel form. For an fp32 out (kScaledLo) what that
+//    rounding leaves is a second fp16 operand, and the MMAs' accumulators are
+//    emptied into fp32 sums every eight of them (an MMA cuts off what passes
+//    its last bit). Costs act's and y's bytes twice.
 //  * All four are chained with programmatic dependent launch; a grid sized
 //    for the worst-case group count exits early past the real count.
 #include <algorithm>
@@ -51,6 +59,7 @@ constexpr int kGG2 = 10;   // k16 groups a W2 warp loads at once
 constexpr int kCols = 8;   // routes per MMA (n8); a group holds 8 or 16 routes (NC), 16 as two MMAs per A fragment
 constexpr int kWideMaxK = 4096;  // 16-route groups: x of 16 tokens staged in shared memory
 constexpr int kRouteThreads = 1024;
+enum Stage { kHalf = 0, kScaled = 1, kScaledLo = 2 };  // roundings of the stages, see above
 constexpr int kMaxCtasPerGroup = 5;  // CTAs per group (each loops over its share of the row octets / 256-row blocks)
 
 struct GArgs {
@@ -65,10 +74,13 @@ struct GArgs {
     int meta_al4;
     const int32_t* ids;  // [M, topk]
     const float* rw;     // [M, topk]
-    void* out;           // [M, K], fp16 or as odt says
+    void* out;           // [M, K], fp16; kScaled, kScaledLo: as odt says
     int odt;             // 0 fp32, 1 bf16, 2 fp16
     __half* act_ws;      // [M * topk, I]
     __half* y_ws;        // [M * topk, K]
+    float* act32;        // kScaled, kScaledLo: the same in fp32
+    float* y32;
+    int* amax;           // and [M * topk]: bits of the largest |act|, zero before
     int* route_list;     // [M * topk]: route indices sorted by expert
     int4* groups;        // {expert, first position in route_list, count, 0}
     int* n_groups;
@@ -118,6 +130,12 @@ QMLP_DEV uint32_t gawq_pair(uint32_t w, uint32_t sel, uint32_t s2, uint32_t b2) 
     return ghfma2(q, s2, b2);
 }
 QMLP_DEV uint32_t gpair_selector(int t) { return (uint32_t)t | (4u << 4) | ((uint32_t)t << 8) | (4u << 12); }
+
+// MMA accumulators to sums of their own.
+QMLP_DEV void empty(float (&d)[4], float (&sum)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) sum[q] += d[q], d[q] = 0.0f;
+}
 
 // ---------------------------------------------------------------------------
 // routing: valid routes sorted by expert, groups of <= 8
@@ -201,14 +219,15 @@ __global__ void __launch_bounds__(kRouteThreads) moe_route_kernel(const GArgs a)
 // ---------------------------------------------------------------------------
 // W13 + SwiGLU for a group of routes sharing one expert
 // ---------------------------------------------------------------------------
-template <int MB, int NC>
-__global__ void __launch_bounds__(kGW13 * 32, 3) moe_w13_grouped_kernel(const GArgs a) {
+template <int MB, int NC, int ST>
+__global__ void __launch_bounds__(kGW13 * 32, ST == kScaledLo ? 2 : 3) moe_w13_grouped_kernel(const GArgs a) {
     extern __shared__ __align__(16) uint32_t xs[];  // [NC][K/2 + 4] fp16 pairs (padded: no bank conflicts)
     __shared__ float part[kGW13][16][NC];
     __shared__ int s_route[NC];
     __shared__ int s_max[NC];
     __shared__ int s_sig[NC];
     __shared__ int s_tok[NC];  // slot's token, -1 past the group's routes
+    __shared__ int s_act[ST == kHalf ? 1 : NC];  // bits of the largest |act| of this CTA's rows
     pdl_wait();
     pdl_launch_dependents();
     if ((int)blockIdx.x >= *a.n_groups) return;
@@ -278,6 +297,7 @@ __global__ void __launch_bounds__(kGW13 * 32, 3) moe_w13_grouped_kernel(const GA
         s_route[threadIdx.x] = r;
         s_tok[threadIdx.x] = r >= 0 ? r / a.topk : -1;
         s_max[threadIdx.x] = 0;
+        if constexpr (ST != kHalf) s_act[threadIdx.x] = 0;
     }
     __syncthreads();
     const uint32_t* xin = reinterpret_cast<const uint32_t*>(a.x);
@@ -341,6 +361,7 @@ __global__ void __launch_bounds__(kGW13 * 32, 3) moe_w13_grouped_kernel(const GA
     for (; tp < ntp; tp += gridDim.y) {
         float d[4] = {0.f, 0.f, 0.f, 0.f};
         float d1[4] = {0.f, 0.f, 0.f, 0.f};
+        float sum[4] = {0.f, 0.f, 0.f, 0.f}, sum1[4] = {0.f, 0.f, 0.f, 0.f};  // kScaledLo
         for (int cb = c0; cb < c1; cb += kGC13) {
             if (cb != c0) load_batch(cb, tp);
 #pragma unroll
@@ -368,6 +389,14 @@ __global__ void __launch_bounds__(kGW13 * 32, 3) moe_w13_grouped_kernel(const GA
                     }
                 }
             }
+            if constexpr (ST == kScaledLo) {  // four MMAs
+                empty(d, sum);
+                if (two) empty(d1, sum1);
+            }
+        }
+        if constexpr (ST == kScaledLo) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[q] = sum[q], d1[q] = sum1[q];
         }
         // C fragment: (row g, cols 2t, 2t+1) and (row g+8, the same cols)
         part[warp][g][2 * t] = d[0];
@@ -395,23 +424,36 @@ __global__ void __launch_bounds__(kGW13 * 32, 3) moe_w13_grouped_kernel(const GA
                     hu += part[w][8 + j][c];
                 }
                 const int sg = s_sig[c];
-                const __half gh = __float2half_rn(scalbnf(hg, -sg)), uh = __float2half_rn(scalbnf(hu, -sg));
-                if (QMLP_INB((size_t)s_route[c] * a.I + 8 * tp + j, (size_t)a.M * a.topk * a.I, 45))
-                    a.act_ws[(size_t)s_route[c] * a.I + 8 * tp + j] =
-                        __float2half_rn(silu_f32(__half2float(gh)) * __half2float(uh));
+                const bool in = QMLP_INB((size_t)s_route[c] * a.I + 8 * tp + j, (size_t)a.M * a.topk * a.I, 45);
+                if constexpr (ST == kHalf) {
+                    const __half gh = __float2half_rn(scalbnf(hg, -sg)), uh = __float2half_rn(scalbnf(hu, -sg));
+                    if (in)
+                        a.act_ws[(size_t)s_route[c] * a.I + 8 * tp + j] =
+                            __float2half_rn(silu_f32(__half2float(gh)) * __half2float(uh));
+                } else {
+                    const float v = silu_f32(scalbnf(hg, -sg)) * scalbnf(hu, -sg);
+                    if (in) a.act32[(size_t)s_route[c] * a.I + 8 * tp + j] = v;
+                    atomicMax(&s_act[c], __float_as_int(fabsf(v)));  // (a maximum: any order)
+                }
             }
         }
         __syncthreads();  // part is rewritten by the next octet
     }
+    if constexpr (ST != kHalf) {
+        if ((int)threadIdx.x < cnt && QMLP_INB(s_route[threadIdx.x], a.M * a.topk, 45))
+            atomicMax(a.amax + s_route[threadIdx.x], s_act[threadIdx.x]);
+    }
 }
 
 // ---------------------------------------------------------------------------
-// W2 for a group of routes sharing one expert -> y (fp16)
+// W2 for a group of routes sharing one expert -> y (fp16; kScaled: fp32)
 // ---------------------------------------------------------------------------
-template <int MB, int NC>
+template <int MB, int NC, int ST>
 __global__ void __launch_bounds__(16 * 32) moe_w2_grouped_kernel(const GArgs a) {
-    extern __shared__ __align__(16) uint32_t acts[];  // [NC][I/2 + 4]
+    constexpr bool LO = ST == kScaledLo;
+    extern __shared__ __align__(16) uint32_t acts[];  // [NC][I/2 + 4]; LO: and what their rounding leaves
     __shared__ int s_route[NC];
+    __shared__ int s_exp[ST == kHalf ? 1 : NC];  // the routes' exponents
     pdl_wait();
     pdl_launch_dependents();
     if ((int)blockIdx.x >= *a.n_groups) return;
@@ -421,9 +463,42 @@ __global__ void __launch_bounds__(16 * 32) moe_w2_grouped_kernel(const GArgs a) 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int astride = a.I / 2 + 4;
     const bool two = NC == 16 && cnt > kCols;  // two MMA column sets on the same A fragments
-    if (threadIdx.x < NC) s_route[threadIdx.x] = threadIdx.x < cnt ? a.route_list[grp.y + threadIdx.x] : -1;
+    if (threadIdx.x < NC) {
+        const int r = threadIdx.x < cnt ? a.route_list[grp.y + threadIdx.x] : -1;
+        s_route[threadIdx.x] = r;
+        if constexpr (ST != kHalf)
+            s_exp[threadIdx.x] = r >= 0 && QMLP_INB(r, a.M * a.topk, 46) ? act_exponent(a.amax[r]) : 0;
+    }
     __syncthreads();
-    {
+    if constexpr (ST != kHalf) {
+        // the same in fp32, to fp16 times a power of two of the route
+        const int ih = a.I / 2, ns = two ? 2 * kCols : kCols;
+        const float2* act2 = reinterpret_cast<const float2*>(a.act32);
+        for (int k2 = threadIdx.x; k2 < ih; k2 += blockDim.x) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < ns; c0 += kCols) {
+                float2 v[kCols];
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    const int r = s_route[c0 + c];
+                    v[c] = r >= 0 && QMLP_INB((size_t)r * ih + k2, (size_t)a.M * a.topk * ih, 46) ? act2[(size_t)r * ih + k2]
+                                                                                              : make_float2(0.0f, 0.0f);
+                }
+#pragma unroll
+                for (int c = 0; c < kCols; ++c) {
+                    const float up = __int_as_float((127 + s_exp[c0 + c]) << 23);
+                    const float2 w = make_float2(v[c].x * up, v[c].y * up);
+                    const __half2 h = __floats2half2_rn(w.x, w.y);
+                    acts[(c0 + c) * astride + k2] = *reinterpret_cast<const uint32_t*>(&h);
+                    if (LO) {  // (nothing of what is not finite)
+                        const float2 f = __half22float2(h);
+                        const __half2 l = __floats2half2_rn(isfinite(f.x) ? w.x - f.x : 0.0f, isfinite(f.y) ? w.y - f.y : 0.0f);
+                        acts[(NC + c0 + c) * astride + k2] = *reinterpret_cast<const uint32_t*>(&l);
+                    }
+                }
+            }
+        }
+    } else {
         // the group's act rows: a thread takes pairs k2 = threadIdx.x + n * blockDim.x
         // of every slot, eight slots' loads in flight together
         const int ih = a.I / 2;
@@ -463,6 +538,7 @@ __global__ void __launch_bounds__(16 * 32) moe_w2_grouped_kernel(const GArgs a) 
         continue;
     float d[4] = {0.f, 0.f, 0.f, 0.f};
     float d1[4] = {0.f, 0.f, 0.f, 0.f};
+    float sum[4] = {0.f, 0.f, 0.f, 0.f}, sum1[4] = {0.f, 0.f, 0.f, 0.f};  // LO
     for (int gb = 0; gb < ng; gb += kGG2) {
         uint32_t cs[kGG2 / 2][2];  // this lane's 4 bytes of unit (gb/2 + i): k16 groups gb+2i, gb+2i+1
         uint32_t mw[kGG2 / 2][2];
@@ -493,17 +569,34 @@ __global__ void __launch_bounds__(16 * 32) moe_w2_grouped_kernel(const GArgs a) 
                 const uint32_t a2 = gawq_pair(cs[i / 2][0], sb, s0, b0), a3 = gawq_pair(cs[i / 2][1], sb, s8, b8);
                 mma_f16_16816(d, a0, a1, a2, a3, xcol[8 * j + t], xcol[8 * j + 4 + t]);
                 if (two) mma_f16_16816(d1, a0, a1, a2, a3, xcol1[8 * j + t], xcol1[8 * j + 4 + t]);
+                if constexpr (LO) {
+                    const uint32_t *lcol = xcol + NC * astride, *lcol1 = xcol1 + NC * astride;
+                    mma_f16_16816(d, a0, a1, a2, a3, lcol[8 * j + t], lcol[8 * j + 4 + t]);
+                    if (two) mma_f16_16816(d1, a0, a1, a2, a3, lcol1[8 * j + t], lcol1[8 * j + 4 + t]);
+                    if ((j & 3) == 3 || j == ng - 1) {  // eight MMAs
+                        empty(d, sum);
+                        if (two) empty(d1, sum1);
+                    }
+                }
             }
         }
+    }
+    if constexpr (LO) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) d[q] = sum[q], d1[q] = sum1[q];
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int c = 2 * t + (q & 1), row = n0 + g + 8 * (q >> 1);
         const size_t ycap = (size_t)a.M * a.topk * a.K;
-        if (c < cnt && QMLP_INB((size_t)s_route[c] * a.K + row, ycap, 48))
-            a.y_ws[(size_t)s_route[c] * a.K + row] = __float2half_rn(d[q]);
-        if (two && kCols + c < cnt && QMLP_INB((size_t)s_route[kCols + c] * a.K + row, ycap, 48))
-            a.y_ws[(size_t)s_route[kCols + c] * a.K + row] = __float2half_rn(d1[q]);
+        auto put = [&](int col, float v) {
+            const size_t at = (size_t)s_route[col] * a.K + row;
+            if (!QMLP_INB(at, ycap, 48)) return;
+            if constexpr (ST == kHalf) a.y_ws[at] = __float2half_rn(v);
+            else a.y32[at] = v * __int_as_float((127 - s_exp[col]) << 23);
+        };
+        if (c < cnt) put(c, d[q]);
+        if (two && kCols + c < cnt) put(kCols + c, d1[q]);
     }
     }
 }
@@ -545,25 +638,59 @@ __global__ void __launch_bounds__(kCombThr) moe_combine_kernel(const GArgs a) {
             for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[r], __half2float(h[e]), acc[e]);
         }
     }
+    uint4 o;
+    __half* oh = reinterpret_cast<__half*>(&o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) oh[e] = __float2half_rn(acc[e]);
+    if (QMLP_INB((size_t)tok * a.K + n + 7, (size_t)a.M * a.K, 49))
+        *reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + (size_t)tok * a.K + n) = o;
+}
+
+// The same of y in fp32, four elements a thread.
+__global__ void __launch_bounds__(kCombThr) moe_combine_scaled_kernel(const GArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tok = blockIdx.x, n = 4 * (kCombThr * blockIdx.y + threadIdx.x);
+    if (n >= a.K) return;
+    float w[16];
+    float4 y[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        if (r < a.topk) {
+            const int i = tok * a.topk + r, id = a.ids[i];
+            // (a route without an expert has no y: nothing is read or added for it)
+            const bool in = id >= 0 && id < a.E && QMLP_INB((size_t)i * a.K + n + 3, (size_t)a.M * a.topk * a.K, 49);
+            w[r] = in ? a.rw[i] : 0.0f;
+            y[r] = in ? *reinterpret_cast<const float4*>(a.y32 + (size_t)i * a.K + n) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        }
+    }
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        if (r < a.topk) {
+            acc[0] = fmaf(w[r], y[r].x, acc[0]);
+            acc[1] = fmaf(w[r], y[r].y, acc[1]);
+            acc[2] = fmaf(w[r], y[r].z, acc[2]);
+            acc[3] = fmaf(w[r], y[r].w, acc[3]);
+        }
+    }
     const size_t at = (size_t)tok * a.K + n;
-    if (!QMLP_INB(at + 7, (size_t)a.M * a.K, 49)) return;
+    if (!QMLP_INB(at + 3, (size_t)a.M * a.K, 49)) return;
     if (a.odt == 0) {
-        float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
-        o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(acc[0], acc[1], acc[2], acc[3]);
         return;
     }
-    uint4 o;
+    uint2 o;
     if (a.odt == 1) {
         __nv_bfloat16* ob = reinterpret_cast<__nv_bfloat16*>(&o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ob[e] = __float2bfloat16_rn(acc[e]);
+        for (int e = 0; e < 4; ++e) ob[e] = __float2bfloat16_rn(acc[e]);
     } else {
         __half* oh = reinterpret_cast<__half*>(&o);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) oh[e] = __float2half_rn(acc[e]);
+        for (int e = 0; e < 4; ++e) oh[e] = __float2half_rn(acc[e]);
     }
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = o;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = o;
 }
 
 cudaLaunchConfig_t pdl_cfg(dim3 grid, dim3 block, size_t smem, cudaStream_t s, cudaLaunchAttribute* at) {
@@ -579,18 +706,22 @@ cudaLaunchConfig_t pdl_cfg(dim3 grid, dim3 block, size_t smem, cudaStream_t s, c
     return c;
 }
 
-template <int MB, int NC>
-cudaError_t launch_grouped_mb(const GArgs& a, int gmax, int cpg, cudaStream_t s) {
+template <int MB, int NC, int ST>
+cudaError_t launch_grouped_st(const GArgs& a, int gmax, int cpg, cudaStream_t s) {
     const size_t rsmem = (size_t)4 * a.E * sizeof(int);
     const size_t xsmem = (size_t)NC * (a.K / 2 + 4) * 4;
-    const size_t asmem = (size_t)NC * (a.I / 2 + 4) * 4;
+    constexpr int planes = ST == kScaledLo ? 2 : 1;
+    const size_t asmem = (size_t)planes * NC * (a.I / 2 + 4) * 4;
     static bool attr = false;
     if (!attr) {
         cudaError_t e = cudaFuncSetAttribute(moe_route_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kMoeGroupedMaxE * 4 * (int)sizeof(int));
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(moe_w13_grouped_kernel<MB, NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(moe_w13_grouped_kernel<MB, NC, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      NC * ((NC == kCols ? kMoeGroupedMaxK : kWideMaxK) / 2 + 4) * 4);
+        if (e == cudaSuccess && planes > 1)  // (one plane of I <= 1024 fits without)
+            e = cudaFuncSetAttribute(moe_w2_grouped_kernel<MB, NC, ST>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     planes * NC * (kMoeMaxI / 2 + 4) * 4);
         if (e != cudaSuccess) return e;
         attr = true;
     }
@@ -599,11 +730,17 @@ cudaError_t launch_grouped_mb(const GArgs& a, int gmax, int cpg, cudaStream_t s)
     cudaError_t e = cudaLaunchKernelEx(&c, moe_route_kernel, a);
     if (e != cudaSuccess) return e;
     c = pdl_cfg(dim3(gmax, std::min(a.I / 8, cpg)), dim3(kGW13 * 32), xsmem, s, at);
-    if ((e = cudaLaunchKernelEx(&c, moe_w13_grouped_kernel<MB, NC>, a)) != cudaSuccess) return e;
+    if ((e = cudaLaunchKernelEx(&c, moe_w13_grouped_kernel<MB, NC, ST>, a)) != cudaSuccess) return e;
     c = pdl_cfg(dim3(gmax, std::min((a.K + 255) / 256, cpg)), dim3(16 * 32), asmem, s, at);
-    if ((e = cudaLaunchKernelEx(&c, moe_w2_grouped_kernel<MB, NC>, a)) != cudaSuccess) return e;
-    c = pdl_cfg(dim3(a.M, (a.K / 8 + kCombThr - 1) / kCombThr), dim3(kCombThr), 0, s, at);
-    return cudaLaunchKernelEx(&c, moe_combine_kernel, a);
+    if ((e = cudaLaunchKernelEx(&c, moe_w2_grouped_kernel<MB, NC, ST>, a)) != cudaSuccess) return e;
+    constexpr int per = ST == kHalf ? 8 : 4;
+    c = pdl_cfg(dim3(a.M, (a.K / per + kCombThr - 1) / kCombThr), dim3(kCombThr), 0, s, at);
+    return cudaLaunchKernelEx(&c, ST == kHalf ? moe_combine_kernel : moe_combine_scaled_kernel, a);
+}
+template <int MB, int NC>
+cudaError_t launch_grouped_mb(const GArgs& a, int gmax, int cpg, cudaStream_t s) {
+    if (!a.act32) return launch_grouped_st<MB, NC, kHalf>(a, gmax, cpg, s);
+    return a.odt == 0 ? launch_grouped_st<MB, NC, kScaledLo>(a, gmax, cpg, s) : launch_grouped_st<MB, NC, kScaled>(a, gmax, cpg, s);
 }
 
 }  // namespace
@@ -612,7 +749,8 @@ size_t moe_grouped_max_groups(int routes, int E) { return (size_t)routes / kCols
 
 cudaError_t launch_moe_grouped(const MoeGroupedLaunch& L, cudaStream_t s) {
     if (L.M < 1 || L.topk < 1 || L.topk > 16 || L.K % 64 || L.I % 32 || L.K > kMoeGroupedMaxK ||
-        L.E > kMoeGroupedMaxE || L.E < 1)
+        L.E > kMoeGroupedMaxE || L.E < 1 || L.I > kMoeMaxI || (L.act32 && (!L.y32 || !L.amax)) ||
+        (!L.act32 && (!L.act_ws || !L.y_ws || L.odt != 2)))
         return cudaErrorInvalidValue;
     GArgs a;
     a.E = L.E;
@@ -633,6 +771,9 @@ cudaError_t launch_moe_grouped(const MoeGroupedLaunch& L, cudaStream_t s) {
     a.odt = L.odt;
     a.act_ws = L.act_ws;
     a.y_ws = L.y_ws;
+    a.act32 = L.act32;
+    a.y32 = L.y32;
+    a.amax = L.amax;
     a.route_list = L.route_list;
     a.groups = L.groups;
     a.n_groups = L.n_groups;

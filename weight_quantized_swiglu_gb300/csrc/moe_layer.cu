@@ -37,7 +37,8 @@
 // the bank, 16 rows of W2 likewise. W2's first ones are on their way before the second
 // barrier. (Where the ring does not fit beside x, the warps load for themselves.)
 // More tokens: router and selection as two kernels, then the grouped kernels
-// (moe_grouped.cu) with the shared experts as further routes.
+// (moe_grouped.cu) with the shared experts as further routes, act in fp32 and scaled
+// as here.
 #include <algorithm>
 
 #include "common.cuh"
@@ -493,8 +494,6 @@ QMLP_DEV uint4 ldcg4_if(const uint4* p, bool on) {
         : "l"(p), "r"((uint32_t)on));
     return v;
 }
-// The exponent that a row of act is scaled by, from the bits of its largest value.
-QMLP_DEV int act_exponent(int bits) { return max(-113, min(126, prescale_exponent(__int_as_float(bits)))); }
 
 // act (fp32, rows of I) -> fp16 times the row's power of two, in the order of the
 // MMAs: piece (r I / 32 + unit) 4 + t, to `out` (shared or device memory), by threads
@@ -1107,6 +1106,7 @@ __global__ void __launch_bounds__(128) select_kernel(const MoeLayerArgs a) {
     if (lane < nsel) {
         a.ids[(size_t)m * nsel + lane] = se[w][lane];
         a.weights[(size_t)m * nsel + lane] = sw[w][lane];
+        a.amax[(size_t)m * nsel + lane] = 0;  // (W13's kernel takes maxima into it)
     }
     if (lane < a.topk) {
         if (a.ids_out) a.ids_out[(size_t)m * a.topk + lane] = se[w][lane];
