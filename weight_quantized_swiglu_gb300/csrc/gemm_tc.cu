@@ -265,6 +265,11 @@ QMLP_DEV void store16(__nv_bfloat16* dst, const uint32_t (&v)[8]) {
     reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
 }
 
+// What out holds and a second product on top. Where the first is not finite it is the
+// result: an infinite activation times what a weight's rounding left is infinite of
+// either sign, or NaN where that is zero.
+QMLP_DEV float joined(float h, float v) { return isfinite(h) ? h + v : h; }
+
 // kEpiOut: n values of row m from column col on, whole vectors where out has the
 // room and the alignment for them.
 template <int N>
@@ -279,14 +284,14 @@ QMLP_DEV void store_any(const Args& a, int m, int col, const float (&v)[N]) {
                 float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
                 if (a.onto) {
                     const float4 h = *reinterpret_cast<const float4*>(o + j);
-                    w.x += h.x, w.y += h.y, w.z += h.z, w.w += h.w;
+                    w = make_float4(joined(h.x, w.x), joined(h.y, w.y), joined(h.z, w.z), joined(h.w, w.w));
                 }
                 *reinterpret_cast<float4*>(o + j) = w;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (col + j < a.ncols) o[j] = a.onto ? o[j] + v[j] : v[j];
+                if (col + j < a.ncols) o[j] = a.onto ? joined(o[j], v[j]) : v[j];
         }
         return;
     }
