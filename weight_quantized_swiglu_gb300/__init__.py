@@ -936,30 +936,34 @@ class BlockNorm:
 
 class QuantLinear:
     """One projection y = x W^T + bias with 4-bit weights and group scales
-    (qmlp_linear_*): "nvfp4" (w u8 [N, K/2], scale E4M3 [N, K/16], global_scale) or
-    "int4" (w, scale fp16 [N, K/group], zero u8 [N, K/group]; group 32, 64 or 128).
-    The low nibble of a byte is the even k. bias: fp32 [N] or None. Arrays may be
-    numpy arrays (host) or torch CUDA tensors; they are copied at construction."""
+    (qmlp_linear_*): "nvfp4" (w u8 [N, K/2], scale E4M3 or its bytes [N, K/16],
+    global_scale) or "int4" (w, scale fp16 [N, K/group], zero u8 [N, K/group]; group 32,
+    64 or 128). The low nibble of a byte is the even k. bias: fp32 [N] or None. Arrays may
+    be numpy arrays (host) or torch CUDA tensors; they are copied at construction, and
+    another type or shape is refused (a bf16 scale has to be converted)."""
 
     def __init__(self, fmt, N, K, max_M, w, scale, zero=None, group=None, global_scale=1.0, bias=None, stream=None):
         if fmt not in ("nvfp4", "int4"):
             raise ValueError("QuantLinear: fmt is nvfp4 or int4")
         group = (16 if fmt == "nvfp4" else 128) if group is None else group
         self.N, self.K, self.max_M = N, K, max_M
-        cells = N * (K // group) if group > 0 else 0
-        want = {"w": (w, N * (K // 2)), "scale": (scale, cells * (1 if fmt == "nvfp4" else 2)), "zero": (zero, cells),
-                "bias": (bias, 4 * N)}
+        groups = K // group if group > 0 else 0
+        scales = ("uint8", "float8_e4m3fn") if fmt == "nvfp4" else ("float16",)
+        want = {"w": (w, (N, K // 2), ("uint8",)), "scale": (scale, (N, groups), scales),
+                "zero": (zero, (N, groups), ("uint8",)), "bias": (bias, (N,), ("float32",))}
         keep, ptr = [], {}
-        for n, (a, nbytes) in want.items():
+        for n, (a, shape, kinds) in want.items():
             ptr[n] = None
             if a is None:
                 continue
-            if isinstance(a, int):
+            if isinstance(a, int):  # a raw address: the caller's
                 ptr[n] = a
                 continue
-            size = a.nbytes if isinstance(a, np.ndarray) else a.numel() * a.element_size()
-            if size != nbytes or (not isinstance(a, np.ndarray) and not a.is_contiguous()):
-                raise ValueError(f"QuantLinear: {n} has to be contiguous, of {nbytes} bytes")
+            host = isinstance(a, np.ndarray)
+            kind = a.dtype.name if host else str(a.dtype).removeprefix("torch.")
+            if (kind not in kinds or tuple(a.shape) != shape or (host and not a.dtype.isnative) or
+                    (not host and not a.is_contiguous())):
+                raise ValueError(f"QuantLinear: {n} has to be a contiguous array of {' or '.join(kinds)}, {shape}")
             ptr[n], owner = _host_or_dev(a)
             keep.append(owner)
         self.h = qmlp_linear_create(
