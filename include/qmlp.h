@@ -730,9 +730,10 @@ typedef struct qmlp_moe_layer_s qmlp_moe_layer_t;
 
 /* Make a layer over the handle's banks (which must outlive it and whose workspace
  * for more than 16 tokens it shares: calls on both go on one stream at a time).
- * Reserves max_tokens on the handle (qmlp_moe_reserve and its limits; with more than
- * eight selected and shared experts a token a larger workspace, 4 bytes for each of
- * them and each of K + I values), copies the router. E <= 1024. Synchronizes `stream`.
+ * Reserves max_tokens on the handle (qmlp_moe_reserve; its limits, K <= 8192 among them,
+ * hold where not every call of up to max_tokens is the one kernel's, and with more than
+ * eight selected and shared experts a token the workspace is then larger: 4 bytes for each
+ * of them and each of K + I values). Copies the router. E <= 1024. Synchronizes `stream`.
  * Errors: INVALID_ARG, SHAPE, OOM, CUDA. */
 qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const qmlp_moe_layer_desc* desc,
                                   qmlp_stream_t stream);

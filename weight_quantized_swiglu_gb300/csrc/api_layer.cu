@@ -426,9 +426,14 @@ qmlp_status qmlp_moe_layer_create(qmlp_moe_layer_t** out, qmlp_moe_t* moe, const
             d->max_tokens < 1 || d->max_tokens > (1 << 20))
             return QMLP_ERR_SHAPE;
         cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+        // the grouped kernels' workspace; what it does not take is no fault where every
+        // number of tokens is the one kernel's
+        bool one = d->max_tokens <= kMoeLayerFew;
+        for (int m = 1; one && m <= d->max_tokens; ++m) one = moe_layer_few(m, moe->K, moe->I, E, d->shared, d->topk, moe->meta);
         if (d->max_tokens > 1) {
-            const qmlp_status st = moe_reserve(moe, d->max_tokens, std::max<size_t>(moe->g_bytes, 4 * (size_t)nsel), s);
-            if (st != QMLP_OK) return st;
+            const size_t bytes = one ? moe->g_bytes : std::max<size_t>(moe->g_bytes, 4 * (size_t)nsel);
+            const qmlp_status st = moe_reserve(moe, d->max_tokens, bytes, s);
+            if (st != QMLP_OK && !(one && st == QMLP_ERR_SHAPE)) return st;
         }
         qmlp_moe_layer_t* h = new qmlp_moe_layer_t();
         h->moe = moe;
