@@ -1,5 +1,6 @@
-"""Rows of more than 8192 values, which the one-kernel form of the mixture-of-experts
-layer alone takes."""
+"""Sizes at the ends of the mixture-of-experts layer's ranges: rows of more than 8192
+values, which the one-kernel form alone takes, and more tokens than eight times a grid's
+second dimension."""
 import pytest
 
 import test_gpu_moe_layer as base
@@ -28,4 +29,22 @@ def test_long_rows_of_too_many_tokens_are_refused(torch):  # noqa: F811
         with pytest.raises(q.QmlpError) as e:
             q.MoeLayer(moe, router, 2, max_tokens=tokens)
         assert e.value.status == 4
+    moe.close()
+
+
+def test_more_tokens_than_a_grids_second_dimension(torch):  # noqa: F811
+    E, K, M = 6, 64, 8 * 65535 + 9
+    moe = base.Bank(E, K, 32, 4, 3).handle()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    router = torch.randn((E, K), generator=g, device="cuda").bfloat16()
+    layer = q.MoeLayer(moe, router, 2, max_tokens=M)
+    x = torch.randn((M, K), generator=g, device="cuda").bfloat16()
+    out, ids = torch.empty((M, K), device="cuda"), torch.empty((M, 2), dtype=torch.int32, device="cuda")
+    layer.forward(x, out, ids=ids)
+    for at in (0, 4096, M // 2 // 8 * 8, M - 65):  # a token's result does not depend on the others
+        n = min(65, M - at)
+        part, pid = torch.empty((n, K), device="cuda"), torch.empty((n, 2), dtype=torch.int32, device="cuda")
+        layer.forward(x[at:at + n].contiguous(), part, ids=pid)
+        assert torch.equal(part, out[at:at + n]) and torch.equal(pid, ids[at:at + n])
+    layer.close()
     moe.close()

@@ -1080,10 +1080,10 @@ __global__ void __launch_bounds__(256) router_kernel(const MoeLayerArgs a) {
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ int s_max[16], s_sig[16];
     uint4* xsm = reinterpret_cast<uint4*>(sm);
-    const int m0 = blockIdx.y * 8, M = min(8, a.M - m0), rows = a.E + (a.sgate ? a.S : 0);
+    const int m0 = blockIdx.x * 8, M = min(8, a.M - m0), rows = a.E + (a.sgate ? a.S : 0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     stage_x(a, static_cast<const uint16_t*>(a.x) + (size_t)m0 * a.K, M, xsm, s_max, s_sig, 256, [] { __syncthreads(); });
-    const int tile = blockIdx.x * 8 + warp;
+    const int tile = blockIdx.y * 8 + warp;
     if (tile * 16 >= rows) return;
     float d[1][4];
     router_tile<1>(a, xsm, M, tile, 0, a.K / 32, 1, lane, d);
@@ -1212,7 +1212,8 @@ cudaError_t launch_moe_router(const MoeLayerArgs& a, cudaStream_t s) {
     static unsigned long done = 0;
     if (const cudaError_t e = smem_once(router_kernel, kSmemMax, done); e != cudaSuccess) return e;
     if (smem > kSmemMax) return cudaErrorInvalidValue;
-    router_kernel<<<dim3((unsigned)((tiles + 7) / 8), (unsigned)((a.M + 7) / 8)), 256, smem, s>>>(a);
+    // (tokens along x: a grid's second dimension ends at 65535)
+    router_kernel<<<dim3((unsigned)((a.M + 7) / 8), (unsigned)((tiles + 7) / 8)), 256, smem, s>>>(a);
     const cudaError_t e = cudaPeekAtLastError();
     if (e != cudaSuccess) return e;
     select_kernel<<<(unsigned)((a.M + 3) / 4), 128, 0, s>>>(a);
