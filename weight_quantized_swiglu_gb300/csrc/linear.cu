@@ -147,11 +147,17 @@ QMLP_DEV void e2m1x8(uint32_t w, __half2 sp, uint32_t (&p)[4]) {
 
 // One record times one tile of eight tokens. xb: this lane's x of the record in shared
 // memory, 16 bytes a pair of steps, `xs` apart. The steps go to two accumulators in
-// turn: a warp's MMAs would otherwise wait for one another.
-template <int G, bool ONE>
+// turn: a warp's MMAs would otherwise wait for one another. NVFP4's are all of the warp's
+// k, or (SUM, for an fp32 out) a record's, added in fp32: an MMA cuts off what passes its last
+// bit, and chains over k = 17408 were 6e-7 off (8 tokens of 17408 x 5120 take 17.4 us with
+// it, 16.7 without; one of 128000 x 5120 72 and 73).
+template <int G, bool ONE, bool SUM>
 QMLP_DEV void mma_record(const Frag<G>& f, uint32_t xb, uint32_t xs, float (&acc)[2][4]) {
     using R = Rec<G>;
     if constexpr (R::kNv) {
+        float sum[SUM ? 2 : 1][4];
+        float (&d0)[4] = SUM ? sum[0] : acc[0];
+        float (&d1)[4] = SUM ? sum[SUM ? 1 : 0] : acc[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // two steps: groups 2i and 2i + 1 of both rows
             uint32_t a[2][4];
@@ -162,9 +168,17 @@ QMLP_DEV void mma_record(const Frag<G>& f, uint32_t xb, uint32_t xs, float (&acc
                 e2m1x8(word_of(f.c[h], i), h2((i & 1) ? s23 : s01), a[h]);
             }
             const uint4 x = lds4(xb + i * xs);
-            mma_f16_16816(acc[0], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-            mma_f16_16816(acc[1], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+            if (SUM && i == 0) {
+                mma_f16_16816_zc(d0, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                mma_f16_16816_zc(d1, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+            } else {
+                mma_f16_16816(d0, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                mma_f16_16816(d1, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+            }
         }
+        if constexpr (SUM)
+#pragma unroll
+            for (int e = 0; e < 4; e += ONE ? 2 : 1) acc[0][e] += sum[0][e] + sum[1][e];
     } else {
 #pragma unroll
         for (int q = 0; q < R::kPer; ++q) {
@@ -408,7 +422,7 @@ constexpr int few_ctas() { return ONE ? 3 : 1; }
 // depend on anything before this launch, so they start at once), W warps consume
 // them. Shared memory: x, the ring, the warps' sums (two buffers: one barrier a group
 // is enough), this CTA's sums of a batch of groups where k is split.
-template <int G, bool ONE>
+template <int G, bool ONE, bool SUM>
 __global__ void __launch_bounds__((few_warps<ONE>() + 1) * 32, few_ctas<ONE>())
     linear_few_kernel(const LinearArgs a, const FewPlan P) {
     using R = Rec<G>;
@@ -562,7 +576,7 @@ __global__ void __launch_bounds__((few_warps<ONE>() + 1) * 32, few_ctas<ONE>())
                 load_frag<G>(f, at.slot + lane * 16, at.slot + 1024 + g * (R::kScales / 8),
                              at.slot + 1024 + R::kScales + g * (R::kZeros / 8));
             at.release_and_step(lane);
-            if (has) mma_record<G, ONE>(f, xb, xs, acc);
+            if (has) mma_record<G, ONE, SUM>(f, xb, xs, acc);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[0][e] += acc[1][e];
@@ -979,7 +993,7 @@ cudaLaunchConfig_t few_config(const FewPlan& P, int threads, size_t smem, cudaSt
     return cfg;
 }
 
-template <int G, bool ONE>
+template <int G, bool ONE, bool SUM>
 cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     constexpr int kC = ONE ? 1 : 8, W = few_warps<ONE>(), kStage = W * Rec<G>::kBytes, kCtas = few_ctas<ONE>();
     const int Kc = (a.K + kCh - 1) / kCh, Nt = (a.N + 15) / 16;
@@ -1024,10 +1038,10 @@ cudaError_t launch_few(const LinearArgs& a, int num_sms, cudaStream_t s) {
     const size_t fixed = x + red + group_own * P.batch;
     P.stages = (int)std::min<size_t>(kMaxStages, std::max<size_t>(2, (all - fixed) / kStage));
     static unsigned long done = 0;
-    if (const cudaError_t e = smem_once(linear_few_kernel<G, ONE>, kSmemMax, done); e != cudaSuccess) return e;
+    if (const cudaError_t e = smem_once(linear_few_kernel<G, ONE, SUM>, kSmemMax, done); e != cudaSuccess) return e;
     cudaLaunchAttribute at[2];
     const cudaLaunchConfig_t cfg = few_config(P, (W + 1) * 32, fixed + (size_t)P.stages * kStage, s, at);
-    return cudaLaunchKernelEx(&cfg, linear_few_kernel<G, ONE>, a, P);
+    return cudaLaunchKernelEx(&cfg, linear_few_kernel<G, ONE, SUM>, a, P);
 }
 
 template <int G, int NT, bool SUM>
@@ -1064,13 +1078,17 @@ cudaError_t launch_tiles(const LinearArgs& a, int num_sms, cudaStream_t s) {
     if (a.M <= 16) return launch_mid<G, 2, SUM>(a, num_sms, s);
     return a.M <= 32 ? launch_mid<G, 4, SUM>(a, num_sms, s) : launch_mid<G, 8, SUM>(a, num_sms, s);
 }
+template <int G, bool SUM>
+cudaError_t launch_sums(const LinearArgs& a, int num_sms, cudaStream_t s) {
+    if (a.M == 1) return launch_few<G, true, SUM>(a, num_sms, s);
+    if (a.M <= kLinearFew) return launch_few<G, false, SUM>(a, num_sms, s);
+    return launch_tiles<G, SUM>(a, num_sms, s);
+}
 template <int G>
 cudaError_t launch_g(const LinearArgs& a, int num_sms, cudaStream_t s) {
-    if (a.M == 1) return launch_few<G, true>(a, num_sms, s);
-    if (a.M <= kLinearFew) return launch_few<G, false>(a, num_sms, s);
     if (a.M > kLinearMid) return cudaErrorInvalidValue;  // (the GEMM's)
-    if (Rec<G>::kNv && a.odt == 0) return launch_tiles<G, Rec<G>::kNv>(a, num_sms, s);
-    return launch_tiles<G, false>(a, num_sms, s);
+    if (Rec<G>::kNv && a.odt == 0) return launch_sums<G, Rec<G>::kNv>(a, num_sms, s);
+    return launch_sums<G, false>(a, num_sms, s);
 }
 
 }  // namespace
