@@ -270,6 +270,13 @@ QMLP_DEV void store16(__nv_bfloat16* dst, const uint32_t (&v)[8]) {
 // either sign, or NaN where that is zero.
 QMLP_DEV float joined(float h, float v) { return isfinite(h) ? h + v : h; }
 
+// kEpiOut: a sum times 2^-sg and its row's factor. The power of two in two halves with the
+// factor between them: a token near the ends of bf16's range has a sum past fp32's that
+// the factor brings back.
+QMLP_DEV float out_value(float y, int sg, float f) {
+    return y * __int_as_float((127 - (sg >> 1)) << 23) * f * __int_as_float((127 - sg + (sg >> 1)) << 23);
+}
+
 // kEpiOut: n values of row m from column col on, whole vectors where out has the
 // room and the alignment for them.
 template <int N>
@@ -474,7 +481,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
                     const float4 f = factor4<FMT>(a.cs0, a.inv0, col + j);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        y[j + e] = y[j + e] * pw * f4_at(f, e);
+                        y[j + e] = out_value(y[j + e], sg, f4_at(f, e));
                         if (a.bias && col + j + e < a.ncols) y[j + e] += __ldg(a.bias + col + j + e);
                     }
                 }
@@ -1289,8 +1296,7 @@ __global__ void __launch_bounds__(256) tail_reduce_kernel(const Args a) {
     const int sg = a.sig ? a.sig[m] : 0;
     if (a.epi == kEpiOut) {
         if (n >= a.ncols) return;
-        const float pw = scalbnf(1.0f, -sg);
-        float v[4] = {s.x * pw * f.x, s.y * pw * f.y, s.z * pw * f.z, s.w * pw * f.w};
+        float v[4] = {out_value(s.x, sg, f.x), out_value(s.y, sg, f.y), out_value(s.z, sg, f.z), out_value(s.w, sg, f.w)};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (a.bias && n + e < a.ncols) v[e] += a.bias[n + e];

@@ -331,7 +331,7 @@ QMLP_DEV void store4(const LinearArgs& a, int m, int n, const float4& s, int sig
     const size_t at = (size_t)m * a.N + n;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        v[e] = v[e] * p0 * p1 * a.factor;
+        v[e] = v[e] * p0 * a.factor * p1;  // (a sum past fp32's range that the factor brings back)
         if (a.bias && n + e < a.N) v[e] += __ldg(a.bias + n + e);
     }
     if (n + 3 < a.N && (a.N & 3) == 0) {
