@@ -268,12 +268,24 @@ QMLP_DEV void select_tokens(const MoeLayerArgs& a, const float* lg, int M, int w
             if (lane == r) mine = l[e];
         }
     }
-    if (a.softmax && a.renorm && !a.bias) {  // (any shift will do: the largest selected logit)
+    // renormed, only the selected scores' ratios count: what they share goes before it
+    // underflows. Of softmax any shift will do, the largest selected logit
+    if (a.softmax && a.renorm) {
         mx = lane < a.topk ? mine : -INFINITY;
+        total = 1.0f;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     }
-    const float p = lane < a.topk ? score(mine) : 0.0f;
+    // of sigmoids whose logits are all far below zero the largest one's: p = 1 / (1 + exp(-l))
+    // is taken over exp(shift)
+    float shift = 0.0f;
+    if (!a.softmax && a.renorm) {
+        shift = lane < a.topk ? mine : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) shift = fmaxf(shift, __shfl_xor_sync(0xffffffffu, shift, o));
+        shift = shift < -60.0f ? shift : 0.0f;
+    }
+    const float p = lane < a.topk ? (a.softmax ? expf(mine - mx) / total : 1.0f / (expf(shift) + expf(shift - mine))) : 0.0f;
     const float sum = a.renorm ? wsum(p) : 1.0f;
     if (lane < a.topk) sw[lane] = p / sum * a.rscale;
     if (lane < a.S) {
