@@ -605,7 +605,7 @@ typedef struct {
     const void* post_w;   /* [K], or NULL: no norm after the block                   */
     const void* pre_w;    /* [K], or NULL: no norm before the next one (no out)      */
     const void* gate;     /* as the handle's gate; NULL without one or without z     */
-    void* residual_out;   /* h [M, K], or NULL; may be residual itself               */
+    void* residual_out;   /* h [M, K], or NULL; may be residual itself (no backward then) */
     void* out;            /* y [M, K], exactly where pre_w is                        */
     float* stats;         /* [M][2]: 1/rms of z and h, for the backward pass, or NULL */
 } qmlp_norm_io;
@@ -637,8 +637,10 @@ void qmlp_norm_destroy(qmlp_norm_t* h);
 qmlp_status qmlp_norm_forward(qmlp_norm_t* h, const qmlp_norm_io* io, int M, qmlp_stream_t stream);
 
 /* Backward: io as the forward's, with the stats that it wrote (residual_out and
- * out are not read). Errors: as the forward; INVALID_ARG also for no stats, no
- * gradient to start from, or a gradient of what io lacks. */
+ * out are not read). residual is the one that the forward read: one that it wrote
+ * residual_out over is gone, and the caller keeps a copy. Errors: as the forward;
+ * INVALID_ARG also for no stats, no gradient to start from, or a gradient of what io
+ * lacks; ALIAS also where residual_out overlaps residual. */
 qmlp_status qmlp_norm_backward(qmlp_norm_t* h, const qmlp_norm_io* io, const qmlp_norm_grads* grads, int M,
                                qmlp_stream_t stream);
 

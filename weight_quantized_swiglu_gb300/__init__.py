@@ -898,8 +898,9 @@ class BlockNorm:
 
     def forward(self, z=None, residual=None, post_w=None, pre_w=None, gate=None, residual_out=None, out=None,
                 stats=None, M=None, stream=None):
-        """Writes residual_out (h) and out (y); stats [M, 2] fp32 keeps what
-        backward needs. Returns (residual_out, out)."""
+        """Writes residual_out (h; may be residual itself where no backward follows)
+        and out (y); stats [M, 2] fp32 keeps what backward needs. Returns
+        (residual_out, out)."""
         M = self._rows(z, residual) if M is None else M
         addr = self._addr
         io = qmlp_norm_io(addr("z", z, M), addr("residual", residual, M), addr("post_w", post_w, M),
@@ -912,7 +913,8 @@ class BlockNorm:
                  dresidual_out=None, dz=None, dresidual=None, dpost_w=None, dpre_w=None, dgate=None, M=None,
                  stream=None):
         """From dout (y's gradient) and dresidual_out (h's, None: zero) the
-        gradients that are given: dz, dresidual, dpost_w, dpre_w, dgate."""
+        gradients that are given: dz, dresidual, dpost_w, dpre_w, dgate. residual is
+        the array that forward read, as it was then."""
         M = self._rows(z, residual) if M is None else M
         addr = self._addr
         io = qmlp_norm_io(addr("z", z, M), addr("residual", residual, M), addr("post_w", post_w, M),

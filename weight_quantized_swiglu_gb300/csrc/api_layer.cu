@@ -209,6 +209,10 @@ qmlp_status qmlp_norm_backward(qmlp_norm_t* h, const qmlp_norm_io* io, const qml
             (g->dpre_w && !io->pre_w) || (g->dgate && !io->gate))
             return QMLP_ERR_INVALID_ARG;
         const size_t n = (size_t)M * d.K;
+        // the arrays of a forward in place: its residual is gone
+        if (io->residual && io->residual_out &&
+            overlaps(io->residual, n * dt_bytes(d.rdt), io->residual_out, n * dt_bytes(d.rdt)))
+            return QMLP_ERR_ALIAS;
         auto add = [&](const void* p, qmlp_dtype t, size_t k, bool w) {
             if (st == QMLP_OK) st = c.add(p, t, k, w);
         };
