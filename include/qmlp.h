@@ -683,11 +683,13 @@ void qmlp_linear_destroy(qmlp_linear_t* h);
  *  out = device [M, N], bf16, fp16 or fp32 per odt
  * Allocates nothing; can be captured in a CUDA graph. The same call gives the same
  * bytes. One handle serves one stream at a time.
- * Up to 64 tokens every product is exact. From 65 on the weights are decoded once a
- * call into images of the tensor-core GEMM (at most 1 GiB held by a handle made for
- * 65 tokens or more, in turn for larger projections), in which an INT4 weight is
- * rounded once to fp16; NVFP4's are exact in it. Into an fp32 out what that rounding
- * leaves is added by a second product.
+ * x is exact: fp16 as it is, bf16 times a power of two a token, exact for every value
+ * within 2^29 of the token's largest. Up to 64 tokens every product is exact too. From 65
+ * on the weights are decoded once a call into images of the tensor-core GEMM (at most
+ * 1 GiB held by a handle made for 65 tokens or more, in turn for larger projections), in
+ * which an INT4 weight is rounded once to fp16; NVFP4's are exact in it. Into an fp32 out
+ * what that rounding leaves is added by a second product, and sums leave the tensor cores'
+ * accumulators every few steps whatever M is, so that it keeps fp32's precision.
  * Errors: INVALID_ARG, ALIGNMENT (16 bytes), ALIAS, SHAPE (M < 1 or over max_M),
  * CUDA. */
 qmlp_status qmlp_linear_forward(qmlp_linear_t* h, const void* x, qmlp_dtype xdt, int M, void* out, qmlp_dtype odt,

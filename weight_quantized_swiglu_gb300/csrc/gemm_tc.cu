@@ -283,24 +283,26 @@ template <int N>
 QMLP_DEV void store_any(const Args& a, int m, int col, const float (&v)[N]) {
     const size_t at = (size_t)m * a.ldo + col;
     if (!QMLP_INB(m, a.M, 12)) return;
-    if (a.odt == 0) {
-        float* o = static_cast<float*>(a.out) + at;
-        if (col + N <= a.ncols && (a.ldo & 3) == 0) {
+    if constexpr (N < 32) {  // (fp32 outs come sixteen or four at a time)
+        if (a.odt == 0) {
+            float* o = static_cast<float*>(a.out) + at;
+            if (col + N <= a.ncols && (a.ldo & 3) == 0) {
 #pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-                if (a.onto) {
-                    const float4 h = *reinterpret_cast<const float4*>(o + j);
-                    w = make_float4(joined(h.x, w.x), joined(h.y, w.y), joined(h.z, w.z), joined(h.w, w.w));
+                for (int j = 0; j < N; j += 4) {
+                    float4 w = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    if (a.onto) {
+                        const float4 h = *reinterpret_cast<const float4*>(o + j);
+                        w = make_float4(joined(h.x, w.x), joined(h.y, w.y), joined(h.z, w.z), joined(h.w, w.w));
+                    }
+                    *reinterpret_cast<float4*>(o + j) = w;
                 }
-                *reinterpret_cast<float4*>(o + j) = w;
-            }
-        } else {
+            } else {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (col + j < a.ncols) o[j] = a.onto ? joined(o[j], v[j]) : v[j];
+                for (int j = 0; j < N; ++j)
+                    if (col + j < a.ncols) o[j] = a.onto ? joined(o[j], v[j]) : v[j];
+            }
+            return;
         }
-        return;
     }
     uint32_t p[N / 2];
 #pragma unroll
@@ -322,6 +324,21 @@ QMLP_DEV void store_any(const Args& a, int m, int col, const float (&v)[N]) {
         for (int j = 0; j < N; ++j)
             if (col + j < a.ncols) o[j] = (uint16_t)(p[j / 2] >> (16 * (j & 1)));
     }
+}
+
+// kEpiOut: row m's sums from column col on to out.
+template <int FMT, int N>
+QMLP_DEV void out_columns(const Args& a, int m, int col, int sg, float (&y)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+        const float4 f = factor4<FMT>(a.cs0, a.inv0, col + j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            y[j + e] = out_value(y[j + e], sg, f4_at(f, e));
+            if (a.bias && col + j + e < a.ncols) y[j + e] += __ldg(a.bias + col + j + e);
+        }
+    }
+    store_any<N>(a, m, col, y);
 }
 
 // EXT: the instances of low-rank adapters, which add their fp32 terms.
@@ -475,18 +492,7 @@ QMLP_DEV void store_tile(const Args& a, uint32_t tbase, int m, bool live, int sg
             float y[32];
             tmem_ld32(tbase + c0, y);
             const int col = nt * BN + c0;
-            if (live && col < a.ncols) {
-#pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const float4 f = factor4<FMT>(a.cs0, a.inv0, col + j);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[j + e] = out_value(y[j + e], sg, f4_at(f, e));
-                        if (a.bias && col + j + e < a.ncols) y[j + e] += __ldg(a.bias + col + j + e);
-                    }
-                }
-                store_any<32>(a, m, col, y);
-            }
+            if (live && col < a.ncols) out_columns<FMT, 32>(a, m, col, sg, y);
         }
     } else if (a.epi == kEpiPlain) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
@@ -905,7 +911,14 @@ QMLP_DEV void umma_commit_pair(uint32_t bar) {
         : "memory");
 }
 
-template <int FMT, bool PRE, bool EXT = false>
+// SUMS (kEpiOut into fp32): an MMA cuts off what passes its accumulator's last bit, always
+// downward in size, and a chain over k = 17408 was 2e-5 off (2000 tokens). Every kSumSteps
+// steps, 16 MMAs, the accumulators are emptied into fp32 sums in the epilogue's registers,
+// the other buffer's MMAs running meanwhile: 3.3e-7 off (5120 x 17408 NVFP4, 2000 tokens 320
+// us, 269 as one chain; INT4, two products, 621 and 524).
+constexpr int kSumSteps = 4;
+
+template <int FMT, bool PRE, bool EXT = false, bool SUMS = false>
 __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_constant__ CUtensorMap amap,
                                                                 const __grid_constant__ CUtensorMap bmap,
                                                                 const __grid_constant__ CUtensorMap amap2,
@@ -1083,56 +1096,54 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
         if (lane == 0) {
             int it = 0, tc = 0;
             bool ok = true, issued = false;
-            int u, sp, first, k0, k1;
-            for (; ok && piece(tc, u, sp); ++tc) {
+            // steps [k0, k1) into accumulator tc & 1
+            auto chain = [&](int k0, int k1) {
                 const int buf = tc & 1, use = tc >> 1;
-                if (rank == 0) {
-                    steps(u, sp, first, k0, k1);
-                    // ---------------- MMA issuer (leader) ----------------
-                    if (use > 0 &&
-                        (!wait_or_abort(acc_empty(buf), (uint32_t)((use - 1) & 1), abort_flag, a.err, 42, a.limit) ||
-                         !wait_cluster_or_abort(pacc(buf), (uint32_t)((use - 1) & 1), abort_flag, a.err, 43,
-                                                a.limit))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t d_tmem = tmem + (uint32_t)(buf * BN);
-                    for (int ks = k0; ks < k1; ++ks, ++it) {
-                        const int s = it % kL, b = it % kBSd;
-                        const bool ready =
-                            wait_or_abort(full(s), (uint32_t)((it / kL) & 1), abort_flag, a.err, 44, a.limit) &&
-                            (PRE || (wait_or_abort(bfull(b), (uint32_t)((it / kBSd) & 1), abort_flag, a.err, 45,
-                                                   a.limit) &&
-                                     wait_cluster_or_abort(pbfull(b), (uint32_t)((it / kBSd) & 1), abort_flag, a.err,
-                                                           46, a.limit)));
-                        if (!ready) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t sa = base_s + S::A + s * kABytes;
-                        const uint32_t sb = PRE ? base_s + S::Raw + s * kR : base_s + S::B + b * kBHalf;
-#pragma unroll
-                        for (int k = 0; k < BK / 16; ++k)
-                            umma_f16_pair(d_tmem, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32),
-                                          PRE && !(EXT && a.f16) ? kIdescPairBF16 : kIdescPair,
-                                          (ks != k0 || k != 0) ? 1u : 0u);
-                        issued = true;
-                        umma_commit_pair(empty(s));
-                        if (!PRE) umma_commit_pair(bempty(b));
-                    }
-                    if (!ok) break;
-                    umma_commit_pair(acc_full(buf));
-                } else {
+                if (rank != 0) {
                     // ---------------- forwarder (peer): accumulator drained ----------------
                     if (use > 0) {
-                        if (!wait_or_abort(acc_empty(buf), (uint32_t)((use - 1) & 1), abort_flag, a.err, 47, a.limit)) {
-                            ok = false;
-                            break;
-                        }
+                        if (!wait_or_abort(acc_empty(buf), (uint32_t)((use - 1) & 1), abort_flag, a.err, 47, a.limit)) return false;
                         mbar_arrive_remote(pacc(buf), 0);
                     }
+                    return true;
+                }
+                // ---------------- MMA issuer (leader) ----------------
+                if (use > 0 &&
+                    (!wait_or_abort(acc_empty(buf), (uint32_t)((use - 1) & 1), abort_flag, a.err, 42, a.limit) ||
+                     !wait_cluster_or_abort(pacc(buf), (uint32_t)((use - 1) & 1), abort_flag, a.err, 43, a.limit)))
+                    return false;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem + (uint32_t)(buf * BN);
+                for (int ks = k0; ks < k1; ++ks, ++it) {
+                    const int s = it % kL, b = it % kBSd;
+                    const bool ready =
+                        wait_or_abort(full(s), (uint32_t)((it / kL) & 1), abort_flag, a.err, 44, a.limit) &&
+                        (PRE ||
+                         (wait_or_abort(bfull(b), (uint32_t)((it / kBSd) & 1), abort_flag, a.err, 45, a.limit) &&
+                          wait_cluster_or_abort(pbfull(b), (uint32_t)((it / kBSd) & 1), abort_flag, a.err, 46, a.limit)));
+                    if (!ready) return false;
+                    tc_fence_after();
+                    const uint32_t sa = base_s + S::A + s * kABytes;
+                    const uint32_t sb = PRE ? base_s + S::Raw + s * kR : base_s + S::B + b * kBHalf;
+#pragma unroll
+                    for (int k = 0; k < BK / 16; ++k)
+                        umma_f16_pair(d_tmem, smem_desc_sw128(sa + k * 32), smem_desc_sw128(sb + k * 32),
+                                      PRE && !(EXT && a.f16) ? kIdescPairBF16 : kIdescPair, (ks != k0 || k != 0) ? 1u : 0u);
+                    issued = true;
+                    umma_commit_pair(empty(s));
+                    if (!PRE) umma_commit_pair(bempty(b));
+                }
+                umma_commit_pair(acc_full(buf));
+                return true;
+            };
+            int u, sp, first, k0, k1;
+            for (int i = 0; ok && piece(i, u, sp); ++i) {
+                steps(u, sp, first, k0, k1);
+                if constexpr (SUMS) {
+                    for (; ok && k0 < k1; k0 += kSumSteps, ++tc) ok = chain(k0, min(k1, k0 + kSumSteps));
+                } else {
+                    ok = chain(k0, k1);
+                    if (ok) ++tc;
                 }
             }
             // every MMA that wrote either CTA's TMEM must be finished before
@@ -1146,35 +1157,88 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
         const int q = warp & 3;
         const int grp = (warp - 2) / kEpiWarps;
         const int row_in_tile = q * 32 + lane;
-        int tc = 0, u, sp;
-        for (; piece(tc, u, sp); ++tc) {
-            int nt, mt2;
-            tile(u, nt, mt2);
-            const int buf = tc & 1, use = tc >> 1;
-            const bool ready = wait_or_abort(acc_full(buf), (uint32_t)(use & 1), abort_flag, a.err, 50, a.limit);
-            if (!__all_sync(0xffffffffu, ready)) break;
-            tc_fence_after();
-            const int m = mt2 * 2 * BM + (int)rank * BM + row_in_tile;
-            const bool live = m < a.M;
-            const int sg = live && a.sig ? a.sig[m] : 0;  // no prescale (null sig): bf16 operands
-            const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
-            if (EXT && u >= whole) {
-                float* ws = a.ws + (((size_t)pair * 2 + rank) * BM + row_in_tile) * BN;
-#pragma unroll 1
-                for (int c0 = grp * 32; c0 < BN; c0 += kGroups * 32) {
-                    float y[32];
-                    tmem_ld32(tbase + c0, y);
-                    if (live && QMLP_INB(ws - a.ws + c0 + 31, a.ws_elems, 13)) {
-                        float4* dst = reinterpret_cast<float4*>(ws + c0);
+        if constexpr (SUMS) {
+            constexpr int kCols = 16, kParts = (BN + kGroups * kCols - 1) / (kGroups * kCols);
+            int tc = 0, u, sp, first, k0, k1;
+            bool ok = true;
+            for (int i = 0; ok && piece(i, u, sp); ++i) {
+                steps(u, sp, first, k0, k1);
+                float sum[kParts][kCols];  // columns (i kGroups + grp) kCols..
 #pragma unroll
-                        for (int v = 0; v < 8; ++v) dst[v] = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+                for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                    for (int j = 0; j < kCols; ++j) sum[p][j] = 0.0f;
+                for (; k0 < k1; k0 += kSumSteps, ++tc) {
+                    const int buf = tc & 1, use = tc >> 1;
+                    ok = __all_sync(0xffffffffu, wait_or_abort(acc_full(buf), (uint32_t)(use & 1), abort_flag, a.err, 50, a.limit));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) {
+                        const int c0 = (p * kGroups + grp) * kCols;
+                        if (c0 < BN) {
+                            float y[kCols];
+                            tmem_ld16(tbase + c0, y);
+#pragma unroll
+                            for (int j = 0; j < kCols; ++j) sum[p][j] += y[j];
+                        }
+                    }
+                    tc_fence_before();
+                    mbar_arrive(acc_empty(buf));
+                }
+                if (!ok) break;
+                int nt, mt2;
+                tile(u, nt, mt2);
+                const int m = mt2 * 2 * BM + (int)rank * BM + row_in_tile;
+                if (m >= a.M) continue;
+                const int sg = a.sig ? a.sig[m] : 0;
+#pragma unroll
+                for (int p = 0; p < kParts; ++p) {
+                    const int c0 = (p * kGroups + grp) * kCols, col = nt * BN + c0;
+                    if (c0 >= BN) continue;
+                    if (u >= whole) {
+                        float* ws = a.ws + (((size_t)pair * 2 + rank) * BM + row_in_tile) * BN + c0;
+                        if (!QMLP_INB(ws - a.ws + kCols - 1, a.ws_elems, 13)) continue;
+#pragma unroll
+                        for (int j = 0; j < kCols; j += 4)
+                            *reinterpret_cast<float4*>(ws + j) = make_float4(sum[p][j], sum[p][j + 1], sum[p][j + 2], sum[p][j + 3]);
+                    } else if (col < a.ncols) {
+                        out_columns<FMT, kCols>(a, m, col, sg, sum[p]);
                     }
                 }
-            } else {
-                store_tile<FMT, EXT>(a, tbase, m, live, sg, nt, grp * 32, kGroups * 32);
             }
-            tc_fence_before();
-            mbar_arrive(acc_empty(buf));
+        } else {
+            int tc = 0, u, sp;
+            for (; piece(tc, u, sp); ++tc) {
+                int nt, mt2;
+                tile(u, nt, mt2);
+                const int buf = tc & 1, use = tc >> 1;
+                const bool ready = wait_or_abort(acc_full(buf), (uint32_t)(use & 1), abort_flag, a.err, 50, a.limit);
+                if (!__all_sync(0xffffffffu, ready)) break;
+                tc_fence_after();
+                const int m = mt2 * 2 * BM + (int)rank * BM + row_in_tile;
+                const bool live = m < a.M;
+                const int sg = live && a.sig ? a.sig[m] : 0;  // no prescale (null sig): bf16 operands
+                const uint32_t tbase = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * BN);
+                if (EXT && u >= whole) {
+                    float* ws = a.ws + (((size_t)pair * 2 + rank) * BM + row_in_tile) * BN;
+#pragma unroll 1
+                    for (int c0 = grp * 32; c0 < BN; c0 += kGroups * 32) {
+                        float y[32];
+                        tmem_ld32(tbase + c0, y);
+                        if (live && QMLP_INB(ws - a.ws + c0 + 31, a.ws_elems, 13)) {
+                            float4* dst = reinterpret_cast<float4*>(ws + c0);
+#pragma unroll
+                            for (int v = 0; v < 8; ++v) dst[v] = make_float4(y[4 * v], y[4 * v + 1], y[4 * v + 2], y[4 * v + 3]);
+                        }
+                    }
+                } else {
+                    store_tile<FMT, EXT>(a, tbase, m, live, sg, nt, grp * 32, kGroups * 32);
+                }
+                tc_fence_before();
+                mbar_arrive(acc_empty(buf));
+            }
         }
     } else if (!PRE) {
         // ---------------- decoders: rows 128 rank.. of each weight block ----------------
@@ -1603,7 +1667,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // The CTA-pair GEMM over `pairs_wanted` clusters of two (fewer if fewer fit at
 // once: the pairs loop over the tiles).
-template <int FMT, bool PRE, bool EXT = false>
+template <int FMT, bool PRE, bool EXT = false, bool SUMS = false>
 cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const CUtensorMap& map2,
                         const CUtensorMap& bmap2, Args a, int pairs_wanted, int pairs_max, cudaStream_t s) {
     static int max_pairs = -1;
@@ -1619,12 +1683,12 @@ cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const C
     cfg.attrs = at;
     cfg.numAttrs = 1;
     if (max_pairs < 0) {
-        cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<FMT, PRE, EXT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel<FMT, PRE, EXT, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              SmemP<FMT, PRE>::Bytes);
         if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2);
         int n = 0;
-        e = cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<FMT, PRE, EXT>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&n, gemm_pair_kernel<FMT, PRE, EXT, SUMS>, &cfg);
         if (e != cudaSuccess) return e;
         if (n < 1) return cudaErrorInvalidConfiguration;
         max_pairs = n;
@@ -1645,7 +1709,7 @@ cudaError_t launch_pair(const CUtensorMap& map, const CUtensorMap& bmap, const C
         }
     }
     cfg.gridDim = dim3((unsigned)(2 * pairs));
-    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_pair_kernel<FMT, PRE, EXT>, map, bmap, map2, bmap2, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_pair_kernel<FMT, PRE, EXT, SUMS>, map, bmap, map2, bmap2, a);
     if (e != cudaSuccess || !a.tail) return e;
     tail_reduce_kernel<FMT><<<(unsigned)(a.tail * (2 * BM * BN / 4 / 256)), 256, 0, s>>>(a);
     return cudaPeekAtLastError();
@@ -1917,6 +1981,8 @@ cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
                 return cudaErrorInvalidValue;
         }
+        if (a.epi == kEpiOut && a.odt == 0)
+            return launch_pair<kFP8, true, true, true>(map, bmap, map2, bmap2, a, pairs, std::max(num_sms, 2) / 2, s);
         return P.fmt == kFP8 ? launch_pair<kFP8, true, true>(map, bmap, map2, bmap2, a, pairs, std::max(num_sms, 2) / 2, s)
                              : launch_pair<kNVFP4, true, true>(map, bmap, map2, bmap2, a, pairs, std::max(num_sms, 2) / 2, s);
     }
