@@ -1,5 +1,5 @@
-// handle.h -- the dense handle and the host-side helpers shared by the files
-// that implement the C ABI (api.cu, api_adapt.cu).
+// handle.h -- the dense and routed-expert handles and the host-side helpers shared by
+// the files that implement the C ABI (api.cu, api_adapt.cu, api_layer.cu).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -240,7 +240,10 @@ constexpr int kPairMinM = 256;  // one 256-token tile of a CTA pair
 // Fewest tokens of one projection that the GEMM takes, a 256-token tile of them in part:
 // its time hardly depends on their number (17408 x 5120 81 us from 65 to 255 tokens; launches
 // of 64 tokens each 80 us at 128, 120 at 192; 5120 x 5120 36 to 73 us, 1024 x 5120 22 to 58
-// at 130), one launch of up to 64 takes half of it.
+// at 130), one launch of up to 64 takes half of it. (The MLP's GEMM with decoder warps, which
+// has neither these records nor INT4, is ahead of images up to some 700 tokens: three
+// projections of the 27B-class block 178 us at 256 tokens and 322 at 512, images 103 to 132 a
+// projection at 300.)
 constexpr int kLinearGemmM = 65;
 cudaError_t launch_gemm_prescale(const void* a, int M, int K, void* a16, int* sig, int num_sms, cudaStream_t s);
 cudaError_t launch_gemm(const GemmLaunch& L, int num_sms, cudaStream_t s);

@@ -119,9 +119,9 @@ QMLP_DEV float warp_sum(float v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// The sums of N values over a row's threads, in every thread. ROWS > 1: a warp a
-// row; else the CTA, through one of two buffers in turn (`turn` flips), so that
-// one barrier a sum is enough.
+// The sums of N values over a row's threads, in every thread. WARP: a warp has the row;
+// else the CTA, through one of two buffers in turn (`turn` flips), so that one barrier a
+// sum is enough.
 template <bool WARP, int N>
 QMLP_DEV void row_sum(float (&v)[N], float (*buf)[N][32], int& turn) {
 #pragma unroll
