@@ -294,10 +294,21 @@ QMLP_DEV void select_tokens(const MoeLayerArgs& a, const float* lg, int M, int w
     }
 }
 
+// The MMAs' accumulators to sums of their own: an MMA cuts off what passes its last
+// bit, always downward in size, and a chain of 128 of them was 1.4e-6 off, eight at a time 5e-7.
+template <int NT>
+QMLP_DEV void flush(float (&d)[NT][4], float (&sum)[NT][4]) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[n][e] += d[n][e], d[n][e] = 0.0f;
+}
 // Sixteen rows of the router times NT tiles of eight tokens over pairs of steps
 // (32 k) j0 + w, w + hop, ... < j1, both planes of an fp32 router: fragments of 1 KB a
-// pair, [plane][tile][pair][2][lane] of 16 bytes.
-template <int NT>
+// pair, [plane][tile][pair][2][lane] of 16 bytes. SUM: for long shares of k; the MMAs'
+// accumulators, which lose their last bits at every step, go to fp32 sums every eight MMAs (a
+// chain over k = 8192: weights 8e-6 to 3.4e-5 off, fp32 arithmetic 4e-7).
+template <int NT, bool SUM>
 QMLP_DEV void router_tile(const MoeLayerArgs& a, const uint4* xsm, int M, int tile, int j0, int j1, int hop, int lane,
                           float (&d)[NT][4]) {
     const int g = lane >> 2, t = lane & 3, n32 = a.K / 32;
@@ -305,6 +316,7 @@ QMLP_DEV void router_tile(const MoeLayerArgs& a, const uint4* xsm, int M, int ti
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
+    float sum[SUM ? NT : 1][4] = {};
     for (int pl = 0; pl < a.planes; ++pl) {
         const uint4* f = a.rfrag + ((size_t)(pl * a.rtiles + tile) * n32) * 64 + lane;
 #pragma unroll 2
@@ -317,8 +329,15 @@ QMLP_DEV void router_tile(const MoeLayerArgs& a, const uint4* xsm, int M, int ti
                 mma_f16_16816(d[n], a0.x, a0.y, a0.z, a0.w, x.x, x.y);
                 mma_f16_16816(d[n], a1.x, a1.y, a1.z, a1.w, x.z, x.w);
             }
+            if constexpr (SUM)
+                if ((((j - j0) / hop) & 3) == 3 || j + hop >= j1) flush<NT>(d, sum);
         }
     }
+    if constexpr (SUM)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[n][e] = sum[n][e];
 }
 // The order of a lane's eight k of a unit of 32, for A and B alike: a byte of the
 // lane-sliced banks holds two neighbours, and the codes are taken as nibbles p and p +
@@ -551,15 +570,6 @@ QMLP_DEV void convert_act(const MoeLayerArgs& a, int rows, uint4* out, size_t ou
     }
 }
 
-// The MMAs' accumulators to sums of their own (LO): an MMA cuts off what passes its last
-// bit, always downward in size, and a chain of 128 of them was 1.4e-6 off, eight at a time 5e-7.
-template <int NT>
-QMLP_DEV void flush(float (&d)[NT][4], float (&sum)[NT][4]) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[n][e] += d[n][e], d[n][e] = 0.0f;
-}
 // A unit's results, times the weights, to part.
 template <int NT>
 QMLP_DEV void unit_out(const float (&d)[NT][4], int M, int t, int g, const uint16_t* ridx, const float* coef, float* part) {
@@ -715,7 +725,7 @@ __global__ void __launch_bounds__(kThreads + 32, 1) moe_layer_kernel(const MoeLa
             const int tile = u / splits, sp = u % splits;
             const int j0 = (int)((long)sp * n32 / splits), j1 = (int)((long)(sp + 1) * n32 / splits);
             float d[NT][4];
-            router_tile<NT>(a, xsm, M, tile, j0 + warp, j1, kWarps, lane, d);
+            router_tile<NT, false>(a, xsm, M, tile, j0 + warp, j1, kWarps, lane, d);
             if (u != (int)blockIdx.x) named_bar_sync(1, kThreads);  // the sums before are read
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -1098,7 +1108,7 @@ __global__ void __launch_bounds__(256) router_kernel(const MoeLayerArgs a) {
     const int tile = blockIdx.y * 8 + warp;
     if (tile * 16 >= rows) return;
     float d[1][4];
-    router_tile<1>(a, xsm, M, tile, 0, a.K / 32, 1, lane, d);
+    router_tile<1, true>(a, xsm, M, tile, 0, a.K / 32, 1, lane, d);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int row = tile * 16 + g + 4 * (e & 2), m = 2 * t + (e & 1);
